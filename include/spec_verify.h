@@ -73,7 +73,9 @@ typedef enum {
                                            SPEC_VERIFY_NOALLOC_SCRATCH_BYTES of scratch */
 } spec_status_t;
 
-typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1 } spec_dtype_t;
+/* SPEC_DTYPE_E4M3 (8-bit floats: 4 exponent bits, 3 mantissa bits, largest 448) is a type of
+ * cache contents only (spec_kv_cache_t). */
+typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_E4M3 = 2 } spec_dtype_t;
 
 /* Bits of the device error word. */
 #define SPEC_DEVERR_TOKEN_RANGE  1   /* a draft / node token outside [0, V) */
@@ -81,6 +83,8 @@ typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1 } spec_dtype_t;
 #define SPEC_DEVERR_TREE_PARENT  4   /* parents[0] != -1 or parents[n] not in [0, n) */
 #define SPEC_DEVERR_TIMEOUT      8   /* a bounded wait inside a kernel ran out (internal error;
                                         the affected results are not valid) */
+#define SPEC_DEVERR_CACHE_RANGE 16   /* a length, position or page id outside the cache, or a
+                                        node id outside the tree (cache calls) */
 
 /*
  * Bytes of workspace any of the three verification calls needs for B
@@ -346,6 +350,169 @@ spec_status_t spec_verify_sample_noalloc(const void* target_logits, const void* 
                                          int gamma, int V, int32_t* out_tokens,
                                          int32_t* out_num_accepted, float* out_logprobs,
                                          cudaStream_t stream);
+
+/* ==========================================================================
+ * The target model's side of a verification step.  [SD] "What happens in one
+ * round", step 2: the target scores the drafted positions in one pass over
+ * its cached context; the source pages leave that pass to the model.  These
+ * calls are its cache and attention parts, for chains and for draft trees,
+ * and the log-probabilities a server reports about the emitted tokens.
+ *
+ * A paged key-value cache: position t of sequence b lives in page
+ * block_table[b, t / page_size], slot t % page_size.  Entry (page, slot,
+ * head) of layer 0 holds head_dim contiguous elements at
+ *   k + page * page_stride + slot * token_stride + head * head_stride
+ * (strides in elements, the same for v), so token-first and head-first pages,
+ * and keys beside values in one tensor, are all described by strides.
+ *
+ *   dtype BF16: no scales.
+ *   dtype E4M3: element = e4m3 value * scale, one fp32 scale for each (page,
+ *     slot, head), at k_scale / v_scale with the scale_* strides (elements).
+ *
+ * head_dim is 64, 128 or 256; page_size, num_pages, max_pages >= 1.  k and v
+ * are 16-byte aligned and their strides multiples of 16 bytes
+ * (SPEC_ERR_MISALIGNED otherwise).  `layers` and the layer strides matter to
+ * spec_kv_compact only; the other calls work on the layer that k and v point
+ * to.  `error` (nullable) is a device error word (int32, zeroed by the
+ * caller; spec_verify_read_error reads and clears it).
+ *
+ * New positions: a call brings N positions for each of B sequences, sequence
+ * b's at cache positions context_lens[b] .. context_lens[b] + n_b - 1, where
+ * n_b is new_lens[b] (NULL: N).  A sequence whose lengths are negative, pass N or pass
+ * max_pages * page_size, or whose table names a page outside
+ * [0, num_pages) at a position the call reads or writes, sets
+ * SPEC_DEVERR_CACHE_RANGE; nothing outside the cache is touched, and what
+ * such a sequence gets instead is said at each call.
+ * ======================================================================== */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* block_table;          /* [B, max_pages] */
+    int32_t* error;                      /* nullable */
+    int64_t page_stride, token_stride, head_stride, layer_stride;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride, scale_layer_stride;
+    int32_t dtype;                       /* SPEC_DTYPE_BF16 or SPEC_DTYPE_E4M3 */
+    int32_t layers, num_pages, page_size, max_pages, kv_heads, head_dim;
+} spec_kv_cache_t;
+
+/*
+ * Prepares the new positions' queries and keys and writes keys and values
+ * into the cache, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight       (per head; weight NULL: y = x)
+ *   y's first rot_dim elements rotated by the position's angles:
+ *     (a, b) -> (a cos - b sin, b cos + a sin) with a, b = y[i], y[i + rot_dim/2]
+ *     (interleaved = 0) or y[2i], y[2i+1] (interleaved = 1)
+ * for queries and keys; values are stored as they are.  All in fp32, rounded
+ * once: to bf16 (q_out, a BF16 cache), or to e4m3 with the row's scale
+ * max(max|y|, 1e-20) / 448.
+ *   q, k, v      bf16, token i = b * N + n at q + i * q_token_stride (elements; likewise
+ *                k, v), heads contiguous: q_heads, kv_heads and kv_heads rows of head_dim.
+ *                16-byte aligned, strides multiples of 8.  q and q_out NULL with
+ *                q_heads 0: keys and values only
+ *   q_weight, k_weight  [head_dim] bf16, nullable
+ *   rope         [rope_rows, rot_dim] fp32: the cosines of a position's rot_dim/2 angles,
+ *                then their sines; rot_dim a multiple of 16, at most head_dim (0: no rotation,
+ *                rope NULL)
+ *   positions    [B, N] int32: row of `rope` for each new position (NULL: its cache
+ *                position); a draft tree passes context + depth
+ *   q_out        [B, N, q_heads, head_dim] bf16
+ * Positions n >= n_b are skipped: nothing is written for them.  For a bad
+ * sequence, and for a position outside [0, rope_rows), no cache entry is
+ * written and q_out is NaN.
+ */
+spec_status_t spec_kv_append(const spec_kv_cache_t* cache, const void* q, const void* k,
+                             const void* v, int64_t q_token_stride, int64_t k_token_stride,
+                             int64_t v_token_stride, const void* q_weight, const void* k_weight,
+                             float eps, const float* rope, int rope_rows, int rot_dim,
+                             int interleaved, const int32_t* context_lens,
+                             const int32_t* new_lens, const int32_t* positions, int B, int N,
+                             int q_heads, void* q_out, cudaStream_t stream);
+
+/*
+ * Reads cached positions back as dense rows: out_k, out_v [B, T, kv_heads,
+ * head_dim] of out_dtype (BF16 or F32), row t of sequence b holding position
+ * starts[b] + t (NULL: t) for t < counts[b] (NULL: T), zeros for the other
+ * rows.  E4M3 entries are multiplied by their scale in fp32 and rounded once.
+ * A bad sequence's rows are NaN, and so is the row of a bad page.
+ */
+spec_status_t spec_kv_read(const spec_kv_cache_t* cache, const int32_t* starts,
+                           const int32_t* counts, int B, int T, spec_dtype_t out_dtype,
+                           void* out_k, void* out_v, cudaStream_t stream);
+
+/*
+ * Moves the accepted path of a draft tree to the front of its slots, in every
+ * layer of the cache: entry context_lens[b] + path_nodes[b, i] goes to
+ * context_lens[b] + i + 1 for i < num_accepted[b].  path_nodes [B, N] and
+ * num_accepted [B] are spec_verify_tree_greedy's outputs (node n of the tree
+ * was appended at position context + n; the root stays where it is), so node
+ * ids ascend along the path.  After it the first context_lens[b] + 1 +
+ * num_accepted[b] positions are the verified context.  Entries are moved as
+ * they are (scales with them); keys were rotated for the node's depth, which
+ * is its new distance from the root.  A sequence with num_accepted -1 is
+ * skipped; a path that is not ascending in 1..N-1, or that is longer than
+ * N-1, sets SPEC_DEVERR_CACHE_RANGE and moves nothing.  1 <= N <= 1024.
+ */
+spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* context_lens,
+                              const int32_t* path_nodes, const int32_t* num_accepted, int B,
+                              int N, cudaStream_t stream);
+
+/*
+ * Attention of the new positions over the cache, which already holds them
+ * (spec_kv_append): for query head h of position n, with cached head
+ * h / (q_heads / kv_heads),
+ *   s_t = scale * q . k_t,   out = sum_t softmax(s)_t v_t,   lse = ln sum_t e^(s_t)
+ * over the positions t that n sees: every t < context_lens[b], and of the new
+ * ones
+ *   parents NULL: those up to itself (a chain, N <= 257);
+ *   parents [B, N] int32: itself and its ancestors (a tree, N <= 64;
+ *     parents[0] = -1, 0 <= parents[n] < n as in spec_verify_tree_greedy).
+ *   q      [B, N, q_heads, head_dim] bf16, token i at q + i * q_token_stride (elements,
+ *          a multiple of 8), heads contiguous; 16-byte aligned
+ *   out    [B, N, q_heads, head_dim] bf16, contiguous
+ *   lse    [B, N, q_heads] fp32, nullable
+ * q_heads is a multiple of kv_heads, at most 64 times it.  Scores, softmax
+ * statistics and sums are fp32.  Positions n >= n_b give out = 0 and lse =
+ * -inf.  A bad sequence (or a malformed tree, SPEC_DEVERR_TREE_PARENT) gives
+ * NaN.  What the masked entries of the cache hold does not matter, NaN and
+ * infinities included.
+ *
+ * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned,
+ * zero-filled once (spec_verify_workspace_init).  Its counters are zero again
+ * after every call, so it serves attention calls of any size in turn (and
+ * replays of a captured one), but no other entry point may write to it.
+ */
+size_t spec_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim);
+spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
+                                   int64_t q_token_stride, const int32_t* context_lens,
+                                   const int32_t* new_lens, const int32_t* parents, float scale,
+                                   int B, int N, int q_heads, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Log-probabilities of given tokens with the distribution's entropy and its
+ * top alternatives, p = softmax(z / T) over each of `rows` rows of V logits:
+ *   out_logprob [rows]          ln p(tokens[r])
+ *   out_entropy [rows]          -sum p ln p (nats), nullable
+ *   out_top_idx [rows, K]       the K largest logits' tokens (larger first, lower index
+ *                               first among equal logits, -0.0 equal to +0.0)
+ *   out_top_logprob [rows, K]   their ln p
+ * 0 <= K <= 8 (K = 0: no lists, both may be NULL); with V < K the lists are
+ * padded with -1 and -inf.  A masked (-inf) logit has ln p = -inf and adds
+ * nothing to the entropy.  A token outside [0, V) gives ln p = NaN and sets
+ * SPEC_DEVERR_TOKEN_RANGE; a row of -inf alone gives NaN everywhere (list
+ * tokens -1) and sets SPEC_DEVERR_EMPTY_ROW.  Sums are fp32.  Logits are
+ * 16-byte aligned; V and its row length need no alignment.  Workspace:
+ * spec_logprobs_workspace_size(rows, V, K) bytes, 256-byte aligned, its first
+ * 256 bytes zero-filled once (the error word).
+ */
+size_t spec_logprobs_workspace_size(int rows, int V, int K);
+spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const int32_t* tokens,
+                                  float temperature, int rows, int V, int K, float* out_logprob,
+                                  float* out_entropy, int32_t* out_top_idx,
+                                  float* out_top_logprob, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Test hook for the kernels' bounded waits (the source pages have no

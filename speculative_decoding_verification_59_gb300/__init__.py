@@ -10,6 +10,7 @@ without the built library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -20,6 +21,8 @@ __all__ = [
     "spec_verify_sample_stats", "spec_verify_sample_finish", "spec_verify_sample_noalloc",
     "spec_verify_greedy", "spec_verify_tree_greedy", "spec_verify_read_error",
     "spec_verify_status_string", "Workspace", "verify_sample", "verify_greedy", "verify_tree_greedy",
+    "SPEC_DTYPE_E4M3", "KVCache", "kv_append", "kv_read", "kv_compact", "paged_attention",
+    "token_logprobs",
 ]
 
 SPEC_OK = 0
@@ -33,10 +36,12 @@ SPEC_ERR_EXCEEDS_STATIC_SCRATCH = 7
 SPEC_VERIFY_NOALLOC_SCRATCH_BYTES = 8 << 20
 SPEC_DTYPE_F32 = 0
 SPEC_DTYPE_BF16 = 1
+SPEC_DTYPE_E4M3 = 2
 SPEC_DEVERR_TOKEN_RANGE = 1
 SPEC_DEVERR_EMPTY_ROW = 2
 SPEC_DEVERR_TREE_PARENT = 4
 SPEC_DEVERR_TIMEOUT = 8
+SPEC_DEVERR_CACHE_RANGE = 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libspecverify.so")
@@ -44,6 +49,19 @@ _lib = None
 
 # name -> (argtypes, restype); pointers travel as c_void_p, the stream as c_void_p
 _P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_int64, ctypes.c_float
+
+
+class KVCacheStruct(ctypes.Structure):
+    """spec_kv_cache_t of include/spec_verify.h."""
+    _fields_ = [(n, _P) for n in ("k", "v", "k_scale", "v_scale", "block_table", "error")] + \
+        [(n, _L) for n in ("page_stride", "token_stride", "head_stride", "layer_stride",
+                           "scale_page_stride", "scale_token_stride", "scale_head_stride",
+                           "scale_layer_stride")] + \
+        [(n, ctypes.c_int32) for n in ("dtype", "layers", "num_pages", "page_size", "max_pages",
+                                       "kv_heads", "head_dim")]
+
+
 SIGNATURES = {
     "spec_verify_workspace_size": ([_I, _I, _I], _S),
     "spec_verify_workspace_init": ([_P, _S, _P], _I),
@@ -65,6 +83,14 @@ SIGNATURES = {
     "spec_ngram_retrieve": ([_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P], _I),
     "spec_cosine_workspace_size": ([_I, _I], _S),
     "spec_cosine_topk": ([_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _S, _P], _I),
+    "spec_kv_append": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _I, _I, _I, _P, _P, _P, _I, _I,
+                        _I, _P, _P], _I),
+    "spec_kv_read": ([_P, _P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "spec_kv_compact": ([_P, _P, _P, _P, _I, _I, _P], _I),
+    "spec_attention_workspace_size": ([_I, _I, _I, _I, _I], _S),
+    "spec_paged_attention": ([_P, _P, _L, _P, _P, _P, _F, _I, _I, _I, _P, _P, _P, _S, _P], _I),
+    "spec_logprobs_workspace_size": ([_I, _I, _I], _S),
+    "spec_token_logprobs": ([_P, _I, _P, _F, _I, _I, _I, _P, _P, _P, _P, _P, _S, _P], _I),
     "spec_verify_read_error": ([_P, _P, _P], _I),
     "spec_verify_status_string": ([_I], ctypes.c_char_p),
     "spec_verify_set_wait_limit": ([ctypes.c_uint32], None),
@@ -490,3 +516,319 @@ def verify_tree_greedy(target, node_tokens, parents, *, workspace: Optional[Work
                                  _stream(stream))
     _check(st, "spec_verify_tree_greedy")
     return nodes, tok, acc
+
+
+# ---- cache, attention and log-probabilities ------------------------------------------
+# These calls run on every layer of every step, where the host's share counts:
+# the fixed part of their arguments is checked once (KVCache), and each of the
+# others by a handful of comparisons that end in _check_tensor's message only
+# when one fails.
+_call_ws = {}
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of the current stream of a device."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
+def _under(stream):
+    """Outputs and workspaces of a call on a stream other than the current one are
+    allocated under that stream, so that the allocator reuses their memory in its order."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _scratch(kind: str, dev, handle: int, need: int):
+    """(tensor, pointer, bytes) of the default workspace of one kind of call on one stream
+    of one device: calls on different streams overlap and must not share one."""
+    key = (kind, dev.index, handle)
+    ws = _call_ws.get(key)
+    if ws is None or ws[2] < need:
+        t = _torch().zeros(max(need, 256), dtype=_torch().uint8, device=dev)
+        ws = _call_ws[key] = (t, t.data_ptr(), t.numel())
+    return ws
+
+
+def _given_workspace(ws, need: int, dev):
+    _check_tensor(ws, "workspace", (None,), (_torch().uint8,), dev)
+    if ws.numel() < need:
+        raise SpecVerifyError(SPEC_ERR_WORKSPACE_TOO_SMALL, "workspace")
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _ints(t, name: str, shape, dev):
+    """The pointer of a contiguous int32 tensor of the given shape on dev; None for None."""
+    if t is None:
+        return None
+    torch = _torch()
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev.index or not t.is_contiguous():
+        _check_tensor(t, name, tuple(shape), (torch.int32,), dev)
+    return t.data_ptr()
+
+
+class KVCache:
+    """A paged key-value cache (see spec_kv_cache_t): views of the caller's tensors,
+    checked once.
+
+    k, v         [pages, page_size, kv_heads, head_dim], or [layers, pages, ...]: bfloat16, or
+                 float8_e4m3fn with k_scale / v_scale (float32, the shape without head_dim).
+                 Any strides with the last dimension contiguous, the same for k and v:
+                 a head-first pool is passed transposed, keys beside values as slices.
+    block_table  [B, max_pages] int32, contiguous
+    A call on one layer takes cache.layer(i) (layer 0 of a cache without layers is
+    the cache itself); kv_compact takes them all."""
+
+    def __init__(self, k, v, block_table, k_scale=None, v_scale=None, _error=None):
+        torch = _torch()
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+            if t.device.type != "cuda":
+                raise ValueError(f"{name} must be a CUDA tensor, got device {t.device}")
+            if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+                raise TypeError(f"{name} must have dtype bfloat16 or float8_e4m3fn, got {t.dtype}")
+            if t.dim() not in (4, 5) or t.stride(-1) != 1:
+                raise ValueError(f"{name} must be [layers,] pages, page_size, kv_heads, head_dim "
+                                 "with head_dim contiguous")
+        if v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("k and v must agree in shape, strides, dtype and device")
+        dev = k.device
+        _check_tensor(block_table, "block_table", (None, None), (torch.int32,), dev)
+        if dev.index is None or dev.index != block_table.get_device():
+            raise ValueError(f"the cache is on {dev}, its block table on {block_table.device}")
+        fp8 = k.dtype == torch.float8_e4m3fn
+        if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and to it alone")
+        if fp8:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t.dtype != torch.float32 or t.shape != k.shape[:-1] or t.device != dev:
+                    raise ValueError(f"{name} must be float32 {tuple(k.shape[:-1])} on {dev}")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("k_scale and v_scale must have the same strides")
+        self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
+        self.error = torch.zeros(1, dtype=torch.int32, device=dev) if _error is None else _error
+        self.device = dev
+        L = k.dim() == 5
+        pages, page, heads, dim = k.shape[-4:]
+        ks, ss = k.stride(), k_scale.stride() if fp8 else (0,) * (k.dim() - 1)
+        self.batch, self.max_pages = block_table.shape
+        self.layers = k.shape[0] if L else 1
+        self.page_size, self.kv_heads, self.head_dim, self.fp8 = page, heads, dim, fp8
+        self.struct = KVCacheStruct(
+            k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), block_table.data_ptr(),
+            self.error.data_ptr(), ks[-4], ks[-3], ks[-2], ks[0] if L else 0,
+            ss[-3], ss[-2], ss[-1], ss[0] if L else 0,
+            SPEC_DTYPE_E4M3 if fp8 else SPEC_DTYPE_BF16, self.layers, pages, page, self.max_pages,
+            heads, dim)
+        self.addr = ctypes.addressof(self.struct)
+
+    def layer(self, i: int) -> "KVCache":
+        """One layer of the cache (sharing its block table and error word)."""
+        if self.k.dim() == 4:
+            if i != 0:
+                raise IndexError(f"layer {i} of a cache of one layer")
+            return self
+        sc = (self.k_scale[i], self.v_scale[i]) if self.fp8 else (None, None)
+        return KVCache(self.k[i], self.v[i], self.block_table, *sc, _error=self.error)
+
+    def read_error(self, stream=None) -> int:
+        """The SPEC_DEVERR_* bits that calls on this cache raised; clears them."""
+        st, code = spec_verify_read_error(self.error.data_ptr(), _stream(stream))
+        _check(st, "spec_verify_read_error")
+        return code
+
+
+def _heads(t, name: str, B: int, N: int, heads: int, D: int, dev) -> int:
+    """The token stride of a bfloat16 [B, N, heads, D] tensor whose tokens lie one stride
+    apart, each with its heads side by side."""
+    torch = _torch()
+    shape, (sb, sn, sh, sd) = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev.index:
+        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if shape != (B, N, heads, D):
+        raise ValueError(f"{name} must have shape {(B, N, heads, D)}, got {tuple(shape)}")
+    if sd != 1 or (sh != D and heads > 1) or (sb != N * sn and B > 1 and N > 1):
+        raise ValueError(f"{name}: heads must lie side by side and tokens one stride apart, "
+                         f"got strides {(sb, sn, sh, sd)}")
+    return sn if N > 1 else sb
+
+
+def _rows_of(t, name: str, cache: KVCache):
+    """(B, N, heads) of a [B, N, heads, head_dim] tensor that the cache has room for."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have shape (B, N, heads, {cache.head_dim}), got {tuple(t.shape)}")
+    B, N, H, _ = t.shape
+    if B > cache.batch:
+        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
+    return B, N, H
+
+
+def kv_append(cache: KVCache, q, k, v, context_lens, rope=None, *, q_weight=None, k_weight=None,
+              eps: float = 1e-6, interleaved: bool = False, new_lens=None, positions=None, out=None,
+              stream=None):
+    """Normalises and rotates the new positions' queries and keys and writes keys and
+    values into the cache (see spec_kv_append).  q [B, N, q_heads, head_dim] (None: keys
+    and values only), k, v [B, N, kv_heads, head_dim] bfloat16; slices of one fused
+    projection are fine.  context_lens [B] int32, rope [rows, rot_dim] float32 (cosines, then
+    sines) or None, weights [head_dim] bfloat16 or None, positions [B, N] int32 or None,
+    new_lens [B] int32 or None.  Returns the prepared queries [B, N, q_heads, head_dim]."""
+    torch = _torch()
+    dev, D, H = cache.device, cache.head_dim, cache.kv_heads
+    B, N, _ = _rows_of(k, "k", cache)
+    ks, vs = _heads(k, "k", B, N, H, D, dev), _heads(v, "v", B, N, H, D, dev)
+    Hq = qs = rows = rot = 0
+    qp = op = rp = qw = kw = None
+    if q is not None:
+        Hq = _rows_of(q, "q", cache)[2]
+        qs, qp = _heads(q, "q", B, N, Hq, D, dev), q.data_ptr()
+        if out is None:
+            with _under(stream):
+                out = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_tensor(out, "out", (B, N, Hq, D), (torch.bfloat16,), dev)
+        op = out.data_ptr()
+    if q_weight is not None:
+        _check_tensor(q_weight, "q_weight", (D,), (torch.bfloat16,), dev)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _check_tensor(k_weight, "k_weight", (D,), (torch.bfloat16,), dev)
+        kw = k_weight.data_ptr()
+    if rope is not None:
+        _check_tensor(rope, "rope", (None, None), (torch.float32,), dev)
+        (rows, rot), rp = rope.shape, rope.data_ptr()
+    if context_lens is None:
+        raise TypeError("context_lens must be a torch tensor, got NoneType")
+    st = load_library().spec_kv_append(
+        cache.addr, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qw, kw, eps, rp, rows, rot,
+        1 if interleaved else 0, _ints(context_lens, "context_lens", (B,), dev),
+        _ints(new_lens, "new_lens", (B,), dev), _ints(positions, "positions", (B, N), dev), B, N, Hq,
+        op, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "spec_kv_append")
+    return out
+
+
+def kv_read(cache: KVCache, T: int, *, starts=None, counts=None, dtype=None, stream=None):
+    """Cached positions as dense rows (see spec_kv_read): (k, v), each [B, T, kv_heads,
+    head_dim] of dtype (bfloat16 by default, or float32), row t holding position
+    starts[b] + t for t < counts[b], zeros after that.  B is the length of starts or
+    counts, or the cache's batch."""
+    torch = _torch()
+    dev = cache.device
+    if dtype is None:
+        dtype = torch.bfloat16
+    elif dtype not in _logits_dtypes():
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    B = cache.batch if starts is None and counts is None else (counts if starts is None else starts).shape[0]
+    if B > cache.batch:
+        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
+    shape = (B, T, cache.kv_heads, cache.head_dim)
+    with _under(stream):
+        k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    st = load_library().spec_kv_read(
+        cache.addr, _ints(starts, "starts", (B,), dev), _ints(counts, "counts", (B,), dev), B, T,
+        SPEC_DTYPE_F32 if dtype is torch.float32 else SPEC_DTYPE_BF16, k.data_ptr(), v.data_ptr(),
+        _raw_stream(dev.index) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "spec_kv_read")
+    return k, v
+
+
+def kv_compact(cache: KVCache, context_lens, path_nodes, num_accepted, *, stream=None) -> None:
+    """Moves the accepted path of every sequence's draft tree to the front of its slots, in
+    every layer (see spec_kv_compact).  path_nodes [B, N] and num_accepted [B] are
+    verify_tree_greedy's."""
+    dev = cache.device
+    if path_nodes.dim() != 2:
+        raise ValueError(f"path_nodes must have shape (B, N), got {tuple(path_nodes.shape)}")
+    B, N = path_nodes.shape
+    if B > cache.batch:
+        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
+    st = load_library().spec_kv_compact(
+        cache.addr, _ints(context_lens, "context_lens", (B,), dev),
+        _ints(path_nodes, "path_nodes", (B, N), dev), _ints(num_accepted, "num_accepted", (B,), dev),
+        B, N, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "spec_kv_compact")
+
+
+_attention_need = {}
+
+
+def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=None,
+                    scale: Optional[float] = None, lse: bool = False, out=None, workspace=None,
+                    stream=None):
+    """Attention of new positions, already appended, over the cache (see
+    spec_paged_attention).  q [B, N, q_heads, head_dim] bfloat16, context_lens [B] int32,
+    parents [B, N] int32 for draft trees (None: chains), new_lens [B] int32 or None; scale
+    defaults to head_dim ** -0.5.  Returns out [B, N, q_heads, head_dim] bfloat16, with
+    lse=True also [B, N, q_heads] float32.  workspace: a zero-filled uint8 tensor of
+    spec_attention_workspace_size() bytes that only this call uses (None: one kept
+    for the device and stream)."""
+    torch = _torch()
+    dev, D, H = cache.device, cache.head_dim, cache.kv_heads
+    B, N, Hq = _rows_of(q, "q", cache)
+    qs = _heads(q, "q", B, N, Hq, D, dev)
+    if context_lens is None:
+        raise TypeError("context_lens must be a torch tensor, got NoneType")
+    lib = load_library()
+    need = _attention_need.get((N, Hq, H, D))
+    if need is None:
+        need = lib.spec_attention_workspace_size(B, N, Hq, H, D)
+        if need == 0:
+            raise ValueError(f"paged_attention: unsupported sizes N={N} q_heads={Hq} kv_heads={H} head_dim={D}")
+        _attention_need[(N, Hq, H, D)] = need
+    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    if out is not None:
+        _check_tensor(out, "out", (B, N, Hq, D), (torch.bfloat16,), dev)
+    with _under(stream):
+        if out is None:
+            out = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=dev)
+        e = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if lse else None
+        w = _scratch("attention", dev, h, need) if workspace is None else _given_workspace(workspace, need, dev)
+    st = lib.spec_paged_attention(
+        cache.addr, q.data_ptr(), qs, _ints(context_lens, "context_lens", (B,), dev),
+        _ints(new_lens, "new_lens", (B,), dev), _ints(parents, "parents", (B, N), dev),
+        D ** -0.5 if scale is None else scale, B, N, Hq, out.data_ptr(), e.data_ptr() if lse else None,
+        w[1], w[2], h)
+    if st:
+        _check(st, "spec_paged_attention")
+    return (out, e) if lse else out
+
+
+def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, workspace=None,
+                   stream=None):
+    """Log-probabilities of tokens with entropies and top alternatives (see
+    spec_token_logprobs).  logits [..., V] contiguous bfloat16 or float32, tokens [...]
+    int32.  Returns (logprob [...], entropy [...], top_idx [..., K] int32, top_logprob
+    [..., K]); the last two None for K = 0."""
+    torch = _torch()
+    _check_tensor(logits, "logits", (None,) * max(logits.dim(), 1), _logits_dtypes())
+    dev, shape = logits.device, logits.shape
+    lead, V = shape[:-1], shape[-1]
+    if tokens is None:
+        raise TypeError("tokens must be a torch tensor, got NoneType")
+    tp = _ints(tokens, "tokens", lead, dev)
+    rows = tokens.numel()
+    lib = load_library()
+    need = lib.spec_logprobs_workspace_size(rows, V, K)
+    if need == 0:
+        raise ValueError(f"token_logprobs: unsupported sizes rows={rows} V={V} K={K}")
+    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    ti = tl = ip = fp = None
+    with _under(stream):
+        lp = torch.empty(lead, dtype=torch.float32, device=dev)
+        ent = torch.empty(lead, dtype=torch.float32, device=dev)
+        if K:
+            ti = torch.empty((*lead, K), dtype=torch.int32, device=dev)
+            tl = torch.empty((*lead, K), dtype=torch.float32, device=dev)
+            ip, fp = ti.data_ptr(), tl.data_ptr()
+        w = _scratch("logprobs", dev, h, need) if workspace is None else _given_workspace(workspace, need, dev)
+    st = lib.spec_token_logprobs(logits.data_ptr(), _dtype_code(logits), tp, temperature, rows, V, K,
+                                 lp.data_ptr(), ent.data_ptr(), ip, fp, w[1], w[2], h)
+    if st:
+        _check(st, "spec_token_logprobs")
+    return lp, ent, ti, tl

@@ -1,0 +1,351 @@
+// The paged cache's own calls: appending new positions (head norms, rotation
+// and quantisation in the same pass), reading positions back, and moving a
+// draft tree's accepted path.  All three move each byte once and compute
+// little: HBM bounds them when they are large, the launch when small.
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr int kKvThreads = 256;
+
+// ---- append -------------------------------------------------------------------
+// One row (a token's query, key or value head) per D / 8 lanes, 8 elements a
+// lane: 16-byte loads, the norm's sum and the row's largest magnitude by
+// shuffles among those lanes.  A half-split rotation pairs element i with
+// i + rot/2, which another lane holds at the same offset (rot is a multiple
+// of 16), so it takes one shuffle per element; an interleaved one pairs a
+// lane's own neighbours.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kKvThreads) append_kernel(const AppendArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int L = D / 8;                                  // lanes per row
+    const int heads = a.Hq + 2 * a.c.kv_heads;
+    const long long rows = (long long)a.B * a.N * heads;
+    const long long r = ((long long)blockIdx.x * kKvThreads + threadIdx.x) / L;
+    const bool live = r < rows;                               // a row's lanes agree; idle rows keep the shuffles whole
+    const int lr = threadIdx.x % L;
+    const int tok = live ? (int)(r / heads) : 0;
+    const int h = live ? (int)(r - (long long)tok * heads) : 0;
+    const int b = tok / a.N, n = tok - b * a.N;
+    const int kind = h < a.Hq ? 0 : h < a.Hq + a.c.kv_heads ? 1 : 2;   // query, key, value
+    const int head = kind == 0 ? h : kind == 1 ? h - a.Hq : h - a.Hq - a.c.kv_heads;
+
+    const int ctx = __ldg(a.ctx + b);
+    const int nb = a.newl ? __ldg(a.newl + b) : a.N;
+    const char* src = kind == 0 ? a.q + tok * a.qs : kind == 1 ? a.k + tok * a.ks : a.v + tok * a.vs;
+    float x[8];
+    unpack8(ld_stream16(src + ((size_t)head * D + lr * 8) * 2), x);
+
+    const int cap = a.c.max_pages * a.c.page_size;
+    bool bad = ctx < 0 || nb < 0 || nb > a.N || ctx > cap - nb;
+    const bool skip = !live || (!bad && n >= nb);
+    const int t = bad ? 0 : ctx + n;
+    int rp = t;
+    if (a.rot > 0 && !bad && !skip) {
+        if (a.pos) rp = __ldg(a.pos + tok);
+        if ((unsigned)rp >= (unsigned)a.rope_rows) bad = true;
+    }
+    int page = 0, slot = 0;
+    if (!bad && !skip && !cache_place(a.c, b, t, &page, &slot)) bad = true;
+
+    const char* wsrc = kind == 0 ? a.qw : kind == 1 ? a.kw : nullptr;
+    if (a.qw || a.kw) {                                       // every lane takes part in the shuffles
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (wsrc) {
+            float w[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(wsrc) + lr), w);
+            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+        }
+    }
+    if (a.rot > 0) {                                          // and in these
+        const int half = a.rot >> 1;
+        const bool turn = kind < 2 && lr * 8 < a.rot && !bad && !skip;
+        const float* cs = a.rope + (size_t)(turn ? rp : 0) * a.rot;
+        if (a.inter) {
+            if (turn) {
+                const float4 co = __ldg(reinterpret_cast<const float4*>(cs + lr * 4));
+                const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + lr * 4));
+                const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = x[2 * i], q = x[2 * i + 1];
+                    x[2 * i] = p * c4[i] - q * s4[i];
+                    x[2 * i + 1] = q * c4[i] + p * s4[i];
+                }
+            }
+        } else {
+            const bool upper = lr * 8 >= half;
+            const int step = half >> 3;                       // lanes between the halves
+            const int base = (threadIdx.x & 31) - lr;
+            const int other = lr * 8 < a.rot ? base + (upper ? lr - step : lr + step) : (threadIdx.x & 31);
+            const int i0 = turn ? (upper ? lr * 8 - half : lr * 8) : 0;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float4 co = __ldg(reinterpret_cast<const float4*>(cs + i0) + v);
+                const float4 si = __ldg(reinterpret_cast<const float4*>(cs + half + i0) + v);
+                const float c4[4] = {co.x, co.y, co.z, co.w}, s4[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = __shfl_sync(0xffffffffu, x[4 * v + i], other);
+                    if (turn) x[4 * v + i] = upper ? x[4 * v + i] * c4[i] + y * s4[i] : x[4 * v + i] * c4[i] - y * s4[i];
+                }
+            }
+        }
+    }
+    if (kind == 0) {
+        if (skip) return;
+        uint4 o;
+        if (bad) {
+            o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            if (lr == 0 && head == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+        } else {
+            o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        }
+        *reinterpret_cast<uint4*>(a.q_out + (((size_t)tok * a.Hq + head) * D + lr * 8) * 2) = o;
+        return;
+    }
+    if constexpr (!FP8) {
+        if (skip) return;
+        if (bad) {
+            if (lr == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+            return;
+        }
+        char* dst = static_cast<char*>(kind == 1 ? a.c.k : a.c.v) + 2 * entry_off(a.c, page, slot, head);
+        *reinterpret_cast<uint4*>(dst + lr * 16) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    } else {
+        if (bad && !skip && lr == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+        if (bad || skip) return;
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+        const unsigned mask = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << ((threadIdx.x & 31) / L * L);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+        // the nearest e4m3 of y / scale: a true division, so that the row's
+        // largest element always lands on 448
+        const float sc = fmaxf(m, kFp8AmaxFloor) / kFp8Max;
+        uint2 o;
+        o.x = pack_e4m3(x[0] / sc, x[1] / sc) | pack_e4m3(x[2] / sc, x[3] / sc) << 16;
+        o.y = pack_e4m3(x[4] / sc, x[5] / sc) | pack_e4m3(x[6] / sc, x[7] / sc) << 16;
+        char* dst = static_cast<char*>(kind == 1 ? a.c.k : a.c.v) + entry_off(a.c, page, slot, head);
+        *reinterpret_cast<uint2*>(dst + lr * 8) = o;
+        if (lr == 0) (kind == 1 ? a.c.k_scale : a.c.v_scale)[scale_off(a.c, page, slot, head)] = sc;
+    }
+}
+
+template <int D>
+static cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.B * a.N * (a.Hq + 2 * a.c.kv_heads);
+    const dim3 grid((unsigned)((rows * (D / 8) + kKvThreads - 1) / kKvThreads));
+    return a.c.dtype == SPEC_DTYPE_E4M3 ? launch_pdl(append_kernel<D, true>, grid, kKvThreads, 0, st, a)
+                                        : launch_pdl(append_kernel<D, false>, grid, kKvThreads, 0, st, a);
+}
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
+    return a.c.head_dim == 64 ? launch_append_t<64>(a, st) : a.c.head_dim == 128 ? launch_append_t<128>(a, st)
+                                                                                 : launch_append_t<256>(a, st);
+}
+
+// ---- read ---------------------------------------------------------------------
+struct ReadArgs {
+    spec_kv_cache_t c;
+    const int32_t *starts, *counts;
+    int T;
+    char *out_k, *out_v;
+};
+
+// A lane takes the same 8 elements of a position's key and of its value.
+// blockIdx.y is the sequence; the rows (position, head) run along x.
+template <int D, bool FP8, bool F32>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int L = D / 8;
+    const long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x;
+    const int H = a.c.kv_heads;
+    const long long row = i / L;                              // (t, head)
+    if (row >= (long long)a.T * H) return;
+    const int lr = (int)(i % L), b = blockIdx.y;
+    const int t = (int)(row / H), head = (int)(row - (long long)t * H);
+    const int start = a.starts ? __ldg(a.starts + b) : 0;
+    const int count = a.counts ? __ldg(a.counts + b) : a.T;
+    const int cap = a.c.max_pages * a.c.page_size;
+    bool bad = start < 0 || count < 0 || count > a.T || start > cap - count;
+    float xk[8], xv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xk[j] = xv[j] = 0.f;
+    if (!bad && t < count) {
+        int page, slot;
+        if (!cache_place(a.c, b, start + t, &page, &slot)) {
+            bad = true;
+        } else {
+            const int64_t off = entry_off(a.c, page, slot, head) + lr * 8;
+            if constexpr (FP8) {
+                const uint2 wk = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.k) + off));
+                const uint2 wv = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.v) + off));
+                const int64_t so = scale_off(a.c, page, slot, head);
+                const float sk = __ldg(a.c.k_scale + so), sv_ = __ldg(a.c.v_scale + so);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int sh = 16 * (j & 1);
+                    f16x2_to_f32(e4m3_to_f16x2((j < 2 ? wk.x : wk.y) >> sh), &xk[2 * j], &xk[2 * j + 1]);
+                    f16x2_to_f32(e4m3_to_f16x2((j < 2 ? wv.x : wv.y) >> sh), &xv[2 * j], &xv[2 * j + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) { xk[j] *= sk; xv[j] *= sv_; }
+            } else {
+                unpack8(ld_stream16(static_cast<const char*>(a.c.k) + 2 * off), xk);
+                unpack8(ld_stream16(static_cast<const char*>(a.c.v) + 2 * off), xv);
+            }
+        }
+    }
+    if (bad) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xk[j] = xv[j] = CUDART_NAN_F;
+        if (lr == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+    }
+    const size_t o = ((size_t)b * a.T * H + row) * D + lr * 8;
+    if constexpr (F32) {
+        float4* k4 = reinterpret_cast<float4*>(a.out_k) + o / 4;
+        float4* v4 = reinterpret_cast<float4*>(a.out_v) + o / 4;
+        k4[0] = make_float4(xk[0], xk[1], xk[2], xk[3]);
+        k4[1] = make_float4(xk[4], xk[5], xk[6], xk[7]);
+        v4[0] = make_float4(xv[0], xv[1], xv[2], xv[3]);
+        v4[1] = make_float4(xv[4], xv[5], xv[6], xv[7]);
+    } else {
+        reinterpret_cast<uint4*>(a.out_k)[o / 8] =
+            make_uint4(pack_bf16(xk[0], xk[1]), pack_bf16(xk[2], xk[3]), pack_bf16(xk[4], xk[5]), pack_bf16(xk[6], xk[7]));
+        reinterpret_cast<uint4*>(a.out_v)[o / 8] =
+            make_uint4(pack_bf16(xv[0], xv[1]), pack_bf16(xv[2], xv[3]), pack_bf16(xv[4], xv[5]), pack_bf16(xv[6], xv[7]));
+    }
+}
+
+template <int D>
+static cudaError_t launch_read_t(const ReadArgs& a, int B, bool f32, cudaStream_t st) {
+    const long long n = (long long)a.T * a.c.kv_heads * (D / 8);
+    const dim3 grid((unsigned)((n + kKvThreads - 1) / kKvThreads), (unsigned)B);
+    if (a.c.dtype == SPEC_DTYPE_E4M3)
+        return f32 ? launch_pdl(kv_read_kernel<D, true, true>, grid, kKvThreads, 0, st, a)
+                   : launch_pdl(kv_read_kernel<D, true, false>, grid, kKvThreads, 0, st, a);
+    return f32 ? launch_pdl(kv_read_kernel<D, false, true>, grid, kKvThreads, 0, st, a)
+               : launch_pdl(kv_read_kernel<D, false, false>, grid, kKvThreads, 0, st, a);
+}
+
+cudaError_t launch_kv_read(const spec_kv_cache_t& c, const int32_t* starts, const int32_t* counts, int B, int T,
+                           bool f32, void* out_k, void* out_v, cudaStream_t st) {
+    const ReadArgs a{c, starts, counts, T, static_cast<char*>(out_k), static_cast<char*>(out_v)};
+    return c.head_dim == 64 ? launch_read_t<64>(a, B, f32, st) : c.head_dim == 128 ? launch_read_t<128>(a, B, f32, st)
+                                                                                   : launch_read_t<256>(a, B, f32, st);
+}
+
+// ---- compact ------------------------------------------------------------------
+struct CompactArgs {
+    spec_kv_cache_t c;
+    const int32_t *ctx, *path, *acc;
+    int N, cpr;                    // 16-byte chunks of a cache row
+    long long cols;                // columns of the cache: layers x {k, v} x heads x cpr
+    long long scale_cols;          // layers x {k, v} x heads (E4M3)
+};
+
+// A path's ids ascend from at least 1, so node i of the path (from 1) lies
+// at slot >= i, and slot i is never a later node's: a thread that owns one
+// column (layer, k or v, head, 16 bytes) of every slot moves it along the path in
+// order, and no two threads touch the same bytes.  blockIdx.y is the
+// sequence; the CTA first lists the moves (source and destination offsets),
+// which are the same for every column.
+__global__ void __launch_bounds__(kKvThreads) kv_compact_kernel(const CompactArgs a) {
+    extern __shared__ int64_t moves[];                        // per move: source, destination, scales' two
+    __shared__ int n_moves, bad;
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.y;
+    const int acc = __ldg(a.acc + b), ctx = __ldg(a.ctx + b);
+    if (acc == -1) return;
+    const int cap = a.c.max_pages * a.c.page_size;
+    const bool off = acc < 0 || acc >= a.N || ctx < 0 || ctx > cap - 1 - acc;
+    if (threadIdx.x == 0) {
+        n_moves = 0;
+        bad = off;
+    }
+    __syncthreads();
+    const int32_t* path = a.path + (size_t)b * a.N;
+    int first = 0;
+    if (!off) {                                               // CTA-uniform
+        // the path's form, and how many of its first ids are in place already
+        // (ids ascend, so after the first that is not none is)
+        bool wrong = false;
+        int here = 0;
+        for (int i = threadIdx.x; i < acc; i += kKvThreads) {
+            const int p = __ldg(path + i), before = i ? __ldg(path + i - 1) : 0;
+            wrong |= p <= before || p >= a.N;
+            here += p == i + 1;
+        }
+        if (wrong) bad = 1;
+        if (here) atomicAdd(&n_moves, here);
+        __syncthreads();
+        first = min(n_moves, acc);
+        for (int i = first + threadIdx.x; i < acc; i += kKvThreads) {
+            int sp, ss, dp, ds;
+            if (!cache_place(a.c, b, ctx + __ldg(path + i), &sp, &ss) ||
+                !cache_place(a.c, b, ctx + i + 1, &dp, &ds)) {
+                bad = 1;
+                continue;
+            }
+            int64_t* m = moves + 4 * (i - first);
+            m[0] = entry_off(a.c, sp, ss, 0);
+            m[1] = entry_off(a.c, dp, ds, 0);
+            m[2] = scale_off(a.c, sp, ss, 0);
+            m[3] = scale_off(a.c, dp, ds, 0);
+        }
+    }
+    __syncthreads();
+    if (bad) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+        return;
+    }
+    const int n = acc - first;
+    if (n == 0) return;
+    const int elt = a.c.dtype == SPEC_DTYPE_E4M3 ? 1 : 2;
+    const long long step = (long long)gridDim.x * kKvThreads;
+    for (long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x; i < a.cols; i += step) {
+        const int chunk = (int)(i % a.cpr);
+        long long r = i / a.cpr;
+        const int head = (int)(r % a.c.kv_heads);
+        r /= a.c.kv_heads;
+        char* base = static_cast<char*>(r & 1 ? a.c.v : a.c.k) +
+                     ((r >> 1) * a.c.layer_stride + head * a.c.head_stride) * elt + chunk * 16;
+        for (int j = 0; j < n; ++j)
+            *reinterpret_cast<uint4*>(base + moves[4 * j + 1] * elt) =
+                *reinterpret_cast<const uint4*>(base + moves[4 * j] * elt);
+    }
+    for (long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x; i < a.scale_cols; i += step) {
+        const int head = (int)(i % a.c.kv_heads);
+        const long long r = i / a.c.kv_heads;
+        float* base = (r & 1 ? a.c.v_scale : a.c.k_scale) + (r >> 1) * a.c.scale_layer_stride +
+                      head * a.c.scale_head_stride;
+        for (int j = 0; j < n; ++j) base[moves[4 * j + 3]] = base[moves[4 * j + 2]];
+    }
+}
+
+cudaError_t launch_kv_compact(const spec_kv_cache_t& c, const int32_t* ctx, const int32_t* path,
+                              const int32_t* acc, int B, int N, cudaStream_t st) {
+    CompactArgs a{c, ctx, path, acc, N, 0, 0, 0};
+    const bool fp8 = c.dtype == SPEC_DTYPE_E4M3;
+    a.cpr = c.head_dim * (fp8 ? 1 : 2) / 16;
+    a.cols = (long long)c.layers * 2 * c.kv_heads * a.cpr;
+    a.scale_cols = fp8 ? (long long)c.layers * 2 * c.kv_heads : 0;
+    long long g = (a.cols + kKvThreads - 1) / kKvThreads;
+    if (g > 1024) g = 1024;
+    const size_t smem = (size_t)N * 4 * sizeof(int64_t);      // at most 32 KB
+    return launch_pdl(kv_compact_kernel, dim3((unsigned)g, (unsigned)B), kKvThreads, smem, st, a);
+}
+
+}  // namespace sv

@@ -1,0 +1,293 @@
+"""Paged attention of new positions against its 64-bit form (tests/kv_ref.py): chains and
+trees, both cache types, head layouts, page sizes, lengths, splits, masked entries that are no
+numbers, bad input, streams and captured calls."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import kv_ref as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import __graft_entry__
+    __graft_entry__.build()
+    import speculative_decoding_verification_59_gb300 as m
+    return m
+
+
+def tree(g, B, N):
+    p = torch.full((B, N), -1, dtype=torch.int32)
+    for n in range(1, N):
+        p[:, n] = (torch.rand(B, generator=g) * n).to(torch.int32).clamp(0, n - 1)
+    return p
+
+
+def case(seed, B, N, Hq, H, D, page, ctx, fp8=False, hnd=False, is_tree=False, newl=None, qscale=1.5):
+    g = torch.Generator().manual_seed(seed + 1)
+    parts = R.make_cache(seed, B, max(ctx) + N, page, H, D, fp8, hnd)
+    q = (torch.randn((B, N, Hq, D), generator=g) * qscale).to(torch.bfloat16)
+    par = tree(g, B, N) if is_tree else None
+    c = torch.tensor(ctx, dtype=torch.int32)
+    nb = torch.full((B,), N, dtype=torch.int32) if newl is None else torch.tensor(newl, dtype=torch.int32)
+    return parts, q, par, c, nb
+
+
+def check(sv, parts, q, par, c, nb, scale=None, **kw):
+    cache = R.on_gpu(sv, parts)
+    out, lse = sv.paged_attention(q.cuda(), cache, c.cuda(), parents=None if par is None else par.cuda(),
+                                  new_lens=nb.cuda(), scale=scale, lse=True, **kw)
+    o, l, to, tl = R.attention(q, *parts, c, nb, par, scale)
+    assert cache.read_error() == 0
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert torch.isfinite(out).all()
+    worst = ((out - o).abs() / to.clamp_min(1e-30)).max()
+    assert ((out - o).abs() <= to).all(), f"out off by {worst} of its tolerance"
+    assert torch.equal(torch.isinf(lse), torch.isinf(l))
+    fin = torch.isfinite(l)
+    assert ((lse - l).abs()[fin] <= tl[fin]).all(), "lse"
+    return out
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,N,Hq,H,D,page,ctx", [
+    (1, 1, 1, 1, 64, 16, [0]),                       # one position that sees itself alone
+    (1, 1, 32, 8, 128, 16, [777]),
+    (3, 1, 8, 1, 128, 1, [0, 1, 130]),               # pages of one position
+    (2, 8, 8, 2, 128, 64, [63, 64]),                 # 32 rows; a page's end at, and inside, the new positions
+    (2, 5, 10, 2, 128, 5, [7, 201]),                 # odd everything
+    (4, 3, 4, 4, 64, 48, [15, 16, 17, 333]),
+    (1, 17, 12, 12, 64, 16, [99]),
+    (2, 9, 16, 2, 128, 16, [40, 3]),                 # 72 rows: several row blocks
+    (1, 2, 6, 2, 256, 16, [500]),
+    (2, 7, 14, 2, 256, 32, [31, 65]),
+    (1, 3, 64, 1, 128, 16, [70]),                    # all query heads on one cached head
+    (1, 33, 2, 1, 64, 16, [20]),
+])
+def test_chains(sv, fp8, B, N, Hq, H, D, page, ctx):
+    check(sv, *case(B * 100 + N, B, N, Hq, H, D, page, ctx, fp8, hnd=N % 2 == 0))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,N,Hq,H,D,ctx", [(2, 2, 4, 2, 64, [0, 5]), (2, 36, 8, 2, 128, [100, 17]),
+                                           (1, 64, 4, 1, 128, [63]), (1, 64, 2, 2, 256, [1]),
+                                           (3, 11, 8, 8, 64, [0, 250, 31])])
+def test_trees(sv, fp8, B, N, Hq, H, D, ctx):
+    check(sv, *case(N, B, N, Hq, H, D, 16, ctx, fp8, is_tree=True))
+
+
+def test_tree_shaped_as_a_chain_is_a_chain(sv):
+    parts, q, _, c, nb = case(3, 2, 8, 8, 2, 128, 16, [100, 37])
+    cache = R.on_gpu(sv, parts)
+    par = (torch.arange(8, dtype=torch.int32) - 1).repeat(2, 1)
+    a = sv.paged_attention(q.cuda(), cache, c.cuda())
+    b = sv.paged_attention(q.cuda(), cache, c.cuda(), parents=par.cuda())
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_context_is_split_and_joined(sv, fp8):
+    """One sequence over every CTA, ragged beside short ones, and the same bits every time."""
+    args = case(5, 3, 2, 8, 2, 128, 16, [9001, 3, 1500], fp8)
+    check(sv, *args)
+    parts, q, _, c, nb = args
+    cache = R.on_gpu(sv, parts)
+    runs = [sv.paged_attention(q.cuda(), cache, c.cuda()) for _ in range(5)]
+    assert all(torch.equal(runs[0], r) for r in runs)
+
+
+def test_longest_chain(sv):
+    check(sv, *case(8, 1, 257, 1, 1, 64, 16, [40]))
+
+
+@pytest.mark.parametrize("is_tree", [False, True])
+def test_ragged_new_lengths_and_empty_rows(sv, is_tree):
+    """Rows past a sequence's new positions are zero with lse -inf; a sequence may have none."""
+    args = case(9, 5, 6, 8, 2, 128, 16, [10, 0, 77, 0, 200], is_tree=is_tree, newl=[6, 1, 0, 0, 3])
+    out = check(sv, *args)
+    assert (out[2] == 0).all() and (out[4, 3:] == 0).all() and (out[4, :3] != 0).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_masked_entries_may_hold_anything(sv, value, fp8):
+    """A branch's keys, values and scales that are no numbers reach only the rows that see it."""
+    if fp8 and value != math.nan:
+        value = math.nan
+    parts, q, _, c, nb = case(11, 1, 20, 4, 2, 128, 16, [30], fp8)
+    par = torch.tensor([[-1, 0, 1, 2, 3] + [0] * 15], dtype=torch.int32)    # node 7 is a leaf
+    k, v, table, ks, vs = parts
+    pos = 30 + 7
+    at = (int(table[0, pos // 16]), pos % 16)
+    clean = R.on_gpu(sv, parts)
+    want, wl = sv.paged_attention(q.cuda(), clean, c.cuda(), parents=par.cuda(), lse=True)
+    for name in (k, v):
+        x = name.float()
+        x[at[0], at[1], :, 5:9] = value
+        name.copy_(x.to(name.dtype))
+    cache = R.on_gpu(sv, parts)
+    got, gl = sv.paged_attention(q.cuda(), cache, c.cuda(), parents=par.cuda(), lse=True)
+    others = [n for n in range(20) if n != 7]
+    assert torch.equal(got[:, others], want[:, others]) and torch.equal(gl[:, others], wl[:, others])
+    assert not torch.isfinite(got[:, 7]).all()
+    # a value alone, seen by its own row: no number where it is none, the rest as before
+    parts2, *_ = case(11, 1, 20, 4, 2, 128, 16, [30], fp8)
+    x = parts2[1].float()
+    x[at[0], at[1], :, 5] = value
+    parts2[1].copy_(x.to(parts2[1].dtype))
+    got = sv.paged_attention(q.cuda(), R.on_gpu(sv, parts2), c.cuda(), parents=par.cuda())
+    assert torch.equal(got[:, others], want[:, others])
+    bad = ~torch.isfinite(got[:, 7].float())
+    assert bad[..., 5].all() and not bad[..., 6:].any() and not bad[..., :5].any()
+    diff = (got[:, 7].float() - want[:, 7].float()).abs()
+    ok = ~bad
+    assert (diff[ok] <= 2.0 ** -6 * want[:, 7].float().abs()[ok] + 2.0 ** -6).all()
+
+
+def test_scores_of_any_size(sv):
+    """Large scores (a softmax of one entry), equal scores, and a negative scale."""
+    for qscale, scale in ((60.0, None), (0.0, None), (1.0, -0.2), (1.0, 0.0)):
+        check(sv, *case(13, 2, 4, 8, 2, 128, 16, [100, 259], qscale=qscale), scale=scale)
+        check(sv, *case(13, 2, 4, 8, 2, 128, 16, [100, 259], fp8=True, qscale=qscale), scale=scale)
+
+
+def test_value_scales_far_apart(sv):
+    """An 8-bit cache whose positions' value scales span many powers of two, zeros among
+    the rows."""
+    parts, q, par, c, nb = case(14, 1, 4, 8, 2, 128, 16, [300], fp8=True)
+    g = torch.Generator().manual_seed(3)
+    parts[4].copy_(parts[4] * torch.pow(2.0, torch.randint(-40, 10, parts[4].shape, generator=g).float()))
+    check(sv, parts, q, par, c, nb)
+
+
+def test_strided_queries_and_joint_pool(sv):
+    """Queries sliced from a fused projection; keys beside values in one tensor."""
+    B, N, Hq, H, D, page = 2, 4, 8, 2, 128, 16
+    parts, q, par, c, nb = case(15, B, N, Hq, H, D, page, [50, 90])
+    k, v, table, _, _ = parts
+    pool = torch.stack([k, v], 1).cuda()                       # [pages, 2, page, H, D]
+    cache = sv.KVCache(pool[:, 0], pool[:, 1], table.cuda())
+    fused = torch.randn((B, N, Hq + 2 * H, D)).to(torch.bfloat16)
+    fused[:, :, :Hq] = q
+    out = sv.paged_attention(fused.cuda()[:, :, :Hq], cache, c.cuda())
+    o, _, to, _ = R.attention(q, *parts, c, nb)
+    assert ((out.cpu().double() - o).abs() <= to).all()
+
+
+def test_offsets_past_32_bits(sv):
+    """Pages whose elements lie beyond 2^32 of the cache's first."""
+    page, H, D, N = 64, 8, 128, 2
+    pages = (1 << 32) // (page * H * D) + 40
+    k = torch.empty((pages, page, H, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    parts, q, par, c, nb = case(16, 1, N, 8, H, D, page, [150])
+    high = torch.tensor([[pages - 1, pages - 30, 3, pages - 2, -1]], dtype=torch.int32)
+    for i in range(3):
+        k[int(high[0, i])] = parts[0][int(parts[2][0, i])].cuda()
+        v[int(high[0, i])] = parts[1][int(parts[2][0, i])].cuda()
+    out = sv.paged_attention(q.cuda(), sv.KVCache(k, v, high.cuda()), c.cuda())
+    o, _, to, _ = R.attention(q, *parts, c, nb)
+    assert ((out.cpu().double() - o).abs() <= to).all()
+
+
+def test_bad_sequences_are_marked_and_the_others_hold(sv):
+    parts, q, _, c, nb = case(17, 6, 4, 8, 2, 128, 16, [40, 100, 60, 20, 30, 1000])
+    good = R.on_gpu(sv, parts)
+    want = sv.paged_attention(q.cuda(), good, c.cuda())
+    table = parts[2].clone()
+    table[1, 2] = 1 << 20                                       # a page that is none
+    table[2, 0] = -5
+    c2, n2 = c.clone(), nb.clone()
+    c2[3] = -1
+    n2[4] = 5                                                   # more than the call brings
+    c2[5] = table.shape[1] * 16 - 3                             # runs past the table
+    cache = R.on_gpu(sv, (parts[0], parts[1], table, None, None))
+    got, lse = sv.paged_attention(q.cuda(), cache, c2.cuda(), new_lens=n2.cuda(), lse=True)
+    assert cache.read_error() == sv.SPEC_DEVERR_CACHE_RANGE
+    assert torch.equal(got[0], want[0])
+    assert torch.isnan(got[1:]).all() and torch.isnan(lse[1:]).all()
+    assert torch.equal(sv.paged_attention(q.cuda(), good, c.cuda()), want)
+
+
+def test_malformed_trees(sv):
+    parts, q, _, c, nb = case(18, 3, 4, 4, 2, 64, 16, [20, 30, 40])
+    par = torch.tensor([[-1, 0, 1, 1], [0, 0, 1, 1], [-1, 0, 2, 1]], dtype=torch.int32)
+    cache = R.on_gpu(sv, parts)
+    out = sv.paged_attention(q.cuda(), cache, c.cuda(), parents=par.cuda())
+    assert cache.read_error() == sv.SPEC_DEVERR_TREE_PARENT
+    assert torch.isfinite(out[0]).all() and torch.isnan(out[1:]).all()
+
+
+def test_one_workspace_for_calls_of_every_size(sv):
+    """Calls of different sizes in turn through one workspace, nothing waiting between them."""
+    ws = torch.zeros(sv.load_library().spec_attention_workspace_size(8, 64, 32, 2, 128), dtype=torch.uint8, device="cuda")
+    sizes = [(20, 1, 8, 32, 8, 128, [2000], False), (21, 3, 36, 8, 2, 128, [700, 30, 1500], True),
+             (22, 2, 3, 4, 4, 64, [4000, 100], False), (23, 1, 64, 2, 1, 128, [900], True)]
+    held = []
+    for seed, B, N, Hq, H, D, ctx, tr in sizes:
+        parts, q, par, c, nb = case(seed, B, N, Hq, H, D, 16, ctx, is_tree=tr)
+        cache = R.on_gpu(sv, parts)
+        kw = dict(parents=None if par is None else par.cuda())
+        held.append((q.cuda(), cache, c.cuda(), kw, sv.paged_attention(q.cuda(), cache, c.cuda(), **kw)))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got.append([sv.paged_attention(q, cache, c, workspace=ws, **kw) for q, cache, c, kw, _ in held])
+    for row in got:
+        for x, (_, _, _, _, want) in zip(row, held):
+            assert torch.equal(x, want)
+
+
+def test_on_another_stream(sv):
+    parts, q, par, c, nb = case(24, 2, 4, 8, 2, 128, 16, [1000, 5000])
+    cache, qd, cd = R.on_gpu(sv, parts), q.cuda(), c.cuda()
+    want = sv.paged_attention(qd, cache, cd)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    outs = [sv.paged_attention(qd, cache, cd, stream=s) for _ in range(20) for s in side]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_captured_call_follows_its_lengths(sv):
+    parts, q, par, c, nb = case(25, 2, 2, 8, 2, 128, 16, [3000, 40])
+    cache, qd, cd = R.on_gpu(sv, parts), q.cuda(), c.cuda()
+    out = torch.empty_like(qd)
+    sv.paged_attention(qd, cache, cd, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.paged_attention(qd, cache, cd, out=out)
+    for lens in ([3000, 40], [7, 2900], [0, 0], [1234, 999]):
+        cd.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, sv.paged_attention(qd, cache, cd))
+
+
+def test_refusals(sv):
+    parts, q, par, c, nb = case(26, 2, 4, 8, 2, 128, 16, [10, 20])
+    cache, qd, cd = R.on_gpu(sv, parts), q.cuda(), c.cuda()
+    with pytest.raises(TypeError):
+        sv.paged_attention(qd.float(), cache, cd)
+    with pytest.raises(ValueError):
+        sv.paged_attention(qd[:, :, :, :64], cache, cd)
+    with pytest.raises(ValueError):
+        sv.paged_attention(qd[:, :, :7].contiguous(), cache, cd)
+    with pytest.raises(ValueError):
+        sv.paged_attention(qd.transpose(1, 2).contiguous().transpose(1, 2), cache, cd)
+    with pytest.raises((TypeError, ValueError)):
+        sv.paged_attention(qd, cache, cd.long())
+    with pytest.raises(ValueError):
+        sv.paged_attention(qd, cache, cd[:1])
+    with pytest.raises(sv.SpecVerifyError):
+        sv.paged_attention(qd, cache, cd, scale=math.inf)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.paged_attention(qd, cache, cd, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        sv.KVCache(cache.k, cache.v[:, :, :1], cache.block_table)
+    with pytest.raises(ValueError):
+        sv.KVCache(cache.k, cache.v, cache.block_table, torch.zeros(3, device="cuda"))
