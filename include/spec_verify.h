@@ -478,9 +478,9 @@ spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* conte
  * NaN.  What the masked entries of the cache hold does not matter, NaN and
  * infinities included.
  *
- * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned,
- * zero-filled once (spec_verify_workspace_init).  Its counters are zero again
- * after every call, so it serves attention calls of any size in turn (and
+ * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned, its
+ * first 4096 bytes zero-filled once.  Its counters are zero again after every
+ * call, so it serves attention calls of any size in turn (and
  * replays of a captured one), but no other entry point may write to it.
  */
 size_t spec_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim);

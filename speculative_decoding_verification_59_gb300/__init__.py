@@ -10,7 +10,6 @@ without the built library raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -520,49 +519,24 @@ def verify_tree_greedy(target, node_tokens, parents, *, workspace: Optional[Work
 
 # ---- cache, attention and log-probabilities ------------------------------------------
 # These calls run on every layer of every step, where the host's share counts:
-# the fixed part of their arguments is checked once (KVCache), and each of the
-# others by a handful of comparisons that end in _check_tensor's message only
-# when one fails.
-_call_ws = {}
+# the fixed part of their arguments is checked once (KVCache), the rest in
+# _marshal (csrc/sv_torch.cpp), which also allocates the outputs and makes the
+# C call.
+_marshal_module = None
 
 
-def _raw_stream(index: int) -> int:
-    """The handle of the current stream of a device."""
-    return _torch()._C._cuda_getCurrentRawStream(index)
-
-
-def _under(stream):
-    """Outputs and workspaces of a call on a stream other than the current one are
-    allocated under that stream, so that the allocator reuses their memory in its order."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
-
-
-def _scratch(kind: str, dev, handle: int, need: int):
-    """(tensor, pointer, bytes) of the default workspace of one kind of call on one stream
-    of one device: calls on different streams overlap and must not share one."""
-    key = (kind, dev.index, handle)
-    ws = _call_ws.get(key)
-    if ws is None or ws[2] < need:
-        t = _torch().zeros(max(need, 256), dtype=_torch().uint8, device=dev)
-        ws = _call_ws[key] = (t, t.data_ptr(), t.numel())
-    return ws
-
-
-def _given_workspace(ws, need: int, dev):
-    _check_tensor(ws, "workspace", (None,), (_torch().uint8,), dev)
-    if ws.numel() < need:
-        raise SpecVerifyError(SPEC_ERR_WORKSPACE_TOO_SMALL, "workspace")
-    return ws, ws.data_ptr(), ws.numel()
-
-
-def _ints(t, name: str, shape, dev):
-    """The pointer of a contiguous int32 tensor of the given shape on dev; None for None."""
-    if t is None:
-        return None
-    torch = _torch()
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev.index or not t.is_contiguous():
-        _check_tensor(t, name, tuple(shape), (torch.int32,), dev)
-    return t.data_ptr()
+def _marshal():
+    global _marshal_module
+    if _marshal_module is None:
+        _torch()
+        load_library()
+        import importlib
+        try:
+            _marshal_module = importlib.import_module("._marshal", __name__)
+        except ImportError as e:
+            raise ImportError(f"{os.path.join(_HERE, '_marshal.so')} is not built for this torch; run "
+                              "__graft_entry__.build() first") from e
+    return _marshal_module
 
 
 class KVCache:
@@ -619,7 +593,7 @@ class KVCache:
             ss[-3], ss[-2], ss[-1], ss[0] if L else 0,
             SPEC_DTYPE_E4M3 if fp8 else SPEC_DTYPE_BF16, self.layers, pages, page, self.max_pages,
             heads, dim)
-        self.addr = ctypes.addressof(self.struct)
+        self.addr, self.index, self.scale = ctypes.addressof(self.struct), dev.index, dim ** -0.5
 
     def layer(self, i: int) -> "KVCache":
         """One layer of the cache (sharing its block table and error word)."""
@@ -637,35 +611,6 @@ class KVCache:
         return code
 
 
-def _heads(t, name: str, B: int, N: int, heads: int, D: int, dev) -> int:
-    """The token stride of a bfloat16 [B, N, heads, D] tensor whose tokens lie one stride
-    apart, each with its heads side by side."""
-    torch = _torch()
-    shape, (sb, sn, sh, sd) = t.shape, t.stride()
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must have dtype torch.bfloat16, got {t.dtype}")
-    if t.get_device() != dev.index:
-        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-    if shape != (B, N, heads, D):
-        raise ValueError(f"{name} must have shape {(B, N, heads, D)}, got {tuple(shape)}")
-    if sd != 1 or (sh != D and heads > 1) or (sb != N * sn and B > 1 and N > 1):
-        raise ValueError(f"{name}: heads must lie side by side and tokens one stride apart, "
-                         f"got strides {(sb, sn, sh, sd)}")
-    return sn if N > 1 else sb
-
-
-def _rows_of(t, name: str, cache: KVCache):
-    """(B, N, heads) of a [B, N, heads, head_dim] tensor that the cache has room for."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have shape (B, N, heads, {cache.head_dim}), got {tuple(t.shape)}")
-    B, N, H, _ = t.shape
-    if B > cache.batch:
-        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
-    return B, N, H
-
-
 def kv_append(cache: KVCache, q, k, v, context_lens, rope=None, *, q_weight=None, k_weight=None,
               eps: float = 1e-6, interleaved: bool = False, new_lens=None, positions=None, out=None,
               stream=None):
@@ -675,40 +620,9 @@ def kv_append(cache: KVCache, q, k, v, context_lens, rope=None, *, q_weight=None
     projection are fine.  context_lens [B] int32, rope [rows, rot_dim] float32 (cosines, then
     sines) or None, weights [head_dim] bfloat16 or None, positions [B, N] int32 or None,
     new_lens [B] int32 or None.  Returns the prepared queries [B, N, q_heads, head_dim]."""
-    torch = _torch()
-    dev, D, H = cache.device, cache.head_dim, cache.kv_heads
-    B, N, _ = _rows_of(k, "k", cache)
-    ks, vs = _heads(k, "k", B, N, H, D, dev), _heads(v, "v", B, N, H, D, dev)
-    Hq = qs = rows = rot = 0
-    qp = op = rp = qw = kw = None
-    if q is not None:
-        Hq = _rows_of(q, "q", cache)[2]
-        qs, qp = _heads(q, "q", B, N, Hq, D, dev), q.data_ptr()
-        if out is None:
-            with _under(stream):
-                out = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_tensor(out, "out", (B, N, Hq, D), (torch.bfloat16,), dev)
-        op = out.data_ptr()
-    if q_weight is not None:
-        _check_tensor(q_weight, "q_weight", (D,), (torch.bfloat16,), dev)
-        qw = q_weight.data_ptr()
-    if k_weight is not None:
-        _check_tensor(k_weight, "k_weight", (D,), (torch.bfloat16,), dev)
-        kw = k_weight.data_ptr()
-    if rope is not None:
-        _check_tensor(rope, "rope", (None, None), (torch.float32,), dev)
-        (rows, rot), rp = rope.shape, rope.data_ptr()
-    if context_lens is None:
-        raise TypeError("context_lens must be a torch tensor, got NoneType")
-    st = load_library().spec_kv_append(
-        cache.addr, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qw, kw, eps, rp, rows, rot,
-        1 if interleaved else 0, _ints(context_lens, "context_lens", (B,), dev),
-        _ints(new_lens, "new_lens", (B,), dev), _ints(positions, "positions", (B, N), dev), B, N, Hq,
-        op, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
-    if st:
-        _check(st, "spec_kv_append")
-    return out
+    return (_marshal_module or _marshal()).kv_append(
+        cache.addr, cache.batch, cache.index, q, k, v, context_lens, rope, q_weight, k_weight, eps,
+        interleaved, new_lens, positions, out, stream)
 
 
 def kv_read(cache: KVCache, T: int, *, starts=None, counts=None, dtype=None, stream=None):
@@ -716,46 +630,21 @@ def kv_read(cache: KVCache, T: int, *, starts=None, counts=None, dtype=None, str
     head_dim] of dtype (bfloat16 by default, or float32), row t holding position
     starts[b] + t for t < counts[b], zeros after that.  B is the length of starts or
     counts, or the cache's batch."""
-    torch = _torch()
-    dev = cache.device
-    if dtype is None:
-        dtype = torch.bfloat16
-    elif dtype not in _logits_dtypes():
-        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    B = cache.batch if starts is None and counts is None else (counts if starts is None else starts).shape[0]
-    if B > cache.batch:
-        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
-    shape = (B, T, cache.kv_heads, cache.head_dim)
-    with _under(stream):
-        k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
-    st = load_library().spec_kv_read(
-        cache.addr, _ints(starts, "starts", (B,), dev), _ints(counts, "counts", (B,), dev), B, T,
-        SPEC_DTYPE_F32 if dtype is torch.float32 else SPEC_DTYPE_BF16, k.data_ptr(), v.data_ptr(),
-        _raw_stream(dev.index) if stream is None else stream.cuda_stream)
-    if st:
-        _check(st, "spec_kv_read")
-    return k, v
+    f32 = False
+    if dtype is not None:
+        if dtype not in _logits_dtypes():
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        f32 = dtype == _torch().float32
+    return (_marshal_module or _marshal()).kv_read(
+        cache.addr, cache.batch, cache.index, T, starts, counts, f32, stream)
 
 
 def kv_compact(cache: KVCache, context_lens, path_nodes, num_accepted, *, stream=None) -> None:
     """Moves the accepted path of every sequence's draft tree to the front of its slots, in
     every layer (see spec_kv_compact).  path_nodes [B, N] and num_accepted [B] are
     verify_tree_greedy's."""
-    dev = cache.device
-    if path_nodes.dim() != 2:
-        raise ValueError(f"path_nodes must have shape (B, N), got {tuple(path_nodes.shape)}")
-    B, N = path_nodes.shape
-    if B > cache.batch:
-        raise ValueError(f"{B} sequences, the cache's block table has {cache.batch}")
-    st = load_library().spec_kv_compact(
-        cache.addr, _ints(context_lens, "context_lens", (B,), dev),
-        _ints(path_nodes, "path_nodes", (B, N), dev), _ints(num_accepted, "num_accepted", (B,), dev),
-        B, N, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
-    if st:
-        _check(st, "spec_kv_compact")
-
-
-_attention_need = {}
+    (_marshal_module or _marshal()).kv_compact(
+        cache.addr, cache.batch, cache.index, context_lens, path_nodes, num_accepted, stream)
 
 
 def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=None,
@@ -765,38 +654,12 @@ def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=N
     spec_paged_attention).  q [B, N, q_heads, head_dim] bfloat16, context_lens [B] int32,
     parents [B, N] int32 for draft trees (None: chains), new_lens [B] int32 or None; scale
     defaults to head_dim ** -0.5.  Returns out [B, N, q_heads, head_dim] bfloat16, with
-    lse=True also [B, N, q_heads] float32.  workspace: a zero-filled uint8 tensor of
-    spec_attention_workspace_size() bytes that only this call uses (None: one kept
-    for the device and stream)."""
-    torch = _torch()
-    dev, D, H = cache.device, cache.head_dim, cache.kv_heads
-    B, N, Hq = _rows_of(q, "q", cache)
-    qs = _heads(q, "q", B, N, Hq, D, dev)
-    if context_lens is None:
-        raise TypeError("context_lens must be a torch tensor, got NoneType")
-    lib = load_library()
-    need = _attention_need.get((N, Hq, H, D))
-    if need is None:
-        need = lib.spec_attention_workspace_size(B, N, Hq, H, D)
-        if need == 0:
-            raise ValueError(f"paged_attention: unsupported sizes N={N} q_heads={Hq} kv_heads={H} head_dim={D}")
-        _attention_need[(N, Hq, H, D)] = need
-    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
-    if out is not None:
-        _check_tensor(out, "out", (B, N, Hq, D), (torch.bfloat16,), dev)
-    with _under(stream):
-        if out is None:
-            out = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=dev)
-        e = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if lse else None
-        w = _scratch("attention", dev, h, need) if workspace is None else _given_workspace(workspace, need, dev)
-    st = lib.spec_paged_attention(
-        cache.addr, q.data_ptr(), qs, _ints(context_lens, "context_lens", (B,), dev),
-        _ints(new_lens, "new_lens", (B,), dev), _ints(parents, "parents", (B, N), dev),
-        D ** -0.5 if scale is None else scale, B, N, Hq, out.data_ptr(), e.data_ptr() if lse else None,
-        w[1], w[2], h)
-    if st:
-        _check(st, "spec_paged_attention")
-    return (out, e) if lse else out
+    lse=True also [B, N, q_heads] float32.  workspace: a uint8 tensor of
+    spec_attention_workspace_size() bytes, its first 4096 zero, that only this call uses
+    (None: one kept for the device and stream)."""
+    return (_marshal_module or _marshal()).paged_attention(
+        cache.addr, cache.batch, cache.index, q, context_lens, parents, new_lens,
+        cache.scale if scale is None else scale, lse, out, workspace, stream)
 
 
 def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, workspace=None,
@@ -804,31 +667,7 @@ def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, work
     """Log-probabilities of tokens with entropies and top alternatives (see
     spec_token_logprobs).  logits [..., V] contiguous bfloat16 or float32, tokens [...]
     int32.  Returns (logprob [...], entropy [...], top_idx [..., K] int32, top_logprob
-    [..., K]); the last two None for K = 0."""
-    torch = _torch()
-    _check_tensor(logits, "logits", (None,) * max(logits.dim(), 1), _logits_dtypes())
-    dev, shape = logits.device, logits.shape
-    lead, V = shape[:-1], shape[-1]
-    if tokens is None:
-        raise TypeError("tokens must be a torch tensor, got NoneType")
-    tp = _ints(tokens, "tokens", lead, dev)
-    rows = tokens.numel()
-    lib = load_library()
-    need = lib.spec_logprobs_workspace_size(rows, V, K)
-    if need == 0:
-        raise ValueError(f"token_logprobs: unsupported sizes rows={rows} V={V} K={K}")
-    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
-    ti = tl = ip = fp = None
-    with _under(stream):
-        lp = torch.empty(lead, dtype=torch.float32, device=dev)
-        ent = torch.empty(lead, dtype=torch.float32, device=dev)
-        if K:
-            ti = torch.empty((*lead, K), dtype=torch.int32, device=dev)
-            tl = torch.empty((*lead, K), dtype=torch.float32, device=dev)
-            ip, fp = ti.data_ptr(), tl.data_ptr()
-        w = _scratch("logprobs", dev, h, need) if workspace is None else _given_workspace(workspace, need, dev)
-    st = lib.spec_token_logprobs(logits.data_ptr(), _dtype_code(logits), tp, temperature, rows, V, K,
-                                 lp.data_ptr(), ent.data_ptr(), ip, fp, w[1], w[2], h)
-    if st:
-        _check(st, "spec_token_logprobs")
-    return lp, ent, ti, tl
+    [..., K]); the last two None for K = 0.  workspace: a uint8 tensor of
+    spec_logprobs_workspace_size() bytes, its first 256 zero (None: one kept for the
+    device and stream)."""
+    return (_marshal_module or _marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)

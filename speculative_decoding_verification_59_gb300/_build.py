@@ -3,6 +3,10 @@
 Each .cu file under csrc/ is compiled in parallel to an object file under
 _build/, then linked into a shared library next to this file.  The CUDA
 runtime is linked statically, so the library only needs the driver.
+
+_marshal.so, the torch marshalling of the calls that run on every layer
+(csrc/sv_torch.cpp), is host code: compiled beside them with g++ against the
+installed torch, linked to libspecverify.so.
 """
 from __future__ import annotations
 
@@ -17,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -32,6 +37,23 @@ def nvcc() -> str:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+
+
+def _marshal_commands():
+    """(source, object, compile command, link command) of _marshal.so."""
+    import importlib.util
+    import sysconfig
+    # the package's place without importing it (minutes on a cold machine)
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    src, obj = os.path.join(CSRC, "sv_torch.cpp"), os.path.join(BUILD, "sv_torch.o")
+    inc = [INCLUDE, os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    lib = os.path.join(torch_dir, "lib")
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", *("-I" + i for i in inc), "-c", src, "-o", obj]
+    link = ["g++", "-shared", obj, "-o", MARSHAL, "-L" + HERE, "-lspecverify", "-Wl,-rpath,$ORIGIN", "-L" + lib,
+            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return src, obj, compile_, link
 
 
 def _stale(out: str, deps) -> bool:
@@ -55,6 +77,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(" ".join(cmd), flush=True)
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
+    msrc, mobj, mcompile, mlink = _marshal_commands()
+    if force or _stale(mobj, [msrc, os.path.join(INCLUDE, "spec_verify.h")]):
+        if verbose:
+            print(" ".join(mcompile), flush=True)
+        procs.append((mcompile, subprocess.Popen(mcompile, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT, text=True)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -64,7 +92,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             failed.append((cmd, out))
     if failed:
         msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
+        raise RuntimeError("compilation failed:\n" + msg)
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -72,6 +100,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if force or _stale(MARSHAL, [mobj, LIB]):
+        tmp = MARSHAL + ".tmp%d" % os.getpid()
+        subprocess.run([tmp if x == MARSHAL else x for x in mlink], check=True)
+        os.replace(tmp, MARSHAL)
     return LIB
 
 

@@ -32,6 +32,8 @@ constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttCtasPerSm = 2;
 constexpr int kAttMaxCtas = 512;            // workspace slots are sized for this many
+constexpr size_t kAttHead = 4096;           // bytes of the workspace before the parts: counters from 256 on
+static_assert(256 + kAttMaxCtas * 4 <= kAttHead, "the counters lie in the zeroed head");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The reference m of a row moves only when a score passes it by more than
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
     int anc_b = -1, tree_bad = 0;
     const float c2 = a.scale * kLog2e;
     int* counters = reinterpret_cast<int*>(a.ws + 256);
-    float* slots = reinterpret_cast<float*>(a.ws + 256 + kAttMaxCtas * 4);
+    float* slots = reinterpret_cast<float*>(a.ws + kAttHead);
     const int srows = min(C::ROWS, RT);
     const size_t slot_floats = part_floats(srows, D);
 
@@ -759,7 +761,7 @@ size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D) {
     // a reserved block, one counter per CTA (both at a fixed place whatever the
     // call's sizes, so that no call's parts overwrite another's counters), two parts per CTA
     const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G, D);
-    return 256 + kAttMaxCtas * 4 + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
+    return kAttHead + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
 }
 
 template <int D, int MT, bool FP8>
