@@ -24,22 +24,13 @@
 // fp16 (exact) next to the matrix instruction; queries then go in as fp16,
 // each row scaled by a power of two, and a position's key scale multiplies
 // its score, its value scale its probability (as a summand of the exponent).
-#include "sv_kv.cuh"
+#include "sv_attend.cuh"
 
 namespace sv {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttCtasPerSm = 2;
-constexpr int kAttMaxCtas = 512;            // workspace slots are sized for this many
-constexpr size_t kAttHead = 4096;           // bytes of the workspace before the parts: counters from 256 on
-static_assert(256 + kAttMaxCtas * 4 <= kAttHead, "the counters lie in the zeroed head");
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// The reference m of a row moves only when a score passes it by more than
-// this (in powers of two): sums stay below 2^8 per position, and the sums in
-// registers are rarely rescaled.
-constexpr float kRefSlack = 8.f;
 
 template <int D, int MT, bool FP8>
 struct AttCfg {
@@ -64,17 +55,6 @@ struct AttCfg {
     static constexpr int SMEM = QOFF + (QSM ? MT * (D / 16) * 512 : 0);
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -105,86 +85,6 @@ __device__ __forceinline__ int swz(int t, int c) {
     else return (t * CPR + (c ^ ((t >> 1) & 3))) * 16;          // CPR = 4: two rows per 128 bytes
 }
 
-// The lengths of one sequence; bad ones read as empty.
-struct SeqLen {
-    int ctx, total;          // cached before the call, and with the new positions
-    int nb;
-    bool bad;
-};
-__device__ __forceinline__ SeqLen seq_len(const AttendArgs& a, int b) {
-    SeqLen s;
-    s.ctx = __ldg(a.ctx + b);
-    s.nb = a.newl ? __ldg(a.newl + b) : a.N;
-    s.bad = s.ctx < 0 || s.nb < 0 || s.nb > a.N || s.ctx > a.c.max_pages * a.c.page_size - s.nb;
-    s.total = s.bad || s.nb == 0 ? 0 : s.ctx + s.nb;
-    return s;
-}
-
-// Share i of `total` tiles among n CTAs begins at tile i * total / n.
-__device__ __forceinline__ long long share_begin(long long total, long long n, long long i) { return i * total / n; }
-// The CTA whose share holds tile t.
-__device__ __forceinline__ int share_of(long long total, long long n, long long t) {
-    return (int)(((t + 1) * n - 1) / total);
-}
-
-// Floats of one part of a split unit: rows sums of D, then the rows' references
-// and totals; a multiple of 16 bytes, as the parts are read and written in
-// 16-byte pieces.
-__host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * D + (2 * rows + 3) / 4 * 4; }
-
-struct AttPlan {
-    int n;                   // CTAs that take part
-    long long total;         // tiles of all units
-    int b;                   // sequence of this CTA's first tile
-    long long at;            // that sequence's first tile
-};
-
-// Sums the tiles of all sequences and finds the sequence of this CTA's first
-// tile.  Every thread takes a run of sequences.
-template <int TILE>
-__device__ __forceinline__ void make_plan(const AttendArgs& a, int units, int grid, AttPlan* out) {
-    __shared__ long long sums[kAttThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (a.B + kAttThreads - 1) / kAttThreads;
-    const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += max(1, (seq_len(a, b).total + TILE - 1) / TILE);
-    mine *= units;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttThreads / 32; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    const int n = (int)min((long long)grid, total);
-    long long at = before + incl - mine;
-    const long long first = blockIdx.x < n ? share_begin(total, n, blockIdx.x) : -1;
-    if (first >= at && first < at + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const long long t = (long long)units * max(1, (seq_len(a, b).total + TILE - 1) / TILE);
-            if (first < at + t) {
-                out->b = b;
-                out->at = at;
-                break;
-            }
-            at += t;
-        }
-    }
-    if (threadIdx.x == 0) {
-        out->n = n;
-        out->total = total;
-    }
-    __syncthreads();
-}
-
 template <int D, int MT, bool FP8>
 __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(const AttendArgs a) {
     using C = AttCfg<D, MT, FP8>;
@@ -201,13 +101,11 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
 
     const int RT = a.N * a.G;                                  // rows of a cached head
     const int RB = (RT + C::ROWS - 1) / C::ROWS;
-    const int units = a.c.kv_heads * RB;                       // of a sequence
-    make_plan<C::TILE>(a, units, gridDim.x, &plan);
+    make_plan<C::TILE, kAttThreads>(a, a.c.kv_heads * RB, gridDim.x, &plan);
     if ((int)blockIdx.x >= plan.n) return;
-    const long long t_end = share_begin(plan.total, plan.n, blockIdx.x + 1);
-    long long t = share_begin(plan.total, plan.n, blockIdx.x);
-    int b = plan.b;
-    long long seq_at = plan.at;
+    AttWalk walk;
+    walk.init(plan);
+    AttUnit un;
     int anc_b = -1, tree_bad = 0;
     const float c2 = a.scale * kLog2e;
     int* counters = reinterpret_cast<int*>(a.ws + 256);
@@ -215,19 +113,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
     const int srows = min(C::ROWS, RT);
     const size_t slot_floats = part_floats(srows, D);
 
-    while (t < t_end) {
-        const SeqLen sl = seq_len(a, b);
-        const int tiles = max(1, (sl.total + C::TILE - 1) / C::TILE);
-        if (t >= seq_at + (long long)tiles * units) {           // the share goes on in the next sequence
-            seq_at += (long long)tiles * units;
-            ++b;
-            continue;
-        }
-        const int u = (int)((t - seq_at) / tiles);              // unit of the sequence
-        const long long u_at = seq_at + (long long)u * tiles;
-        const int ta = (int)(t - u_at), tb = (int)min((long long)tiles, t_end - u_at);
-        const int hk = u / RB, r0 = (u - hk * RB) * C::ROWS;
-        const int rows = min(C::ROWS, RT - r0);
+    while (walk.next<C::TILE>(a, RB, C::ROWS, &un)) {
+        const SeqLen& sl = un.sl;
+        const int b = un.b, tiles = un.tiles, ta = un.ta, tb = un.tb, hk = un.hk, r0 = un.r0, rows = un.rows;
         __syncthreads();                                        // the unit before is done with shared memory
         if (a.par && anc_b != b) {
             // ancestors by pointer doubling: 2^6 steps cover any path of 64 nodes
@@ -343,19 +231,17 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         const int nsl = tb - ta;
         auto slice_at = [&](int i) { return ((ta + i) * kAttWarps + warp) * C::ST; };
         bool lost = false;
-        int64_t off = 0, soff = 0;                              // lane t: entry t of the next slice to copy
-        bool ok = false;
+        // Lane t finds entry t of the next slice to copy.  Its page id is loaded one
+        // slice before it is used, so that nothing waits for the table.
+        int page = -1, slot = 0;
         auto locate = [&](int i) {
             const int pos = slice_at(i) + lane;
-            ok = i < nsl && lane < C::ST && pos < sl.total;
-            if (ok) {
-                int page, slot;
-                ok = cache_place(a.c, b, pos, &page, &slot);
-                lost |= !ok;
-                off = ok ? entry_off(a.c, page, slot, hk) : 0;
-                if constexpr (FP8) soff = ok ? scale_off(a.c, page, slot, hk) : 0;
-            } else {
-                off = soff = 0;
+            page = -1;
+            if (i < nsl && lane < C::ST && pos < sl.total) {
+                const int pg = pos / a.c.page_size;
+                slot = pos - pg * a.c.page_size;
+                page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)b * a.c.max_pages + pg) : -2;
+                if (page == -1) page = -2;                      // -1: no position
             }
         };
         auto copy = [&](int i) {                                // slice i, located before
@@ -363,6 +249,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 const uint32_t st = ring_s + (i % C::NS) * C::STAGE;
                 constexpr int RP = 32 / C::CPR;                // rows the warp copies at once
                 const int ch = lane % C::CPR, sub = lane / C::CPR;
+                const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
+                lost |= !ok && page != -1;
+                const int64_t off = ok ? entry_off(a.c, page, slot, hk) : 0;
                 const unsigned okm = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
                 for (int p = 0; p < C::ST / RP; ++p) {
@@ -376,6 +265,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 if constexpr (FP8) {
                     if (lane < C::ST) {
                         const uint32_t d = st + 2 * C::ST * C::ROWB + lane * 4;
+                        const int64_t soff = ok ? scale_off(a.c, page, slot, hk) : 0;
                         cp4(d, a.c.k_scale + soff, ok);
                         cp4(d + C::ST * 4, a.c.v_scale + soff, ok);
                     }
@@ -671,18 +561,8 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) bad |= wbad[w] != 0;
         const bool whole = ta == 0 && tb == tiles;
-        const int slot = 2 * (int)blockIdx.x + (ta == 0 ? 1 : 0);
-        float* sp = slots + (size_t)slot * slot_floats;
-        auto put = [&](int r, int d, float4 x, float lsum, float mref) {
-            // row r, elements d .. d + 3 of the whole unit
-            const int R = r0 + r, n = R / a.G, g = R - n * a.G;
-            const size_t row = ((size_t)b * a.N + n) * a.Hq + (size_t)hk * a.G + g;
-            const bool empty = n >= sl.nb && !bad;
-            const float f = empty ? 0.f : 1.f / lsum;
-            if (empty) x = make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
-            if (a.lse && d == 0) a.lse[row] = empty ? kNegInf : (mref + __log2f(lsum)) * kLn2;
-        };
+        const int mine = 2 * (int)blockIdx.x + (ta == 0 ? 1 : 0);
+        float* sp = slots + (size_t)mine * slot_floats;
         for (int i = threadIdx.x; i < rows * (D / 4); i += kAttThreads) {
             const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
             float M = kNegInf;
@@ -703,7 +583,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             }
             if (bad) L = CUDART_NAN_F;
             if (whole) {
-                put(r, d, x, L, M);
+                put_row(a, un, bad, D, r, d, x, L, M);
             } else {
                 __stcg(reinterpret_cast<float4*>(sp + (size_t)r * D + d), x);
                 if (d == 0) {
@@ -714,7 +594,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         }
         if (!whole) {
             // ---- the unit's CTAs: c0 begins it, c1 ends it; the last to arrive adds the parts
-            const int c0 = share_of(plan.total, plan.n, u_at), c1 = share_of(plan.total, plan.n, u_at + tiles - 1);
+            const int c0 = share_of(plan.total, plan.n, un.at), c1 = share_of(plan.total, plan.n, un.at + tiles - 1);
             int* counter = counters + c0;                      // no CTA begins two units that others end
             __threadfence();
             __syncthreads();
@@ -726,31 +606,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             __syncthreads();
             if (last_cta) {
                 __threadfence();
-                const int parts = c1 - c0 + 1;
-                auto part = [&](int p) { return slots + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
-                for (int i = threadIdx.x; i < rows * (D / 4); i += kAttThreads) {
-                    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
-                    float M = kNegInf;
-                    for (int p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(part(p) + (size_t)srows * D + r));
-                    const float Ms = M == kNegInf ? 0.f : M;
-                    float L = 0.f;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int p = 0; p < parts; ++p) {
-                        const float* q = part(p);
-                        const float f = ex2_approx(__ldcg(q + (size_t)srows * D + r) - Ms);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(q + (size_t)r * D + d));
-                        L = fmaf(f, __ldcg(q + (size_t)srows * (D + 1) + r), L);
-                        x.x = fmaf(f, y.x, x.x);
-                        x.y = fmaf(f, y.y, x.y);
-                        x.z = fmaf(f, y.z, x.z);
-                        x.w = fmaf(f, y.w, x.w);
-                    }
-                    put(r, d, x, L, M);
-                }
+                join_parts<D, kAttThreads>(a, un, threadIdx.x, slots, slot_floats, srows, c0, c1, 0, rows);
             }
         }
-        t = u_at + tb;
     }
 }
 
@@ -761,6 +619,7 @@ size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D) {
     // a reserved block, one counter per CTA (both at a fixed place whatever the
     // call's sizes, so that no call's parts overwrite another's counters), two parts per CTA
     const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G, D);
+    if (attend_takes_tc(N, G, D)) return attend_tc_workspace(N, G);
     return kAttHead + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
 }
 
@@ -798,6 +657,7 @@ static cudaError_t launch_attend_d(const AttendArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const bool f8 = a.c.dtype == SPEC_DTYPE_E4M3;
+    if (attend_takes_tc(a.N, a.G, a.c.head_dim)) return launch_attend_tc(a, st);
     switch (a.c.head_dim) {
         case 64: return f8 ? launch_attend_d<64, true>(a, st) : launch_attend_d<64, false>(a, st);
         case 128: return f8 ? launch_attend_d<128, true>(a, st) : launch_attend_d<128, false>(a, st);

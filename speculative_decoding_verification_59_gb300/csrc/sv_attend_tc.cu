@@ -1,0 +1,801 @@
+// Paged attention on the fifth-generation tensor cores, for heads of 128
+// elements: the same units, shares and join as sv_attend.cu, with the two
+// products as tcgen05.mma and the accumulators in tensor memory.
+//
+// Both products are taken transposed, so that the 128 positions of a tile and
+// the 128 elements of a head are the 128 rows that the instruction wants, and the
+// few query rows its free dimension N (a multiple of 16 up to 160):
+//   S^T [positions x rows] = K [positions x 128] Q^T,
+//   O^T [elements x rows] += V^T [elements x positions] P^T.
+// K and V lie in shared memory as they come from the cache (128-byte swizzled
+// rows of 64 elements); V is the transposed operand.  A thread of the softmax
+// warps owns one position, that is one lane of tensor memory: its key and value
+// scales are scalars, it reads its scores of all rows, and writes its
+// probabilities as one row of P.
+//
+// The warps of a CTA, one CTA per SM, each walking the CTA's share:
+//   softmax   4 warps (8 from 65 rows on, each 4 taking half of the rows)
+//   MMA       1 thread issues every tcgen05.mma
+//   loaders   4 warps gather K and V through the page table with 16-byte
+//             cp.async into a ring of 32 KB buffers, three to four in flight, and the
+//             queries; an E4M3 cache's rows are widened to fp16 on the way (a
+//             chunk by the thread that copied it; 8 warps where registers allow).
+// Scores pass through two buffers in tensor memory, so the next tile's first
+// product runs beside this tile's softmax.
+//
+// The running reference m_r of a row is common to the CTA's positions, so a
+// new one would need a maximum over 128 threads for every row and tile.  A tile
+// only asks whether any score passes its row's reference by 2^8 (one maximum
+// per score, one barrier vote); the rows' maxima, the new references and the
+// rescaling of O run when one does: on a unit's first tile, and rarely after.
+#include "sv_attend.cuh"
+#include "sv_tma.cuh"
+
+namespace sv {
+
+constexpr int kTcTile = 128;
+constexpr int kTcD = 128;
+constexpr int kTcBuf = kTcTile * kTcD * 2;       // a tile's keys or values as the products read them: 32 KB
+constexpr int kTcRaw = kTcTile * kTcD;           // the same as the cache's 8-bit rows: 16 KB
+constexpr int kTcScaleRing = 8;                  // tiles whose scales are held
+// The loaders run at most 6 units ahead of the softmax (raw and widened buffers,
+// two score buffers), so what they tell it by unit is kept for 8.
+constexpr int kTcUnitRing = 8;
+constexpr int kTcMaxCtas = 256;                  // two counters each fit the workspace's head
+constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
+
+template <int CH, int NSM, bool FP8>
+struct TcCfg {
+    static constexpr int COLS = CH * 16;         // rows of a softmax warpgroup
+    static constexpr int RP = NSM * COLS;        // rows of a unit, at most
+    static constexpr int PB = (RP + 63) / 64;    // 64-row blocks of P
+    static constexpr int QB = RP <= 32 || (RP <= 64 && !FP8) ? 2 : 1;    // units whose queries are held
+    static constexpr int NBUF = FP8 ? (RP > 64 ? 3 : 4) : (RP > 64 ? 4 : 5);
+    static constexpr int NRAW = FP8 ? (RP > 64 ? 2 : 3) : 0;
+    static constexpr int SM_THREADS = NSM * 128;
+    static constexpr int LOADERS = FP8 && NSM == 1 ? 256 : 128;
+    static constexpr int THREADS = SM_THREADS + 32 + LOADERS;
+    static constexpr int P_OFF = NBUF * kTcBuf;
+    static constexpr int Q_OFF = P_OFF + PB * 16384;
+    static constexpr int QBYTES = RP * 256;
+    static constexpr int RAW_OFF = Q_OFF + QB * QBYTES;
+    static constexpr int SCALE_OFF = RAW_OFF + NRAW * kTcRaw;
+    static constexpr int SMEM = SCALE_OFF + (FP8 ? kTcScaleRing * 2 * kTcTile * 4 : 0) + 1024;   // and room to align
+    static constexpr int TMEM = 3 * RP <= 64 ? 64 : 3 * RP <= 128 ? 128 : 3 * RP <= 256 ? 256 : 512;
+};
+
+// ---- tcgen05 in inline PTX ------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t at, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Arrives on the barrier when every tcgen05.mma issued so far has completed.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 16 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tc_ld16(uint32_t at, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+    tc_wait_st();
+}
+
+// Shared-memory operand with 128-byte swizzled rows.  K-major (the contraction
+// contiguous): sbo is the step between groups of 8 rows.  MN-major: lbo the step
+// between blocks of 64 elements of the other dimension, sbo between groups of 8
+// steps of the contraction.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// Instruction descriptor: fp32 accumulators, both operands bf16 (or fp16),
+// M = 128, N = n; ta / tb: that operand is MN-major.
+__device__ __forceinline__ uint32_t tc_idesc(bool f16, bool ta, bool tb, int n) {
+    const uint32_t t = f16 ? 0u : 1u;
+    return 1u << 4 | t << 7 | t << 10 | (uint32_t)ta << 15 | (uint32_t)tb << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
+// Byte offset of chunk c (16 bytes of 16) of row t in a tile of 128 rows of
+// 256 bytes kept as two blocks of 128-byte swizzled half rows.
+__device__ __forceinline__ int tc_off(int t, int c) { return (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4); }
+
+// ORs e4m3's not-a-number pattern test over a word.
+__device__ __forceinline__ bool has_odd_e4m3(uint32_t y) {
+    bool x = false;
+#pragma unroll
+    for (int q = 0; q < 32; q += 8) x |= ((y >> q) & 0x7fu) == 0x7fu;
+    return x;
+}
+
+template <int CH, int NSM, bool FP8>
+__global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, uint32_t limit) {
+    using C = TcCfg<CH, NSM, FP8>;
+    constexpr int RP = C::RP, NBUF = C::NBUF;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ AttPlan plan;
+    __shared__ __align__(8) uint64_t full[NBUF], empty[NBUF], s_full[2], s_free[2], p_full, pv_done, q_full[C::QB], q_free[C::QB];
+    __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
+    __shared__ float wred[NSM * 4][C::COLS];
+    __shared__ short rown[RP];                                  // new position of a row
+    __shared__ unsigned long long desc_bits[NSM][kMaxNewTree]; // a node's descendants and itself
+    __shared__ uint32_t tmem_at;
+    __shared__ int unit_bad[NSM][kTcUnitRing];                  // a page that is none
+    __shared__ float unit_qinv[kTcUnitRing];                    // E4M3: what takes back the queries' scaling
+    __shared__ int odd_any, last_cta[NSM], tree_bad[NSM];
+    __shared__ __align__(8) uint64_t drained;
+    unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kMmaWarp = C::SM_THREADS / 32;
+
+    if (tid == 0) {
+        for (int i = 0; i < NBUF; ++i) {
+            mbar_init(&full[i], C::LOADERS / 32);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_free[i], C::SM_THREADS / 32);
+        }
+        mbar_init(&p_full, C::SM_THREADS / 32);
+        mbar_init(&pv_done, 1);
+        for (int i = 0; i < C::QB; ++i) {
+            mbar_init(&q_full[i], C::LOADERS / 32);
+            mbar_init(&q_free[i], 1);
+        }
+        mbar_init(&drained, 1);
+        mbar_init_fence();
+        odd_any = 0;
+        for (int i = 0; i < NSM * kTcUnitRing; ++i) unit_bad[0][i] = 0;
+    }
+    if (warp == kMmaWarp) tc_alloc(&tmem_at, C::TMEM);
+    pdl_trigger();
+    pdl_wait();
+    const int RB = (a.N * a.G + block_rows - 1) / block_rows;
+    tc_before();
+    make_plan<kTcTile, C::THREADS>(a, a.c.kv_heads * RB, gridDim.x, &plan);   // ends in a barrier
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    AttWalk walk;
+    AttUnit un;
+    if ((int)blockIdx.x < plan.n) {
+        walk.init(plan);
+    } else {
+        walk.t = walk.end = 0;
+        walk.seq_at = 0;
+        walk.b = 0;
+    }
+
+    if (warp > kMmaWarp) {
+        // ================= loaders =================
+        const int lt = tid - C::SM_THREADS - 32, lw = lt >> 5;
+        constexpr int LW = C::LOADERS / 32;
+        constexpr int CPR = FP8 ? 8 : 16;                      // 16-byte chunks of a cached row
+        constexpr int RPI = 32 / CPR;                          // rows a warp copies at once
+        constexpr int WROWS = kTcTile / LW;                    // rows of a tile that a warp copies
+        constexpr int PIECES = WROWS / RPI;                    // of 16 bytes a thread
+        // buffers in flight behind the one being issued
+        constexpr int LAG = FP8 ? C::NRAW - 1 : NBUF - 2;
+        const int ch = lane % CPR, sub = lane / CPR;
+        bool ok = true;
+        unsigned q = 0;                                        // buffers issued (keys and values in turn)
+        unsigned uc = 0;                                       // units
+        unsigned done = 0;                                     // buffers handed over
+        struct Flight {                                        // what handing one over needs
+            int p0, ctx, total;
+            bool val;
+        };
+        Flight fl[LAG + 1];
+        auto finish = [&](unsigned j, const Flight& f) {       // buffer j has landed: (widen and) hand it over
+            unsigned char* dst = smem + (j % NBUF) * kTcBuf;
+            if constexpr (FP8) {
+                if (ok && j >= (unsigned)NBUF) ok = wait_bounded(&empty[j % NBUF], (j / NBUF - 1) & 1u, limit);
+                const unsigned char* raw = smem + C::RAW_OFF + (j % C::NRAW) * kTcRaw;
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+                    const int row = lw * WROWS + p * RPI + sub;
+                    uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ch * 16);
+                    if (f.val && f.p0 + row >= f.ctx && f.p0 + row < f.total &&
+                        (has_odd_e4m3(w.x) || has_odd_e4m3(w.y) || has_odd_e4m3(w.z) || has_odd_e4m3(w.w))) {
+                        odd_any = 1;                           // rare: see the epilogue
+                        uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int s = 0; s < 32; s += 8)
+                                if (((y[i] >> s) & 0x7fu) == 0x7fu) y[i] &= ~(0xffu << s);
+                        w = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                    uint4 lo, hi;
+                    lo.x = e4m3_to_f16x2(w.x & 0xffffu);
+                    lo.y = e4m3_to_f16x2(w.x >> 16);
+                    lo.z = e4m3_to_f16x2(w.y & 0xffffu);
+                    lo.w = e4m3_to_f16x2(w.y >> 16);
+                    hi.x = e4m3_to_f16x2(w.z & 0xffffu);
+                    hi.y = e4m3_to_f16x2(w.z >> 16);
+                    hi.z = e4m3_to_f16x2(w.w & 0xffffu);
+                    hi.w = e4m3_to_f16x2(w.w >> 16);
+                    *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch)) = lo;
+                    *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch + 1)) = hi;
+                }
+            } else {
+                if (f.val && f.p0 + kTcTile > f.ctx) {         // new positions: values that are no numbers
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        const int row = lw * WROWS + p * RPI + sub;
+                        if (f.p0 + row < f.ctx || f.p0 + row >= f.total) continue;
+                        uint32_t* at = reinterpret_cast<uint32_t*>(dst + tc_off(row, ch));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t y = at[i];
+                            if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[i] = y; }
+                            if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[i] = y; }
+                        }
+                    }
+                }
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[j % NBUF]);
+        };
+        while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
+            // ---- the unit's queries
+            const int qb = (int)(uc % C::QB);
+            if (C::QB == 1 && done < q) {                      // what frees them are the keys still in flight
+                cp_wait<0>();
+                for (; done < q && ok; ++done) finish(done, fl[done % (LAG + 1)]);
+            }
+            if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            unsigned char* qs = smem + C::Q_OFF + qb * C::QBYTES;
+            float qscale = 1.f;
+            auto query_row = [&](int r) {
+                const int R = un.r0 + r, n = R / a.G, g = R - n * a.G;
+                return a.q + ((int64_t)un.b * a.N + n) * a.qs + ((size_t)un.hk * a.G + g) * kTcD * 2;
+            };
+            if constexpr (FP8) {
+                // fp16 queries, scaled by one power of two so that the unit's largest
+                // element is in [2^12, 2^13): exact down to 2^-26 of it.  Every warp
+                // finds the maximum by itself.
+                float mx = 0.f;
+                for (int i = lane; i < un.rows * 16; i += 32) {
+                    float x[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(query_row(i >> 4)) + (i & 15)), x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]) < CUDART_INF_F ? fabsf(x[j]) : 0.f);
+                }
+                mx = warp_max(mx);
+                const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 139 - ex;
+                qscale = __uint_as_float((uint32_t)(127 + sh) << 23);
+                if (lt == 0) unit_qinv[uc % kTcUnitRing] = __uint_as_float((uint32_t)(127 - sh) << 23);
+            }
+            for (int i = lt; i < rp * 16; i += C::LOADERS) {
+                const int r = i >> 4, c16 = i & 15;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (r < un.rows) {
+                    w = __ldg(reinterpret_cast<const uint4*>(query_row(r)) + c16);
+                    if constexpr (FP8) {
+                        float x[8];
+                        unpack8(w, x);
+                        w = make_uint4(pack_f16(x[0] * qscale, x[1] * qscale), pack_f16(x[2] * qscale, x[3] * qscale),
+                                       pack_f16(x[4] * qscale, x[5] * qscale), pack_f16(x[6] * qscale, x[7] * qscale));
+                    }
+                }
+                *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w;
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[qb]);
+
+            // ---- the unit's tiles; a lane finds the page of one of the warp's rows, one
+            // tile before it is used
+            int page = -1, slot = 0;
+            auto locate = [&](int i) {
+                const int pos = i * kTcTile + lw * WROWS + lane;
+                page = -1;
+                if (i < un.tb && lane < WROWS && pos < un.sl.total) {
+                    const int pg = pos / a.c.page_size;
+                    slot = pos - pg * a.c.page_size;
+                    page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -2;
+                    if (page == -1) page = -2;                  // -1: no position
+                }
+            };
+            locate(un.ta);
+            for (int i = un.ta; i < un.tb && ok; ++i) {
+                const bool have = (unsigned)page < (unsigned)a.c.num_pages;
+                if (__any_sync(0xffffffffu, !have && page != -1) && lane == 0) {
+#pragma unroll
+                    for (int w = 0; w < NSM; ++w) unit_bad[w][uc % kTcUnitRing] = 1;
+                    raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+                }
+                const int64_t off = have ? entry_off(a.c, page, slot, un.hk) : 0;
+                const int64_t soff = FP8 && have ? scale_off(a.c, page, slot, un.hk) : 0;
+                const unsigned havem = __ballot_sync(0xffffffffu, have);
+                locate(i + 1);
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint32_t dst;
+                    if constexpr (FP8) {
+                        dst = smem_addr(smem + C::RAW_OFF + (q % C::NRAW) * kTcRaw);
+                    } else {
+                        if (q >= (unsigned)NBUF && !wait_bounded(&empty[q % NBUF], (q / NBUF - 1) & 1u, limit)) ok = false;
+                        dst = smem_addr(smem + (q % NBUF) * kTcBuf);
+                    }
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    const char* base = static_cast<const char*>(kv ? a.c.v : a.c.k);
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        const int wr = p * RPI + sub, row = lw * WROWS + wr;
+                        const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
+                        cp16(dst + (FP8 ? row * 128 + ch * 16 : tc_off(row, ch)), base + e, (havem >> wr) & 1u);
+                    }
+                    if constexpr (FP8) {
+                        if (kv == 0 && lane < WROWS) {          // both scales: the softmax wants them with the scores
+                            const uint32_t at = smem_addr(smem + C::SCALE_OFF) +
+                                                (((q >> 1) % kTcScaleRing) * 2 * kTcTile + lw * WROWS + lane) * 4;
+                            cp4(at, a.c.k_scale + soff, have);
+                            cp4(at + kTcTile * 4, a.c.v_scale + soff, have);
+                        }
+                    }
+                    cp_commit();
+                    fl[q % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total, kv == 1};
+                    ++q;
+                    if (q - done > (unsigned)LAG) {
+                        cp_wait<LAG>();
+                        finish(done, fl[done % (LAG + 1)]);
+                        ++done;
+                    }
+                }
+            }
+            ++uc;
+        }
+        // ---- the buffers still in flight
+        cp_wait<0>();
+        for (; done < q && ok; ++done) finish(done, fl[done % (LAG + 1)]);
+        if (!ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+    } else if (warp == kMmaWarp) {
+        // ================= the products =================
+        if (lane == 0) {
+            const uint32_t id_qk = tc_idesc(FP8, false, false, rp), id_pv = tc_idesc(FP8, true, true, rp);
+            const uint32_t base = smem_addr(smem);
+            bool ok = true;
+            unsigned g = 0, uc = 0;                            // tiles, units whose first product was issued
+            auto scores = [&](int qb, bool first, bool last) { // S of tile g
+                if (first && !wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit)) return false;
+                const unsigned kb = 2 * g;
+                if (!wait_bounded(&full[kb % NBUF], (kb / NBUF) & 1u, limit)) return false;
+                if (g >= 2 && !wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit)) return false;
+                tc_after();
+                const uint32_t k0 = base + (kb % NBUF) * kTcBuf, q0 = base + C::Q_OFF + qb * C::QBYTES;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc_mma(tmem + (g & 1) * RP, tc_desc(k0 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                           tc_desc(q0 + (ks >> 2) * (RP * 128) + (ks & 3) * 32, 16, 1024), id_qk, ks > 0);
+                tc_commit(&empty[kb % NBUF]);
+                tc_commit(&s_full[g & 1]);
+                if (last) tc_commit(&q_free[qb]);
+                return true;
+            };
+            auto sums = [&](unsigned t, bool first) {           // O += V P of tile t
+                const unsigned vb = 2 * t + 1;
+                if (!wait_bounded(&full[vb % NBUF], (vb / NBUF) & 1u, limit)) return false;
+                if (!wait_bounded(&p_full, t & 1u, limit)) return false;
+                tc_after();
+                const uint32_t v0 = base + (vb % NBUF) * kTcBuf, p0 = base + C::P_OFF;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc_mma(tmem + 2 * RP, tc_desc(v0 + ks * 2048, 16384, 1024), tc_desc(p0 + ks * 2048, 16384, 1024), id_pv,
+                           !(first && ks == 0));
+                tc_commit(&empty[vb % NBUF]);
+                tc_commit(&pv_done);
+                return true;
+            };
+            bool pend = false, pend_first = false;
+            while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
+                for (int i = un.ta; i < un.tb && ok; ++i) {
+                    ok = scores((int)(uc % C::QB), i == un.ta, i + 1 == un.tb);
+                    if (ok && pend) ok = sums(g - 1, pend_first);
+                    pend = true;
+                    pend_first = i == un.ta;
+                    ++g;
+                }
+                ++uc;
+            }
+            if (ok && pend) ok = sums(g - 1, pend_first);
+            // every product must have ended before tensor memory is given back
+            tc_commit(&drained);
+            if (!wait_bounded(&drained, 0) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax =================
+        const int wg = NSM > 1 ? warp >> 2 : 0;
+        const int row = tid & 127;                             // position of a tile; element of a head
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const int c0 = wg * C::COLS;                           // first row of the warpgroup
+        const int chunks = min(CH, max(0, (rp - c0 + 15) / 16));
+        const int bar = 1 + wg;
+        float* slots = reinterpret_cast<float*>(a.ws + kAttHead);
+        int* counters = reinterpret_cast<int*>(a.ws + 256);
+        const int srows = min(block_rows, a.N * a.G);
+        const size_t slot_floats = part_floats(srows, kTcD);
+        unsigned g = 0, uc = 0;
+        int tree_b = -1;
+        bool dead = false;                                     // a wait ran out: the same for the warpgroup,
+        bool late = false;                                     // once it has voted on this
+        float l[CH * 16];
+        while (walk.next<kTcTile>(a, RB, block_rows, &un)) {
+            const SeqLen& sl = un.sl;
+            // ---- the unit's rows, and who sees whom
+            named_sync(bar, 128);                              // the unit before is done with the tables
+            if (a.par && tree_b != un.b) {
+                // descendants: every node adds itself to each of its ancestors
+                int wrong = 0;
+                if (row < a.N) desc_bits[wg][row] = 0ull;
+                if (row == 0) tree_bad[wg] = 0;
+                named_sync(bar, 128);
+                if (row < a.N) {
+                    const int32_t* par = a.par + (size_t)un.b * a.N;
+                    const int p = __ldg(par + row);
+                    wrong = row < sl.nb && (row == 0 ? p != -1 : (p < 0 || p >= row));
+                    int at = row;
+                    for (int k = 0; k < kMaxNewTree && at >= 0; ++k) {
+                        atomicOr(&desc_bits[wg][at], 1ull << row);
+                        const int up = at == 0 || at >= sl.nb ? -1 : __ldg(par + at);
+                        at = up < at ? up : -1;
+                    }
+                    if (wrong) {
+                        tree_bad[wg] = 1;
+                        raise_error(a.c.error, SPEC_DEVERR_TREE_PARENT);
+                    }
+                }
+                tree_b = un.b;
+            }
+            if (sl.bad && tid == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+            if (row < C::COLS) {
+                rown[c0 + row] = (short)((un.r0 + min(c0 + row, un.rows - 1)) / a.G);
+                nref[c0 + row] = -kNoRef;
+            }
+            const float c2 = a.scale * kLog2e;
+#pragma unroll
+            for (int j = 0; j < CH * 16; ++j) l[j] = 0.f;
+            named_sync(bar, 128);
+
+            for (int i = un.ta; i < un.tb && !dead; ++i, ++g) {
+                const int p0 = i * kTcTile, pos = p0 + row;
+                const bool masked = p0 + kTcTile > sl.ctx;     // uniform: new positions, or past the end
+                const int d = pos - sl.ctx;
+                const bool gone = pos >= sl.total;
+                unsigned long long seen = 0ull;                // tree: the nodes that see this position
+                if (masked && a.par && d >= 0 && !gone) seen = desc_bits[wg][d & 63];
+                bool ok = wait_bounded(&s_full[g & 1], (g >> 1) & 1u, limit);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_after();
+                float f = c2, add = 0.f, vinv = 0.f;
+                if constexpr (FP8) {
+                    const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + (g % kTcScaleRing) * 2 * kTcTile;
+                    f = c2 * unit_qinv[uc % kTcUnitRing] * sc[row];
+                    add = __log2f(sc[kTcTile + row]);
+                    vinv = 1.f / sc[kTcTile + row];
+                }
+                // row r's score in powers of two, plus nr (less its reference)
+                auto arg = [&](float s, int r, float nr) {
+                    float x = FP8 ? fmaf(s, f, add + nr) : fmaf(s, f, nr);
+                    if (masked) {
+                        const bool sees = d < 0 || (!gone && (a.par ? (seen >> rown[r]) & 1ull : d <= rown[r]));
+                        x = sees ? x : kNegInf;
+                    }
+                    return x;
+                };
+                const uint32_t s_at = lanes + (g & 1) * RP + c0;
+                float top = kNegInf;
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch)
+                    if (ch < chunks) {
+                        float v[16];
+                        tc_ld16(s_at + ch * 16, v);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const int r = c0 + ch * 16 + j;
+                            const float4 nr = *reinterpret_cast<const float4*>(&nref[r]);
+                            top = fmaxf(top, fmaxf(fmaxf(arg(v[j], r, nr.x), arg(v[j + 1], r + 1, nr.y)),
+                                                   fmaxf(arg(v[j + 2], r + 2, nr.z), arg(v[j + 3], r + 3, nr.w))));
+                        }
+                    }
+                const bool first = i == un.ta;
+                ok = ok && !late;
+                if (named_any(bar, 128, !ok || top > kRefSlack)) {
+                    // ---- new references (or a wait that ran out)
+                    if (!first && ok) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);    // O is at rest
+                    if (named_any(bar, 128, !ok)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_after();
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch < chunks) {
+                            float v[16];
+                            tc_ld16(s_at + ch * 16, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float x = warp_max(arg(v[j], c0 + ch * 16 + j, 0.f));
+                                if (lane == 0) wred[warp][ch * 16 + j] = x;
+                            }
+                        }
+                    named_sync(bar, 128);
+                    if (row < chunks * 16) {
+                        const int w0 = wg * 4;
+                        const float x = fmaxf(fmaxf(wred[w0][row], wred[w0 + 1][row]), fmaxf(wred[w0 + 2][row], wred[w0 + 3][row]));
+                        const float m = -nref[c0 + row];
+                        const bool up = x > m + kRefSlack;
+                        nref[c0 + row] = up ? -x : -m;
+                        alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - x);
+                    }
+                    named_sync(bar, 128);
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch < chunks) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) l[ch * 16 + j] *= alpha[c0 + ch * 16 + j];
+                            if (!first) {
+                                float v[16];
+                                tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] *= alpha[c0 + ch * 16 + j];
+                                tc_st16(lanes + 2 * RP + c0 + ch * 16, v);
+                            }
+                        }
+                }
+                // ---- probabilities; P is free once the tile before has been summed
+                if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
+                late = !ok;
+                unsigned char* prow = smem + C::P_OFF + row * 128;
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch)
+                    if (ch < chunks) {
+                        float v[16];
+                        tc_ld16(s_at + ch * 16, v);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const int r = c0 + ch * 16 + j;
+                            const float4 nr = *reinterpret_cast<const float4*>(&nref[r]);
+                            v[j] = ex2_approx(arg(v[j], r, nr.x));
+                            v[j + 1] = ex2_approx(arg(v[j + 1], r + 1, nr.y));
+                            v[j + 2] = ex2_approx(arg(v[j + 2], r + 2, nr.z));
+                            v[j + 3] = ex2_approx(arg(v[j + 3], r + 3, nr.w));
+                        }
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if constexpr (FP8) l[ch * 16 + j] += v[j] != 0.f ? v[j] * vinv : 0.f;   // a masked scale may be anything
+                            else l[ch * 16 + j] += v[j];
+                            if (j & 1) w[j >> 1] = FP8 ? pack_f16(v[j - 1], v[j]) : pack_bf16(v[j - 1], v[j]);
+                        }
+                        const int c = c0 + ch * 16;
+                        unsigned char* at = prow + (c >> 6) * 16384;
+                        const int k = (c & 63) >> 3;
+                        *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                proxy_fence();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s_free[g & 1]);
+                    mbar_arrive(&p_full);
+                }
+            }
+
+            // ---- the unit's end
+            bool ok = !dead && !late;
+            if (ok) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
+            dead = named_any(bar, 128, !ok);
+            tc_after();
+            // totals: over the lanes, then over the four warps
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+                if (ch < chunks) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float x = warp_sum(l[ch * 16 + j]);
+                        if (lane == 0) wred[warp][ch * 16 + j] = x;
+                    }
+                }
+            named_sync(bar, 128);
+            const bool bad = sl.bad || (a.par && tree_bad[wg]) || unit_bad[wg][uc % kTcUnitRing] || dead;
+            const int mine = min(chunks * 16, un.rows - c0);   // rows of the warpgroup (may be none)
+            float lsum = 0.f;
+            if (row < mine) {
+                const int w0 = wg * 4;
+                lsum = (wred[w0][row] + wred[w0 + 1][row]) + (wred[w0 + 2][row] + wred[w0 + 3][row]);
+                if (bad) lsum = CUDART_NAN_F;
+            }
+            const bool whole = un.ta == 0 && un.tb == un.tiles;
+            float* sp = slots + (size_t)(2 * (int)blockIdx.x + (un.ta == 0 ? 1 : 0)) * slot_floats;
+            if (row < mine) {                                  // thread r: row r's totals
+                const int r = c0 + row, R = un.r0 + r, n = R / a.G;
+                const float m = -nref[r];
+                if (whole) {
+                    const bool none = n >= sl.nb && !bad;
+                    alpha[r] = none ? 0.f : 1.f / lsum;
+                    if (a.lse) {
+                        const size_t at = ((size_t)un.b * a.N + n) * a.Hq + (size_t)un.hk * a.G + (R - n * a.G);
+                        a.lse[at] = none ? kNegInf : (m + __log2f(lsum)) * kLn2;
+                    }
+                } else {
+                    // a row that has seen nothing joins with weight zero
+                    __stcg(sp + (size_t)srows * kTcD + r, m == kNoRef && !bad ? kNegInf : m);
+                    __stcg(sp + (size_t)srows * (kTcD + 1) + r, lsum);
+                }
+            }
+            named_sync(bar, 128);
+            if (row == 0) unit_bad[wg][uc % kTcUnitRing] = 0;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+                if (ch * 16 < mine) {
+                    float v[16];
+                    tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
+                    if (odd_any) {
+                        // Rare: some new position's value was no number.  The loaders zeroed
+                        // it, so that it does not spoil the rows that mask it; those that
+                        // see it get it here.
+                        const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
+                        for (int j = j0; j < j1; ++j) {
+                            int page, slot;
+                            if (!cache_place(a.c, un.b, j, &page, &slot)) continue;
+                            const int64_t off = entry_off(a.c, page, slot, un.hk) + row;
+                            float x;
+                            if constexpr (FP8) {
+                                float unused;
+                                f16x2_to_f32(e4m3_to_f16x2(static_cast<const unsigned char*>(a.c.v)[off]), &x, &unused);
+                            } else {
+                                x = __uint_as_float((uint32_t)static_cast<const unsigned short*>(a.c.v)[off] << 16);
+                            }
+                            if (fabsf(x) < CUDART_INF_F) continue;
+                            const int d = j - sl.ctx;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int n = rown[c0 + ch * 16 + k];
+                                if (a.par ? (desc_bits[wg][d & 63] >> n) & 1ull : d <= n) v[k] += x;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int r = c0 + ch * 16 + j;
+                        if (ch * 16 + j < mine) {
+                            if (whole) {
+                                const int R = un.r0 + r, n = rown[r], gq = R - n * a.G;
+                                const size_t at = ((size_t)un.b * a.N + n) * a.Hq + (size_t)un.hk * a.G + gq;
+                                const float y = n >= sl.nb && !bad ? 0.f : v[j] * alpha[r];
+                                reinterpret_cast<unsigned short*>(a.out)[at * kTcD + row] = (unsigned short)(pack_bf16(y, 0.f) & 0xffffu);
+                            } else {
+                                __stcg(sp + (size_t)r * kTcD + row, v[j]);
+                            }
+                        }
+                    }
+                }
+            tc_before();
+            if (!whole && mine > 0) {
+                // the unit's CTAs: c0 begins it, c1 ends it; the last warpgroup to arrive adds
+                // its rows' parts
+                const int f0 = share_of(plan.total, plan.n, un.at), f1 = share_of(plan.total, plan.n, un.at + un.tiles - 1);
+                int* counter = counters + 2 * f0 + wg;         // no CTA begins two units that others end
+                __threadfence();
+                named_sync(bar, 128);
+                if (row == 0) {
+                    const int got = atomicAdd(counter, 1);
+                    last_cta[wg] = got == f1 - f0;
+                    if (last_cta[wg]) *counter = 0;            // as the next call finds it
+                }
+                named_sync(bar, 128);
+                if (last_cta[wg]) {
+                    __threadfence();
+                    join_parts<kTcD, 128>(a, un, row, slots, slot_floats, srows, f0, f1, c0, c0 + mine);
+                }
+            }
+            ++uc;
+        }
+        if (dead && row == 0) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+        tc_before();
+    }
+    __syncthreads();
+    tc_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, C::TMEM);
+}
+
+// Rows of a unit: all of a cached head's, or equal blocks of at most `most`.
+static int tc_block_rows(int rt, int most) {
+    const int blocks = (rt + most - 1) / most;
+    return ((rt + blocks - 1) / blocks + 15) / 16 * 16;
+}
+constexpr int kTcMostBf16 = 160, kTcMostFp8 = 128;
+
+bool attend_takes_tc(int N, int G, int D) { return D == kTcD; }
+
+size_t attend_tc_workspace(int N, int G) {
+    const int rt = N * G, rows = tc_block_rows(rt, kTcMostBf16) > tc_block_rows(rt, kTcMostFp8) ? tc_block_rows(rt, kTcMostBf16)
+                                                                                             : tc_block_rows(rt, kTcMostFp8);
+    return kAttHead + align256((size_t)2 * kTcMaxCtas * part_floats(rt < rows ? rt : rows, kTcD) * 4);
+}
+
+template <int CH, int NSM, bool FP8>
+static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cudaStream_t st) {
+    using C = TcCfg<CH, NSM, FP8>;
+    auto kfn = attend_tc_kernel<CH, NSM, FP8>;
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    static DeviceSlots slots = {};
+    int unused = 0;
+    e = device_once(slots, &unused, [&](int, int* o) {
+        *o = 1;
+        return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    const long long rb = ((long long)a.N * a.G + block_rows - 1) / block_rows;
+    const long long most = ((long long)a.c.max_pages * a.c.page_size + kTcTile - 1) / kTcTile;   // tiles of a unit
+    long long g = di.sm_count < kTcMaxCtas ? di.sm_count : kTcMaxCtas;
+    const long long tiles = (long long)a.B * a.c.kv_heads * rb * most;
+    if (g > tiles) g = tiles;
+    return launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, ring_wait_limit());
+}
+
+template <bool FP8>
+static cudaError_t launch_tc_e(const AttendArgs& a, cudaStream_t st) {
+    const int rt = a.N * a.G, br = tc_block_rows(rt, FP8 ? kTcMostFp8 : kTcMostBf16);
+    const int rp = br;                                          // a multiple of 16, as N of the products
+    if (rp <= 16) return launch_tc_t<1, 1, FP8>(a, br, rp, st);
+    if (rp <= 32) return launch_tc_t<2, 1, FP8>(a, br, rp, st);
+    if (rp <= 64) return launch_tc_t<4, 1, FP8>(a, br, rp, st);
+    return launch_tc_t<FP8 ? 4 : 5, 2, FP8>(a, br, rp, st);
+}
+
+cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st) {
+    return a.c.dtype == SPEC_DTYPE_E4M3 ? launch_tc_e<true>(a, st) : launch_tc_e<false>(a, st);
+}
+
+}  // namespace sv
