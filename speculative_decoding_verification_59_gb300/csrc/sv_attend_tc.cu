@@ -16,10 +16,13 @@
 // The warps of a CTA, one CTA per SM, each walking the CTA's share:
 //   softmax   4 warps (8 from 65 rows on, each 4 taking half of the rows)
 //   MMA       1 thread issues every tcgen05.mma
-//   loaders   4 warps gather K and V through the page table with 16-byte
-//             cp.async into a ring of 32 KB buffers, three to four in flight, and the
-//             queries; an E4M3 cache's rows are widened to fp16 on the way (a
-//             chunk by the thread that copied it; 8 warps where registers allow).
+//   loaders   4 warps bring the queries, keys and values into a ring of 32 KB
+//             buffers.  A tile of old positions whose pages fit it (page sizes
+//             that divide 128, from 8 on, or are multiples of it) comes by TMA, a box
+//             per page; other page sizes, and the tiles with new positions, where
+//             stale entries are left out, by the threads' 16-byte cp.async.  The
+//             rows of an E4M3 cache go to a ring of their own first, and the
+//             loaders (8 warps where registers allow) widen them to fp16.
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
 //
@@ -28,6 +31,8 @@
 // only asks whether any score passes its row's reference by 2^8 (one maximum
 // per score, one barrier vote); the rows' maxima, the new references and the
 // rescaling of O run when one does: on a unit's first tile, and rarely after.
+#include <cuda.h>
+
 #include "sv_attend.cuh"
 #include "sv_tma.cuh"
 
@@ -41,8 +46,15 @@ constexpr int kTcScaleRing = 8;                  // tiles whose scales are held
 // The loaders run at most 6 units ahead of the softmax (raw and widened buffers,
 // two score buffers), so what they tell it by unit is kept for 8.
 constexpr int kTcUnitRing = 8;
+// Polls of a wait before it gives up, whatever larger bound is in force: a poll
+// sleeps for up to some ten microseconds here, and no wait of this kernel lasts
+// longer than the memory takes to answer.
+constexpr uint32_t kTcWaitLimit = 1u << 18;
 constexpr int kTcMaxCtas = 256;                  // two counters each fit the workspace's head
 constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 template <int CH, int NSM, bool FP8>
 struct TcCfg {
@@ -50,8 +62,9 @@ struct TcCfg {
     static constexpr int RP = NSM * COLS;        // rows of a unit, at most
     static constexpr int PB = (RP + 63) / 64;    // 64-row blocks of P
     static constexpr int QB = RP <= 32 || (RP <= 64 && !FP8) ? 2 : 1;    // units whose queries are held
-    static constexpr int NBUF = FP8 ? (RP > 64 ? 3 : 4) : (RP > 64 ? 4 : 5);
-    static constexpr int NRAW = FP8 ? (RP > 64 ? 2 : 3) : 0;
+    static constexpr int NBUF = FP8 ? 3 : RP > 64 ? 4 : 5;
+    static constexpr int NRAW = FP8 ? (RP > 64 ? 3 : 5) : 1;    // (a bf16 cache has none)
+    static constexpr int WORDS = (COLS + 31) / 32;   // a bit for each row of a warpgroup
     static constexpr int SM_THREADS = NSM * 128;
     static constexpr int LOADERS = FP8 && NSM == 1 ? 256 : 128;
     static constexpr int THREADS = SM_THREADS + 32 + LOADERS;
@@ -59,7 +72,7 @@ struct TcCfg {
     static constexpr int Q_OFF = P_OFF + PB * 16384;
     static constexpr int QBYTES = RP * 256;
     static constexpr int RAW_OFF = Q_OFF + QB * QBYTES;
-    static constexpr int SCALE_OFF = RAW_OFF + NRAW * kTcRaw;
+    static constexpr int SCALE_OFF = RAW_OFF + (FP8 ? NRAW * kTcRaw : 0);
     static constexpr int SMEM = SCALE_OFF + (FP8 ? kTcScaleRing * 2 * kTcTile * 4 : 0) + 1024;   // and room to align
     static constexpr int TMEM = 3 * RP <= 64 ? 64 : 3 * RP <= 128 ? 128 : 3 * RP <= 256 ? 256 : 512;
 };
@@ -111,6 +124,20 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
     tc_wait_st();
 }
 
+// A box of a 4-D tensor into shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
+
 // Shared-memory operand with 128-byte swizzled rows.  K-major (the contraction
 // contiguous): sbo is the step between groups of 8 rows.  MN-major: lbo the step
 // between blocks of 64 elements of the other dimension, sbo between groups of 8
@@ -139,11 +166,16 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
     return r != 0;
 }
 
+// Arrives on the barrier when the thread's cp.asyncs so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Byte offset of chunk c (16 bytes of 16) of row t in a tile of 128 rows of
 // 256 bytes kept as two blocks of 128-byte swizzled half rows.
 __device__ __forceinline__ int tc_off(int t, int c) { return (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4); }
 
-// ORs e4m3's not-a-number pattern test over a word.
+// Whether one of a word's four e4m3 values is no number.
 __device__ __forceinline__ bool has_odd_e4m3(uint32_t y) {
     bool x = false;
 #pragma unroll
@@ -151,8 +183,33 @@ __device__ __forceinline__ bool has_odd_e4m3(uint32_t y) {
     return x;
 }
 
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+// Reduces 16 columns over the warp's lanes in 16 shuffles: halving the columns
+// a lane still holds at each step.  Both lanes of a pair end with the result
+// of column fold_column(lane).
+template <typename Op>
+__device__ __forceinline__ float fold16(float (&v)[16], int lane, Op op) {
+#pragma unroll
+    for (int h = 8; h >= 1; h >>= 1) {
+        const bool high = lane & (2 * h);
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+            const float give = high ? v[j] : v[j + h], keep = high ? v[j + h] : v[j];
+            v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, 2 * h));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+__device__ __forceinline__ int fold_column(int lane) { return lane >> 1; }
+
 template <int CH, int NSM, bool FP8>
-__global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, uint32_t limit) {
+__global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, int box, uint32_t limit, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
     using C = TcCfg<CH, NSM, FP8>;
     constexpr int RP = C::RP, NBUF = C::NBUF;
     extern __shared__ unsigned char smem_raw[];
@@ -161,7 +218,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
-    __shared__ unsigned long long desc_bits[NSM][kMaxNewTree]; // a node's descendants and itself
+    __shared__ int rowat[RP];                                   // its row of the output, from the sequence's first
+    __shared__ unsigned long long anc[NSM][2][kMaxNewTree];    // trees: ancestors and itself, by node
+    __shared__ short up[NSM][2][kMaxNewTree];
+    __shared__ uint32_t vis[NSM][kMaxNewTree][C::WORDS];       // trees: the warpgroup's rows that see a node
+    __shared__ __align__(8) uint64_t raw_full[C::NRAW], raw_empty[C::NRAW];
     __shared__ uint32_t tmem_at;
     __shared__ int unit_bad[NSM][kTcUnitRing];                  // a page that is none
     __shared__ float unit_qinv[kTcUnitRing];                    // E4M3: what takes back the queries' scaling
@@ -173,9 +234,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 
     if (tid == 0) {
         for (int i = 0; i < NBUF; ++i) {
-            mbar_init(&full[i], C::LOADERS / 32);
+            mbar_init(&full[i], FP8 ? C::LOADERS / 32 : C::LOADERS);
             mbar_init(&empty[i], 1);
         }
+        if constexpr (FP8)
+            for (int i = 0; i < C::NRAW; ++i) {
+                mbar_init(&raw_full[i], C::LOADERS);
+                mbar_init(&raw_empty[i], C::LOADERS / 32);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], C::SM_THREADS / 32);
@@ -217,76 +283,65 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         constexpr int RPI = 32 / CPR;                          // rows a warp copies at once
         constexpr int WROWS = kTcTile / LW;                    // rows of a tile that a warp copies
         constexpr int PIECES = WROWS / RPI;                    // of 16 bytes a thread
-        // buffers in flight behind the one being issued
-        constexpr int LAG = FP8 ? C::NRAW - 1 : NBUF - 2;
+        constexpr int LAG = C::NRAW - 1;                       // raw buffers in flight behind the one being issued
         const int ch = lane % CPR, sub = lane / CPR;
         bool ok = true;
         unsigned q = 0;                                        // buffers issued (keys and values in turn)
         unsigned uc = 0;                                       // units
-        unsigned done = 0;                                     // buffers handed over
-        struct Flight {                                        // what handing one over needs
+        unsigned done = 0;                                     // E4M3: buffers widened
+        struct Flight {                                        // what widening one needs
             int p0, ctx, total;
-            bool val;
         };
         Flight fl[LAG + 1];
-        auto finish = [&](unsigned j, const Flight& f) {       // buffer j has landed: (widen and) hand it over
+        unsigned ends[C::QB];                                  // by query buffer: q after the unit that had it
+        auto widen = [&](unsigned j, const Flight& f) {        // E4M3: raw buffer j to the products' form
+            if (ok) ok = wait_bounded(&raw_full[j % C::NRAW], (j / C::NRAW) & 1u, limit);
+            if (ok && j >= (unsigned)NBUF) ok = wait_bounded(&empty[j % NBUF], (j / NBUF - 1) & 1u, limit);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
             unsigned char* dst = smem + (j % NBUF) * kTcBuf;
-            if constexpr (FP8) {
-                if (ok && j >= (unsigned)NBUF) ok = wait_bounded(&empty[j % NBUF], (j / NBUF - 1) & 1u, limit);
-                const unsigned char* raw = smem + C::RAW_OFF + (j % C::NRAW) * kTcRaw;
+            const unsigned char* raw = smem + C::RAW_OFF + (j % C::NRAW) * kTcRaw;
+            const bool fresh = (j & 1u) && f.p0 + kTcTile > f.ctx;             // values, new positions among them
 #pragma unroll
-                for (int p = 0; p < PIECES; ++p) {
-                    const int row = lw * WROWS + p * RPI + sub;
-                    uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ch * 16);
-                    if (f.val && f.p0 + row >= f.ctx && f.p0 + row < f.total &&
-                        (has_odd_e4m3(w.x) || has_odd_e4m3(w.y) || has_odd_e4m3(w.z) || has_odd_e4m3(w.w))) {
-                        odd_any = 1;                           // rare: see the epilogue
-                        uint32_t y[4] = {w.x, w.y, w.z, w.w};
+            for (int p = 0; p < PIECES; ++p) {
+                const int row = lw * WROWS + p * RPI + sub;
+                uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ch * 16);
+                if (fresh && f.p0 + row >= f.ctx && f.p0 + row < f.total &&
+                    (has_odd_e4m3(w.x) || has_odd_e4m3(w.y) || has_odd_e4m3(w.z) || has_odd_e4m3(w.w))) {
+                    odd_any = 1;                               // rare: see the epilogue
+                    uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int s = 0; s < 32; s += 8)
-                                if (((y[i] >> s) & 0x7fu) == 0x7fu) y[i] &= ~(0xffu << s);
-                        w = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                    uint4 lo, hi;
-                    lo.x = e4m3_to_f16x2(w.x & 0xffffu);
-                    lo.y = e4m3_to_f16x2(w.x >> 16);
-                    lo.z = e4m3_to_f16x2(w.y & 0xffffu);
-                    lo.w = e4m3_to_f16x2(w.y >> 16);
-                    hi.x = e4m3_to_f16x2(w.z & 0xffffu);
-                    hi.y = e4m3_to_f16x2(w.z >> 16);
-                    hi.z = e4m3_to_f16x2(w.w & 0xffffu);
-                    hi.w = e4m3_to_f16x2(w.w >> 16);
-                    *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch)) = lo;
-                    *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch + 1)) = hi;
+                        for (int s = 0; s < 32; s += 8)
+                            if (((y[i] >> s) & 0x7fu) == 0x7fu) y[i] &= ~(0xffu << s);
+                    w = make_uint4(y[0], y[1], y[2], y[3]);
                 }
-            } else {
-                if (f.val && f.p0 + kTcTile > f.ctx) {         // new positions: values that are no numbers
-#pragma unroll
-                    for (int p = 0; p < PIECES; ++p) {
-                        const int row = lw * WROWS + p * RPI + sub;
-                        if (f.p0 + row < f.ctx || f.p0 + row >= f.total) continue;
-                        uint32_t* at = reinterpret_cast<uint32_t*>(dst + tc_off(row, ch));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t y = at[i];
-                            if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[i] = y; }
-                            if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[i] = y; }
-                        }
-                    }
-                }
+                uint4 lo, hi;
+                lo.x = e4m3_to_f16x2(w.x & 0xffffu);
+                lo.y = e4m3_to_f16x2(w.x >> 16);
+                lo.z = e4m3_to_f16x2(w.y & 0xffffu);
+                lo.w = e4m3_to_f16x2(w.y >> 16);
+                hi.x = e4m3_to_f16x2(w.z & 0xffffu);
+                hi.y = e4m3_to_f16x2(w.z >> 16);
+                hi.z = e4m3_to_f16x2(w.w & 0xffffu);
+                hi.w = e4m3_to_f16x2(w.w >> 16);
+                *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch)) = lo;
+                *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch + 1)) = hi;
             }
             proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[j % NBUF]);
+            if (lane == 0) {
+                mbar_arrive(&raw_empty[j % C::NRAW]);
+                mbar_arrive(&full[j % NBUF]);
+            }
         };
         while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
             // ---- the unit's queries
             const int qb = (int)(uc % C::QB);
-            if (C::QB == 1 && done < q) {                      // what frees them are the keys still in flight
-                cp_wait<0>();
-                for (; done < q && ok; ++done) finish(done, fl[done % (LAG + 1)]);
+            if constexpr (FP8) {
+                // what frees them is the last product of the unit that had them, whose keys
+                // may still be raw
+                for (; uc >= (unsigned)C::QB && done < ends[qb] && ok; ++done) widen(done, fl[done % (LAG + 1)]);
             }
             if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -330,71 +385,154 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[qb]);
 
-            // ---- the unit's tiles; a lane finds the page of one of the warp's rows, one
-            // tile before it is used
+            // ---- the unit's tiles.  What a tile needs of the block table is loaded one tile
+            // before it is used: for a TMA tile, lane i of the first warp finds the page of
+            // box i; else every warp's lanes find those of its rows.
             int page = -1, slot = 0;
+            auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
+            const int boxes = box > 0 ? kTcTile / box : 0;
             auto locate = [&](int i) {
-                const int pos = i * kTcTile + lw * WROWS + lane;
                 page = -1;
-                if (i < un.tb && lane < WROWS && pos < un.sl.total) {
+                if (i >= un.tb) return;
+                const bool tma = by_tma(i);
+                const int pos = i * kTcTile + (tma ? lane * box : lw * WROWS + lane);
+                if (tma ? lw == 0 && lane < boxes : lane < WROWS && pos < un.sl.total) {
                     const int pg = pos / a.c.page_size;
                     slot = pos - pg * a.c.page_size;
                     page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -2;
                     if (page == -1) page = -2;                  // -1: no position
                 }
             };
+            // E4M3: the page of the row whose scales the lane copies
+            int spage = -1, sslot = 0;
+            auto locate_scale = [&](int i) {
+                spage = -1;
+                const int pos = i * kTcTile + lw * WROWS + lane;
+                if (i < un.tb && lane < WROWS && pos < un.sl.total) {
+                    const int pg = pos / a.c.page_size;
+                    sslot = pos - pg * a.c.page_size;
+                    spage = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
+                }
+            };
             locate(un.ta);
+            if constexpr (FP8) locate_scale(un.ta);
             for (int i = un.ta; i < un.tb && ok; ++i) {
+                const bool tma = by_tma(i);
                 const bool have = (unsigned)page < (unsigned)a.c.num_pages;
                 if (__any_sync(0xffffffffu, !have && page != -1) && lane == 0) {
 #pragma unroll
                     for (int w = 0; w < NSM; ++w) unit_bad[w][uc % kTcUnitRing] = 1;
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
                 }
-                const int64_t off = have ? entry_off(a.c, page, slot, un.hk) : 0;
-                const int64_t soff = FP8 && have ? scale_off(a.c, page, slot, un.hk) : 0;
+                const int at_page = have ? page : 0, at_slot = slot;      // a bad page's unit ends as NaN anyway
+                const int64_t off = have && !tma ? entry_off(a.c, page, slot, un.hk) : 0;
                 const unsigned havem = __ballot_sync(0xffffffffu, have);
                 locate(i + 1);
                 for (int kv = 0; kv < 2; ++kv) {
+                    // the buffer's stage, once it is free
                     uint32_t dst;
+                    uint64_t* bar;
                     if constexpr (FP8) {
+                        if (lane == 0 && q >= (unsigned)C::NRAW)
+                            ok = wait_bounded(&raw_empty[q % C::NRAW], (q / C::NRAW - 1) & 1u, limit);
                         dst = smem_addr(smem + C::RAW_OFF + (q % C::NRAW) * kTcRaw);
+                        bar = &raw_full[q % C::NRAW];
                     } else {
-                        if (q >= (unsigned)NBUF && !wait_bounded(&empty[q % NBUF], (q / NBUF - 1) & 1u, limit)) ok = false;
+                        // Every warp waits for every buffer and arrives for it, the ones that have
+                        // no part in a TMA tile too: a barrier tells its last two phases apart,
+                        // no more, so none may fall behind or run ahead.
+                        if (lane == 0 && q >= (unsigned)NBUF)
+                            ok = wait_bounded(&empty[q % NBUF], (q / NBUF - 1) & 1u, limit);
                         dst = smem_addr(smem + (q % NBUF) * kTcBuf);
+                        bar = &full[q % NBUF];
                     }
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    const char* base = static_cast<const char*>(kv ? a.c.v : a.c.k);
+                    if (tma) {
+                        if (lw == 0) {
+                            if (lane == 0) mbar_expect(bar, FP8 ? kTcRaw : kTcBuf);
+                            __syncwarp();
+                            if (lane < boxes) {
+                                const CUtensorMap* map = kv ? &vmap : &kmap;
+                                if constexpr (FP8) {
+                                    tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
+                                } else {
+                                    tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
+                                    tma_load(dst + 16384 + lane * box * 128, map, 64, at_slot, un.hk, at_page, bar);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        // every warp arrives, so that none is a phase of a barrier behind
+                        if ((!FP8 || kv == 1) && lane == 0) mbar_arrive_n(bar, 32);
+                    } else {
+                        const char* base = static_cast<const char*>(kv ? a.c.v : a.c.k);
 #pragma unroll
-                    for (int p = 0; p < PIECES; ++p) {
-                        const int wr = p * RPI + sub, row = lw * WROWS + wr;
-                        const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
-                        cp16(dst + (FP8 ? row * 128 + ch * 16 : tc_off(row, ch)), base + e, (havem >> wr) & 1u);
+                        for (int p = 0; p < PIECES; ++p) {
+                            const int wr = p * RPI + sub, row = lw * WROWS + wr;
+                            const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
+                            cp16(dst + (FP8 ? row * 128 + ch * 16 : tc_off(row, ch)), base + e, (havem >> wr) & 1u);
+                        }
                     }
                     if constexpr (FP8) {
                         if (kv == 0 && lane < WROWS) {          // both scales: the softmax wants them with the scores
+                            const bool in = (unsigned)spage < (unsigned)a.c.num_pages;
+                            const int64_t so = in ? scale_off(a.c, spage, sslot, un.hk) : 0;
                             const uint32_t at = smem_addr(smem + C::SCALE_OFF) +
                                                 (((q >> 1) % kTcScaleRing) * 2 * kTcTile + lw * WROWS + lane) * 4;
-                            cp4(at, a.c.k_scale + soff, have);
-                            cp4(at + kTcTile * 4, a.c.v_scale + soff, have);
+                            cp4(at, a.c.k_scale + so, in);
+                            cp4(at + kTcTile * 4, a.c.v_scale + so, in);
                         }
-                    }
-                    cp_commit();
-                    fl[q % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total, kv == 1};
-                    ++q;
-                    if (q - done > (unsigned)LAG) {
-                        cp_wait<LAG>();
-                        finish(done, fl[done % (LAG + 1)]);
-                        ++done;
+                        // the keys' barrier waits for every thread's copies of scales
+                        if (!tma || kv == 0) cp_arrive(bar);
+                        if (kv == 0) locate_scale(i + 1);
+                        fl[q % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total};
+                        ++q;
+                        if (q - done > (unsigned)LAG) {
+                            widen(done, fl[done % (LAG + 1)]);
+                            ++done;
+                        }
+                    } else {
+                        if (tma) {
+                        } else if (kv == 1 && i * kTcTile + kTcTile > un.sl.ctx) {
+                            // new positions: values that are no numbers are taken out (see the
+                            // epilogue), so these rows are waited for here
+                            cp_commit();
+                            cp_wait<0>();
+#pragma unroll
+                            for (int p = 0; p < PIECES; ++p) {
+                                const int row = lw * WROWS + p * RPI + sub, pos = i * kTcTile + row;
+                                if (pos < un.sl.ctx || pos >= un.sl.total) continue;
+                                uint32_t* at = reinterpret_cast<uint32_t*>(smem + (q % NBUF) * kTcBuf + tc_off(row, ch));
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    uint32_t y = at[k];
+                                    if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[k] = y; }
+                                    if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[k] = y; }
+                                }
+                            }
+                            mbar_arrive(bar);
+                        } else {
+                            cp_arrive(bar);                     // when this thread's copies have landed
+                        }
+                        ++q;
                     }
                 }
             }
+            ends[qb] = q;
             ++uc;
         }
         // ---- the buffers still in flight
         cp_wait<0>();
-        for (; done < q && ok; ++done) finish(done, fl[done % (LAG + 1)]);
-        if (!ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+        if constexpr (FP8)
+            for (; done < q && ok; ++done) widen(done, fl[done % (LAG + 1)]);
+        if (!ok) {
+            // a wait ran out: do not leave while a box may still be on its way
+            raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+            constexpr unsigned DEPTH = FP8 ? C::NRAW : NBUF;
+            if (lw == 0 && lane == 0)
+                for (unsigned j = q > DEPTH ? q - DEPTH : 0u; j < q; ++j)
+                    wait_bounded(FP8 ? &raw_full[j % C::NRAW] : &full[j % NBUF], (j / DEPTH) & 1u, kTcWaitLimit);
+        }
     } else if (warp == kMmaWarp) {
         // ================= the products =================
         if (lane == 0) {
@@ -402,17 +540,21 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             const uint32_t base = smem_addr(smem);
             bool ok = true;
             unsigned g = 0, uc = 0;                            // tiles, units whose first product was issued
+            // operands at their first buffers; a step in bytes is a sixteenth of it here
+            const uint64_t k_d = tc_desc(base, 16, 1024), q_d = tc_desc(base + C::Q_OFF, 16, 1024);
+            const uint64_t v_d = tc_desc(base, 16384, 1024), p_d = tc_desc(base + C::P_OFF, 16384, 1024);
             auto scores = [&](int qb, bool first, bool last) { // S of tile g
                 if (first && !wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit)) return false;
                 const unsigned kb = 2 * g;
                 if (!wait_bounded(&full[kb % NBUF], (kb / NBUF) & 1u, limit)) return false;
                 if (g >= 2 && !wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit)) return false;
+                proxy_fence();                                 // copies that arrived by themselves
                 tc_after();
-                const uint32_t k0 = base + (kb % NBUF) * kTcBuf, q0 = base + C::Q_OFF + qb * C::QBYTES;
+                const uint64_t kd = k_d + (kb % NBUF) * (kTcBuf / 16), qd = q_d + qb * (C::QBYTES / 16);
+                const uint32_t at = tmem + (g & 1) * RP;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    tc_mma(tmem + (g & 1) * RP, tc_desc(k0 + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                           tc_desc(q0 + (ks >> 2) * (RP * 128) + (ks & 3) * 32, 16, 1024), id_qk, ks > 0);
+                    tc_mma(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id_qk, ks > 0);
                 tc_commit(&empty[kb % NBUF]);
                 tc_commit(&s_full[g & 1]);
                 if (last) tc_commit(&q_free[qb]);
@@ -422,12 +564,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 const unsigned vb = 2 * t + 1;
                 if (!wait_bounded(&full[vb % NBUF], (vb / NBUF) & 1u, limit)) return false;
                 if (!wait_bounded(&p_full, t & 1u, limit)) return false;
+                proxy_fence();
                 tc_after();
-                const uint32_t v0 = base + (vb % NBUF) * kTcBuf, p0 = base + C::P_OFF;
+                const uint64_t vd = v_d + (vb % NBUF) * (kTcBuf / 16);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc_mma(tmem + 2 * RP, tc_desc(v0 + ks * 2048, 16384, 1024), tc_desc(p0 + ks * 2048, 16384, 1024), id_pv,
-                           !(first && ks == 0));
+                for (int ks = 0; ks < 8; ++ks) tc_mma(tmem + 2 * RP, vd + ks * 128, p_d + ks * 128, id_pv, ks > 0 || !first);
                 tc_commit(&empty[vb % NBUF]);
                 tc_commit(&pv_done);
                 return true;
@@ -446,7 +587,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             if (ok && pend) ok = sums(g - 1, pend_first);
             // every product must have ended before tensor memory is given back
             tc_commit(&drained);
-            if (!wait_bounded(&drained, 0) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+            if (!wait_bounded(&drained, 0, kTcWaitLimit) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -470,34 +611,45 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             const SeqLen& sl = un.sl;
             // ---- the unit's rows, and who sees whom
             named_sync(bar, 128);                              // the unit before is done with the tables
-            if (a.par && tree_b != un.b) {
-                // descendants: every node adds itself to each of its ancestors
+            if (row < C::COLS) {
+                const int R = un.r0 + min(c0 + row, un.rows - 1), n = R / a.G;
+                rown[c0 + row] = (short)n;
+                rowat[c0 + row] = n * a.Hq + un.hk * a.G + (R - n * a.G);
+                nref[c0 + row] = -kNoRef;
+            }
+            if (a.par && (tree_b != un.b || RB > 1)) {
+                // ancestors by pointer doubling: 2^6 steps cover any path of 64 nodes
                 int wrong = 0;
-                if (row < a.N) desc_bits[wg][row] = 0ull;
                 if (row == 0) tree_bad[wg] = 0;
-                named_sync(bar, 128);
                 if (row < a.N) {
-                    const int32_t* par = a.par + (size_t)un.b * a.N;
-                    const int p = __ldg(par + row);
+                    const int p = __ldg(a.par + (size_t)un.b * a.N + row);
                     wrong = row < sl.nb && (row == 0 ? p != -1 : (p < 0 || p >= row));
-                    int at = row;
-                    for (int k = 0; k < kMaxNewTree && at >= 0; ++k) {
-                        atomicOr(&desc_bits[wg][at], 1ull << row);
-                        const int up = at == 0 || at >= sl.nb ? -1 : __ldg(par + at);
-                        at = up < at ? up : -1;
+                    anc[wg][0][row] = 1ull << row;
+                    up[wg][0][row] = (short)(wrong || row == 0 || row >= sl.nb ? -1 : p);
+                }
+                named_sync(bar, 128);
+                for (int k = 0; k < 6; ++k) {
+                    if (row < a.N) {
+                        const int p = up[wg][k & 1][row];
+                        anc[wg][(k + 1) & 1][row] = anc[wg][k & 1][row] | (p >= 0 ? anc[wg][k & 1][p] : 0ull);
+                        up[wg][(k + 1) & 1][row] = p >= 0 ? up[wg][k & 1][p] : (short)-1;
                     }
-                    if (wrong) {
-                        tree_bad[wg] = 1;
-                        raise_error(a.c.error, SPEC_DEVERR_TREE_PARENT);
-                    }
+                    named_sync(bar, 128);
+                }
+                for (int i = row; i < kMaxNewTree * C::WORDS; i += 128) {
+                    const int node = i / C::WORDS, w = i - node * C::WORDS;
+                    uint32_t bits = 0u;
+                    for (int k = 0; k < 32 && w * 32 + k < C::COLS; ++k)
+                        bits |= (uint32_t)((anc[wg][0][rown[c0 + w * 32 + k]] >> node) & 1ull) << k;
+                    vis[wg][node][w] = bits;
+                }
+                if (wrong) {
+                    tree_bad[wg] = 1;
+                    raise_error(a.c.error, SPEC_DEVERR_TREE_PARENT);
                 }
                 tree_b = un.b;
             }
             if (sl.bad && tid == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
-            if (row < C::COLS) {
-                rown[c0 + row] = (short)((un.r0 + min(c0 + row, un.rows - 1)) / a.G);
-                nref[c0 + row] = -kNoRef;
-            }
             const float c2 = a.scale * kLog2e;
 #pragma unroll
             for (int j = 0; j < CH * 16; ++j) l[j] = 0.f;
@@ -508,8 +660,20 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 const bool masked = p0 + kTcTile > sl.ctx;     // uniform: new positions, or past the end
                 const int d = pos - sl.ctx;
                 const bool gone = pos >= sl.total;
-                unsigned long long seen = 0ull;                // tree: the nodes that see this position
-                if (masked && a.par && d >= 0 && !gone) seen = desc_bits[wg][d & 63];
+                // the warpgroup's rows that see this position, a bit each
+                uint32_t sees[C::WORDS];
+#pragma unroll
+                for (int w = 0; w < C::WORDS; ++w) {
+                    sees[w] = gone ? 0u : 0xffffffffu;
+                    if (masked && d >= 0 && !gone) {
+                        if (a.par) {
+                            sees[w] = vis[wg][d & 63][w];
+                        } else {                               // a chain: rows d G and up of the cached head
+                            const int from = d * a.G - un.r0 - c0 - w * 32;
+                            sees[w] = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+                        }
+                    }
+                }
                 bool ok = wait_bounded(&s_full[g & 1], (g >> 1) & 1u, limit);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_after();
@@ -520,30 +684,33 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     add = __log2f(sc[kTcTile + row]);
                     vinv = 1.f / sc[kTcTile + row];
                 }
-                // row r's score in powers of two, plus nr (less its reference)
-                auto arg = [&](float s, int r, float nr) {
-                    float x = FP8 ? fmaf(s, f, add + nr) : fmaf(s, f, nr);
-                    if (masked) {
-                        const bool sees = d < 0 || (!gone && (a.par ? (seen >> rown[r]) & 1ull : d <= rown[r]));
-                        x = sees ? x : kNegInf;
-                    }
-                    return x;
+                // The score of the warpgroup's row k in powers of two, plus nr (less its
+                // reference).  The tiles that hold new positions, or the end, are masked;
+                // the others run without.
+                auto arg = [&](auto mask, float s, int k, float nr) {
+                    const float x = FP8 ? fmaf(s, f, add + nr) : fmaf(s, f, nr);
+                    if constexpr (decltype(mask)::value) return (sees[k >> 5] >> (k & 31)) & 1u ? x : kNegInf;
+                    else return x;
                 };
                 const uint32_t s_at = lanes + (g & 1) * RP + c0;
-                float top = kNegInf;
+                auto highest = [&](auto mask) {
+                    float top = kNegInf;
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-                    if (ch < chunks) {
-                        float v[16];
-                        tc_ld16(s_at + ch * 16, v);
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch < chunks) {
+                            float v[16];
+                            tc_ld16(s_at + ch * 16, v);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const int r = c0 + ch * 16 + j;
-                            const float4 nr = *reinterpret_cast<const float4*>(&nref[r]);
-                            top = fmaxf(top, fmaxf(fmaxf(arg(v[j], r, nr.x), arg(v[j + 1], r + 1, nr.y)),
-                                                   fmaxf(arg(v[j + 2], r + 2, nr.z), arg(v[j + 3], r + 3, nr.w))));
+                            for (int j = 0; j < 16; j += 4) {
+                                const int k = ch * 16 + j;
+                                const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
+                                top = fmaxf(top, fmaxf(fmaxf(arg(mask, v[j], k, nr.x), arg(mask, v[j + 1], k + 1, nr.y)),
+                                                       fmaxf(arg(mask, v[j + 2], k + 2, nr.z), arg(mask, v[j + 3], k + 3, nr.w))));
+                            }
                         }
-                    }
+                    return top;
+                };
+                const float top = masked ? highest(Yes{}) : highest(No{});
                 const bool first = i == un.ta;
                 ok = ok && !late;
                 if (named_any(bar, 128, !ok || top > kRefSlack)) {
@@ -554,17 +721,19 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         break;
                     }
                     tc_after();
+                    for (int ch = 0; ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
+                        float v[16];
+                        tc_ld16(s_at + ch * 16, v);
+                        uint32_t bits = sees[0];
 #pragma unroll
-                    for (int ch = 0; ch < CH; ++ch)
-                        if (ch < chunks) {
-                            float v[16];
-                            tc_ld16(s_at + ch * 16, v);
+                        for (int w = 1; w < C::WORDS; ++w)
+                            if (ch >> 1 == w) bits = sees[w];
+                        bits = masked ? bits >> (16 * (ch & 1)) : 0xffffu;
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float x = warp_max(arg(v[j], c0 + ch * 16 + j, 0.f));
-                                if (lane == 0) wred[warp][ch * 16 + j] = x;
-                            }
-                        }
+                        for (int j = 0; j < 16; ++j) v[j] = (bits >> j) & 1u ? (FP8 ? fmaf(v[j], f, add) : v[j] * f) : kNegInf;
+                        const float x = fold16(v, lane, Max{});
+                        if (!(lane & 1)) wred[warp][ch * 16 + fold_column(lane)] = x;
+                    }
                     named_sync(bar, 128);
                     if (row < chunks * 16) {
                         const int w0 = wg * 4;
@@ -592,34 +761,38 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 // ---- probabilities; P is free once the tile before has been summed
                 if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
                 late = !ok;
-                unsigned char* prow = smem + C::P_OFF + row * 128;
+                auto weigh = [&](auto mask) {
+                    unsigned char* prow = smem + C::P_OFF + row * 128;
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-                    if (ch < chunks) {
-                        float v[16];
-                        tc_ld16(s_at + ch * 16, v);
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch < chunks) {
+                            float v[16];
+                            tc_ld16(s_at + ch * 16, v);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const int r = c0 + ch * 16 + j;
-                            const float4 nr = *reinterpret_cast<const float4*>(&nref[r]);
-                            v[j] = ex2_approx(arg(v[j], r, nr.x));
-                            v[j + 1] = ex2_approx(arg(v[j + 1], r + 1, nr.y));
-                            v[j + 2] = ex2_approx(arg(v[j + 2], r + 2, nr.z));
-                            v[j + 3] = ex2_approx(arg(v[j + 3], r + 3, nr.w));
+                            for (int j = 0; j < 16; j += 4) {
+                                const int k = ch * 16 + j;
+                                const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
+                                v[j] = ex2_approx(arg(mask, v[j], k, nr.x));
+                                v[j + 1] = ex2_approx(arg(mask, v[j + 1], k + 1, nr.y));
+                                v[j + 2] = ex2_approx(arg(mask, v[j + 2], k + 2, nr.z));
+                                v[j + 3] = ex2_approx(arg(mask, v[j + 3], k + 3, nr.w));
+                            }
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                if constexpr (FP8) l[ch * 16 + j] += v[j] != 0.f ? v[j] * vinv : 0.f;   // a masked scale may be anything
+                                else l[ch * 16 + j] += v[j];
+                                if (j & 1) w[j >> 1] = FP8 ? pack_f16(v[j - 1], v[j]) : pack_bf16(v[j - 1], v[j]);
+                            }
+                            const int c = c0 + ch * 16;
+                            unsigned char* at = prow + (c >> 6) * 16384;
+                            const int k = (c & 63) >> 3;
+                            *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
                         }
-                        uint32_t w[8];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if constexpr (FP8) l[ch * 16 + j] += v[j] != 0.f ? v[j] * vinv : 0.f;   // a masked scale may be anything
-                            else l[ch * 16 + j] += v[j];
-                            if (j & 1) w[j >> 1] = FP8 ? pack_f16(v[j - 1], v[j]) : pack_bf16(v[j - 1], v[j]);
-                        }
-                        const int c = c0 + ch * 16;
-                        unsigned char* at = prow + (c >> 6) * 16384;
-                        const int k = (c & 63) >> 3;
-                        *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
+                };
+                if (masked) weigh(Yes{});
+                else weigh(No{});
                 proxy_fence();
                 tc_before();
                 __syncwarp();
@@ -638,11 +811,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch)
                 if (ch < chunks) {
+                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float x = warp_sum(l[ch * 16 + j]);
-                        if (lane == 0) wred[warp][ch * 16 + j] = x;
-                    }
+                    for (int j = 0; j < 16; ++j) v[j] = l[ch * 16 + j];
+                    const float x = fold16(v, lane, Add{});
+                    if (!(lane & 1)) wred[warp][ch * 16 + fold_column(lane)] = x;
                 }
             named_sync(bar, 128);
             const bool bad = sl.bad || (a.par && tree_bad[wg]) || unit_bad[wg][uc % kTcUnitRing] || dead;
@@ -656,15 +829,12 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             const bool whole = un.ta == 0 && un.tb == un.tiles;
             float* sp = slots + (size_t)(2 * (int)blockIdx.x + (un.ta == 0 ? 1 : 0)) * slot_floats;
             if (row < mine) {                                  // thread r: row r's totals
-                const int r = c0 + row, R = un.r0 + r, n = R / a.G;
+                const int r = c0 + row;
                 const float m = -nref[r];
                 if (whole) {
-                    const bool none = n >= sl.nb && !bad;
+                    const bool none = rown[r] >= sl.nb && !bad;
                     alpha[r] = none ? 0.f : 1.f / lsum;
-                    if (a.lse) {
-                        const size_t at = ((size_t)un.b * a.N + n) * a.Hq + (size_t)un.hk * a.G + (R - n * a.G);
-                        a.lse[at] = none ? kNegInf : (m + __log2f(lsum)) * kLn2;
-                    }
+                    if (a.lse) a.lse[(size_t)un.b * a.N * a.Hq + rowat[r]] = none ? kNegInf : (m + __log2f(lsum)) * kLn2;
                 } else {
                     // a row that has seen nothing joins with weight zero
                     __stcg(sp + (size_t)srows * kTcD + r, m == kNoRef && !bad ? kNegInf : m);
@@ -673,51 +843,48 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             }
             named_sync(bar, 128);
             if (row == 0) unit_bad[wg][uc % kTcUnitRing] = 0;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
-                if (ch * 16 < mine) {
-                    float v[16];
-                    tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
-                    if (odd_any) {
-                        // Rare: some new position's value was no number.  The loaders zeroed
-                        // it, so that it does not spoil the rows that mask it; those that
-                        // see it get it here.
-                        const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
-                        for (int j = j0; j < j1; ++j) {
-                            int page, slot;
-                            if (!cache_place(a.c, un.b, j, &page, &slot)) continue;
-                            const int64_t off = entry_off(a.c, page, slot, un.hk) + row;
-                            float x;
-                            if constexpr (FP8) {
-                                float unused;
-                                f16x2_to_f32(e4m3_to_f16x2(static_cast<const unsigned char*>(a.c.v)[off]), &x, &unused);
-                            } else {
-                                x = __uint_as_float((uint32_t)static_cast<const unsigned short*>(a.c.v)[off] << 16);
-                            }
-                            if (fabsf(x) < CUDART_INF_F) continue;
-                            const int d = j - sl.ctx;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int n = rown[c0 + ch * 16 + k];
-                                if (a.par ? (desc_bits[wg][d & 63] >> n) & 1ull : d <= n) v[k] += x;
-                            }
+            for (int ch = 0; ch * 16 < mine; ++ch) {
+                float v[16];
+                tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
+                if (odd_any) {
+                    // Rare: some new position's value was no number.  The loaders zeroed
+                    // it, so that it does not spoil the rows that mask it; those that
+                    // see it get it here.
+                    const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
+                    for (int j = j0; j < j1; ++j) {
+                        int page, slot;
+                        if (!cache_place(a.c, un.b, j, &page, &slot)) continue;
+                        const int64_t off = entry_off(a.c, page, slot, un.hk) + row;
+                        float x;
+                        if constexpr (FP8) {
+                            float unused;
+                            f16x2_to_f32(e4m3_to_f16x2(static_cast<const unsigned char*>(a.c.v)[off]), &x, &unused);
+                        } else {
+                            x = __uint_as_float((uint32_t)static_cast<const unsigned short*>(a.c.v)[off] << 16);
                         }
-                    }
+                        if (fabsf(x) < CUDART_INF_F) continue;
+                        const int d = j - sl.ctx;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int r = c0 + ch * 16 + j;
-                        if (ch * 16 + j < mine) {
-                            if (whole) {
-                                const int R = un.r0 + r, n = rown[r], gq = R - n * a.G;
-                                const size_t at = ((size_t)un.b * a.N + n) * a.Hq + (size_t)un.hk * a.G + gq;
-                                const float y = n >= sl.nb && !bad ? 0.f : v[j] * alpha[r];
-                                reinterpret_cast<unsigned short*>(a.out)[at * kTcD + row] = (unsigned short)(pack_bf16(y, 0.f) & 0xffffu);
-                            } else {
-                                __stcg(sp + (size_t)r * kTcD + row, v[j]);
-                            }
+                        for (int k = 0; k < 16; ++k) {
+                            const int n = rown[c0 + ch * 16 + k];
+                            if (a.par ? (anc[wg][0][n] >> (d & 63)) & 1ull : d <= n) v[k] += x;
                         }
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int r = c0 + ch * 16 + j;
+                    if (ch * 16 + j < mine) {
+                        if (whole) {
+                            const float y = rown[r] >= sl.nb && !bad ? 0.f : v[j] * alpha[r];
+                            reinterpret_cast<unsigned short*>(a.out)[((size_t)un.b * a.N * a.Hq + rowat[r]) * kTcD + row] =
+                                (unsigned short)(pack_bf16(y, 0.f) & 0xffffu);
+                        } else {
+                            __stcg(sp + (size_t)r * kTcD + row, v[j]);
+                        }
+                    }
+                }
+            }
             tc_before();
             if (!whole && mine > 0) {
                 // the unit's CTAs: c0 begins it, c1 ends it; the last warpgroup to arrive adds
@@ -762,6 +929,38 @@ size_t attend_tc_workspace(int N, int G) {
     return kAttHead + align256((size_t)2 * kTcMaxCtas * part_floats(rt < rows ? rt : rows, kTcD) * 4);
 }
 
+// The driver's tensor map encoder (the library links the runtime only).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// A layer's keys (or values) as [page, head, slot, element], boxes of `box`
+// slots: 64 elements wide and 128-byte swizzled for bf16, whole rows for E4M3.
+static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int box) {
+    const bool f8 = c.dtype == SPEC_DTYPE_E4M3;
+    const cuuint64_t elt = f8 ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * elt, (cuuint64_t)c.head_stride * elt, (cuuint64_t)c.page_stride * elt};
+    for (cuuint64_t s : strides)
+        if (s == 0 || s >= (1ull << 40)) return false;
+    const cuuint32_t boxes[4] = {f8 ? 128u : 64u, (cuuint32_t)box, 1u, 1u}, one[4] = {1u, 1u, 1u, 1u};
+    return encoder() && encoder()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
+                                  boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int CH, int NSM, bool FP8>
 static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cudaStream_t st) {
     using C = TcCfg<CH, NSM, FP8>;
@@ -781,7 +980,13 @@ static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cuda
     long long g = di.sm_count < kTcMaxCtas ? di.sm_count : kTcMaxCtas;
     const long long tiles = (long long)a.B * a.c.kv_heads * rb * most;
     if (g > tiles) g = tiles;
-    return launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, ring_wait_limit());
+    // TMA boxes: one page, or 128 of its slots; tiles then begin and end with boxes
+    const int ps = a.c.page_size;
+    int box = ps % kTcTile == 0 ? kTcTile : ps >= 8 && kTcTile % ps == 0 ? ps : 0;
+    CUtensorMap km = {}, vm = {};
+    if (box > 0 && (!encode_map(&km, a.c, a.c.k, box) || !encode_map(&vm, a.c, a.c.v, box))) box = 0;
+    const uint32_t limit = ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit;
+    return launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, limit, km, vm);
 }
 
 template <bool FP8>

@@ -38,6 +38,21 @@ def make_cache(seed, B, tokens, page, H, D, fp8=False, hnd=False, layers=None, e
     return k, v, table, ks, vs
 
 
+def make_cache_on_gpu(seed, B, tokens, page, H, D, fp8=False):
+    """make_cache for large ones, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    per = -(-tokens // page)
+    pages = B * per + 3
+    table = torch.randperm(pages, generator=g, device="cuda")[:B * per].view(B, per).to(torch.int32)
+    out = []
+    for _ in range(2):
+        x = torch.randn((pages, page, H, D), generator=g, device="cuda")
+        sc = (torch.rand((pages, page, H), generator=g, device="cuda") + 0.5) / 100 if fp8 else None
+        out.append(((x / sc[..., None]).clamp(-448, 448).to(F8) if fp8 else x.to(torch.bfloat16), sc))
+    (k, ks), (v, vs) = out
+    return k, v, table, ks, vs
+
+
 def cuda_like(t):
     """A copy on the GPU with t's strides."""
     if t is None:

@@ -291,3 +291,46 @@ def test_refusals(sv):
         sv.KVCache(cache.k, cache.v[:, :, :1], cache.block_table)
     with pytest.raises(ValueError):
         sv.KVCache(cache.k, cache.v, cache.block_table, torch.zeros(3, device="cuda"))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_waits_that_run_out_report_and_return(sv, fp8):
+    """With the kernels' bounded waits set to give up at once: the error word says so, the rows
+    are NaN, and later calls through the same workspace are right again."""
+    args = case(27, 2, 4, 8, 2, 128, 16, [700, 3000], fp8)
+    parts, q, par, c, nb = args
+    cache = R.on_gpu(sv, parts)
+    want = sv.paged_attention(q.cuda(), cache, c.cuda())
+    torch.cuda.synchronize()
+    sv.spec_verify_set_wait_limit(0)
+    try:
+        out = sv.paged_attention(q.cuda(), cache, c.cuda())
+        torch.cuda.synchronize()
+    finally:
+        sv.spec_verify_set_wait_limit(sv.spec_verify_default_wait_limit())
+    assert cache.read_error() & sv.SPEC_DEVERR_TIMEOUT
+    assert torch.isnan(out).all()
+    assert torch.equal(sv.paged_attention(q.cuda(), cache, c.cuda()), want)
+    assert cache.read_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [8, 16, 64, 128, 256, 48])
+def test_long_shares(sv, fp8, page):
+    """Shares of many tiles, old positions and new ones in turn, against the rows one by one: every
+    sequence's answer is that of the sequence alone."""
+    g = torch.Generator().manual_seed(page)
+    B, N, Hq, H, D = 40, 3, 16, 8, 128
+    ctx = torch.randint(0, 3000, (B,), generator=g).tolist()
+    cache = sv.KVCache(*R.make_cache_on_gpu(28, B, max(ctx) + N, page, H, D, fp8))
+    qd = (torch.randn((B, N, Hq, D), generator=g) * 1.5).to(torch.bfloat16).cuda()
+    cd = torch.tensor(ctx, dtype=torch.int32).cuda()
+    whole = [sv.paged_attention(qd, cache, cd) for _ in range(4)]
+    assert all(torch.equal(w, whole[0]) for w in whole)
+    assert cache.read_error() == 0
+    for b in range(0, B, 7):
+        one = sv.KVCache(cache.k, cache.v, cache.block_table[b:b + 1].contiguous(), cache.k_scale, cache.v_scale)
+        alone = sv.paged_attention(qd[b:b + 1].contiguous(), one, cd[b:b + 1].contiguous())
+        # the split differs, so sums come in another order and references differ: P and the
+        # result are each rounded anew (two unit roundoffs of the values' magnitude, at most 4.5)
+        assert (alone.float() - whole[0][b:b + 1].float()).abs().max() <= 4.5 * 2 * R.U_BF16
