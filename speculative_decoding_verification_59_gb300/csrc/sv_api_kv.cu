@@ -140,6 +140,10 @@ spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
     a.N = N;
     a.Hq = q_heads;
     a.G = q_heads / Hkv;
+    a.g_mul = (uint32_t)(((1ull << 32) + (uint64_t)a.G - 1) / (uint64_t)a.G);
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (cache->page_size == 1 << i) a.page_shift = i;
     a.out = static_cast<char*>(out);
     a.lse = lse;
     a.ws = static_cast<char*>(workspace);

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             for (int hrow = 0; hrow < 2; ++hrow) {
                 const int r = mt * 16 + hrow * 8 + lrow, R = r0 + r;
                 const bool on = r < rows;
-                const int n = on ? R / a.G : 0, g = on ? R - n * a.G : 0;
+                const int n = on ? row_position(a, R) : 0, g = on ? R - n * a.G : 0;
                 rn[mt][hrow] = n;
                 rs[mt][hrow] = c2;
                 const char* src = a.q + ((int64_t)b * a.N + n) * a.qs + ((size_t)hk * a.G + g) * D * 2;
@@ -233,15 +233,14 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         bool lost = false;
         // Lane t finds entry t of the next slice to copy.  Its page id is loaded one
         // slice before it is used, so that nothing waits for the table.
-        int page = -1, slot = 0;
+        int page = 0, slot = 0;
+        bool want = false;                                      // the lane has a position (whose page is not looked at yet)
         auto locate = [&](int i) {
             const int pos = slice_at(i) + lane;
-            page = -1;
-            if (i < nsl && lane < C::ST && pos < sl.total) {
-                const int pg = pos / a.c.page_size;
-                slot = pos - pg * a.c.page_size;
-                page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)b * a.c.max_pages + pg) : -2;
-                if (page == -1) page = -2;                      // -1: no position
+            want = i < nsl && lane < C::ST && pos < sl.total;
+            if (want) {
+                const int pg = page_index(a, pos, &slot);
+                page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)b * a.c.max_pages + pg) : -1;
             }
         };
         auto copy = [&](int i) {                                // slice i, located before
@@ -249,8 +248,8 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 const uint32_t st = ring_s + (i % C::NS) * C::STAGE;
                 constexpr int RP = 32 / C::CPR;                // rows the warp copies at once
                 const int ch = lane % C::CPR, sub = lane / C::CPR;
-                const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
-                lost |= !ok && page != -1;
+                const bool ok = want && (unsigned)page < (unsigned)a.c.num_pages;
+                lost |= want && !ok;
                 const int64_t off = ok ? entry_off(a.c, page, slot, hk) : 0;
                 const unsigned okm = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             __syncthreads();
             if (last_cta) {
                 __threadfence();
-                join_parts<D, kAttThreads>(a, un, threadIdx.x, slots, slot_floats, srows, c0, c1, 0, rows);
+                join_parts<D, kAttWarps>(a, un, warp, slots, slot_floats, srows, c0, c1, 0, rows);
             }
         }
     }

@@ -42,6 +42,17 @@ __device__ __forceinline__ SeqLen seq_len(const AttendArgs& a, int b) {
     return s;
 }
 
+// The new position of row R of a cached head, R / G.
+__device__ __forceinline__ int row_position(const AttendArgs& a, int R) {
+    return a.G == 1 ? R : (int)__umulhi((uint32_t)R, a.g_mul);
+}
+// The page index and slot of a position.
+__device__ __forceinline__ int page_index(const AttendArgs& a, int pos, int* slot) {
+    const int pg = a.page_shift >= 0 ? pos >> a.page_shift : pos / a.c.page_size;
+    *slot = pos - pg * a.c.page_size;
+    return pg;
+}
+
 // Share i of `total` tiles among n CTAs begins at tile i * total / n.
 __device__ __forceinline__ long long share_begin(long long total, long long n, long long i) { return i * total / n; }
 // The CTA whose share holds tile t.
@@ -160,7 +171,7 @@ struct AttWalk {
 // Writes elements d .. d + 3 of row r of a finished unit.
 __device__ __forceinline__ void put_row(const AttendArgs& a, const AttUnit& x, bool bad, int D, int r, int d, float4 v,
                                         float lsum, float mref) {
-    const int R = x.r0 + r, n = R / a.G, g = R - n * a.G;
+    const int R = x.r0 + r, n = row_position(a, R), g = R - n * a.G;
     const size_t row = ((size_t)x.b * a.N + n) * a.Hq + (size_t)x.hk * a.G + g;
     const bool empty = n >= x.sl.nb && !bad;
     const float f = empty ? 0.f : 1.f / lsum;
@@ -170,31 +181,97 @@ __device__ __forceinline__ void put_row(const AttendArgs& a, const AttUnit& x, b
 }
 
 // Adds rows ra .. rb - 1 of the parts of a unit that CTAs c0 .. c1 hold, in
-// that order, and writes them; by THREADS threads (thread tid of them).
-template <int D, int THREADS>
-__device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x, int tid, float* slots, size_t slot_floats,
+// that order, and writes them; by WARPS warps (warp w of them).  A warp takes
+// kJoinRows rows at once, one lane per part for their references and totals,
+// then its lanes across the elements: the loads of several rows and parts are
+// in flight together (a row and part at a time, the join of 32 rows in 5 parts
+// took 22 us; the parts come from L2, about 0.5 us away).
+constexpr int kJoinRows = 4;
+template <int D, int WARPS>
+__device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
                                            int srows, int c0, int c1, int ra, int rb) {
-    const int parts = c1 - c0 + 1;
+    constexpr int V = D / 32;                                 // elements of a lane: 2, 4 or 8
+    constexpr int V4 = V >= 4 ? V / 4 : 1;
+    const int lane = threadIdx.x & 31, parts = c1 - c0 + 1;
     auto part = [&](int p) { return slots + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
-    for (int i = tid; i < (rb - ra) * (D / 4); i += THREADS) {
-        const int r = ra + i / (D / 4), d = i % (D / 4) * 4;
-        float M = kNegInf;
-        for (int p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(part(p) + (size_t)srows * D + r));
-        const float Ms = M == kNegInf ? 0.f : M;
-        float L = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-            const float* q = part(p);
-            const float f = ex2_approx(__ldcg(q + (size_t)srows * D + r) - Ms);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(q + (size_t)r * D + d));
-            L = fmaf(f, __ldcg(q + (size_t)srows * (D + 1) + r), L);
-            v.x = fmaf(f, y.x, v.x);
-            v.y = fmaf(f, y.y, v.y);
-            v.z = fmaf(f, y.z, v.z);
-            v.w = fmaf(f, y.w, v.w);
+    for (int r0 = ra + w * kJoinRows; r0 < rb; r0 += WARPS * kJoinRows) {
+        float M[kJoinRows], L[kJoinRows];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) { M[k] = kNegInf; L[k] = 0.f; }
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float m[kJoinRows];
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k)
+                m[k] = p0 + lane < parts && r0 + k < rb ? __ldcg(part(p0 + lane) + (size_t)srows * D + r0 + k) : kNegInf;
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) M[k] = fmaxf(M[k], m[k]);
         }
-        put_row(a, x, false, D, r, d, v, L, M);
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            M[k] = warp_max(M[k]);
+            if (M[k] == kNegInf) M[k] = 0.f;                  // no part has seen a position
+        }
+        float v[kJoinRows][V];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float f[kJoinRows];
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) {
+                const bool on = p0 + lane < parts && r0 + k < rb;
+                const float* q = part(on ? p0 + lane : 0) + (size_t)srows * D + (on ? r0 + k : ra);
+                f[k] = on ? ex2_approx(__ldcg(q) - M[k]) : 0.f;
+                L[k] = on ? fmaf(f[k], __ldcg(q + srows), L[k]) : L[k];
+            }
+            const int n = min(32, parts - p0);
+#pragma unroll 2
+            for (int p = 0; p < n; ++p) {
+                const float* q = part(p0 + p) + (size_t)r0 * D + lane * V;
+                float y[kJoinRows][V];
+#pragma unroll
+                for (int k = 0; k < kJoinRows; ++k) {
+                    const float* at = q + (r0 + k < rb ? k * D : 0);
+                    if constexpr (V == 2) {
+                        const float2 t = __ldcg(reinterpret_cast<const float2*>(at));
+                        y[k][0] = t.x;
+                        y[k][1] = t.y;
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < V4; ++h) {
+                            const float4 t = __ldcg(reinterpret_cast<const float4*>(at) + h);
+                            y[k][4 * h] = t.x;
+                            y[k][4 * h + 1] = t.y;
+                            y[k][4 * h + 2] = t.z;
+                            y[k][4 * h + 3] = t.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kJoinRows; ++k) {
+                    const float fp = __shfl_sync(0xffffffffu, f[k], p);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[k][e] = fmaf(fp, y[k][e], v[k][e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            // the lanes' totals in a fixed order
+            const float lsum = warp_sum(L[k]);
+            if (r0 + k < rb) {
+                if constexpr (V == 2) {
+                    const float2 o = make_float2(__shfl_down_sync(0xffffffffu, v[k][0], 1), __shfl_down_sync(0xffffffffu, v[k][1], 1));
+                    if (!(lane & 1)) put_row(a, x, false, D, r0 + k, lane * 2, make_float4(v[k][0], v[k][1], o.x, o.y), lsum, M[k]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < V4; ++h)
+                        put_row(a, x, false, D, r0 + k, lane * V + 4 * h,
+                                make_float4(v[k][4 * h], v[k][4 * h + 1], v[k][4 * h + 2], v[k][4 * h + 3]), lsum, M[k]);
+                }
+            }
+        }
     }
 }
 

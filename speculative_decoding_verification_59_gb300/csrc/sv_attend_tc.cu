@@ -4,7 +4,7 @@
 //
 // Both products are taken transposed, so that the 128 positions of a tile and
 // the 128 elements of a head are the 128 rows that the instruction wants, and the
-// few query rows its free dimension N (a multiple of 16 up to 160):
+// few query rows its free dimension N (a multiple of 16 up to 144):
 //   S^T [positions x rows] = K [positions x 128] Q^T,
 //   O^T [elements x rows] += V^T [elements x positions] P^T.
 // K and V lie in shared memory as they come from the cache (128-byte swizzled
@@ -14,7 +14,7 @@
 // probabilities as one row of P.
 //
 // The warps of a CTA, one CTA per SM, each walking the CTA's share:
-//   softmax   4 warps (8 from 65 rows on, each 4 taking half of the rows)
+//   softmax   4 warps (8 or 12 from 65 rows on, each 4 with their share of the rows)
 //   MMA       1 thread issues every tcgen05.mma
 //   loaders   4 warps bring the queries, keys and values into a ring of 32 KB
 //             buffers.  A tile of old positions whose pages fit it (page sizes
@@ -50,7 +50,8 @@ constexpr int kTcUnitRing = 8;
 // sleeps for up to some ten microseconds here, and no wait of this kernel lasts
 // longer than the memory takes to answer.
 constexpr uint32_t kTcWaitLimit = 1u << 18;
-constexpr int kTcMaxCtas = 256;                  // two counters each fit the workspace's head
+constexpr int kTcMaxCtas = 256;                  // three counters each fit the workspace's head
+static_assert(256 + 3 * kTcMaxCtas * 4 <= kAttHead, "the counters lie in the zeroed head");
 constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
 
 struct Yes { static constexpr bool value = true; };
@@ -65,6 +66,10 @@ struct TcCfg {
     static constexpr int NBUF = FP8 ? 3 : RP > 64 ? 4 : 5;
     static constexpr int NRAW = FP8 ? (RP > 64 ? 3 : 5) : 1;    // (a bf16 cache has none)
     static constexpr int WORDS = (COLS + 31) / 32;   // a bit for each row of a warpgroup
+    // Up to 32 rows the scores stay in registers between the vote and the
+    // probabilities, beside as many running totals; beyond, they are read from
+    // tensor memory twice.
+    static constexpr bool KEEP = CH <= 2;
     static constexpr int SM_THREADS = NSM * 128;
     static constexpr int LOADERS = FP8 && NSM == 1 ? 256 : 128;
     static constexpr int THREADS = SM_THREADS + 32 + LOADERS;
@@ -111,6 +116,19 @@ __device__ __forceinline__ void tc_ld16(uint32_t at, float (&v)[16]) {
     tc_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The same, the wait left to the caller (tc_wait_ld, then tc_ld16_done: nothing
+// may use the registers before).
+__device__ __forceinline__ void tc_ld16_start(uint32_t at, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tc_ld16_done(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 __device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
     uint32_t r[16];
@@ -348,7 +366,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             unsigned char* qs = smem + C::Q_OFF + qb * C::QBYTES;
             float qscale = 1.f;
             auto query_row = [&](int r) {
-                const int R = un.r0 + r, n = R / a.G, g = R - n * a.G;
+                const int R = un.r0 + r, n = row_position(a, R), g = R - n * a.G;
                 return a.q + ((int64_t)un.b * a.N + n) * a.qs + ((size_t)un.hk * a.G + g) * kTcD * 2;
             };
             if constexpr (FP8) {
@@ -356,51 +374,64 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 // element is in [2^12, 2^13): exact down to 2^-26 of it.  Every warp
                 // finds the maximum by itself.
                 float mx = 0.f;
-                for (int i = lane; i < un.rows * 16; i += 32) {
-                    float x[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(query_row(i >> 4)) + (i & 15)), x);
+                for (int i0 = lane; i0 < un.rows * 16; i0 += 32 * 8) {
+                    uint4 w[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]) < CUDART_INF_F ? fabsf(x[j]) : 0.f);
+                    for (int k = 0; k < 8; ++k) {
+                        const int i = i0 + 32 * k;
+                        w[k] = i < un.rows * 16 ? __ldg(reinterpret_cast<const uint4*>(query_row(i >> 4)) + (i & 15)) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float x[8];
+                        unpack8(w[k], x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]) < CUDART_INF_F ? fabsf(x[j]) : 0.f);
+                    }
                 }
                 mx = warp_max(mx);
                 const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 139 - ex;
                 qscale = __uint_as_float((uint32_t)(127 + sh) << 23);
                 if (lt == 0) unit_qinv[uc % kTcUnitRing] = __uint_as_float((uint32_t)(127 - sh) << 23);
             }
-            for (int i = lt; i < rp * 16; i += C::LOADERS) {
-                const int r = i >> 4, c16 = i & 15;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (r < un.rows) {
-                    w = __ldg(reinterpret_cast<const uint4*>(query_row(r)) + c16);
+            constexpr int QK = 6;                              // loads of a thread in flight
+            for (int i0 = lt; i0 < rp * 16; i0 += C::LOADERS * QK) {
+                uint4 w[QK];
+#pragma unroll
+                for (int k = 0; k < QK; ++k) {
+                    const int i = i0 + C::LOADERS * k, r = i >> 4;
+                    w[k] = r < un.rows ? __ldg(reinterpret_cast<const uint4*>(query_row(r)) + (i & 15)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < QK; ++k) {
+                    const int i = i0 + C::LOADERS * k, r = i >> 4, c16 = i & 15;
                     if constexpr (FP8) {
                         float x[8];
-                        unpack8(w, x);
-                        w = make_uint4(pack_f16(x[0] * qscale, x[1] * qscale), pack_f16(x[2] * qscale, x[3] * qscale),
-                                       pack_f16(x[4] * qscale, x[5] * qscale), pack_f16(x[6] * qscale, x[7] * qscale));
+                        unpack8(w[k], x);
+                        w[k] = make_uint4(pack_f16(x[0] * qscale, x[1] * qscale), pack_f16(x[2] * qscale, x[3] * qscale),
+                                          pack_f16(x[4] * qscale, x[5] * qscale), pack_f16(x[6] * qscale, x[7] * qscale));
                     }
+                    if (r < rp) *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w[k];
                 }
-                *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w;
             }
             proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[qb]);
 
             // ---- the unit's tiles.  What a tile needs of the block table is loaded one tile
-            // before it is used: for a TMA tile, lane i of the first warp finds the page of
-            // box i; else every warp's lanes find those of its rows.
-            int page = -1, slot = 0;
+            // before it is used: for a TMA tile, lane i of the first two warps (one issues the
+            // keys, one the values) finds the page of box i; else every warp's lanes find those of its rows.
             auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
             const int boxes = box > 0 ? kTcTile / box : 0;
+            int page = 0, slot = 0;
+            bool want = false;                                  // the lane has one to look up (not looked at yet)
             auto locate = [&](int i) {
-                page = -1;
-                if (i >= un.tb) return;
                 const bool tma = by_tma(i);
                 const int pos = i * kTcTile + (tma ? lane * box : lw * WROWS + lane);
-                if (tma ? lw == 0 && lane < boxes : lane < WROWS && pos < un.sl.total) {
-                    const int pg = pos / a.c.page_size;
-                    slot = pos - pg * a.c.page_size;
-                    page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -2;
-                    if (page == -1) page = -2;                  // -1: no position
+                want = i < un.tb && (tma ? lw < 2 && lane < boxes : lane < WROWS && pos < un.sl.total);
+                if (want) {
+                    const int pg = page_index(a, pos, &slot);
+                    page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
                 }
             };
             // E4M3: the page of the row whose scales the lane copies
@@ -409,17 +440,16 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 spage = -1;
                 const int pos = i * kTcTile + lw * WROWS + lane;
                 if (i < un.tb && lane < WROWS && pos < un.sl.total) {
-                    const int pg = pos / a.c.page_size;
-                    sslot = pos - pg * a.c.page_size;
-                    spage = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
+                    const int pg = page_index(a, pos, &sslot);
+                    if (pg < a.c.max_pages) spage = __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg);
                 }
             };
             locate(un.ta);
             if constexpr (FP8) locate_scale(un.ta);
             for (int i = un.ta; i < un.tb && ok; ++i) {
                 const bool tma = by_tma(i);
-                const bool have = (unsigned)page < (unsigned)a.c.num_pages;
-                if (__any_sync(0xffffffffu, !have && page != -1) && lane == 0) {
+                const bool have = want && (unsigned)page < (unsigned)a.c.num_pages;
+                if (__any_sync(0xffffffffu, want && !have) && lane == 0) {
 #pragma unroll
                     for (int w = 0; w < NSM; ++w) unit_bad[w][uc % kTcUnitRing] = 1;
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
@@ -448,7 +478,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     }
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     if (tma) {
-                        if (lw == 0) {
+                        if (lw == kv) {
                             if (lane == 0) mbar_expect(bar, FP8 ? kTcRaw : kTcBuf);
                             __syncwarp();
                             if (lane < boxes) {
@@ -543,12 +573,13 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             // operands at their first buffers; a step in bytes is a sixteenth of it here
             const uint64_t k_d = tc_desc(base, 16, 1024), q_d = tc_desc(base + C::Q_OFF, 16, 1024);
             const uint64_t v_d = tc_desc(base, 16384, 1024), p_d = tc_desc(base + C::P_OFF, 16384, 1024);
-            auto scores = [&](int qb, bool first, bool last) { // S of tile g
+            // own_copies: the threads' cp.asyncs, which arrived by themselves, unfenced
+            auto scores = [&](int qb, bool first, bool last, bool own_copies) { // S of tile g
                 if (first && !wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit)) return false;
                 const unsigned kb = 2 * g;
                 if (!wait_bounded(&full[kb % NBUF], (kb / NBUF) & 1u, limit)) return false;
                 if (g >= 2 && !wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit)) return false;
-                proxy_fence();                                 // copies that arrived by themselves
+                if (own_copies) proxy_fence();
                 tc_after();
                 const uint64_t kd = k_d + (kb % NBUF) * (kTcBuf / 16), qd = q_d + qb * (C::QBYTES / 16);
                 const uint32_t at = tmem + (g & 1) * RP;
@@ -560,11 +591,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 if (last) tc_commit(&q_free[qb]);
                 return true;
             };
-            auto sums = [&](unsigned t, bool first) {           // O += V P of tile t
+            auto sums = [&](unsigned t, bool first, bool own_copies) {          // O += V P of tile t
                 const unsigned vb = 2 * t + 1;
                 if (!wait_bounded(&full[vb % NBUF], (vb / NBUF) & 1u, limit)) return false;
                 if (!wait_bounded(&p_full, t & 1u, limit)) return false;
-                proxy_fence();
+                if (own_copies) proxy_fence();
                 tc_after();
                 const uint64_t vd = v_d + (vb % NBUF) * (kTcBuf / 16);
 #pragma unroll
@@ -573,18 +604,20 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 tc_commit(&pv_done);
                 return true;
             };
-            bool pend = false, pend_first = false;
+            bool pend = false, pend_first = false, pend_copies = false;
             while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
                 for (int i = un.ta; i < un.tb && ok; ++i) {
-                    ok = scores((int)(uc % C::QB), i == un.ta, i + 1 == un.tb);
-                    if (ok && pend) ok = sums(g - 1, pend_first);
+                    const bool copies = !FP8 && !(box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total));
+                    ok = scores((int)(uc % C::QB), i == un.ta, i + 1 == un.tb, copies);
+                    if (ok && pend) ok = sums(g - 1, pend_first, pend_copies);
                     pend = true;
+                    pend_copies = copies;
                     pend_first = i == un.ta;
                     ++g;
                 }
                 ++uc;
             }
-            if (ok && pend) ok = sums(g - 1, pend_first);
+            if (ok && pend) ok = sums(g - 1, pend_first, pend_copies);
             // every product must have ended before tensor memory is given back
             tc_commit(&drained);
             if (!wait_bounded(&drained, 0, kTcWaitLimit) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
@@ -612,7 +645,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             // ---- the unit's rows, and who sees whom
             named_sync(bar, 128);                              // the unit before is done with the tables
             if (row < C::COLS) {
-                const int R = un.r0 + min(c0 + row, un.rows - 1), n = R / a.G;
+                const int R = un.r0 + min(c0 + row, un.rows - 1), n = row_position(a, R);
                 rown[c0 + row] = (short)n;
                 rowat[c0 + row] = n * a.Hq + un.hk * a.G + (R - n * a.G);
                 nref[c0 + row] = -kNoRef;
@@ -693,24 +726,52 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     else return x;
                 };
                 const uint32_t s_at = lanes + (g & 1) * RP + c0;
-                auto highest = [&](auto mask) {
-                    float top = kNegInf;
+                // Reads the scores two chunks at a time, takes them relative to the references
+                // and gives them to `use(first row, 16 values)`.
+                auto each = [&](auto mask, auto use) {
 #pragma unroll
-                    for (int ch = 0; ch < CH; ++ch)
-                        if (ch < chunks) {
-                            float v[16];
-                            tc_ld16(s_at + ch * 16, v);
+                    for (int c2_ = 0; c2_ < CH; c2_ += 2) {
+                        if (c2_ < chunks) {
+                        float v[2][16];
+                        const bool two = c2_ + 1 < CH;         // (a second chunk past the unit's rows is read and left)
+                        tc_ld16_start(s_at + c2_ * 16, v[0]);
+                        if (two) tc_ld16_start(s_at + c2_ * 16 + 16, v[1]);
+                        tc_wait_ld();
+                        tc_ld16_done(v[0]);
+                        if (two) tc_ld16_done(v[1]);
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const int k = ch * 16 + j;
-                                const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
-                                top = fmaxf(top, fmaxf(fmaxf(arg(mask, v[j], k, nr.x), arg(mask, v[j + 1], k + 1, nr.y)),
-                                                       fmaxf(arg(mask, v[j + 2], k + 2, nr.z), arg(mask, v[j + 3], k + 3, nr.w))));
+                        for (int h = 0; h < 2; ++h)
+                            if (h == 0 || (two && c2_ + 1 < chunks)) {
+#pragma unroll
+                                for (int j = 0; j < 16; j += 4) {
+                                    const int k = (c2_ + h) * 16 + j;
+                                    const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
+                                    v[h][j] = arg(mask, v[h][j], k, nr.x);
+                                    v[h][j + 1] = arg(mask, v[h][j + 1], k + 1, nr.y);
+                                    v[h][j + 2] = arg(mask, v[h][j + 2], k + 2, nr.z);
+                                    v[h][j + 3] = arg(mask, v[h][j + 3], k + 3, nr.w);
+                                }
+                                use((c2_ + h) * 16, v[h]);
                             }
                         }
+                    }
+                };
+                float x[C::KEEP ? CH * 16 : 1];
+                auto score_all = [&](auto mask) {
+                    float top = kNegInf;
+                    each(mask, [&](int k0, const float (&v)[16]) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            top = fmaxf(top, fmaxf(fmaxf(v[j], v[j + 1]), fmaxf(v[j + 2], v[j + 3])));
+                            if constexpr (C::KEEP) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) x[k0 + j + e] = v[j + e];
+                            }
+                        }
+                    });
                     return top;
                 };
-                const float top = masked ? highest(Yes{}) : highest(No{});
+                const float top = masked ? score_all(Yes{}) : score_all(No{});
                 const bool first = i == un.ta;
                 ok = ok && !late;
                 if (named_any(bar, 128, !ok || top > kRefSlack)) {
@@ -757,42 +818,49 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                                 tc_st16(lanes + 2 * RP + c0 + ch * 16, v);
                             }
                         }
+                    if (C::KEEP) {
+                        if (masked) score_all(Yes{});
+                        else score_all(No{});
+                    }
                 }
                 // ---- probabilities; P is free once the tile before has been summed
                 if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
                 late = !ok;
-                auto weigh = [&](auto mask) {
-                    unsigned char* prow = smem + C::P_OFF + row * 128;
+                unsigned char* prow = smem + C::P_OFF + row * 128;
+                auto weigh = [&](int k0, const float (&v)[16]) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
+                        if constexpr (FP8) {                   // a masked scale may be anything
+                            l[k0 + j] += y != 0.f ? y * vinv : 0.f;
+                            l[k0 + j + 1] += z != 0.f ? z * vinv : 0.f;
+                            w[j >> 1] = pack_f16(y, z);
+                        } else {
+                            l[k0 + j] += y;
+                            l[k0 + j + 1] += z;
+                            w[j >> 1] = pack_bf16(y, z);
+                        }
+                    }
+                    const int c = c0 + k0;
+                    unsigned char* at = prow + (c >> 6) * 16384;
+                    const int k = (c & 63) >> 3;
+                    *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                };
+                if constexpr (C::KEEP) {
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch)
                         if (ch < chunks) {
                             float v[16];
-                            tc_ld16(s_at + ch * 16, v);
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const int k = ch * 16 + j;
-                                const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
-                                v[j] = ex2_approx(arg(mask, v[j], k, nr.x));
-                                v[j + 1] = ex2_approx(arg(mask, v[j + 1], k + 1, nr.y));
-                                v[j + 2] = ex2_approx(arg(mask, v[j + 2], k + 2, nr.z));
-                                v[j + 3] = ex2_approx(arg(mask, v[j + 3], k + 3, nr.w));
-                            }
-                            uint32_t w[8];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if constexpr (FP8) l[ch * 16 + j] += v[j] != 0.f ? v[j] * vinv : 0.f;   // a masked scale may be anything
-                                else l[ch * 16 + j] += v[j];
-                                if (j & 1) w[j >> 1] = FP8 ? pack_f16(v[j - 1], v[j]) : pack_bf16(v[j - 1], v[j]);
-                            }
-                            const int c = c0 + ch * 16;
-                            unsigned char* at = prow + (c >> 6) * 16384;
-                            const int k = (c & 63) >> 3;
-                            *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                            for (int j = 0; j < 16; ++j) v[j] = x[ch * 16 + j];
+                            weigh(ch * 16, v);
                         }
-                };
-                if (masked) weigh(Yes{});
-                else weigh(No{});
+                } else {
+                    if (masked) each(Yes{}, weigh);
+                    else each(No{}, weigh);
+                }
                 proxy_fence();
                 tc_before();
                 __syncwarp();
@@ -890,7 +958,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 // the unit's CTAs: c0 begins it, c1 ends it; the last warpgroup to arrive adds
                 // its rows' parts
                 const int f0 = share_of(plan.total, plan.n, un.at), f1 = share_of(plan.total, plan.n, un.at + un.tiles - 1);
-                int* counter = counters + 2 * f0 + wg;         // no CTA begins two units that others end
+                int* counter = counters + NSM * f0 + wg;         // no CTA begins two units that others end
                 __threadfence();
                 named_sync(bar, 128);
                 if (row == 0) {
@@ -901,7 +969,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 named_sync(bar, 128);
                 if (last_cta[wg]) {
                     __threadfence();
-                    join_parts<kTcD, 128>(a, un, row, slots, slot_floats, srows, f0, f1, c0, c0 + mine);
+                    join_parts<kTcD, 4>(a, un, warp & 3, slots, slot_floats, srows, f0, f1, c0, c0 + mine);
                 }
             }
             ++uc;
@@ -919,14 +987,15 @@ static int tc_block_rows(int rt, int most) {
     const int blocks = (rt + most - 1) / most;
     return ((rt + blocks - 1) / blocks + 15) / 16 * 16;
 }
-constexpr int kTcMostBf16 = 160, kTcMostFp8 = 128;
+constexpr int kTcMostBf16 = 144, kTcMostFp8 = 128;
 
 bool attend_takes_tc(int N, int G, int D) { return D == kTcD; }
 
 size_t attend_tc_workspace(int N, int G) {
-    const int rt = N * G, rows = tc_block_rows(rt, kTcMostBf16) > tc_block_rows(rt, kTcMostFp8) ? tc_block_rows(rt, kTcMostBf16)
-                                                                                             : tc_block_rows(rt, kTcMostFp8);
-    return kAttHead + align256((size_t)2 * kTcMaxCtas * part_floats(rt < rows ? rt : rows, kTcD) * 4);
+    // the largest block of rows that N G or fewer can come in, so that more rows
+    // never need less
+    const int rt = N * G, rows = rt < kTcMostBf16 ? rt : kTcMostBf16;
+    return kAttHead + align256((size_t)2 * kTcMaxCtas * part_floats(rows, kTcD) * 4);
 }
 
 // The driver's tensor map encoder (the library links the runtime only).
@@ -996,7 +1065,7 @@ static cudaError_t launch_tc_e(const AttendArgs& a, cudaStream_t st) {
     if (rp <= 16) return launch_tc_t<1, 1, FP8>(a, br, rp, st);
     if (rp <= 32) return launch_tc_t<2, 1, FP8>(a, br, rp, st);
     if (rp <= 64) return launch_tc_t<4, 1, FP8>(a, br, rp, st);
-    return launch_tc_t<FP8 ? 4 : 5, 2, FP8>(a, br, rp, st);
+    return launch_tc_t<FP8 ? 4 : 3, FP8 ? 2 : 3, FP8>(a, br, rp, st);
 }
 
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st) {

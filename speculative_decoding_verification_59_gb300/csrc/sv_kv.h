@@ -39,6 +39,8 @@ struct AttendArgs {
     const int32_t *ctx, *newl, *par;
     float scale;
     int B, N, Hq, G;                       // G query heads per cached head
+    uint32_t g_mul;                        // ceil(2^32 / G), for G > 1: R / G = mulhi(R, g_mul), R < 2^32 / G
+    int page_shift;                        // log2(page_size), -1 when it is no power of two
     char* out;                             // bf16
     float* lse;
     char* ws;
