@@ -15,14 +15,15 @@
 //
 // The warps of a CTA, one CTA per SM, each walking the CTA's share:
 //   softmax   4 warps (8 or 12 from 65 rows on, each 4 with their share of the rows)
-//   MMA       1 thread issues every tcgen05.mma
-//   loaders   4 warps bring the queries, keys and values into a ring of 32 KB
-//             buffers.  A tile of old positions whose pages fit it (page sizes
+//   MMA       2 threads: one issues the first product, one the second
+//   loaders   4 warps bring the queries, and keys and values into a ring of 32 KB
+//             buffers each.  A tile of old positions whose pages fit it (page sizes
 //             that divide 128, from 8 on, or are multiples of it) comes by TMA, a box
 //             per page; other page sizes, and the tiles with new positions, where
 //             stale entries are left out, by the threads' 16-byte cp.async.  The
-//             rows of an E4M3 cache go to a ring of their own first, and the
-//             loaders (8 warps where registers allow) widen them to fp16.
+//             rows of an E4M3 cache go to rings of their own first and are widened
+//             to fp16 by the loaders, then 8 warps in two teams, one for the keys and
+//             one for the values.
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
 //
@@ -42,9 +43,10 @@ constexpr int kTcTile = 128;
 constexpr int kTcD = 128;
 constexpr int kTcBuf = kTcTile * kTcD * 2;       // a tile's keys or values as the products read them: 32 KB
 constexpr int kTcRaw = kTcTile * kTcD;           // the same as the cache's 8-bit rows: 16 KB
-constexpr int kTcScaleRing = 8;                  // tiles whose scales are held
-// The loaders run at most 6 units ahead of the softmax (raw and widened buffers,
-// two score buffers), so what they tell it by unit is kept for 8.
+// The loaders run at most 6 tiles ahead of the softmax (raw and widened buffers,
+// two score buffers): scales are held for 7 tiles, what the loaders tell the
+// softmax by unit for 8.
+constexpr int kTcScaleRing = 7;
 constexpr int kTcUnitRing = 8;
 // Polls of a wait before it gives up, whatever larger bound is in force: a poll
 // sleeps for up to some ten microseconds here, and no wait of this kernel lasts
@@ -62,23 +64,27 @@ struct TcCfg {
     static constexpr int COLS = CH * 16;         // rows of a softmax warpgroup
     static constexpr int RP = NSM * COLS;        // rows of a unit, at most
     static constexpr int PB = (RP + 63) / 64;    // 64-row blocks of P
-    static constexpr int QB = RP <= 32 || (RP <= 64 && !FP8) ? 2 : 1;    // units whose queries are held
-    static constexpr int NBUF = FP8 ? 3 : RP > 64 ? 4 : 5;
-    static constexpr int NRAW = FP8 ? (RP > 64 ? 3 : 5) : 1;    // (a bf16 cache has none)
+    static constexpr int QB = RP <= 32 && !FP8 ? 2 : 1;        // units whose queries are held
+    static constexpr int KB = FP8 && RP > 32 ? 1 : 2;            // buffers of keys, of values
+    static constexpr int VB = FP8 || RP > 64 ? 2 : 3;
+    static constexpr int TEAMS = FP8 ? 2 : 1;
+    static constexpr int KR = FP8 ? 2 : 1, VR = FP8 ? 2 : 1;     // raw buffers (a bf16 cache has none)
     static constexpr int WORDS = (COLS + 31) / 32;   // a bit for each row of a warpgroup
     // Up to 32 rows the scores stay in registers between the vote and the
     // probabilities, beside as many running totals; beyond, they are read from
     // tensor memory twice.
     static constexpr bool KEEP = CH <= 2;
     static constexpr int SM_THREADS = NSM * 128;
-    static constexpr int LOADERS = FP8 && NSM == 1 ? 256 : 128;
-    static constexpr int THREADS = SM_THREADS + 32 + LOADERS;
-    static constexpr int P_OFF = NBUF * kTcBuf;
+    static constexpr int LOADERS = 128 * TEAMS;
+    static constexpr int THREADS = SM_THREADS + 64 + LOADERS;
+    static constexpr int V_OFF = KB * kTcBuf;
+    static constexpr int P_OFF = V_OFF + VB * kTcBuf;
     static constexpr int Q_OFF = P_OFF + PB * 16384;
     static constexpr int QBYTES = RP * 256;
     static constexpr int RAW_OFF = Q_OFF + QB * QBYTES;
-    static constexpr int SCALE_OFF = RAW_OFF + (FP8 ? NRAW * kTcRaw : 0);
+    static constexpr int SCALE_OFF = RAW_OFF + (FP8 ? (KR + VR) * kTcRaw : 0);
     static constexpr int SMEM = SCALE_OFF + (FP8 ? kTcScaleRing * 2 * kTcTile * 4 : 0) + 1024;   // and room to align
+    static_assert(SMEM <= 227 * 1024, "dynamic shared memory");
     static constexpr int TMEM = 3 * RP <= 64 ? 64 : 3 * RP <= 128 ? 128 : 3 * RP <= 256 ? 256 : 512;
 };
 
@@ -229,10 +235,12 @@ template <int CH, int NSM, bool FP8>
 __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, int box, uint32_t limit, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
     using C = TcCfg<CH, NSM, FP8>;
-    constexpr int RP = C::RP, NBUF = C::NBUF;
+    constexpr int RP = C::RP, KB = C::KB, VB = C::VB;
     extern __shared__ unsigned char smem_raw[];
     __shared__ AttPlan plan;
-    __shared__ __align__(8) uint64_t full[NBUF], empty[NBUF], s_full[2], s_free[2], p_full, pv_done, q_full[C::QB], q_free[C::QB];
+    __shared__ __align__(8) uint64_t k_full[KB], k_empty[KB], v_full[VB], v_empty[VB], s_full[2], s_free[2], p_full, pv_done,
+        q_full[C::QB], q_free[C::QB], drained[2];
+    __shared__ __align__(8) uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
@@ -240,26 +248,37 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ unsigned long long anc[NSM][2][kMaxNewTree];    // trees: ancestors and itself, by node
     __shared__ short up[NSM][2][kMaxNewTree];
     __shared__ uint32_t vis[NSM][kMaxNewTree][C::WORDS];       // trees: the warpgroup's rows that see a node
-    __shared__ __align__(8) uint64_t raw_full[C::NRAW], raw_empty[C::NRAW];
     __shared__ uint32_t tmem_at;
     __shared__ int unit_bad[NSM][kTcUnitRing];                  // a page that is none
     __shared__ float unit_qinv[kTcUnitRing];                    // E4M3: what takes back the queries' scaling
     __shared__ int odd_any, last_cta[NSM], tree_bad[NSM];
-    __shared__ __align__(8) uint64_t drained;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kMmaWarp = C::SM_THREADS / 32;
 
     if (tid == 0) {
-        for (int i = 0; i < NBUF; ++i) {
-            mbar_init(&full[i], FP8 ? C::LOADERS / 32 : C::LOADERS);
-            mbar_init(&empty[i], 1);
+        // operands: every thread of the loaders that copies arrives, or a lane of each
+        // of the four warps that widen
+        for (int i = 0; i < KB; ++i) {
+            mbar_init(&k_full[i], FP8 ? 4 : 128);
+            mbar_init(&k_empty[i], 1);
         }
-        if constexpr (FP8)
-            for (int i = 0; i < C::NRAW; ++i) {
-                mbar_init(&raw_full[i], C::LOADERS);
-                mbar_init(&raw_empty[i], C::LOADERS / 32);
+        for (int i = 0; i < VB; ++i) {
+            mbar_init(&v_full[i], FP8 ? 4 : 128);
+            mbar_init(&v_empty[i], 1);
+        }
+        if constexpr (FP8) {
+            for (int i = 0; i < C::KR; ++i) {
+                mbar_init(&kr_full[i], 128);
+                mbar_init(&kr_empty[i], 4);
             }
+            for (int i = 0; i < C::VR; ++i) {
+                mbar_init(&vr_full[i], 128);
+                mbar_init(&vr_empty[i], 4);
+            }
+        }
+        mbar_init(&drained[0], 1);
+        mbar_init(&drained[1], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_free[i], C::SM_THREADS / 32);
@@ -270,7 +289,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             mbar_init(&q_full[i], C::LOADERS / 32);
             mbar_init(&q_free[i], 1);
         }
-        mbar_init(&drained, 1);
         mbar_init_fence();
         odd_any = 0;
         for (int i = 0; i < NSM * kTcUnitRing; ++i) unit_bad[0][i] = 0;
@@ -293,35 +311,38 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         walk.b = 0;
     }
 
-    if (warp > kMmaWarp) {
+    if (warp > kMmaWarp + 1) {
         // ================= loaders =================
-        const int lt = tid - C::SM_THREADS - 32, lw = lt >> 5;
-        constexpr int LW = C::LOADERS / 32;
+        const int lt = tid - C::SM_THREADS - 64, lw = (lt >> 5) & 3;
+        const int team = C::TEAMS == 2 ? lt >> 7 : 0;          // two teams: 0 keys, 1 values
         constexpr int CPR = FP8 ? 8 : 16;                      // 16-byte chunks of a cached row
         constexpr int RPI = 32 / CPR;                          // rows a warp copies at once
-        constexpr int WROWS = kTcTile / LW;                    // rows of a tile that a warp copies
-        constexpr int PIECES = WROWS / RPI;                    // of 16 bytes a thread
-        constexpr int LAG = C::NRAW - 1;                       // raw buffers in flight behind the one being issued
+        constexpr int PIECES = 32 / RPI;                       // a warp's 32 rows: pieces of 16 bytes a thread
         const int ch = lane % CPR, sub = lane / CPR;
         bool ok = true;
-        unsigned q = 0;                                        // buffers issued (keys and values in turn)
+        unsigned t = 0;                                        // tiles issued
         unsigned uc = 0;                                       // units
-        unsigned done = 0;                                     // E4M3: buffers widened
-        struct Flight {                                        // what widening one needs
+        unsigned done = 0;                                     // E4M3: tiles widened
+        unsigned ends[C::QB];                                  // by query buffer: t after the unit that had it
+        struct Flight {                                        // what widening a tile needs
             int p0, ctx, total;
         };
-        Flight fl[LAG + 1];
-        unsigned ends[C::QB];                                  // by query buffer: q after the unit that had it
-        auto widen = [&](unsigned j, const Flight& f) {        // E4M3: raw buffer j to the products' form
-            if (ok) ok = wait_bounded(&raw_full[j % C::NRAW], (j / C::NRAW) & 1u, limit);
-            if (ok && j >= (unsigned)NBUF) ok = wait_bounded(&empty[j % NBUF], (j / NBUF - 1) & 1u, limit);
+        constexpr int LAG = FP8 ? C::KR - 1 : 0;               // raw tiles in flight behind the one being issued
+        static_assert(!FP8 || C::KR == C::VR, "one lag for both");
+        Flight fl[LAG + 1] = {};
+        auto widen_one = [&](unsigned j, const Flight& f, bool val) {      // E4M3: a raw tile to the products' form
+            uint64_t* rf = val ? &vr_full[j % C::VR] : &kr_full[j % C::KR];
+            uint64_t* em = val ? &v_empty[j % VB] : &k_empty[j % KB];
+            const unsigned n = val ? VB : KB, nr = val ? C::VR : C::KR;
+            if (ok) ok = wait_bounded(rf, (j / nr) & 1u, limit);
+            if (ok && j >= n) ok = wait_bounded(em, (j / n - 1) & 1u, limit);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
-            unsigned char* dst = smem + (j % NBUF) * kTcBuf;
-            const unsigned char* raw = smem + C::RAW_OFF + (j % C::NRAW) * kTcRaw;
-            const bool fresh = (j & 1u) && f.p0 + kTcTile > f.ctx;             // values, new positions among them
+            unsigned char* dst = smem + (val ? C::V_OFF + (j % VB) * kTcBuf : (j % KB) * kTcBuf);
+            const unsigned char* raw = smem + C::RAW_OFF + (val ? C::KR + j % C::VR : j % C::KR) * kTcRaw;
+            const bool fresh = val && f.p0 + kTcTile > f.ctx;                  // values, new positions among them
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) {
-                const int row = lw * WROWS + p * RPI + sub;
+                const int row = lw * 32 + p * RPI + sub;
                 uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ch * 16);
                 if (fresh && f.p0 + row >= f.ctx && f.p0 + row < f.total &&
                     (has_odd_e4m3(w.x) || has_odd_e4m3(w.y) || has_odd_e4m3(w.z) || has_odd_e4m3(w.w))) {
@@ -349,17 +370,18 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             proxy_fence();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&raw_empty[j % C::NRAW]);
-                mbar_arrive(&full[j % NBUF]);
+                mbar_arrive(val ? &vr_empty[j % C::VR] : &kr_empty[j % C::KR]);
+                mbar_arrive(val ? &v_full[j % VB] : &k_full[j % KB]);
             }
         };
+        auto widen = [&](unsigned j) { widen_one(j, fl[j % (LAG + 1)], team == 1); };
         while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
             // ---- the unit's queries
             const int qb = (int)(uc % C::QB);
             if constexpr (FP8) {
                 // what frees them is the last product of the unit that had them, whose keys
                 // may still be raw
-                for (; uc >= (unsigned)C::QB && done < ends[qb] && ok; ++done) widen(done, fl[done % (LAG + 1)]);
+                for (; uc >= (unsigned)C::QB && done < ends[qb] && ok; ++done) widen(done);
             }
             if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -418,209 +440,208 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[qb]);
 
-            // ---- the unit's tiles.  What a tile needs of the block table is loaded one tile
-            // before it is used: for a TMA tile, lane i of the first two warps (one issues the
-            // keys, one the values) finds the page of box i; else every warp's lanes find those of its rows.
+            // ---- the unit's tiles
             auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
-            const int boxes = box > 0 ? kTcTile / box : 0;
-            int page = 0, slot = 0;
-            bool want = false;                                  // the lane has one to look up (not looked at yet)
-            auto locate = [&](int i) {
-                const bool tma = by_tma(i);
-                const int pos = i * kTcTile + (tma ? lane * box : lw * WROWS + lane);
-                want = i < un.tb && (tma ? lw < 2 && lane < boxes : lane < WROWS && pos < un.sl.total);
-                if (want) {
-                    const int pg = page_index(a, pos, &slot);
-                    page = pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
-                }
+            auto table = [&](int pg) {                          // entry pg of the sequence's row; -1 past it
+                return pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
             };
-            // E4M3: the page of the row whose scales the lane copies
-            int spage = -1, sslot = 0;
-            auto locate_scale = [&](int i) {
-                spage = -1;
-                const int pos = i * kTcTile + lw * WROWS + lane;
-                if (i < un.tb && lane < WROWS && pos < un.sl.total) {
-                    const int pg = page_index(a, pos, &sslot);
-                    if (pg < a.c.max_pages) spage = __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg);
-                }
+            // What TMA tiles need of the block table is loaded for 32 boxes at once, a
+            // group before it is used: lane l holds box l of the group (a load of
+            // its own before each tile cost 1400 cycles a tile).
+            const int boxes = box > 0 ? kTcTile / box : 1;      // a tile's: 1, 2, .. 16
+            const int group = 32 / boxes;                       // tiles of a group
+            auto group_page = [&](int i0) {                     // group of tiles from i0 on
+                int slot;
+                const int pos = i0 * kTcTile + lane * box;
+                return box > 0 && pos + box <= min(un.sl.ctx, un.sl.total) ? table(page_index(a, pos, &slot)) : -1;
             };
-            locate(un.ta);
-            if constexpr (FP8) locate_scale(un.ta);
+            int g0 = un.ta, pages = group_page(g0), pages_next = group_page(g0 + group);
+            // The other tiles: lane l finds row l of the warp's 32.  E4M3: so do the
+            // scales of every tile, one tile ahead.
+            auto row_page = [&](int i, int* slot) {
+                const int pos = i * kTcTile + lw * 32 + lane;
+                *slot = 0;
+                return pos < un.sl.total ? table(page_index(a, pos, slot)) : -2;      // -2: no position
+            };
+            int spage = -2, sslot = 0;
+            if (FP8 && team == 0) spage = row_page(un.ta, &sslot);
             for (int i = un.ta; i < un.tb && ok; ++i) {
                 const bool tma = by_tma(i);
-                const bool have = want && (unsigned)page < (unsigned)a.c.num_pages;
-                if (__any_sync(0xffffffffu, want && !have) && lane == 0) {
+                int at_page = 0, at_slot = 0;                   // TMA: the lane's box; else the lane's row
+                bool have = false, lost = false;
+                if (tma) {
+                    if (i == g0 + group) {
+                        g0 = i;
+                        pages = pages_next;
+                        pages_next = group_page(g0 + group);
+                    }
+                    at_page = __shfl_sync(0xffffffffu, pages, ((i - g0) * boxes + lane) & 31);
+                    if (box == kTcTile) page_index(a, i * kTcTile, &at_slot);       // a page may hold several tiles
+                    have = (unsigned)at_page < (unsigned)a.c.num_pages;
+                    lost = lane < boxes && !have;
+                    if (!have) at_page = 0;                     // the unit ends as NaN anyway
+                } else {
+                    at_page = row_page(i, &at_slot);
+                    have = (unsigned)at_page < (unsigned)a.c.num_pages;
+                    lost = !have && at_page != -2;
+                }
+                if (__any_sync(0xffffffffu, lost) && lane == 0) {
 #pragma unroll
                     for (int w = 0; w < NSM; ++w) unit_bad[w][uc % kTcUnitRing] = 1;
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
                 }
-                const int at_page = have ? page : 0, at_slot = slot;      // a bad page's unit ends as NaN anyway
-                const int64_t off = have && !tma ? entry_off(a.c, page, slot, un.hk) : 0;
+                const int64_t off = have && !tma ? entry_off(a.c, at_page, at_slot, un.hk) : 0;
                 const unsigned havem = __ballot_sync(0xffffffffu, have);
-                locate(i + 1);
-                for (int kv = 0; kv < 2; ++kv) {
-                    // the buffer's stage, once it is free
+                for (int kv = C::TEAMS == 2 ? team : 0; kv < (C::TEAMS == 2 ? team + 1 : 2); ++kv) {
+                    // The buffer, once it is free.  Every warp waits for every buffer of its
+                    // kind and arrives for it, the ones that have no part in a TMA tile too: a
+                    // barrier tells its last two phases apart, no more, so none may
+                    // fall behind or run ahead.
                     uint32_t dst;
                     uint64_t* bar;
                     if constexpr (FP8) {
-                        if (lane == 0 && q >= (unsigned)C::NRAW)
-                            ok = wait_bounded(&raw_empty[q % C::NRAW], (q / C::NRAW - 1) & 1u, limit);
-                        dst = smem_addr(smem + C::RAW_OFF + (q % C::NRAW) * kTcRaw);
-                        bar = &raw_full[q % C::NRAW];
+                        constexpr int n = C::KR;
+                        if (lane == 0 && t >= (unsigned)n) ok = wait_bounded(kv ? &vr_empty[t % n] : &kr_empty[t % n], (t / n - 1) & 1u, limit);
+                        dst = smem_addr(smem + C::RAW_OFF + (kv ? n + t % n : t % n) * kTcRaw);
+                        bar = kv ? &vr_full[t % n] : &kr_full[t % n];
                     } else {
-                        // Every warp waits for every buffer and arrives for it, the ones that have
-                        // no part in a TMA tile too: a barrier tells its last two phases apart,
-                        // no more, so none may fall behind or run ahead.
-                        if (lane == 0 && q >= (unsigned)NBUF)
-                            ok = wait_bounded(&empty[q % NBUF], (q / NBUF - 1) & 1u, limit);
-                        dst = smem_addr(smem + (q % NBUF) * kTcBuf);
-                        bar = &full[q % NBUF];
+                        const unsigned n = kv ? VB : KB;
+                        if (lane == 0 && t >= n) ok = wait_bounded(kv ? &v_empty[t % VB] : &k_empty[t % KB], (t / n - 1) & 1u, limit);
+                        dst = smem_addr(smem + (kv ? C::V_OFF + (t % VB) * kTcBuf : (t % KB) * kTcBuf));
+                        bar = kv ? &v_full[t % VB] : &k_full[t % KB];
                     }
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     if (tma) {
-                        if (lw == kv) {
+                        if (lw == (C::TEAMS == 2 ? 0 : kv)) {   // one warp issues the keys, one the values
                             if (lane == 0) mbar_expect(bar, FP8 ? kTcRaw : kTcBuf);
                             __syncwarp();
                             if (lane < boxes) {
                                 const CUtensorMap* map = kv ? &vmap : &kmap;
-                                if constexpr (FP8) {
-                                    tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
-                                } else {
-                                    tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
-                                    tma_load(dst + 16384 + lane * box * 128, map, 64, at_slot, un.hk, at_page, bar);
-                                }
+                                tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
+                                if constexpr (!FP8) tma_load(dst + 16384 + lane * box * 128, map, 64, at_slot, un.hk, at_page, bar);
                             }
                             __syncwarp();
                         }
-                        // every warp arrives, so that none is a phase of a barrier behind
-                        if ((!FP8 || kv == 1) && lane == 0) mbar_arrive_n(bar, 32);
                     } else {
                         const char* base = static_cast<const char*>(kv ? a.c.v : a.c.k);
 #pragma unroll
                         for (int p = 0; p < PIECES; ++p) {
-                            const int wr = p * RPI + sub, row = lw * WROWS + wr;
+                            const int wr = p * RPI + sub, row = lw * 32 + wr;
                             const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
                             cp16(dst + (FP8 ? row * 128 + ch * 16 : tc_off(row, ch)), base + e, (havem >> wr) & 1u);
                         }
                     }
+                    bool copies = !tma;                         // the threads have copies of their own in flight
                     if constexpr (FP8) {
-                        if (kv == 0 && lane < WROWS) {          // both scales: the softmax wants them with the scores
+                        if (kv == 0) {                          // both scales: the softmax wants them with the scores
                             const bool in = (unsigned)spage < (unsigned)a.c.num_pages;
                             const int64_t so = in ? scale_off(a.c, spage, sslot, un.hk) : 0;
-                            const uint32_t at = smem_addr(smem + C::SCALE_OFF) +
-                                                (((q >> 1) % kTcScaleRing) * 2 * kTcTile + lw * WROWS + lane) * 4;
+                            const uint32_t at = smem_addr(smem + C::SCALE_OFF) + ((t % kTcScaleRing) * 2 * kTcTile + lw * 32 + lane) * 4;
                             cp4(at, a.c.k_scale + so, in);
                             cp4(at + kTcTile * 4, a.c.v_scale + so, in);
+                            spage = i + 1 < un.tb ? row_page(i + 1, &sslot) : -2;
+                            copies = true;
                         }
-                        // the keys' barrier waits for every thread's copies of scales
-                        if (!tma || kv == 0) cp_arrive(bar);
-                        if (kv == 0) locate_scale(i + 1);
-                        fl[q % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total};
-                        ++q;
-                        if (q - done > (unsigned)LAG) {
-                            widen(done, fl[done % (LAG + 1)]);
-                            ++done;
-                        }
-                    } else {
-                        if (tma) {
-                        } else if (kv == 1 && i * kTcTile + kTcTile > un.sl.ctx) {
-                            // new positions: values that are no numbers are taken out (see the
-                            // epilogue), so these rows are waited for here
-                            cp_commit();
-                            cp_wait<0>();
+                    } else if (!tma && kv == 1 && i * kTcTile + kTcTile > un.sl.ctx) {
+                        // new positions: values that are no numbers are taken out (see the
+                        // epilogue), so these rows are waited for here
+                        cp_commit();
+                        cp_wait<0>();
 #pragma unroll
-                            for (int p = 0; p < PIECES; ++p) {
-                                const int row = lw * WROWS + p * RPI + sub, pos = i * kTcTile + row;
-                                if (pos < un.sl.ctx || pos >= un.sl.total) continue;
-                                uint32_t* at = reinterpret_cast<uint32_t*>(smem + (q % NBUF) * kTcBuf + tc_off(row, ch));
+                        for (int p = 0; p < PIECES; ++p) {
+                            const int row = lw * 32 + p * RPI + sub, pos = i * kTcTile + row;
+                            if (pos < un.sl.ctx || pos >= un.sl.total) continue;
+                            uint32_t* at = reinterpret_cast<uint32_t*>(smem + C::V_OFF + (t % VB) * kTcBuf + tc_off(row, ch));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    uint32_t y = at[k];
-                                    if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[k] = y; }
-                                    if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[k] = y; }
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t y = at[k];
+                                if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[k] = y; }
+                                if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[k] = y; }
                             }
-                            mbar_arrive(bar);
-                        } else {
-                            cp_arrive(bar);                     // when this thread's copies have landed
                         }
-                        ++q;
+                    }
+                    if (copies) cp_arrive(bar);                 // when this thread's copies have landed
+                    else if (lane == 0) mbar_arrive_n(bar, 32);
+                }
+                if (!ok) break;
+                if constexpr (FP8) {
+                    fl[t % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total};
+                    if (t - done >= (unsigned)LAG) {
+                        widen(done);
+                        ++done;
                     }
                 }
+                ++t;
             }
-            ends[qb] = q;
+            ends[qb] = t;
             ++uc;
         }
-        // ---- the buffers still in flight
+        // ---- the tiles still in flight
         cp_wait<0>();
         if constexpr (FP8)
-            for (; done < q && ok; ++done) widen(done, fl[done % (LAG + 1)]);
+            for (; done < t && ok; ++done) widen(done);
         if (!ok) {
             // a wait ran out: do not leave while a box may still be on its way
             raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
-            constexpr unsigned DEPTH = FP8 ? C::NRAW : NBUF;
-            if (lw == 0 && lane == 0)
-                for (unsigned j = q > DEPTH ? q - DEPTH : 0u; j < q; ++j)
-                    wait_bounded(FP8 ? &raw_full[j % C::NRAW] : &full[j % NBUF], (j / DEPTH) & 1u, kTcWaitLimit);
+            if (lt == 0) {
+                const unsigned nk = FP8 ? C::KR : KB, nv = FP8 ? C::VR : VB;
+                for (unsigned j = t > nk ? t - nk : 0u; j <= t; ++j)
+                    wait_bounded(FP8 ? &kr_full[j % C::KR] : &k_full[j % KB], (j / nk) & 1u, j < t ? kTcWaitLimit : 1u << 8);
+                for (unsigned j = t > nv ? t - nv : 0u; j <= t; ++j)
+                    wait_bounded(FP8 ? &vr_full[j % C::VR] : &v_full[j % VB], (j / nv) & 1u, j < t ? kTcWaitLimit : 1u << 8);
+            }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
         // ================= the products =================
+        // One thread of the first warp issues S = K Q, one of the second O += V P, so that
+        // neither waits for the other's operands.  A step of an operand in bytes
+        // is a sixteenth of it in its descriptor.
         if (lane == 0) {
-            const uint32_t id_qk = tc_idesc(FP8, false, false, rp), id_pv = tc_idesc(FP8, true, true, rp);
+            const bool second = warp > kMmaWarp;
             const uint32_t base = smem_addr(smem);
+            const uint32_t id = second ? tc_idesc(FP8, true, true, rp) : tc_idesc(FP8, false, false, rp);
+            const uint64_t a_d = second ? tc_desc(base + C::V_OFF, 16384, 1024) : tc_desc(base, 16, 1024);
+            const uint64_t b_d = second ? tc_desc(base + C::P_OFF, 16384, 1024) : tc_desc(base + C::Q_OFF, 16, 1024);
             bool ok = true;
-            unsigned g = 0, uc = 0;                            // tiles, units whose first product was issued
-            // operands at their first buffers; a step in bytes is a sixteenth of it here
-            const uint64_t k_d = tc_desc(base, 16, 1024), q_d = tc_desc(base + C::Q_OFF, 16, 1024);
-            const uint64_t v_d = tc_desc(base, 16384, 1024), p_d = tc_desc(base + C::P_OFF, 16384, 1024);
-            // own_copies: the threads' cp.asyncs, which arrived by themselves, unfenced
-            auto scores = [&](int qb, bool first, bool last, bool own_copies) { // S of tile g
-                if (first && !wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit)) return false;
-                const unsigned kb = 2 * g;
-                if (!wait_bounded(&full[kb % NBUF], (kb / NBUF) & 1u, limit)) return false;
-                if (g >= 2 && !wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit)) return false;
-                if (own_copies) proxy_fence();
-                tc_after();
-                const uint64_t kd = k_d + (kb % NBUF) * (kTcBuf / 16), qd = q_d + qb * (C::QBYTES / 16);
-                const uint32_t at = tmem + (g & 1) * RP;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc_mma(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id_qk, ks > 0);
-                tc_commit(&empty[kb % NBUF]);
-                tc_commit(&s_full[g & 1]);
-                if (last) tc_commit(&q_free[qb]);
-                return true;
-            };
-            auto sums = [&](unsigned t, bool first, bool own_copies) {          // O += V P of tile t
-                const unsigned vb = 2 * t + 1;
-                if (!wait_bounded(&full[vb % NBUF], (vb / NBUF) & 1u, limit)) return false;
-                if (!wait_bounded(&p_full, t & 1u, limit)) return false;
-                if (own_copies) proxy_fence();
-                tc_after();
-                const uint64_t vd = v_d + (vb % NBUF) * (kTcBuf / 16);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) tc_mma(tmem + 2 * RP, vd + ks * 128, p_d + ks * 128, id_pv, ks > 0 || !first);
-                tc_commit(&empty[vb % NBUF]);
-                tc_commit(&pv_done);
-                return true;
-            };
-            bool pend = false, pend_first = false, pend_copies = false;
+            unsigned g = 0, uc = 0;                            // tiles, units
             while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
-                for (int i = un.ta; i < un.tb && ok; ++i) {
-                    const bool copies = !FP8 && !(box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total));
-                    ok = scores((int)(uc % C::QB), i == un.ta, i + 1 == un.tb, copies);
-                    if (ok && pend) ok = sums(g - 1, pend_first, pend_copies);
-                    pend = true;
-                    pend_copies = copies;
-                    pend_first = i == un.ta;
-                    ++g;
+                const unsigned qb = uc % C::QB;
+                for (int i = un.ta; i < un.tb && ok; ++i, ++g) {
+                    // the threads' own cp.asyncs arrived by themselves, unfenced
+                    const bool fence = !FP8 && !(box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total));
+                    if (!second) {
+                        if (i == un.ta) ok = wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit);
+                        if (ok) ok = wait_bounded(&k_full[g % KB], (g / KB) & 1u, limit);
+                        if (ok && g >= 2) ok = wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit);
+                        if (!ok) break;
+                        if (fence) proxy_fence();
+                        tc_after();
+                        const uint64_t kd = a_d + (g % KB) * (kTcBuf / 16), qd = b_d + qb * (C::QBYTES / 16);
+                        const uint32_t at = tmem + (g & 1) * RP;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc_mma(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id, ks > 0);
+                        tc_commit(&s_full[g & 1]);
+                        tc_commit(&k_empty[g % KB]);
+                        if (i + 1 == un.tb) tc_commit(&q_free[qb]);
+                    } else {
+                        ok = wait_bounded(&v_full[g % VB], (g / VB) & 1u, limit);
+                        if (ok) ok = wait_bounded(&p_full, g & 1u, limit);
+                        if (!ok) break;
+                        if (fence) proxy_fence();
+                        tc_after();
+                        const uint64_t vd = a_d + (g % VB) * (kTcBuf / 16);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) tc_mma(tmem + 2 * RP, vd + ks * 128, b_d + ks * 128, id, ks > 0 || i > un.ta);
+                        tc_commit(&pv_done);
+                        tc_commit(&v_empty[g % VB]);
+                    }
                 }
                 ++uc;
             }
-            if (ok && pend) ok = sums(g - 1, pend_first, pend_copies);
             // every product must have ended before tensor memory is given back
-            tc_commit(&drained);
-            if (!wait_bounded(&drained, 0, kTcWaitLimit) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
+            tc_commit(&drained[second]);
+            if (!wait_bounded(&drained[second], 0, kTcWaitLimit) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -987,7 +1008,7 @@ static int tc_block_rows(int rt, int most) {
     const int blocks = (rt + most - 1) / most;
     return ((rt + blocks - 1) / blocks + 15) / 16 * 16;
 }
-constexpr int kTcMostBf16 = 144, kTcMostFp8 = 128;
+constexpr int kTcMostBf16 = 144, kTcMostFp8 = 64;
 
 bool attend_takes_tc(int N, int G, int D) { return D == kTcD; }
 
@@ -1065,7 +1086,8 @@ static cudaError_t launch_tc_e(const AttendArgs& a, cudaStream_t st) {
     if (rp <= 16) return launch_tc_t<1, 1, FP8>(a, br, rp, st);
     if (rp <= 32) return launch_tc_t<2, 1, FP8>(a, br, rp, st);
     if (rp <= 64) return launch_tc_t<4, 1, FP8>(a, br, rp, st);
-    return launch_tc_t<FP8 ? 4 : 3, FP8 ? 2 : 3, FP8>(a, br, rp, st);
+    if constexpr (!FP8) return launch_tc_t<3, 3, false>(a, br, rp, st);
+    return cudaErrorInvalidValue;                               // (blocks of an 8-bit cache are no larger)
 }
 
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st) {
