@@ -595,9 +595,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             // ---- the unit's CTAs: c0 begins it, c1 ends it; the last to arrive adds the parts
             const int c0 = share_of(plan.total, plan.n, un.at), c1 = share_of(plan.total, plan.n, un.at + tiles - 1);
             int* counter = counters + c0;                      // no CTA begins two units that others end
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                __threadfence();                               // the barrier put the CTA's writes before it
                 const int got = atomicAdd(counter, 1);
                 last_cta = got == c1 - c0;
                 if (last_cta) *counter = 0;                    // as the next call finds it

@@ -53,11 +53,16 @@ __device__ __forceinline__ int page_index(const AttendArgs& a, int pos, int* slo
     return pg;
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division takes some hundred
+// cycles, and these stand before a CTA's first load).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Share i of `total` tiles among n CTAs begins at tile i * total / n.
-__device__ __forceinline__ long long share_begin(long long total, long long n, long long i) { return i * total / n; }
+__device__ __forceinline__ long long share_begin(long long total, long long n, long long i) { return quotient(i * total, n); }
 // The CTA whose share holds tile t.
 __device__ __forceinline__ int share_of(long long total, long long n, long long t) {
-    return (int)(((t + 1) * n - 1) / total);
+    return (int)quotient((t + 1) * n - 1, total);
 }
 
 // Floats of one part of a split unit: rows sums of D, then the rows' references
@@ -154,7 +159,7 @@ struct AttWalk {
             x->b = b;
             x->sl = sl;
             x->tiles = tiles;
-            x->u = (int)((t - seq_at) / tiles);
+            x->u = (int)quotient(t - seq_at, tiles);
             x->at = seq_at + (long long)x->u * tiles;
             x->ta = (int)(t - x->at);
             x->tb = (int)min((long long)tiles, end - x->at);

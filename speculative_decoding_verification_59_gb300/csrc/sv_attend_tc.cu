@@ -136,6 +136,13 @@ __device__ __forceinline__ void tc_ld16_done(float* v) {
     asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
                  "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
+__device__ __forceinline__ void tc_ld4(uint32_t at, float (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(at));
+    tc_wait_ld();
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]));
+}
 __device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
     uint32_t r[16];
 #pragma unroll
@@ -198,6 +205,13 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
 // Byte offset of chunk c (16 bytes of 16) of row t in a tile of 128 rows of
 // 256 bytes kept as two blocks of 128-byte swizzled half rows.
 __device__ __forceinline__ int tc_off(int t, int c) { return (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4); }
+
+// A pair of bf16 values with infinities and NaN set to zero.
+__device__ __forceinline__ uint32_t drop_odd_bf16(uint32_t y) {
+    if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+    if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+    return y;
+}
 
 // Whether one of a word's four e4m3 values is no number.
 __device__ __forceinline__ bool has_odd_e4m3(uint32_t y) {
@@ -376,6 +390,32 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         };
         auto widen = [&](unsigned j) { widen_one(j, fl[j % (LAG + 1)], team == 1); };
         while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
+            // ---- the block table's entries, their loads under way beside the queries'
+            auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
+            auto table = [&](int pg) {                          // entry pg of the sequence's row; -1 past it
+                return pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
+            };
+            // What TMA tiles need of the block table is loaded for 32 boxes at once, a
+            // group before it is used: lane l holds box l of the group (a load of
+            // its own before each tile cost 1400 cycles a tile).
+            const int boxes = box > 0 ? kTcTile / box : 1;      // a tile's: 1, 2, .. 16
+            const int group = 32 / boxes;                       // tiles of a group
+            auto group_page = [&](int i0) {                     // group of tiles from i0 on
+                int slot;
+                const int pos = i0 * kTcTile + lane * box;
+                return box > 0 && pos + box <= min(un.sl.ctx, un.sl.total) ? table(page_index(a, pos, &slot)) : -1;
+            };
+            int g0 = un.ta, pages = group_page(g0), pages_next = group_page(g0 + group);
+            // The other tiles: lane l finds row l of the warp's 32, one tile ahead (E4M3: of
+            // every tile, for the scales).
+            auto row_page = [&](int i, int* slot) {
+                const int pos = i * kTcTile + lw * 32 + lane;
+                *slot = 0;
+                return pos < un.sl.total ? table(page_index(a, pos, slot)) : -2;      // -2: no position
+            };
+            auto by_row = [&](int i) { return i < un.tb && (!by_tma(i) || (FP8 && team == 0)); };
+            int rpage = -2, rslot = 0;
+            if (by_row(un.ta)) rpage = row_page(un.ta, &rslot);
             // ---- the unit's queries
             const int qb = (int)(uc % C::QB);
             if constexpr (FP8) {
@@ -441,30 +481,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             if (lane == 0) mbar_arrive(&q_full[qb]);
 
             // ---- the unit's tiles
-            auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
-            auto table = [&](int pg) {                          // entry pg of the sequence's row; -1 past it
-                return pg < a.c.max_pages ? __ldg(a.c.block_table + (size_t)un.b * a.c.max_pages + pg) : -1;
-            };
-            // What TMA tiles need of the block table is loaded for 32 boxes at once, a
-            // group before it is used: lane l holds box l of the group (a load of
-            // its own before each tile cost 1400 cycles a tile).
-            const int boxes = box > 0 ? kTcTile / box : 1;      // a tile's: 1, 2, .. 16
-            const int group = 32 / boxes;                       // tiles of a group
-            auto group_page = [&](int i0) {                     // group of tiles from i0 on
-                int slot;
-                const int pos = i0 * kTcTile + lane * box;
-                return box > 0 && pos + box <= min(un.sl.ctx, un.sl.total) ? table(page_index(a, pos, &slot)) : -1;
-            };
-            int g0 = un.ta, pages = group_page(g0), pages_next = group_page(g0 + group);
-            // The other tiles: lane l finds row l of the warp's 32.  E4M3: so do the
-            // scales of every tile, one tile ahead.
-            auto row_page = [&](int i, int* slot) {
-                const int pos = i * kTcTile + lw * 32 + lane;
-                *slot = 0;
-                return pos < un.sl.total ? table(page_index(a, pos, slot)) : -2;      // -2: no position
-            };
-            int spage = -2, sslot = 0;
-            if (FP8 && team == 0) spage = row_page(un.ta, &sslot);
             for (int i = un.ta; i < un.tb && ok; ++i) {
                 const bool tma = by_tma(i);
                 int at_page = 0, at_slot = 0;                   // TMA: the lane's box; else the lane's row
@@ -481,7 +497,8 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     lost = lane < boxes && !have;
                     if (!have) at_page = 0;                     // the unit ends as NaN anyway
                 } else {
-                    at_page = row_page(i, &at_slot);
+                    at_page = rpage;
+                    at_slot = rslot;
                     have = (unsigned)at_page < (unsigned)a.c.num_pages;
                     lost = !have && at_page != -2;
                 }
@@ -491,6 +508,10 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
                 }
                 const int64_t off = have && !tma ? entry_off(a.c, at_page, at_slot, un.hk) : 0;
+                const bool scaled = (unsigned)rpage < (unsigned)a.c.num_pages;
+                const int64_t so = FP8 && scaled ? scale_off(a.c, rpage, rslot, un.hk) : 0;
+                rpage = -2;
+                if (by_row(i + 1)) rpage = row_page(i + 1, &rslot);
                 const unsigned havem = __ballot_sync(0xffffffffu, have);
                 for (int kv = C::TEAMS == 2 ? team : 0; kv < (C::TEAMS == 2 ? team + 1 : 2); ++kv) {
                     // The buffer, once it is free.  Every warp waits for every buffer of its
@@ -534,30 +555,10 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     bool copies = !tma;                         // the threads have copies of their own in flight
                     if constexpr (FP8) {
                         if (kv == 0) {                          // both scales: the softmax wants them with the scores
-                            const bool in = (unsigned)spage < (unsigned)a.c.num_pages;
-                            const int64_t so = in ? scale_off(a.c, spage, sslot, un.hk) : 0;
                             const uint32_t at = smem_addr(smem + C::SCALE_OFF) + ((t % kTcScaleRing) * 2 * kTcTile + lw * 32 + lane) * 4;
-                            cp4(at, a.c.k_scale + so, in);
-                            cp4(at + kTcTile * 4, a.c.v_scale + so, in);
-                            spage = i + 1 < un.tb ? row_page(i + 1, &sslot) : -2;
+                            cp4(at, a.c.k_scale + so, scaled);
+                            cp4(at + kTcTile * 4, a.c.v_scale + so, scaled);
                             copies = true;
-                        }
-                    } else if (!tma && kv == 1 && i * kTcTile + kTcTile > un.sl.ctx) {
-                        // new positions: values that are no numbers are taken out (see the
-                        // epilogue), so these rows are waited for here
-                        cp_commit();
-                        cp_wait<0>();
-#pragma unroll
-                        for (int p = 0; p < PIECES; ++p) {
-                            const int row = lw * 32 + p * RPI + sub, pos = i * kTcTile + row;
-                            if (pos < un.sl.ctx || pos >= un.sl.total) continue;
-                            uint32_t* at = reinterpret_cast<uint32_t*>(smem + C::V_OFF + (t % VB) * kTcBuf + tc_off(row, ch));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t y = at[k];
-                                if ((y & 0x7f80u) == 0x7f80u) { y &= 0xffff0000u; odd_any = 1; at[k] = y; }
-                                if ((y & 0x7f800000u) == 0x7f800000u) { y &= 0xffffu; odd_any = 1; at[k] = y; }
-                            }
                         }
                     }
                     if (copies) cp_arrive(bar);                 // when this thread's copies have landed
@@ -792,7 +793,9 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     });
                     return top;
                 };
-                const float top = masked ? score_all(Yes{}) : score_all(No{});
+                // (up to 32 rows all tiles take the masked code: the few instructions it
+                // costs are not missed, those of a second copy would be)
+                const float top = C::KEEP || masked ? score_all(Yes{}) : score_all(No{});
                 const bool first = i == un.ta;
                 ok = ok && !late;
                 if (named_any(bar, 128, !ok || top > kRefSlack)) {
@@ -829,20 +832,17 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch)
                         if (ch < chunks) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) l[ch * 16 + j] *= alpha[c0 + ch * 16 + j];
                             if (!first) {
                                 float v[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) l[ch * 16 + j] *= alpha[c0 + ch * 16 + j];
                                 tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) v[j] *= alpha[c0 + ch * 16 + j];
                                 tc_st16(lanes + 2 * RP + c0 + ch * 16, v);
                             }
                         }
-                    if (C::KEEP) {
-                        if (masked) score_all(Yes{});
-                        else score_all(No{});
-                    }
+                    if constexpr (C::KEEP) score_all(Yes{});
                 }
                 // ---- probabilities; P is free once the tile before has been summed
                 if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
@@ -881,6 +881,30 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 } else {
                     if (masked) each(Yes{}, weigh);
                     else each(No{}, weigh);
+                }
+                if (!FP8 && masked && wg == 0) {
+                    // A new position's value that is no number, times a row's probability of
+                    // zero, would spoil the row's sum: such values are taken out of the tile
+                    // here, a position a thread, and given to the rows that see them at the
+                    // unit's end.  (E4M3: while widening.)
+                    late |= !wait_bounded(&v_full[g % VB], (g / VB) & 1u, limit);
+                    if (d >= 0 && !gone) {
+                        unsigned char* vb = smem + C::V_OFF + (g % VB) * kTcBuf;
+#pragma unroll 4
+                        for (int k = 0; k < 16; ++k) {
+                            uint4* at = reinterpret_cast<uint4*>(vb + tc_off(row, k));
+                            uint4 w = *at;
+                            const uint4 was = w;
+                            w.x = drop_odd_bf16(w.x);
+                            w.y = drop_odd_bf16(w.y);
+                            w.z = drop_odd_bf16(w.z);
+                            w.w = drop_odd_bf16(w.w);
+                            if (w.x != was.x || w.y != was.y || w.z != was.z || w.w != was.w) {
+                                odd_any = 1;
+                                *at = w;
+                            }
+                        }
+                    }
                 }
                 proxy_fence();
                 tc_before();
@@ -932,13 +956,12 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             }
             named_sync(bar, 128);
             if (row == 0) unit_bad[wg][uc % kTcUnitRing] = 0;
-            for (int ch = 0; ch * 16 < mine; ++ch) {
-                float v[16];
-                tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
+            // (a small loop: it runs once a unit, its instructions seldom at hand)
+#pragma unroll 1
+            for (int k0 = 0; k0 < mine; k0 += 4) {
+                float v[4];
+                tc_ld4(lanes + 2 * RP + c0 + k0, v);
                 if (odd_any) {
-                    // Rare: some new position's value was no number.  The loaders zeroed
-                    // it, so that it does not spoil the rows that mask it; those that
-                    // see it get it here.
                     const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
                     for (int j = j0; j < j1; ++j) {
                         int page, slot;
@@ -954,22 +977,22 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (fabsf(x) < CUDART_INF_F) continue;
                         const int d = j - sl.ctx;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int n = rown[c0 + ch * 16 + k];
+                        for (int k = 0; k < 4; ++k) {
+                            const int n = rown[c0 + k0 + k];
                             if (a.par ? (anc[wg][0][n] >> (d & 63)) & 1ull : d <= n) v[k] += x;
                         }
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int r = c0 + ch * 16 + j;
-                    if (ch * 16 + j < mine) {
+                for (int k = 0; k < 4; ++k) {
+                    const int r = c0 + k0 + k;
+                    if (k0 + k < mine) {
                         if (whole) {
-                            const float y = rown[r] >= sl.nb && !bad ? 0.f : v[j] * alpha[r];
+                            const float y = rown[r] >= sl.nb && !bad ? 0.f : v[k] * alpha[r];
                             reinterpret_cast<unsigned short*>(a.out)[((size_t)un.b * a.N * a.Hq + rowat[r]) * kTcD + row] =
                                 (unsigned short)(pack_bf16(y, 0.f) & 0xffffu);
                         } else {
-                            __stcg(sp + (size_t)r * kTcD + row, v[j]);
+                            __stcg(sp + (size_t)r * kTcD + row, v[k]);
                         }
                     }
                 }
@@ -980,9 +1003,9 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 // its rows' parts
                 const int f0 = share_of(plan.total, plan.n, un.at), f1 = share_of(plan.total, plan.n, un.at + un.tiles - 1);
                 int* counter = counters + NSM * f0 + wg;         // no CTA begins two units that others end
-                __threadfence();
                 named_sync(bar, 128);
                 if (row == 0) {
+                    __threadfence();                           // the barrier put the warpgroup's writes before it
                     const int got = atomicAdd(counter, 1);
                     last_cta[wg] = got == f1 - f0;
                     if (last_cta[wg]) *counter = 0;            // as the next call finds it
