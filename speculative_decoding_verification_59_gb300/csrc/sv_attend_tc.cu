@@ -16,14 +16,18 @@
 // The warps of a CTA, one CTA per SM, each walking the CTA's share:
 //   softmax   4 warps (8 or 12 from 65 rows on, each 4 with their share of the rows)
 //   MMA       2 threads: one issues the first product, one the second
-//   loaders   4 warps bring the queries, and keys and values into a ring of 32 KB
-//             buffers each.  A tile of old positions whose pages fit it (page sizes
-//             that divide 128, from 8 on, or are multiples of it) comes by TMA, a box
-//             per page; other page sizes, and the tiles with new positions, where
-//             stale entries are left out, by the threads' 16-byte cp.async.  The
-//             rows of an E4M3 cache go to rings of their own first and are widened
-//             to fp16 by the loaders, then 8 warps in two teams, one for the keys and
-//             one for the values.
+//   loaders   4 warps bring the queries, and keys and values into a ring of buffers
+//             each.  A tile of old positions whose pages fit it (page sizes that divide
+//             128, from 8 on, or are multiples of it) comes by TMA, a box per page;
+//             other page sizes, and the tiles with new positions, where stale
+//             entries are left out, by the threads' 16-byte cp.async.
+// An E4M3 cache is multiplied as it lies (kind::f8f6f4), the other operand split
+// into e4m3 terms, each the rounding of sixteen times what the one before left
+// over: two for a query (a bf16 significand has two e4m3 significands' bits), three
+// for a probability (12 bits, as fp16 would have).  The terms are columns of their
+// own: S has two columns a row, O three, weighed 1, 1/16, 1/256 when they are
+// read.  (Widening the cache to fp16 in shared memory instead moved three times the
+// bytes there and bound the kernel: 183 us for 8 x 32768 positions.)
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
 //
@@ -41,10 +45,8 @@ namespace sv {
 
 constexpr int kTcTile = 128;
 constexpr int kTcD = 128;
-constexpr int kTcBuf = kTcTile * kTcD * 2;       // a tile's keys or values as the products read them: 32 KB
-constexpr int kTcRaw = kTcTile * kTcD;           // the same as the cache's 8-bit rows: 16 KB
-// The loaders run at most 6 tiles ahead of the softmax (raw and widened buffers,
-// two score buffers): scales are held for 7 tiles, what the loaders tell the
+// The loaders run at most 6 tiles ahead of the softmax (key buffers and two
+// score buffers): scales are held for 7 tiles, what the loaders tell the
 // softmax by unit for 8.
 constexpr int kTcScaleRing = 7;
 constexpr int kTcUnitRing = 8;
@@ -63,29 +65,32 @@ template <int CH, int NSM, bool FP8>
 struct TcCfg {
     static constexpr int COLS = CH * 16;         // rows of a softmax warpgroup
     static constexpr int RP = NSM * COLS;        // rows of a unit, at most
-    static constexpr int PB = (RP + 63) / 64;    // 64-row blocks of P
-    static constexpr int QB = RP <= 32 && !FP8 ? 2 : 1;        // units whose queries are held
-    static constexpr int KB = FP8 && RP > 32 ? 1 : 2;            // buffers of keys, of values
-    static constexpr int VB = FP8 || RP > 64 ? 2 : 3;
-    static constexpr int TEAMS = FP8 ? 2 : 1;
-    static constexpr int KR = FP8 ? 2 : 1, VR = FP8 ? 2 : 1;     // raw buffers (a bf16 cache has none)
+    static constexpr int BUF = kTcTile * kTcD * (FP8 ? 1 : 2);   // a tile's keys or values
+    static constexpr int QT = FP8 ? 2 : 1, PT = FP8 ? 3 : 1;     // terms of a query, of a probability
+    static constexpr int PROWS = FP8 ? 128 : 64; // columns of P in 128 bytes
+    static constexpr int PB = (PT * RP + PROWS - 1) / PROWS;     // blocks of them
+    static constexpr int QB = RP <= 64 ? 2 : 1;  // units whose queries are held
+    static constexpr int KB = FP8 ? 4 : 2;       // buffers of keys, of values
+    static constexpr int VB = FP8 ? (RP > 32 ? 4 : 5) : RP > 64 ? 2 : 3;
+    static constexpr int S_COLS = QT * RP;       // columns of tensor memory: scores, sums
+    static constexpr int O_AT = 2 * S_COLS, T_COLS = O_AT + PT * RP;
     static constexpr int WORDS = (COLS + 31) / 32;   // a bit for each row of a warpgroup
     // Up to 32 rows the scores stay in registers between the vote and the
     // probabilities, beside as many running totals; beyond, they are read from
     // tensor memory twice.
     static constexpr bool KEEP = CH <= 2;
     static constexpr int SM_THREADS = NSM * 128;
-    static constexpr int LOADERS = 128 * TEAMS;
+    static constexpr int LOADERS = 128;
     static constexpr int THREADS = SM_THREADS + 64 + LOADERS;
-    static constexpr int V_OFF = KB * kTcBuf;
-    static constexpr int P_OFF = V_OFF + VB * kTcBuf;
+    static constexpr int V_OFF = KB * BUF;
+    static constexpr int P_OFF = V_OFF + VB * BUF;
     static constexpr int Q_OFF = P_OFF + PB * 16384;
-    static constexpr int QBYTES = RP * 256;
-    static constexpr int RAW_OFF = Q_OFF + QB * QBYTES;
-    static constexpr int SCALE_OFF = RAW_OFF + (FP8 ? (KR + VR) * kTcRaw : 0);
+    static constexpr int QBYTES = RP * 256;      // bf16: two blocks of half rows; E4M3: two terms
+    static constexpr int SCALE_OFF = Q_OFF + QB * QBYTES;
     static constexpr int SMEM = SCALE_OFF + (FP8 ? kTcScaleRing * 2 * kTcTile * 4 : 0) + 1024;   // and room to align
     static_assert(SMEM <= 227 * 1024, "dynamic shared memory");
-    static constexpr int TMEM = 3 * RP <= 64 ? 64 : 3 * RP <= 128 ? 128 : 3 * RP <= 256 ? 256 : 512;
+    static_assert(T_COLS <= 512, "tensor memory");
+    static constexpr int TMEM = T_COLS <= 64 ? 64 : T_COLS <= 128 ? 128 : T_COLS <= 256 ? 256 : 512;
 };
 
 // ---- tcgen05 in inline PTX ------------------------------------------------------
@@ -96,12 +101,20 @@ __device__ __forceinline__ void tc_alloc(uint32_t* dst, uint32_t cols) {
 __device__ __forceinline__ void tc_dealloc(uint32_t at, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
 }
+template <bool F8>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
 }
 // Arrives on the barrier when every tcgen05.mma issued so far has completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -171,15 +184,15 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 
 // Shared-memory operand with 128-byte swizzled rows.  K-major (the contraction
 // contiguous): sbo is the step between groups of 8 rows.  MN-major: lbo the step
-// between blocks of 64 elements of the other dimension, sbo between groups of 8
+// between blocks of 128 bytes of the other dimension, sbo between groups of 8
 // steps of the contraction.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
-// Instruction descriptor: fp32 accumulators, both operands bf16 (or fp16),
+// Instruction descriptor: fp32 accumulators, both operands bf16 (or e4m3),
 // M = 128, N = n; ta / tb: that operand is MN-major.
-__device__ __forceinline__ uint32_t tc_idesc(bool f16, bool ta, bool tb, int n) {
-    const uint32_t t = f16 ? 0u : 1u;
+__device__ __forceinline__ uint32_t tc_idesc(bool e4m3, bool ta, bool tb, int n) {
+    const uint32_t t = e4m3 ? 0u : 1u;
     return 1u << 4 | t << 7 | t << 10 | (uint32_t)ta << 15 | (uint32_t)tb << 16 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
@@ -202,8 +215,8 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Byte offset of chunk c (16 bytes of 16) of row t in a tile of 128 rows of
-// 256 bytes kept as two blocks of 128-byte swizzled half rows.
+// Byte offset of 16-byte chunk c of row t in a tile of 128 rows, kept as blocks
+// of 128-byte swizzled (half) rows.
 __device__ __forceinline__ int tc_off(int t, int c) { return (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4); }
 
 // A pair of bf16 values with infinities and NaN set to zero.
@@ -213,12 +226,23 @@ __device__ __forceinline__ uint32_t drop_odd_bf16(uint32_t y) {
     return y;
 }
 
-// Whether one of a word's four e4m3 values is no number.
-__device__ __forceinline__ bool has_odd_e4m3(uint32_t y) {
-    bool x = false;
+// Four e4m3 values with NaN set to zero.
+__device__ __forceinline__ uint32_t drop_odd_e4m3(uint32_t y) {
 #pragma unroll
-    for (int q = 0; q < 32; q += 8) x |= ((y >> q) & 0x7fu) == 0x7fu;
-    return x;
+    for (int s = 0; s < 32; s += 8)
+        if (((y >> s) & 0x7fu) == 0x7fu) y &= ~(0xffu << s);
+    return y;
+}
+
+// The e4m3 rounding of a pair, which is replaced by sixteen times what that
+// leaves over.
+__device__ __forceinline__ uint32_t e4m3_term(float& a, float& b) {
+    const uint32_t t = pack_e4m3(a, b);
+    float x, y;
+    f16x2_to_f32(e4m3_to_f16x2(t), &x, &y);
+    a = (a - x) * 16.f;
+    b = (b - y) * 16.f;
+    return t;
 }
 
 struct Max {
@@ -254,7 +278,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ AttPlan plan;
     __shared__ __align__(8) uint64_t k_full[KB], k_empty[KB], v_full[VB], v_empty[VB], s_full[2], s_free[2], p_full, pv_done,
         q_full[C::QB], q_free[C::QB], drained[2];
-    __shared__ __align__(8) uint64_t kr_full[C::KR], kr_empty[C::KR], vr_full[C::VR], vr_empty[C::VR];
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
@@ -264,32 +287,20 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ uint32_t vis[NSM][kMaxNewTree][C::WORDS];       // trees: the warpgroup's rows that see a node
     __shared__ uint32_t tmem_at;
     __shared__ int unit_bad[NSM][kTcUnitRing];                  // a page that is none
-    __shared__ float unit_qinv[kTcUnitRing];                    // E4M3: what takes back the queries' scaling
+    __shared__ __align__(16) float qinv[4][FP8 ? RP : 4];       // E4M3: by unit, what takes back a row's scaling
     __shared__ int odd_any, last_cta[NSM], tree_bad[NSM];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kMmaWarp = C::SM_THREADS / 32;
 
     if (tid == 0) {
-        // operands: every thread of the loaders that copies arrives, or a lane of each
-        // of the four warps that widen
         for (int i = 0; i < KB; ++i) {
-            mbar_init(&k_full[i], FP8 ? 4 : 128);
+            mbar_init(&k_full[i], 128);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < VB; ++i) {
-            mbar_init(&v_full[i], FP8 ? 4 : 128);
+            mbar_init(&v_full[i], 128);
             mbar_init(&v_empty[i], 1);
-        }
-        if constexpr (FP8) {
-            for (int i = 0; i < C::KR; ++i) {
-                mbar_init(&kr_full[i], 128);
-                mbar_init(&kr_empty[i], 4);
-            }
-            for (int i = 0; i < C::VR; ++i) {
-                mbar_init(&vr_full[i], 128);
-                mbar_init(&vr_empty[i], 4);
-            }
         }
         mbar_init(&drained[0], 1);
         mbar_init(&drained[1], 1);
@@ -328,7 +339,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     if (warp > kMmaWarp + 1) {
         // ================= loaders =================
         const int lt = tid - C::SM_THREADS - 64, lw = (lt >> 5) & 3;
-        const int team = C::TEAMS == 2 ? lt >> 7 : 0;          // two teams: 0 keys, 1 values
         constexpr int CPR = FP8 ? 8 : 16;                      // 16-byte chunks of a cached row
         constexpr int RPI = 32 / CPR;                          // rows a warp copies at once
         constexpr int PIECES = 32 / RPI;                       // a warp's 32 rows: pieces of 16 bytes a thread
@@ -336,59 +346,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         bool ok = true;
         unsigned t = 0;                                        // tiles issued
         unsigned uc = 0;                                       // units
-        unsigned done = 0;                                     // E4M3: tiles widened
-        unsigned ends[C::QB];                                  // by query buffer: t after the unit that had it
-        struct Flight {                                        // what widening a tile needs
-            int p0, ctx, total;
-        };
-        constexpr int LAG = FP8 ? C::KR - 1 : 0;               // raw tiles in flight behind the one being issued
-        static_assert(!FP8 || C::KR == C::VR, "one lag for both");
-        Flight fl[LAG + 1] = {};
-        auto widen_one = [&](unsigned j, const Flight& f, bool val) {      // E4M3: a raw tile to the products' form
-            uint64_t* rf = val ? &vr_full[j % C::VR] : &kr_full[j % C::KR];
-            uint64_t* em = val ? &v_empty[j % VB] : &k_empty[j % KB];
-            const unsigned n = val ? VB : KB, nr = val ? C::VR : C::KR;
-            if (ok) ok = wait_bounded(rf, (j / nr) & 1u, limit);
-            if (ok && j >= n) ok = wait_bounded(em, (j / n - 1) & 1u, limit);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
-            unsigned char* dst = smem + (val ? C::V_OFF + (j % VB) * kTcBuf : (j % KB) * kTcBuf);
-            const unsigned char* raw = smem + C::RAW_OFF + (val ? C::KR + j % C::VR : j % C::KR) * kTcRaw;
-            const bool fresh = val && f.p0 + kTcTile > f.ctx;                  // values, new positions among them
-#pragma unroll
-            for (int p = 0; p < PIECES; ++p) {
-                const int row = lw * 32 + p * RPI + sub;
-                uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ch * 16);
-                if (fresh && f.p0 + row >= f.ctx && f.p0 + row < f.total &&
-                    (has_odd_e4m3(w.x) || has_odd_e4m3(w.y) || has_odd_e4m3(w.z) || has_odd_e4m3(w.w))) {
-                    odd_any = 1;                               // rare: see the epilogue
-                    uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int s = 0; s < 32; s += 8)
-                            if (((y[i] >> s) & 0x7fu) == 0x7fu) y[i] &= ~(0xffu << s);
-                    w = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-                uint4 lo, hi;
-                lo.x = e4m3_to_f16x2(w.x & 0xffffu);
-                lo.y = e4m3_to_f16x2(w.x >> 16);
-                lo.z = e4m3_to_f16x2(w.y & 0xffffu);
-                lo.w = e4m3_to_f16x2(w.y >> 16);
-                hi.x = e4m3_to_f16x2(w.z & 0xffffu);
-                hi.y = e4m3_to_f16x2(w.z >> 16);
-                hi.z = e4m3_to_f16x2(w.w & 0xffffu);
-                hi.w = e4m3_to_f16x2(w.w >> 16);
-                *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch)) = lo;
-                *reinterpret_cast<uint4*>(dst + tc_off(row, 2 * ch + 1)) = hi;
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(val ? &vr_empty[j % C::VR] : &kr_empty[j % C::KR]);
-                mbar_arrive(val ? &v_full[j % VB] : &k_full[j % KB]);
-            }
-        };
-        auto widen = [&](unsigned j) { widen_one(j, fl[j % (LAG + 1)], team == 1); };
         while (ok && walk.next<kTcTile>(a, RB, block_rows, &un)) {
             // ---- the block table's entries, their loads under way beside the queries'
             auto by_tma = [&](int i) { return box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total); };
@@ -413,49 +370,18 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 *slot = 0;
                 return pos < un.sl.total ? table(page_index(a, pos, slot)) : -2;      // -2: no position
             };
-            auto by_row = [&](int i) { return i < un.tb && (!by_tma(i) || (FP8 && team == 0)); };
+            auto by_row = [&](int i) { return i < un.tb && (!by_tma(i) || FP8); };
             int rpage = -2, rslot = 0;
             if (by_row(un.ta)) rpage = row_page(un.ta, &rslot);
             // ---- the unit's queries
             const int qb = (int)(uc % C::QB);
-            if constexpr (FP8) {
-                // what frees them is the last product of the unit that had them, whose keys
-                // may still be raw
-                for (; uc >= (unsigned)C::QB && done < ends[qb] && ok; ++done) widen(done);
-            }
             if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             unsigned char* qs = smem + C::Q_OFF + qb * C::QBYTES;
-            float qscale = 1.f;
             auto query_row = [&](int r) {
                 const int R = un.r0 + r, n = row_position(a, R), g = R - n * a.G;
                 return a.q + ((int64_t)un.b * a.N + n) * a.qs + ((size_t)un.hk * a.G + g) * kTcD * 2;
             };
-            if constexpr (FP8) {
-                // fp16 queries, scaled by one power of two so that the unit's largest
-                // element is in [2^12, 2^13): exact down to 2^-26 of it.  Every warp
-                // finds the maximum by itself.
-                float mx = 0.f;
-                for (int i0 = lane; i0 < un.rows * 16; i0 += 32 * 8) {
-                    uint4 w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int i = i0 + 32 * k;
-                        w[k] = i < un.rows * 16 ? __ldg(reinterpret_cast<const uint4*>(query_row(i >> 4)) + (i & 15)) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float x[8];
-                        unpack8(w[k], x);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]) < CUDART_INF_F ? fabsf(x[j]) : 0.f);
-                    }
-                }
-                mx = warp_max(mx);
-                const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 139 - ex;
-                qscale = __uint_as_float((uint32_t)(127 + sh) << 23);
-                if (lt == 0) unit_qinv[uc % kTcUnitRing] = __uint_as_float((uint32_t)(127 - sh) << 23);
-            }
             constexpr int QK = 6;                              // loads of a thread in flight
             for (int i0 = lt; i0 < rp * 16; i0 += C::LOADERS * QK) {
                 uint4 w[QK];
@@ -467,13 +393,41 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll
                 for (int k = 0; k < QK; ++k) {
                     const int i = i0 + C::LOADERS * k, r = i >> 4, c16 = i & 15;
-                    if constexpr (FP8) {
-                        float x[8];
+                    if constexpr (!FP8) {
+                        if (r < rp) *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w[k];
+                    } else {
+                        // the row's 16 lanes find the power of two that brings its largest
+                        // element into [2^7, 2^8), and write its two terms
+                        float x[8], mx = 0.f;
                         unpack8(w[k], x);
-                        w[k] = make_uint4(pack_f16(x[0] * qscale, x[1] * qscale), pack_f16(x[2] * qscale, x[3] * qscale),
-                                          pack_f16(x[4] * qscale, x[5] * qscale), pack_f16(x[6] * qscale, x[7] * qscale));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (!(fabsf(x[j]) < CUDART_INF_F)) x[j] = CUDART_NAN_F;        // (e4m3 has no infinity)
+                            else mx = fmaxf(mx, fabsf(x[j]));
+                        }
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 134 - ex;
+                        const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] *= f;
+                        uint2 term[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            term[q].x = e4m3_term(x[0], x[1]);
+                            term[q].x |= e4m3_term(x[2], x[3]) << 16;
+                            term[q].y = e4m3_term(x[4], x[5]);
+                            term[q].y |= e4m3_term(x[6], x[7]) << 16;
+                        }
+                        if (r < rp) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int at = q * rp + r;
+                                *reinterpret_cast<uint2*>(qs + at * 128 + (((c16 >> 1) ^ (at & 7)) << 4) + (c16 & 1) * 8) = term[q];
+                            }
+                            if (c16 == 0) qinv[uc & 3][r] = __uint_as_float((uint32_t)(127 - sh) << 23);
+                        }
                     }
-                    if (r < rp) *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w[k];
                 }
             }
             proxy_fence();
@@ -513,28 +467,19 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 rpage = -2;
                 if (by_row(i + 1)) rpage = row_page(i + 1, &rslot);
                 const unsigned havem = __ballot_sync(0xffffffffu, have);
-                for (int kv = C::TEAMS == 2 ? team : 0; kv < (C::TEAMS == 2 ? team + 1 : 2); ++kv) {
+                for (int kv = 0; kv < 2; ++kv) {
                     // The buffer, once it is free.  Every warp waits for every buffer of its
                     // kind and arrives for it, the ones that have no part in a TMA tile too: a
                     // barrier tells its last two phases apart, no more, so none may
                     // fall behind or run ahead.
-                    uint32_t dst;
-                    uint64_t* bar;
-                    if constexpr (FP8) {
-                        constexpr int n = C::KR;
-                        if (lane == 0 && t >= (unsigned)n) ok = wait_bounded(kv ? &vr_empty[t % n] : &kr_empty[t % n], (t / n - 1) & 1u, limit);
-                        dst = smem_addr(smem + C::RAW_OFF + (kv ? n + t % n : t % n) * kTcRaw);
-                        bar = kv ? &vr_full[t % n] : &kr_full[t % n];
-                    } else {
-                        const unsigned n = kv ? VB : KB;
-                        if (lane == 0 && t >= n) ok = wait_bounded(kv ? &v_empty[t % VB] : &k_empty[t % KB], (t / n - 1) & 1u, limit);
-                        dst = smem_addr(smem + (kv ? C::V_OFF + (t % VB) * kTcBuf : (t % KB) * kTcBuf));
-                        bar = kv ? &v_full[t % VB] : &k_full[t % KB];
-                    }
+                    const unsigned n = kv ? VB : KB;
+                    if (lane == 0 && t >= n) ok = wait_bounded(kv ? &v_empty[t % VB] : &k_empty[t % KB], (t / n - 1) & 1u, limit);
+                    const uint32_t dst = smem_addr(smem + (kv ? C::V_OFF + (t % VB) * C::BUF : (t % KB) * C::BUF));
+                    uint64_t* bar = kv ? &v_full[t % VB] : &k_full[t % KB];
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     if (tma) {
-                        if (lw == (C::TEAMS == 2 ? 0 : kv)) {   // one warp issues the keys, one the values
-                            if (lane == 0) mbar_expect(bar, FP8 ? kTcRaw : kTcBuf);
+                        if (lw == kv) {                         // one warp issues the keys, one the values
+                            if (lane == 0) mbar_expect(bar, C::BUF);
                             __syncwarp();
                             if (lane < boxes) {
                                 const CUtensorMap* map = kv ? &vmap : &kmap;
@@ -549,7 +494,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         for (int p = 0; p < PIECES; ++p) {
                             const int wr = p * RPI + sub, row = lw * 32 + wr;
                             const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
-                            cp16(dst + (FP8 ? row * 128 + ch * 16 : tc_off(row, ch)), base + e, (havem >> wr) & 1u);
+                            cp16(dst + tc_off(row, ch), base + e, (havem >> wr) & 1u);
                         }
                     }
                     bool copies = !tma;                         // the threads have copies of their own in flight
@@ -565,31 +510,20 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     else if (lane == 0) mbar_arrive_n(bar, 32);
                 }
                 if (!ok) break;
-                if constexpr (FP8) {
-                    fl[t % (LAG + 1)] = Flight{i * kTcTile, un.sl.ctx, un.sl.total};
-                    if (t - done >= (unsigned)LAG) {
-                        widen(done);
-                        ++done;
-                    }
-                }
                 ++t;
             }
-            ends[qb] = t;
             ++uc;
         }
         // ---- the tiles still in flight
         cp_wait<0>();
-        if constexpr (FP8)
-            for (; done < t && ok; ++done) widen(done);
         if (!ok) {
             // a wait ran out: do not leave while a box may still be on its way
             raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
             if (lt == 0) {
-                const unsigned nk = FP8 ? C::KR : KB, nv = FP8 ? C::VR : VB;
-                for (unsigned j = t > nk ? t - nk : 0u; j <= t; ++j)
-                    wait_bounded(FP8 ? &kr_full[j % C::KR] : &k_full[j % KB], (j / nk) & 1u, j < t ? kTcWaitLimit : 1u << 8);
-                for (unsigned j = t > nv ? t - nv : 0u; j <= t; ++j)
-                    wait_bounded(FP8 ? &vr_full[j % C::VR] : &v_full[j % VB], (j / nv) & 1u, j < t ? kTcWaitLimit : 1u << 8);
+                for (unsigned j = t > KB ? t - KB : 0u; j <= t; ++j)
+                    wait_bounded(&k_full[j % KB], (j / KB) & 1u, j < t ? kTcWaitLimit : 1u << 8);
+                for (unsigned j = t > VB ? t - VB : 0u; j <= t; ++j)
+                    wait_bounded(&v_full[j % VB], (j / VB) & 1u, j < t ? kTcWaitLimit : 1u << 8);
             }
         }
     } else if (warp >= kMmaWarp) {
@@ -600,7 +534,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         if (lane == 0) {
             const bool second = warp > kMmaWarp;
             const uint32_t base = smem_addr(smem);
-            const uint32_t id = second ? tc_idesc(FP8, true, true, rp) : tc_idesc(FP8, false, false, rp);
+            const uint32_t id = second ? tc_idesc(FP8, true, true, C::PT * rp) : tc_idesc(FP8, false, false, C::QT * rp);
             const uint64_t a_d = second ? tc_desc(base + C::V_OFF, 16384, 1024) : tc_desc(base, 16, 1024);
             const uint64_t b_d = second ? tc_desc(base + C::P_OFF, 16384, 1024) : tc_desc(base + C::Q_OFF, 16, 1024);
             bool ok = true;
@@ -609,7 +543,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 const unsigned qb = uc % C::QB;
                 for (int i = un.ta; i < un.tb && ok; ++i, ++g) {
                     // the threads' own cp.asyncs arrived by themselves, unfenced
-                    const bool fence = !FP8 && !(box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total));
+                    const bool fence = !(box > 0 && (i + 1) * kTcTile <= min(un.sl.ctx, un.sl.total));
                     if (!second) {
                         if (i == un.ta) ok = wait_bounded(&q_full[qb], (uc / C::QB) & 1u, limit);
                         if (ok) ok = wait_bounded(&k_full[g % KB], (g / KB) & 1u, limit);
@@ -617,11 +551,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (!ok) break;
                         if (fence) proxy_fence();
                         tc_after();
-                        const uint64_t kd = a_d + (g % KB) * (kTcBuf / 16), qd = b_d + qb * (C::QBYTES / 16);
-                        const uint32_t at = tmem + (g & 1) * RP;
+                        const uint64_t kd = a_d + (g % KB) * (C::BUF / 16), qd = b_d + qb * (C::QBYTES / 16);
+                        const uint32_t at = tmem + (g & 1) * C::S_COLS;
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id, ks > 0);
+                        for (int ks = 0; ks < C::BUF / 4096; ++ks)              // 32 bytes of a row at a time
+                            tc_mma<FP8>(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id, ks > 0);
                         tc_commit(&s_full[g & 1]);
                         tc_commit(&k_empty[g % KB]);
                         if (i + 1 == un.tb) tc_commit(&q_free[qb]);
@@ -631,9 +565,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (!ok) break;
                         if (fence) proxy_fence();
                         tc_after();
-                        const uint64_t vd = a_d + (g % VB) * (kTcBuf / 16);
+                        const uint64_t vd = a_d + (g % VB) * (C::BUF / 16);
+                        constexpr int STEP = FP8 ? 256 : 128;   // 32 (16) positions
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) tc_mma(tmem + 2 * RP, vd + ks * 128, b_d + ks * 128, id, ks > 0 || i > un.ta);
+                        for (int ks = 0; ks < 1024 / STEP; ++ks)
+                            tc_mma<FP8>(tmem + C::O_AT, vd + ks * STEP, b_d + ks * STEP, id, ks > 0 || i > un.ta);
                         tc_commit(&pv_done);
                         tc_commit(&v_empty[g % VB]);
                     }
@@ -735,7 +671,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 float f = c2, add = 0.f, vinv = 0.f;
                 if constexpr (FP8) {
                     const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + (g % kTcScaleRing) * 2 * kTcTile;
-                    f = c2 * unit_qinv[uc % kTcUnitRing] * sc[row];
+                    f = c2 * sc[row];
                     add = __log2f(sc[kTcTile + row]);
                     vinv = 1.f / sc[kTcTile + row];
                 }
@@ -747,20 +683,31 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     if constexpr (decltype(mask)::value) return (sees[k >> 5] >> (k & 31)) & 1u ? x : kNegInf;
                     else return x;
                 };
-                const uint32_t s_at = lanes + (g & 1) * RP + c0;
-                // Reads the scores two chunks at a time, takes them relative to the references
+                const uint32_t s_at = lanes + (g & 1) * C::S_COLS + c0;
+                const float* qf = qinv[uc & 3];
+                // Reads the scores two chunks (E4M3: a chunk's two terms) at a time, takes them relative to the references
                 // and gives them to `use(first row, 16 values)`.
                 auto each = [&](auto mask, auto use) {
 #pragma unroll
-                    for (int c2_ = 0; c2_ < CH; c2_ += 2) {
+                    for (int c2_ = 0; c2_ < CH; c2_ += FP8 ? 1 : 2) {
                         if (c2_ < chunks) {
                         float v[2][16];
-                        const bool two = c2_ + 1 < CH;         // (a second chunk past the unit's rows is read and left)
+                        const bool two = !FP8 && c2_ + 1 < CH; // (a second chunk past the unit's rows is read and left)
                         tc_ld16_start(s_at + c2_ * 16, v[0]);
-                        if (two) tc_ld16_start(s_at + c2_ * 16 + 16, v[1]);
+                        if (two || FP8) tc_ld16_start(s_at + (FP8 ? rp + c2_ * 16 : c2_ * 16 + 16), v[1]);
                         tc_wait_ld();
                         tc_ld16_done(v[0]);
-                        if (two) tc_ld16_done(v[1]);
+                        if (two || FP8) tc_ld16_done(v[1]);
+                        if constexpr (FP8) {                   // the two terms, and the row's scaling
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 q = *reinterpret_cast<const float4*>(&qf[c0 + c2_ * 16 + j]);
+                                v[0][j] = fmaf(v[1][j], 0.0625f, v[0][j]) * q.x;
+                                v[0][j + 1] = fmaf(v[1][j + 1], 0.0625f, v[0][j + 1]) * q.y;
+                                v[0][j + 2] = fmaf(v[1][j + 2], 0.0625f, v[0][j + 2]) * q.z;
+                                v[0][j + 3] = fmaf(v[1][j + 3], 0.0625f, v[0][j + 3]) * q.w;
+                            }
+                        }
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             if (h == 0 || (two && c2_ + 1 < chunks)) {
@@ -809,6 +756,12 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     for (int ch = 0; ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
                         float v[16];
                         tc_ld16(s_at + ch * 16, v);
+                        if constexpr (FP8) {
+                            float u[16];
+                            tc_ld16(s_at + rp + ch * 16, u);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = fmaf(u[j], 0.0625f, v[j]) * qf[c0 + ch * 16 + j];
+                        }
                         uint32_t bits = sees[0];
 #pragma unroll
                         for (int w = 1; w < C::WORDS; ++w)
@@ -833,13 +786,17 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     for (int ch = 0; ch < CH; ++ch)
                         if (ch < chunks) {
                             if (!first) {
-                                float v[16];
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) l[ch * 16 + j] *= alpha[c0 + ch * 16 + j];
-                                tc_ld16(lanes + 2 * RP + c0 + ch * 16, v);
+#pragma unroll 1
+                                for (int q = 0; q < C::PT; ++q) {
+                                    float v[16];
+                                    const uint32_t at = lanes + C::O_AT + q * rp + c0 + ch * 16;
+                                    tc_ld16(at, v);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) v[j] *= alpha[c0 + ch * 16 + j];
-                                tc_st16(lanes + 2 * RP + c0 + ch * 16, v);
+                                    for (int j = 0; j < 16; ++j) v[j] *= alpha[c0 + ch * 16 + j];
+                                    tc_st16(at, v);
+                                }
                             }
                         }
                     if constexpr (C::KEEP) score_all(Yes{});
@@ -849,25 +806,41 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 late = !ok;
                 unsigned char* prow = smem + C::P_OFF + row * 128;
                 auto weigh = [&](int k0, const float (&v)[16]) {
-                    uint32_t w[8];
+                    if constexpr (FP8) {
+                        uint32_t w[3][4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
-                        if constexpr (FP8) {                   // a masked scale may be anything
-                            l[k0 + j] += y != 0.f ? y * vinv : 0.f;
+                        for (int j = 0; j < 16; j += 2) {
+                            float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
+                            l[k0 + j] += y != 0.f ? y * vinv : 0.f;            // a masked scale may be anything
                             l[k0 + j + 1] += z != 0.f ? z * vinv : 0.f;
-                            w[j >> 1] = pack_f16(y, z);
-                        } else {
+#pragma unroll
+                            for (int q = 0; q < 3; ++q) {
+                                const uint32_t t = q < 2 ? e4m3_term(y, z) : pack_e4m3(y, z);
+                                if (j & 2) w[q][j >> 2] |= t << 16;
+                                else w[q][j >> 2] = t;
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+                            const int c = q * rp + c0 + k0;    // a column of P, a multiple of 16
+                            *reinterpret_cast<uint4*>(prow + (c >> 7) * 16384 + ((((c & 127) >> 4) ^ (row & 7)) << 4)) =
+                                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                        }
+                    } else {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
                             l[k0 + j] += y;
                             l[k0 + j + 1] += z;
                             w[j >> 1] = pack_bf16(y, z);
                         }
+                        const int c = c0 + k0;
+                        unsigned char* at = prow + (c >> 6) * 16384;
+                        const int k = (c & 63) >> 3;
+                        *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
                     }
-                    const int c = c0 + k0;
-                    unsigned char* at = prow + (c >> 6) * 16384;
-                    const int k = (c & 63) >> 3;
-                    *reinterpret_cast<uint4*>(at + ((k ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(at + (((k + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
                 };
                 if constexpr (C::KEEP) {
 #pragma unroll
@@ -882,23 +855,23 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     if (masked) each(Yes{}, weigh);
                     else each(No{}, weigh);
                 }
-                if (!FP8 && masked && wg == 0) {
+                if (masked && wg == 0) {
                     // A new position's value that is no number, times a row's probability of
                     // zero, would spoil the row's sum: such values are taken out of the tile
                     // here, a position a thread, and given to the rows that see them at the
-                    // unit's end.  (E4M3: while widening.)
+                    // unit's end.
                     late |= !wait_bounded(&v_full[g % VB], (g / VB) & 1u, limit);
                     if (d >= 0 && !gone) {
-                        unsigned char* vb = smem + C::V_OFF + (g % VB) * kTcBuf;
+                        unsigned char* vb = smem + C::V_OFF + (g % VB) * C::BUF;
 #pragma unroll 4
-                        for (int k = 0; k < 16; ++k) {
+                        for (int k = 0; k < C::BUF / 2048; ++k) {
                             uint4* at = reinterpret_cast<uint4*>(vb + tc_off(row, k));
                             uint4 w = *at;
                             const uint4 was = w;
-                            w.x = drop_odd_bf16(w.x);
-                            w.y = drop_odd_bf16(w.y);
-                            w.z = drop_odd_bf16(w.z);
-                            w.w = drop_odd_bf16(w.w);
+                            w.x = FP8 ? drop_odd_e4m3(w.x) : drop_odd_bf16(w.x);
+                            w.y = FP8 ? drop_odd_e4m3(w.y) : drop_odd_bf16(w.y);
+                            w.z = FP8 ? drop_odd_e4m3(w.z) : drop_odd_bf16(w.z);
+                            w.w = FP8 ? drop_odd_e4m3(w.w) : drop_odd_bf16(w.w);
                             if (w.x != was.x || w.y != was.y || w.z != was.z || w.w != was.w) {
                                 odd_any = 1;
                                 *at = w;
@@ -960,7 +933,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll 1
             for (int k0 = 0; k0 < mine; k0 += 4) {
                 float v[4];
-                tc_ld4(lanes + 2 * RP + c0 + k0, v);
+                tc_ld4(lanes + C::O_AT + c0 + k0, v);
+                if constexpr (FP8) {
+                    float y[4], z[4];
+                    tc_ld4(lanes + C::O_AT + rp + c0 + k0, y);
+                    tc_ld4(lanes + C::O_AT + 2 * rp + c0 + k0, z);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = fmaf(fmaf(z[k], 0.0625f, y[k]), 0.0625f, v[k]);
+                }
                 if (odd_any) {
                     const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
                     for (int j = j0; j < j1; ++j) {
@@ -1059,7 +1039,7 @@ static EncodeFn encoder() {
 }
 
 // A layer's keys (or values) as [page, head, slot, element], boxes of `box`
-// slots: 64 elements wide and 128-byte swizzled for bf16, whole rows for E4M3.
+// slots and 128 swizzled bytes: half a row of bf16, a row of E4M3.
 static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int box) {
     const bool f8 = c.dtype == SPEC_DTYPE_E4M3;
     const cuuint64_t elt = f8 ? 1 : 2;
@@ -1070,7 +1050,7 @@ static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int
     const cuuint32_t boxes[4] = {f8 ? 128u : 64u, (cuuint32_t)box, 1u, 1u}, one[4] = {1u, 1u, 1u, 1u};
     return encoder() && encoder()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
                                   boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
