@@ -14,7 +14,8 @@
 // probabilities as one row of P.
 //
 // The warps of a CTA, one CTA per SM, each walking the CTA's share:
-//   softmax   4 warps (8 or 12 from 65 rows on, each 4 with their share of the rows)
+//   softmax   4 warps, or two or three times 4 where there are more rows, each 4
+//             with their share of them
 //   MMA       2 threads: one issues the first product, one the second
 //   loaders   4 warps bring the queries, and keys and values into a ring of buffers
 //             each.  A tile of old positions whose pages fit it (page sizes that divide
@@ -1087,8 +1088,10 @@ static cudaError_t launch_tc_e(const AttendArgs& a, cudaStream_t st) {
     const int rt = a.N * a.G, br = tc_block_rows(rt, FP8 ? kTcMostFp8 : kTcMostBf16);
     const int rp = br;                                          // a multiple of 16, as N of the products
     if (rp <= 16) return launch_tc_t<1, 1, FP8>(a, br, rp, st);
-    if (rp <= 32) return launch_tc_t<2, 1, FP8>(a, br, rp, st);
-    if (rp <= 64) return launch_tc_t<4, 1, FP8>(a, br, rp, st);
+    // (an E4M3 tile's softmax has more to do, splitting the probabilities, in half the
+    // time: two warpgroups from 17 rows on; with one it took 3300 cycles a tile of 32 rows)
+    if (rp <= 32) return launch_tc_t<FP8 ? 1 : 2, FP8 ? 2 : 1, FP8>(a, br, rp, st);
+    if (rp <= 64) return launch_tc_t<FP8 ? 2 : 4, FP8 ? 2 : 1, FP8>(a, br, rp, st);
     if constexpr (!FP8) return launch_tc_t<3, 3, false>(a, br, rp, st);
     return cudaErrorInvalidValue;                               // (blocks of an 8-bit cache are no larger)
 }
