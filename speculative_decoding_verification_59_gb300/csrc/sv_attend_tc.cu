@@ -81,7 +81,10 @@ struct TcCfg {
     // tensor memory twice.
     static constexpr bool KEEP = CH <= 2;
     static constexpr int SM_THREADS = NSM * 128;
-    static constexpr int LOADERS = 128;
+    // loader warps: 4, or 2 where that leaves the softmax's twelve warps 128 registers
+    // a thread (18 warps count as 20: 96)
+    static constexpr int LW = NSM == 3 ? 2 : 4;
+    static constexpr int LOADERS = LW * 32;
     static constexpr int THREADS = SM_THREADS + 64 + LOADERS;
     static constexpr int V_OFF = KB * BUF;
     static constexpr int P_OFF = V_OFF + VB * BUF;
@@ -150,12 +153,12 @@ __device__ __forceinline__ void tc_ld16_done(float* v) {
     asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
                  "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
-__device__ __forceinline__ void tc_ld4(uint32_t at, float (&v)[4]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+__device__ __forceinline__ void tc_ld8(uint32_t at, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(at));
     tc_wait_ld();
-    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]));
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
 }
 __device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
     uint32_t r[16];
@@ -296,11 +299,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 
     if (tid == 0) {
         for (int i = 0; i < KB; ++i) {
-            mbar_init(&k_full[i], 128);
+            mbar_init(&k_full[i], C::LOADERS);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < VB; ++i) {
-            mbar_init(&v_full[i], 128);
+            mbar_init(&v_full[i], C::LOADERS);
             mbar_init(&v_empty[i], 1);
         }
         mbar_init(&drained[0], 1);
@@ -339,10 +342,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 
     if (warp > kMmaWarp + 1) {
         // ================= loaders =================
-        const int lt = tid - C::SM_THREADS - 64, lw = (lt >> 5) & 3;
+        const int lt = tid - C::SM_THREADS - 64, lw = lt >> 5;
+        constexpr int RS = 4 / C::LW;                          // sets of 32 rows of a warp: rows (h LW + lw) 32 ..
         constexpr int CPR = FP8 ? 8 : 16;                      // 16-byte chunks of a cached row
         constexpr int RPI = 32 / CPR;                          // rows a warp copies at once
-        constexpr int PIECES = 32 / RPI;                       // a warp's 32 rows: pieces of 16 bytes a thread
+        constexpr int PIECES = 32 / RPI;                       // 32 rows: pieces of 16 bytes a thread
         const int ch = lane % CPR, sub = lane / CPR;
         bool ok = true;
         unsigned t = 0;                                        // tiles issued
@@ -364,16 +368,21 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 return box > 0 && pos + box <= min(un.sl.ctx, un.sl.total) ? table(page_index(a, pos, &slot)) : -1;
             };
             int g0 = un.ta, pages = group_page(g0), pages_next = group_page(g0 + group);
-            // The other tiles: lane l finds row l of the warp's 32, one tile ahead (E4M3: of
+            // The other tiles: lane l finds row l of each of the warp's sets, one tile ahead (E4M3: of
             // every tile, for the scales).
-            auto row_page = [&](int i, int* slot) {
-                const int pos = i * kTcTile + lw * 32 + lane;
+            auto row_page = [&](int i, int h, int* slot) {
+                const int pos = i * kTcTile + (h * C::LW + lw) * 32 + lane;
                 *slot = 0;
                 return pos < un.sl.total ? table(page_index(a, pos, slot)) : -2;      // -2: no position
             };
             auto by_row = [&](int i) { return i < un.tb && (!by_tma(i) || FP8); };
-            int rpage = -2, rslot = 0;
-            if (by_row(un.ta)) rpage = row_page(un.ta, &rslot);
+            int rpage[RS], rslot[RS];
+#pragma unroll
+            for (int h = 0; h < RS; ++h) {
+                rpage[h] = -2;
+                rslot[h] = 0;
+                if (by_row(un.ta)) rpage[h] = row_page(un.ta, h, &rslot[h]);
+            }
             // ---- the unit's queries
             const int qb = (int)(uc % C::QB);
             if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
@@ -438,8 +447,8 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             // ---- the unit's tiles
             for (int i = un.ta; i < un.tb && ok; ++i) {
                 const bool tma = by_tma(i);
-                int at_page = 0, at_slot = 0;                   // TMA: the lane's box; else the lane's row
-                bool have = false, lost = false;
+                int at_page = 0, at_slot = 0;                   // TMA: the lane's box
+                bool lost = false;
                 if (tma) {
                     if (i == g0 + group) {
                         g0 = i;
@@ -448,26 +457,27 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     }
                     at_page = __shfl_sync(0xffffffffu, pages, ((i - g0) * boxes + lane) & 31);
                     if (box == kTcTile) page_index(a, i * kTcTile, &at_slot);       // a page may hold several tiles
-                    have = (unsigned)at_page < (unsigned)a.c.num_pages;
-                    lost = lane < boxes && !have;
-                    if (!have) at_page = 0;                     // the unit ends as NaN anyway
-                } else {
-                    at_page = rpage;
-                    at_slot = rslot;
-                    have = (unsigned)at_page < (unsigned)a.c.num_pages;
-                    lost = !have && at_page != -2;
+                    lost = lane < boxes && (unsigned)at_page >= (unsigned)a.c.num_pages;
+                    if (lost) at_page = 0;                      // the unit ends as NaN anyway
+                }
+                int64_t off[RS], so[RS];                        // the lane's rows and scales
+                unsigned havem[RS];
+                bool scaled[RS];
+#pragma unroll
+                for (int h = 0; h < RS; ++h) {
+                    scaled[h] = (unsigned)rpage[h] < (unsigned)a.c.num_pages;
+                    lost |= !tma && !scaled[h] && rpage[h] != -2;
+                    off[h] = scaled[h] && !tma ? entry_off(a.c, rpage[h], rslot[h], un.hk) : 0;
+                    so[h] = FP8 && scaled[h] ? scale_off(a.c, rpage[h], rslot[h], un.hk) : 0;
+                    havem[h] = __ballot_sync(0xffffffffu, scaled[h]);
+                    rpage[h] = -2;
+                    if (by_row(i + 1)) rpage[h] = row_page(i + 1, h, &rslot[h]);
                 }
                 if (__any_sync(0xffffffffu, lost) && lane == 0) {
 #pragma unroll
                     for (int w = 0; w < NSM; ++w) unit_bad[w][uc % kTcUnitRing] = 1;
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
                 }
-                const int64_t off = have && !tma ? entry_off(a.c, at_page, at_slot, un.hk) : 0;
-                const bool scaled = (unsigned)rpage < (unsigned)a.c.num_pages;
-                const int64_t so = FP8 && scaled ? scale_off(a.c, rpage, rslot, un.hk) : 0;
-                rpage = -2;
-                if (by_row(i + 1)) rpage = row_page(i + 1, &rslot);
-                const unsigned havem = __ballot_sync(0xffffffffu, have);
                 for (int kv = 0; kv < 2; ++kv) {
                     // The buffer, once it is free.  Every warp waits for every buffer of its
                     // kind and arrives for it, the ones that have no part in a TMA tile too: a
@@ -492,18 +502,24 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     } else {
                         const char* base = static_cast<const char*>(kv ? a.c.v : a.c.k);
 #pragma unroll
-                        for (int p = 0; p < PIECES; ++p) {
-                            const int wr = p * RPI + sub, row = lw * 32 + wr;
-                            const int64_t e = __shfl_sync(0xffffffffu, off, wr) * (FP8 ? 1 : 2) + ch * 16;
-                            cp16(dst + tc_off(row, ch), base + e, (havem >> wr) & 1u);
-                        }
+                        for (int h = 0; h < RS; ++h)
+#pragma unroll
+                            for (int p = 0; p < PIECES; ++p) {
+                                const int wr = p * RPI + sub, row = (h * C::LW + lw) * 32 + wr;
+                                const int64_t e = __shfl_sync(0xffffffffu, off[h], wr) * (FP8 ? 1 : 2) + ch * 16;
+                                cp16(dst + tc_off(row, ch), base + e, (havem[h] >> wr) & 1u);
+                            }
                     }
                     bool copies = !tma;                         // the threads have copies of their own in flight
                     if constexpr (FP8) {
                         if (kv == 0) {                          // both scales: the softmax wants them with the scores
-                            const uint32_t at = smem_addr(smem + C::SCALE_OFF) + ((t % kTcScaleRing) * 2 * kTcTile + lw * 32 + lane) * 4;
-                            cp4(at, a.c.k_scale + so, scaled);
-                            cp4(at + kTcTile * 4, a.c.v_scale + so, scaled);
+#pragma unroll
+                            for (int h = 0; h < RS; ++h) {
+                                const uint32_t at = smem_addr(smem + C::SCALE_OFF) +
+                                                    ((t % kTcScaleRing) * 2 * kTcTile + (h * C::LW + lw) * 32 + lane) * 4;
+                                cp4(at, a.c.k_scale + so[h], scaled[h]);
+                                cp4(at + kTcTile * 4, a.c.v_scale + so[h], scaled[h]);
+                            }
                             copies = true;
                         }
                     }
@@ -932,15 +948,15 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             if (row == 0) unit_bad[wg][uc % kTcUnitRing] = 0;
             // (a small loop: it runs once a unit, its instructions seldom at hand)
 #pragma unroll 1
-            for (int k0 = 0; k0 < mine; k0 += 4) {
-                float v[4];
-                tc_ld4(lanes + C::O_AT + c0 + k0, v);
+            for (int k0 = 0; k0 < mine; k0 += 8) {
+                float v[8];
+                tc_ld8(lanes + C::O_AT + c0 + k0, v);
                 if constexpr (FP8) {
-                    float y[4], z[4];
-                    tc_ld4(lanes + C::O_AT + rp + c0 + k0, y);
-                    tc_ld4(lanes + C::O_AT + 2 * rp + c0 + k0, z);
+                    float y[8], z[8];
+                    tc_ld8(lanes + C::O_AT + rp + c0 + k0, y);
+                    tc_ld8(lanes + C::O_AT + 2 * rp + c0 + k0, z);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = fmaf(fmaf(z[k], 0.0625f, y[k]), 0.0625f, v[k]);
+                    for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(z[k], 0.0625f, y[k]), 0.0625f, v[k]);
                 }
                 if (odd_any) {
                     const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
@@ -958,14 +974,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (fabsf(x) < CUDART_INF_F) continue;
                         const int d = j - sl.ctx;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 8; ++k) {
                             const int n = rown[c0 + k0 + k];
                             if (a.par ? (anc[wg][0][n] >> (d & 63)) & 1ull : d <= n) v[k] += x;
                         }
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const int r = c0 + k0 + k;
                     if (k0 + k < mine) {
                         if (whole) {
