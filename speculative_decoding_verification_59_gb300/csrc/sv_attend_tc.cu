@@ -695,10 +695,16 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 // The score of the warpgroup's row k in powers of two, plus nr (less its
                 // reference).  The tiles that hold new positions, or the end, are masked;
                 // the others run without.
-                auto arg = [&](auto mask, float s, int k, float nr) {
-                    const float x = FP8 ? fmaf(s, f, add + nr) : fmaf(s, f, nr);
-                    if constexpr (decltype(mask)::value) return (sees[k >> 5] >> (k & 31)) & 1u ? x : kNegInf;
-                    else return x;
+                // Two rows an instruction.
+                const f32x2 ff = f2_pack(f, f), aa = f2_pack(add, add);
+                auto arg = [&](auto mask, float& s0, float& s1, int k, float nr0, float nr1) {
+                    f32x2 r = f2_pack(nr0, nr1);
+                    if constexpr (FP8) r = f2_add(r, aa);
+                    f2_unpack(f2_fma(f2_pack(s0, s1), ff, r), s0, s1);
+                    if constexpr (decltype(mask)::value) {
+                        if (!((sees[k >> 5] >> (k & 31)) & 1u)) s0 = kNegInf;
+                        if (!((sees[k >> 5] >> ((k + 1) & 31)) & 1u)) s1 = kNegInf;
+                    }
                 };
                 const uint32_t s_at = lanes + (g & 1) * C::S_COLS + c0;
                 const float* qf = qinv[uc & 3];
@@ -732,10 +738,8 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                                 for (int j = 0; j < 16; j += 4) {
                                     const int k = (c2_ + h) * 16 + j;
                                     const float4 nr = *reinterpret_cast<const float4*>(&nref[c0 + k]);
-                                    v[h][j] = arg(mask, v[h][j], k, nr.x);
-                                    v[h][j + 1] = arg(mask, v[h][j + 1], k + 1, nr.y);
-                                    v[h][j + 2] = arg(mask, v[h][j + 2], k + 2, nr.z);
-                                    v[h][j + 3] = arg(mask, v[h][j + 3], k + 3, nr.w);
+                                    arg(mask, v[h][j], v[h][j + 1], k, nr.x, nr.y);
+                                    arg(mask, v[h][j + 2], v[h][j + 3], k + 2, nr.z, nr.w);
                                 }
                                 use((c2_ + h) * 16, v[h]);
                             }
@@ -848,8 +852,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
-                            l[k0 + j] += y;
-                            l[k0 + j + 1] += z;
+                            f2_unpack(f2_add(f2_pack(l[k0 + j], l[k0 + j + 1]), f2_pack(y, z)), l[k0 + j], l[k0 + j + 1]);
                             w[j >> 1] = pack_bf16(y, z);
                         }
                         const int c = c0 + k0;
