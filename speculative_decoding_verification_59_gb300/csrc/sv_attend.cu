@@ -330,7 +330,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             for (int nt = 0; nt < C::NT; ++nt) {
                 if constexpr (FP8) {
                     const float2 kk = *reinterpret_cast<const float2*>(ksc + nt * 8 + 2 * quad);
-                    const float2 vv = *reinterpret_cast<const float2*>(ksc + C::ST + nt * 8 + 2 * quad);
+                    float2 vv = *reinterpret_cast<const float2*>(ksc + C::ST + nt * 8 + 2 * quad);
+                    vv.x = value_scale(vv.x);
+                    vv.y = value_scale(vv.y);
                     const float g0 = __log2f(vv.x), g1 = __log2f(vv.y);
                     vinv[nt][0] = 1.f / vv.x;
                     vinv[nt][1] = 1.f / vv.y;

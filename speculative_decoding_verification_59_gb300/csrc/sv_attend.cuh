@@ -58,6 +58,11 @@ __device__ __forceinline__ int page_index(const AttendArgs& a, int pos, int* slo
 __device__ __forceinline__ long long quotient(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
+// The scale of an E4M3 position's values as a factor of its probability: not
+// below any that spec_kv_append writes, so that a scale of zero (values of
+// zero) leaves the position its weight.
+__device__ __forceinline__ float value_scale(float s) { return s < 1e-23f ? 1e-23f : s; }
+
 // Share i of `total` tiles among n CTAs begins at tile i * total / n.
 __device__ __forceinline__ long long share_begin(long long total, long long n, long long i) { return quotient(i * total, n); }
 // The CTA whose share holds tile t.

@@ -249,6 +249,19 @@ __device__ __forceinline__ uint32_t e4m3_term(float& a, float& b) {
     return t;
 }
 
+// The same of a pair of fp16 values (both steps are exact there): their e4m3
+// roundings, and sixteen times what those leave over.
+__device__ __forceinline__ uint32_t e4m3_of_f16x2(uint32_t p) {
+    unsigned short t;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(p));
+    return t;
+}
+__device__ __forceinline__ uint32_t left_over_f16x2(uint32_t p, uint32_t t) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(p), "r"(e4m3_to_f16x2(t)), "r"(0x4c004c00u));
+    return r;
+}
+
 struct Max {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
@@ -689,8 +702,9 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 if constexpr (FP8) {
                     const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + (g % kTcScaleRing) * 2 * kTcTile;
                     f = c2 * sc[row];
-                    add = __log2f(sc[kTcTile + row]);
-                    vinv = 1.f / sc[kTcTile + row];
+                    const float vs = value_scale(sc[kTcTile + row]);
+                    add = __log2f(vs);
+                    vinv = fabsf(vs) < CUDART_INF_F ? 1.f / vs : 0.f;         // (of a masked position it may be anything)
                 }
                 // The score of the warpgroup's row k in powers of two, plus nr (less its
                 // reference).  The tiles that hold new positions, or the end, are masked;
@@ -725,10 +739,11 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
                                 const float4 q = *reinterpret_cast<const float4*>(&qf[c0 + c2_ * 16 + j]);
-                                v[0][j] = fmaf(v[1][j], 0.0625f, v[0][j]) * q.x;
-                                v[0][j + 1] = fmaf(v[1][j + 1], 0.0625f, v[0][j + 1]) * q.y;
-                                v[0][j + 2] = fmaf(v[1][j + 2], 0.0625f, v[0][j + 2]) * q.z;
-                                v[0][j + 3] = fmaf(v[1][j + 3], 0.0625f, v[0][j + 3]) * q.w;
+                                const f32x2 w = f2_pack(0.0625f, 0.0625f);
+                                f2_unpack(f2_mul(f2_fma(f2_pack(v[1][j], v[1][j + 1]), w, f2_pack(v[0][j], v[0][j + 1])), f2_pack(q.x, q.y)),
+                                          v[0][j], v[0][j + 1]);
+                                f2_unpack(f2_mul(f2_fma(f2_pack(v[1][j + 2], v[1][j + 3]), w, f2_pack(v[0][j + 2], v[0][j + 3])), f2_pack(q.z, q.w)),
+                                          v[0][j + 2], v[0][j + 3]);
                             }
                         }
 #pragma unroll
@@ -831,12 +846,13 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         uint32_t w[3][4];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
-                            l[k0 + j] += y != 0.f ? y * vinv : 0.f;            // a masked scale may be anything
-                            l[k0 + j + 1] += z != 0.f ? z * vinv : 0.f;
+                            const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
+                            f2_unpack(f2_fma(f2_pack(y, z), f2_pack(vinv, vinv), f2_pack(l[k0 + j], l[k0 + j + 1])), l[k0 + j], l[k0 + j + 1]);
+                            uint32_t p = pack_f16(y, z);       // to 11 bits; what follows is exact
 #pragma unroll
                             for (int q = 0; q < 3; ++q) {
-                                const uint32_t t = q < 2 ? e4m3_term(y, z) : pack_e4m3(y, z);
+                                const uint32_t t = e4m3_of_f16x2(p);
+                                if (q < 2) p = left_over_f16x2(p, t);
                                 if (j & 2) w[q][j >> 2] |= t << 16;
                                 else w[q][j >> 2] = t;
                             }
