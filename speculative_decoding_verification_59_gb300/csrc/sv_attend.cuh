@@ -287,7 +287,9 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x
 
 // The matrix-unit kernel of sv_attend_tc.cu (rows of 128 elements).
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);
-bool attend_takes_tc(int N, int G, int D);
+// Whether that kernel takes a call; capacity: positions that a sequence's row of
+// the block table has room for.
+bool attend_takes_tc(int N, int G, int D, long long capacity);
 size_t attend_tc_workspace(int N, int G);
 
 }  // namespace sv

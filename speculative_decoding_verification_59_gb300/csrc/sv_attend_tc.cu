@@ -1049,7 +1049,18 @@ static int tc_block_rows(int rt, int most) {
 }
 constexpr int kTcMostBf16 = 144, kTcMostFp8 = 64;
 
-bool attend_takes_tc(int N, int G, int D) { return D == kTcD; }
+// Which kernel takes heads of 128 (each side measured on one GB300, bf16, 8 cached
+// heads; us here / in sv_attend.cu).  Up to 16 rows that one's single matrix tile
+// is enough and its units cost less to begin and end: 152 / 128 for 64 sequences of
+// 4 rows over up to 4000 positions, 14.1 / 9.1 for one over 1000.  Above 32 rows it
+// would read the cache once per 32: 111 / 224 for 32 trees of 144 rows over up to
+// 2048.  Between, this one gains per position what it loses per unit: 154 / 178 for
+// 64 x 32 rows over up to 4096, but 111 / 90 for 20 rows over up to 2000 -- so the
+// longest context that the block table has room for decides.
+constexpr long long kTcMinCapacity = 2560;
+bool attend_takes_tc(int N, int G, int D, long long capacity) {
+    return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= kTcMinCapacity));
+}
 
 size_t attend_tc_workspace(int N, int G) {
     // the largest block of rows that N G or fewer can come in, so that more rows

@@ -89,9 +89,10 @@ def test_tree_shaped_as_a_chain_is_a_chain(sv):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-def test_long_context_is_split_and_joined(sv, fp8):
+@pytest.mark.parametrize("N", [2, 5, 12, 36])                     # 8, 20, 48 and 144 rows of a cached head
+def test_long_context_is_split_and_joined(sv, fp8, N):
     """One sequence over every CTA, ragged beside short ones, and the same bits every time."""
-    args = case(5, 3, 2, 8, 2, 128, 16, [9001, 3, 1500], fp8)
+    args = case(5, 3, N, 8, 2, 128, 16, [9001, 3, 1500], fp8)
     check(sv, *args)
     parts, q, _, c, nb = args
     cache = R.on_gpu(sv, parts)
@@ -297,7 +298,7 @@ def test_refusals(sv):
 def test_waits_that_run_out_report_and_return(sv, fp8):
     """With the kernels' bounded waits set to give up at once: the error word says so, the rows
     are NaN, and later calls through the same workspace are right again."""
-    args = case(27, 2, 4, 8, 2, 128, 16, [700, 3000], fp8)
+    args = case(27, 2, 10, 8, 2, 128, 16, [700, 3000], fp8)       # 40 rows: the kernel that has waits
     parts, q, par, c, nb = args
     cache = R.on_gpu(sv, parts)
     want = sv.paged_attention(q.cuda(), cache, c.cuda())
@@ -316,11 +317,12 @@ def test_waits_that_run_out_report_and_return(sv, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("page", [8, 16, 64, 128, 256, 48])
-def test_long_shares(sv, fp8, page):
+@pytest.mark.parametrize("Hq", [16, 64, 160])                   # 6, 24 and 60 rows of a cached head
+def test_long_shares(sv, fp8, page, Hq):
     """Shares of many tiles, old positions and new ones in turn, against the rows one by one: every
     sequence's answer is that of the sequence alone."""
     g = torch.Generator().manual_seed(page)
-    B, N, Hq, H, D = 40, 3, 16, 8, 128
+    B, N, H, D = 40, 3, 8, 128
     ctx = torch.randint(0, 3000, (B,), generator=g).tolist()
     cache = sv.KVCache(*R.make_cache_on_gpu(28, B, max(ctx) + N, page, H, D, fp8))
     qd = (torch.randn((B, N, Hq, D), generator=g) * 1.5).to(torch.bfloat16).cuda()
@@ -334,3 +336,21 @@ def test_long_shares(sv, fp8, page):
         # the split differs, so sums come in another order and references differ: P and the
         # result are each rounded anew (two unit roundoffs of the values' magnitude, at most 4.5)
         assert (alone.float() - whole[0][b:b + 1].float()).abs().max() <= 4.5 * 2 * R.U_BF16
+
+
+@pytest.mark.parametrize("N", [2, 12])
+def test_scale_of_zero(sv, N):
+    """An 8-bit position whose value scale is zero has a value of zero and keeps its weight."""
+    parts, q, par, c, nb = case(29, 1, N, 8, 2, 128, 16, [200], fp8=True)
+    parts[4].view(-1)[::3] = 0.0
+    check(sv, parts, q, par, c, nb)
+
+
+@pytest.mark.parametrize("N,G", [(6, 4), (7, 5), (16, 1), (33, 1), (5, 7), (64, 2), (1, 40)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_around_the_kernels_bounds(sv, fp8, N, G):
+    """Row counts on both sides of 16, 32, 64 and 144, in a table with room for long contexts."""
+    parts = R.make_cache(30 + N, 2, 300, 16, 2, 128, fp8, max_pages=200)
+    g = torch.Generator().manual_seed(N)
+    q = (torch.randn((2, N, 2 * G, 128), generator=g) * 1.5).to(torch.bfloat16)
+    check(sv, parts, q, None, torch.tensor([200, 77], dtype=torch.int32), torch.full((2,), N, dtype=torch.int32))
