@@ -498,7 +498,7 @@ spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
  *   out_top_idx [rows, K]       the K largest logits' tokens (larger first, lower index
  *                               first among equal logits, -0.0 equal to +0.0)
  *   out_top_logprob [rows, K]   their ln p
- * 0 <= K <= 8 (K = 0: no lists, both may be NULL); with V < K the lists are
+ * 1 <= V <= 8388608, 0 <= K <= 8 (K = 0: no lists, both may be NULL); with V < K the lists are
  * padded with -1 and -inf.  A masked (-inf) logit has ln p = -inf and adds
  * nothing to the entropy.  A token outside [0, V) gives ln p = NaN and sets
  * SPEC_DEVERR_TOKEN_RANGE; a row of -inf alone gives NaN everywhere (list

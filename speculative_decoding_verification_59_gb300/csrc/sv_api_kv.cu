@@ -151,7 +151,7 @@ spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
 }
 
 size_t spec_logprobs_workspace_size(int rows, int V, int K) {
-    if (rows < 0 || V < 1 || K < 0 || K > 8) return 0;
+    if (rows < 0 || V < 1 || V > kMaxLogprobVocab || K < 0 || K > 8) return 0;
     return logprobs_workspace_size(rows, V, K);
 }
 
@@ -161,7 +161,7 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
                                   float* out_top_logprob, void* workspace,
                                   size_t workspace_bytes, cudaStream_t stream) {
     if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16) return SPEC_ERR_UNSUPPORTED_DTYPE;
-    if (rows < 0 || V < 1 || K < 0 || K > 8) return SPEC_ERR_INVALID_ARG;
+    if (rows < 0 || V < 1 || V > kMaxLogprobVocab || K < 0 || K > 8) return SPEC_ERR_INVALID_ARG;
     if (!(temperature >= 1e-20f) || !isfinite(temperature)) return SPEC_ERR_INVALID_ARG;
     if ((long long)rows * ((long long)nseg(V, elt_size(dtype)) + 1) >= (1LL << 31)) return SPEC_ERR_INVALID_ARG;
     if (rows == 0) return SPEC_OK;

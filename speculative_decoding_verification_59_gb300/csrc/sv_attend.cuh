@@ -192,56 +192,55 @@ __device__ __forceinline__ void put_row(const AttendArgs& a, const AttUnit& x, b
 
 // Adds rows ra .. rb - 1 of the parts of a unit that CTAs c0 .. c1 hold, in
 // that order, and writes them; by WARPS warps (warp w of them).  A warp takes
-// kJoinRows rows at once, one lane per part for their references and totals,
-// then its lanes across the elements: the loads of several rows and parts are
-// in flight together (a row and part at a time, the join of 32 rows in 5 parts
-// took 22 us; the parts come from L2, about 0.5 us away).
-constexpr int kJoinRows = 4;
-template <int D, int WARPS>
-__device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
-                                           int srows, int c0, int c1, int ra, int rb) {
+// ROWS rows at once, one lane per part for their references and totals, then its
+// lanes across the elements: the loads of several rows and parts are in flight
+// together (a row and part at a time, the join of 32 rows in 5 parts took 22 us;
+// the parts come from L2, about 0.5 us away).
+template <int D, int WARPS, int ROWS>
+__device__ __forceinline__ void join_rows(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
+                                          int srows, int c0, int c1, int ra, int rb) {
     constexpr int V = D / 32;                                 // elements of a lane: 2, 4 or 8
     constexpr int V4 = V >= 4 ? V / 4 : 1;
     const int lane = threadIdx.x & 31, parts = c1 - c0 + 1;
     auto part = [&](int p) { return slots + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
-    for (int r0 = ra + w * kJoinRows; r0 < rb; r0 += WARPS * kJoinRows) {
-        float M[kJoinRows], L[kJoinRows];
+    for (int r0 = ra + w * ROWS; r0 < rb; r0 += WARPS * ROWS) {
+        float M[ROWS], L[ROWS];
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) { M[k] = kNegInf; L[k] = 0.f; }
+        for (int k = 0; k < ROWS; ++k) { M[k] = kNegInf; L[k] = 0.f; }
         for (int p0 = 0; p0 < parts; p0 += 32) {
-            float m[kJoinRows];
+            float m[ROWS];
 #pragma unroll
-            for (int k = 0; k < kJoinRows; ++k)
+            for (int k = 0; k < ROWS; ++k)
                 m[k] = p0 + lane < parts && r0 + k < rb ? __ldcg(part(p0 + lane) + (size_t)srows * D + r0 + k) : kNegInf;
 #pragma unroll
-            for (int k = 0; k < kJoinRows; ++k) M[k] = fmaxf(M[k], m[k]);
+            for (int k = 0; k < ROWS; ++k) M[k] = fmaxf(M[k], m[k]);
         }
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) {
+        for (int k = 0; k < ROWS; ++k) {
             M[k] = warp_max(M[k]);
             if (M[k] == kNegInf) M[k] = 0.f;                  // no part has seen a position
         }
-        float v[kJoinRows][V];
+        float v[ROWS][V];
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k)
+        for (int k = 0; k < ROWS; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) v[k][e] = 0.f;
         for (int p0 = 0; p0 < parts; p0 += 32) {
-            float f[kJoinRows];
+            float f[ROWS];
 #pragma unroll
-            for (int k = 0; k < kJoinRows; ++k) {
+            for (int k = 0; k < ROWS; ++k) {
                 const bool on = p0 + lane < parts && r0 + k < rb;
                 const float* q = part(on ? p0 + lane : 0) + (size_t)srows * D + (on ? r0 + k : ra);
                 f[k] = on ? ex2_approx(__ldcg(q) - M[k]) : 0.f;
                 L[k] = on ? fmaf(f[k], __ldcg(q + srows), L[k]) : L[k];
             }
             const int n = min(32, parts - p0);
-#pragma unroll 2
+#pragma unroll(ROWS == 1 ? 8 : 2)
             for (int p = 0; p < n; ++p) {
                 const float* q = part(p0 + p) + (size_t)r0 * D + lane * V;
-                float y[kJoinRows][V];
+                float y[ROWS][V];
 #pragma unroll
-                for (int k = 0; k < kJoinRows; ++k) {
+                for (int k = 0; k < ROWS; ++k) {
                     const float* at = q + (r0 + k < rb ? k * D : 0);
                     if constexpr (V == 2) {
                         const float2 t = __ldcg(reinterpret_cast<const float2*>(at));
@@ -259,7 +258,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kJoinRows; ++k) {
+                for (int k = 0; k < ROWS; ++k) {
                     const float fp = __shfl_sync(0xffffffffu, f[k], p);
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[k][e] = fmaf(fp, y[k][e], v[k][e]);
@@ -267,7 +266,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x
             }
         }
 #pragma unroll
-        for (int k = 0; k < kJoinRows; ++k) {
+        for (int k = 0; k < ROWS; ++k) {
             // the lanes' totals in a fixed order
             const float lsum = warp_sum(L[k]);
             if (r0 + k < rb) {
@@ -283,6 +282,14 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x
             }
         }
     }
+}
+
+// One row a warp while there is a warp for each, else four.
+template <int D, int WARPS>
+__device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
+                                           int srows, int c0, int c1, int ra, int rb) {
+    if (rb - ra <= WARPS) join_rows<D, WARPS, 1>(a, x, w, slots, slot_floats, srows, c0, c1, ra, rb);
+    else join_rows<D, WARPS, 4>(a, x, w, slots, slot_floats, srows, c0, c1, ra, rb);
 }
 
 // The matrix-unit kernel of sv_attend_tc.cu (rows of 128 elements).

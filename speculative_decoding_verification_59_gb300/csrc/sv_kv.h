@@ -48,6 +48,8 @@ struct AttendArgs {
 size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
 
+// The merge keeps two bytes for each 4 KB chunk of a row in shared memory.
+constexpr int kMaxLogprobVocab = 1 << 23;
 size_t logprobs_workspace_size(int rows, int V, int K);
 cudaError_t launch_logprobs(const void* z, spec_dtype_t dt, const int32_t* tok, float T, int rows, int V, int K,
                             float* lp, float* ent, int32_t* ti, float* tl, void* ws, cudaStream_t st);

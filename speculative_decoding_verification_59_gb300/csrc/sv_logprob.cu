@@ -5,9 +5,12 @@
 //   Z = sum 2^a_j,  W = sum a_j 2^a_j,
 //   ln p(x) = (z_x - M) / T - ln Z,   H = -sum p ln p = ln Z - ln 2 W / Z.
 // Each 4 KB warp chunk of a row leaves its own maximum m with Z and W taken
-// relative to it, and the elements that can still be among the row's top K;
-// one CTA per row then brings the chunks to the common maximum and orders
-// the candidates.
+// relative to it; one CTA per row then brings the chunks to the common maximum.
+// The K alternatives cost the stream nothing: the K-th largest chunk maximum is
+// a lower bound of the row's K-th largest logit, so that CTA reads again only the
+// chunks whose maximum reaches it -- K of them, unless maxima are equal -- and
+// orders their logits that do.  (Collecting candidates while streaming took 61 us
+// for 512 rows of 151936 bf16 logits and K = 5, against 35 without lists.)
 //
 // The stream is a ring of bulk copies (one producer warp, kWarps consumer
 // warps, 32 KB stages).  Rows may begin at any element: a row's chunks are cut
@@ -21,18 +24,17 @@
 namespace sv {
 
 constexpr int kMergeThreads = 128;
-constexpr int kMergePool = 32;
+constexpr int kMaxAlternatives = 8;
 constexpr float kArgFloor = -256.f;           // 2^-256 is zero in fp32, and -256 times it too
 constexpr float kLn2f = 0.6931471805599453f;
 
 struct LogprobArgs {
     const char* z;
     const int32_t* tok;
-    float T, s;
+    float T, s, inv_s;
     int rows, V, K, nseg;
     long long chunks;
     float4* stats;             // per warp chunk: m, Z, W (relative to m)
-    float2* cand;              // per warp chunk: 2 KC candidates
     int* err;
     float *lp, *ent;
     int32_t* ti;
@@ -49,160 +51,74 @@ __device__ __forceinline__ void row_span(const LogprobArgs& a, int elt, int r, l
 }
 
 // (Z, W) of a warp chunk relative to its maximum m > -inf, over the warp.
-// While m s is moderate the arguments are one FMA each, z s - fl(m s): off
-// by the rounding r = m s - fl(m s), which the sums take back at the end
-// (2^(a + r): Z = 2^-r Z', W = 2^-r W' - r Z).  Masked logits (-inf) would
-// give 0 x inf in W; kArgFloor keeps their argument finite.
+// The arguments are one FMA each, z s - fl(m s): off by the rounding r = m s -
+// fl(m s), which the sums take back at the end (2^(a + r): Z = 2^-r Z', W =
+// 2^-r W' - r Z).  Masked logits (-inf) would give 0 x inf in W: logits are
+// first raised to one whose power is zero, bf16 ones two an instruction.  Where
+// no such logit is near (tiny temperatures, where one step of a bf16 logit
+// already counts; chunks of the type's lowest value) the arguments (z - m) s
+// are clamped instead.
 template <int ELT>
-__device__ __forceinline__ void chunk_sums(const uint4 (&v)[kVecPerLane], float m, float s, float* Z, float* W) {
-    const float ms = m * s;
-    const bool direct = !(fabsf(ms) < kFmaArgLimit);
-    const f32x2 s2 = f2_pack(s, s), off = direct ? f2_pack(0.f, 0.f) : f2_pack(-ms, -ms);
-    const f32x2 sub = direct ? f2_pack(m, m) : f2_pack(0.f, 0.f);
+__device__ __forceinline__ void chunk_sums(const uint4 (&v)[kVecPerLane], float m, float s, float inv_s, float* Z, float* W) {
     f32x2 z2 = f2_pack(0.f, 0.f), w2 = z2;
+    float r = 0.f;
+    const float below = kArgFloor * inv_s;                     // 256 powers of two below the maximum
+    if (m < -3.3e38f || !(below <= -fabsf(m) * 0.015625f)) {   // warp-uniform
 #pragma unroll
-    for (int t = 0; t < kVecPerLane; ++t)
+        for (int t = 0; t < kVecPerLane; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; c += (ELT == 2 ? 1 : 2)) {
-            f32x2 x;
-            if constexpr (ELT == 2) {
+            for (int c = 0; c < 4; ++c) {
                 const uint32_t w = u4_get(v[t], c);
-                x = f2_pack(bf16_lo(w), bf16_hi(w));
-            } else {
-                x = f2_pack(__uint_as_float(u4_get(v[t], c)), __uint_as_float(u4_get(v[t], c + 1)));
+                const float p = fmaxf(((ELT == 2 ? bf16_lo(w) : __uint_as_float(w)) - m) * s, kArgFloor);
+                const float q = ELT == 2 ? fmaxf((bf16_hi(w) - m) * s, kArgFloor) : kArgFloor;
+                const f32x2 e = f2_pack(ex2_approx(p), ex2_approx(q));
+                z2 = f2_add(z2, e);
+                w2 = f2_fma(e, f2_pack(p, q), w2);
             }
-            if (direct) x = f2_sub(x, sub);                    // uniform; tiny temperatures only
-            float p, q;
-            f2_unpack(f2_fma(x, s2, off), p, q);
-            p = fmaxf(p, kArgFloor);
-            q = fmaxf(q, kArgFloor);
-            const f32x2 e = f2_pack(ex2_approx(p), ex2_approx(q));
-            z2 = f2_add(z2, e);
-            w2 = f2_fma(e, f2_pack(p, q), w2);
-        }
+    } else {
+        const float ms = m * s;
+        r = fmaf(m, s, -ms);
+        const f32x2 s2 = f2_pack(s, s), off = f2_pack(-ms, -ms);
+        const float low = fmaxf(m + below, -3.3e38f);          // finite, and its bf16 rounding too
+        uint32_t low2;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(low2) : "f"(low));
+#pragma unroll
+        for (int t = 0; t < kVecPerLane; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; c += (ELT == 2 ? 1 : 2)) {
+                f32x2 x;
+                if constexpr (ELT == 2) {
+                    uint32_t w = u4_get(v[t], c);
+                    asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(low2));
+                    x = f2_pack(bf16_lo(w), bf16_hi(w));
+                } else {
+                    x = f2_pack(fmaxf(__uint_as_float(u4_get(v[t], c)), low), fmaxf(__uint_as_float(u4_get(v[t], c + 1)), low));
+                }
+                const f32x2 arg = f2_fma(x, s2, off);
+                float p, q;
+                f2_unpack(arg, p, q);
+                const f32x2 e = f2_pack(ex2_approx(p), ex2_approx(q));
+                z2 = f2_add(z2, e);
+                w2 = f2_fma(e, arg, w2);
+            }
+    }
     float z0, z1, w0, w1;
     f2_unpack(z2, z0, z1);
     f2_unpack(w2, w0, w1);
-    const float zs = warp_sum(z0 + z1), ws = warp_sum(w0 + w1);
-    const float r = direct ? 0.f : fmaf(m, s, -ms);
-    const float f = direct ? 1.f : exp2f(-r);
-    *Z = zs * f;
-    *W = ws * f - r * (zs * f);
+    const float f = r == 0.f ? 1.f : exp2f(-r);
+    const float zs = warp_sum(z0 + z1) * f;
+    *Z = zs;
+    *W = warp_sum(w0 + w1) * f - r * zs;
 }
 
-// The chunk's candidates for the row's top KC: as warp_topk_chunk
-// (sv_stream.cuh), with elements outside the row (index below 0 or from V on)
-// left out.  thr is a lower bound of the row's KC-th largest logit.
-template <int ELT, int KC>
-__device__ __forceinline__ void chunk_candidates(const uint4 (&v)[kVecPerLane], const unsigned char* chunk, int base,
-                                                 int V, float2* out, float& thr, bool have_thr) {
-    const int lane = threadIdx.x & 31;
-    constexpr int PV = 16 / ELT;
-    constexpr int KS = topk_slots(KC);
-    if (!have_thr) {                                           // warp-uniform
-        float x = lane_max<ELT>(v);
-        thr = kNegInf;
-#pragma unroll
-        for (int r = 0; r < KC; ++r) {
-            thr = warp_max(x);
-            const unsigned own = __ballot_sync(0xffffffffu, x == thr);
-            if (lane == __ffs(own) - 1) x = kNegInf;
-        }
-    }
-    unsigned long long mask = 0ull;
-    if constexpr (ELT == 2) {
-        const uint32_t tb = __float_as_uint(thr) >> 16;        // a logit of the row or -inf: exact in bf16
-        const uint32_t t2 = tb | (tb << 16);
-        uint32_t lo = 0u, hi = 0u;
-#pragma unroll
-        for (int t = 0; t < kVecPerLane; ++t) {
-            const uint32_t b = vec_ge_bits_bf16(v[t], t2);
-            if (t < 4) lo |= b << (8 * t);
-            else hi |= b << (8 * (t - 4));
-        }
-        mask = (unsigned long long)hi << 32 | lo;
-    } else {
-#pragma unroll
-        for (int t = 0; t < kVecPerLane; ++t)
-            if (vec_max_value<ELT>(vec_max_bits<ELT>(v[t])) >= thr) {
-                unsigned bits = 0u;
-#pragma unroll
-                for (int e = 0; e < PV; ++e) bits |= (__uint_as_float(u4_get(v[t], e)) >= thr ? 1u : 0u) << e;
-                mask |= (unsigned long long)bits << (8 * t);
-            }
-    }
-    if (base < 0 || base + 32 * kLaneBytes / ELT > V) {        // warp-uniform: elements that are not the row's
-#pragma unroll 1
-        for (unsigned long long left = mask; left; left &= left - 1ull) {
-            const int bit = __ffsll((long long)left) - 1;
-            const int j = base + (lane + 32 * (bit >> 3)) * PV + (bit & 7);
-            if (j < 0 || j >= V) mask &= ~(1ull << bit);
-        }
-    }
-    const int n = __popcll(mask);
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    auto element = [&](int bit, float* y, int* j) {
-        const int t = bit >> 3, e = bit & 7;
-        const int off = (lane + 32 * t) * 16 + e * ELT;
-        if constexpr (ELT == 4) *y = *reinterpret_cast<const float*>(chunk + off);
-        else *y = __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(chunk + off) << 16);
-        *y += 0.0f;                                            // -0.0 counts as +0.0
-        *j = base + (lane + 32 * t) * PV + e;
-    };
-    if (total <= KS) {                                         // warp-uniform, nearly always
-        int slot = incl - n;
-#pragma unroll 1
-        for (; mask; mask &= mask - 1ull) {
-            float y;
-            int j;
-            element(__ffsll((long long)mask) - 1, &y, &j);
-            out[slot++] = make_float2(y, __int_as_float(j));
-        }
-        if (lane >= total && lane < KS) out[lane] = make_float2(kNegInf, __int_as_float(0x7fffffff));
-        return;
-    }
-    TopList<KC> L;
-    L.init();
-#pragma unroll 1
-    for (; mask; mask &= mask - 1ull) {
-        float y;
-        int j;
-        element(__ffsll((long long)mask) - 1, &y, &j);
-        L.insert(y, j);
-    }
-    float ov[KC];
-    int oi[KC];
-    warp_merge_topk<KC>(L, ov, oi);
-    if (lane == 0)
-#pragma unroll
-        for (int r = 0; r < KC; ++r) out[r] = make_float2(ov[r], __int_as_float(oi[r]));
-    if (lane >= KC && lane < KS) out[lane] = make_float2(kNegInf, __int_as_float(0x7fffffff));
-    thr = fmaxf(thr, ov[KC - 1]);
-}
-
-template <int ELT, int KC>
+template <int ELT>
 __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const LogprobArgs a) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    __shared__ int4 stage_info[kStages];                       // row, segment, lead, span a stage holds
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps);
-        }
-        mbar_init_fence();
-    }
-    __syncthreads();
     unsigned c0, c1;
     cta_range((unsigned)a.chunks, blockIdx.x, gridDim.x, &c0, &c1);
-    pdl_trigger();
-    pdl_wait();
     const long long tensor_bytes = (long long)a.rows * a.V * ELT;
     // bytes of chunk (r, seg): those that the span still has, and the whole
     // vectors of them that lie inside the tensor
@@ -215,6 +131,24 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
         const long long whole = (tensor_bytes & ~15LL) - *begin;       // whole vectors left in the tensor
         *copied = (int)max(0LL, min((long long)((*span + 15) & ~15), whole));
     };
+    if (threadIdx.x == 0) {
+        // the first chunks into L2 while the kernel before ends (as in sv_stream.cuh)
+        if (a.chunks >= kPrefetchMinChunks)
+            for (unsigned c = c0; c < c1 && c < c0 + kPrefetchChunks; ++c) {
+                long long begin;
+                int lead, span, copied;
+                extent((int)(c / (unsigned)a.nseg), (int)(c % (unsigned)a.nseg), &begin, &lead, &span, &copied);
+                if (copied > 0) bulk_prefetch_l2(a.z + begin, (uint32_t)copied);
+            }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -227,7 +161,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
                 if (it >= kStages && !wait_bounded(&empty[st], (it / kStages - 1) & 1u, a.wait_limit)) { ok = false; break; }
                 long long begin;
                 int lead, span, copied;
-                extent((int)(c / (unsigned)a.nseg), (int)(c % (unsigned)a.nseg), &begin, &lead, &span, &copied);
+                const int r = (int)(c / (unsigned)a.nseg), seg = (int)(c - (unsigned)r * (unsigned)a.nseg);
+                extent(r, seg, &begin, &lead, &span, &copied);
+                stage_info[st] = make_int4(r, seg, lead, span);
                 mbar_arrive_expect_tx(&full[st], (uint32_t)copied);
                 if (copied > 0) bulk_g2s(ring + (size_t)st * kStageBytes, a.z + begin, (uint32_t)copied, &full[st], policy);
             }
@@ -243,19 +179,14 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
         return;
     }
     const int cw = warp - 1;
-    unsigned tk_row = 0xffffffffu;
-    float tk_thr = kNegInf;
     bool ok = true;
     for (unsigned c = c0; c < c1; ++c) {
         const unsigned it = c - c0;
         const int st = (int)(it % kStages);
         if (!wait_bounded(&full[st], (it / kStages) & 1u, a.wait_limit)) ok = false;
         if (!__all_sync(0xffffffffu, ok)) break;
-        const unsigned r = c / (unsigned)a.nseg;
-        const int seg = (int)(c - r * (unsigned)a.nseg);
-        long long begin;
-        int lead, span, copied;
-        extent((int)r, seg, &begin, &lead, &span, &copied);
+        const int4 info = stage_info[st];
+        const int r = info.x, seg = info.y, lead = info.z, span = info.w;
         const int wb = span - cw * (32 * kLaneBytes);          // the warp chunk's bytes
         const size_t pi = ((size_t)r * a.nseg + seg) * kWarps + cw;
         float m = kNegInf, Z = 0.f, W = 0.f;
@@ -264,6 +195,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
             const int base = (seg * kStageBytes + cw * (32 * kLaneBytes)) / ELT - lead;
             if (base < 0 || base + 32 * kLaneBytes / ELT > a.V) {
                 // the tensor's last, partial vector; then the neighbours' elements
+                long long begin;
+                int l_, s_, copied;
+                extent(r, seg, &begin, &l_, &s_, &copied);
                 const int have = copied - cw * (32 * kLaneBytes);
                 const int e0 = max(0, have) / ELT, e1 = min(wb, 32 * kLaneBytes) / ELT;
                 for (int e = e0 + lane; e < e1; e += 32) {
@@ -290,13 +224,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
             uint4 v[kVecPerLane];
             lane_words<ELT>(chunk, wb, v);
             m = warp_max(lane_max<ELT>(v));
-            if (m != kNegInf) chunk_sums<ELT>(v, m, a.s, &Z, &W);
-            if constexpr (KC > 0) {
-                chunk_candidates<ELT, KC>(v, chunk, base, a.V, a.cand + pi * topk_slots(KC), tk_thr, tk_row == r);
-                tk_row = r;
-            }
-        } else if constexpr (KC > 0) {
-            if (lane < topk_slots(KC)) a.cand[pi * topk_slots(KC) + lane] = make_float2(kNegInf, __int_as_float(0x7fffffff));
+            if (m != kNegInf) chunk_sums<ELT>(v, m, a.s, a.inv_s, &Z, &W);
         }
         __syncwarp();
         if (lane == 0) {
@@ -307,18 +235,43 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
     if (!ok && lane == 0) atomicOr(a.err, SPEC_DEVERR_TIMEOUT);
 }
 
+// The first K of warp_merge_topk (sv_stream.cuh); the other entries say none.
+template <int KC>
+__device__ __forceinline__ void merge_lists(TopList<KC>& L, int K, float (&ov)[KC], int (&oi)[KC]) {
+#pragma unroll
+    for (int r = 0; r < KC; ++r) {
+        float hv = kNegInf;
+        int hi = 0x7fffffff;
+        if (r < K) {                                           // uniform
+            hv = L.v[0];
+            hi = L.i[0];
+            warp_argmax(hv, hi);
+            if (L.i[0] == hi && hi != 0x7fffffff) {
+#pragma unroll
+                for (int k = 0; k < KC - 1; ++k) { L.v[k] = L.v[k + 1]; L.i[k] = L.i[k + 1]; }
+                L.v[KC - 1] = kNegInf;
+                L.i[KC - 1] = 0x7fffffff;
+            }
+        }
+        ov[r] = hv;
+        oi[r] = hi;
+    }
+}
+
 // One CTA per row.
-template <int ELT, int KC>
+template <int ELT, bool LISTS>
 __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const LogprobArgs a) {
-    constexpr int NW = kMergeThreads / 32;
+    constexpr int NW = kMergeThreads / 32, KC = kMaxAlternatives, PV = 16 / ELT;
     __shared__ float red[3][NW];
-    __shared__ float2 pool[kMergePool];
-    __shared__ int pool_n;
-    __shared__ float best_v[NW];
-    __shared__ int best_i[NW];
+    __shared__ int keys[NW][KC];
+    __shared__ float list_v[NW][KC];
+    __shared__ int list_i[NW][KC];
+    __shared__ int thr_key, n_sel;
+    __shared__ __align__(16) unsigned char chunks[LISTS ? NW : 1][32 * kLaneBytes];    // a warp's chunk
+    extern __shared__ unsigned short sel[];                    // chunks that reach the bound
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x;
-    if (threadIdx.x == 0) pool_n = 0;
+    if (threadIdx.x == 0) n_sel = 0;
     pdl_wait();
     const int P = a.nseg * kWarps;
     const int tok = __ldg(a.tok + r);
@@ -326,18 +279,34 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
     float zx = kNegInf;
     if (threadIdx.x == 0 && tok_ok) zx = load_logit<ELT>(a.z + (size_t)r * a.V * ELT, tok);
 
+    // ---- the chunks' sums at the row's maximum
     const float4* st = a.stats + (size_t)r * P;
-    float M = kNegInf;
-    for (int i = threadIdx.x; i < P; i += kMergeThreads) M = fmaxf(M, __ldcg(st + i).x);
+    float4 first = make_float4(kNegInf, 0.f, 0.f, 0.f);        // the thread's first chunk stays at hand
+    if ((int)threadIdx.x < P) first = __ldcg(st + threadIdx.x);
+    float M = first.x;
+    for (int i = threadIdx.x + kMergeThreads; i < P; i += kMergeThreads) M = fmaxf(M, __ldcg(st + i).x);
+    const float mine = M;
     M = warp_max(M);
     if (lane == 0) red[0][warp] = M;
+    if constexpr (LISTS) {
+        // each warp's K largest thread maxima
+        int k = ord_key(mine);
+#pragma unroll
+        for (int q = 0; q < KC; ++q) {
+            if (q >= a.K) break;
+            const int top = __reduce_max_sync(0xffffffffu, k);
+            const unsigned own = __ballot_sync(0xffffffffu, k == top);
+            if (lane == __ffs(own) - 1) k = kNoKey;
+            if (lane == 0) keys[warp][q] = top;
+        }
+    }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, red[0][w]);
     const bool empty = M == kNegInf;
     float Z = 0.f, W = 0.f;
     for (int i = threadIdx.x; i < P; i += kMergeThreads) {
-        const float4 q = __ldcg(st + i);
+        const float4 q = i == (int)threadIdx.x ? first : __ldcg(st + i);
         if (q.x == kNegInf) continue;
         const float d = fmaxf((q.x - M) * a.s, kArgFloor);
         const float f = ex2_approx(d);
@@ -347,6 +316,21 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
     Z = warp_sum(Z);
     W = warp_sum(W);
     if (lane == 0) { red[1][warp] = Z; red[2][warp] = W; }
+    if constexpr (LISTS) {
+        if (warp == 0) {
+            // the K-th largest of the warps' lists, an entry a lane
+            static_assert(NW * KC == 32, "an entry a lane");
+            int k = (lane & (KC - 1)) < a.K ? keys[lane / KC][lane & (KC - 1)] : kNoKey, t = kNoKey;
+#pragma unroll
+            for (int q = 0; q < KC; ++q) {
+                if (q >= a.K) break;
+                t = __reduce_max_sync(0xffffffffu, k);
+                const unsigned own = __ballot_sync(0xffffffffu, k == t);
+                if (lane == __ffs(own) - 1) k = kNoKey;
+            }
+            if (lane == 0) thr_key = t;
+        }
+    }
     __syncthreads();
     Z = W = 0.f;
 #pragma unroll
@@ -358,107 +342,159 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
         if (empty) atomicOr(a.err, SPEC_DEVERR_EMPTY_ROW);
         if (!tok_ok) atomicOr(a.err, SPEC_DEVERR_TOKEN_RANGE);
     }
-    if constexpr (KC > 0) {
-        // A lower bound of the KC-th largest: the KC-th largest thread maximum
-        // of any one warp.
-        const int n = P * topk_slots(KC);
-        const float2* ca = a.cand + (size_t)r * n;
-        float x = kNegInf;
-        for (int i = threadIdx.x; i < n; i += kMergeThreads) x = fmaxf(x, __ldcg(ca + i).x);
-        int k = ord_key(x), t = kNoKey;
-#pragma unroll
-        for (int q = 0; q < KC; ++q) {
-            t = __reduce_max_sync(0xffffffffu, k);
-            const unsigned own = __ballot_sync(0xffffffffu, k == t);
-            if (lane == __ffs(own) - 1) k = kNoKey;
+    if constexpr (LISTS) {
+        // ---- the chunks that reach the bound, a warp each; every lane keeps the
+        // best of its logits
+        float thr = thr_key == kNoKey ? kNegInf : key_value(thr_key);
+        for (int i = threadIdx.x; i < P; i += kMergeThreads) {
+            const float m = i == (int)threadIdx.x ? first.x : __ldcg(st + i).x;
+            if (m >= thr && (m > kNegInf || !empty)) sel[atomicAdd(&n_sel, 1)] = (unsigned short)i;
         }
-        if (lane == 0) best_v[warp] = key_value(t);
         __syncthreads();
-        float thr = best_v[0];
+        const int n = empty ? 0 : n_sel;
+        long long begin, bytes;
+        int lead;
+        row_span(a, ELT, r, &begin, &lead, &bytes);
+        const long long tensor_bytes = (long long)a.rows * a.V * ELT;
+        TopList<KC> L;
+        L.init();
+        for (int c = warp; c < n; c += NW) {
+            const long long at = (long long)sel[c] * (32 * kLaneBytes);       // the chunk's place in the span
+            if (at >= bytes) continue;                         // warp-uniform: an empty chunk
+            const int base = (int)(at / ELT) - lead;
+            uint4 v[kVecPerLane];
+            unsigned have = 0u;                                // whole vectors of the row's span
 #pragma unroll
-        for (int w = 1; w < NW; ++w) thr = fmaxf(thr, best_v[w]);
-        for (int i = threadIdx.x; i < n; i += kMergeThreads) {
-            const float2 e = __ldcg(ca + i);
-            if (e.x >= thr && __float_as_int(e.y) != 0x7fffffff) {
-                const int at = atomicAdd(&pool_n, 1);
-                if (at < kMergePool) pool[at] = e;
+            for (int t = 0; t < kVecPerLane; ++t) {
+                const long long o = begin + at + (lane + 32 * t) * 16;
+                const bool in = o + 16 <= tensor_bytes && o < begin + bytes;   // (the tensor's last, partial one is read by element)
+                v[t] = in ? ld_stream16(a.z + o) : make_uint4(0u, 0u, 0u, 0u);
+                have |= (unsigned)in << t;
             }
-        }
-        __syncthreads();
-        const int total = pool_n;
-        auto put = [&](int q, float v, int j) {
-            const bool none = j == 0x7fffffff || empty;
-            a.ti[(size_t)r * a.K + q] = none ? -1 : j;
-            a.tl[(size_t)r * a.K + q] = empty ? CUDART_NAN_F : none ? kNegInf : (v - M) / a.T - lnz;
-        };
-        if (total <= kMergePool) {
-            if (warp == 0) {
-                const float2 e = lane < total ? pool[lane] : make_float2(kNegInf, 0.f);
-                int ck = lane < total ? ord_key(e.x) : kNoKey;
-                const unsigned ci = lane < total ? (unsigned)__float_as_int(e.y) : 0x7fffffffu;
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < kVecPerLane; ++t) *reinterpret_cast<uint4*>(&chunks[warp][(lane + 32 * t) * 16]) = v[t];
+            // the lane's elements of the row, as bits 8 t + e
+            unsigned long long row = 0ull;
+#pragma unroll
+            for (int t = 0; t < kVecPerLane; ++t) {
+                const int j = base + (lane + 32 * t) * PV;     // the vector's elements are j .. j + PV - 1
+                unsigned bits = (1u << PV) - 1u;
+                if (j < 0) bits = j <= -PV ? 0u : bits << -j & bits;
+                if (j + PV > a.V) bits = j >= a.V ? 0u : bits & ((1u << (a.V - j)) - 1u);
+                if ((have >> t) & 1u) row |= (unsigned long long)bits << (8 * t);
+            }
+            auto value = [&](int bit) {
+                const unsigned char* p = &chunks[warp][(lane + 32 * (bit >> 3)) * 16 + (bit & 7) * ELT];
+                if constexpr (ELT == 4) return *reinterpret_cast<const float*>(p);
+                else return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
+            };
+            auto reach = [&](float bound) {                     // those that reach a bound
+                unsigned long long mask = 0ull;
+#pragma unroll
+                for (int t = 0; t < kVecPerLane; ++t) {
+                    if (vec_max_value<ELT>(vec_max_bits<ELT>(v[t])) >= bound) {
+#pragma unroll
+                        for (int e = 0; e < PV; ++e) {
+                            float x;
+                            if constexpr (ELT == 4) x = __uint_as_float(u4_get(v[t], e));
+                            else x = (e & 1) ? bf16_hi(u4_get(v[t], e >> 1)) : bf16_lo(u4_get(v[t], e >> 1));
+                            if (x >= bound) mask |= 1ull << (8 * t + e);
+                        }
+                    }
+                }
+                return mask & row;
+            };
+            unsigned long long mask = reach(thr);
+            if (__reduce_add_sync(0xffffffffu, (unsigned)__popcll(mask)) > 24u) {
+                // many: the K-th largest of the lanes' maxima is a bound too
+                float x = kNegInf;
+#pragma unroll
+                for (int t = 0; t < kVecPerLane; ++t)
+#pragma unroll
+                    for (int e = 0; e < PV; ++e) {
+                        float y;
+                        if constexpr (ELT == 4) y = __uint_as_float(u4_get(v[t], e));
+                        else y = (e & 1) ? bf16_hi(u4_get(v[t], e >> 1)) : bf16_lo(u4_get(v[t], e >> 1));
+                        if ((mask >> (8 * t + e)) & 1ull) x = fmaxf(x, y);
+                    }
+                int k = mask ? ord_key(x) : kNoKey, t = kNoKey;
 #pragma unroll
                 for (int q = 0; q < KC; ++q) {
-                    const int kk = __reduce_max_sync(0xffffffffu, ck);
-                    const unsigned j = kk == kNoKey ? 0x7fffffffu : __reduce_min_sync(0xffffffffu, ck == kk ? ci : 0x7fffffffu);
-                    if (lane == 0 && q < a.K) put(q, key_value(kk), (int)j);
-                    if (ck == kk && ci == j) ck = kNoKey;
+                    if (q >= a.K) break;
+                    t = __reduce_max_sync(0xffffffffu, k);
+                    const unsigned own = __ballot_sync(0xffffffffu, k == t);
+                    if (lane == __ffs(own) - 1) k = kNoKey;
+                }
+                if (t != kNoKey) thr = fmaxf(thr, key_value(t));
+                mask = reach(thr);
+            }
+            const long long tail = tensor_bytes & ~15LL;       // elements from here on are read one by one
+            if (begin + at + 32 * kLaneBytes > tail && begin + bytes > tail) {
+                for (long long o = tail + lane * ELT; o < tensor_bytes; o += 32 * ELT) {
+                    const int j = (int)((o - begin) / ELT) - lead;
+                    if (o >= begin + at && j >= 0 && j < a.V) {
+                        const float x = load_logit<ELT>(a.z + (size_t)r * a.V * ELT, j) + 0.0f;
+                        if (x >= thr) L.insert(x, j);
+                    }
                 }
             }
-            return;
-        }
-        // many equal logits: K rounds over all candidates, each taking the best
-        // one after the last
-        float lv = 0.f;
-        int li = -1;
-        for (int q = 0; q < a.K; ++q) {
-            float bv = kNegInf;
-            int bi = 0x7fffffff;
-            for (int i = threadIdx.x; i < n; i += kMergeThreads) {
-                const float2 e = __ldcg(ca + i);
-                const int j = __float_as_int(e.y);
-                if (j != 0x7fffffff && (li < 0 || am_better(lv, li, e.x, j)) && am_better(e.x, j, bv, bi)) { bv = e.x; bi = j; }
+#pragma unroll 1
+            for (; mask; mask &= mask - 1ull) {
+                const int bit = __ffsll((long long)mask) - 1;
+                L.insert(value(bit) + 0.0f, base + (lane + 32 * (bit >> 3)) * PV + (bit & 7));
             }
-            warp_argmax(bv, bi);
-            __syncthreads();
-            if (lane == 0) { best_v[warp] = bv; best_i[warp] = bi; }
-            __syncthreads();
+        }
+        float ov[KC];
+        int oi[KC];
+        merge_lists<KC>(L, a.K, ov, oi);
+        if (lane == 0) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                if (am_better(best_v[w], best_i[w], bv, bi)) { bv = best_v[w]; bi = best_i[w]; }
-            if (threadIdx.x == 0) put(q, bv, bi);
-            lv = bv;
-            li = bi;
-            if (bi == 0x7fffffff) li = 0x7ffffffe;             // none left
+            for (int q = 0; q < KC; ++q) { list_v[warp][q] = ov[q]; list_i[warp][q] = oi[q]; }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            L.init();
+            L.insert(list_v[lane / KC][lane & (KC - 1)], list_i[lane / KC][lane & (KC - 1)]);
+            merge_lists<KC>(L, a.K, ov, oi);
+            if (lane == 0) {
+#pragma unroll
+                for (int q = 0; q < KC; ++q)
+                    if (q < a.K) {
+                        const bool none = oi[q] == 0x7fffffff || empty;
+                        a.ti[(size_t)r * a.K + q] = none ? -1 : oi[q];
+                        a.tl[(size_t)r * a.K + q] = empty ? CUDART_NAN_F : none ? kNegInf : (ov[q] - M) / a.T - lnz;
+                    }
+            }
         }
     }
 }
-
-static int list_len(int K) { return K <= 0 ? 0 : topk_list_len(K); }
 
 static int logprob_nseg(int V, int elt) {
     return (int)(((long long)V * elt + (16 - elt) + kStageBytes - 1) / kStageBytes);
 }
 
 size_t logprobs_workspace_size(int rows, int V, int K) {
-    // error word, then for every warp chunk (fp32 has the most) its sums and candidates
-    const size_t chunks = (size_t)rows * (size_t)logprob_nseg(V, 4) * kWarps;
-    return 256 + align256(chunks * sizeof(float4)) + align256(chunks * topk_slots(list_len(K)) * sizeof(float2));
+    // error word, then the sums of every warp chunk (fp32 has the most)
+    return 256 + align256((size_t)rows * (size_t)logprob_nseg(V, 4) * kWarps * sizeof(float4));
 }
 
-template <int ELT, int KC>
-static cudaError_t launch_logprobs_t(const LogprobArgs& a, const DeviceInfo& di, cudaStream_t st) {
-    auto kfn = logprob_stream_kernel<ELT, KC>;
+template <int ELT>
+static cudaError_t launch_logprobs_e(const LogprobArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    auto kfn = logprob_stream_kernel<ELT>;
+    auto merge = a.K > 0 ? logprob_merge_kernel<ELT, true> : logprob_merge_kernel<ELT, false>;
     const int smem = kStages * kStageBytes;
     static DeviceSlots slots = {};
     int occ = 0;
     cudaError_t e = device_once(slots, &occ, [&](int, int* o) {
         cudaError_t r = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (r != cudaSuccess) return r;
-        r = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        if (r != cudaSuccess) return r;
-        r = cudaFuncSetAttribute(logprob_merge_kernel<ELT, KC>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared);
-        if (r != cudaSuccess) return r;
+        // the whole carveout as shared memory for all of them, so that an SM can
+        // hold the merge's CTAs beside the stream's
+        for (const void* f : {(const void*)kfn, (const void*)logprob_merge_kernel<ELT, true>, (const void*)logprob_merge_kernel<ELT, false>}) {
+            r = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            if (r != cudaSuccess) return r;
+        }
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(o, kfn, kRingThreads, smem);
     });
     if (e != cudaSuccess) return e;
@@ -466,17 +502,8 @@ static cudaError_t launch_logprobs_t(const LogprobArgs& a, const DeviceInfo& di,
     if (a.chunks < g) g = a.chunks;
     e = launch_pdl(kfn, dim3((unsigned)g), kRingThreads, smem, st, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(logprob_merge_kernel<ELT, KC>, dim3((unsigned)a.rows), kMergeThreads, 0, st, a);
-}
-
-template <int ELT>
-static cudaError_t launch_logprobs_e(const LogprobArgs& a, const DeviceInfo& di, cudaStream_t st) {
-    switch (list_len(a.K)) {
-        case 0: return launch_logprobs_t<ELT, 0>(a, di, st);
-        case 2: return launch_logprobs_t<ELT, 2>(a, di, st);
-        case 4: return launch_logprobs_t<ELT, 4>(a, di, st);
-        default: return launch_logprobs_t<ELT, 8>(a, di, st);
-    }
+    const size_t sel = a.K > 0 ? (size_t)a.nseg * kWarps * sizeof(unsigned short) : 0;
+    return launch_pdl(merge, dim3((unsigned)a.rows), kMergeThreads, sel, st, a);
 }
 
 cudaError_t launch_logprobs(const void* z, spec_dtype_t dt, const int32_t* tok, float T, int rows, int V, int K,
@@ -491,6 +518,7 @@ cudaError_t launch_logprobs(const void* z, spec_dtype_t dt, const int32_t* tok, 
     a.tok = tok;
     a.T = T;
     a.s = (float)(1.4426950408889634 / (double)T);
+    a.inv_s = (float)((double)T / 1.4426950408889634);
     a.rows = rows;
     a.V = V;
     a.K = K;
@@ -498,7 +526,6 @@ cudaError_t launch_logprobs(const void* z, spec_dtype_t dt, const int32_t* tok, 
     a.chunks = (long long)rows * a.nseg;
     a.err = reinterpret_cast<int*>(w);
     a.stats = reinterpret_cast<float4*>(w + 256);
-    a.cand = reinterpret_cast<float2*>(w + 256 + align256((size_t)a.chunks * kWarps * sizeof(float4)));
     a.lp = lp;
     a.ent = ent;
     a.ti = ti;

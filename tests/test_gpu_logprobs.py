@@ -94,6 +94,35 @@ def test_masked_logits(sv, f32):
     check(sv, z, tok, 8, 0.9)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+def test_rows_masked_with_the_lowest_value(sv, f32):
+    """Whole chunks, and whole rows, of the type's lowest finite value or beside -inf."""
+    V = 50000
+    z, tok = rows(13, 4, V, f32)
+    low = torch.finfo(z.dtype).min
+    z[0, 3000:] = low
+    z[1] = low
+    z[2] = low
+    z[2, ::2] = -math.inf
+    z[3, :-5] = -math.inf
+    check(sv, z, torch.tensor([5, 7, 1, V - 2], dtype=torch.int32), 8, 1.0)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_top_tokens_in_few_chunks_and_in_many(sv, f32):
+    """Sorted rows (all of the top in one chunk), rows of few values, and a long row."""
+    V = 100003
+    dt = torch.float32 if f32 else torch.bfloat16
+    z = torch.empty((4, V), dtype=dt)
+    z[0] = torch.linspace(-9, 9, V).to(dt)
+    z[1] = torch.linspace(9, -9, V).to(dt)
+    z[2] = (torch.arange(V) % 7).to(dt)
+    z[3] = torch.where(torch.arange(V) % 5000 == 4999, 3.0, -2.0).to(dt)
+    check(sv, z, torch.tensor([V - 1, 0, 6, 4999], dtype=torch.int32), 8, 1.0)
+    z, tok = rows(14, 2, 1500007, f32)
+    check(sv, z, tok, 7, 1.0)
+
+
 def test_large_logits_and_small_temperatures(sv):
     z, tok = rows(9, 4, 9001, True)
     check(sv, z + 1000.0, tok, 3, 1.0)

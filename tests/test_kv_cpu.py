@@ -121,7 +121,7 @@ def test_logprobs_refusals(lib):
         a = dict(ok, **kw)
         return f(*(a[n] for n in a), None)
     inv, mis = sv.SPEC_ERR_INVALID_ARG, sv.SPEC_ERR_MISALIGNED
-    for kw, status in ((dict(dt=2), sv.SPEC_ERR_UNSUPPORTED_DTYPE), (dict(rows=-1), inv), (dict(V=0), inv), (dict(K=9), inv),
+    for kw, status in ((dict(dt=2), sv.SPEC_ERR_UNSUPPORTED_DTYPE), (dict(rows=-1), inv), (dict(V=0), inv), (dict(V=(1 << 24) + 1), inv), (dict(K=9), inv),
                        (dict(K=-1), inv), (dict(T=0.0), inv), (dict(T=float("nan")), inv), (dict(z=None), inv), (dict(tok=None), inv),
                        (dict(lp=None), inv), (dict(ti=None), inv), (dict(tl=None), inv), (dict(ws=None), inv), (dict(z=FAKE + 2), mis),
                        (dict(ws=WS + 8), mis), (dict(wb=need - 1), sv.SPEC_ERR_WORKSPACE_TOO_SMALL), (dict(rows=0), sv.SPEC_OK)):
