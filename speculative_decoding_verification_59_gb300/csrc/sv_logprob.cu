@@ -258,20 +258,309 @@ __device__ __forceinline__ void merge_lists(TopList<KC>& L, int K, float (&ov)[K
     }
 }
 
-// One CTA per row.
+// Element e of a vector as a float.
+template <int ELT>
+__device__ __forceinline__ float vec_value(const uint4& q, int e) {
+    if constexpr (ELT == 4) return __uint_as_float(u4_get(q, e));
+    else return (e & 1) ? bf16_hi(u4_get(q, e >> 1)) : bf16_lo(u4_get(q, e >> 1));
+}
+
+// A warp's chunk of row r straight from memory, at byte `at` of the row's
+// span: what is not the row's reads as -inf.  row: the lane's elements of the row,
+// as bits 8 t + e.  Returns the row index of the chunk's first element.
+template <int ELT>
+__device__ __forceinline__ int load_chunk(const LogprobArgs& a, int r, long long at, uint4 (&v)[kVecPerLane],
+                                          unsigned long long& row) {
+    constexpr int PV = 16 / ELT;
+    const int lane = threadIdx.x & 31;
+    long long begin, bytes;
+    int lead;
+    row_span(a, ELT, r, &begin, &lead, &bytes);
+    const long long tensor_bytes = (long long)a.rows * a.V * ELT;
+    const int base = (int)(at / ELT) - lead;
+    const uint32_t ninf = ELT == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+    for (int t = 0; t < kVecPerLane; ++t) {
+        const long long o = begin + at + (lane + 32 * t) * 16;
+        v[t] = o + 16 <= tensor_bytes && o < begin + bytes ? ld_stream16(a.z + o) : make_uint4(ninf, ninf, ninf, ninf);
+    }
+    row = ~0ull;
+    if (ELT == 4) row = 0x0f0f0f0f0f0f0f0full;
+    if (base < 0 || base + 32 * kLaneBytes / ELT > a.V) {      // warp-uniform: the row's first or last chunk
+        row = 0ull;
+#pragma unroll
+        for (int t = 0; t < kVecPerLane; ++t) {
+            const int j = base + (lane + 32 * t) * PV;         // the vector's elements are j .. j + PV - 1
+            if (j >= a.V || j <= -PV) {
+                v[t] = make_uint4(ninf, ninf, ninf, ninf);
+                continue;
+            }
+            unsigned bits = (1u << PV) - 1u;
+            if (j < 0) bits &= bits << -j;
+            if (j + PV > a.V) bits &= (1u << (a.V - j)) - 1u;
+            row |= (unsigned long long)bits << (8 * t);
+            const bool whole = begin + at + (lane + 32 * t) * 16 + 16 <= tensor_bytes;
+            uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+#pragma unroll
+            for (int e = 0; e < PV; ++e) {
+                // (a vector that the tensor ends in is read by element)
+                uint32_t x = ELT == 4 ? 0xff800000u : 0xff80u;
+                if ((bits >> e) & 1u) {
+                    if (whole) {
+                        x = ELT == 4 ? w[e] : (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                    } else {
+                        const float f = load_logit<ELT>(a.z + (size_t)r * a.V * ELT, j + e);
+                        x = ELT == 4 ? __float_as_uint(f) : __float_as_uint(f) >> 16;
+                    }
+                }
+                if constexpr (ELT == 4) w[e] = x;
+                else w[e >> 1] = (w[e >> 1] & (0xffff0000u >> (16 * (e & 1)))) | x << (16 * (e & 1));
+            }
+            v[t] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    return base;
+}
+
+// The lane's logits of a chunk that reach a bound, as bits 8 t + e.
+template <int ELT>
+__device__ __forceinline__ unsigned long long reach(const uint4 (&v)[kVecPerLane], unsigned long long row, float bound) {
+    unsigned long long mask = 0ull;
+#pragma unroll
+    for (int t = 0; t < kVecPerLane; ++t) {
+        if (vec_max_value<ELT>(vec_max_bits<ELT>(v[t])) >= bound) {
+#pragma unroll
+            for (int e = 0; e < 16 / ELT; ++e)
+                if (vec_value<ELT>(v[t], e) >= bound) mask |= 1ull << (8 * t + e);
+        }
+    }
+    return mask & row;
+}
+
+// Calls take(value, row index) for the lane's marked logits.  room: 4 KB of
+// shared memory of the warp's own, where each lane reads back what it wrote.
+template <int ELT, typename F>
+__device__ __forceinline__ void each_marked(const uint4 (&v)[kVecPerLane], unsigned long long mask, int base, unsigned char* room, F take) {
+    constexpr int PV = 16 / ELT;
+    const int lane = threadIdx.x & 31;
+    if (mask == 0ull) return;
+#pragma unroll
+    for (int t = 0; t < kVecPerLane; ++t) *reinterpret_cast<uint4*>(room + (lane + 32 * t) * 16) = v[t];
+#pragma unroll 1
+    for (; mask; mask &= mask - 1ull) {
+        const int bit = __ffsll((long long)mask) - 1;
+        const unsigned char* p = room + (lane + 32 * (bit >> 3)) * 16 + (bit & 7) * ELT;
+        float x;
+        if constexpr (ELT == 4) x = *reinterpret_cast<const float*>(p);
+        else x = __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
+        take(x + 0.0f, base + (lane + 32 * (bit >> 3)) * PV + (bit & 7));      // -0.0 counts as +0.0
+    }
+}
+
+// The logits of a row that reach a lower bound of its K-th largest: K of them
+// and a few more as a rule, so that a lane each holds them all.
+constexpr int kPool = 32;
+struct Pool {
+    float v[kPool];
+    int i[kPool];
+    int n;
+};
+template <int ELT>
+__device__ __forceinline__ void pool_chunk(const uint4 (&v)[kVecPerLane], unsigned long long row, int base, float thr,
+                                           unsigned char* room, Pool& p) {
+    each_marked<ELT>(v, reach<ELT>(v, row, thr), base, room, [&](float x, int j) {
+        const int at = atomicAdd(&p.n, 1);
+        if (at < kPool) {
+            p.v[at] = x;
+            p.i[at] = j;
+        }
+    });
+}
+// The pool's first K in order (a warp; n <= kPool entries).
+__device__ __forceinline__ void pool_lists(const Pool& p, int n, int K, float (&ov)[kMaxAlternatives], int (&oi)[kMaxAlternatives]) {
+    const int lane = threadIdx.x & 31;
+    int ck = lane < n ? ord_key(p.v[lane]) : kNoKey;
+    const unsigned ci = lane < n ? (unsigned)p.i[lane] : 0x7fffffffu;
+#pragma unroll
+    for (int q = 0; q < kMaxAlternatives; ++q) {
+        ov[q] = kNegInf;
+        oi[q] = 0x7fffffff;
+        if (q < K) {                                           // uniform
+            const int t = __reduce_max_sync(0xffffffffu, ck);
+            const unsigned j = __reduce_min_sync(0xffffffffu, ck == t ? ci : 0x7fffffffu);
+            if (t != kNoKey) {
+                ov[q] = key_value(t);
+                oi[q] = (int)j;
+            }
+            if (ck == t && ci == j) ck = kNoKey;
+        }
+    }
+}
+
+// Where more reach it than a pool holds (many equal logits, one chunk above
+// all others): adds the chunk's logits that can be among the K largest to the
+// lane's list.  thr is raised when many reach it (the K-th largest of the lanes'
+// maxima is a bound too).
+template <int ELT>
+__device__ __forceinline__ void pick_chunk(const uint4 (&v)[kVecPerLane], unsigned long long row, int base, int K, float& thr,
+                                           unsigned char* room, TopList<kMaxAlternatives>& L) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long mask = reach<ELT>(v, row, thr);
+    if (__reduce_add_sync(0xffffffffu, (unsigned)__popcll(mask)) > 24u) {
+        int k = mask ? ord_key(lane_max<ELT>(v)) : kNoKey, t = kNoKey;
+#pragma unroll
+        for (int q = 0; q < kMaxAlternatives; ++q) {
+            if (q >= K) break;
+            t = __reduce_max_sync(0xffffffffu, k);
+            const unsigned own = __ballot_sync(0xffffffffu, k == t);
+            if (lane == __ffs(own) - 1) k = kNoKey;
+        }
+        if (t != kNoKey) thr = fmaxf(thr, key_value(t));
+        mask = reach<ELT>(v, row, thr);
+    }
+    each_marked<ELT>(v, mask, base, room, [&](float x, int j) { L.insert(x, j); });
+}
+
+// The row's results, by its CTA's first thread.
+__device__ __forceinline__ void put_row(const LogprobArgs& a, int r, bool empty, bool tok_ok, float zx, float M, float lnz,
+                                        float inner) {
+    a.lp[r] = empty || !tok_ok ? CUDART_NAN_F : (zx - M) / a.T - lnz;
+    if (a.ent) a.ent[r] = empty ? CUDART_NAN_F : fmaxf(0.f, lnz - kLn2f * inner);
+    if (empty) atomicOr(a.err, SPEC_DEVERR_EMPTY_ROW);
+    if (!tok_ok) atomicOr(a.err, SPEC_DEVERR_TOKEN_RANGE);
+}
+__device__ __forceinline__ void put_list(const LogprobArgs& a, int r, bool empty, float M, float lnz,
+                                         const float (&ov)[kMaxAlternatives], const int (&oi)[kMaxAlternatives]) {
+#pragma unroll
+    for (int q = 0; q < kMaxAlternatives; ++q)
+        if (q < a.K) {
+            const bool none = oi[q] == 0x7fffffff || empty;
+            a.ti[(size_t)r * a.K + q] = none ? -1 : oi[q];
+            a.tl[(size_t)r * a.K + q] = empty ? CUDART_NAN_F : none ? kNegInf : (ov[q] - M) / a.T - lnz;
+        }
+}
+
+// Short rows (up to kRowChunks warp chunks): one CTA does all of a row, its
+// chunks straight from memory, in one launch.  Through the ring, a 32 KB stage
+// carried one short row: 14714 rows of 1400 bf16 logits took 184 us.
+constexpr int kRowChunks = 16;
+constexpr int kRowWarps = 8;
+template <int ELT, bool LISTS>
+__global__ void __launch_bounds__(kRowWarps * 32) logprob_row_kernel(const LogprobArgs a, int chunks) {
+    constexpr int KC = kMaxAlternatives;
+    __shared__ float part[kRowWarps][3], lmax[kRowChunks][32]; // the lanes' maxima of every chunk
+    __shared__ Pool pool;
+    __shared__ float list_v[kRowWarps][KC];
+    __shared__ int list_i[kRowWarps][KC];
+    extern __shared__ __align__(16) unsigned char rooms[];
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5, r = blockIdx.x;
+    if (threadIdx.x == 0) pool.n = 0;
+    pdl_wait();
+    const int tok = __ldg(a.tok + r);
+    const bool tok_ok = (unsigned)tok < (unsigned)a.V;
+    float zx = kNegInf;
+    if (threadIdx.x == 0 && tok_ok) zx = load_logit<ELT>(a.z + (size_t)r * a.V * ELT, tok);
+    uint4 v[kVecPerLane];
+    unsigned long long row = 0ull;
+    int base = 0;
+    float M = kNegInf, Z = 0.f, W = 0.f;                       // the warp's
+    for (int c = warp; c < chunks; c += nw) {
+        base = load_chunk<ELT>(a, r, (long long)c * (32 * kLaneBytes), v, row);
+        const float lm = lane_max<ELT>(v), m = warp_max(lm);
+        if constexpr (LISTS) lmax[c][lane] = lm;
+        if (m == kNegInf) continue;                            // warp-uniform
+        float z, w;
+        chunk_sums<ELT>(v, m, a.s, a.inv_s, &z, &w);
+        // both at the larger maximum
+        const float top = fmaxf(M, m);
+        const float d0 = M == kNegInf ? kArgFloor : fmaxf((M - top) * a.s, kArgFloor), d1 = fmaxf((m - top) * a.s, kArgFloor);
+        const float f0 = ex2_approx(d0), f1 = ex2_approx(d1);
+        W = f0 * fmaf(d0, Z, W) + f1 * fmaf(d1, z, w);
+        Z = f0 * Z + f1 * z;
+        M = top;
+    }
+    if (lane == 0) { part[warp][0] = M; part[warp][1] = Z; part[warp][2] = W; }
+    __syncthreads();
+    // every warp brings the warps' sums together: a lane each
+    const float pm = lane < nw ? part[lane][0] : kNegInf;
+    M = warp_max(pm);
+    const bool empty = M == kNegInf;
+    const float d = pm == kNegInf ? kArgFloor : fmaxf((pm - M) * a.s, kArgFloor), f = ex2_approx(d);
+    Z = warp_sum(lane < nw ? f * part[lane][1] : 0.f);
+    W = warp_sum(lane < nw ? f * fmaf(d, part[lane][1], part[lane][2]) : 0.f);
+    const float lnz = logf(Z);
+    if (threadIdx.x == 0) put_row(a, r, empty, tok_ok, zx, M, lnz, W / Z);
+    if constexpr (LISTS) {
+        // The K-th largest of the lanes' maxima over all chunks (distinct logits, near
+        // the K-th largest of all) is the bound; every warp finds it.
+        float x = kNegInf;
+        for (int c = 0; c < chunks; ++c) x = fmaxf(x, lmax[c][lane]);
+        int k = ord_key(x), t = kNoKey;
+#pragma unroll
+        for (int q = 0; q < KC; ++q) {
+            if (q >= a.K) break;
+            t = __reduce_max_sync(0xffffffffu, k);
+            const unsigned own = __ballot_sync(0xffffffffu, k == t);
+            if (lane == __ffs(own) - 1) k = kNoKey;
+        }
+        float thr = key_value(t);                              // -inf when so many lanes hold nothing finite
+        const int last = warp + (chunks - 1 - warp) / nw * nw;   // the chunk that v still holds
+        unsigned char* room = rooms + warp * (32 * kLaneBytes);
+        for (int c = last; c >= 0 && !empty; c -= nw) {
+            if (!__any_sync(0xffffffffu, lmax[c][lane] >= thr)) continue;
+            if (c != last) base = load_chunk<ELT>(a, r, (long long)c * (32 * kLaneBytes), v, row);
+            pool_chunk<ELT>(v, row, base, thr, room, pool);
+        }
+        __syncthreads();
+        float ov[KC];
+        int oi[KC];
+        const int n = pool.n;
+        if (n <= kPool) {                                      // uniform
+            if (warp == 0) {
+                pool_lists(pool, n, a.K, ov, oi);
+                if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
+            }
+            return;
+        }
+        TopList<KC> L;
+        L.init();
+        for (int c = warp; c < chunks; c += nw) {
+            if (!__any_sync(0xffffffffu, lmax[c][lane] >= thr)) continue;
+            base = load_chunk<ELT>(a, r, (long long)c * (32 * kLaneBytes), v, row);
+            pick_chunk<ELT>(v, row, base, a.K, thr, room, L);
+        }
+        merge_lists<KC>(L, a.K, ov, oi);
+        if (nw > 1) {                                          // uniform
+            if (lane == 0) {
+#pragma unroll
+                for (int q = 0; q < KC; ++q) { list_v[warp][q] = ov[q]; list_i[warp][q] = oi[q]; }
+            }
+            __syncthreads();
+            if (warp > 0) return;
+            L.init();
+            for (int i = lane; i < nw * KC; i += 32) L.insert(list_v[i / KC][i & (KC - 1)], list_i[i / KC][i & (KC - 1)]);
+            merge_lists<KC>(L, a.K, ov, oi);
+        }
+        if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
+    }
+}
+
+// Long rows: one CTA per row, after the stream.
 template <int ELT, bool LISTS>
 __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const LogprobArgs a) {
-    constexpr int NW = kMergeThreads / 32, KC = kMaxAlternatives, PV = 16 / ELT;
+    constexpr int NW = kMergeThreads / 32, KC = kMaxAlternatives;
     __shared__ float red[3][NW];
     __shared__ int keys[NW][KC];
     __shared__ float list_v[NW][KC];
     __shared__ int list_i[NW][KC];
     __shared__ int thr_key, n_sel;
+    __shared__ Pool pool;
     __shared__ __align__(16) unsigned char chunks[LISTS ? NW : 1][32 * kLaneBytes];    // a warp's chunk
     extern __shared__ unsigned short sel[];                    // chunks that reach the bound
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x;
-    if (threadIdx.x == 0) n_sel = 0;
+    if (threadIdx.x == 0) n_sel = pool.n = 0;
     pdl_wait();
     const int P = a.nseg * kWarps;
     const int tok = __ldg(a.tok + r);
@@ -336,12 +625,7 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
 #pragma unroll
     for (int w = 0; w < NW; ++w) { Z += red[1][w]; W += red[2][w]; }
     const float lnz = logf(Z);
-    if (threadIdx.x == 0) {
-        a.lp[r] = empty || !tok_ok ? CUDART_NAN_F : (zx - M) / a.T - lnz;
-        if (a.ent) a.ent[r] = empty ? CUDART_NAN_F : fmaxf(0.f, lnz - kLn2f * (W / Z));
-        if (empty) atomicOr(a.err, SPEC_DEVERR_EMPTY_ROW);
-        if (!tok_ok) atomicOr(a.err, SPEC_DEVERR_TOKEN_RANGE);
-    }
+    if (threadIdx.x == 0) put_row(a, r, empty, tok_ok, zx, M, lnz, W / Z);
     if constexpr (LISTS) {
         // ---- the chunks that reach the bound, a warp each; every lane keeps the
         // best of its logits
@@ -352,101 +636,31 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
         }
         __syncthreads();
         const int n = empty ? 0 : n_sel;
-        long long begin, bytes;
-        int lead;
-        row_span(a, ELT, r, &begin, &lead, &bytes);
-        const long long tensor_bytes = (long long)a.rows * a.V * ELT;
+        for (int c = warp; c < n; c += NW) {
+            uint4 v[kVecPerLane];
+            unsigned long long row;
+            const int base = load_chunk<ELT>(a, r, (long long)sel[c] * (32 * kLaneBytes), v, row);
+            pool_chunk<ELT>(v, row, base, thr, chunks[warp], pool);
+        }
+        __syncthreads();
+        float ov[KC];
+        int oi[KC];
+        const int got = pool.n;
+        if (got <= kPool) {                                    // uniform
+            if (warp == 0) {
+                pool_lists(pool, got, a.K, ov, oi);
+                if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
+            }
+            return;
+        }
         TopList<KC> L;
         L.init();
         for (int c = warp; c < n; c += NW) {
-            const long long at = (long long)sel[c] * (32 * kLaneBytes);       // the chunk's place in the span
-            if (at >= bytes) continue;                         // warp-uniform: an empty chunk
-            const int base = (int)(at / ELT) - lead;
             uint4 v[kVecPerLane];
-            unsigned have = 0u;                                // whole vectors of the row's span
-#pragma unroll
-            for (int t = 0; t < kVecPerLane; ++t) {
-                const long long o = begin + at + (lane + 32 * t) * 16;
-                const bool in = o + 16 <= tensor_bytes && o < begin + bytes;   // (the tensor's last, partial one is read by element)
-                v[t] = in ? ld_stream16(a.z + o) : make_uint4(0u, 0u, 0u, 0u);
-                have |= (unsigned)in << t;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < kVecPerLane; ++t) *reinterpret_cast<uint4*>(&chunks[warp][(lane + 32 * t) * 16]) = v[t];
-            // the lane's elements of the row, as bits 8 t + e
-            unsigned long long row = 0ull;
-#pragma unroll
-            for (int t = 0; t < kVecPerLane; ++t) {
-                const int j = base + (lane + 32 * t) * PV;     // the vector's elements are j .. j + PV - 1
-                unsigned bits = (1u << PV) - 1u;
-                if (j < 0) bits = j <= -PV ? 0u : bits << -j & bits;
-                if (j + PV > a.V) bits = j >= a.V ? 0u : bits & ((1u << (a.V - j)) - 1u);
-                if ((have >> t) & 1u) row |= (unsigned long long)bits << (8 * t);
-            }
-            auto value = [&](int bit) {
-                const unsigned char* p = &chunks[warp][(lane + 32 * (bit >> 3)) * 16 + (bit & 7) * ELT];
-                if constexpr (ELT == 4) return *reinterpret_cast<const float*>(p);
-                else return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
-            };
-            auto reach = [&](float bound) {                     // those that reach a bound
-                unsigned long long mask = 0ull;
-#pragma unroll
-                for (int t = 0; t < kVecPerLane; ++t) {
-                    if (vec_max_value<ELT>(vec_max_bits<ELT>(v[t])) >= bound) {
-#pragma unroll
-                        for (int e = 0; e < PV; ++e) {
-                            float x;
-                            if constexpr (ELT == 4) x = __uint_as_float(u4_get(v[t], e));
-                            else x = (e & 1) ? bf16_hi(u4_get(v[t], e >> 1)) : bf16_lo(u4_get(v[t], e >> 1));
-                            if (x >= bound) mask |= 1ull << (8 * t + e);
-                        }
-                    }
-                }
-                return mask & row;
-            };
-            unsigned long long mask = reach(thr);
-            if (__reduce_add_sync(0xffffffffu, (unsigned)__popcll(mask)) > 24u) {
-                // many: the K-th largest of the lanes' maxima is a bound too
-                float x = kNegInf;
-#pragma unroll
-                for (int t = 0; t < kVecPerLane; ++t)
-#pragma unroll
-                    for (int e = 0; e < PV; ++e) {
-                        float y;
-                        if constexpr (ELT == 4) y = __uint_as_float(u4_get(v[t], e));
-                        else y = (e & 1) ? bf16_hi(u4_get(v[t], e >> 1)) : bf16_lo(u4_get(v[t], e >> 1));
-                        if ((mask >> (8 * t + e)) & 1ull) x = fmaxf(x, y);
-                    }
-                int k = mask ? ord_key(x) : kNoKey, t = kNoKey;
-#pragma unroll
-                for (int q = 0; q < KC; ++q) {
-                    if (q >= a.K) break;
-                    t = __reduce_max_sync(0xffffffffu, k);
-                    const unsigned own = __ballot_sync(0xffffffffu, k == t);
-                    if (lane == __ffs(own) - 1) k = kNoKey;
-                }
-                if (t != kNoKey) thr = fmaxf(thr, key_value(t));
-                mask = reach(thr);
-            }
-            const long long tail = tensor_bytes & ~15LL;       // elements from here on are read one by one
-            if (begin + at + 32 * kLaneBytes > tail && begin + bytes > tail) {
-                for (long long o = tail + lane * ELT; o < tensor_bytes; o += 32 * ELT) {
-                    const int j = (int)((o - begin) / ELT) - lead;
-                    if (o >= begin + at && j >= 0 && j < a.V) {
-                        const float x = load_logit<ELT>(a.z + (size_t)r * a.V * ELT, j) + 0.0f;
-                        if (x >= thr) L.insert(x, j);
-                    }
-                }
-            }
-#pragma unroll 1
-            for (; mask; mask &= mask - 1ull) {
-                const int bit = __ffsll((long long)mask) - 1;
-                L.insert(value(bit) + 0.0f, base + (lane + 32 * (bit >> 3)) * PV + (bit & 7));
-            }
+            unsigned long long row;
+            const int base = load_chunk<ELT>(a, r, (long long)sel[c] * (32 * kLaneBytes), v, row);
+            pick_chunk<ELT>(v, row, base, a.K, thr, chunks[warp], L);
         }
-        float ov[KC];
-        int oi[KC];
         merge_lists<KC>(L, a.K, ov, oi);
         if (lane == 0) {
 #pragma unroll
@@ -457,15 +671,7 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
             L.init();
             L.insert(list_v[lane / KC][lane & (KC - 1)], list_i[lane / KC][lane & (KC - 1)]);
             merge_lists<KC>(L, a.K, ov, oi);
-            if (lane == 0) {
-#pragma unroll
-                for (int q = 0; q < KC; ++q)
-                    if (q < a.K) {
-                        const bool none = oi[q] == 0x7fffffff || empty;
-                        a.ti[(size_t)r * a.K + q] = none ? -1 : oi[q];
-                        a.tl[(size_t)r * a.K + q] = empty ? CUDART_NAN_F : none ? kNegInf : (ov[q] - M) / a.T - lnz;
-                    }
-            }
+            if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
         }
     }
 }
@@ -481,6 +687,13 @@ size_t logprobs_workspace_size(int rows, int V, int K) {
 
 template <int ELT>
 static cudaError_t launch_logprobs_e(const LogprobArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    const int span = (int)(((long long)a.V * ELT + (16 - ELT) + 32 * kLaneBytes - 1) / (32 * kLaneBytes));     // warp chunks of a row
+    if (span <= kRowChunks) {
+        const int turns = (span + kRowWarps - 1) / kRowWarps, warps = (span + turns - 1) / turns;
+        const dim3 grid((unsigned)a.rows);
+        if (a.K == 0) return launch_pdl(logprob_row_kernel<ELT, false>, grid, warps * 32, 0, st, a, span);
+        return launch_pdl(logprob_row_kernel<ELT, true>, grid, warps * 32, (size_t)warps * 32 * kLaneBytes, st, a, span);
+    }
     auto kfn = logprob_stream_kernel<ELT>;
     auto merge = a.K > 0 ? logprob_merge_kernel<ELT, true> : logprob_merge_kernel<ELT, false>;
     const int smem = kStages * kStageBytes;
