@@ -436,6 +436,7 @@ spec_status_t spec_kv_append(const spec_kv_cache_t* cache, const void* q, const 
  * starts[b] + t (NULL: t) for t < counts[b] (NULL: T), zeros for the other
  * rows.  E4M3 entries are multiplied by their scale in fp32 and rounded once.
  * A bad sequence's rows are NaN, and so is the row of a bad page.
+ * T * kv_heads < 2^31.
  */
 spec_status_t spec_kv_read(const spec_kv_cache_t* cache, const int32_t* starts,
                            const int32_t* counts, int B, int T, spec_dtype_t out_dtype,

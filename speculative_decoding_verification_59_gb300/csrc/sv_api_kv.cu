@@ -88,7 +88,7 @@ spec_status_t spec_kv_read(const spec_kv_cache_t* cache, const int32_t* starts,
     if (B == 0 || T == 0) return SPEC_OK;
     const spec_status_t s = check_cache(cache);
     if (s != SPEC_OK) return s;
-    if (!out_k || !out_v || B > 65535) return SPEC_ERR_INVALID_ARG;
+    if (!out_k || !out_v || B > 65535 || (long long)T * cache->kv_heads >= (1LL << 31)) return SPEC_ERR_INVALID_ARG;
     if (!is_aligned(out_k, 16) || !is_aligned(out_v, 16)) return SPEC_ERR_MISALIGNED;
     return status_of(launch_kv_read(*cache, starts, counts, B, T, out_dtype == SPEC_DTYPE_F32, out_k, out_v, stream));
 }

@@ -162,77 +162,102 @@ struct ReadArgs {
     char *out_k, *out_v;
 };
 
-// A lane takes the same 8 elements of a position's key and of its value.
-// blockIdx.y is the sequence; the rows (position, head) run along x.
+// A lane takes the same 8 elements of a position's key and of its value, and
+// kReadRows rows (position, head) that lie a CTA's width apart, so that its
+// loads are all in flight before the first store and the index arithmetic is
+// shared.  blockIdx.y is the sequence; the rows run along x.  Outputs are
+// stored as data that is not read again soon.  64 x 2048 positions of 8 e4m3
+// heads of 128 as bf16 (0.75 GB): 112 us, 6.65 TB/s, 98 % of a plain copy's
+// rate; one row a lane with 64-bit divisions took 127 us, and 16 elements a
+// lane (whose two 16-byte stores fill half sectors) 130 us.
+constexpr int kReadRows = 2;
+
 template <int D, bool FP8, bool F32>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadArgs a) {
     pdl_trigger();
     pdl_wait();
-    constexpr int L = D / 8;
-    const long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x;
-    const int H = a.c.kv_heads;
-    const long long row = i / L;                              // (t, head)
-    if (row >= (long long)a.T * H) return;
-    const int lr = (int)(i % L), b = blockIdx.y;
-    const int t = (int)(row / H), head = (int)(row - (long long)t * H);
+    constexpr int E = 8, L = D / E, R = kKvThreads / L;       // elements of a lane, lanes of a row, rows abreast
+    const int H = a.c.kv_heads, lr = threadIdx.x % L, b = blockIdx.y;
+    const unsigned rows = (unsigned)a.T * H, row0 = blockIdx.x * (R * kReadRows) + threadIdx.x / L;
     const int start = a.starts ? __ldg(a.starts + b) : 0;
     const int count = a.counts ? __ldg(a.counts + b) : a.T;
-    const int cap = a.c.max_pages * a.c.page_size;
-    bool bad = start < 0 || count < 0 || count > a.T || start > cap - count;
-    float xk[8], xv[8];
+    const bool off = start < 0 || count < 0 || count > a.T || start > a.c.max_pages * a.c.page_size - count;
+    uint4 wk[kReadRows], wv[kReadRows];
+    float sk[kReadRows], sv_[kReadRows];
+    bool bad[kReadRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) xk[j] = xv[j] = 0.f;
-    if (!bad && t < count) {
+    for (int u = 0; u < kReadRows; ++u) {
+        const unsigned row = row0 + u * R;
+        const int t = (int)(row / (unsigned)H), head = (int)(row - (unsigned)t * H);
+        wk[u] = wv[u] = make_uint4(0, 0, 0, 0);
+        sk[u] = sv_[u] = 0.f;
+        bad[u] = off;
+        if (row >= rows || off || t >= count) continue;
         int page, slot;
         if (!cache_place(a.c, b, start + t, &page, &slot)) {
-            bad = true;
+            bad[u] = true;
+            continue;
+        }
+        const int64_t at = (entry_off(a.c, page, slot, head) + lr * E) * (FP8 ? 1 : 2);
+        if constexpr (!FP8) {
+            wk[u] = ld_stream16(static_cast<const char*>(a.c.k) + at);
+            wv[u] = ld_stream16(static_cast<const char*>(a.c.v) + at);
         } else {
-            const int64_t off = entry_off(a.c, page, slot, head) + lr * 8;
-            if constexpr (FP8) {
-                const uint2 wk = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.k) + off));
-                const uint2 wv = __ldg(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.v) + off));
-                const int64_t so = scale_off(a.c, page, slot, head);
-                const float sk = __ldg(a.c.k_scale + so), sv_ = __ldg(a.c.v_scale + so);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int sh = 16 * (j & 1);
-                    f16x2_to_f32(e4m3_to_f16x2((j < 2 ? wk.x : wk.y) >> sh), &xk[2 * j], &xk[2 * j + 1]);
-                    f16x2_to_f32(e4m3_to_f16x2((j < 2 ? wv.x : wv.y) >> sh), &xv[2 * j], &xv[2 * j + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) { xk[j] *= sk; xv[j] *= sv_; }
-            } else {
-                unpack8(ld_stream16(static_cast<const char*>(a.c.k) + 2 * off), xk);
-                unpack8(ld_stream16(static_cast<const char*>(a.c.v) + 2 * off), xv);
-            }
+            const uint2 k2 = __ldcs(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.k) + at));
+            const uint2 v2 = __ldcs(reinterpret_cast<const uint2*>(static_cast<const char*>(a.c.v) + at));
+            wk[u].x = k2.x; wk[u].y = k2.y;
+            wv[u].x = v2.x; wv[u].y = v2.y;
+            const int64_t so = scale_off(a.c, page, slot, head);
+            sk[u] = __ldg(a.c.k_scale + so);
+            sv_[u] = __ldg(a.c.v_scale + so);
         }
     }
-    if (bad) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xk[j] = xv[j] = CUDART_NAN_F;
-        if (lr == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
-    }
-    const size_t o = ((size_t)b * a.T * H + row) * D + lr * 8;
-    if constexpr (F32) {
-        float4* k4 = reinterpret_cast<float4*>(a.out_k) + o / 4;
-        float4* v4 = reinterpret_cast<float4*>(a.out_v) + o / 4;
-        k4[0] = make_float4(xk[0], xk[1], xk[2], xk[3]);
-        k4[1] = make_float4(xk[4], xk[5], xk[6], xk[7]);
-        v4[0] = make_float4(xv[0], xv[1], xv[2], xv[3]);
-        v4[1] = make_float4(xv[4], xv[5], xv[6], xv[7]);
-    } else {
-        reinterpret_cast<uint4*>(a.out_k)[o / 8] =
-            make_uint4(pack_bf16(xk[0], xk[1]), pack_bf16(xk[2], xk[3]), pack_bf16(xk[4], xk[5]), pack_bf16(xk[6], xk[7]));
-        reinterpret_cast<uint4*>(a.out_v)[o / 8] =
-            make_uint4(pack_bf16(xv[0], xv[1]), pack_bf16(xv[2], xv[3]), pack_bf16(xv[4], xv[5]), pack_bf16(xv[6], xv[7]));
+    for (int u = 0; u < kReadRows; ++u) {
+        const unsigned row = row0 + u * R;
+        if (row >= rows) return;
+        if (bad[u] && lr == 0) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
+        const size_t o = ((size_t)b * rows + row) * D + lr * E;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint4 w = kv ? wv[u] : wk[u];
+            char* out = (kv ? a.out_v : a.out_k) + o * (F32 ? 4 : 2);
+            float x[E];
+            if constexpr (FP8) {
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j)
+                    f16x2_to_f32(e4m3_to_f16x2(u4_get(w, j / 2) >> 16 * (j & 1)), &x[2 * j], &x[2 * j + 1]);
+                const float sc = kv ? sv_[u] : sk[u];
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[j] *= sc;
+            } else {
+                unpack8(w, x);
+            }
+            if (bad[u]) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[j] = CUDART_NAN_F;
+            }
+            if constexpr (F32) {
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j)
+                    __stcs(reinterpret_cast<float4*>(out) + j, make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < E / 8; ++j)
+                    __stcs(reinterpret_cast<uint4*>(out) + j,
+                           make_uint4(pack_bf16(x[8 * j], x[8 * j + 1]), pack_bf16(x[8 * j + 2], x[8 * j + 3]),
+                                      pack_bf16(x[8 * j + 4], x[8 * j + 5]), pack_bf16(x[8 * j + 6], x[8 * j + 7])));
+            }
+        }
     }
 }
 
 template <int D>
 static cudaError_t launch_read_t(const ReadArgs& a, int B, bool f32, cudaStream_t st) {
-    const long long n = (long long)a.T * a.c.kv_heads * (D / 8);
-    const dim3 grid((unsigned)((n + kKvThreads - 1) / kKvThreads), (unsigned)B);
-    if (a.c.dtype == SPEC_DTYPE_E4M3)
+    const bool fp8 = a.c.dtype == SPEC_DTYPE_E4M3;
+    const long long per = kKvThreads / (D / 8) * kReadRows;
+    const dim3 grid((unsigned)(((long long)a.T * a.c.kv_heads + per - 1) / per), (unsigned)B);
+    if (fp8)
         return f32 ? launch_pdl(kv_read_kernel<D, true, true>, grid, kKvThreads, 0, st, a)
                    : launch_pdl(kv_read_kernel<D, true, false>, grid, kKvThreads, 0, st, a);
     return f32 ? launch_pdl(kv_read_kernel<D, false, true>, grid, kKvThreads, 0, st, a)
