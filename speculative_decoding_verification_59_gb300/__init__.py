@@ -667,7 +667,7 @@ def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, work
     """Log-probabilities of tokens with entropies and top alternatives (see
     spec_token_logprobs).  logits [..., V] contiguous bfloat16 or float32, tokens [...]
     int32.  Returns (logprob [...], entropy [...], top_idx [..., K] int32, top_logprob
-    [..., K]); the last two None for K = 0.  workspace: a uint8 tensor of
+    [..., K]), which share one allocation; the last two None for K = 0.  workspace: a uint8 tensor of
     spec_logprobs_workspace_size() bytes, its first 256 zero (None: one kept for the
     device and stream)."""
     return (_marshal_module or _marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)
