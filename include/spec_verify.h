@@ -479,10 +479,9 @@ spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* conte
  * NaN.  What the masked entries of the cache hold does not matter, NaN and
  * infinities included.
  *
- * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned, its
- * first 4096 bytes zero-filled once.  Its counters are zero again after every
- * call, so it serves attention calls of any size in turn (and
- * replays of a captured one), but no other entry point may write to it.
+ * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned, of any
+ * contents.  Nothing is carried between calls, so calls of any size may use
+ * one in turn, but not at the same time.
  */
 size_t spec_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim);
 spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,

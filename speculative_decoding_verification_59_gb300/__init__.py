@@ -655,8 +655,8 @@ def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=N
     parents [B, N] int32 for draft trees (None: chains), new_lens [B] int32 or None; scale
     defaults to head_dim ** -0.5.  Returns out [B, N, q_heads, head_dim] bfloat16, with
     lse=True also [B, N, q_heads] float32.  workspace: a uint8 tensor of
-    spec_attention_workspace_size() bytes, its first 4096 zero, that only this call uses
-    (None: one kept for the device and stream)."""
+    spec_attention_workspace_size() bytes, of any contents, that no call on another stream
+    uses at the same time (None: one kept for the device and stream)."""
     return (_marshal_module or _marshal()).paged_attention(
         cache.addr, cache.batch, cache.index, q, context_lens, parents, new_lens,
         cache.scale if scale is None else scale, lse, out, workspace, stream)

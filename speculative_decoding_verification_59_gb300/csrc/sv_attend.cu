@@ -1,5 +1,5 @@
 // Attention of a few new positions per sequence over the paged cache, split
-// over the cache's length and joined in the same launch.
+// over the cache's length, and the join of what was split.
 //
 // out = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m), s_t = (scale log2 e) q.k_t,
 // with the running reference m of a one-pass softmax.  The rows of one cached
@@ -12,9 +12,8 @@
 // the device from the lengths (ragged batches balance, and a captured call
 // follows its lengths).  A share may end one unit and begin the next.  A unit
 // within one share is written at once; otherwise each CTA leaves its
-// unnormalised sum, reference and total in the workspace, and the last of
-// the unit's CTAs to arrive (a counter that it sets back to zero) adds them in
-// the order of the shares, whichever came last.
+// unnormalised sum, reference and total in the workspace, and a second small
+// kernel adds them in the order of the shares.
 //
 // Inside a CTA each of the four warps takes its own slice of every tile and
 // its own running softmax, so the warps never wait for one another while
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
     __shared__ unsigned long long anc[2][kMaxNewTree];         // ancestors and itself, by node
     __shared__ short up[2][kMaxNewTree];
     __shared__ float wm[kAttWarps][C::ROWS], wl[kAttWarps][C::ROWS];
-    __shared__ int wbad[kAttWarps], last_cta;
+    __shared__ int wbad[kAttWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = lane & 3, lrow = lane >> 2;
     pdl_trigger();
@@ -102,13 +101,15 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
     const int RT = a.N * a.G;                                  // rows of a cached head
     const int RB = (RT + C::ROWS - 1) / C::ROWS;
     make_plan<C::TILE, kAttThreads>(a, a.c.kv_heads * RB, gridDim.x, &plan);
-    if ((int)blockIdx.x >= plan.n) return;
     AttWalk walk;
-    walk.init(plan);
     AttUnit un;
+    if ((int)blockIdx.x >= plan.n) {
+        if (threadIdx.x == 0) note_split(a, plan, un);
+        return;
+    }
+    walk.init(plan);
     int anc_b = -1, tree_bad = 0;
     const float c2 = a.scale * kLog2e;
-    int* counters = reinterpret_cast<int*>(a.ws + 256);
     float* slots = reinterpret_cast<float*>(a.ws + kAttHead);
     const int srows = min(C::ROWS, RT);
     const size_t slot_floats = part_floats(srows, D);
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
             }
             if (bad) L = CUDART_NAN_F;
             if (whole) {
-                put_row(a, un, bad, D, r, d, x, L, M);
+                put_row(a, b, hk, r0, sl.nb, bad, D, r, d, x, L, M);
             } else {
                 __stcg(reinterpret_cast<float4*>(sp + (size_t)r * D + d), x);
                 if (d == 0) {
@@ -593,32 +594,140 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 }
             }
         }
-        if (!whole) {
-            // ---- the unit's CTAs: c0 begins it, c1 ends it; the last to arrive adds the parts
-            const int c0 = share_of(plan.total, plan.n, un.at), c1 = share_of(plan.total, plan.n, un.at + tiles - 1);
-            int* counter = counters + c0;                      // no CTA begins two units that others end
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                __threadfence();                               // the barrier put the CTA's writes before it
-                const int got = atomicAdd(counter, 1);
-                last_cta = got == c1 - c0;
-                if (last_cta) *counter = 0;                    // as the next call finds it
+    }
+    if (threadIdx.x == 0) note_split(a, plan, un);
+}
+
+// ---- the join -------------------------------------------------------------------
+// One row per `per` warps: each takes every per-th part, four at a time (their
+// loads under way together), with a running reference; the row's first warp then
+// adds the warps' sums in order.  blockIdx.x is the CTA that began the unit, so the
+// grid is the attention kernel's times the rows.
+// A launch of its own rather than the last CTA of a unit to arrive: that CTA was
+// alone with its unit's parts, behind a fence and a counter, and its code weighed on
+// the attention kernel's registers.  13 rows x 4 heads over 4749 positions in 38
+// parts: 53.0 us then, 18.4 now; 4 rows x 8 heads over 1000: 8.45 and 7.40; 512
+// units of 32 rows over up to 4096: 155.9 and 148.8.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int block_rows, int per) {
+    constexpr int W = kJoinThreads / 32, V = D / 32, U = 4;   // warps, elements of a lane, parts at a time
+    constexpr int VEC = V < 4 ? V : 4;
+    __shared__ __align__(16) float sum[W][D];
+    __shared__ float ref[W], tot[W];
+    pdl_trigger();
+    pdl_wait();
+    const int4* note = reinterpret_cast<const int4*>(a.ws + blockIdx.x * sizeof(AttSplit));
+    const int4 n0 = __ldcg(note), n1 = __ldcg(note + 1);       // parts, b, hk, r0; rows, nb
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * (W / per) + warp / per, w = warp % per;
+    if (n0.x == 0 || (int)blockIdx.y * (W / per) >= n1.x) return;   // CTA-uniform
+    const int srows = min(block_rows, a.N * a.G);
+    const size_t slot_floats = part_floats(srows, D);
+    const float* slots = reinterpret_cast<const float*>(a.ws + kAttHead);
+    float M = kNegInf, L = 0.f, v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
+    if (r < n1.x) {
+        for (int p = w; p < n0.x; p += U * per) {
+            float m[U], l[U], y[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int q = min(p + u * per, n0.x - 1);
+                const float* at = slots + (size_t)(2 * ((int)blockIdx.x + q) + (q == 0 ? 1 : 0)) * slot_floats;
+                m[u] = __ldcg(at + (size_t)srows * D + r);
+                l[u] = __ldcg(at + (size_t)srows * (D + 1) + r);
+                const float* z = at + (size_t)r * D + lane * VEC;
+#pragma unroll
+                for (int h = 0; h < V / VEC; ++h) {
+                    if constexpr (VEC == 2) {
+                        const float2 t = __ldcg(reinterpret_cast<const float2*>(z));
+                        y[u][0] = t.x;
+                        y[u][1] = t.y;
+                    } else {
+                        const float4 t = __ldcg(reinterpret_cast<const float4*>(z) + 32 * h);
+                        y[u][4 * h] = t.x;
+                        y[u][4 * h + 1] = t.y;
+                        y[u][4 * h + 2] = t.z;
+                        y[u][4 * h + 3] = t.w;
+                    }
+                }
             }
-            __syncthreads();
-            if (last_cta) {
-                __threadfence();
-                join_parts<D, kAttWarps>(a, un, warp, slots, slot_floats, srows, c0, c1, 0, rows);
-            }
+            float mx = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) mx = p + u * per < n0.x ? fmaxf(mx, m[u]) : mx;
+            const float base = mx == kNegInf ? 0.f : mx;       // (no position seen yet)
+            const float f = ex2_approx(M - base);
+            M = mx;
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (p + u * per < n0.x) {                      // warp-uniform
+                    const float fu = ex2_approx(m[u] - base);
+                    L = fmaf(fu, l[u], L);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] = fmaf(fu, y[u][e], v[e]);
+                }
         }
     }
+    if (per > 1) {                                             // the row's warps: CTA-uniform
+#pragma unroll
+        for (int h = 0; h < V / VEC; ++h)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum[warp][h * 128 + lane * VEC + e] = v[h * VEC + e];
+        if (lane == 0) {
+            ref[warp] = M;
+            tot[warp] = L;
+        }
+        __syncthreads();
+        if (w > 0) return;
+        for (int i = 1; i < per; ++i) M = fmaxf(M, ref[warp + i]);
+        const float base = M == kNegInf ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = 0.f;
+        for (int i = 0; i < per; ++i) {
+            const float f = ex2_approx(ref[warp + i] - base);
+            L = fmaf(f, tot[warp + i], L);
+#pragma unroll
+            for (int h = 0; h < V / VEC; ++h)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[h * VEC + e] = fmaf(f, sum[warp + i][h * 128 + lane * VEC + e], v[h * VEC + e]);
+        }
+    }
+    if (r >= n1.x) return;                                     // warp-uniform
+    const float base = M == kNegInf ? 0.f : M;
+    if constexpr (VEC == 2) {
+        const float2 o = make_float2(__shfl_down_sync(0xffffffffu, v[0], 1), __shfl_down_sync(0xffffffffu, v[1], 1));
+        if (!(lane & 1)) put_row(a, n0.y, n0.z, n0.w, n1.y, false, D, r, lane * 2, make_float4(v[0], v[1], o.x, o.y), L, base);
+    } else {
+#pragma unroll
+        for (int h = 0; h < V / VEC; ++h)
+            put_row(a, n0.y, n0.z, n0.w, n1.y, false, D, r, h * 128 + lane * 4,
+                    make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]), L, base);
+    }
+}
+
+cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int block_rows, long long tiles, cudaStream_t st) {
+    if (tiles == 1) return cudaSuccess;                        // no unit is split
+    // about four parts a warp
+    long long parts = ctas / units + 2;
+    if (parts > tiles) parts = tiles;
+    const int per = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;
+    const int rows = min(block_rows, a.N * a.G), rpc = kJoinThreads / 32 / per;
+    const dim3 grid((unsigned)ctas, (unsigned)((rows + rpc - 1) / rpc));
+    return a.c.head_dim == 64    ? launch_pdl(attend_join_kernel<64>, grid, kJoinThreads, 0, st, a, block_rows, per)
+           : a.c.head_dim == 128 ? launch_pdl(attend_join_kernel<128>, grid, kJoinThreads, 0, st, a, block_rows, per)
+                                 : launch_pdl(attend_join_kernel<256>, grid, kJoinThreads, 0, st, a, block_rows, per);
 }
 
 // Rows of a cached head that a unit holds.
 static int att_rows(int N, int G, int D) { return N * G <= 16 || D == 256 ? 16 : 32; }
 
 size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D) {
-    // counters (at a fixed place whatever the call's sizes, so that no call's parts
-    // overwrite another's), then two parts per CTA, for either kernel
+    // the join's notes, then two parts per CTA, for either kernel
     const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G, D);
     const size_t here = kAttHead + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
     const size_t tc = attend_takes_tc(N, G, D, INT64_MAX) ? attend_tc_workspace(N, G) : 0;
@@ -648,7 +757,8 @@ static cudaError_t launch_attend_t(const AttendArgs& a, cudaStream_t st) {
     if (g > kAttMaxCtas) g = kAttMaxCtas;
     const long long tiles = (long long)a.B * a.c.kv_heads * rb * (most < 1 ? 1 : most);
     if (g > tiles) g = tiles;
-    return launch_pdl(kfn, dim3((unsigned)g), kAttThreads, C::SMEM, st, a);
+    e = launch_pdl(kfn, dim3((unsigned)g), kAttThreads, C::SMEM, st, a);
+    return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, C::ROWS, most, st);
 }
 
 template <int D, bool FP8>

@@ -6,9 +6,16 @@
 
 namespace sv {
 
-constexpr int kAttMaxCtas = 512;            // workspace slots are sized for this many
-constexpr size_t kAttHead = 4096;           // bytes of the workspace before the parts: counters from 256 on
-static_assert(256 + kAttMaxCtas * 4 <= kAttHead, "the counters lie in the zeroed head");
+constexpr int kAttMaxCtas = 512;            // the workspace is sized for this many
+// What the join of the parts (attend_join_kernel) knows of the unit that CTA c
+// begins and others end: at the head of the workspace, one for each CTA.
+struct __align__(16) AttSplit {
+    int parts;               // CTAs c .. c + parts - 1 hold one each; 0: no such unit
+    int b, hk, r0;           // sequence, cached head, first row of the block
+    int rows, nb;            // rows of the block, new positions of the sequence
+    int unused[2];
+};
+constexpr size_t kAttHead = kAttMaxCtas * sizeof(AttSplit);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The reference m of a row moves only when a score passes it by more than
@@ -178,119 +185,31 @@ struct AttWalk {
     }
 };
 
-// Writes elements d .. d + 3 of row r of a finished unit.
-__device__ __forceinline__ void put_row(const AttendArgs& a, const AttUnit& x, bool bad, int D, int r, int d, float4 v,
-                                        float lsum, float mref) {
-    const int R = x.r0 + r, n = row_position(a, R), g = R - n * a.G;
-    const size_t row = ((size_t)x.b * a.N + n) * a.Hq + (size_t)x.hk * a.G + g;
-    const bool empty = n >= x.sl.nb && !bad;
+// Notes for the join which unit, if any, the CTA has begun and others end: the
+// last one of its share.  By one thread, its walk at the end.
+__device__ __forceinline__ void note_split(const AttendArgs& a, const AttPlan& p, const AttUnit& x) {
+    AttSplit s = {};
+    if ((int)blockIdx.x < p.n && x.ta == 0 && x.tb < x.tiles)
+        s = {share_of(p.total, p.n, x.at + x.tiles - 1) - (int)blockIdx.x + 1, x.b, x.hk, x.r0, x.rows, x.sl.nb, {0, 0}};
+    reinterpret_cast<AttSplit*>(a.ws)[blockIdx.x] = s;
+}
+
+// Writes elements d .. d + 3 of row r of a finished unit: row r0 + r of cached head
+// hk of sequence b, which has nb new positions.
+__device__ __forceinline__ void put_row(const AttendArgs& a, int b, int hk, int r0, int nb, bool bad, int D, int r, int d,
+                                        float4 v, float lsum, float mref) {
+    const int R = r0 + r, n = row_position(a, R), g = R - n * a.G;
+    const size_t row = ((size_t)b * a.N + n) * a.Hq + (size_t)hk * a.G + g;
+    const bool empty = n >= nb && !bad;
     const float f = empty ? 0.f : 1.f / lsum;
     if (empty) v = make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
     if (a.lse && d == 0) a.lse[row] = empty ? kNegInf : (mref + __log2f(lsum)) * kLn2;
 }
 
-// Adds rows ra .. rb - 1 of the parts of a unit that CTAs c0 .. c1 hold, in
-// that order, and writes them; by WARPS warps (warp w of them).  A warp takes
-// ROWS rows at once, one lane per part for their references and totals, then its
-// lanes across the elements: the loads of several rows and parts are in flight
-// together (a row and part at a time, the join of 32 rows in 5 parts took 22 us;
-// the parts come from L2, about 0.5 us away).
-template <int D, int WARPS, int ROWS>
-__device__ __forceinline__ void join_rows(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
-                                          int srows, int c0, int c1, int ra, int rb) {
-    constexpr int V = D / 32;                                 // elements of a lane: 2, 4 or 8
-    constexpr int V4 = V >= 4 ? V / 4 : 1;
-    const int lane = threadIdx.x & 31, parts = c1 - c0 + 1;
-    auto part = [&](int p) { return slots + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
-    for (int r0 = ra + w * ROWS; r0 < rb; r0 += WARPS * ROWS) {
-        float M[ROWS], L[ROWS];
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) { M[k] = kNegInf; L[k] = 0.f; }
-        for (int p0 = 0; p0 < parts; p0 += 32) {
-            float m[ROWS];
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k)
-                m[k] = p0 + lane < parts && r0 + k < rb ? __ldcg(part(p0 + lane) + (size_t)srows * D + r0 + k) : kNegInf;
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k) M[k] = fmaxf(M[k], m[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            M[k] = warp_max(M[k]);
-            if (M[k] == kNegInf) M[k] = 0.f;                  // no part has seen a position
-        }
-        float v[ROWS][V];
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
-        for (int p0 = 0; p0 < parts; p0 += 32) {
-            float f[ROWS];
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k) {
-                const bool on = p0 + lane < parts && r0 + k < rb;
-                const float* q = part(on ? p0 + lane : 0) + (size_t)srows * D + (on ? r0 + k : ra);
-                f[k] = on ? ex2_approx(__ldcg(q) - M[k]) : 0.f;
-                L[k] = on ? fmaf(f[k], __ldcg(q + srows), L[k]) : L[k];
-            }
-            const int n = min(32, parts - p0);
-#pragma unroll(ROWS == 1 ? 8 : 2)
-            for (int p = 0; p < n; ++p) {
-                const float* q = part(p0 + p) + (size_t)r0 * D + lane * V;
-                float y[ROWS][V];
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
-                    const float* at = q + (r0 + k < rb ? k * D : 0);
-                    if constexpr (V == 2) {
-                        const float2 t = __ldcg(reinterpret_cast<const float2*>(at));
-                        y[k][0] = t.x;
-                        y[k][1] = t.y;
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < V4; ++h) {
-                            const float4 t = __ldcg(reinterpret_cast<const float4*>(at) + h);
-                            y[k][4 * h] = t.x;
-                            y[k][4 * h + 1] = t.y;
-                            y[k][4 * h + 2] = t.z;
-                            y[k][4 * h + 3] = t.w;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
-                    const float fp = __shfl_sync(0xffffffffu, f[k], p);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[k][e] = fmaf(fp, y[k][e], v[k][e]);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            // the lanes' totals in a fixed order
-            const float lsum = warp_sum(L[k]);
-            if (r0 + k < rb) {
-                if constexpr (V == 2) {
-                    const float2 o = make_float2(__shfl_down_sync(0xffffffffu, v[k][0], 1), __shfl_down_sync(0xffffffffu, v[k][1], 1));
-                    if (!(lane & 1)) put_row(a, x, false, D, r0 + k, lane * 2, make_float4(v[k][0], v[k][1], o.x, o.y), lsum, M[k]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < V4; ++h)
-                        put_row(a, x, false, D, r0 + k, lane * V + 4 * h,
-                                make_float4(v[k][4 * h], v[k][4 * h + 1], v[k][4 * h + 2], v[k][4 * h + 3]), lsum, M[k]);
-                }
-            }
-        }
-    }
-}
-
-// One row a warp while there is a warp for each, else four.
-template <int D, int WARPS>
-__device__ __forceinline__ void join_parts(const AttendArgs& a, const AttUnit& x, int w, float* slots, size_t slot_floats,
-                                           int srows, int c0, int c1, int ra, int rb) {
-    if (rb - ra <= WARPS) join_rows<D, WARPS, 1>(a, x, w, slots, slot_floats, srows, c0, c1, ra, rb);
-    else join_rows<D, WARPS, 4>(a, x, w, slots, slot_floats, srows, c0, c1, ra, rb);
-}
+// Joins the parts that `ctas` CTAs of the call's kernel have left, units of up to
+// `units` row blocks of block_rows rows, `tiles` tiles at most (sv_attend.cu).
+cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int block_rows, long long tiles, cudaStream_t st);
 
 // The matrix-unit kernel of sv_attend_tc.cu (rows of 128 elements).
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);

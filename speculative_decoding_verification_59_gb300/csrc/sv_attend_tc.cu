@@ -55,8 +55,8 @@ constexpr int kTcUnitRing = 8;
 // sleeps for up to some ten microseconds here, and no wait of this kernel lasts
 // longer than the memory takes to answer.
 constexpr uint32_t kTcWaitLimit = 1u << 18;
-constexpr int kTcMaxCtas = 256;                  // three counters each fit the workspace's head
-static_assert(256 + 3 * kTcMaxCtas * 4 <= kAttHead, "the counters lie in the zeroed head");
+constexpr int kTcMaxCtas = 256;
+static_assert(kTcMaxCtas <= kAttMaxCtas, "a note for each");
 constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
 
 struct Yes { static constexpr bool value = true; };
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ uint32_t tmem_at;
     __shared__ int unit_bad[NSM][kTcUnitRing];                  // a page that is none
     __shared__ __align__(16) float qinv[4][FP8 ? RP : 4];       // E4M3: by unit, what takes back a row's scaling
-    __shared__ int odd_any, last_cta[NSM], tree_bad[NSM];
+    __shared__ int odd_any, tree_bad[NSM];
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kMmaWarp = C::SM_THREADS / 32;
@@ -606,6 +606,10 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 }
                 ++uc;
             }
+            if (second) {
+                while (walk.next<kTcTile>(a, RB, block_rows, &un)) {}          // (a wait ran out)
+                note_split(a, plan, un);
+            }
             // every product must have ended before tensor memory is given back
             tc_commit(&drained[second]);
             if (!wait_bounded(&drained[second], 0, kTcWaitLimit) || !ok) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
@@ -620,7 +624,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         const int chunks = min(CH, max(0, (rp - c0 + 15) / 16));
         const int bar = 1 + wg;
         float* slots = reinterpret_cast<float*>(a.ws + kAttHead);
-        int* counters = reinterpret_cast<int*>(a.ws + 256);
         const int srows = min(block_rows, a.N * a.G);
         const size_t slot_floats = part_floats(srows, kTcD);
         unsigned g = 0, uc = 0;
@@ -1014,24 +1017,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 }
             }
             tc_before();
-            if (!whole && mine > 0) {
-                // the unit's CTAs: c0 begins it, c1 ends it; the last warpgroup to arrive adds
-                // its rows' parts
-                const int f0 = share_of(plan.total, plan.n, un.at), f1 = share_of(plan.total, plan.n, un.at + un.tiles - 1);
-                int* counter = counters + NSM * f0 + wg;         // no CTA begins two units that others end
-                named_sync(bar, 128);
-                if (row == 0) {
-                    __threadfence();                           // the barrier put the warpgroup's writes before it
-                    const int got = atomicAdd(counter, 1);
-                    last_cta[wg] = got == f1 - f0;
-                    if (last_cta[wg]) *counter = 0;            // as the next call finds it
-                }
-                named_sync(bar, 128);
-                if (last_cta[wg]) {
-                    __threadfence();
-                    join_parts<kTcD, 4>(a, un, warp & 3, slots, slot_floats, srows, f0, f1, c0, c0 + mine);
-                }
-            }
             ++uc;
         }
         if (dead && row == 0) raise_error(a.c.error, SPEC_DEVERR_TIMEOUT);
@@ -1126,7 +1111,8 @@ static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cuda
     CUtensorMap km = {}, vm = {};
     if (box > 0 && (!encode_map(&km, a.c, a.c.k, box) || !encode_map(&vm, a.c, a.c.v, box))) box = 0;
     const uint32_t limit = ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit;
-    return launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, limit, km, vm);
+    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, limit, km, vm);
+    return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, block_rows, most, st);
 }
 
 template <bool FP8>

@@ -181,7 +181,7 @@ at::Tensor stretch(const at::Tensor& whole, c10::IntArrayRef shape, at::ScalarTy
 // on different streams overlap and must not share one.  Kept for later calls,
 // except when first needed inside a capture: that one belongs to the graph.
 // Never freed at exit (the CUDA context may be gone by then).
-constexpr size_t kHeadBytes = 4096;      // what the calls want zeroed once
+constexpr size_t kHeadBytes = 256;       // what a call may want zeroed once (the error word)
 at::Tensor scratch(int kind, int device, cudaStream_t h, size_t need) {
     using Key = std::tuple<int, int, cudaStream_t>;
     static std::mutex* lock = new std::mutex;

@@ -354,3 +354,18 @@ def test_rows_around_the_kernels_bounds(sv, fp8, N, G):
     g = torch.Generator().manual_seed(N)
     q = (torch.randn((2, N, 2 * G, 128), generator=g) * 1.5).to(torch.bfloat16)
     check(sv, parts, q, None, torch.tensor([200, 77], dtype=torch.int32), torch.full((2,), N, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("N,Hq,H,D,ctx", [(1, 32, 8, 128, [2000]), (9, 32, 8, 128, [3000, 40, 1]), (16, 8, 1, 64, [1300, 0]),
+                                          (13, 4, 1, 128, [4749]), (12, 8, 1, 256, [2000, 1999])])
+def test_workspace_of_any_contents(sv, N, Hq, H, D, ctx):
+    """What lies in the workspace before a call does not matter: results are those of a clear one,
+    and right (the many parts of one long unit are joined by several warps a row)."""
+    parts, q, par, c, nb = case(31, len(ctx), N, Hq, H, D, 16, ctx)
+    cache = R.on_gpu(sv, parts)
+    n = sv.load_library().spec_attention_workspace_size(len(ctx), N, Hq, H, D)
+    got = [sv.paged_attention(q.cuda(), cache, c.cuda(), lse=True, workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+           for fill in (0, 255, 1)]
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+    check(sv, parts, q, par, c, nb)
