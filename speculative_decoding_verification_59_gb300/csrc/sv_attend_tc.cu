@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
-    __shared__ int rowat[RP];                                   // its row of the output, from the sequence's first
+    __shared__ __align__(16) int rowat[RP];                                   // its row of the output, from the sequence's first
     __shared__ unsigned long long anc[NSM][2][kMaxNewTree];    // trees: ancestors and itself, by node
     __shared__ short up[NSM][2][kMaxNewTree];
     __shared__ uint32_t vis[NSM][kMaxNewTree][C::WORDS];       // trees: the warpgroup's rows that see a node
@@ -897,24 +897,25 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 if (masked && wg == 0) {
                     // A new position's value that is no number, times a row's probability of
                     // zero, would spoil the row's sum: such values are taken out of the tile
-                    // here, a position a thread, and given to the rows that see them at the
-                    // unit's end.
+                    // here, and given to the rows that see them at the unit's end.
+                    // (by all threads, 16 bytes each: a position a thread was 16 rounds of a
+                    // few threads, 3000 cycles at every unit's end)
                     late |= !wait_bounded(&v_full[g % VB], (g / VB) & 1u, limit);
-                    if (d >= 0 && !gone) {
-                        unsigned char* vb = smem + C::V_OFF + (g % VB) * C::BUF;
-#pragma unroll 4
-                        for (int k = 0; k < C::BUF / 2048; ++k) {
-                            uint4* at = reinterpret_cast<uint4*>(vb + tc_off(row, k));
-                            uint4 w = *at;
-                            const uint4 was = w;
-                            w.x = FP8 ? drop_odd_e4m3(w.x) : drop_odd_bf16(w.x);
-                            w.y = FP8 ? drop_odd_e4m3(w.y) : drop_odd_bf16(w.y);
-                            w.z = FP8 ? drop_odd_e4m3(w.z) : drop_odd_bf16(w.z);
-                            w.w = FP8 ? drop_odd_e4m3(w.w) : drop_odd_bf16(w.w);
-                            if (w.x != was.x || w.y != was.y || w.z != was.z || w.w != was.w) {
-                                odd_any = 1;
-                                *at = w;
-                            }
+                    constexpr int PIECES = C::BUF / 2048;       // of a position
+                    const int t0 = max(sl.ctx - p0, 0), n = (min(sl.total - p0, kTcTile) - t0) * PIECES;
+                    unsigned char* vb = smem + C::V_OFF + (g % VB) * C::BUF;
+#pragma unroll 1
+                    for (int e = row; e < n; e += 128) {
+                        uint4* at = reinterpret_cast<uint4*>(vb + tc_off(t0 + e / PIECES, e % PIECES));
+                        uint4 w = *at;
+                        const uint4 was = w;
+                        w.x = FP8 ? drop_odd_e4m3(w.x) : drop_odd_bf16(w.x);
+                        w.y = FP8 ? drop_odd_e4m3(w.y) : drop_odd_bf16(w.y);
+                        w.z = FP8 ? drop_odd_e4m3(w.z) : drop_odd_bf16(w.z);
+                        w.w = FP8 ? drop_odd_e4m3(w.w) : drop_odd_bf16(w.w);
+                        if (w.x != was.x || w.y != was.y || w.z != was.z || w.w != was.w) {
+                            odd_any = 1;
+                            *at = w;
                         }
                     }
                 }
@@ -1002,18 +1003,25 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         }
                     }
                 }
+                if (whole) {
+                    unsigned short* to = reinterpret_cast<unsigned short*>(a.out) + (size_t)un.b * a.N * a.Hq * kTcD + row;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = c0 + k0 + k;
-                    if (k0 + k < mine) {
-                        if (whole) {
-                            const float y = rown[r] >= sl.nb && !bad ? 0.f : v[k] * alpha[r];
-                            reinterpret_cast<unsigned short*>(a.out)[((size_t)un.b * a.N * a.Hq + rowat[r]) * kTcD + row] =
-                                (unsigned short)(pack_bf16(y, 0.f) & 0xffffu);
-                        } else {
-                            __stcg(sp + (size_t)r * kTcD + row, v[k]);
-                        }
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(&alpha[c0 + k0 + k]);
+                        const int4 at = *reinterpret_cast<const int4*>(&rowat[c0 + k0 + k]);
+                        const float f[4] = {w.x, w.y, w.z, w.w};
+                        const int r[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + k + e < mine)
+                                to[(int64_t)r[e] * kTcD] =
+                                    (unsigned short)(pack_bf16(f[e] == 0.f ? 0.f : v[k + e] * f[e], 0.f) & 0xffffu);
                     }
+                } else {
+                    float* to = sp + (size_t)(c0 + k0) * kTcD + row;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k0 + k < mine) __stcg(to + k * kTcD, v[k]);
                 }
             }
             tc_before();
