@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         mbar_init(&p_full, C::SM_THREADS / 32);
         mbar_init(&pv_done, 1);
         for (int i = 0; i < C::QB; ++i) {
-            mbar_init(&q_full[i], C::LOADERS / 32);
+            mbar_init(&q_full[i], FP8 ? C::LOADERS / 32 : C::LOADERS);
             mbar_init(&q_free[i], 1);
         }
         mbar_init_fence();
@@ -396,66 +396,79 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 rslot[h] = 0;
                 if (by_row(un.ta)) rpage[h] = row_page(un.ta, h, &rslot[h]);
             }
-            // ---- the unit's queries
-            const int qb = (int)(uc % C::QB);
-            if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            unsigned char* qs = smem + C::Q_OFF + qb * C::QBYTES;
-            auto query_row = [&](int r) {
-                const int R = un.r0 + r, n = row_position(a, R), g = R - n * a.G;
-                return a.q + ((int64_t)un.b * a.N + n) * a.qs + ((size_t)un.hk * a.G + g) * kTcD * 2;
-            };
-            constexpr int QK = 6;                              // loads of a thread in flight
-            for (int i0 = lt; i0 < rp * 16; i0 += C::LOADERS * QK) {
-                uint4 w[QK];
+            // ---- the unit's queries.  bf16: behind its first keys, which wait for nothing that the
+            // unit before still has to do, and the thread goes on while the copies are under
+            // way (before them and through registers, 144 rows kept the loaders for 8000
+            // cycles a unit).  E4M3: through registers, in terms (few rows; among the tiles'
+            // code, that of every tile was slower: 133 us for 111 at 8 x 32768 positions).
+            auto queries = [&] {
+                const int qb = (int)(uc % C::QB);
+                if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                unsigned char* qs = smem + C::Q_OFF + qb * C::QBYTES;
+                auto query_row = [&](int r) {
+                    const int R = un.r0 + r, n = row_position(a, R), g = R - n * a.G;
+                    return a.q + ((int64_t)un.b * a.N + n) * a.qs + ((size_t)un.hk * a.G + g) * kTcD * 2;
+                };
+                if constexpr (!FP8) {
+                    const uint32_t to = smem_addr(qs) + (lt >> 3 & 1) * (RP * 128);
+#pragma unroll 4
+                    for (int r = lt >> 4; r < rp; r += C::LOADERS / 16)
+                        cp16(to + r * 128 + (((lt & 7) ^ (r & 7)) << 4), query_row(min(r, un.rows - 1)) + (lt & 15) * 16, r < un.rows);
+                    cp_arrive(&q_full[qb]);
+                } else {
+                    constexpr int QK = 6;                      // loads of a thread in flight
+                    for (int i0 = lt; i0 < rp * 16; i0 += C::LOADERS * QK) {
+                        uint4 w[QK];
 #pragma unroll
-                for (int k = 0; k < QK; ++k) {
-                    const int i = i0 + C::LOADERS * k, r = i >> 4;
-                    w[k] = r < un.rows ? __ldg(reinterpret_cast<const uint4*>(query_row(r)) + (i & 15)) : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int k = 0; k < QK; ++k) {
-                    const int i = i0 + C::LOADERS * k, r = i >> 4, c16 = i & 15;
-                    if constexpr (!FP8) {
-                        if (r < rp) *reinterpret_cast<uint4*>(qs + (c16 >> 3) * (RP * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = w[k];
-                    } else {
-                        // the row's 16 lanes find the power of two that brings its largest
-                        // element into [2^7, 2^8), and write its two terms
-                        float x[8], mx = 0.f;
-                        unpack8(w[k], x);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (!(fabsf(x[j]) < CUDART_INF_F)) x[j] = CUDART_NAN_F;        // (e4m3 has no infinity)
-                            else mx = fmaxf(mx, fabsf(x[j]));
+                        for (int k = 0; k < QK; ++k) {
+                            const int i = i0 + C::LOADERS * k, r = i >> 4;
+                            w[k] = r < un.rows ? __ldg(reinterpret_cast<const uint4*>(query_row(r)) + (i & 15)) : make_uint4(0u, 0u, 0u, 0u);
                         }
 #pragma unroll
-                        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 134 - ex;
-                        const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+                        for (int k = 0; k < QK; ++k) {
+                            const int i = i0 + C::LOADERS * k, r = i >> 4, c16 = i & 15;
+                            // the row's 16 lanes find the power of two that brings its largest
+                            // element into [2^7, 2^8), and write its two terms
+                            float x[8], mx = 0.f;
+                            unpack8(w[k], x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] *= f;
-                        uint2 term[2];
+                            for (int j = 0; j < 8; ++j) {
+                                if (!(fabsf(x[j]) < CUDART_INF_F)) x[j] = CUDART_NAN_F;        // (e4m3 has no infinity)
+                                else mx = fmaxf(mx, fabsf(x[j]));
+                            }
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            term[q].x = e4m3_term(x[0], x[1]);
-                            term[q].x |= e4m3_term(x[2], x[3]) << 16;
-                            term[q].y = e4m3_term(x[4], x[5]);
-                            term[q].y |= e4m3_term(x[6], x[7]) << 16;
-                        }
-                        if (r < rp) {
+                            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            const int ex = (int)(__float_as_uint(mx) >> 23), sh = ex < 24 || ex > 240 ? 0 : 134 - ex;
+                            const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[j] *= f;
+                            uint2 term[2];
 #pragma unroll
                             for (int q = 0; q < 2; ++q) {
-                                const int at = q * rp + r;
-                                *reinterpret_cast<uint2*>(qs + at * 128 + (((c16 >> 1) ^ (at & 7)) << 4) + (c16 & 1) * 8) = term[q];
+                                term[q].x = e4m3_term(x[0], x[1]);
+                                term[q].x |= e4m3_term(x[2], x[3]) << 16;
+                                term[q].y = e4m3_term(x[4], x[5]);
+                                term[q].y |= e4m3_term(x[6], x[7]) << 16;
                             }
-                            if (c16 == 0) qinv[uc & 3][r] = __uint_as_float((uint32_t)(127 - sh) << 23);
+                            if (r < rp) {
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const int at = q * rp + r;
+                                    *reinterpret_cast<uint2*>(qs + at * 128 + (((c16 >> 1) ^ (at & 7)) << 4) + (c16 & 1) * 8) = term[q];
+                                }
+                                if (c16 == 0) qinv[uc & 3][r] = __uint_as_float((uint32_t)(127 - sh) << 23);
+                            }
                         }
                     }
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_full[qb]);
                 }
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[qb]);
+            };
+
+            if constexpr (FP8) queries();
 
             // ---- the unit's tiles
             for (int i = un.ta; i < un.tb && ok; ++i) {
@@ -492,12 +505,13 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
                 }
                 for (int kv = 0; kv < 2; ++kv) {
+                    if (!FP8 && kv == 1 && i == un.ta) queries();
                     // The buffer, once it is free.  Every warp waits for every buffer of its
                     // kind and arrives for it, the ones that have no part in a TMA tile too: a
                     // barrier tells its last two phases apart, no more, so none may
                     // fall behind or run ahead.
                     const unsigned n = kv ? VB : KB;
-                    if (lane == 0 && t >= n) ok = wait_bounded(kv ? &v_empty[t % VB] : &k_empty[t % KB], (t / n - 1) & 1u, limit);
+                    if (ok && lane == 0 && t >= n) ok = wait_bounded(kv ? &v_empty[t % VB] : &k_empty[t % KB], (t / n - 1) & 1u, limit);
                     const uint32_t dst = smem_addr(smem + (kv ? C::V_OFF + (t % VB) * C::BUF : (t % KB) * C::BUF));
                     uint64_t* bar = kv ? &v_full[t % VB] : &k_full[t % KB];
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (ok) ok = wait_bounded(&k_full[g % KB], (g / KB) & 1u, limit);
                         if (ok && g >= 2) ok = wait_bounded(&s_free[g & 1], ((g >> 1) - 1) & 1u, limit);
                         if (!ok) break;
-                        if (fence) proxy_fence();
+                        if (fence || i == un.ta) proxy_fence();
                         tc_after();
                         const uint64_t kd = a_d + (g % KB) * (C::BUF / 16), qd = b_d + qb * (C::QBYTES / 16);
                         const uint32_t at = tmem + (g & 1) * C::S_COLS;
