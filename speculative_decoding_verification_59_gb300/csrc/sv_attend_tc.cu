@@ -70,8 +70,8 @@ struct TcCfg {
     static constexpr int QT = FP8 ? 2 : 1, PT = FP8 ? 3 : 1;     // terms of a query, of a probability
     static constexpr int PROWS = FP8 ? 128 : 64; // columns of P in 128 bytes
     static constexpr int PB = (PT * RP + PROWS - 1) / PROWS;     // blocks of them
-    static constexpr int QB = RP <= 64 ? 2 : 1;  // units whose queries are held
-    static constexpr int KB = FP8 ? 4 : 2;       // buffers of keys, of values
+    static constexpr int QB = RP <= 64 && (FP8 || RP != 32) ? 2 : 1;  // units whose queries are held
+    static constexpr int KB = FP8 ? 4 : RP > 32 ? 2 : 3;       // buffers of keys, of values
     static constexpr int VB = FP8 ? (RP > 32 ? 4 : 5) : RP > 64 ? 2 : 3;
     static constexpr int S_COLS = QT * RP;       // columns of tensor memory: scores, sums
     static constexpr int O_AT = 2 * S_COLS, T_COLS = O_AT + PT * RP;
@@ -172,12 +172,20 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const float (&v)[16]) {
     tc_wait_st();
 }
 
-// A box of a 4-D tensor into shared memory.
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int tok, int head, int page, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(smem_addr(bar))
-        : "memory");
+// The box from `slot` (a multiple of 8) of a page's head (entry `place` of the map)
+// into shared memory.
+template <bool FP8>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int slot, int place, uint64_t* bar) {
+    if constexpr (FP8)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(0), "r"(slot), "r"(place), "r"(smem_addr(bar))
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(map), "r"(0), "r"(slot >> 3), "r"(place), "r"(smem_addr(bar))
+            : "memory");
 }
 __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
@@ -219,9 +227,14 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Byte offset of 16-byte chunk c of row t in a tile of 128 rows, kept as blocks
-// of 128-byte swizzled (half) rows.
-__device__ __forceinline__ int tc_off(int t, int c) { return (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4); }
+// Byte offset of 16-byte chunk c of row t in a tile: groups of 8 rows, in each the
+// 128-byte swizzled rows (bf16: first halves, then second halves, so that a page comes
+// in one box: with a box for each half, pages of 16 took 158 us for 64 x 32 rows over
+// up to 4096, those of 8 190).
+template <bool FP8>
+__device__ __forceinline__ int tc_off(int t, int c) {
+    return (t >> 3) * (FP8 ? 1024 : 2048) + (c >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4);
+}
 
 // A pair of bf16 values with infinities and NaN set to zero.
 __device__ __forceinline__ uint32_t drop_odd_bf16(uint32_t y) {
@@ -287,7 +300,7 @@ __device__ __forceinline__ float fold16(float (&v)[16], int lane, Op op) {
 __device__ __forceinline__ int fold_column(int lane) { return lane >> 1; }
 
 template <int CH, int NSM, bool FP8>
-__global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, int box, uint32_t limit, const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_kernel(const AttendArgs a, int block_rows, int rp, int box, int page_places, int head_places, uint32_t limit, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
     using C = TcCfg<CH, NSM, FP8>;
     constexpr int RP = C::RP, KB = C::KB, VB = C::VB;
@@ -521,8 +534,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                             __syncwarp();
                             if (lane < boxes) {
                                 const CUtensorMap* map = kv ? &vmap : &kmap;
-                                tma_load(dst + lane * box * 128, map, 0, at_slot, un.hk, at_page, bar);
-                                if constexpr (!FP8) tma_load(dst + 16384 + lane * box * 128, map, 64, at_slot, un.hk, at_page, bar);
+                                tma_load<FP8>(dst + lane * box * (FP8 ? 128 : 256), map, at_slot, at_page * page_places + un.hk * head_places, bar);
                             }
                             __syncwarp();
                         }
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                             for (int p = 0; p < PIECES; ++p) {
                                 const int wr = p * RPI + sub, row = (h * C::LW + lw) * 32 + wr;
                                 const int64_t e = __shfl_sync(0xffffffffu, off[h], wr) * (FP8 ? 1 : 2) + ch * 16;
-                                cp16(dst + tc_off(row, ch), base + e, (havem[h] >> wr) & 1u);
+                                cp16(dst + tc_off<FP8>(row, ch), base + e, (havem[h] >> wr) & 1u);
                             }
                     }
                     bool copies = !tma;                         // the threads have copies of their own in flight
@@ -579,7 +591,8 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             const bool second = warp > kMmaWarp;
             const uint32_t base = smem_addr(smem);
             const uint32_t id = second ? tc_idesc(FP8, true, true, C::PT * rp) : tc_idesc(FP8, false, false, C::QT * rp);
-            const uint64_t a_d = second ? tc_desc(base + C::V_OFF, 16384, 1024) : tc_desc(base, 16, 1024);
+            constexpr uint32_t GROUP = FP8 ? 1024 : 2048;          // 8 positions of a tile
+            const uint64_t a_d = second ? tc_desc(base + C::V_OFF, 1024, GROUP) : tc_desc(base, 16, GROUP);
             const uint64_t b_d = second ? tc_desc(base + C::P_OFF, 16384, 1024) : tc_desc(base + C::Q_OFF, 16, 1024);
             bool ok = true;
             unsigned g = 0, uc = 0;                            // tiles, units
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         const uint32_t at = tmem + (g & 1) * C::S_COLS;
 #pragma unroll
                         for (int ks = 0; ks < C::BUF / 4096; ++ks)              // 32 bytes of a row at a time
-                            tc_mma<FP8>(at, kd + ((ks >> 2) * 1024 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id, ks > 0);
+                            tc_mma<FP8>(at, kd + ((ks >> 2) * 64 + (ks & 3) * 2), qd + ((ks >> 2) * (RP * 8) + (ks & 3) * 2), id, ks > 0);
                         tc_commit(&s_full[g & 1]);
                         tc_commit(&k_empty[g % KB]);
                         if (i + 1 == un.tb) tc_commit(&q_free[qb]);
@@ -610,10 +623,10 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         if (fence) proxy_fence();
                         tc_after();
                         const uint64_t vd = a_d + (g % VB) * (C::BUF / 16);
-                        constexpr int STEP = FP8 ? 256 : 128;   // 32 (16) positions
+                        constexpr int VS = 256, PS = FP8 ? 256 : 128;   // 32 (16) positions, in 16 bytes
 #pragma unroll
-                        for (int ks = 0; ks < 1024 / STEP; ++ks)
-                            tc_mma<FP8>(tmem + C::O_AT, vd + ks * STEP, b_d + ks * STEP, id, ks > 0 || i > un.ta);
+                        for (int ks = 0; ks < (FP8 ? 4 : 8); ++ks)
+                            tc_mma<FP8>(tmem + C::O_AT, vd + ks * VS, b_d + ks * PS, id, ks > 0 || i > un.ta);
                         tc_commit(&pv_done);
                         tc_commit(&v_empty[g % VB]);
                     }
@@ -920,7 +933,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     unsigned char* vb = smem + C::V_OFF + (g % VB) * C::BUF;
 #pragma unroll 1
                     for (int e = row; e < n; e += 128) {
-                        uint4* at = reinterpret_cast<uint4*>(vb + tc_off(t0 + e / PIECES, e % PIECES));
+                        uint4* at = reinterpret_cast<uint4*>(vb + tc_off<FP8>(t0 + e / PIECES, e % PIECES));
                         uint4 w = *at;
                         const uint4 was = w;
                         w.x = FP8 ? drop_odd_e4m3(w.x) : drop_odd_bf16(w.x);
@@ -1092,20 +1105,40 @@ static EncodeFn encoder() {
     return fn;
 }
 
-// A layer's keys (or values) as [page, head, slot, element], boxes of `box`
-// slots and 128 swizzled bytes: half a row of bf16, a row of E4M3.
-static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int box) {
+// Where the places of a tensor map lie: a page's head every `unit` elements, at place
+// page * pages + head * heads.  Pages that hold whole heads, or heads that hold whole
+// pages; 0 for another layout.
+struct Places {
+    int64_t unit;
+    int pages, heads;
+};
+static Places places_of(const spec_kv_cache_t& c) {
+    const int64_t p = c.page_stride, h = c.kv_heads > 1 ? c.head_stride : p;
+    if (p < 1 || h < 1) return {};
+    const int64_t q = p % h == 0 ? p / h : 1, r = p % h == 0 ? 1 : h % p == 0 ? h / p : 0;
+    if (r == 0 || (c.num_pages - 1) * q + (c.kv_heads - 1) * r >= (1ll << 31) || q > INT32_MAX || r > INT32_MAX) return {};
+    return {p < h ? p : h, (int)q, (int)r};
+}
+
+// A layer's keys (or values) as boxes of `box` slots of a page's head.  E4M3: [place, slot,
+// 128 bytes]; bf16: [place, group of 8 slots, half, slot, 128 bytes].  (Groups for E4M3 too
+// were slower: 123 us for 111 at 8 x 32768 positions.)
+static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int box, const Places& at) {
     const bool f8 = c.dtype == SPEC_DTYPE_E4M3;
-    const cuuint64_t elt = f8 ? 1 : 2;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * elt, (cuuint64_t)c.head_stride * elt, (cuuint64_t)c.page_stride * elt};
-    for (cuuint64_t s : strides)
+    const int elt = f8 ? 1 : 2;
+    const cuuint64_t token = (cuuint64_t)c.token_stride * elt, place = (cuuint64_t)at.unit * elt;
+    const cuuint64_t n = (cuuint64_t)(c.num_pages - 1) * at.pages + (cuuint64_t)(c.kv_heads - 1) * at.heads + 1;
+    const cuuint64_t groups = (cuuint64_t)c.page_size / 8;
+    const cuuint64_t dims8[3] = {128, (cuuint64_t)c.page_size, n}, dims16[5] = {64, 8, 2, groups, n};
+    const cuuint64_t strides8[2] = {token, place}, strides16[4] = {token, 128, 8 * token, place};
+    const cuuint32_t boxes8[3] = {128, (cuuint32_t)box, 1}, boxes16[5] = {64, 8, 2, (cuuint32_t)box / 8, 1};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    for (cuuint64_t s : {token, 8 * token, place})
         if (s == 0 || s >= (1ull << 40)) return false;
-    const cuuint32_t boxes[4] = {f8 ? 128u : 64u, (cuuint32_t)box, 1u, 1u}, one[4] = {1u, 1u, 1u, 1u};
-    return encoder() && encoder()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides,
-                                  boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encoder() &&
+           encoder()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f8 ? 3 : 5, base, f8 ? dims8 : dims16,
+                     f8 ? strides8 : strides16, f8 ? boxes8 : boxes16, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CH, int NSM, bool FP8>
@@ -1131,9 +1164,10 @@ static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cuda
     const int ps = a.c.page_size;
     int box = ps % kTcTile == 0 ? kTcTile : ps >= 8 && kTcTile % ps == 0 ? ps : 0;
     CUtensorMap km = {}, vm = {};
-    if (box > 0 && (!encode_map(&km, a.c, a.c.k, box) || !encode_map(&vm, a.c, a.c.v, box))) box = 0;
+    const Places at = places_of(a.c);
+    if (at.unit == 0 || (box > 0 && (!encode_map(&km, a.c, a.c.k, box, at) || !encode_map(&vm, a.c, a.c.v, box, at)))) box = 0;
     const uint32_t limit = ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit;
-    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, limit, km, vm);
+    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, at.pages, at.heads, limit, km, vm);
     return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, block_rows, most, st);
 }
 

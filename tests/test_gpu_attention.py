@@ -369,3 +369,34 @@ def test_workspace_of_any_contents(sv, N, Hq, H, D, ctx):
     for o, l in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
     check(sv, parts, q, par, c, nb)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("layout", ["heads outermost", "keys beside values", "odd page step", "pages reversed in steps of two"])
+@pytest.mark.parametrize("page", [8, 16, 64, 256])
+def test_cache_layouts(sv, fp8, layout, page):
+    """Layers whose pages lie in other ways than one after another, whichever way the kernel brings
+    them: results are those of the plain layout."""
+    B, N, Hq, H, D, ctx = 2, 9, 8, 2, 128, [2700, 300]
+    parts, q, par, c, nb = case(33, B, N, Hq, H, D, page, ctx, fp8=fp8)
+    k, v, table, ks, vs = parts
+    want = sv.paged_attention(q.cuda(), R.on_gpu(sv, parts), c.cuda(), lse=True)
+    P = k.shape[0]
+
+    def lay(x):
+        x = x.cuda()
+        if layout == "heads outermost":
+            return x.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+        if layout == "odd page step":                      # 16 bytes between pages
+            big = torch.zeros(P, page * H * D + 16 // x.element_size(), device="cuda", dtype=torch.uint8 if fp8 else x.dtype)
+            y = big.view(x.dtype)[:, :page * H * D].view(P, page, H, D)
+        elif layout == "keys beside values":
+            y = torch.zeros(P, page, H, 2, D, device="cuda", dtype=torch.uint8 if fp8 else x.dtype).view(x.dtype)[:, :, :, 1]
+        else:
+            y = torch.zeros(2 * P, page, H, D, device="cuda", dtype=torch.uint8 if fp8 else x.dtype).view(x.dtype)[::2]
+        y.copy_(x)
+        return y
+    cache = sv.KVCache(lay(k), lay(v), table.cuda(), None if ks is None else ks.cuda(), None if vs is None else vs.cuda())
+    got = sv.paged_attention(q.cuda(), cache, c.cuda(), lse=True)
+    assert cache.read_error() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
