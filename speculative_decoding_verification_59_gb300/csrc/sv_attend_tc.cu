@@ -233,7 +233,8 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
 // up to 4096, those of 8 190).
 template <bool FP8>
 __device__ __forceinline__ int tc_off(int t, int c) {
-    return (t >> 3) * (FP8 ? 1024 : 2048) + (c >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4);
+    if constexpr (FP8) return t * 128 + ((c ^ (t & 7)) << 4);
+    else return (t >> 3) * 2048 + (c >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4);
 }
 
 // A pair of bf16 values with infinities and NaN set to zero.
@@ -1121,8 +1122,7 @@ static Places places_of(const spec_kv_cache_t& c) {
 }
 
 // A layer's keys (or values) as boxes of `box` slots of a page's head.  E4M3: [place, slot,
-// 128 bytes]; bf16: [place, group of 8 slots, half, slot, 128 bytes].  (Groups for E4M3 too
-// were slower: 123 us for 111 at 8 x 32768 positions.)
+// 128 bytes]; bf16: [place, group of 8 slots, half, slot, 128 bytes].
 static bool encode_map(CUtensorMap* m, const spec_kv_cache_t& c, void* base, int box, const Places& at) {
     const bool f8 = c.dtype == SPEC_DTYPE_E4M3;
     const int elt = f8 ? 1 : 2;
