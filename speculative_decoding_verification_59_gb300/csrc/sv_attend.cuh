@@ -215,7 +215,7 @@ cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int bloc
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);
 // Whether that kernel takes a call; capacity: positions that a sequence's row of
 // the block table has room for.
-bool attend_takes_tc(int N, int G, int D, long long capacity);
+bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity);
 size_t attend_tc_workspace(int N, int G);
 
 }  // namespace sv

@@ -1070,17 +1070,21 @@ static int tc_block_rows(int rt, int most) {
 }
 constexpr int kTcMostBf16 = 144, kTcMostFp8 = 64;
 
-// Which kernel takes heads of 128 (each side measured on one GB300, bf16, 8 cached
-// heads; us here / in sv_attend.cu).  Up to 16 rows that one's single matrix tile
-// is enough and its units cost less to begin and end: 152 / 128 for 64 sequences of
-// 4 rows over up to 4000 positions, 14.1 / 9.1 for one over 1000.  Above 32 rows it
-// would read the cache once per 32: 111 / 224 for 32 trees of 144 rows over up to
-// 2048.  Between, this one gains per position what it loses per unit: 154 / 178 for
-// 64 x 32 rows over up to 4096, but 111 / 90 for 20 rows over up to 2000 -- so the
-// longest context that the block table has room for decides.
-constexpr long long kTcMinCapacity = 2560;
-bool attend_takes_tc(int N, int G, int D, long long capacity) {
-    return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= kTcMinCapacity));
+// Which kernel takes heads of 128 (each side measured on one GB300, 8 cached heads,
+// ragged lengths of half to all of the stated one; us here / in sv_attend.cu).
+//   16 rows and fewer: one matrix tile of that one's is enough, and its units cost less
+//     to begin and end: 78.1 / 73.4 for 64 sequences of 2000 positions, 56.2 / 45.6 of
+//     1000, 22.3 / 20.6 for 8 of 4000.
+//   17 to 32: this one gains per position what it loses per unit, so the longest context
+//     that the block table has room for decides.  bf16, 32 rows: 64.4 / 59.7 for 64
+//     sequences of 1000, 12.4 / 13.0 for one, but 80.5 / 90.8 and 13.3 / 19.0 of 2000.  E4M3,
+//     where the other reads half the bytes and widens them, later: 88.9 / 85.8 for 64 of
+//     2000, 132.3 / 132.2 of 4000, 18.2 / 20.7 for one.
+//   More: that one reads the cache once for every 32: 148.5 / 332.3 for 36 rows and 64 of
+//     4000, 100.8 / 167.4 of 2000, 51.1 / 49.6 of 300.
+constexpr long long kTcMinCapacityBf16 = 1536, kTcMinCapacityFp8 = 2560;
+bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity) {
+    return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= (fp8 ? kTcMinCapacityFp8 : kTcMinCapacityBf16)));
 }
 
 size_t attend_tc_workspace(int N, int G) {
