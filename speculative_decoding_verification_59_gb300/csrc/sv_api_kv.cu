@@ -49,7 +49,8 @@ spec_status_t spec_kv_append(const spec_kv_cache_t* cache, const void* q, const 
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (rot_dim > 0 && (!rope || rope_rows < 1)))
         return SPEC_ERR_INVALID_ARG;
     if ((q_weight || k_weight) && !(eps >= 0.f && isfinite(eps))) return SPEC_ERR_INVALID_ARG;
-    if ((long long)B * N * ((long long)q_heads + 2 * cache->kv_heads) >= (1LL << 31)) return SPEC_ERR_INVALID_ARG;
+    if ((long long)B * N >= (1LL << 31) || (long long)B * N * ((long long)q_heads + 2LL * cache->kv_heads) >= (1LL << 31))
+        return SPEC_ERR_INVALID_ARG;
     if (!is_aligned(k, 16) || !is_aligned(v, 16) || k_token_stride % 8 || v_token_stride % 8 ||
         (q_heads > 0 && (!is_aligned(q, 16) || !is_aligned(q_out, 16) || q_token_stride % 8)) ||
         (q_weight && !is_aligned(q_weight, 16)) || (k_weight && !is_aligned(k_weight, 16)) ||
@@ -101,6 +102,7 @@ spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* conte
     const spec_status_t s = check_cache(cache);
     if (s != SPEC_OK) return s;
     if (!context_lens || !path_nodes || !num_accepted || B > 65535) return SPEC_ERR_INVALID_ARG;
+    if ((long long)cache->layers * cache->kv_heads >= (1LL << 31) / (2 * 256 * 2 / 16)) return SPEC_ERR_INVALID_ARG;
     return status_of(launch_kv_compact(*cache, context_lens, path_nodes, num_accepted, B, N, stream));
 }
 
@@ -123,7 +125,7 @@ spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
     const int Hkv = cache->kv_heads;
     if (q_heads < Hkv || q_heads % Hkv || q_heads / Hkv > kMaxGroup) return SPEC_ERR_INVALID_ARG;
     if (!q || !context_lens || !out || !workspace) return SPEC_ERR_INVALID_ARG;
-    if ((long long)B * N * q_heads >= (1LL << 31)) return SPEC_ERR_INVALID_ARG;
+    if ((long long)B * N >= (1LL << 31) || (long long)B * N * q_heads >= (1LL << 31)) return SPEC_ERR_INVALID_ARG;
     if (!is_aligned(q, 16) || !is_aligned(out, 16) || q_token_stride % 8 || !is_aligned(workspace, 256))
         return SPEC_ERR_MISALIGNED;
     if (workspace_bytes < attend_workspace_size(B, N, q_heads, Hkv, cache->head_dim))

@@ -15,18 +15,20 @@ constexpr int kKvThreads = 256;
 // i + rot/2, which another lane holds at the same offset (rot is a multiple
 // of 16), so it takes one shuffle per element; an interleaved one pairs a
 // lane's own neighbours.
+constexpr int kAppendThreads = 128;
+
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kKvThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
     pdl_trigger();
     pdl_wait();
     constexpr int L = D / 8;                                  // lanes per row
-    const int heads = a.Hq + 2 * a.c.kv_heads;
-    const long long rows = (long long)a.B * a.N * heads;
-    const long long r = ((long long)blockIdx.x * kKvThreads + threadIdx.x) / L;
+    const unsigned heads = a.Hq + 2 * a.c.kv_heads;
+    const unsigned rows = (unsigned)a.B * a.N * heads;        // below 2^31
+    const unsigned r = blockIdx.x * (kAppendThreads / L) + threadIdx.x / L;
     const bool live = r < rows;                               // a row's lanes agree; idle rows keep the shuffles whole
     const int lr = threadIdx.x % L;
     const int tok = live ? (int)(r / heads) : 0;
-    const int h = live ? (int)(r - (long long)tok * heads) : 0;
+    const int h = live ? (int)(r - tok * heads) : 0;
     const int b = tok / a.N, n = tok - b * a.N;
     const int kind = h < a.Hq ? 0 : h < a.Hq + a.c.kv_heads ? 1 : 2;   // query, key, value
     const int head = kind == 0 ? h : kind == 1 ? h - a.Hq : h - a.Hq - a.c.kv_heads;
@@ -144,9 +146,9 @@ __global__ void __launch_bounds__(kKvThreads) append_kernel(const AppendArgs a) 
 template <int D>
 static cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.B * a.N * (a.Hq + 2 * a.c.kv_heads);
-    const dim3 grid((unsigned)((rows * (D / 8) + kKvThreads - 1) / kKvThreads));
-    return a.c.dtype == SPEC_DTYPE_E4M3 ? launch_pdl(append_kernel<D, true>, grid, kKvThreads, 0, st, a)
-                                        : launch_pdl(append_kernel<D, false>, grid, kKvThreads, 0, st, a);
+    const dim3 grid((unsigned)((rows * (D / 8) + kAppendThreads - 1) / kAppendThreads));
+    return a.c.dtype == SPEC_DTYPE_E4M3 ? launch_pdl(append_kernel<D, true>, grid, kAppendThreads, 0, st, a)
+                                        : launch_pdl(append_kernel<D, false>, grid, kAppendThreads, 0, st, a);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st) {
@@ -275,9 +277,10 @@ cudaError_t launch_kv_read(const spec_kv_cache_t& c, const int32_t* starts, cons
 struct CompactArgs {
     spec_kv_cache_t c;
     const int32_t *ctx, *path, *acc;
-    int N, cpr;                    // 16-byte chunks of a cache row
-    long long cols;                // columns of the cache: layers x {k, v} x heads x cpr
-    long long scale_cols;          // layers x {k, v} x heads (E4M3)
+    int N;
+    unsigned cpr;                  // 16-byte chunks of a cache row
+    unsigned cols;                 // columns of the cache: layers x {k, v} x heads x cpr
+    unsigned scale_cols;           // layers x {k, v} x heads (E4M3)
 };
 
 // A path's ids ascend from at least 1, so node i of the path (from 1) lies
@@ -339,22 +342,18 @@ __global__ void __launch_bounds__(kKvThreads) kv_compact_kernel(const CompactArg
     const int n = acc - first;
     if (n == 0) return;
     const int elt = a.c.dtype == SPEC_DTYPE_E4M3 ? 1 : 2;
-    const long long step = (long long)gridDim.x * kKvThreads;
-    for (long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x; i < a.cols; i += step) {
-        const int chunk = (int)(i % a.cpr);
-        long long r = i / a.cpr;
-        const int head = (int)(r % a.c.kv_heads);
-        r /= a.c.kv_heads;
-        char* base = static_cast<char*>(r & 1 ? a.c.v : a.c.k) +
-                     ((r >> 1) * a.c.layer_stride + head * a.c.head_stride) * elt + chunk * 16;
+    const unsigned step = gridDim.x * kKvThreads, H = a.c.kv_heads;
+    for (unsigned i = blockIdx.x * kKvThreads + threadIdx.x; i < a.cols; i += step) {
+        const unsigned r = i / a.cpr, chunk = i - r * a.cpr, lk = r / H, head = r - lk * H;
+        char* base = static_cast<char*>(lk & 1 ? a.c.v : a.c.k) +
+                     ((int64_t)(lk >> 1) * a.c.layer_stride + head * a.c.head_stride) * elt + chunk * 16;
         for (int j = 0; j < n; ++j)
             *reinterpret_cast<uint4*>(base + moves[4 * j + 1] * elt) =
                 *reinterpret_cast<const uint4*>(base + moves[4 * j] * elt);
     }
-    for (long long i = (long long)blockIdx.x * kKvThreads + threadIdx.x; i < a.scale_cols; i += step) {
-        const int head = (int)(i % a.c.kv_heads);
-        const long long r = i / a.c.kv_heads;
-        float* base = (r & 1 ? a.c.v_scale : a.c.k_scale) + (r >> 1) * a.c.scale_layer_stride +
+    for (unsigned i = blockIdx.x * kKvThreads + threadIdx.x; i < a.scale_cols; i += step) {
+        const unsigned lk = i / H, head = i - lk * H;
+        float* base = (lk & 1 ? a.c.v_scale : a.c.k_scale) + (int64_t)(lk >> 1) * a.c.scale_layer_stride +
                       head * a.c.scale_head_stride;
         for (int j = 0; j < n; ++j) base[moves[4 * j + 3]] = base[moves[4 * j + 2]];
     }
@@ -365,9 +364,9 @@ cudaError_t launch_kv_compact(const spec_kv_cache_t& c, const int32_t* ctx, cons
     CompactArgs a{c, ctx, path, acc, N, 0, 0, 0};
     const bool fp8 = c.dtype == SPEC_DTYPE_E4M3;
     a.cpr = c.head_dim * (fp8 ? 1 : 2) / 16;
-    a.cols = (long long)c.layers * 2 * c.kv_heads * a.cpr;
-    a.scale_cols = fp8 ? (long long)c.layers * 2 * c.kv_heads : 0;
-    long long g = (a.cols + kKvThreads - 1) / kKvThreads;
+    a.cols = (unsigned)c.layers * 2 * c.kv_heads * a.cpr;     // (checked below 2^31)
+    a.scale_cols = fp8 ? (unsigned)c.layers * 2 * c.kv_heads : 0;
+    long long g = ((long long)a.cols + kKvThreads - 1) / kKvThreads;
     if (g > 1024) g = 1024;
     const size_t smem = (size_t)N * 4 * sizeof(int64_t);      // at most 32 KB
     return launch_pdl(kv_compact_kernel, dim3((unsigned)g, (unsigned)B), kKvThreads, smem, st, a);
