@@ -15,9 +15,9 @@
 // unnormalised sum, reference and total in the workspace, and a second small
 // kernel adds them in the order of the shares.
 //
-// Inside a CTA each of the four warps takes its own slice of every tile and
-// its own running softmax, so the warps never wait for one another while
-// streaming: a warp copies its slices with 16-byte cp.async into a ring of its
+// Inside a CTA each of the four warps (or pairs of warps, with 16 rows each) takes its
+// own slice of every tile and its own running softmax, so these never wait for one
+// another while streaming: a warp copies its slices with 16-byte cp.async into a ring of its
 // own.  mma.sync (m16n8k16): 16 rows of queries against 8 positions (scores), then
 // probabilities against 8 head elements (sums).  An E4M3 cache is widened to
 // fp16 (exact) next to the matrix instruction; queries then go in as fp16,
@@ -28,11 +28,13 @@
 namespace sv {
 
 constexpr int kAttWarps = 4;
-constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kAttCtasPerSm = 2;
-
-template <int D, int MT, bool FP8>
+// RG = 2: two sets of kAttWarps warps, each with its own rows, over one ring of
+// slices for every two warps (256 elements, more than 16 rows: 16 rows are what a
+// warp's registers hold, and three stages leave room for one CTA on an SM).
+template <int D, int MT, int RG, bool FP8>
 struct AttCfg {
+    static constexpr int THREADS = kAttWarps * 32 * RG;
+    static constexpr int CTAS = RG == 1 ? 2 : 1;               // on an SM
     static constexpr int ELT = FP8 ? 1 : 2;
     static constexpr int ROWB = D * ELT;                       // bytes of a cached row
     static constexpr int CPR = ROWB / 16;                      // 16-byte chunks of it
@@ -40,13 +42,13 @@ struct AttCfg {
     static constexpr int ST = ST0 < 16 ? 16 : ST0 > 32 ? 32 : ST0;   // positions of a slice
     static constexpr int NT = ST / 8;
     static constexpr int STAGE = 2 * ST * ROWB + (FP8 ? 2 * ST * 4 : 0);
-    static constexpr int NS0 = 24576 / (2 * ST * ROWB);
+    static constexpr int NS0 = 24576 * RG / (2 * ST * ROWB);
     static constexpr int NS = NS0 < 3 ? 3 : NS0 > 6 ? 6 : NS0;       // stages of a warp's ring
-    static constexpr int ROWS = 16 * MT;
+    static constexpr int WROWS = 16 * MT, ROWS = WROWS * RG;    // rows of a warp, of a unit
     static constexpr int TILE = kAttWarps * ST;                // positions of a tile
     static constexpr int OP = D + 8;                           // padded row of the warps' sums
     static constexpr int RING = kAttWarps * NS * STAGE;
-    static constexpr int MERGE = kAttWarps * ROWS * OP * 4;
+    static constexpr int MERGE = kAttWarps * ROWS * OP * 4;   // (a set's warps have its rows)
     // 32 rows of 128 elements: the queries' fragments stay in shared memory (one
     // copy for the four warps), the sums need the registers
     static constexpr bool QSM = MT == 2 && D == 128;
@@ -84,23 +86,29 @@ __device__ __forceinline__ int swz(int t, int c) {
     else return (t * CPR + (c ^ ((t >> 1) & 3))) * 16;          // CPR = 4: two rows per 128 bytes
 }
 
-template <int D, int MT, bool FP8>
-__global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(const AttendArgs a) {
-    using C = AttCfg<D, MT, FP8>;
+template <int D, int MT, int RG, bool FP8>
+__global__ void __launch_bounds__(AttCfg<D, MT, RG, FP8>::THREADS, AttCfg<D, MT, RG, FP8>::CTAS) attend_kernel(const AttendArgs a) {
+    using C = AttCfg<D, MT, RG, FP8>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ AttPlan plan;
     __shared__ unsigned long long anc[2][kMaxNewTree];         // ancestors and itself, by node
     __shared__ short up[2][kMaxNewTree];
     __shared__ float wm[kAttWarps][C::ROWS], wl[kAttWarps][C::ROWS];
-    __shared__ int wbad[kAttWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ int wbad[kAttWarps * RG];
+    const int lane = threadIdx.x & 31;
+    const int set = RG > 1 ? threadIdx.x / (kAttWarps * 32) : 0, warp = (threadIdx.x >> 5) - set * kAttWarps;
+    // the warps that share a ring
+    auto ring_sync = [&] {
+        if constexpr (RG > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + warp), "n"(RG * 32) : "memory");
+        else __syncwarp();
+    };
     const int quad = lane & 3, lrow = lane >> 2;
     pdl_trigger();
     pdl_wait();
 
     const int RT = a.N * a.G;                                  // rows of a cached head
     const int RB = (RT + C::ROWS - 1) / C::ROWS;
-    make_plan<C::TILE, kAttThreads>(a, a.c.kv_heads * RB, gridDim.x, &plan);
+    make_plan<C::TILE, C::THREADS>(a, a.c.kv_heads * RB, gridDim.x, &plan);
     AttWalk walk;
     AttUnit un;
     if ((int)blockIdx.x >= plan.n) {
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int hrow = 0; hrow < 2; ++hrow) {
-                const int r = mt * 16 + hrow * 8 + lrow, R = r0 + r;
+                const int r = set * C::WROWS + mt * 16 + hrow * 8 + lrow, R = r0 + r;
                 const bool on = r < rows;
                 const int n = on ? row_position(a, R) : 0, g = on ? R - n * a.G : 0;
                 rn[mt][hrow] = n;
@@ -255,6 +263,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 const unsigned okm = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
                 for (int p = 0; p < C::ST / RP; ++p) {
+                    if (RG > 1 && p % RG != set) continue;     // (warps of a ring take turns)
                     const int row = p * RP + sub;
                     const int64_t e = __shfl_sync(0xffffffffu, off, row) * C::ELT + ch * 16;
                     const bool in = (okm >> row) & 1u;
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                     cp16(d + C::ST * C::ROWB, static_cast<const char*>(a.c.v) + e, in);
                 }
                 if constexpr (FP8) {
-                    if (lane < C::ST) {
+                    if (lane < C::ST && set == 0) {
                         const uint32_t d = st + 2 * C::ST * C::ROWB + lane * 4;
                         const int64_t soff = ok ? scale_off(a.c, page, slot, hk) : 0;
                         cp4(d, a.c.k_scale + soff, ok);
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
 #pragma unroll 1
         for (int i = 0; i < nsl; ++i) {
             cp_wait<C::NS - 2>();
-            __syncwarp();
+            ring_sync();
             copy(i + C::NS - 1);                                // into the stage read last time round
             locate(i + C::NS);
             const uint32_t ks = ring_s + (i % C::NS) * C::STAGE, vs = ks + C::ST * C::ROWB;
@@ -444,9 +453,9 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                     if (x) odd |= 1u << t0;
                 }
                 odd = __reduce_or_sync(0xffffffffu, odd);
-                while (odd) {                                   // warp-uniform, rare
-                    const int t0 = __ffs(odd) - 1;
-                    odd &= odd - 1u;
+                if (RG > 1 && odd) ring_sync();                 // (all have looked: the same for a ring's warps)
+                for (unsigned left = odd; left; left &= left - 1u) {   // warp-uniform, rare
+                    const int t0 = __ffs(left) - 1;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -477,10 +486,13 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                                     }
                             }
                         }
-                    __syncwarp();
-                    for (int ch = lane; ch < C::CPR; ch += 32)
-                        *reinterpret_cast<uint4*>(vb + swz<C::CPR>(t0, ch)) = make_uint4(0u, 0u, 0u, 0u);
-                    __syncwarp();
+                }
+                if (odd) {
+                    ring_sync();
+                    for (int e = lane; e < C::ST * C::CPR; e += 32)
+                        if ((odd >> (e / C::CPR)) & 1u)
+                            *reinterpret_cast<uint4*>(vb + swz<C::CPR>(e / C::CPR, e % C::CPR)) = make_uint4(0u, 0u, 0u, 0u);
+                    ring_sync();
                 }
             }
             // ---- sums
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         cp_wait<0>();
         lost = __any_sync(0xffffffffu, lost);
         if (lane == 0) {
-            wbad[warp] = lost;
+            wbad[set * kAttWarps + warp] = lost;
             if (lost) raise_error(a.c.error, SPEC_DEVERR_CACHE_RANGE);
         }
 
@@ -534,8 +546,8 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 if (quad == 0) {
-                    wm[warp][mt * 16 + h * 8 + lrow] = m[mt][h];
-                    wl[warp][mt * 16 + h * 8 + lrow] = x;
+                    wm[warp][set * C::WROWS + mt * 16 + h * 8 + lrow] = m[mt][h];
+                    wl[warp][set * C::WROWS + mt * 16 + h * 8 + lrow] = x;
                 }
             }
         __syncthreads();                                        // the rings are drained
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = mt * 16 + h * 8 + lrow;
+                const int r = set * C::WROWS + mt * 16 + h * 8 + lrow;
                 if (r < rows) {
                     if constexpr (!FP8) {
 #pragma unroll
@@ -561,11 +573,11 @@ __global__ void __launch_bounds__(kAttThreads, kAttCtasPerSm) attend_kernel(cons
         __syncthreads();
         bool bad = sl.bad || tree_bad;
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) bad |= wbad[w] != 0;
+        for (int w = 0; w < kAttWarps * RG; ++w) bad |= wbad[w] != 0;
         const bool whole = ta == 0 && tb == tiles;
         const int mine = 2 * (int)blockIdx.x + (ta == 0 ? 1 : 0);
         float* sp = slots + (size_t)mine * slot_floats;
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kAttThreads) {
+        for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
             const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
             float M = kNegInf;
 #pragma unroll
@@ -723,21 +735,21 @@ cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int bloc
                                  : launch_pdl(attend_join_kernel<256>, grid, kJoinThreads, 0, st, a, block_rows, per);
 }
 
-// Rows of a cached head that a unit holds.
-static int att_rows(int N, int G, int D) { return N * G <= 16 || D == 256 ? 16 : 32; }
+// Rows of a cached head that a unit holds, at most.
+static int att_rows(int N, int G) { return N * G <= 16 ? 16 : 32; }   // (16 where elements are 256 and blocks few)
 
 size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D) {
     // the join's notes, then two parts per CTA, for either kernel
-    const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G, D);
+    const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G);
     const size_t here = kAttHead + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
     const size_t tc = attend_takes_tc(N, G, D, false, INT64_MAX) ? attend_tc_workspace(N, G) : 0;
     return here > tc ? here : tc;
 }
 
-template <int D, int MT, bool FP8>
+template <int D, int MT, int RG, bool FP8>
 static cudaError_t launch_attend_t(const AttendArgs& a, cudaStream_t st) {
-    using C = AttCfg<D, MT, FP8>;
-    auto kfn = attend_kernel<D, MT, FP8>;
+    using C = AttCfg<D, MT, RG, FP8>;
+    auto kfn = attend_kernel<D, MT, RG, FP8>;
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
@@ -748,7 +760,7 @@ static cudaError_t launch_attend_t(const AttendArgs& a, cudaStream_t st) {
         if (r != cudaSuccess) return r;
         r = cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (r != cudaSuccess) return r;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(o, kfn, kAttThreads, C::SMEM);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(o, kfn, C::THREADS, C::SMEM);
     });
     if (e != cudaSuccess) return e;
     const long long rb = ((long long)a.N * a.G + C::ROWS - 1) / C::ROWS;
@@ -757,14 +769,28 @@ static cudaError_t launch_attend_t(const AttendArgs& a, cudaStream_t st) {
     if (g > kAttMaxCtas) g = kAttMaxCtas;
     const long long tiles = (long long)a.B * a.c.kv_heads * rb * (most < 1 ? 1 : most);
     if (g > tiles) g = tiles;
-    e = launch_pdl(kfn, dim3((unsigned)g), kAttThreads, C::SMEM, st, a);
+    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a);
     return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, C::ROWS, most, st);
 }
 
 template <int D, bool FP8>
 static cudaError_t launch_attend_d(const AttendArgs& a, cudaStream_t st) {
-    if constexpr (D == 256) return launch_attend_t<D, 1, FP8>(a, st);
-    else return att_rows(a.N, a.G, D) == 16 ? launch_attend_t<D, 1, FP8>(a, st) : launch_attend_t<D, 2, FP8>(a, st);
+    if (att_rows(a.N, a.G) == 16) return launch_attend_t<D, 1, 1, FP8>(a, st);
+    if constexpr (D < 256) return launch_attend_t<D, 2, 1, FP8>(a, st);
+    // Rows of 256 bf16 by two sets of warps where there are more blocks of 16 rows than
+    // SMs, or more than 32 tiles for each SM: 190 us for 270 at 64 x 8 heads x 20 rows over
+    // up to 2000, 88 for 118 at 10 x 8 x 285 rows over 69, 80 for 102 at 8 x 8 x 32 rows over
+    // up to 8000, but 26.2 for 22.8 at 8 heads x 68 rows over 1930 (40 blocks of 31 tiles).
+    // Of E4M3 rows two CTAs fit an SM as it is (202 for 196).
+    if constexpr (D == 256 && !FP8) {
+        DeviceInfo di;
+        const cudaError_t e = device_info(&di);
+        if (e != cudaSuccess) return e;
+        const long long blocks = (long long)a.B * a.c.kv_heads * ((a.N * a.G + 15) / 16);
+        const long long tiles = ((long long)a.c.max_pages * a.c.page_size + 63) / 64;
+        if (blocks > di.sm_count || blocks * tiles > 32LL * di.sm_count) return launch_attend_t<D, 1, 2, FP8>(a, st);
+    }
+    if constexpr (D == 256) return launch_attend_t<D, 1, 1, FP8>(a, st);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {

@@ -400,3 +400,36 @@ def test_cache_layouts(sv, fp8, layout, page):
     got = sv.paged_attention(q.cuda(), cache, c.cuda(), lse=True)
     assert cache.read_error() == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("is_tree", [False, True])
+@pytest.mark.parametrize("Hq,H,ctx", [(8, 2, [60 + 7 * b for b in range(40)]), (6, 1, [40000]), (8, 4, [b % 3 for b in range(30)])])
+def test_wide_heads_many_rows(sv, is_tree, Hq, H, ctx):
+    """Heads of 256, more rows than a matrix tile holds, many blocks of them or many tiles."""
+    check(sv, *case(35, len(ctx), 11, Hq, H, 256, 16, ctx, is_tree=is_tree,
+                    newl=[11 - b % 4 for b in range(len(ctx))]))
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("H", [2, 8])
+def test_wide_heads_masked_values(sv, value, H):
+    """The same with branches' values that are no numbers, several in a slice: only the rows that see
+    them have none, where they have none."""
+    B = 24
+    parts, q, _, c, nb = case(36, B, 12, 4 * H, H, 256, 16, [21 + b for b in range(B)])
+    par = torch.tensor([[-1, 0, 1, 2] + [0] * 8] * B, dtype=torch.int32)    # nodes 4 to 11 are leaves
+    want = sv.paged_attention(q.cuda(), R.on_gpu(sv, parts), c.cuda(), parents=par.cuda())
+    table = parts[2]
+    for b in range(B):
+        for n in (5, 6, 9):
+            pos = 21 + b + n
+            parts[1][int(table[b, pos // 16]), pos % 16, :, n::64] = value
+    got = sv.paged_attention(q.cuda(), R.on_gpu(sv, parts), c.cuda(), parents=par.cuda())
+    for n in range(12):
+        bad = torch.zeros(256, dtype=torch.bool, device="cuda")
+        if n in (5, 6, 9):
+            bad[n::64] = True
+        assert not torch.isfinite(got[:, n][..., bad].float()).any()
+        assert torch.isfinite(got[:, n][..., ~bad].float()).all()
+        if n not in (5, 6, 9):
+            assert torch.equal(got[:, n], want[:, n])
