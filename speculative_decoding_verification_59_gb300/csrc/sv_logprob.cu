@@ -300,6 +300,7 @@ __device__ __forceinline__ int load_chunk(const LogprobArgs& a, int r, long long
             if (j + PV > a.V) bits &= (1u << (a.V - j)) - 1u;
             row |= (unsigned long long)bits << (8 * t);
             const bool whole = begin + at + (lane + 32 * t) * 16 + 16 <= tensor_bytes;
+            if (bits == (1u << PV) - 1u && whole) continue;    // (most lanes' by far)
             uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
 #pragma unroll
             for (int e = 0; e < PV; ++e) {
@@ -441,12 +442,18 @@ __device__ __forceinline__ void put_list(const LogprobArgs& a, int r, bool empty
 }
 
 // Short rows (up to kRowChunks warp chunks): one CTA does all of a row, its
-// chunks straight from memory, in one launch.  Through the ring, a 32 KB stage
-// carried one short row: 14714 rows of 1400 bf16 logits took 184 us.
-constexpr int kRowChunks = 16;
+// chunks straight from memory, in one launch.  Through the ring a 32 KB stage
+// carries one short row, and the lists of many rows cost a second kernel more than
+// here.  bf16, us here / through the ring: 33.5 / 538 for 14714 rows of 1400 with 5
+// alternatives, 29.7 / 36.3 for 2048 of 16000, 45.4 / 45.4 of 32000; without lists
+// 17.8 / 57.1 and 17.1 / 19.4 for 4000 of 8000, 2.9 / 4.1 for 64 of 16000, but
+// 17.7 / 13.9 for 2048 of 16000 (a CTA a row does not keep the memory busy): there the
+// ring takes the rows of more than kFewChunks.  With lists three CTAs an SM (80
+// registers) are worth the spills: 29.7 for 56.3.
+constexpr int kRowChunks = 16, kFewChunks = 4;
 constexpr int kRowWarps = 8;
 template <int ELT, bool LISTS>
-__global__ void __launch_bounds__(kRowWarps * 32) logprob_row_kernel(const LogprobArgs a, int chunks) {
+__global__ void __launch_bounds__(kRowWarps * 32, LISTS ? 3 : 1) logprob_row_kernel(const LogprobArgs a, int chunks) {
     constexpr int KC = kMaxAlternatives;
     __shared__ float part[kRowWarps][3], lmax[kRowChunks][32]; // the lanes' maxima of every chunk
     __shared__ Pool pool;
@@ -688,7 +695,7 @@ size_t logprobs_workspace_size(int rows, int V, int K) {
 template <int ELT>
 static cudaError_t launch_logprobs_e(const LogprobArgs& a, const DeviceInfo& di, cudaStream_t st) {
     const int span = (int)(((long long)a.V * ELT + (16 - ELT) + 32 * kLaneBytes - 1) / (32 * kLaneBytes));     // warp chunks of a row
-    if (span <= kRowChunks) {
+    if (span <= kRowChunks && (a.K > 0 || span <= kFewChunks || (long long)a.rows * span <= kRowChunks * di.sm_count)) {
         const int turns = (span + kRowWarps - 1) / kRowWarps, warps = (span + turns - 1) / turns;
         const dim3 grid((unsigned)a.rows);
         if (a.K == 0) return launch_pdl(logprob_row_kernel<ELT, false>, grid, warps * 32, 0, st, a, span);

@@ -184,3 +184,14 @@ def test_shapes_and_refusals(sv):
         sv.token_logprobs(z.cuda().half(), tok.cuda(), 2)
     with pytest.raises(sv.SpecVerifyError):
         sv.token_logprobs(z.cuda(), tok.cuda(), 2, temperature=0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V,K", [(700, 8999, 0), (700, 8999, 1), (2600, 2001, 0), (30, 32001, 0), (610, 10300, 0)])
+def test_many_middling_rows(sv, dtype, rows, V, K):
+    """Rows of a few chunks, enough of them for the stream and too few for it."""
+    g = torch.Generator().manual_seed(V + rows)
+    z = (torch.randn(rows, V, generator=g) * 3).to(dtype)
+    z[torch.rand(rows, V, generator=g) < 0.05] = -math.inf
+    z[:, V // 3] = 1.0
+    check(sv, z, torch.randint(0, V, (rows,), generator=g, dtype=torch.int32), K, 0.8)
