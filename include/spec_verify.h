@@ -367,7 +367,8 @@ spec_status_t spec_verify_sample_noalloc(const void* target_logits, const void* 
  *
  *   dtype BF16: no scales.
  *   dtype E4M3: element = e4m3 value * scale, one fp32 scale for each (page,
- *     slot, head), at k_scale / v_scale with the scale_* strides (elements).
+ *     slot, head), at k_scale / v_scale with the scale_* strides (elements),
+ *     zero or positive as spec_kv_append writes them.
  *
  * head_dim is 64, 128 or 256; page_size, num_pages, max_pages >= 1.  k and v
  * are 16-byte aligned and their strides multiples of 16 bytes

