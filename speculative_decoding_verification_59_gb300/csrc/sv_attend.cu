@@ -10,7 +10,8 @@
 // Work split.  A unit's positions are cut into tiles; all units' tiles, laid
 // end to end, are dealt to the CTAs in equal contiguous shares, computed on
 // the device from the lengths (ragged batches balance, and a captured call
-// follows its lengths).  A share may end one unit and begin the next.  A unit
+// follows its lengths).  A share may end one unit and begin the next.  (Short units are
+// dealt whole.)  A unit
 // within one share is written at once; otherwise each CTA leaves its
 // unnormalised sum, reference and total in the workspace, and a second small
 // kernel adds them in the order of the shares.
@@ -728,8 +729,19 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     }
 }
 
+// Short units are not worth splitting: the second launch, the parts, CTAs that begin
+// two units.  How short depends on how many CTAs would have nothing to do (us whole /
+// by tiles; 8 cached heads, 4 rows of 128, but for * 48 rows on the tcgen05 kernel, and for
+// + 32 rows of 64): 8 units of 250 positions 6.6 / 6.9, of 380 8.1 / 7.1; 64 of 380 8.6 /
+// 9.0 and * 13.3 / 19.7, of 630 11.5 / 10.6; 160 of 500 11.2 / 12.2, + 12.2 / 16.1, but *
+// 28.1 / 25.8; 512 of 250 13.5 / 17.0, * 36.8 / 44.7, + 16.3 / 22.6, of 630 28.7 / 29.9, * 70.6
+// / 73.2, + 25.9 / 32.7, of 1000 40.8 / 40.4, * 67.6 / 75.0, + 39.1 / 38.1.
+bool attend_whole(long long units, long long positions, long long ctas) {
+    return positions <= 256 || (positions <= 512 && 4 * units >= ctas) || (positions <= 768 && 2 * units >= 3 * ctas);
+}
+
 cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int block_rows, long long tiles, cudaStream_t st) {
-    if (tiles == 1) return cudaSuccess;                        // no unit is split
+    if (a.whole) return cudaSuccess;                           // no unit is split
     // about four parts a warp
     long long parts = ctas / units + 2;
     if (parts > tiles) parts = tiles;
@@ -773,10 +785,12 @@ static cudaError_t launch_attend_t(const AttendArgs& a, cudaStream_t st) {
     const long long most = ((long long)a.c.max_pages * a.c.page_size + C::TILE - 1) / C::TILE;   // tiles of a unit
     long long g = (long long)di.sm_count * occ;
     if (g > kAttMaxCtas) g = kAttMaxCtas;
-    const long long tiles = (long long)a.B * a.c.kv_heads * rb * (most < 1 ? 1 : most);
-    if (g > tiles) g = tiles;
-    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a);
-    return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, C::ROWS, most, st);
+    const long long units = (long long)a.B * a.c.kv_heads * rb;
+    AttendArgs w = a;
+    w.whole = most == 1 || attend_whole(units, (long long)a.c.max_pages * a.c.page_size, g);
+    if (g > units * (w.whole ? 1 : most)) g = units * (w.whole ? 1 : most);
+    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, w);
+    return e != cudaSuccess ? e : launch_join(w, (int)g, units, C::ROWS, most, st);
 }
 
 template <int D, bool FP8>

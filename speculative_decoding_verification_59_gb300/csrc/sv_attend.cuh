@@ -84,7 +84,7 @@ __host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size
 
 struct AttPlan {
     int n;                   // CTAs that take part
-    long long total;         // tiles of all units
+    long long total;         // tiles of all units (or units, where they are dealt whole)
     int b;                   // sequence of this CTA's first tile
     long long at;            // that sequence's first tile
 };
@@ -98,7 +98,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& a, int units, int gr
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += max(1, (seq_len(a, b).total + TILE - 1) / TILE);
+    for (int b = b0; b < b1; ++b) mine += a.whole ? 1 : max(1, (seq_len(a, b).total + TILE - 1) / TILE);
     mine *= units;
     long long incl = mine;
 #pragma unroll
@@ -119,7 +119,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& a, int units, int gr
     const long long first = blockIdx.x < n ? share_begin(total, n, blockIdx.x) : -1;
     if (first >= at && first < at + mine) {
         for (int b = b0; b < b1; ++b) {
-            const long long t = (long long)units * max(1, (seq_len(a, b).total + TILE - 1) / TILE);
+            const long long t = (long long)units * (a.whole ? 1 : max(1, (seq_len(a, b).total + TILE - 1) / TILE));
             if (first < at + t) {
                 out->b = b;
                 out->at = at;
@@ -162,23 +162,23 @@ struct AttWalk {
         const int units = a.c.kv_heads * RB;
         while (t < end) {
             const SeqLen sl = seq_len(a, b);
-            const int tiles = max(1, (sl.total + TILE - 1) / TILE);
-            if (t >= seq_at + (long long)tiles * units) {       // the share goes on in the next sequence
-                seq_at += (long long)tiles * units;
+            const int tiles = max(1, (sl.total + TILE - 1) / TILE), dealt = a.whole ? 1 : tiles;
+            if (t >= seq_at + (long long)dealt * units) {       // the share goes on in the next sequence
+                seq_at += (long long)dealt * units;
                 ++b;
                 continue;
             }
             x->b = b;
             x->sl = sl;
             x->tiles = tiles;
-            x->u = (int)quotient(t - seq_at, tiles);
-            x->at = seq_at + (long long)x->u * tiles;
+            x->u = (int)quotient(t - seq_at, dealt);
+            x->at = seq_at + (long long)x->u * dealt;
             x->ta = (int)(t - x->at);
-            x->tb = (int)min((long long)tiles, end - x->at);
+            x->tb = a.whole ? tiles : (int)min((long long)tiles, end - x->at);
             x->hk = x->u / RB;
             x->r0 = (x->u - x->hk * RB) * block_rows;
             x->rows = min(block_rows, a.N * a.G - x->r0);
-            t = x->at + x->tb;
+            t = a.whole ? x->at + 1 : x->at + x->tb;
             return true;
         }
         return false;
@@ -210,6 +210,9 @@ __device__ __forceinline__ void put_row(const AttendArgs& a, int b, int hk, int 
 // Joins the parts that `ctas` CTAs of the call's kernel have left, units of up to
 // `units` row blocks of block_rows rows, `tiles` tiles at most (sv_attend.cu).
 cudaError_t launch_join(const AttendArgs& a, int ctas, long long units, int block_rows, long long tiles, cudaStream_t st);
+
+// Whether a call deals its units whole: `units` of them, of up to `positions`, to `ctas`.
+bool attend_whole(long long units, long long positions, long long ctas);
 
 // The matrix-unit kernel of sv_attend_tc.cu (rows of 128 elements).
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);

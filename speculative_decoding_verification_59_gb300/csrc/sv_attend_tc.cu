@@ -1173,8 +1173,10 @@ static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cuda
     const long long rb = ((long long)a.N * a.G + block_rows - 1) / block_rows;
     const long long most = ((long long)a.c.max_pages * a.c.page_size + kTcTile - 1) / kTcTile;   // tiles of a unit
     long long g = di.sm_count < kTcMaxCtas ? di.sm_count : kTcMaxCtas;
-    const long long tiles = (long long)a.B * a.c.kv_heads * rb * most;
-    if (g > tiles) g = tiles;
+    const long long units = (long long)a.B * a.c.kv_heads * rb;
+    AttendArgs w = a;
+    w.whole = most == 1 || attend_whole(units, (long long)a.c.max_pages * a.c.page_size, g);
+    if (g > units * (w.whole ? 1 : most)) g = units * (w.whole ? 1 : most);
     // TMA boxes: one page, or 128 of its slots; tiles then begin and end with boxes
     const int ps = a.c.page_size;
     int box = ps % kTcTile == 0 ? kTcTile : ps >= 8 && kTcTile % ps == 0 ? ps : 0;
@@ -1182,8 +1184,8 @@ static cudaError_t launch_tc_t(const AttendArgs& a, int block_rows, int rp, cuda
     const Places at = places_of(a.c);
     if (at.unit == 0 || (box > 0 && (!encode_map(&km, a.c, a.c.k, box, at) || !encode_map(&vm, a.c, a.c.v, box, at)))) box = 0;
     const uint32_t limit = ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit;
-    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, a, block_rows, rp, box, at.pages, at.heads, limit, km, vm);
-    return e != cudaSuccess ? e : launch_join(a, (int)g, a.B * a.c.kv_heads * rb, block_rows, most, st);
+    e = launch_pdl(kfn, dim3((unsigned)g), C::THREADS, C::SMEM, st, w, block_rows, rp, box, at.pages, at.heads, limit, km, vm);
+    return e != cudaSuccess ? e : launch_join(w, (int)g, units, block_rows, most, st);
 }
 
 template <bool FP8>

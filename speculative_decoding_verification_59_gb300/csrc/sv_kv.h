@@ -41,6 +41,7 @@ struct AttendArgs {
     int B, N, Hq, G;                       // G query heads per cached head
     uint32_t g_mul;                        // ceil(2^32 / G), for G > 1: R / G = mulhi(R, g_mul), R < 2^32 / G
     int page_shift;                        // log2(page_size), -1 when it is no power of two
+    int whole;                             // units are dealt whole, not by tiles (set at the launch)
     char* out;                             // bf16
     float* lse;
     char* ws;

@@ -433,3 +433,16 @@ def test_wide_heads_masked_values(sv, value, H):
         assert torch.isfinite(got[:, n][..., ~bad].float()).all()
         if n not in (5, 6, 9):
             assert torch.equal(got[:, n], want[:, n])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,N,Hq,H,D,longest", [(3, 1, 8, 2, 128, 200), (3, 1, 8, 2, 128, 300), (12, 11, 32, 8, 128, 420),
+                                                (2, 11, 32, 8, 128, 420), (60, 9, 16, 8, 128, 700), (5, 9, 16, 8, 128, 700),
+                                                (50, 5, 32, 8, 64, 500), (70, 2, 16, 8, 256, 240)])
+def test_units_whole_and_split(sv, fp8, B, N, Hq, H, D, longest):
+    """Short contexts on both sides of the bounds up to which a head's positions stay together, the
+    empty one among them, more units than fit at once and fewer."""
+    g = torch.Generator().manual_seed(longest + B)
+    ctx = torch.randint(0, longest, (B,), generator=g).tolist()
+    ctx[0], ctx[-1] = longest - N, 0
+    check(sv, *case(41, B, N, Hq, H, D, 16, ctx, fp8=fp8, newl=[N - b % 2 for b in range(B)]))
