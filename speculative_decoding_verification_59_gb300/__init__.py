@@ -629,7 +629,8 @@ def kv_read(cache: KVCache, T: int, *, starts=None, counts=None, dtype=None, str
     """Cached positions as dense rows (see spec_kv_read): (k, v), each [B, T, kv_heads,
     head_dim] of dtype (bfloat16 by default, or float32), row t holding position
     starts[b] + t for t < counts[b], zeros after that.  B is the length of starts or
-    counts, or the cache's batch."""
+    counts, or the cache's batch.  Small results (up to 2^20 elements) share one
+    allocation."""
     f32 = False
     if dtype is not None:
         if dtype not in _logits_dtypes():

@@ -8,7 +8,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/core/Allocator.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -148,7 +149,9 @@ void fits(const Cache& c, int64_t B) {
 struct OnStream {
     cudaStream_t h;
     std::optional<c10::cuda::CUDAStreamGuard> guard;
+    std::optional<c10::cuda::CUDAGuard> other;               // the tensors are not the current device's
     OnStream(PyObject* stream, int device) {
+        if (c10::cuda::current_device() != device) other.emplace((c10::DeviceIndex)device);
         if (stream == Py_None) {
             h = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
             return;
@@ -163,8 +166,11 @@ struct OnStream {
     }
 };
 
-at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type, int device) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)device)));
+// A new tensor on the current device, which OnStream has made the call's: straight
+// from torch's allocator (at::empty's way there takes the host 0.4 us more).
+at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type) {
+    static c10::Allocator* const from = c10::GetAllocator(c10::kCUDA);
+    return at::detail::empty_generic(shape, from, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
 // A contiguous tensor over a stretch of another's storage, from element `at` of
@@ -176,6 +182,8 @@ at::Tensor stretch(const at::Tensor& whole, c10::IntArrayRef shape, at::ScalarTy
     t.unsafeGetTensorImpl()->set_storage_offset(at);
     return t;
 }
+
+constexpr int64_t kSharedOutput = 1 << 20;     // elements of an output that may share its allocation
 
 // The default workspace of one kind of call on one stream of one device: calls
 // on different streams overlap and must not share one.  Kept for later calls,
@@ -191,7 +199,7 @@ at::Tensor scratch(int kind, int device, cudaStream_t h, size_t need) {
     const auto it = kept->find(key);
     if (it != kept->end() && (size_t)it->second.nbytes() >= need) return it->second;
     const size_t n = need < kHeadBytes ? kHeadBytes : need;
-    at::Tensor t = empty({(int64_t)n}, at::kByte, device);
+    at::Tensor t = empty({(int64_t)n}, at::kByte);
     const spec_status_t s = spec_verify_workspace_init(t.data_ptr(), kHeadBytes, h);
     if (s != SPEC_OK) throw StatusFail{s, "spec_verify_workspace_init"};
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) (*kept)[key] = t;
@@ -297,7 +305,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* op = nullptr;
         if (a[3] != Py_None) {
             if (a[14] == Py_None) {
-                out = empty({k.B, k.N, q.H, D}, at::kBFloat16, c.device);
+                out = empty({k.B, k.N, q.H, D}, at::kBFloat16);
                 op = out.data_ptr();
             } else {
                 op = plain<void>(a[14], "out", at::kBFloat16, {k.B, k.N, q.H, D}, c.device);
@@ -330,8 +338,19 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool f32 = truth(a[6]);
         const OnStream on(a[7], c.device);
         const int64_t shape[4] = {B, T, c.c->kv_heads, c.c->head_dim};
-        const at::Tensor k = empty(shape, f32 ? at::kFloat : at::kBFloat16, c.device);
-        const at::Tensor v = empty(shape, f32 ? at::kFloat : at::kBFloat16, c.device);
+        // a small call's two outputs in one allocation (1 us of the host's time each); large
+        // ones apart, so that either can be given up without the other
+        const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
+        const int64_t n = B * T * shape[2] * shape[3];
+        at::Tensor k, v;
+        if (n > 0 && n <= kSharedOutput) {
+            const at::Tensor both = empty({2 * n}, type);
+            k = stretch(both, shape, type, 0);
+            v = stretch(both, shape, type, n);
+        } else {
+            k = empty(shape, type);
+            v = empty(shape, type);
+        }
         done(spec_kv_read(c.c, starts, counts, (int)B, (int)T, f32 ? SPEC_DTYPE_F32 : SPEC_DTYPE_BF16, k.data_ptr(),
                           v.data_ptr(), on.h),
              "spec_kv_read");
@@ -375,14 +394,14 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor out, lse;
         void* op;
         if (a[9] == Py_None) {
-            out = empty({q.B, q.N, q.H, D}, at::kBFloat16, c.device);
+            out = empty({q.B, q.N, q.H, D}, at::kBFloat16);
             op = out.data_ptr();
         } else {
             op = plain<void>(a[9], "out", at::kBFloat16, {q.B, q.N, q.H, D}, c.device);
             out = *tensor_of(a[9], "out");
         }
         const bool want = truth(a[8]);
-        if (want) lse = empty({q.B, q.N, q.H}, at::kFloat, c.device);
+        if (want) lse = empty({q.B, q.N, q.H}, at::kFloat);
         const at::Tensor ws = workspace_of(a[10], 0, c.device, on.h, need);
         done(spec_paged_attention(c.c, q.p, q.stride, ctx, newl, par, scale, (int)q.B, (int)q.N, (int)q.H, op,
                                   want ? static_cast<float*>(lse.data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(), on.h),
@@ -414,7 +433,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const OnStream on(a[5], device);
         // one allocation for the four outputs, 4 bytes an element: an allocation takes
         // the host 1.2 us, and a call on a few short rows the GPU 3.7
-        const at::Tensor all = empty({rows * (2 + 2 * K)}, at::kFloat, device);
+        const at::Tensor all = empty({rows * (2 + 2 * K)}, at::kFloat);
         const at::Tensor lp = stretch(all, lead, at::kFloat, 0), ent = stretch(all, lead, at::kFloat, rows);
         at::Tensor ti, tl;
         if (K > 0) {
