@@ -39,12 +39,12 @@
 // rescaling of O run when one does: on a unit's first tile, and rarely after.
 //
 // Measured (lengths from half of the stated one to all of it, 8 cached heads):
-//   64 sequences x 32 rows over 4096, bf16: 139 us, 5.8 TB/s of the cache's 812 MB, 86 % of
+//   64 sequences x 32 rows over 4096, bf16: 140 us, 5.8 TB/s of the cache's 812 MB, 86 % of
 //     a plain copy's rate.  Memory bounds the tiles; what is left is units' begins and ends.
-//   32 trees x 144 rows over 2048, bf16: 95.6 us, 310 TFLOP/s.  A tile's softmax is four
+//   32 trees x 144 rows over 2048, bf16: 97.3 us, 305 TFLOP/s.  A tile's softmax is four
 //     dependent steps of some 700 to 1500 cycles together 3700 (scores, vote, powers, P),
 //     and a unit begins and ends in some 13000, mostly code that is not at hand.
-//   8 sequences x 32 rows over 32768, E4M3: 108.5 us, 3.7 TB/s: the same softmax, 2600
+//   8 sequences x 32 rows over 32768, E4M3: 109.6 us, 3.6 TB/s: the same softmax, 2600
 //     cycles for a tile that the memory brings in 1400.
 #include <cuda.h>
 
