@@ -24,6 +24,9 @@
 // fp16 (exact) next to the matrix instruction; queries then go in as fp16,
 // each row scaled by a power of two, and a position's key scale multiplies
 // its score, its value scale its probability (as a summand of the exponent).
+// Probabilities then are fp16 too, whose steps end at 2^-24: a row's reference is
+// kept kFp16Head below its largest score, where fp16 still holds the largest
+// (2^(kFp16Head + kRefSlack)), so that next to nothing is what is lost.
 //
 // Measured (8 cached heads of 128, bf16, lengths from half of the stated one to all of it):
 // 64 sequences x 4 rows over 4000 in 127 us, 6.2 TB/s of the cache's 0.79 GB, memory-bound;
@@ -35,6 +38,7 @@
 namespace sv {
 
 constexpr int kAttWarps = 4;
+constexpr float kFp16Head = 7.f;
 // RG = 2: two sets of kAttWarps warps, each with its own rows, over one ring of
 // slices for every two warps (256 elements, more than 16 rows: 16 rows are what a
 // warp's registers hold, and three stages leave room for one CTA on an SM).
@@ -392,14 +396,14 @@ __global__ void __launch_bounds__(AttCfg<D, MT, RG, FP8>::THREADS, AttCfg<D, MT,
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     mx[mt][h] = x;
-                    grow |= x > m[mt][h] + kRefSlack;
+                    grow |= x > m[mt][h] + kRefSlack + (FP8 ? kFp16Head : 0.f);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float mn = mx[mt][h] > m[mt][h] ? mx[mt][h] : m[mt][h];
+                        const float to = FP8 ? mx[mt][h] - kFp16Head : mx[mt][h], mn = to > m[mt][h] ? to : m[mt][h];
                         const float f = m[mt][h] == kNegInf ? 0.f : ex2_approx(m[mt][h] - mn);
                         m[mt][h] = mn;
                         l[mt][h] *= f;

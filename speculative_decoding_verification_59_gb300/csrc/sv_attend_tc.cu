@@ -23,11 +23,13 @@
 //             other page sizes, and the tiles with new positions, where stale
 //             entries are left out, by the threads' 16-byte cp.async.
 // An E4M3 cache is multiplied as it lies (kind::f8f6f4), the other operand split
-// into e4m3 terms, each the rounding of sixteen times what the one before left
-// over: two for a query (a bf16 significand has two e4m3 significands' bits), three
-// for a probability (12 bits, as fp16 would have).  The terms are columns of their
-// own: S has two columns a row, O three, weighed 1, 1/16, 1/256 when they are
-// read.  (Widening the cache to fp16 in shared memory instead moved three times the
+// into e4m3 terms: two for a query (a bf16 significand has two e4m3 significands'
+// bits), the second the rounding of 16 times what the first left over; three for a
+// probability, each the rounding of 32 times what the one before left over (at most
+// 8, of values up to 2^8).  The terms are columns of their own: S has two columns a
+// row, O three, weighed 1, 1/32, 1/1024 when they are read.  A probability keeps 12
+// bits, but no step below 2^-19, so a row's largest is held at 2^kTcHead and
+// up: what is less than 2^-(20 + kTcHead) of it counts as nothing.  (Widening the cache to fp16 in shared memory instead moved three times the
 // bytes there and bound the kernel: 183 us for 8 x 32768 positions.)
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
@@ -67,6 +69,17 @@ constexpr uint32_t kTcWaitLimit = 1u << 18;
 constexpr int kTcMaxCtas = 256;
 static_assert(kTcMaxCtas <= kAttMaxCtas, "a note for each");
 constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
+// E4M3: a moved reference lies this far below the row's largest score (in powers of
+// two), and moves with any growth once the vote has stopped the warpgroup: weights
+// down to 2^-24 of the largest count, as they would in fp16.  (At 0, and with terms
+// 16 times apart, a score 18 powers of two above 8192 others took the 3 % of the weight
+// that those held.)  More range costs more stops, as a row may grow by less before one:
+// for scores of two standard deviations, 4 / 5 / 7 took 106 / 114 / 121 us for 32 trees of
+// 64 rows over up to 2048 positions (0 / 0: 93), 144 / 149 / 169 (142) for 64 x 20 rows
+// over up to 4000, 128 / 129 / 140 (130) for 8 x 32 rows over up to 32768 (calls one at
+// a time).
+constexpr float kTcHead = 4.f;
+static_assert(kTcHead < kRefSlack, "a score that stops the warpgroup moves its reference");
 
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
@@ -275,7 +288,7 @@ __device__ __forceinline__ uint32_t e4m3_term(float& a, float& b) {
 }
 
 // The same of a pair of fp16 values (both steps are exact there): their e4m3
-// roundings, and sixteen times what those leave over.
+// roundings, and 32 times what those leave over.
 __device__ __forceinline__ uint32_t e4m3_of_f16x2(uint32_t p) {
     unsigned short t;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(p));
@@ -283,7 +296,7 @@ __device__ __forceinline__ uint32_t e4m3_of_f16x2(uint32_t p) {
 }
 __device__ __forceinline__ uint32_t left_over_f16x2(uint32_t p, uint32_t t) {
     uint32_t r;
-    asm("{\n\t.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(p), "r"(e4m3_to_f16x2(t)), "r"(0x4c004c00u));
+    asm("{\n\t.reg .b32 d;\n\tsub.f16x2 d, %1, %2;\n\tmul.f16x2 %0, d, %3;\n\t}" : "=r"(r) : "r"(p), "r"(e4m3_to_f16x2(t)), "r"(0x50005000u));
     return r;
 }
 
@@ -854,10 +867,10 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     if (row < chunks * 16) {
                         const int w0 = wg * 4;
                         const float x = fmaxf(fmaxf(wred[w0][row], wred[w0 + 1][row]), fmaxf(wred[w0 + 2][row], wred[w0 + 3][row]));
-                        const float m = -nref[c0 + row];
-                        const bool up = x > m + kRefSlack;
-                        nref[c0 + row] = up ? -x : -m;
-                        alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - x);
+                        const float m = -nref[c0 + row], to = FP8 ? x - kTcHead : x;
+                        const bool up = FP8 ? to > m : x > m + kRefSlack;
+                        nref[c0 + row] = up ? -to : -m;
+                        alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - to);
                     }
                     named_sync(bar, 128);
 #pragma unroll
@@ -1018,7 +1031,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     tc_ld8(lanes + C::O_AT + rp + c0 + k0, y);
                     tc_ld8(lanes + C::O_AT + 2 * rp + c0 + k0, z);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(z[k], 0.0625f, y[k]), 0.0625f, v[k]);
+                    for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(z[k], 0.03125f, y[k]), 0.03125f, v[k]);
                 }
                 if (odd_any) {
                     const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);
