@@ -186,23 +186,29 @@ at::Tensor stretch(const at::Tensor& whole, c10::IntArrayRef shape, at::ScalarTy
 constexpr int64_t kSharedOutput = 1 << 20;     // elements of an output that may share its allocation
 
 // The default workspace of one kind of call on one stream of one device: calls
-// on different streams overlap and must not share one.  Kept for later calls,
-// except when first needed inside a capture: that one belongs to the graph.
-// Never freed at exit (the CUDA context may be gone by then).
+// on different streams overlap and must not share one.  Kept for later calls until
+// one needs more, and never freed at exit (the CUDA context may be gone by then).
+// A captured call gets one of its own, never the kept one: a graph would go on
+// writing there after a larger call has given it back, or, replayed on another
+// stream, beside a call on this one.  Its memory is the graph's (the allocator
+// serves a capture from that graph's pool), its error word is not cleared,
+// as nobody can read it.
 constexpr size_t kHeadBytes = 256;       // what a call may want zeroed once (the error word)
 at::Tensor scratch(int kind, int device, cudaStream_t h, size_t need) {
     using Key = std::tuple<int, int, cudaStream_t>;
     static std::mutex* lock = new std::mutex;
     static auto* kept = new std::map<Key, at::Tensor>;
     const Key key{kind, device, h};
+    const size_t n = need < kHeadBytes ? kHeadBytes : need;
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+        return empty({(int64_t)n}, at::kByte);
     const std::lock_guard<std::mutex> hold(*lock);
     const auto it = kept->find(key);
     if (it != kept->end() && (size_t)it->second.nbytes() >= need) return it->second;
-    const size_t n = need < kHeadBytes ? kHeadBytes : need;
     at::Tensor t = empty({(int64_t)n}, at::kByte);
     const spec_status_t s = spec_verify_workspace_init(t.data_ptr(), kHeadBytes, h);
     if (s != SPEC_OK) throw StatusFail{s, "spec_verify_workspace_init"};
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) (*kept)[key] = t;
+    (*kept)[key] = t;
     return t;
 }
 at::Tensor workspace_of(PyObject* given, int kind, int device, cudaStream_t h, size_t need) {
