@@ -29,8 +29,9 @@
 // 8, of values up to 2^8).  The terms are columns of their own: S has two columns a
 // row, O three, weighed 1, 1/32, 1/1024 when they are read.  A probability keeps 12
 // bits, but no step below 2^-19, so a row's largest is held at 2^kTcHead and
-// up: what is less than 2^-(20 + kTcHead) of it counts as nothing.  (Widening the cache to fp16 in shared memory instead moved three times the
-// bytes there and bound the kernel: 183 us for 8 x 32768 positions.)
+// up: what is less than 2^-(20 + kTcHead) of it counts as nothing.  (Widening the
+// cache to fp16 in shared memory instead moved three times the bytes there and bound
+// the kernel: 183 us for 8 x 32768 positions.)
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
 //
@@ -74,10 +75,10 @@ constexpr float kNoRef = -1e30f;                 // reference of a row that has 
 // down to 2^-24 of the largest count, as they would in fp16.  (At 0, and with terms
 // 16 times apart, a score 18 powers of two above 8192 others took the 3 % of the weight
 // that those held.)  More range costs more stops, as a row may grow by less before one:
-// for scores of two standard deviations, 4 / 5 / 7 took 106 / 114 / 121 us for 32 trees of
-// 64 rows over up to 2048 positions (0 / 0: 93), 144 / 149 / 169 (142) for 64 x 20 rows
-// over up to 4000, 128 / 129 / 140 (130) for 8 x 32 rows over up to 32768 (calls one at
-// a time).
+// for scores of two standard deviations, 3 / 4 took 97 / 103 us for 32 trees of 64 rows
+// over up to 2048 positions (0 / 0: 93), 138 / 142 (142) for 64 x 20 rows over up to 4000,
+// 124 / 124 (130) for 8 x 32 rows over up to 32768 (calls one at a time); 5 and 7, with
+// stops that cost some 2 % more, 114 and 121, 149 and 169, 129 and 140.
 constexpr float kTcHead = 4.f;
 static_assert(kTcHead < kRefSlack, "a score that stops the warpgroup moves its reference");
 
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ __align__(8) uint64_t k_full[KB], k_empty[KB], v_full[VB], v_empty[VB], s_full[2], s_free[2], p_full, pv_done,
         q_full[C::QB], q_free[C::QB], drained[2];
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
+    __shared__ __align__(16) float delta[FP8 ? RP : 4];        // E4M3: by how much a reference moved, negative
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
     __shared__ __align__(16) int rowat[RP];                                   // its row of the output, from the sequence's first
@@ -682,6 +684,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         int tree_b = -1;
         bool dead = false;                                     // a wait ran out: the same for the warpgroup,
         bool late = false;                                     // once it has voted on this
+        bool open = false;                                     // E4M3: a row has no reference yet (uniform)
         float l[CH * 16];
         while (walk.next<kTcTile>(a, RB, block_rows, &un)) {
             const SeqLen& sl = un.sl;
@@ -844,7 +847,23 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         break;
                     }
                     tc_after();
-                    for (int ch = 0; ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
+                    // E4M3, once all rows have a reference: from the scores at hand, which are relative
+                    // to it (reading them again, 115 us for 112 at 8 x 32 rows over up to 32768; before,
+                    // their rounding would be that of a difference to no reference)
+                    const bool near = FP8 && !first && !open;
+                    if constexpr (FP8)
+                        if (near) {
+#pragma unroll
+                            for (int ch = 0; ch < CH; ++ch)
+                                if (ch < chunks) {
+                                    float v[16];
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) v[j] = x[ch * 16 + j];
+                                    const float y = fold16(v, lane, Max{});
+                                    if (!(lane & 1)) wred[warp][ch * 16 + fold_column(lane)] = y;
+                                }
+                        }
+                    for (int ch = 0; !near && ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
                         float v[16];
                         tc_ld16(s_at + ch * 16, v);
                         if constexpr (FP8) {
@@ -867,12 +886,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     if (row < chunks * 16) {
                         const int w0 = wg * 4;
                         const float x = fmaxf(fmaxf(wred[w0][row], wred[w0 + 1][row]), fmaxf(wred[w0 + 2][row], wred[w0 + 3][row]));
-                        const float m = -nref[c0 + row], to = FP8 ? x - kTcHead : x;
+                        const float m = -nref[c0 + row], to = (near ? m + x : x) - (FP8 ? kTcHead : 0.f);
                         const bool up = FP8 ? to > m : x > m + kRefSlack;
                         nref[c0 + row] = up ? -to : -m;
                         alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - to);
+                        if constexpr (FP8) delta[c0 + row] = up ? m - to : 0.f;
                     }
-                    named_sync(bar, 128);
+                    if constexpr (FP8) open = named_any(bar, 128, row < chunks * 16 && nref[c0 + row] == -kNoRef);
+                    else named_sync(bar, 128);
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch)
                         if (ch < chunks) {
@@ -890,7 +911,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                                 }
                             }
                         }
-                    if constexpr (C::KEEP) score_all(Yes{});
+                    if (near) {
+                        if constexpr (FP8)
+#pragma unroll
+                            for (int j = 0; j < CH * 16; ++j)
+                                if (j / 16 < chunks) x[j] += delta[c0 + j];
+                    } else if constexpr (C::KEEP) {
+                        score_all(Yes{});
+                    }
                 }
                 // ---- probabilities; P is free once the tile before has been summed
                 if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
