@@ -476,8 +476,9 @@ spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* conte
  *   lse    [B, N, q_heads] fp32, nullable
  * q_heads is a multiple of kv_heads, at most 64 times it.  Scores, softmax
  * statistics and sums are fp32.  Positions n >= n_b give out = 0 and lse =
- * -inf.  A bad sequence (or a malformed tree, SPEC_DEVERR_TREE_PARENT) gives
- * NaN.  What the masked entries of the cache hold does not matter, NaN and
+ * -inf.  The others of a bad sequence (or of a malformed tree,
+ * SPEC_DEVERR_TREE_PARENT) give NaN, and where the lengths themselves are bad
+ * all N do.  What the masked entries of the cache hold does not matter, NaN and
  * infinities included.
  *
  * Workspace: spec_attention_workspace_size() bytes, 256-byte aligned, of any

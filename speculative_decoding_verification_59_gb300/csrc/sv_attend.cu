@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(AttCfg<D, MT, RG, FP8>::THREADS, AttCfg<D, MT,
             }
             if (bad) L = CUDART_NAN_F;
             if (whole) {
-                put_row(a, b, hk, r0, sl.nb, bad, D, r, d, x, L, M);
+                put_row(a, b, hk, r0, sl.nb, sl.bad, D, r, d, x, L, M);
             } else {
                 __stcg(reinterpret_cast<float4*>(sp + (size_t)r * D + d), x);
                 if (d == 0) {

@@ -195,12 +195,14 @@ __device__ __forceinline__ void note_split(const AttendArgs& a, const AttPlan& p
 }
 
 // Writes elements d .. d + 3 of row r of a finished unit: row r0 + r of cached head
-// hk of sequence b, which has nb new positions.
-__device__ __forceinline__ void put_row(const AttendArgs& a, int b, int hk, int r0, int nb, bool bad, int D, int r, int d,
+// hk of sequence b, which has nb new positions.  Rows past those are empty, whatever
+// else the sequence has, a bad page or a malformed tree (whose total is NaN), unless
+// its lengths are bad: then nobody knows which rows they are.
+__device__ __forceinline__ void put_row(const AttendArgs& a, int b, int hk, int r0, int nb, bool bad_lengths, int D, int r, int d,
                                         float4 v, float lsum, float mref) {
     const int R = r0 + r, n = row_position(a, R), g = R - n * a.G;
     const size_t row = ((size_t)b * a.N + n) * a.Hq + (size_t)hk * a.G + g;
-    const bool empty = n >= nb && !bad;
+    const bool empty = n >= nb && !bad_lengths;
     const float f = empty ? 0.f : 1.f / lsum;
     if (empty) v = make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<uint2*>(a.out + (row * D + d) * 2) = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));

@@ -1038,7 +1038,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 const int r = c0 + row;
                 const float m = -nref[r];
                 if (whole) {
-                    const bool none = rown[r] >= sl.nb && !bad;
+                    const bool none = rown[r] >= sl.nb && !sl.bad;         // (as in put_row)
                     alpha[r] = none ? 0.f : 1.f / lsum;
                     if (a.lse) a.lse[(size_t)un.b * a.N * a.Hq + rowat[r]] = none ? kNegInf : (m + __log2f(lsum)) * kLn2;
                 } else {
