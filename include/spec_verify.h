@@ -504,7 +504,8 @@ spec_status_t spec_paged_attention(const spec_kv_cache_t* cache, const void* q,
  * padded with -1 and -inf.  A masked (-inf) logit has ln p = -inf and adds
  * nothing to the entropy.  A token outside [0, V) gives ln p = NaN and sets
  * SPEC_DEVERR_TOKEN_RANGE; a row of -inf alone gives NaN everywhere (list
- * tokens -1) and sets SPEC_DEVERR_EMPTY_ROW.  Sums are fp32.  Logits are
+ * tokens -1) and sets SPEC_DEVERR_EMPTY_ROW, and so does, with SPEC_DEVERR_TIMEOUT, a row
+ * of which a wait that ran out has left something unread.  Sums are fp32.  Logits are
  * 16-byte aligned; V and its row length need no alignment.  Workspace:
  * spec_logprobs_workspace_size(rows, V, K) bytes, 256-byte aligned, its first
  * 256 bytes zero-filled once (the error word).

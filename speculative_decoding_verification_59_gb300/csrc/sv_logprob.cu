@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
     }
     const int cw = warp - 1;
     bool ok = true;
-    for (unsigned c = c0; c < c1; ++c) {
+    unsigned c = c0;
+    for (; c < c1; ++c) {
         const unsigned it = c - c0;
         const int st = (int)(it % kStages);
         if (!wait_bounded(&full[st], (it / kStages) & 1u, a.wait_limit)) ok = false;
@@ -232,7 +233,10 @@ __global__ void __launch_bounds__(kRingThreads, 2) logprob_stream_kernel(const L
             a.stats[pi] = make_float4(m, Z, W, 0.f);
         }
     }
-    if (!ok && lane == 0) atomicOr(a.err, SPEC_DEVERR_TIMEOUT);
+    if (c == c1) return;
+    // a wait ran out: the sums of the chunks not seen are no numbers, and so are their rows' results
+    for (c += lane; c < c1; c += 32) a.stats[(size_t)c * kWarps + cw] = make_float4(0.f, CUDART_NAN_F, CUDART_NAN_F, 0.f);
+    if (lane == 0) atomicOr(a.err, SPEC_DEVERR_TIMEOUT);
 }
 
 // The first K of warp_merge_topk (sv_stream.cuh); the other entries say none.
@@ -426,7 +430,8 @@ __device__ __forceinline__ void pick_chunk(const uint4 (&v)[kVecPerLane], unsign
 __device__ __forceinline__ void put_row(const LogprobArgs& a, int r, bool empty, bool tok_ok, float zx, float M, float lnz,
                                         float inner) {
     a.lp[r] = empty || !tok_ok ? CUDART_NAN_F : (zx - M) / a.T - lnz;
-    if (a.ent) a.ent[r] = empty ? CUDART_NAN_F : fmaxf(0.f, lnz - kLn2f * inner);
+    const float ent = lnz - kLn2f * inner;
+    if (a.ent) a.ent[r] = empty ? CUDART_NAN_F : ent < 0.f ? 0.f : ent;       // (a row without sums: NaN)
     if (empty) atomicOr(a.err, SPEC_DEVERR_EMPTY_ROW);
     if (!tok_ok) atomicOr(a.err, SPEC_DEVERR_TOKEN_RANGE);
 }
@@ -637,12 +642,13 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
         // ---- the chunks that reach the bound, a warp each; every lane keeps the
         // best of its logits
         float thr = thr_key == kNoKey ? kNegInf : key_value(thr_key);
+        const bool none = empty || Z != Z;                     // (a wait of the stream ran out)
         for (int i = threadIdx.x; i < P; i += kMergeThreads) {
             const float m = i == (int)threadIdx.x ? first.x : __ldcg(st + i).x;
-            if (m >= thr && (m > kNegInf || !empty)) sel[atomicAdd(&n_sel, 1)] = (unsigned short)i;
+            if (m >= thr && !none) sel[atomicAdd(&n_sel, 1)] = (unsigned short)i;
         }
         __syncthreads();
-        const int n = empty ? 0 : n_sel;
+        const int n = none ? 0 : n_sel;
         for (int c = warp; c < n; c += NW) {
             uint4 v[kVecPerLane];
             unsigned long long row;
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
         if (got <= kPool) {                                    // uniform
             if (warp == 0) {
                 pool_lists(pool, got, a.K, ov, oi);
-                if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
+                if (lane == 0) put_list(a, r, none, M, lnz, ov, oi);
             }
             return;
         }
@@ -678,7 +684,7 @@ __global__ void __launch_bounds__(kMergeThreads) logprob_merge_kernel(const Logp
             L.init();
             L.insert(list_v[lane / KC][lane & (KC - 1)], list_i[lane / KC][lane & (KC - 1)]);
             merge_lists<KC>(L, a.K, ov, oi);
-            if (lane == 0) put_list(a, r, empty, M, lnz, ov, oi);
+            if (lane == 0) put_list(a, r, none, M, lnz, ov, oi);
         }
     }
 }
