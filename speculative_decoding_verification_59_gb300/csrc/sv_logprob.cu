@@ -56,14 +56,15 @@ __device__ __forceinline__ void row_span(const LogprobArgs& a, int elt, int r, l
 // 2^-r W' - r Z).  Masked logits (-inf) would give 0 x inf in W: logits are
 // first raised to one whose power is zero, bf16 ones two an instruction.  Where
 // no such logit is near (tiny temperatures, where one step of a bf16 logit
-// already counts; chunks of the type's lowest value) the arguments (z - m) s
+// already counts; chunks of the type's lowest value; temperatures past 1e36, 256
+// powers of two below the maximum being past fp32's range) the arguments (z - m) s
 // are clamped instead.
 template <int ELT>
 __device__ __forceinline__ void chunk_sums(const uint4 (&v)[kVecPerLane], float m, float s, float inv_s, float* Z, float* W) {
     f32x2 z2 = f2_pack(0.f, 0.f), w2 = z2;
     float r = 0.f;
     const float below = kArgFloor * inv_s;                     // 256 powers of two below the maximum
-    if (m < -3.3e38f || !(below <= -fabsf(m) * 0.015625f)) {   // warp-uniform
+    if (!(m + below > -3.3e38f) || !(below <= -fabsf(m) * 0.015625f)) {   // warp-uniform
 #pragma unroll
         for (int t = 0; t < kVecPerLane; ++t)
 #pragma unroll
@@ -79,7 +80,7 @@ __device__ __forceinline__ void chunk_sums(const uint4 (&v)[kVecPerLane], float 
         const float ms = m * s;
         r = fmaf(m, s, -ms);
         const f32x2 s2 = f2_pack(s, s), off = f2_pack(-ms, -ms);
-        const float low = fmaxf(m + below, -3.3e38f);          // finite, and its bf16 rounding too
+        const float low = m + below;                           // finite, and its bf16 rounding too
         uint32_t low2;
         asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(low2) : "f"(low));
 #pragma unroll

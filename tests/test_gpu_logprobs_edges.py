@@ -46,3 +46,23 @@ def test_a_wait_that_runs_out_leaves_no_numbers(sv, dtype, K):
     again = sv.token_logprobs(z, tok, K, workspace=ws)
     assert all(a is b is None or torch.equal(a, b) for a, b in zip(again, want))
     assert sv.spec_verify_read_error(ws.data_ptr(), stream) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1000, 30001, 151937])
+@pytest.mark.parametrize("T", [1e30, 1e36, 1e38, 3e38])
+def test_masked_logits_at_the_largest_temperatures(sv, dtype, V, T):
+    """A masked logit has no weight at any temperature; the others' are all but equal.  Tolerances
+    as in test_gpu_logprobs.py."""
+    g = torch.Generator().manual_seed(V)
+    z = (torch.randn((4, V), generator=g) * 3).to(dtype)
+    z[0, ::3] = -math.inf
+    z[1, 5:] = -math.inf
+    z[2, :V // 2] = -math.inf
+    tok = torch.tensor([1, 4, V - 1, 0], dtype=torch.int32)
+    lp, ent, ti, tl = (t.cpu() for t in sv.token_logprobs(z.cuda(), tok.cuda(), 4, temperature=T))
+    l, e, i, t = R.logprobs(z, tok, 4, T)
+    assert ((lp.double() - l).abs() <= 2.0 ** -18 + 2.0 ** -22 * l.abs()).all()
+    assert ((ent.double() - e).abs() <= 2.0 ** -18 * (1 + e + math.log(V))).all()
+    assert torch.equal(ti.long(), i)
+    assert ((tl.double() - t).abs() <= 2.0 ** -18 + 2.0 ** -22 * t.abs()).all()
