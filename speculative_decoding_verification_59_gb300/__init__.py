@@ -539,6 +539,12 @@ def _marshal():
     return _marshal_module
 
 
+def _scratch(workspace: Workspace, head: int, need: int, stream):
+    """The bytes of a Workspace from `head` on, grown to head + need, as _marshal takes them."""
+    workspace.get_bytes(head + need, stream)
+    return workspace.buf[head:]
+
+
 class KVCache:
     """A paged key-value cache (see spec_kv_cache_t): views of the caller's tensors,
     checked once.
@@ -655,9 +661,15 @@ def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=N
     spec_paged_attention).  q [B, N, q_heads, head_dim] bfloat16, context_lens [B] int32,
     parents [B, N] int32 for draft trees (None: chains), new_lens [B] int32 or None; scale
     defaults to head_dim ** -0.5.  Returns out [B, N, q_heads, head_dim] bfloat16, with
-    lse=True also [B, N, q_heads] float32.  workspace: a uint8 tensor of
-    spec_attention_workspace_size() bytes, of any contents, that no call on another stream
-    uses at the same time (None: one kept for the device and stream)."""
+    lse=True also [B, N, q_heads] float32.  workspace: a Workspace (the first 256 bytes, with its
+    error word, are left alone), or a uint8 tensor of spec_attention_workspace_size() bytes, of
+    any contents, that no call on another stream uses at the same time.  None: one kept for
+    the device and stream from the first such call to the program's end, as large as the
+    largest has needed (some 38 MB for 144 rows of 128 per cached head); a captured call gets one
+    of its graph's."""
+    if isinstance(workspace, Workspace):
+        workspace = _scratch(workspace, 256, load_library().spec_attention_workspace_size(
+            q.shape[0], q.shape[1], q.shape[2], cache.kv_heads, cache.head_dim), stream)
     return (_marshal_module or _marshal()).paged_attention(
         cache.addr, cache.batch, cache.index, q, context_lens, parents, new_lens,
         cache.scale if scale is None else scale, lse, out, workspace, stream)
@@ -668,7 +680,12 @@ def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, work
     """Log-probabilities of tokens with entropies and top alternatives (see
     spec_token_logprobs).  logits [..., V] contiguous bfloat16 or float32, tokens [...]
     int32.  Returns (logprob [...], entropy [...], top_idx [..., K] int32, top_logprob
-    [..., K]), which share one allocation; the last two None for K = 0.  workspace: a uint8 tensor of
-    spec_logprobs_workspace_size() bytes, its first 256 zero (None: one kept for the
-    device and stream)."""
+    [..., K]), which share one allocation; the last two None for K = 0.  workspace: a Workspace, whose
+    read_error() then tells of bad tokens and empty rows (NaN in the results either way), or a
+    uint8 tensor of spec_logprobs_workspace_size() bytes, its first 256 zero.  None: one kept
+    for the device and stream to the program's end, as large as the largest call has needed (a
+    captured call gets one of its graph's), whose error word is not read."""
+    if isinstance(workspace, Workspace):
+        workspace = _scratch(workspace, 0, load_library().spec_logprobs_workspace_size(
+            logits.numel() // max(logits.shape[-1], 1), logits.shape[-1], K), stream)
     return (_marshal_module or _marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)

@@ -66,3 +66,45 @@ def test_masked_logits_at_the_largest_temperatures(sv, dtype, V, T):
     assert ((ent.double() - e).abs() <= 2.0 ** -18 * (1 + e + math.log(V))).all()
     assert torch.equal(ti.long(), i)
     assert ((tl.double() - t).abs() <= 2.0 ** -18 + 2.0 ** -22 * t.abs()).all()
+
+
+def test_the_packages_workspaces(sv):
+    """A Workspace serves the log-probability and attention calls as it does the verification calls,
+    in turn with them, grows with them, and its error word tells what went wrong."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ws = sv.Workspace()
+    z = torch.randn((9, 50257), generator=g, device="cuda") * 3
+    tok = torch.randint(0, 50257, (9,), generator=g, device="cuda").to(torch.int32)
+    cache = sv.KVCache(*R.make_cache_on_gpu(3, 2, 3000, 16, 2, 128))
+    q = torch.randn((2, 9, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+    ctx = torch.tensor([2900, 40], dtype=torch.int32, device="cuda")
+    draft = tok.view(3, 3)[:, :2].contiguous()
+    calls = [lambda **k: sv.token_logprobs(z, tok, 3, **k), lambda **k: sv.paged_attention(q, cache, ctx, lse=True, **k),
+             lambda **k: sv.verify_greedy(z.view(3, 3, -1), draft, **k), lambda **k: sv.token_logprobs(z[:1], tok[:1], 0, **k)]
+    want = [f() for f in calls]
+    for _ in range(3):
+        for f, w in zip(calls, want):
+            assert all(a is b is None or torch.equal(a, b) for a, b in zip(f(workspace=ws), w))
+            assert ws.read_error() == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = sv.Workspace()
+    got = [f(workspace=other, stream=side) for f in calls]
+    torch.cuda.synchronize()
+    for r, w in zip(got, want):
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(r, w))
+    tok[4] = -1
+    z[7] = -math.inf
+    lp, *_ = calls[0](workspace=ws)
+    assert torch.isnan(lp[[4, 7]]).all()
+    calls[1](workspace=ws)                                     # leaves the error word alone
+    assert ws.read_error() == sv.SPEC_DEVERR_TOKEN_RANGE | sv.SPEC_DEVERR_EMPTY_ROW
+    for bad in (torch.zeros(64, device="cuda"), "ws", 7):
+        with pytest.raises(TypeError):
+            calls[0](workspace=bad)
+        with pytest.raises(TypeError):
+            calls[1](workspace=bad)
+    with pytest.raises(ValueError):
+        sv.token_logprobs(z, tok, 9, workspace=ws)
+    with pytest.raises(ValueError):
+        sv.paged_attention(q[:, :, :7].contiguous(), cache, ctx, workspace=ws)
