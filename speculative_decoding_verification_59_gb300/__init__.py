@@ -528,10 +528,14 @@ _marshal_module = None
 def _marshal():
     global _marshal_module
     if _marshal_module is None:
-        _torch()
+        torch = _torch()
         load_library()
         import importlib
+        from . import _build
         try:
+            # (one of another torch may load and take its classes for something else)
+            if not _build.marshal_matches(os.path.dirname(torch.__file__)):
+                raise ImportError("_marshal.so was built with another torch or Python")
             _marshal_module = importlib.import_module("._marshal", __name__)
         except ImportError as e:
             raise ImportError(f"{os.path.join(_HERE, '_marshal.so')} is not built for this torch; run "

@@ -6,14 +6,19 @@ runtime is linked statically, so the library only needs the driver.
 
 _marshal.so, the torch marshalling of the calls that run on every layer
 (csrc/sv_torch.cpp), is host code: compiled beside them with g++ against the
-installed torch, linked to libspecverify.so.
+installed torch, linked to libspecverify.so.  It uses torch's C++ classes, so it
+is built again when torch or Python is another one than it was built with, and
+left out where torch is not installed (libspecverify.so does not need it).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_STAMP = os.path.join(BUILD, "sv_torch.stamp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -39,12 +45,34 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _marshal_commands():
+def _torch_dir():
+    """Where torch is installed, without importing it (minutes on a cold machine); None if it is not."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None or not spec.origin else os.path.dirname(spec.origin)
+
+
+def _marshal_stamp(torch_dir: str) -> str:
+    """What _marshal.so depends on beside its sources: torch, by its place and version file, and
+    Python, by its extension modules' suffix."""
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return "\n".join((torch_dir, str(sysconfig.get_config_var("EXT_SUFFIX")), version))
+
+
+def marshal_matches(torch_dir: str) -> bool:
+    """Whether _marshal.so was built for this torch and Python."""
+    try:
+        with open(MARSHAL_STAMP) as f:
+            return f.read() == _marshal_stamp(torch_dir)
+    except OSError:
+        return False
+
+
+def _marshal_commands(torch_dir: str):
     """(source, object, compile command, link command) of _marshal.so."""
-    import importlib.util
-    import sysconfig
-    # the package's place without importing it (minutes on a cold machine)
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     src, obj = os.path.join(CSRC, "sv_torch.cpp"), os.path.join(BUILD, "sv_torch.o")
     inc = [INCLUDE, os.path.join(torch_dir, "include"),
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -77,8 +105,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(" ".join(cmd), flush=True)
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
-    msrc, mobj, mcompile, mlink = _marshal_commands()
-    if force or _stale(mobj, [msrc, os.path.join(INCLUDE, "spec_verify.h")]):
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        print("torch is not installed: _marshal.so, which the cache, attention and log-probability "
+              "helpers of the Python package need, is left out", file=sys.stderr)
+    else:
+        msrc, mobj, mcompile, mlink = _marshal_commands(torch_dir)
+        remake = force or not marshal_matches(torch_dir)
+    if torch_dir is not None and (remake or _stale(mobj, [msrc, os.path.join(INCLUDE, "spec_verify.h")])):
         if verbose:
             print(" ".join(mcompile), flush=True)
         procs.append((mcompile, subprocess.Popen(mcompile, stdout=subprocess.PIPE,
@@ -100,13 +134,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or _stale(MARSHAL, [mobj, LIB]):
+    if torch_dir is not None and (remake or _stale(MARSHAL, [mobj, LIB])):
         tmp = MARSHAL + ".tmp%d" % os.getpid()
         subprocess.run([tmp if x == MARSHAL else x for x in mlink], check=True)
         os.replace(tmp, MARSHAL)
+        with open(MARSHAL_STAMP, "w") as f:
+            f.write(_marshal_stamp(torch_dir))
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))
