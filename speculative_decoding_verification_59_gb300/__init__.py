@@ -525,7 +525,7 @@ def verify_tree_greedy(target, node_tokens, parents, *, workspace: Optional[Work
 _marshal_module = None
 
 
-def _marshal():
+def _load_marshal():          # (importing the submodule binds the package's name _marshal to it)
     global _marshal_module
     if _marshal_module is None:
         torch = _torch()
@@ -630,7 +630,7 @@ def kv_append(cache: KVCache, q, k, v, context_lens, rope=None, *, q_weight=None
     projection are fine.  context_lens [B] int32, rope [rows, rot_dim] float32 (cosines, then
     sines) or None, weights [head_dim] bfloat16 or None, positions [B, N] int32 or None,
     new_lens [B] int32 or None.  Returns the prepared queries [B, N, q_heads, head_dim]."""
-    return (_marshal_module or _marshal()).kv_append(
+    return (_marshal_module or _load_marshal()).kv_append(
         cache.addr, cache.batch, cache.index, q, k, v, context_lens, rope, q_weight, k_weight, eps,
         interleaved, new_lens, positions, out, stream)
 
@@ -646,7 +646,7 @@ def kv_read(cache: KVCache, T: int, *, starts=None, counts=None, dtype=None, str
         if dtype not in _logits_dtypes():
             raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
         f32 = dtype == _torch().float32
-    return (_marshal_module or _marshal()).kv_read(
+    return (_marshal_module or _load_marshal()).kv_read(
         cache.addr, cache.batch, cache.index, T, starts, counts, f32, stream)
 
 
@@ -654,7 +654,7 @@ def kv_compact(cache: KVCache, context_lens, path_nodes, num_accepted, *, stream
     """Moves the accepted path of every sequence's draft tree to the front of its slots, in
     every layer (see spec_kv_compact).  path_nodes [B, N] and num_accepted [B] are
     verify_tree_greedy's."""
-    (_marshal_module or _marshal()).kv_compact(
+    (_marshal_module or _load_marshal()).kv_compact(
         cache.addr, cache.batch, cache.index, context_lens, path_nodes, num_accepted, stream)
 
 
@@ -674,7 +674,7 @@ def paged_attention(q, cache: KVCache, context_lens, *, parents=None, new_lens=N
     if isinstance(workspace, Workspace):
         workspace = _scratch(workspace, 256, load_library().spec_attention_workspace_size(
             q.shape[0], q.shape[1], q.shape[2], cache.kv_heads, cache.head_dim), stream)
-    return (_marshal_module or _marshal()).paged_attention(
+    return (_marshal_module or _load_marshal()).paged_attention(
         cache.addr, cache.batch, cache.index, q, context_lens, parents, new_lens,
         cache.scale if scale is None else scale, lse, out, workspace, stream)
 
@@ -692,4 +692,4 @@ def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, work
     if isinstance(workspace, Workspace):
         workspace = _scratch(workspace, 0, load_library().spec_logprobs_workspace_size(
             logits.numel() // max(logits.shape[-1], 1), logits.shape[-1], K), stream)
-    return (_marshal_module or _marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)
+    return (_marshal_module or _load_marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)

@@ -103,6 +103,16 @@ def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
     monkeypatch.setattr(sv, "_marshal_module", None)
     monkeypatch.setattr(_build, "marshal_matches", lambda d: False)
     with pytest.raises(ImportError, match="not built for this torch"):
-        sv._marshal()
+        sv._load_marshal()
     monkeypatch.undo()
-    assert sv._marshal() is sys.modules[sv.__name__ + "._marshal"]
+    assert sv._load_marshal() is sys.modules[sv.__name__ + "._marshal"]
+
+
+def test_two_threads_load_the_module_at_once(monkeypatch):
+    """Another thread that finds the module imported, but not yet noted, loads it too."""
+    torch = pytest.importorskip("torch")
+    module = sv._load_marshal()
+    monkeypatch.setattr(sv, "_marshal_module", None)
+    with pytest.raises(ValueError, match="CUDA"):
+        sv.token_logprobs(torch.zeros((2, 10)), torch.zeros(2, dtype=torch.int32))
+    assert sv._marshal_module is module
