@@ -148,8 +148,9 @@ void fits(const Cache& c, int64_t B) {
 // allocated under it, so that the allocator reuses their memory in its order.
 struct OnStream {
     cudaStream_t h;
-    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    // (in this order: the stream's guard, made second, has to be the first to go)
     std::optional<c10::cuda::CUDAGuard> other;               // the tensors are not the current device's
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
     OnStream(PyObject* stream, int device) {
         if (c10::cuda::current_device() != device) other.emplace((c10::DeviceIndex)device);
         if (stream == Py_None) {
