@@ -106,7 +106,7 @@ Rows rows_of(PyObject* o, const char* name, int64_t D, int device) {
     const auto s = t.strides();
     if (s[3] != 1 || (s[2] != D && r.H > 1) || (s[0] != r.N * s[1] && r.B > 1 && r.N > 1))
         throw PyFail{PyExc_ValueError, std::string(name) + ": heads must lie side by side and tokens one stride apart, got strides " + shape_text(s)};
-    r.stride = r.N > 1 ? s[1] : s[0];
+    r.stride = r.N > 1 ? s[1] : r.B > 1 ? s[0] : r.H * D;      // (of one token any stride may stand there)
     return r;
 }
 void same_rows(const Rows& r, const char* name, int64_t B, int64_t N, int64_t H) {

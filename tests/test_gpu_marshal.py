@@ -58,3 +58,20 @@ def test_the_current_device_stays_when_the_tensors_are_anothers(sv):
                 f()
                 assert current() == before
     torch.cuda.synchronize(1)
+
+
+def test_one_token_has_no_stride(sv):
+    """A single token's row cut from a buffer whose rows are of any length."""
+    cache = sv.KVCache(*R.make_cache_on_gpu(5, 1, 64, 16, 2, 64))
+    ctx = torch.tensor([7], dtype=torch.int32, device="cuda")
+    buffer = torch.randn(3, 1, 8 * 64 + 3, device="cuda").to(torch.bfloat16)
+    q, k, v = buffer[:, :, :512].view(3, 1, 8, 64)[:1].split((4, 2, 2), 2)
+    assert q.stride(0) % 8
+    prepared = sv.kv_append(cache, q, k, v, ctx)
+    assert torch.equal(prepared, q)
+    got = [t[0, 7] for t in sv.kv_read(cache, 8)]
+    assert torch.equal(got[0], k[0, 0]) and torch.equal(got[1], v[0, 0])
+    assert torch.equal(sv.paged_attention(q, cache, ctx), sv.paged_attention(q.contiguous(), cache, ctx))
+    with pytest.raises(sv.SpecVerifyError):                    # two such rows are as far apart as they say
+        two = torch.randn(2, 1, 8 * 64 + 3, device="cuda").to(torch.bfloat16)[:, :, :256].view(2, 1, 4, 64)
+        sv.paged_attention(two, sv.KVCache(cache.k, cache.v, cache.block_table.repeat(2, 1)), ctx.repeat(2))
