@@ -187,7 +187,9 @@ at::Tensor stretch(const at::Tensor& whole, c10::IntArrayRef shape, at::ScalarTy
 constexpr int64_t kSharedOutput = 1 << 20;     // elements of an output that may share its allocation
 
 // The default workspace of one kind of call on one stream of one device: calls
-// on different streams overlap and must not share one.  Kept for later calls until
+// on different streams overlap and must not share one.  (Host threads may share a
+// stream: a call keeps the interpreter's lock over its launches, so no other's
+// come between an attention kernel and the join of its parts.)  Kept for later calls until
 // one needs more, and never freed at exit (the CUDA context may be gone by then).
 // A captured call gets one of its own, never the kept one: a graph would go on
 // writing there after a larger call has given it back, or, replayed on another

@@ -75,3 +75,50 @@ def test_one_token_has_no_stride(sv):
     with pytest.raises(sv.SpecVerifyError):                    # two such rows are as far apart as they say
         two = torch.randn(2, 1, 8 * 64 + 3, device="cuda").to(torch.bfloat16)[:, :, :256].view(2, 1, 4, 64)
         sv.paged_attention(two, sv.KVCache(cache.k, cache.v, cache.block_table.repeat(2, 1)), ctx.repeat(2))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_host_threads(sv, shared):
+    """Six threads make their calls at once, with the default workspaces: each on a stream of its own,
+    or all on one.  Every result is that of the call made alone."""
+    def job(i):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        N, longest = 1 + 5 * (i % 3), 700 + 900 * (i % 4)
+        cache = sv.KVCache(*R.make_cache_on_gpu(i, 2, longest + N, 16, 2, 128, fp8=i % 2 == 1))
+        q = torch.randn((2, N, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+        k, v = (torch.randn((2, N, 2, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        ctx = torch.tensor([longest, 40 + i], dtype=torch.int32, device="cuda")
+        z = torch.randn((20 + 30 * i, 30011), generator=g, device="cuda") * 3
+        tok = torch.randint(0, 30011, (len(z),), generator=g, device="cuda").to(torch.int32)
+
+        def run(stream, reps):
+            out = []
+            for _ in range(reps):
+                p = sv.kv_append(cache, q, k, v, ctx, stream=stream)
+                out.append((*sv.paged_attention(p, cache, ctx, lse=True, stream=stream), *sv.kv_read(cache, 60, stream=stream),
+                            *sv.token_logprobs(z, tok, 4, stream=stream)))
+            stream.synchronize()
+            return out
+        return run
+    jobs = [job(i) for i in range(6)]
+    torch.cuda.synchronize()
+    one = torch.cuda.Stream()
+    got, wrong = [None] * 6, []
+
+    def worker(i):
+        try:
+            got[i] = jobs[i](one if shared else torch.cuda.Stream(), 25)
+        except Exception as e:                                 # reported below
+            wrong.append((i, repr(e)))
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    torch.cuda.synchronize()
+    for i in range(6):
+        alone = jobs[i](torch.cuda.Stream(), 1)[0]
+        torch.cuda.synchronize()
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, alone))
