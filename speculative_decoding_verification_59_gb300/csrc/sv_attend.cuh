@@ -19,8 +19,8 @@ constexpr size_t kAttHead = kAttMaxCtas * sizeof(AttSplit);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The reference m of a row moves only when a score passes it by more than
-// this (in powers of two): sums stay below 2^8 per position, and the sums in
-// registers are rarely rescaled.
+// this (in powers of two): probabilities stay below 2^8 (E4M3 in sv_attend.cu:
+// 2^(kFp16Head + 8)), and the sums are rarely rescaled.
 constexpr float kRefSlack = 8.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {

@@ -24,14 +24,18 @@
 //             entries are left out, by the threads' 16-byte cp.async.
 // An E4M3 cache is multiplied as it lies (kind::f8f6f4), the other operand split
 // into e4m3 terms: two for a query (a bf16 significand has two e4m3 significands'
-// bits), the second the rounding of 16 times what the first left over; three for a
-// probability, each the rounding of 32 times what the one before left over (at most
-// 8, of values up to 2^8).  The terms are columns of their own: S has two columns a
-// row, O three, weighed 1, 1/32, 1/1024 when they are read.  A probability keeps 12
-// bits, but no step below 2^-19, so a row's largest is held at 2^kTcHead and
-// up: what is less than 2^-(20 + kTcHead) of it counts as nothing.  (Widening the
-// cache to fp16 in shared memory instead moved three times the bytes there and bound
-// the kernel: 183 us for 8 x 32768 positions.)
+// bits), the second the rounding of 16 times what the first left over; four for a
+// probability, each the rounding of 32 times what the one before left over (at
+// most 8, of values up to 2^8), which hold what fp16 does, steps of 2^-24 included.
+// The terms are columns of their own: S has two columns a row, O four, weighed 1,
+// 2^-5, 2^-10, 2^-15 when they are read.  (Three terms have the significand's bits, but
+// no steps below 2^-17, or 2^-19 at 32 times: one score far above thousands of others
+// took the weight that those have together.  With references 2^4 below the rows' largest
+// scores, three reach 2^-23 of those, but the references then move often: 105.3 us for 95.5
+// with four, 91 with three and no such range, at 32 trees of 64 rows over up to 2048;
+// 149 / 143.6 / 133 for 64 x 32 rows over up to 4000, 114.5 / 116 / 113.8 for 8 x 32 rows
+// over up to 32768.  Widening the cache to fp16 in shared memory moved three times the
+// bytes there and bound the kernel: 183 us for 8 x 32768 positions.)
 // Scores pass through two buffers in tensor memory, so the next tile's first
 // product runs beside this tile's softmax.
 //
@@ -70,17 +74,6 @@ constexpr uint32_t kTcWaitLimit = 1u << 18;
 constexpr int kTcMaxCtas = 256;
 static_assert(kTcMaxCtas <= kAttMaxCtas, "a note for each");
 constexpr float kNoRef = -1e30f;                 // reference of a row that has seen no position
-// E4M3: a moved reference lies this far below the row's largest score (in powers of
-// two), and moves with any growth once the vote has stopped the warpgroup: weights
-// down to 2^-24 of the largest count, as they would in fp16.  (At 0, and with terms
-// 16 times apart, a score 18 powers of two above 8192 others took the 3 % of the weight
-// that those held.)  More range costs more stops, as a row may grow by less before one:
-// for scores of two standard deviations, 3 / 4 took 97 / 103 us for 32 trees of 64 rows
-// over up to 2048 positions (0 / 0: 93), 138 / 142 (142) for 64 x 20 rows over up to 4000,
-// 124 / 124 (130) for 8 x 32 rows over up to 32768 (calls one at a time); 5 and 7, with
-// stops that cost some 2 % more, 114 and 121, 149 and 169, 129 and 140.
-constexpr float kTcHead = 4.f;
-static_assert(kTcHead < kRefSlack, "a score that stops the warpgroup moves its reference");
 
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
@@ -90,7 +83,7 @@ struct TcCfg {
     static constexpr int COLS = CH * 16;         // rows of a softmax warpgroup
     static constexpr int RP = NSM * COLS;        // rows of a unit, at most
     static constexpr int BUF = kTcTile * kTcD * (FP8 ? 1 : 2);   // a tile's keys or values
-    static constexpr int QT = FP8 ? 2 : 1, PT = FP8 ? 3 : 1;     // terms of a query, of a probability
+    static constexpr int QT = FP8 ? 2 : 1, PT = FP8 ? 4 : 1;     // terms of a query, of a probability
     static constexpr int PROWS = FP8 ? 128 : 64; // columns of P in 128 bytes
     static constexpr int PB = (PT * RP + PROWS - 1) / PROWS;     // blocks of them
     static constexpr int QB = FP8 || RP == 64 ? 2 : 1;          // units whose queries are held
@@ -335,7 +328,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
     __shared__ __align__(8) uint64_t k_full[KB], k_empty[KB], v_full[VB], v_empty[VB], s_full[2], s_free[2], p_full, pv_done,
         q_full[C::QB], q_free[C::QB], drained[2];
     __shared__ __align__(16) float nref[RP], alpha[RP];        // minus the rows' references; the rescaling
-    __shared__ __align__(16) float delta[FP8 ? RP : 4];        // E4M3: by how much a reference moved, negative
     __shared__ float wred[NSM * 4][C::COLS];
     __shared__ short rown[RP];                                  // new position of a row
     __shared__ __align__(16) int rowat[RP];                                   // its row of the output, from the sequence's first
@@ -684,7 +676,6 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
         int tree_b = -1;
         bool dead = false;                                     // a wait ran out: the same for the warpgroup,
         bool late = false;                                     // once it has voted on this
-        bool open = false;                                     // E4M3: a row has no reference yet (uniform)
         float l[CH * 16];
         while (walk.next<kTcTile>(a, RB, block_rows, &un)) {
             const SeqLen& sl = un.sl;
@@ -847,23 +838,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                         break;
                     }
                     tc_after();
-                    // E4M3, once all rows have a reference: from the scores at hand, which are relative
-                    // to it (reading them again, 115 us for 112 at 8 x 32 rows over up to 32768; before,
-                    // their rounding would be that of a difference to no reference)
-                    const bool near = FP8 && !first && !open;
-                    if constexpr (FP8)
-                        if (near) {
-#pragma unroll
-                            for (int ch = 0; ch < CH; ++ch)
-                                if (ch < chunks) {
-                                    float v[16];
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) v[j] = x[ch * 16 + j];
-                                    const float y = fold16(v, lane, Max{});
-                                    if (!(lane & 1)) wred[warp][ch * 16 + fold_column(lane)] = y;
-                                }
-                        }
-                    for (int ch = 0; !near && ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
+                    for (int ch = 0; ch < chunks; ++ch) {      // the rows' maxima over the warp, 16 at a time
                         float v[16];
                         tc_ld16(s_at + ch * 16, v);
                         if constexpr (FP8) {
@@ -886,14 +861,12 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                     if (row < chunks * 16) {
                         const int w0 = wg * 4;
                         const float x = fmaxf(fmaxf(wred[w0][row], wred[w0 + 1][row]), fmaxf(wred[w0 + 2][row], wred[w0 + 3][row]));
-                        const float m = -nref[c0 + row], to = (near ? m + x : x) - (FP8 ? kTcHead : 0.f);
-                        const bool up = FP8 ? to > m : x > m + kRefSlack;
-                        nref[c0 + row] = up ? -to : -m;
-                        alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - to);
-                        if constexpr (FP8) delta[c0 + row] = up ? m - to : 0.f;
+                        const float m = -nref[c0 + row];
+                        const bool up = x > m + kRefSlack;
+                        nref[c0 + row] = up ? -x : -m;
+                        alpha[c0 + row] = !up ? 1.f : m == kNoRef ? 0.f : ex2_approx(m - x);
                     }
-                    if constexpr (FP8) open = named_any(bar, 128, row < chunks * 16 && nref[c0 + row] == -kNoRef);
-                    else named_sync(bar, 128);
+                    named_sync(bar, 128);
 #pragma unroll
                     for (int ch = 0; ch < CH; ++ch)
                         if (ch < chunks) {
@@ -911,14 +884,7 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                                 }
                             }
                         }
-                    if (near) {
-                        if constexpr (FP8)
-#pragma unroll
-                            for (int j = 0; j < CH * 16; ++j)
-                                if (j / 16 < chunks) x[j] += delta[c0 + j];
-                    } else if constexpr (C::KEEP) {
-                        score_all(Yes{});
-                    }
+                    if constexpr (C::KEEP) score_all(Yes{});
                 }
                 // ---- probabilities; P is free once the tile before has been summed
                 if (g > 0) ok = wait_bounded(&pv_done, (g - 1) & 1u, limit);
@@ -926,25 +892,26 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 unsigned char* prow = smem + C::P_OFF + row * 128;
                 auto weigh = [&](int k0, const float (&v)[16]) {
                     if constexpr (FP8) {
-                        uint32_t w[3][4];
+                        uint32_t p[8];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float y = ex2_approx(v[j]), z = ex2_approx(v[j + 1]);
                             f2_unpack(f2_fma(f2_pack(y, z), f2_pack(vinv, vinv), f2_pack(l[k0 + j], l[k0 + j + 1])), l[k0 + j], l[k0 + j + 1]);
-                            uint32_t p = pack_f16(y, z);       // to 11 bits; what follows is exact
-#pragma unroll
-                            for (int q = 0; q < 3; ++q) {
-                                const uint32_t t = e4m3_of_f16x2(p);
-                                if (q < 2) p = left_over_f16x2(p, t);
-                                if (j & 2) w[q][j >> 2] |= t << 16;
-                                else w[q][j >> 2] = t;
-                            }
+                            p[j >> 1] = pack_f16(y, z);        // to 11 bits; what follows is exact
                         }
 #pragma unroll
-                        for (int q = 0; q < 3; ++q) {
+                        for (int q = 0; q < C::PT; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t t = e4m3_of_f16x2(p[j]);
+                                if (q + 1 < C::PT) p[j] = left_over_f16x2(p[j], t);
+                                if (j & 1) w[j >> 1] |= t << 16;
+                                else w[j >> 1] = t;
+                            }
                             const int c = q * rp + c0 + k0;    // a column of P, a multiple of 16
                             *reinterpret_cast<uint4*>(prow + (c >> 7) * 16384 + ((((c & 127) >> 4) ^ (row & 7)) << 4)) =
-                                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
                         uint32_t w[8];
@@ -1055,11 +1022,14 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
                 float v[8];
                 tc_ld8(lanes + C::O_AT + c0 + k0, v);
                 if constexpr (FP8) {
-                    float y[8], z[8];
-                    tc_ld8(lanes + C::O_AT + rp + c0 + k0, y);
-                    tc_ld8(lanes + C::O_AT + 2 * rp + c0 + k0, z);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = fmaf(fmaf(z[k], 0.03125f, y[k]), 0.03125f, v[k]);
+                    for (int q = 1; q < C::PT; ++q) {
+                        float y[8];
+                        tc_ld8(lanes + C::O_AT + q * rp + c0 + k0, y);
+                        const float f = __uint_as_float((uint32_t)(127 - 5 * q) << 23);        // 2^-5q
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = fmaf(y[k], f, v[k]);
+                    }
                 }
                 if (odd_any) {
                     const int j0 = max(sl.ctx, un.ta * kTcTile), j1 = min(sl.total, un.tb * kTcTile);

@@ -175,3 +175,44 @@ def test_masked_scales_may_be_anything(sv, value, N, G):
         assert torch.equal(got[:, others], want[:, others]) and torch.equal(gl[:, others], wl[:, others])
         if value != value or 4 in which:                       # (a key scale of infinity may mask the position)
             assert not torch.isfinite(got[:, 7]).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N,G", ROWS)
+@pytest.mark.parametrize("ctx,bits", [(6000, 18), (2500, 16)])
+def test_one_score_far_above_in_long_shares(sv, fp8, N, G, ctx, bits):
+    """The same where a row meets the far score and most others in one running sum: 128 or 192
+    sequences and heads, fewer and more than there are multiprocessors, over the same pages with
+    the same queries."""
+    D, page, B, H = 128, 16, 16 if ctx > 3000 else 24, 8
+    g = torch.Generator().manual_seed(bits + N)
+    T = ctx + N
+    pages = -(-T // page)
+    k = torch.randn((pages * page, 1, D), generator=g) * 0.3
+    v = torch.randn((pages * page, 1, D), generator=g) * 0.2 + 1.0
+    q = torch.randn((1, N, G, D), generator=g) * 0.5
+    q[..., 0] = 8.0
+    k[:, :, 0] = 0.0
+    k[3, :, 0] = bits * math.log(2) / (8.0 * D ** -0.5)
+    v[3] = torch.randn((1, D), generator=g)
+    k, v, q = k.view(pages, page, 1, D), v.view(pages, page, 1, D), q.to(torch.bfloat16)
+    if fp8:
+        (k, ks), (v, vs) = quantise(k), quantise(v)
+    else:
+        k, v, ks, vs = k.to(torch.bfloat16), v.to(torch.bfloat16), None, None
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    c, nb = torch.tensor([ctx], dtype=torch.int32), torch.tensor([N], dtype=torch.int32)
+    o, l, to, tl = R.attention(q, k, v, table, ks, vs, c, nb)
+    to = to + steps(q, k, v, ks, vs, c, nb, table)
+
+    def wide(x):
+        return None if x is None else x.float().expand(pages, page, H, *x.shape[3:]).to(x.dtype).cuda()
+    cache = sv.KVCache(wide(k), wide(v), table.repeat(B, 1).cuda(), *(() if ks is None else (wide(ks), wide(vs))))
+    many = q[:, :, None].expand(B, N, H, G, D).reshape(B, N, H * G, D).cuda()
+    out, lse = sv.paged_attention(many, cache, c.repeat(B).cuda(), lse=True)
+    assert cache.read_error() == 0
+    out, lse = out.cpu().double().view(B, N, H, G, D), lse.cpu().double().view(B, N, H, G)
+    for h in range(H):
+        worst = ((out[:, :, h] - o).abs() / to).max()
+        assert worst <= 1, f"out off by {worst} of its tolerance"
+        assert ((lse[:, :, h] - l).abs() <= tl).all()
