@@ -764,7 +764,7 @@ size_t attend_workspace_size(int B, int N, int Hq, int Hkv, int D) {
     // the join's notes, then two parts per CTA, for either kernel
     const int G = Hq / Hkv, rt = N * G, rows = att_rows(N, G);
     const size_t here = kAttHead + align256((size_t)2 * kAttMaxCtas * part_floats(rt < rows ? rt : rows, D) * 4);
-    const size_t tc = attend_takes_tc(N, G, D, false, INT64_MAX) ? attend_tc_workspace(N, G) : 0;
+    const size_t tc = attend_takes_tc(N, G, D, false, INT64_MAX, 0, 1) ? attend_tc_workspace(N, G) : 0;
     return here > tc ? here : tc;
 }
 
@@ -819,7 +819,12 @@ static cudaError_t launch_attend_d(const AttendArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     const bool f8 = a.c.dtype == SPEC_DTYPE_E4M3;
-    if (attend_takes_tc(a.N, a.G, a.c.head_dim, f8, (long long)a.c.max_pages * a.c.page_size)) return launch_attend_tc(a, st);
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    if (attend_takes_tc(a.N, a.G, a.c.head_dim, f8, (long long)a.c.max_pages * a.c.page_size, (long long)a.B * a.c.kv_heads,
+                        di.sm_count))
+        return launch_attend_tc(a, st);
     switch (a.c.head_dim) {
         case 64: return f8 ? launch_attend_d<64, true>(a, st) : launch_attend_d<64, false>(a, st);
         case 128: return f8 ? launch_attend_d<128, true>(a, st) : launch_attend_d<128, false>(a, st);

@@ -219,8 +219,8 @@ bool attend_whole(long long units, long long positions, long long ctas);
 // The matrix-unit kernel of sv_attend_tc.cu (rows of 128 elements).
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t st);
 // Whether that kernel takes a call; capacity: positions that a sequence's row of
-// the block table has room for.
-bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity);
+// the block table has room for, units: cached heads of all sequences.
+bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity, long long units, int sms);
 size_t attend_tc_workspace(int N, int G);
 
 }  // namespace sv

@@ -1100,13 +1100,18 @@ constexpr int kTcMostBf16 = 144, kTcMostFp8 = 64;
 //   17 to 32: this one gains per position what it loses per unit, so the longest context
 //     that the block table has room for decides.  bf16, 32 rows: 64.4 / 59.7 for 64
 //     sequences of 1000, 12.4 / 13.0 for one, but 80.5 / 90.8 and 13.3 / 19.0 of 2000.  E4M3,
-//     where the other reads half the bytes and widens them, later: 88.9 / 85.8 for 64 of
-//     2000, 132.3 / 132.2 of 4000, 18.2 / 20.7 for one.
+//     where the other reads half the bytes and widens them, per position the two are
+//     alike, and this one gains where CTAs share a unit's positions, as long as there are
+//     fewer units (sequences x cached heads) than SMs.  32 rows: 14.4 / 14.2 for one
+//     sequence of 1000, 16.0 / 16.5 of 2000, 20.4 / 23.2 of 4000, 25.3 / 29.7 for 8 of 2000,
+//     115.4 / 117.8 of 32768, 46.3 / 47.6 for 16 of 4000, but 80.2 / 80.1 for 32 and
+//     143.6 / 136.2 for 64; 20 rows: 14.4 / 13.6 for one of 1500, 24.8 / 27.0 for 8 of 2000,
+//     46.3 / 45.2 for 16 of 4000, 141.9 / 131.4 for 64.
 //   More: that one reads the cache once for every 32: 148.5 / 332.3 for 36 rows and 64 of
 //     4000, 100.8 / 167.4 of 2000, 51.1 / 49.6 of 300.
-constexpr long long kTcMinCapacityBf16 = 1536, kTcMinCapacityFp8 = 2560;
-bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity) {
-    return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= (fp8 ? kTcMinCapacityFp8 : kTcMinCapacityBf16)));
+constexpr long long kTcMinCapacity = 1536;
+bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity, long long units, int sms) {
+    return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= kTcMinCapacity && (!fp8 || units < sms)));
 }
 
 size_t attend_tc_workspace(int N, int G) {
