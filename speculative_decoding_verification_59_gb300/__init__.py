@@ -584,6 +584,8 @@ class KVCache:
             raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and to it alone")
         if fp8:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{name} must be a torch tensor, got {type(t).__name__}")
                 if t.dtype != torch.float32 or t.shape != k.shape[:-1] or t.device != dev:
                     raise ValueError(f"{name} must be float32 {tuple(k.shape[:-1])} on {dev}")
             if k_scale.stride() != v_scale.stride():

@@ -122,3 +122,15 @@ def test_host_threads(sv, shared):
         torch.cuda.synchronize()
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, alone))
+
+
+def test_scales_of_a_cache_are_tensors(sv):
+    k, v, table, ks, vs = R.make_cache_on_gpu(6, 1, 32, 16, 2, 64, fp8=True)
+    for bad in (0.5, [1.0], ks.cpu().numpy()):
+        with pytest.raises(TypeError, match="k_scale must be a torch tensor"):
+            sv.KVCache(k, v, table, bad, vs)
+        with pytest.raises(TypeError, match="v_scale must be a torch tensor"):
+            sv.KVCache(k, v, table, ks, bad)
+    for bad in (ks.double(), ks[:, :, :1], ks.cpu()):
+        with pytest.raises(ValueError, match="k_scale must be float32"):
+            sv.KVCache(k, v, table, bad, vs)
