@@ -421,7 +421,7 @@ typedef struct {
  *   q_out        [B, N, q_heads, head_dim] bf16
  * Positions n >= n_b are skipped: nothing is written for them.  For a bad
  * sequence, and for a position outside [0, rope_rows), no cache entry is
- * written and q_out is NaN.
+ * written and q_out is NaN.  B * N * (q_heads + 2 kv_heads) < 2^31.
  */
 spec_status_t spec_kv_append(const spec_kv_cache_t* cache, const void* q, const void* k,
                              const void* v, int64_t q_token_stride, int64_t k_token_stride,
@@ -437,7 +437,7 @@ spec_status_t spec_kv_append(const spec_kv_cache_t* cache, const void* q, const 
  * starts[b] + t (NULL: t) for t < counts[b] (NULL: T), zeros for the other
  * rows.  E4M3 entries are multiplied by their scale in fp32 and rounded once.
  * A bad sequence's rows are NaN, and so is the row of a bad page.
- * T * kv_heads < 2^31.
+ * T * kv_heads < 2^31, B <= 65535.
  */
 spec_status_t spec_kv_read(const spec_kv_cache_t* cache, const int32_t* starts,
                            const int32_t* counts, int B, int T, spec_dtype_t out_dtype,
@@ -454,7 +454,8 @@ spec_status_t spec_kv_read(const spec_kv_cache_t* cache, const int32_t* starts,
  * they are (scales with them); keys were rotated for the node's depth, which
  * is its new distance from the root.  A sequence with num_accepted -1 is
  * skipped; a path that is not ascending in 1..N-1, or that is longer than
- * N-1, sets SPEC_DEVERR_CACHE_RANGE and moves nothing.  1 <= N <= 1024.
+ * N-1, sets SPEC_DEVERR_CACHE_RANGE and moves nothing.  1 <= N <= 1024,
+ * B <= 65535.
  */
 spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* context_lens,
                               const int32_t* path_nodes, const int32_t* num_accepted, int B,
@@ -468,14 +469,19 @@ spec_status_t spec_kv_compact(const spec_kv_cache_t* cache, const int32_t* conte
  * over the positions t that n sees: every t < context_lens[b], and of the new
  * ones
  *   parents NULL: those up to itself (a chain, N <= 257);
- *   parents [B, N] int32: itself and its ancestors (a tree, N <= 64;
- *     parents[0] = -1, 0 <= parents[n] < n as in spec_verify_tree_greedy).
+ *   parents [B, N] int32: itself and its ancestors (a tree, N <= 64, while
+ *     spec_verify_tree_greedy and spec_kv_compact take 1024;
+ *     parents[0] = -1, 0 <= parents[n] < n as there).
  *   q      [B, N, q_heads, head_dim] bf16, token i at q + i * q_token_stride (elements,
  *          a multiple of 8), heads contiguous; 16-byte aligned
  *   out    [B, N, q_heads, head_dim] bf16, contiguous
  *   lse    [B, N, q_heads] fp32, nullable
- * q_heads is a multiple of kv_heads, at most 64 times it.  Scores, softmax
- * statistics and sums are fp32.  Positions n >= n_b give out = 0 and lse =
+ * q_heads is a multiple of kv_heads, at most 64 times it, B * N * q_heads
+ * < 2^31.  Scores, softmax statistics and sums are fp32.  Before they meet the
+ * values, probabilities are rounded: to bf16 with a BF16 cache (against 64 bits
+ * that is 2.3e-3 of the result beside 1.7e-3 from its own rounding), to fp16
+ * with an E4M3 one (a probability times its position's value scale, the row's
+ * largest such product at least 1).  lse knows nothing of that.  Positions n >= n_b give out = 0 and lse =
  * -inf.  The others of a bad sequence (or of a malformed tree,
  * SPEC_DEVERR_TREE_PARENT) give NaN, and where the lengths themselves are bad
  * all N do.  What the masked entries of the cache hold does not matter, NaN and

@@ -740,6 +740,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 // 9.0 and * 13.3 / 19.7, of 630 11.5 / 10.6; 160 of 500 11.2 / 12.2, + 12.2 / 16.1, but *
 // 28.1 / 25.8; 512 of 250 13.5 / 17.0, * 36.8 / 44.7, + 16.3 / 22.6, of 630 28.7 / 29.9, * 70.6
 // / 73.2, + 25.9 / 32.7, of 1000 40.8 / 40.4, * 67.6 / 75.0, + 39.1 / 38.1.
+// The positions are those that the block table has room for: the host does not know the
+// lengths.  The rule does not ask which kernel runs; of these cases that costs
+// * 160 units of 500.
 bool attend_whole(long long units, long long positions, long long ctas) {
     return positions <= 256 || (positions <= 512 && 4 * units >= ctas) || (positions <= 768 && 2 * units >= 3 * ctas);
 }

@@ -49,10 +49,11 @@
 //   64 sequences x 32 rows over 4096, bf16: 140 us, 5.8 TB/s of the cache's 812 MB, 86 % of
 //     a plain copy's rate.  Memory bounds the tiles; what is left is units' begins and ends.
 //   32 trees x 144 rows over 2048, bf16: 97.3 us, 305 TFLOP/s.  A tile's softmax is four
-//     dependent steps of some 700 to 1500 cycles together 3700 (scores, vote, powers, P),
-//     and a unit begins and ends in some 13000, mostly code that is not at hand.
-//   8 sequences x 32 rows over 32768, E4M3: 109.6 us, 3.6 TB/s: the same softmax, 2600
-//     cycles for a tile that the memory brings in 1400.
+//     dependent steps, together 3900 cycles (the scores' wait 420, scores and vote 1270, P's
+//     buffer 410, powers and P 1770: clock reads in a copy of the kernel), and a unit begins
+//     and ends in some 13000.  In a seventh of their time warps wait for instructions.
+//   8 sequences x 32 rows over 32768, E4M3: 112.4 us, 3.5 TB/s: the same softmax, 2800
+//     cycles for a tile that the memory brings in 1400 (400, 790, 450, 1140).
 #include <cuda.h>
 
 #include "sv_attend.cuh"
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(TcCfg<CH, NSM, FP8>::THREADS, 1) attend_tc_ker
             // unit before still has to do, and the thread goes on while the copies are under
             // way (before them and through registers, 144 rows kept the loaders for 8000
             // cycles a unit).  E4M3: through registers, in terms (few rows; among the tiles'
-            // code, that of every tile was slower: 133 us for 111 at 8 x 32768 positions).
+            // code, that of every tile was slower: 133 us for 111 at 8 x 32768 positions, with
+            // three terms of the probabilities).
             auto queries = [&] {
                 const int qb = (int)(uc % C::QB);
                 if (uc >= (unsigned)C::QB && !wait_bounded(&q_free[qb], (uc / C::QB - 1) & 1u, limit)) ok = false;
@@ -1109,6 +1111,8 @@ constexpr int kTcMostBf16 = 144, kTcMostFp8 = 64;
 //     46.3 / 45.2 for 16 of 4000, 141.9 / 131.4 for 64.
 //   More: that one reads the cache once for every 32: 148.5 / 332.3 for 36 rows and 64 of
 //     4000, 100.8 / 167.4 of 2000, 51.1 / 49.6 of 300.
+// The host does not know the lengths: in a table much wider than its contexts, calls of 17
+// to 32 rows come here however short these are.
 constexpr long long kTcMinCapacity = 1536;
 bool attend_takes_tc(int N, int G, int D, bool fp8, long long capacity, long long units, int sms) {
     return D == kTcD && (N * G > 32 || (N * G > 16 && capacity >= kTcMinCapacity && (!fp8 || units < sms)));
