@@ -523,6 +523,91 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
                                   float* out_top_logprob, void* workspace,
                                   size_t workspace_bytes, cudaStream_t stream);
 
+/* ==========================================================================
+ * The dense side of the target model's pass: what lies between its cache and
+ * attention calls, with weights and rows in 8 bits.  (The source pages leave it
+ * to the model, as they do the calls above.)
+ *
+ * 8-bit values are e4m3 with fp32 scales, one for each block of 128 elements
+ * of a row (the last block of a row may be shorter), or for each 128 x 128 elements
+ * of a weight:
+ *   t = max(max |y| over the block, 1e-20),  q = e4m3(y * (448 / t)),  scale = t / 448,
+ * and an element stands for q * scale.  A NaN stays one; the largest element is taken
+ * over the others.  A block with an infinity has scale infinity: its infinities are NaN,
+ * its other elements 0 times infinity.
+ *   rows:    scale of block b of row r at b * scale_stride + r: a block's scales of
+ *            neighbouring rows lie side by side, as the product reads them
+ *   weights: scale of block (i, b) (rows 128 i on, elements 128 b on) at
+ *            i * scale_stride + b
+ *
+ * Rows of x, gate, up and the residual: row r at r * stride elements, 16-byte
+ * aligned, strides multiples of 16 bytes (SPEC_ERR_MISALIGNED otherwise), bf16 or
+ * fp32.  Outputs `out`: contiguous rows of dim elements, bf16, fp32 or e4m3 (then
+ * out_scale is needed, with scale_stride >= rows, 0 for one row or one block).  dim is a multiple of 8, of 16
+ * for an e4m3 output.  rows * (dim rounded up to 128) < 2^34.  Arithmetic is fp32,
+ * each output rounded once.  An output may not overlap an input except as said.
+ * ======================================================================== */
+
+/*
+ * The residual's addition and the root-mean-square norm of its sum:
+ *   h = x + residual (NULL: h = x),   sum_out = h in sum_dtype (nullable),
+ *   out = h * rsqrt(mean(h^2) + eps) * weight      (h before its rounding; weight NULL: 1)
+ *   residual, sum_out  of sum_dtype, strides of their own; sum_out may be the residual, or x of
+ *                      that type, itself (same stride): the residual stream in place
+ *   weight             [dim] bf16, 16-byte aligned, nullable
+ */
+spec_status_t spec_add_norm(const void* x, spec_dtype_t x_dtype, int64_t x_stride,
+                            const void* residual, spec_dtype_t sum_dtype,
+                            int64_t residual_stride, const void* weight, float eps, int rows,
+                            int dim, void* sum_out, int64_t sum_stride, void* out,
+                            spec_dtype_t out_dtype, float* out_scale, int64_t scale_stride,
+                            cudaStream_t stream);
+
+/*
+ * out = act(gate) * up:
+ *   SPEC_ACT_SILU        x / (1 + e^-x)
+ *   SPEC_ACT_GELU_TANH   x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
+ * gate and up have one dtype; halves of one projection's rows are passed with its stride.
+ */
+typedef enum { SPEC_ACT_SILU = 0, SPEC_ACT_GELU_TANH = 1 } spec_act_t;
+spec_status_t spec_gated_act(const void* gate, const void* up, spec_dtype_t dtype,
+                             int64_t gate_stride, int64_t up_stride, spec_act_t act, int rows,
+                             int dim, void* out, spec_dtype_t out_dtype, float* out_scale,
+                             int64_t scale_stride, cudaStream_t stream);
+
+/*
+ * Rounds rows (block_rows 1) or a weight (block_rows 128) to 8 bits; scales as above
+ * (a weight's scale_stride is at least the number of a row's blocks).
+ */
+spec_status_t spec_quantize_e4m3(const void* x, spec_dtype_t dtype, int64_t x_stride, int rows,
+                                 int dim, int block_rows, void* out, float* out_scale,
+                                 int64_t scale_stride, cudaStream_t stream);
+
+/*
+ * The product of 8-bit rows with an 8-bit weight:
+ *   out[m, n] = sum over blocks b of  x_scale[m, b] w_scale[n / 128, b]
+ *                                     sum over k in b of x[m, k] w[n, k]
+ *   x        [M, K] e4m3, w [N, K] e4m3: 16-byte aligned, strides multiples of 16 and at least K
+ *            (of a single row none is used)
+ *   x_scale  fp32, block b of row m at b * x_scale_stride + m: 16-byte aligned, the stride a
+ *            multiple of 4 and at least M (of a single block none is used).  What lies between
+ *            M and the stride does not matter
+ *   w_scale  fp32, at (n / 128) * w_scale_stride + b
+ *   out      [M, N] bf16 or fp32, row m at m * out_stride (elements, at least N)
+ * Any M, N >= 0 and K >= 1, odd ones included; rows whose stride is a multiple of 16 bytes are
+ * written fastest.  Sums are fp32: of a block's products in tensor memory, then, scaled,
+ * over the blocks, in an order that the sizes alone decide.
+ * Workspace: spec_matmul_workspace_size() bytes, 256-byte aligned, its first 256 bytes
+ * zero-filled once (the error word; a wait that runs out sets SPEC_DEVERR_TIMEOUT there and
+ * leaves NaN in the results it concerns).  Calls that share one must not overlap.
+ */
+size_t spec_matmul_workspace_size(int M, int N, int K);
+spec_status_t spec_matmul_e4m3(const void* x, int64_t x_stride, const float* x_scale,
+                               int64_t x_scale_stride, const void* w, int64_t w_stride,
+                               const float* w_scale, int64_t w_scale_stride, int M, int N, int K,
+                               void* out, spec_dtype_t out_dtype, int64_t out_stride,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /*
  * Test hook for the kernels' bounded waits (the source pages have no
  * counterpart).  Every wait of the streaming kernels on a shared-memory

@@ -21,7 +21,7 @@ __all__ = [
     "spec_verify_greedy", "spec_verify_tree_greedy", "spec_verify_read_error",
     "spec_verify_status_string", "Workspace", "verify_sample", "verify_greedy", "verify_tree_greedy",
     "SPEC_DTYPE_E4M3", "KVCache", "kv_append", "kv_read", "kv_compact", "paged_attention",
-    "token_logprobs",
+    "token_logprobs", "add_norm", "gated_act", "quantize_e4m3", "matmul_e4m3",
 ]
 
 SPEC_OK = 0
@@ -36,6 +36,8 @@ SPEC_VERIFY_NOALLOC_SCRATCH_BYTES = 8 << 20
 SPEC_DTYPE_F32 = 0
 SPEC_DTYPE_BF16 = 1
 SPEC_DTYPE_E4M3 = 2
+SPEC_ACT_SILU = 0
+SPEC_ACT_GELU_TANH = 1
 SPEC_DEVERR_TOKEN_RANGE = 1
 SPEC_DEVERR_EMPTY_ROW = 2
 SPEC_DEVERR_TREE_PARENT = 4
@@ -90,6 +92,11 @@ SIGNATURES = {
     "spec_paged_attention": ([_P, _P, _L, _P, _P, _P, _F, _I, _I, _I, _P, _P, _P, _S, _P], _I),
     "spec_logprobs_workspace_size": ([_I, _I, _I], _S),
     "spec_token_logprobs": ([_P, _I, _P, _F, _I, _I, _I, _P, _P, _P, _P, _P, _S, _P], _I),
+    "spec_add_norm": ([_P, _I, _L, _P, _I, _L, _P, _F, _I, _I, _P, _L, _P, _I, _P, _L, _P], _I),
+    "spec_gated_act": ([_P, _P, _I, _L, _L, _I, _I, _I, _P, _I, _P, _L, _P], _I),
+    "spec_quantize_e4m3": ([_P, _I, _L, _I, _I, _I, _P, _P, _L, _P], _I),
+    "spec_matmul_workspace_size": ([_I, _I, _I], _S),
+    "spec_matmul_e4m3": ([_P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _P, _I, _L, _P, _S, _P], _I),
     "spec_verify_read_error": ([_P, _P, _P], _I),
     "spec_verify_status_string": ([_I], ctypes.c_char_p),
     "spec_verify_set_wait_limit": ([ctypes.c_uint32], None),
@@ -695,3 +702,64 @@ def token_logprobs(logits, tokens, K: int = 0, *, temperature: float = 1.0, work
         workspace = _scratch(workspace, 0, load_library().spec_logprobs_workspace_size(
             logits.numel() // max(logits.shape[-1], 1), logits.shape[-1], K), stream)
     return (_marshal_module or _load_marshal()).token_logprobs(logits, tokens, K, temperature, workspace, stream)
+
+
+# ---- the target model's dense side -----------------------------------------------------
+_ACTS = {"silu": SPEC_ACT_SILU, "gelu": SPEC_ACT_GELU_TANH}
+
+
+def _f32(dtype) -> bool:
+    if dtype is None:
+        return False
+    if dtype not in _logits_dtypes():
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    return dtype == _torch().float32
+
+
+def add_norm(x, weight=None, residual=None, *, eps: float = 1e-6, e4m3: bool = False, dtype=None,
+             sum_out=None, stream=None):
+    """The residual's addition and the root-mean-square norm of its sum (see spec_add_norm).
+    x [..., dim] bfloat16 or float32, weight [dim] bfloat16 or None, residual of x's shape,
+    bfloat16 or float32, or None; rows may be slices (one stride apart, multiples of 16 bytes).
+    Returns the normed rows [..., dim] of dtype (bfloat16 by default, or float32); with e4m3=True
+    float8_e4m3fn rows and their scales [..., ceil(dim / 128)] float32 (strided as matmul_e4m3
+    takes them); and with a residual, last, the sum in the residual's dtype, which sum_out
+    may name a place for: the residual itself, say.  Small outputs (up to 2^20 elements) share
+    one allocation."""
+    return (_marshal_module or _load_marshal()).add_norm(
+        x, weight, residual, eps, e4m3, dtype is not None and _f32(dtype), sum_out, stream)
+
+
+def gated_act(gate, up=None, *, act: str = "silu", e4m3: bool = False, dtype=None, stream=None):
+    """act(gate) * up (see spec_gated_act), act "silu" or "gelu" (its tanh form).  gate and up [...,
+    dim] bfloat16 or float32, slices of one projection or, with up None, gate [..., 2 dim] holding
+    both side by side.  Returns [..., dim] of dtype, or with e4m3=True rows and scales, as
+    add_norm does."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return (_marshal_module or _load_marshal()).gated_act(
+        gate, up, _ACTS[act], e4m3, dtype is not None and _f32(dtype), stream)
+
+
+def quantize_e4m3(x, *, block_rows: int = 1, stream=None):
+    """Rounds bfloat16 or float32 rows to 8 bits (see spec_quantize_e4m3): rows x [..., dim] with a scale
+    for each 128 of their elements, or, with block_rows=128, a weight x [N, dim] with one for each
+    128 x 128.  Returns (float8_e4m3fn of x's shape, scales float32: [..., ceil(dim / 128)], or
+    [ceil(N / 128), ceil(dim / 128)])."""
+    return (_marshal_module or _load_marshal()).quantize_e4m3(x, block_rows, stream)
+
+
+def matmul_e4m3(x, x_scale, w, w_scale, *, dtype=None, out=None, workspace=None, stream=None):
+    """The product of 8-bit rows with an 8-bit weight (see spec_matmul_e4m3): x [..., K] and w [N, K]
+    float8_e4m3fn with the scales that quantize_e4m3, add_norm and gated_act give, [...,
+    ceil(K / 128)] with stride 1 from row to row, and [ceil(N / 128), ceil(K / 128)].  Returns [..., N] of
+    dtype (bfloat16 by default, or float32).  workspace: a Workspace, whose read_error() then
+    tells of waits that ran out (NaN in the results either way), or a uint8 tensor of
+    spec_matmul_workspace_size() bytes, its first 256 zero, that no call on another stream
+    uses at the same time.  None: one kept for the device and stream to the program's end (a
+    captured call gets one of its graph's)."""
+    if isinstance(workspace, Workspace):
+        workspace = _scratch(workspace, 0, load_library().spec_matmul_workspace_size(
+            x.numel() // max(x.shape[-1], 1), w.shape[0], x.shape[-1]), stream)
+    return (_marshal_module or _load_marshal()).matmul_e4m3(
+        x, x_scale, w, w_scale, dtype is not None and _f32(dtype), out, workspace, stream)

@@ -1,4 +1,5 @@
-// Torch marshalling of the cache, attention and log-probability calls.
+// Torch marshalling of the cache, attention and log-probability calls, and of
+// the target model's dense side.
 //
 // These calls run on every layer of every step, and a small one takes the GPU
 // two to ten microseconds: checking tensors and converting arguments in Python
@@ -461,9 +462,241 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A tensor [..., cols] whose rows, all leading dimensions taken together, lie one
+// stride apart with their elements side by side.
+struct Flat {
+    void* p = nullptr;
+    int64_t rows = 0, cols = 0, stride = 0;
+    c10::IntArrayRef lead;
+    at::ScalarType type = at::kByte;
+};
+// The one stride of t's dimensions but the last, taken as rows; that of packed rows where
+// there is one row only.
+int64_t row_stride(const at::Tensor& t, const char* name, int64_t of_one) {
+    int64_t stride = 0, next = 0;
+    for (int64_t d = t.dim() - 2; d >= 0; --d) {
+        if (t.size(d) == 1) continue;
+        if (stride == 0) stride = t.stride(d);
+        else if (t.stride(d) != next)
+            throw PyFail{PyExc_ValueError, std::string(name) + ": rows must lie one stride apart, got strides " + shape_text(t.strides()) +
+                                               " of shape " + shape_text(t.sizes())};
+        next = t.stride(d) * t.size(d);
+    }
+    return stride == 0 ? of_one : stride;
+}
+Flat flat_of(PyObject* o, const char* name, int device) {
+    const at::Tensor& t = *tensor_of(o, name);
+    on_cuda(t, name, device);
+    Flat f;
+    if (t.dim() < 1) throw PyFail{PyExc_ValueError, std::string(name) + " must have shape (..., dim), got ()"};
+    f.p = t.data_ptr();
+    f.type = t.scalar_type();
+    f.cols = t.size(-1);
+    f.lead = t.sizes().slice(0, t.dim() - 1);
+    f.rows = 1;
+    for (int64_t d : f.lead) f.rows *= d;
+    if (t.stride(-1) != 1 && f.cols > 1)
+        throw PyFail{PyExc_ValueError, std::string(name) + ": a row's elements must lie side by side, got strides " + shape_text(t.strides())};
+    f.stride = f.rows > 0 ? row_stride(t, name, f.cols) : f.cols;
+    if (f.rows > INT32_MAX || f.cols > INT32_MAX) throw PyFail{PyExc_ValueError, std::string(name) + " is too large: " + shape_text(t.sizes())};
+    return f;
+}
+spec_dtype_t code_of(at::ScalarType t, const char* name, bool e4m3 = false) {
+    if (t == at::kFloat) return SPEC_DTYPE_F32;
+    if (t == at::kBFloat16) return SPEC_DTYPE_BF16;
+    if (e4m3 && t == at::kFloat8_e4m3fn) return SPEC_DTYPE_E4M3;
+    throw PyFail{PyExc_TypeError, std::string(name) + " must have dtype float32 or bfloat16, got " + c10::toString(t)};
+}
+void same_lead(const Flat& f, const char* name, c10::IntArrayRef lead, int64_t cols) {
+    c10::SmallVector<int64_t, 5> want(lead.begin(), lead.end());
+    want.push_back(cols);
+    c10::SmallVector<int64_t, 5> got(f.lead.begin(), f.lead.end());
+    got.push_back(f.cols);
+    if (got != want) throw PyFail{PyExc_ValueError, std::string(name) + " must have shape " + shape_text(want) + ", got " + shape_text(got)};
+}
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+
+// A row operator's outputs: [lead, dim] of a type, for 8 bits with the scales (a block's of all
+// rows side by side, their number filled up to a multiple of 4), and the sum.  Small ones share
+// one allocation.
+struct RowOut {
+    at::Tensor out, scale, sum;
+    int64_t pitch = 0;
+};
+RowOut row_out(c10::IntArrayRef lead, int64_t rows, int64_t dim, spec_dtype_t type, const at::Tensor* like_sum) {
+    RowOut r;
+    c10::SmallVector<int64_t, 5> shape(lead.begin(), lead.end());
+    shape.push_back(dim);
+    const at::ScalarType t = type == SPEC_DTYPE_E4M3 ? at::kFloat8_e4m3fn : type == SPEC_DTYPE_F32 ? at::kFloat : at::kBFloat16;
+    const int64_t blocks = blocks_of(dim), elt = (int64_t)c10::elementSize(t);
+    const bool e4m3 = type == SPEC_DTYPE_E4M3;
+    r.pitch = up_to(rows, 4);
+    const int64_t scale_bytes = e4m3 ? up_to(blocks * r.pitch * 4, 16) : 0, out_bytes = up_to(rows * dim * elt, 16);
+    const int64_t sum_elt = like_sum ? (int64_t)like_sum->element_size() : 0;
+    const int64_t sum_bytes = like_sum ? rows * dim * sum_elt : 0;
+    if (rows * dim > 0 && rows * dim <= kSharedOutput) {
+        const at::Tensor all = empty({scale_bytes + out_bytes + sum_bytes}, at::kByte);
+        if (e4m3) r.scale = stretch(all, {blocks * r.pitch}, at::kFloat, 0);
+        r.out = stretch(all, shape, t, scale_bytes / elt);
+        if (like_sum) r.sum = stretch(all, shape, like_sum->scalar_type(), (scale_bytes + out_bytes) / sum_elt);
+    } else {
+        if (e4m3) r.scale = empty({blocks * r.pitch}, at::kFloat);
+        r.out = empty(shape, t);
+        if (like_sum) r.sum = empty(shape, like_sum->scalar_type());
+    }
+    if (e4m3) {
+        c10::SmallVector<int64_t, 5> strides(shape.size());
+        int64_t s = 1;
+        for (size_t d = lead.size(); d-- > 0; s *= shape[d] > 0 ? shape[d] : 1) strides[d] = s;
+        shape.back() = blocks;
+        strides.back() = r.pitch;
+        r.scale.unsafeGetTensorImpl()->set_sizes_and_strides(shape, strides);
+    }
+    return r;
+}
+float* floats(const at::Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
+
+// (x, weight, residual, eps, e4m3, dtype float32, sum_out, stream)
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        const Flat x = flat_of(a[0], "x", -1);
+        const int device = tensor_of(a[0], "x")->get_device();
+        const spec_dtype_t xt = code_of(x.type, "x");
+        const void* w = plain<void>(a[1], "weight", at::kBFloat16, {x.cols}, device, true);
+        const bool add = a[2] != Py_None;
+        Flat res, into;
+        spec_dtype_t st = SPEC_DTYPE_BF16;
+        if (add) {
+            res = flat_of(a[2], "residual", device);
+            st = code_of(res.type, "residual");
+            same_lead(res, "residual", x.lead, x.cols);
+        }
+        const bool given = a[6] != Py_None;
+        if (given) {
+            if (!add) throw PyFail{PyExc_ValueError, "sum_out belongs to a residual"};
+            into = flat_of(a[6], "sum_out", device);
+            of_type(*tensor_of(a[6], "sum_out"), "sum_out", res.type);
+            same_lead(into, "sum_out", x.lead, x.cols);
+        }
+        const spec_dtype_t ot = truth(a[4]) ? SPEC_DTYPE_E4M3 : truth(a[5]) ? SPEC_DTYPE_F32 : SPEC_DTYPE_BF16;
+        const OnStream on(a[7], device);
+        const RowOut r = row_out(x.lead, x.rows, x.cols, ot, add && !given ? tensor_of(a[2], "residual") : nullptr);
+        done(spec_add_norm(x.p, xt, x.stride, res.p, st, res.stride, w, (float)real(a[3]), (int)x.rows, (int)x.cols,
+                           given ? into.p : add ? r.sum.data_ptr() : nullptr, given ? into.stride : x.cols, r.out.data_ptr(), ot,
+                           floats(r.scale), r.pitch, on.h),
+             "spec_add_norm");
+        const at::Tensor sum = given ? *tensor_of(a[6], "sum_out") : r.sum;
+        if (ot == SPEC_DTYPE_E4M3) return add ? tuple_of({r.out, r.scale, sum}) : tuple_of({r.out, r.scale});
+        return add ? tuple_of({r.out, sum}) : wrap(r.out);
+    });
+}
+
+// (gate, up, act, e4m3, dtype float32, stream); up None: gate holds both, side by side
+PyObject* gated_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        Flat gate = flat_of(a[0], "gate", -1), up = gate;
+        const int device = tensor_of(a[0], "gate")->get_device();
+        const spec_dtype_t t = code_of(gate.type, "gate");
+        if (a[1] == Py_None) {
+            if (gate.cols % 2) throw PyFail{PyExc_ValueError, "gate without up must hold both halves, got " + std::to_string(gate.cols) + " columns"};
+            gate.cols /= 2;
+            up.p = static_cast<char*>(gate.p) + gate.cols * (int64_t)c10::elementSize(gate.type);
+        } else {
+            up = flat_of(a[1], "up", device);
+            of_type(*tensor_of(a[1], "up"), "up", gate.type);
+            same_lead(up, "up", gate.lead, gate.cols);
+        }
+        const spec_dtype_t ot = truth(a[3]) ? SPEC_DTYPE_E4M3 : truth(a[4]) ? SPEC_DTYPE_F32 : SPEC_DTYPE_BF16;
+        const OnStream on(a[5], device);
+        const RowOut r = row_out(gate.lead, gate.rows, gate.cols, ot, nullptr);
+        done(spec_gated_act(gate.p, up.p, t, gate.stride, up.stride, (spec_act_t)integer(a[2]), (int)gate.rows, (int)gate.cols,
+                            r.out.data_ptr(), ot, floats(r.scale), r.pitch, on.h),
+             "spec_gated_act");
+        return ot == SPEC_DTYPE_E4M3 ? tuple_of({r.out, r.scale}) : wrap(r.out);
+    });
+}
+
+// (x, block_rows, stream)
+PyObject* quantize_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const Flat x = flat_of(a[0], "x", -1);
+        const int device = tensor_of(a[0], "x")->get_device();
+        const spec_dtype_t t = code_of(x.type, "x");
+        const int64_t high = integer(a[1]);
+        if (high != 1 && high != 128) throw PyFail{PyExc_ValueError, "block_rows must be 1 or 128, got " + std::to_string(high)};
+        const OnStream on(a[2], device);
+        RowOut r;
+        if (high == 1) {
+            r = row_out(x.lead, x.rows, x.cols, SPEC_DTYPE_E4M3, nullptr);
+        } else {
+            if (x.lead.size() != 1) throw PyFail{PyExc_ValueError, "a weight must have shape (rows, dim), got " + shape_text(tensor_of(a[0], "x")->sizes())};
+            r.out = empty({x.rows, x.cols}, at::kFloat8_e4m3fn);
+            r.pitch = blocks_of(x.cols);
+            r.scale = empty({blocks_of(x.rows), r.pitch}, at::kFloat);
+        }
+        done(spec_quantize_e4m3(x.p, t, x.stride, (int)x.rows, (int)x.cols, (int)high, r.out.data_ptr(), floats(r.scale), r.pitch, on.h),
+             "spec_quantize_e4m3");
+        return tuple_of({r.out, r.scale});
+    });
+}
+
+// (x, x_scale, w, w_scale, dtype float32, out, workspace, stream)
+PyObject* matmul_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        const Flat x = flat_of(a[0], "x", -1);
+        const int device = tensor_of(a[0], "x")->get_device();
+        of_type(*tensor_of(a[0], "x"), "x", at::kFloat8_e4m3fn);
+        const Flat w = flat_of(a[2], "w", device);
+        const at::Tensor& wt = *tensor_of(a[2], "w");
+        of_type(wt, "w", at::kFloat8_e4m3fn);
+        if (wt.dim() != 2 || w.cols != x.cols)
+            throw PyFail{PyExc_ValueError, "w must have shape (N, " + std::to_string(x.cols) + "), got " + shape_text(wt.sizes())};
+        const int64_t blocks = blocks_of(x.cols);
+        const at::Tensor& xs = *tensor_of(a[1], "x_scale");
+        on_cuda(xs, "x_scale", device);
+        of_type(xs, "x_scale", at::kFloat);
+        c10::SmallVector<int64_t, 5> want(x.lead.begin(), x.lead.end());
+        want.push_back(blocks);
+        of_shape(xs, "x_scale", want);
+        if (x.rows > 1 && row_stride(xs, "x_scale", 1) != 1)
+            throw PyFail{PyExc_ValueError, "x_scale: the scales of a block must lie side by side (stride 1 from row to row), got strides " +
+                                               shape_text(xs.strides())};
+        const Flat ws = flat_of(a[3], "w_scale", device);
+        of_type(*tensor_of(a[3], "w_scale"), "w_scale", at::kFloat);
+        of_shape(*tensor_of(a[3], "w_scale"), "w_scale", {blocks_of(w.rows), blocks});
+        const bool f32 = truth(a[4]);
+        const size_t need = x.cols >= 1 ? spec_matmul_workspace_size((int)x.rows, (int)w.rows, (int)x.cols) : 0;
+        if (need == 0)
+            throw PyFail{PyExc_ValueError, "matmul_e4m3: unsupported sizes M=" + std::to_string(x.rows) + " N=" + std::to_string(w.rows) +
+                                               " K=" + std::to_string(x.cols)};
+        const OnStream on(a[7], device);
+        at::Tensor out;
+        int64_t stride = w.rows;
+        if (a[5] == Py_None) {
+            c10::SmallVector<int64_t, 5> shape(x.lead.begin(), x.lead.end());
+            shape.push_back(w.rows);
+            out = empty(shape, f32 ? at::kFloat : at::kBFloat16);
+        } else {
+            const Flat o = flat_of(a[5], "out", device);
+            out = *tensor_of(a[5], "out");
+            of_type(out, "out", f32 ? at::kFloat : at::kBFloat16);
+            same_lead(o, "out", x.lead, w.rows);
+            stride = o.stride;
+        }
+        const at::Tensor work = workspace_of(a[6], 2, device, on.h, need);
+        done(spec_matmul_e4m3(x.p, x.stride, static_cast<const float*>(xs.data_ptr()), xs.stride(-1), w.p, w.stride,
+                              static_cast<const float*>(ws.p), ws.stride, (int)x.rows, (int)w.rows, (int)x.cols, out.data_ptr(),
+                              f32 ? SPEC_DTYPE_F32 : SPEC_DTYPE_BF16, stride, work.data_ptr(), work.nbytes(), on.h),
+             "spec_matmul_e4m3");
+        return wrap(out);
+    });
+}
+
 #define SV_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {SV_METHOD(kv_append), SV_METHOD(kv_read), SV_METHOD(kv_compact), SV_METHOD(paged_attention),
-                          SV_METHOD(token_logprobs), {nullptr, nullptr, 0, nullptr}};
+                          SV_METHOD(token_logprobs), SV_METHOD(add_norm), SV_METHOD(gated_act), SV_METHOD(quantize_e4m3),
+                          SV_METHOD(matmul_e4m3), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
