@@ -26,6 +26,30 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// One lane of a converged warp.  (Loads and products are issued by loops that the whole warp
+// runs, so that addresses and descriptors stay in uniform registers: in a branch of one lane
+// the four products of a step took 315 cycles to issue.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, limit));
+}
+// Whether the phase is complete, without waiting: asked a step ahead, the answer (some 100 cycles)
+// comes while the step before is issued.
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // The address of a shared-memory place in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -43,23 +67,17 @@ __device__ __forceinline__ float ld_scale(const float* p) {
     asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Four bytes to shared memory, asynchronously (zero without `have`); the arrival of the thread's
+// copies so far on a barrier; the wait for all of them.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool have) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(have ? 4 : 0) : "memory");
 }
-// wait_bounded for a barrier that the other CTA of the pair arrives on.
-__device__ __forceinline__ bool wait_bounded_cluster(uint64_t* bar, uint32_t parity, uint32_t limit) {
-    for (uint32_t i = 0; i < limit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    }
-    return false;
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
@@ -75,9 +93,17 @@ __device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+// A box from shared memory (written through proxy_fence before), as a group of its own; the wait until
+// all but N of the thread's groups have been read, and until all are written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+template <int N>
+__device__ __forceinline__ void tma_store_wait() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void map_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -119,7 +145,7 @@ __device__ __forceinline__ void tc_ld32_done(float* v) {
 }
 
 // ---- few rows ----------------------------------------------------------------------
-// Up to 128 rows of x: the product is taken transposed, so that 128 weight rows are the
+// Up to 64 rows of x: the product is taken transposed, so that 128 weight rows are the
 // rows that the instruction wants and the few rows of x its free dimension T.  The weights are
 // read once, which bounds these calls.  A tile of 128 weight rows is shared by a cluster of S
 // CTAs, each with its part of the contraction; they add their sums over distributed shared
@@ -131,50 +157,51 @@ __device__ __forceinline__ void tc_ld32_done(float* v) {
 template <int T>
 struct FewCfg {
     static constexpr int SCALE = T * 4 < 128 ? 128 : T * 4;
-    static constexpr int STAGES = T <= 32 ? 5 : T <= 64 ? 4 : 3;
-    static constexpr int NB = T <= 64 ? 4 : 2;            // accumulators
-    static constexpr int TMEM = NB * T;                   // columns: 64, 128, 256, 256
+    static constexpr int STAGES = T <= 16 ? 6 : T <= 32 ? 5 : 4;         // and accumulators: one a stage
+    static constexpr int CTAS = 2;                        // on an SM
+    static constexpr int TMEM = T * STAGES <= 128 ? 128 : 256;
     static constexpr int X_AT = kMmBytes, STAGE = kMmBytes + T * kMmTile;
     static constexpr int SCALE_AT = STAGES * STAGE;
     static constexpr int SMEM = SCALE_AT + STAGES * SCALE + 1024;        // and room to align
     static constexpr int THREADS = 192;
-    static_assert(2 * (SMEM + 2048) <= 228 * 1024, "two CTAs an SM");
+    static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && CTAS * TMEM <= 512, "what an SM has");
+    static_assert(3 * (SMEM + 1024) > 228 * 1024, "no more CTAs than tensor memory has room for");
     static_assert(T * 512 <= SCALE_AT, "the sums of a CTA fit the ring");
 };
 
 template <int T>
-__global__ void __launch_bounds__(FewCfg<T>::THREADS, 2) matmul_few_kernel(const MatmulArgs a, uint32_t limit,
+__global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit,
                                                                           const __grid_constant__ CUtensorMap xmap,
                                                                           const __grid_constant__ CUtensorMap wmap,
                                                                           const __grid_constant__ CUtensorMap smap, int S) {
     using C = FewCfg<T>;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], t_full[C::NB], t_empty[C::NB], drained;
+    // done: a step's products are complete; empty: its sums are taken, its stage and accumulator free
+    __shared__ __align__(8) uint64_t full[C::STAGES], done[C::STAGES], empty[C::STAGES], drained;
     __shared__ uint32_t tmem_at;
     __shared__ int failed;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S;     // (a cluster: S consecutive CTAs)
     const int blocks = (a.K + kMmTile - 1) / kMmTile;
     const int b0 = (int)((long long)blocks * rank / S), n = (int)((long long)blocks * (rank + 1) / S) - b0;
     const int n0 = tile * kMmTile;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1 + 4);                   // the products, and four warps that read scales
+    if (warp == 0) {
+        if (elect_one()) {
+            for (int i = 0; i < C::STAGES; ++i) {
+                mbar_init(&full[i], 1);
+                mbar_init(&done[i], 1);
+                mbar_init(&empty[i], 4);
+            }
+            mbar_init(&drained, 1);
+            mbar_init_fence();
+            failed = 0;
+            map_prefetch(&wmap);
+            map_prefetch(&xmap);
+            map_prefetch(&smap);
         }
-        for (int i = 0; i < C::NB; ++i) {
-            mbar_init(&t_full[i], 1);
-            mbar_init(&t_empty[i], 4);
-        }
-        mbar_init(&drained, 1);
-        mbar_init_fence();
-        failed = 0;
-        // the first weights on their way into L2 while the kernel before ends
-        for (int i = 0; i < C::STAGES && i < n; ++i) tma_prefetch_2d(&wmap, (b0 + i) * kMmTile, n0);
-        map_prefetch(&xmap);
-        map_prefetch(&smap);
+        __syncwarp();
     }
     if (warp == 1) tc_alloc(&tmem_at, C::TMEM);
     pdl_trigger();
@@ -186,49 +213,56 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, 2) matmul_few_kernel(const
 
     f32x2 acc[T / 2];
     if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % C::STAGES;
-                if (i >= C::STAGES && !wait_bounded(&empty[s], (i / C::STAGES - 1) & 1, limit)) break;
-                const uint32_t at = smem_addr(smem + s * C::STAGE);
+        int i = 0, s = 0, phase = 0;                       // step, its stage, how often the ring has come round (mod 2)
+        const uint32_t base = smem_addr(smem);
+        for (; i < n; ++i) {
+            if (i >= C::STAGES && !wait_warp(&empty[s], phase ^ 1, limit)) break;
+            const uint32_t at = base + s * C::STAGE;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], C::STAGE + T * 4);
                 tma_2d(at, &wmap, (b0 + i) * kMmTile, n0, &full[s]);
                 tma_2d(at + C::X_AT, &xmap, (b0 + i) * kMmTile, 0, &full[s]);
-                tma_2d(smem_addr(smem + C::SCALE_AT + s * C::SCALE), &smap, 0, b0 + i, &full[s]);
+                tma_2d(base + C::SCALE_AT + s * C::SCALE, &smap, 0, b0 + i, &full[s]);
             }
-            if (i < n) failed = 1;
-            // every copy has landed and every commit has arrived before the CTA ends
-            for (int j = max(0, i - C::STAGES); j < i; ++j) {
-                const int s = j % C::STAGES;
-                const uint32_t parity = (j / C::STAGES) & 1;
-                if (!wait_bounded(&full[s], parity, kTcWaitLimit) || !wait_bounded(&empty[s], parity, limit)) failed = 1;
+            __syncwarp();
+            if (++s == C::STAGES) {
+                s = 0;
+                phase ^= 1;
             }
         }
+        bool ok = i == n;
+        // every copy has landed and every commit has arrived before the CTA ends
+        for (int j = max(0, i - C::STAGES); j < i; ++j) {
+            const int k = j % C::STAGES;
+            const uint32_t parity = (j / C::STAGES) & 1;
+            if (!wait_warp(&full[k], parity, kTcWaitLimit) || !wait_warp(&done[k], parity, limit)) ok = false;
+        }
+        if (!ok) failed = 1;
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id = tc_idesc(true, false, false, T);
-            bool ok = true;
-            int i = 0;
-            for (; i < n; ++i) {
-                const int s = i % C::STAGES, t = i % C::NB;
-                ok = wait_bounded(&full[s], (i / C::STAGES) & 1, limit) &&
-                     (i < C::NB || wait_bounded(&t_empty[t], (i / C::NB - 1) & 1, limit));
-                if (!ok) break;
-                tc_after();
-                const uint32_t at = smem_addr(smem + s * C::STAGE);
-                const uint64_t wd = tc_desc(at, 16, 1024), xd = tc_desc(at + C::X_AT, 16, 1024);
+        const uint32_t id = tc_idesc(true, false, false, T);
+        const uint64_t base = tc_desc(smem_addr(smem), 16, 1024);
+        int i = 0, s = 0, phase = 0;
+        for (; i < n; ++i) {
+            if (!wait_warp(&full[s], phase, limit)) break;
+            tc_after();
+            const uint64_t wd = base + s * (C::STAGE >> 4), xd = wd + (C::X_AT >> 4);
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma<true>(tmem + t * T, wd + 2 * k, xd + 2 * k, id, k > 0);
-                tc_commit(&empty[s]);
-                tc_commit(&t_full[t]);
+                for (int k = 0; k < 4; ++k) tc_mma<true>(tmem + s * T, wd + 2 * k, xd + 2 * k, id, k > 0);
+                tc_commit(&done[s]);
             }
-            if (!ok) {
-                failed = 1;
-                if (i > 0) {
-                    tc_commit(&drained);
-                    wait_bounded(&drained, 0, kTcWaitLimit);
-                }
+            __syncwarp();
+            if (++s == C::STAGES) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        if (i < n) {
+            failed = 1;
+            if (i > 0) {
+                if (elect_one()) tc_commit(&drained);
+                __syncwarp();
+                wait_warp(&drained, 0, kTcWaitLimit);
             }
         }
     } else {
@@ -236,26 +270,28 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, 2) matmul_few_kernel(const
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
         for (int c = 0; c < T / 2; ++c) acc[c] = 0;
+        // the tile's scales, 32 steps at a time, a lane each (one ahead of its use, a load a step
+        // held every step up for the memory's answer)
         const float* wsc = a.wscale + (int64_t)tile * a.ws_stride + b0;
-        float wnext = ld_scale(wsc);
+        float wl = 0.f;
         bool ok = true;
+        int s = 0, phase = 0;
         for (int i = 0; i < n; ++i) {
-            const int s = i % C::STAGES, t = i % C::NB;
-            const f32x2 w2 = f2_pack(wnext, wnext);
-            if (i + 1 < n) wnext = ld_scale(wsc + i + 1);
-            ok = wait_bounded(&t_full[t], (i / C::NB) & 1, limit);
-            ok = __all_sync(0xffffffffu, ok);
+            if ((i & 31) == 0 && i + lane < n) wl = ld_scale(wsc + i + lane);
+            const float wf = __shfl_sync(0xffffffffu, wl, i & 31);
+            const f32x2 w2 = f2_pack(wf, wf);
+            ok = wait_warp(&done[s], phase, limit);
             if (!ok) break;
             tc_after();
             const float4* xs = reinterpret_cast<const float4*>(smem + C::SCALE_AT + s * C::SCALE);
             float v[2][16];
-            tc_ld16_start(from + t * T, v[0]);
+            tc_ld16_start(from + s * T, v[0]);
 #pragma unroll
             for (int c = 0; c < T; c += 16) {
                 float* now = v[(c >> 4) & 1];
                 tc_wait_ld();
                 tc_ld16_done(now);
-                if (c + 16 < T) tc_ld16_start(from + t * T + c + 16, v[((c >> 4) + 1) & 1]);
+                if (c + 16 < T) tc_ld16_start(from + s * T + c + 16, v[((c >> 4) + 1) & 1]);
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 f = xs[(c + e) >> 2];
@@ -267,9 +303,10 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, 2) matmul_few_kernel(const
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&t_empty[t]);
-                mbar_arrive(&empty[s]);
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == C::STAGES) {
+                s = 0;
+                phase ^= 1;
             }
         }
         if (!ok && lane == 0) failed = 1;
@@ -320,54 +357,148 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, 2) matmul_few_kernel(const
     if (warp == 1) tc_dealloc(tmem, C::TMEM);
 }
 
-// ---- many rows ---------------------------------------------------------------------
-// A pair of CTAs takes 256 rows of x times T weight rows (cta_group::2: each loads its 128
-// rows of x and half of the weight rows, and holds its 128 rows' sums), and goes on to
-// further tiles.  A thread of the sums owns a row of x and half of a tile's columns, which lie in one
-// 128-block of the weights: the two scales of a step are one factor.
-//   warp 0      loads, warp 1 issues the products (the pair's first CTA, for both)
-//   warps 4-11  running sums, then the tile's output
-template <int T>
-struct ManyCfg {
-    static constexpr int NB = 512 / T > 4 ? 4 : 512 / T;  // accumulators
-    static constexpr int TMEM = NB * T;
-    static constexpr int X_BYTES = kMmBytes, W_BYTES = T / 2 * kMmTile, STAGE = X_BYTES + W_BYTES;
-    static constexpr int STAGES = 192 * 1024 / STAGE > 8 ? 8 : 192 * 1024 / STAGE;
-    static constexpr int OUT_AT = STAGES * STAGE;         // 4 KB of a warp's output
-    static constexpr int SMEM = OUT_AT + 8 * 4096 + 1024;
-    static constexpr int HALF = T / 2;
-    static constexpr int THREADS = 384;
-    static_assert(SMEM <= 227 * 1024, "dynamic shared memory");
+// ---- shares and parts ----------------------------------------------------------------
+// For more rows the steps (blocks of the contraction) of all tiles, end to end, are dealt to pairs of CTAs:
+// whole tiles, or equal shares that may begin and end inside a tile.  Of a tile in several
+// shares, each warp of each pair leaves its part of the sums in the workspace and takes a ticket; the
+// one that takes the last adds the parts in their order, whichever that was, and writes the
+// output.  Nobody waits for anybody.
+struct MmPlan {
+    long long tiles, total;            // steps of all tiles
+    int pairs, blocks, whole;          // blocks: steps of a tile
+    int W, tiles_m;                    // a tile's weight rows; tiles of 256 rows of x
+    unsigned long long tag;
+    __device__ __forceinline__ long long begin(int p) const { return whole ? tiles * p / pairs * blocks : total * p / pairs; }
+    // the pair whose (equal) share has step u
+    __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * pairs - 1) / total); }
 };
+// The workspace: error word (256 bytes), a ticket for each pair's last tile, CTA and warp, two parts a pair.
+constexpr int kMmMaxPairs = 80;
+constexpr size_t kMmTicketAt = 256;
+constexpr size_t kMmPartAt = kMmTicketAt + (size_t)kMmMaxPairs * 16 * 8;
+constexpr size_t kMmPartBytes = (size_t)256 * 256 * 4;     // of the widest tile
 
-template <int T>
-__global__ void __launch_bounds__(ManyCfg<T>::THREADS, 1) matmul_many_kernel(const MatmulArgs a, uint32_t limit, int tiles_m, int tiles,
-                                                                            const __grid_constant__ CUtensorMap xmap,
-                                                                            const __grid_constant__ CUtensorMap wmap) {
-    using C = ManyCfg<T>;
+// A tile's parts are those of pairs p0 to p1, the first the last part of its pair.
+struct MmParts {
+    long long t0;
+    int p0, p1;
+    __device__ __forceinline__ MmParts(const MmPlan& plan, int tile) {
+        t0 = (long long)tile * plan.blocks;
+        p0 = plan.of(t0);
+        p1 = plan.of(t0 + plan.blocks - 1);
+    }
+    __device__ __forceinline__ float* part(const MmPlan& plan, char* ws, int p) const {
+        return reinterpret_cast<float*>(ws + kMmPartAt + (size_t)(2 * p + (plan.begin(p) < t0)) * kMmPartBytes);
+    }
+};
+// A ticket of those of launch `tag`: how many were taken before.  Whatever the word held, a ticket
+// of another launch counts as none; the last to come leaves zero, for a replay of the same launch.
+__device__ __forceinline__ unsigned tickets_taken(unsigned long long w, unsigned long long tag) {
+    return (w >> 24) == tag ? (unsigned)(w & 0xffffffu) : 0u;
+}
+__device__ __forceinline__ unsigned take_ticket(unsigned long long* w, unsigned long long tag) {
+    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w), seen;
+    do {
+        seen = old;
+        old = atomicCAS(w, seen, (seen >> 24) == tag ? seen + 1 : (tag << 24) + 1);
+    } while (old != seen);
+    return tickets_taken(seen, tag);
+}
+// The warp's, after what its lanes have written: whether it was the last of n.
+__device__ __forceinline__ bool last_ticket(unsigned long long* w, unsigned long long tag, int n, int lane) {
+    __threadfence();
+    __syncwarp();
+    // (votes: a warp that knows that it stays together keeps its counters in uniform registers)
+    if (!__any_sync(0xffffffffu, lane == 0 && (int)take_ticket(w, tag) == n - 1)) return false;
+    if (lane == 0) *w = 0;
+    __threadfence();
+    return true;
+}
+
+// ---- more rows ---------------------------------------------------------------------
+// A pair of CTAs takes 256 rows of x times W weight rows (cta_group::2: each loads its 128
+// rows of x and half of the weight rows, and holds its 128 rows' sums).  W, a multiple of 32 up to
+// 256, is chosen by the launch so that the tiles fill the pairs evenly.
+//   warp 0      loads
+//   warp 1      issues the products (the pair's first CTA, for both)
+//   warp 2      brings the scales
+//   warps 4-11  running sums, then the tile's output: a thread owns a row of x and a half of the
+//               tile's columns
+// TWO (W 192 or 256): the halves of the columns are products of their own, each with its
+// accumulators, so that the second half's run while the first's are read.  Between an
+// accumulator's last product and its next lie a commit, a wake, its reading and an arrival in the other
+// CTA, some 1400 cycles in which two accumulators of 256 columns left the tensor cores idle half the
+// time.
+struct ManyCfg {
+    static constexpr int EW = 8;                           // warps of the sums
+    static constexpr int STAGES = 8, NB = 4;               // at most
+    static constexpr int COLS = 128;                       // a warp's columns, at most
+    static constexpr int X_BYTES = kMmBytes;
+    static constexpr int OUT_AT = 185 * 1024;              // two pieces of 32 rows x 64 bytes a warp
+    static constexpr int FS = 4;                           // groups of four steps whose scales are held
+    static constexpr int F_BYTES = 128 * 16 + 64;          // the rows' four; for each half, those of two blocks of the weights
+    static constexpr int F_AT = OUT_AT + EW * 4096;
+    static constexpr int SMEM = F_AT + FS * F_BYTES + 1024;
+    static constexpr int THREADS = 128 + EW * 32;
+    // registers: the launch's share a thread, and how the warpgroups split it
+    static constexpr int REGS = 65536 / THREADS / 8 * 8, LESS = 56;
+    static constexpr int MORE = (REGS * THREADS - LESS * 128) / (EW * 32) / 8 * 8;
+    static constexpr int PART = COLS * 32;                 // floats of a warp's part
+    static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
+};
+// Whether the halves of a tile's columns are products of their own (a pair's product has a
+// multiple of 32 columns); stages of a ring; accumulators (of a half, where there are two).
+__host__ __device__ constexpr bool two_halves(int W) { return W > 128 && W % 64 == 0; }
+__host__ __device__ constexpr unsigned stages_of(int W) {
+    return ManyCfg::OUT_AT / (ManyCfg::X_BYTES + W / 2 * kMmTile) < ManyCfg::STAGES ? ManyCfg::OUT_AT / (ManyCfg::X_BYTES + W / 2 * kMmTile)
+                                                                                     : ManyCfg::STAGES;
+}
+__host__ __device__ constexpr unsigned buffers_of(int W) {
+    return 512 / W < ManyCfg::NB ? 512 / W : ManyCfg::NB;
+}
+template <int W, bool SPLIT>
+__global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const MatmulArgs a, uint32_t limit, const MmPlan plan,
+                                                                         const __grid_constant__ CUtensorMap xmap,
+                                                                         const __grid_constant__ CUtensorMap wmap,
+                                                                         const __grid_constant__ CUtensorMap omap, bool by_tma, int vec) {
+    using C = ManyCfg;
+    constexpr bool TWO = two_halves(W);
+    constexpr int H = W / 2;
+    constexpr unsigned stages = stages_of(W), buffers = buffers_of(W);
+    constexpr uint32_t stage_bytes = C::X_BYTES + H * kMmTile;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[C::STAGES], empty[C::STAGES], t_full[C::NB], t_empty[C::NB], drained;
+    // done: a step's products (of a half) are complete; after the second half's its stage is free.  (As
+    // many as stages: an accumulator's next product waits for the sums, a stage's next load for done, so
+    // no phase is passed unseen.)
+    __shared__ __align__(8) uint64_t full[C::STAGES], done[2][C::STAGES], t_empty[2][C::NB], f_full[C::FS], f_empty[C::FS], drained;
     __shared__ uint32_t tmem_at;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int blocks = (a.K + kMmTile - 1) / kMmTile;
+    const int pair = blockIdx.x >> 1, blocks = plan.blocks, tiles_m = plan.tiles_m;
+    const long long u0 = plan.begin(pair), u1 = plan.begin(pair + 1);
+    const int first_tile = (int)(u0 / blocks), first_b = (int)(u0 - (long long)first_tile * blocks);
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&done[0][i], 1);
+            mbar_init(&done[1][i], 1);
         }
-        for (int i = 0; i < C::NB; ++i) {
-            mbar_init(&t_full[i], 1);
-            mbar_init(&t_empty[i], 2 * 8);                 // both CTAs' warps
+        for (int i = 0; i < C::NB; ++i) {                  // both CTAs' warps
+            mbar_init(&t_empty[0][i], TWO ? C::EW : 2 * C::EW);
+            mbar_init(&t_empty[1][i], C::EW);
+        }
+        for (int i = 0; i < C::FS; ++i) {
+            mbar_init(&f_full[i], 32);
+            mbar_init(&f_empty[i], C::EW);
         }
         mbar_init(&drained, 1);
         mbar_init_fence();
         map_prefetch(&xmap);
         map_prefetch(&wmap);
+        if (by_tma) map_prefetch(&omap);
     }
-    if (warp == 1) pair_alloc(&tmem_at, C::TMEM);
+    if (warp == 1) pair_alloc(&tmem_at, 512);
     pdl_trigger();
     tc_before();
     cluster_sync();
@@ -377,188 +508,340 @@ __global__ void __launch_bounds__(ManyCfg<T>::THREADS, 1) matmul_many_kernel(con
     int32_t* error = reinterpret_cast<int32_t*>(a.ws);
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 0 && lane == 0) {
-            unsigned it = 0;
-            bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs) {
-                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128, n0 = tn * T + (int)rank * C::HALF;
-                for (int b = 0; b < blocks; ++b, ++it) {
-                    const unsigned s = it % C::STAGES;
-                    if (it >= C::STAGES && !wait_bounded(&empty[s], (it / C::STAGES - 1) & 1, limit)) {
-                        ok = false;
-                        break;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LESS));
+        if (warp == 0) {
+            bool ok = true, free = false;
+            unsigned it = 0, s = 0, phase = 0;             // step, its stage, how often the ring has come round (mod 2)
+            const uint32_t base = smem_addr(smem), bars = cluster_addr(smem_addr(full), 0);
+            uint64_t(&last)[C::STAGES] = done[TWO ? 1 : 0];
+            const bool lead = elect_one();
+            long long left = u1 - u0;
+            for (int tile = first_tile, b = first_b; ok && left > 0; ++tile, b = 0) {
+                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
+                // (a product's columns are half the first CTA's weight rows, half the second's)
+                const int n0 = tn * W + (int)rank * (TWO ? H / 2 : H);
+                for (; b < blocks && left > 0; ++b, ++it, --left) {
+                    if (it >= stages && !free) {
+                        ok = wait_warp(&last[s], phase ^ 1, limit);
+                        if (!ok) break;
                     }
-                    const uint32_t at = smem_addr(smem + s * C::STAGE), bar = cluster_addr(smem_addr(&full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
-                    tma_2d_pair(at, &xmap, b * kMmTile, m0, bar);
-                    tma_2d_pair(at + C::X_BYTES, &wmap, b * kMmTile, n0, bar);
+                    const uint32_t at = base + s * stage_bytes, bar = bars + s * 8;
+                    const unsigned now = s;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    free = phase_done(&last[s], phase ^ 1);
+                    if (lead) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[now], 2 * stage_bytes);
+                        tma_2d_pair(at, &xmap, b * kMmTile, m0, bar);
+                        tma_2d_pair(at + C::X_BYTES, &wmap, b * kMmTile, n0, bar);
+                        if constexpr (TWO) tma_2d_pair(at + C::X_BYTES + H / 2 * kMmTile, &wmap, b * kMmTile, n0 + H, bar);
+                    }
+                    free = __all_sync(0xffffffffu, free);
                 }
             }
             // every copy has landed and every commit has arrived before the CTA ends
-            for (unsigned j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
-                const unsigned s = j % C::STAGES, parity = (j / C::STAGES) & 1;
-                if (rank == 0 && !wait_bounded(&full[s], parity, kTcWaitLimit)) ok = false;
-                if (!wait_bounded(&empty[s], parity, limit)) ok = false;
+            for (unsigned j = it > stages ? it - stages : 0; j < it; ++j) {
+                const unsigned k = j % stages, parity = (j / stages) & 1;
+                if (rank == 0 && !wait_warp(&full[k], parity, kTcWaitLimit)) ok = false;
+                if (!wait_warp(&last[k], parity, limit)) ok = false;
             }
-            if (!ok) raise_error(error, SPEC_DEVERR_TIMEOUT);
-        } else if (warp == 1 && rank == 0 && lane == 0) {
-            const uint32_t id = tc_idesc(true, false, false, T, 256);
-            unsigned it = 0;
-            bool ok = true;
-            for (int tile = pair; ok && tile < tiles; tile += pairs) {
-                for (int b = 0; b < blocks; ++b, ++it) {
-                    const unsigned s = it % C::STAGES, t = it % C::NB;
-                    ok = wait_bounded_cluster(&full[s], (it / C::STAGES) & 1, limit) &&
-                         (it < C::NB || wait_bounded_cluster(&t_empty[t], (it / C::NB - 1) & 1, limit));
+            if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+        } else if (warp == 1 && rank == 0) {
+            const uint32_t id = tc_idesc(true, false, false, TWO ? H : W, 256);
+            const uint64_t base = tc_desc(smem_addr(smem), 16, 1024);
+            unsigned it = 0, s = 0, phase = 0, t = 0, t_phase = 0;
+            const bool lead = elect_one();
+            bool ok = true, ready = false;
+            // (a barrier's phase before its first counts as complete: no step waits for an accumulator that
+            // nothing has used)
+            for (long long left = u1 - u0; left > 0; --left, ++it) {
+                if (!ready) {
+                    ok = wait_warp(&full[s], phase, limit) && wait_warp(&t_empty[0][t], t_phase ^ 1, limit);
                     if (!ok) break;
-                    tc_after();
-                    const uint32_t at = smem_addr(smem + s * C::STAGE);
-                    const uint64_t xd = tc_desc(at, 16, 1024), wd = tc_desc(at + C::X_BYTES, 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) pair_mma(tmem + t * T, xd + 2 * k, wd + 2 * k, id, k > 0);
-                    pair_commit(&empty[s]);
-                    pair_commit(&t_full[t]);
                 }
+                tc_after();
+                const uint64_t xd = base + s * (stage_bytes >> 4), wd = xd + (C::X_BYTES >> 4);
+                const uint32_t to = tmem + t * (TWO ? H : W);
+                const unsigned now = s;
+                if constexpr (TWO) {
+                    const bool second = phase_done(&t_empty[1][t], t_phase ^ 1);
+                    if (lead) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) pair_mma(to, xd + 2 * k, wd + 2 * k, id, k > 0);
+                        pair_commit(&done[0][now]);
+                    }
+                    if (!__all_sync(0xffffffffu, second)) {
+                        ok = wait_warp(&t_empty[1][t], t_phase ^ 1, limit);
+                        if (!ok) {
+                            ++it;                          // (products have been issued)
+                            break;
+                        }
+                    }
+                    tc_after();
+                }
+                if (++s == stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                if (++t == buffers) {
+                    t = 0;
+                    t_phase ^= 1;
+                }
+                const bool next = phase_done(&full[s], phase) & phase_done(&t_empty[0][t], t_phase ^ 1);
+                if (lead) {
+                    const uint64_t wd2 = TWO ? wd + (H / 2 * kMmTile >> 4) : wd;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pair_mma(to + (TWO ? 256 : 0), xd + 2 * k, wd2 + 2 * k, id, k > 0);
+                    pair_commit(&done[TWO ? 1 : 0][now]);
+                }
+                ready = __all_sync(0xffffffffu, next);
             }
             if (!ok) {
-                raise_error(error, SPEC_DEVERR_TIMEOUT);
+                if (lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
                 if (it > 0) {
-                    pair_commit(&drained);
-                    wait_bounded(&drained, 0, kTcWaitLimit);
+                    if (lead) pair_commit(&drained);
+                    __syncwarp();
+                    wait_warp(&drained, 0, kTcWaitLimit);
                 }
             }
+        } else if (warp == 2) {
+            // Scales, four steps at a time, by asynchronous copies some groups ahead of the sums.  (Loaded
+            // through registers by the threads of the sums, four steps ahead, they held each
+            // step up by 600 to 700 cycles.)
+            unsigned gi = 0;
+            bool ok = true;
+            long long left = u1 - u0;
+            for (int tile = first_tile, at = first_b; ok && left > 0; ++tile, at = 0) {
+                const int end = (int)min((long long)blocks, at + left);
+                left -= end - at;
+                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
+                // the first 16 lanes: a half's first or second 128-block of the weights, and a step of the four
+                const int wrow = min((tn * W + (lane >> 3 & 1) * H) / kScaleBlock + (lane >> 2 & 1), (a.N - 1) / kScaleBlock);
+                const float* wsc = a.wscale + (int64_t)wrow * a.ws_stride;
+                for (int b4 = at; b4 < end; b4 += 4, ++gi) {
+                    const unsigned s = gi % C::FS;
+                    if (gi >= C::FS) ok = wait_warp(&f_empty[s], (gi / C::FS - 1) & 1, limit);
+                    if (!ok) break;
+                    const uint32_t to = smem_addr(smem + C::F_AT + s * C::F_BYTES);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int m = m0 + r * 32 + lane;
+                            const bool have = m < a.M && b4 + j < end;
+                            copy4(to + (r * 32 + lane) * 16 + j * 4, have ? a.xscale + (int64_t)(b4 + j) * a.xs_stride + m : a.xscale, have);
+                        }
+                    if (lane < 16) {
+                        const int b = b4 + (lane & 3);
+                        copy4(to + 128 * 16 + lane * 4, b < end ? wsc + b : wsc, b < end);
+                    }
+                    copies_arrive(&f_full[s]);
+                }
+            }
+            copies_done();
+            if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int part = (warp - 4) >> 2, quad = warp & 3;
-        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + part * C::HALF;
-        unsigned char* stage = smem + C::OUT_AT + (warp - 4) * 4096;
-        unsigned it = 0;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE));
+        const int part = (warp - 4) >> 2, quad = warp & 3, half = TWO ? part : 0;
+        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (TWO ? part * 256 : part * H), step = TWO ? H : W;
+        unsigned char* const pieces = smem + C::OUT_AT + (warp - 4) * 4096;
+        const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), 0);
+        unsigned gi = 0, s = 0, phase = 0, t = 0, stored = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles; tile += pairs) {
+        long long left = u1 - u0;
+        for (int tile = first_tile, at = first_b; left > 0; ++tile, at = 0) {
+            const int end = (int)min((long long)blocks, at + left);
+            left -= end - at;
             const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128 + quad * 32;
-            const int n0 = tn * T + part * C::HALF, m = m0 + lane;
-            f32x2 acc[C::HALF / 2];
+            const int n0 = tn * W + part * H;
+            const int split = (n0 / kScaleBlock + 1) * kScaleBlock - n0;     // columns of the first block
+            float acc[C::COLS];
 #pragma unroll
-            for (int c = 0; c < C::HALF / 2; ++c) acc[c] = 0;
-            const float* xsc = a.xscale + m;
-            const float* wsc = a.wscale + (int64_t)min(n0 / kScaleBlock, (a.N - 1) / kScaleBlock) * a.ws_stride;
-            // factors of four steps ahead
-            float f[4], g[4];
-            auto load = [&](int b, int j) {
-                const bool have = b < blocks && m < a.M;
-                f[j] = have ? ld_scale(xsc + (int64_t)b * a.xs_stride) : 0.f;
-                g[j] = b < blocks ? ld_scale(wsc + b) : 0.f;
-            };
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load(j, j);
-            for (int b4 = 0; ok && b4 < blocks; b4 += 4) {
+            for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+            for (int b4 = at; ok && b4 < end; b4 += 4, ++gi) {
+                const unsigned char* scales = smem + C::F_AT + gi % C::FS * C::F_BYTES;
+                ok = wait_warp(&f_full[gi % C::FS], (gi / C::FS) & 1, limit);
+                if (!ok) break;
+                const float4 fx = *reinterpret_cast<const float4*>(scales + (quad * 32 + lane) * 16);
+                const float4 fw = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32);
+                const float4 fv = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32 + 16);
+                const float f[4] = {fx.x * fw.x, fx.y * fw.y, fx.z * fw.z, fx.w * fw.w};
+                const float g[4] = {fx.x * fv.x, fx.y * fv.y, fx.z * fv.z, fx.w * fv.w};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&f_empty[gi % C::FS]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!ok || b4 + j >= blocks) continue;
-                    const unsigned t = it % C::NB;
-                    const float fg = f[j] * g[j];
-                    const f32x2 f2 = f2_pack(fg, fg);
-                    load(b4 + j + 4, j);
-                    ok = wait_bounded(&t_full[t], (it / C::NB) & 1, limit);
-                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok || b4 + j >= end) continue;
+                    ok = wait_warp(&done[half][s], phase, limit);
                     if (!ok) continue;
                     tc_after();
-                    float v[2][32];
-                    tc_ld32_start(from + t * T, v[0]);
+                    constexpr int L = 16;                  // columns a load
+                    float v[2][L];
+                    tc_ld16_start(from + t * step, v[0]);
 #pragma unroll
-                    for (int c = 0; c < C::HALF; c += 32) {
-                        float* now = v[(c >> 5) & 1];
+                    for (int c = 0; c < C::COLS; c += L) {
+                        if (c >= H) break;
+                        float* now = v[(c / L) & 1];
                         tc_wait_ld();
-                        tc_ld32_done(now);
-                        if (c + 32 < C::HALF) {
-                            tc_ld32_start(from + t * T + c + 32, v[((c >> 5) + 1) & 1]);
+                        tc_ld16_done(now);
+                        if (c + L < H) {
+                            tc_ld16_start(from + t * step + c + L, v[(c / L + 1) & 1]);
                         } else {
                             tc_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&t_empty[t]), 0));
+                            if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
                         }
+                        const float fg = c < split ? f[j] : g[j];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            acc[(c + e) >> 1] = f2_fma(f2_pack(now[e], now[e + 1]), f2, acc[(c + e) >> 1]);
+                        for (int e = 0; e < L; ++e) acc[c + e] = fmaf(now[e], fg, acc[c + e]);
                     }
-                    ++it;
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    if (++t == buffers) t = 0;
                 }
             }
-            // ---- the tile's output, 128 bytes (or a narrow tile's 64) of the warp's 32 rows at a time
-            const float bad = ok ? 0.f : CUDART_NAN_F;
-            const int elt = a.f32 ? 4 : 2;
-            const bool wide = a.old * elt % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-            constexpr int G = C::HALF < 64 ? C::HALF : 64;  // columns at a time
+            if (!ok) {                                     // a result that is not valid shows
 #pragma unroll
-            for (int c0 = 0; c0 < C::HALF; c0 += G) {
-                if (n0 + c0 >= a.N) break;
+                for (int c = 0; c < C::COLS; ++c) acc[c] = CUDART_NAN_F;
+            }
+            if (SPLIT && end - at < blocks) {
+                const MmParts parts(plan, tile);
+                const int n = parts.p1 - parts.p0 + 1, w = (int)rank * C::EW + warp - 4;
+                unsigned long long* ticket = reinterpret_cast<unsigned long long*>(a.ws + kMmTicketAt) + parts.p0 * 16 + w;
+                auto part_of = [&](int p) {
+                    return reinterpret_cast<float4*>(parts.part(plan, a.ws, p)) + (size_t)w * (C::PART / 4) + lane;
+                };
+                auto add = [&](int p) {
+                    const float4* q = part_of(p);
+                    constexpr int B = H < 32 ? H / 4 : 8, NBATCH = H / (4 * B);     // loads of a batch; one ahead
+                    float4 x[2][B];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {              // (fp32: 32 columns at a time)
-                    if (h == 1 && (!a.f32 || G < 64)) break;
-                    const int cols = a.f32 ? 32 : G, first = c0 + h * 32;
-                    const int chunks = cols * elt / 16;    // 16-byte pieces of a row: 8, or 4
-                    auto place = [&](int r, int c) {
-                        return stage + (chunks == 8 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4));
-                    };
-                    __syncwarp();
-                    if (a.f32) {
+                    for (int c = 0; c < B; ++c) x[0][c] = __ldcg(q + 4 * c * 8);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            float x0, x1, x2, x3;
-                            f2_unpack(acc[(c0 + (h * 32) % G + 4 * c) >> 1], x0, x1);
-                            f2_unpack(acc[((c0 + (h * 32) % G + 4 * c) >> 1) + 1], x2, x3);
-                            *reinterpret_cast<float4*>(place(lane, c)) = make_float4(x0 + bad, x1 + bad, x2 + bad, x3 + bad);
+                    for (int k = 0; k < NBATCH; ++k) {
+                        if (k + 1 < NBATCH) {
+#pragma unroll
+                            for (int c = 0; c < B; ++c) x[(k + 1) & 1][c] = __ldcg(q + ((k + 1) * B + c) * 4 * 8);
                         }
-                    } else {
 #pragma unroll
-                        for (int c = 0; c < G / 8; ++c) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float lo, hi;
-                                f2_unpack(acc[((c0 + 8 * c) >> 1) + e], lo, hi);
-                                w[e] = pack_bf16(lo + bad, hi + bad);
-                            }
-                            *reinterpret_cast<uint4*>(place(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int c = 0; c < B; ++c) {
+                            float* to = acc + (k * B + c) * 4;
+                            const float4 y = x[k & 1][c];
+                            to[0] += y.x;
+                            to[1] += y.y;
+                            to[2] += y.z;
+                            to[3] += y.w;
                         }
                     }
+                };
+                // (of two parts, the second to be ready need not be written: their order does not matter)
+                bool second = false;
+                if (n == 2) {
+                    second = __any_sync(0xffffffffu, lane == 0 && tickets_taken(*reinterpret_cast<volatile unsigned long long*>(ticket), plan.tag) == 1);
+                }
+                if (!second) {
+                    float4* mine = part_of(pair);
+#pragma unroll
+                    for (int c = 0; c < H; c += 4) __stcg(mine + c * 8, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+                }
+                if (!last_ticket(ticket, plan.tag, n, lane)) continue;
+                if (n > 2) {
+#pragma unroll
+                    for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+                }
+#pragma unroll 1
+                for (int p = parts.p0; p <= parts.p1; ++p)
+                    if (n > 2 || p != pair) add(p);
+            }
+            // ---- the tile's output, in pieces of 64 bytes of the warp's 32 rows: by TMA where the rows are
+            // aligned, else (and for a last piece of half the columns) through the same place and registers
+            if (m0 >= a.M) continue;
+            auto piece = [&](unsigned char* at_, int r, int c) { return reinterpret_cast<uint4*>(at_ + r * 64 + ((c ^ (r >> 1 & 3)) << 4)); };
+            // cols columns from n on of the rows' 64 bytes, `vec` bytes a lane
+            auto put = [&](unsigned char* from_, int n, int cols) {
+                const int elt = a.f32 ? 4 : 2, at_ = lane * vec & 63, e = at_ / elt, step_ = vec / 2;      // rows at a time
+                const bool have = e < cols && n + e < a.N;
+                char* to = a.out + ((int64_t)(m0 + lane * vec / 64) * a.old + n) * elt + at_;
+#pragma unroll 4
+                for (int r = lane * vec / 64; r < 32; r += step_, to += (int64_t)step_ * a.old * elt) {
+                    const unsigned char* x = reinterpret_cast<unsigned char*>(piece(from_, r, at_ >> 4)) + (at_ & 15);
+                    if (!have || m0 + r >= a.M) continue;
+                    if (vec == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(x);
+                    else if (vec == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(x);
+                    else *reinterpret_cast<unsigned short*>(to) = *reinterpret_cast<const unsigned short*>(x);
+                }
+            };
+            auto send = [&](unsigned char* from_, int n, int cols, int full_cols) {
+                if (by_tma && cols == full_cols) {
+                    proxy_fence();
                     __syncwarp();
-                    const int per = 16 / elt;              // elements of a piece
-                    for (int i = lane; i < 32 * chunks; i += 32) {
-                        const int r = i / chunks, c = i - r * chunks, n = n0 + first + c * per;
-                        if (m0 + r >= a.M || n >= a.N) continue;
-                        char* to = a.out + ((int64_t)(m0 + r) * a.old + n) * elt;
-                        const uint4 w = *reinterpret_cast<const uint4*>(place(r, c));
-                        if (wide && n + per <= a.N) {
-                            *reinterpret_cast<uint4*>(to) = w;
-                        } else if (a.f32) {
-                            for (int e = 0; e < 4 && n + e < a.N; ++e) reinterpret_cast<uint32_t*>(to)[e] = u4_get(w, e);
-                        } else {
-                            for (int e = 0; e < 8 && n + e < a.N; ++e)
-                                reinterpret_cast<unsigned short*>(to)[e] = (unsigned short)(u4_get(w, e >> 1) >> 16 * (e & 1));
-                        }
+                    if (lane == 0) tma_store_2d(&omap, n, m0, smem_addr(from_));
+                    ++stored;
+                } else {
+                    __syncwarp();
+                    put(from_, n, cols);
+                    __syncwarp();
+                }
+            };
+            // (a piece's place is free again when the last store but one has been read)
+            auto place = [&]() {
+                if (by_tma) {
+                    if (lane == 0) tma_store_wait<1>();
+                    __syncwarp();
+                }
+                return pieces + (stored & 1) * 2048;
+            };
+            if (a.f32) {
+#pragma unroll
+                for (int c0 = 0; c0 < C::COLS; c0 += 16) {
+                    if (c0 >= H || n0 + c0 >= a.N) break;
+                    unsigned char* to = place();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float* x = acc + c0 + 4 * c;
+                        *piece(to, lane, c) =
+                            make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
                     }
+                    send(to, n0 + c0, 16, 16);
+                }
+            } else {
+#pragma unroll
+                for (int c0 = 0; c0 < C::COLS; c0 += 32) {
+                    if (c0 >= H || n0 + c0 >= a.N) break;
+                    unsigned char* to = place();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float* x = acc + c0 + 8 * c;
+                        *piece(to, lane, c) =
+                            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    }
+                    send(to, n0 + c0, min(32, H - c0), 32);
                 }
             }
         }
+        if (lane == 0) tma_store_wait_all();
+        __syncwarp();
         if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
     }
     tc_before();
     __syncthreads();
     cluster_sync();
     tc_after();
-    if (warp == 1) pair_dealloc(tmem, C::TMEM);
+    if (warp == 1) pair_dealloc(tmem, 512);
 }
 
 // ---- launches -----------------------------------------------------------------------
 static bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t inner, int64_t rows, int64_t stride_bytes, int box_inner,
-                   int box_rows, bool swizzle) {
+                   int box_rows, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows}, one[2] = {1, 1};
     return encoder() && encoder()(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -594,20 +877,65 @@ static cudaError_t launch_few_t(const MatmulArgs& a, int sms, cudaStream_t st) {
     });
     if (e != cudaSuccess) return e;
     const int tiles = (a.N - 1) / kMmTile + 1, blocks = scale_blocks(a.K);
+    // Clusters of a power of two: of six, which would use more of the SMs for 48 tiles, fewer fit at once
+    // (they stay within groups of SMs): 10.1 us for 7.5 at one row, N = 6144, K = 4096.
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= 2 * sms && S * 2 <= blocks) S *= 2;
+    while (S < 8 && tiles * S * 2 <= C::CTAS * sms && S * 2 <= blocks) S *= 2;
     CUtensorMap xm, wm, sm;
-    if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, T, true) ||
-        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, kMmTile, true) ||
-        !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, 1, false))
+    if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, T, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     return launch_clusters(kfn, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), xm, wm, sm, S);
 }
 
-template <int T>
-static cudaError_t launch_many_t(const MatmulArgs& a, int sms, cudaStream_t st) {
-    using C = ManyCfg<T>;
-    auto kfn = matmul_many_kernel<T>;
+// What a step of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows and
+// K = 1024 and 4096).
+struct MmWidth {
+    int W;
+    double step, end;
+};
+constexpr MmWidth kMmWidths[4] = {{64, 0.213, 0.6}, {128, 0.266, 1.2}, {192, 0.36, 1.7}, {256, 0.426, 2.0}};
+
+// Whole tiles in the width whose rounds of all pairs take the least, or equal shares, whose parts
+// cost their writing and reading, where that is less: few tiles with long contractions, or
+// little more than whole rounds.
+static MmPlan plan_many(const MatmulArgs& a, int sms) {
+    MmPlan p = {};
+    p.blocks = scale_blocks(a.K);
+    p.tiles_m = (a.M - 1) / 256 + 1;
+    const long long most = sms / 2 < kMmMaxPairs ? sms / 2 : kMmMaxPairs;
+    double best = 1e300;
+    for (const MmWidth& w : kMmWidths) {
+        const long long tiles = (long long)p.tiles_m * ((a.N - 1) / w.W + 1), total = tiles * p.blocks;
+        const auto take = [&](double us, long long pairs, int whole) {
+            if (us >= best) return;
+            best = us;
+            p.W = w.W;
+            p.whole = whole;
+            p.tiles = tiles;
+            p.total = total;
+            p.pairs = (int)pairs;
+        };
+        take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1);
+        if (w.W != 64 && w.W != 256) continue;
+        for (int n = 2; n <= 8; ++n) {
+            // (n: parts of a tile)
+            const long long pairs = tiles * n < most ? tiles * n : most;
+            if (tiles * (n - 1) >= most && n > 2) break;
+            if (total < 4 * pairs) break;
+            const long long steps = (total + pairs - 1) / pairs;
+            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + 4.0 + (n - 1) * (w.W == 64 ? 1.0 : 3.0), pairs, 0);
+        }
+    }
+    p.tag = next_launch_tag();
+    return p;
+}
+
+template <int W, bool SPLIT>
+static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStream_t st) {
+    using C = ManyCfg;
+    auto kfn = matmul_many_kernel<W, SPLIT>;
     static DeviceSlots slots = {};
     int unused = 0;
     cudaError_t e = device_once(slots, &unused, [&](int, int* o) {
@@ -615,18 +943,33 @@ static cudaError_t launch_many_t(const MatmulArgs& a, int sms, cudaStream_t st) 
         return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
-    const int tiles_m = (a.M - 1) / 256 + 1;
-    const long long tiles = (long long)tiles_m * ((a.N - 1) / T + 1);
-    if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
-    const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
-    CUtensorMap xm, wm;
-    if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, kMmTile, true) ||
-        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, C::HALF, true))
+    const int elt = a.f32 ? 4 : 2;
+    const bool by_tma = is_aligned(a.out, 16) && a.old * elt % 16 == 0 && a.old * elt < (1LL << 40);
+    // else the widest pieces that every row's begin allows
+    const uint64_t align = reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.old * elt;
+    const int vec = align % 8 == 0 ? 8 : align % 4 == 0 ? 4 : 2;
+    CUtensorMap xm, wm, om = {};
+    if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, two_halves(W) ? W / 4 : W / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        (by_tma && !map_2d(&om, a.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.N, a.M, a.old * elt,
+                           64 / elt, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
         return cudaErrorInvalidValue;
-    return launch_clusters(kfn, (int)pairs * 2, 2, C::THREADS, C::SMEM, st, a, wait_limit(), tiles_m, (int)tiles, xm, wm);
+    return launch_clusters(kfn, p.pairs * 2, 2, C::THREADS, C::SMEM, st, a, wait_limit(), p, xm, wm, om, by_tma, vec);
 }
 
-size_t matmul_workspace_size(int M, int N, int K) { return 256; }
+static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
+    if ((long long)((a.M - 1) / 256 + 1) * ((a.N - 1) / 64 + 1) >= (1LL << 31)) return cudaErrorInvalidValue;
+    const MmPlan p = plan_many(a, sms);
+    if (!p.whole) return p.W == 64 ? launch_many_t<64, true>(a, p, st) : launch_many_t<256, true>(a, p, st);
+    switch (p.W) {
+        case 64: return launch_many_t<64, false>(a, p, st);
+        case 128: return launch_many_t<128, false>(a, p, st);
+        case 192: return launch_many_t<192, false>(a, p, st);
+        default: return launch_many_t<256, false>(a, p, st);
+    }
+}
+
+size_t matmul_workspace_size(int M, int N, int K) { return kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
 
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     DeviceInfo di;
@@ -636,12 +979,7 @@ cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     if (a.M <= 16) return launch_few_t<16>(a, sms, st);
     if (a.M <= 32) return launch_few_t<32>(a, sms, st);
     if (a.M <= 64) return launch_few_t<64>(a, sms, st);
-    if (a.M <= 128) return launch_few_t<128>(a, sms, st);
-    // the tile's width by the number of waves that it takes
-    const long long tm = (a.M - 1) / 256 + 1, pairs = sms / 2;
-    auto cost = [&](int T) { return (tm * ((a.N - 1) / T + 1) + pairs - 1) / pairs * (T + 32); };
-    if (cost(256) <= cost(128) && cost(256) <= cost(64)) return launch_many_t<256>(a, sms, st);
-    return cost(128) <= cost(64) ? launch_many_t<128>(a, sms, st) : launch_many_t<64>(a, sms, st);
+    return launch_many(a, sms, st);
 }
 
 }  // namespace sv
