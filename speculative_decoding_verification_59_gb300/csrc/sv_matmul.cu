@@ -969,7 +969,10 @@ static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
     }
 }
 
-size_t matmul_workspace_size(int M, int N, int K) { return kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
+constexpr int kMmFew = 64;             // rows that matmul_few_kernel takes
+
+// (Which calls share tiles depends on the device's SMs: every call of more rows has room for parts.)
+size_t matmul_workspace_size(int M, int, int) { return M <= kMmFew ? kMmTicketAt : kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
 
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     DeviceInfo di;
@@ -978,7 +981,7 @@ cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     const int sms = di.sm_count;
     if (a.M <= 16) return launch_few_t<16>(a, sms, st);
     if (a.M <= 32) return launch_few_t<32>(a, sms, st);
-    if (a.M <= 64) return launch_few_t<64>(a, sms, st);
+    if (a.M <= kMmFew) return launch_few_t<64>(a, sms, st);
     return launch_many(a, sms, st);
 }
 

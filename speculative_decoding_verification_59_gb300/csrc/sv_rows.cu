@@ -17,19 +17,28 @@ __device__ __forceinline__ uint4 ld16(const char* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
-// Vector i of 8 elements at p: 16 bytes of bf16 or 32 of fp32.
-__device__ __forceinline__ void load8(const char* p, int64_t i, bool f32, float (&x)[8]) {
-    if (f32) {
-        const uint4 a = ld16(p + i * 32), b = ld16(p + i * 32 + 16);
+// A vector of 8 elements as it lies in memory, 16 bytes of bf16 or 32 of fp32: kept so until it is
+// used, it takes half the registers, and more loads are under way.
+template <bool F32>
+struct Raw8 {
+    uint4 w[F32 ? 2 : 1];
+    // vector i at p; zeros without `have`
+    __device__ __forceinline__ void load(const char* p, int64_t i, bool have) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] = __uint_as_float(u4_get(a, j));
-            x[4 + j] = __uint_as_float(u4_get(b, j));
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) {
+            w[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (have) w[k] = ld16(p + i * (F32 ? 32 : 16) + k * 16);
         }
-    } else {
-        unpack8(ld16(p + i * 16), x);
     }
-}
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        if constexpr (F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u4_get(w[j >> 2], j & 3));
+        } else {
+            unpack8(w[0], x);
+        }
+    }
+};
 __device__ __forceinline__ void store8(char* p, int64_t i, bool f32, const float (&x)[8]) {
     if (f32) {
         float4* q = reinterpret_cast<float4*>(p + i * 32);
@@ -51,53 +60,46 @@ __device__ __forceinline__ void store8_e4m3(char* p, int64_t i, float top, const
     *reinterpret_cast<uint2*>(p + i * 8) = make_uint2(pack_e4m3(x[0] * f, x[1] * f) | pack_e4m3(x[2] * f, x[3] * f) << 16,
                                                      pack_e4m3(x[4] * f, x[5] * f) | pack_e4m3(x[6] * f, x[7] * f) << 16);
 }
-// Vector v of row r to 8 bits; all 16 lanes of a block take part, those without a vector
-// (have false) with x all zero.
-__device__ __forceinline__ void put_e4m3(char* out, float* scale, int64_t scale_stride, int64_t r, int nv, int v, bool have, const float (&x)[8]) {
+// Vector i of an output to 8 bits; all 16 lanes of a block take part, those without a vector
+// (have false) with x all zero.  The block's largest magnitude.
+__device__ __forceinline__ float put_e4m3(char* out, int64_t i, bool have, const float (&x)[8]) {
     float m = top8(x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = fmaxf(m, kFp8AmaxFloor);
-    if (!have) return;
-    store8_e4m3(out, r * nv + v, m, x);
-    if ((v & 15) == 0) scale[(v >> 4) * scale_stride + r] = m / kFp8Max;
+    if (have) store8_e4m3(out, i, m, x);
+    return m;
 }
 
 // ---- residual and norm ---------------------------------------------------------------
 // A row is a group of TPR threads, VPT vectors each, held in registers between the
 // two uses.  MORE: longer rows, read once more for the second (from L2, mostly).
-struct RowFormat {
-    bool xf, sf;                       // x and the residual are fp32
-    int out;                           // spec_dtype_t
-};
-template <int VPT, bool MORE>
-__global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, const RowFormat f, int tpr) {
-    __shared__ float part[2][16];
+template <bool XF, bool SF, int VPT, bool MORE>
+__global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out, int tpr) {
+    __shared__ float part[16];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, in_row = threadIdx.x & (tpr - 1), nv = a.dim / 8;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     const bool live = row < a.rows;
-    const char* x = a.x + row * a.xs * (f.xf ? 4 : 2);
-    const char* res = a.res + row * a.rs * (f.sf ? 4 : 2);
-    char* sum = a.sum + row * a.ss * (f.sf ? 4 : 2);
+    const char* x = a.x + row * a.xs * (XF ? 4 : 2);
+    const char* res = a.res + row * a.rs * (SF ? 4 : 2);
+    char* sum = a.sum + row * a.ss * (SF ? 4 : 2);
     pdl_wait();
     float h[VPT][8];
     // VPT vectors from vector v0 on (those past the row zero), the residual added
     auto fetch = [&](int v0) {
+        Raw8<XF> p[VPT];
+        Raw8<SF> q[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) p[j].load(x, v0 + j * tpr, live && v0 + j * tpr < nv);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) q[j].load(res, v0 + j * tpr, a.res && live && v0 + j * tpr < nv);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = v0 + j * tpr;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[j][e] = 0.f;
-            if (live && v < nv) load8(x, v, f.xf, h[j]);
-        }
-        if (!a.res) return;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = v0 + j * tpr;
             float r[8];
-            if (live && v < nv) {
-                load8(res, v, f.sf, r);
+            p[j].get(h[j]);
+            q[j].get(r);
+            if (a.res) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[j][e] += r[e];
             }
@@ -113,11 +115,11 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, const R
     }
     ss = warp_sum(ss);
     if (tpr > 32) {
-        if ((threadIdx.x & 31) == 0) part[0][warp] = ss;
+        if ((threadIdx.x & 31) == 0) part[warp] = ss;
         __syncthreads();
         const int first = (threadIdx.x / tpr) * (tpr / 32);
         ss = 0.f;
-        for (int i = 0; i < tpr / 32; ++i) ss += part[0][first + i];
+        for (int i = 0; i < tpr / 32; ++i) ss += part[first + i];
     }
     const float inv = rsqrtf(ss / (float)a.dim + a.eps);
     // (all lanes stay: a block's 16 find its largest element together)
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, const R
         for (int j = 0; j < VPT; ++j) {
             const int v = v0 + j * tpr;
             const bool have = live && v < nv;
-            if (have && a.sum) store8(sum, v, f.sf, h[j]);
+            if (have && a.sum) store8(sum, v, SF, h[j]);
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = h[j][e] * inv;
@@ -137,24 +139,40 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, const R
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] *= w[e];
             }
-            if (f.out == SPEC_DTYPE_E4M3) put_e4m3(a.out, a.scale, a.scale_stride, row, nv, v, have, y);
-            else if (have) store8(a.out, row * nv + v, f.out == SPEC_DTYPE_F32, y);
+            if (out == SPEC_DTYPE_E4M3) {
+                const float m = put_e4m3(a.out, row * nv + v, have, y);
+                if (have && (v & 15) == 0) a.scale[(v >> 4) * a.scale_stride + row] = m / kFp8Max;
+            } else if (have) store8(a.out, row * nv + v, out == SPEC_DTYPE_F32, y);
         }
     }
 }
 
-cudaError_t launch_add_norm(const NormArgs& a, spec_dtype_t x, spec_dtype_t sum, spec_dtype_t out, cudaStream_t st) {
-    const RowFormat f{x == SPEC_DTYPE_F32, sum == SPEC_DTYPE_F32, (int)out};
+template <bool XF, bool SF>
+static cudaError_t launch_add_norm_t(const NormArgs& a, int out, int sms, cudaStream_t st) {
     const int nv = a.dim / 8;
-    const int vpt = nv <= 512 ? 1 : nv <= 1024 ? 2 : 4;
+    // Few rows: as many threads a row as it has vectors (the time is one row's).  More: two or four
+    // vectors a thread, so that an SM holds more rows' loads under way (rows of 4096, one / two / four
+    // a thread: 512 rows 5.9 / 4.5 / 5.5 us, 8192 of an fp32 residual 87 / 61.5 / 62, 8192 to e4m3
+    // 71.6 / 47.5 / 45.8).
+    int vpt = nv > 1024 ? 4 : a.rows <= 2 * sms ? (nv > 512 ? 2 : 1) : a.rows <= 32 * sms ? 2 : 4;
+    while (vpt > 1 && nv <= 32 * (vpt / 2)) vpt /= 2;
     int tpr = 32;
     while (tpr < 512 && tpr * vpt < nv) tpr *= 2;
     const int threads = tpr < 128 ? 128 : tpr;
     const dim3 grid((unsigned)(((long long)a.rows + threads / tpr - 1) / (threads / tpr)));
-    if (nv > 512 * 4) return launch_pdl(add_norm_kernel<4, true>, grid, threads, 0, st, a, f, tpr);
-    if (vpt == 1) return launch_pdl(add_norm_kernel<1, false>, grid, threads, 0, st, a, f, tpr);
-    if (vpt == 2) return launch_pdl(add_norm_kernel<2, false>, grid, threads, 0, st, a, f, tpr);
-    return launch_pdl(add_norm_kernel<4, false>, grid, threads, 0, st, a, f, tpr);
+    if (nv > 512 * 4) return launch_pdl(add_norm_kernel<XF, SF, 4, true>, grid, threads, 0, st, a, out, tpr);
+    if (vpt == 1) return launch_pdl(add_norm_kernel<XF, SF, 1, false>, grid, threads, 0, st, a, out, tpr);
+    if (vpt == 2) return launch_pdl(add_norm_kernel<XF, SF, 2, false>, grid, threads, 0, st, a, out, tpr);
+    return launch_pdl(add_norm_kernel<XF, SF, 4, false>, grid, threads, 0, st, a, out, tpr);
+}
+
+cudaError_t launch_add_norm(const NormArgs& a, spec_dtype_t x, spec_dtype_t sum, spec_dtype_t out, cudaStream_t st) {
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    const bool xf = x == SPEC_DTYPE_F32, sf = a.res && sum == SPEC_DTYPE_F32;
+    if (xf) return sf ? launch_add_norm_t<true, true>(a, (int)out, di.sm_count, st) : launch_add_norm_t<true, false>(a, (int)out, di.sm_count, st);
+    return sf ? launch_add_norm_t<false, true>(a, (int)out, di.sm_count, st) : launch_add_norm_t<false, false>(a, (int)out, di.sm_count, st);
 }
 
 // ---- gated activation, rounding of rows ----------------------------------------------
@@ -165,63 +183,103 @@ __device__ __forceinline__ float activate(float x, int act) {
     return __fdividef(x, 1.f + __expf(-t));
 }
 
-constexpr int kActThreads = 256, kActVectors = 2;
-// Vectors are counted with every row filled up to whole blocks, so that a block's 16 lanes
-// stand side by side.
-__global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, bool f32, int out, unsigned per_row, unsigned total) {
+// A CTA takes RT rows and, 16 lanes a block, 16 / RT blocks of them at a time, V times.  Many rows: 16
+// rows of one block, whose scales then leave together in one line (a scale of 4 bytes by itself
+// costs a sector: 39.4 us for 33 at 16384 rows of 4096).
+constexpr int kActThreads = 256;
+template <bool F32, bool GATED, int RT, int V>
+__global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int out, int chunks) {
+    constexpr int BT = 16 / RT;                           // blocks at a time
+    __shared__ float top[RT > 1 ? V : 1][16];
     pdl_trigger();
-    const int elt = f32 ? 4 : 2, nv = a.dim / 8;
-    float g[kActVectors][8], u[kActVectors][8];
-    unsigned row[kActVectors], v[kActVectors];
-    bool have[kActVectors];
+    const int nv = a.dim / 8, group = blockIdx.x / chunks, chunk = blockIdx.x - group * chunks;
+    const int slot = threadIdx.x >> 4;
+    const int64_t row0 = (int64_t)group * RT, row = row0 + slot / BT;
+    const int v0 = (chunk * BT * V + slot % BT) * 16 + (threadIdx.x & 15);
+    const bool live = row < a.rows;
+    Raw8<F32> g[V], u[V];
     pdl_wait();
 #pragma unroll
-    for (int k = 0; k < kActVectors; ++k) {
-        const unsigned i = (blockIdx.x * kActVectors + k) * kActThreads + threadIdx.x;
-        row[k] = i / per_row;
-        v[k] = i - row[k] * per_row;
-        have[k] = i < total && (int)v[k] < nv;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[k][e] = u[k][e] = 0.f;
-        if (!have[k]) continue;
-        load8(a.gate + (int64_t)row[k] * a.gs * elt, v[k], f32, g[k]);
-        if (a.up) load8(a.up + (int64_t)row[k] * a.us * elt, v[k], f32, u[k]);
+    for (int k = 0; k < V; ++k) {
+        const int v = v0 + k * BT * 16;
+        g[k].load(a.gate + row * a.gs * (F32 ? 4 : 2), v, live && v < nv);
+        if (GATED) u[k].load(a.up + row * a.us * (F32 ? 4 : 2), v, live && v < nv);
     }
 #pragma unroll
-    for (int k = 0; k < kActVectors; ++k) {
-        if (a.up) {
+    for (int k = 0; k < V; ++k) {
+        const int v = v0 + k * BT * 16;
+        const bool have = live && v < nv;
+        float x[8];
+        g[k].get(x);
+        if (GATED) {
+            float y[8];
+            u[k].get(y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[k][e] = activate(g[k][e], a.act) * u[k][e];
+            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], a.act) * y[e];
         }
-        if (out == SPEC_DTYPE_E4M3) put_e4m3(a.out, a.scale, a.scale_stride, row[k], nv, (int)v[k], have[k], g[k]);
-        else if (have[k]) store8(a.out, (int64_t)row[k] * nv + v[k], out == SPEC_DTYPE_F32, g[k]);
+        if (out == SPEC_DTYPE_E4M3) {
+            const float m = put_e4m3(a.out, row * nv + v, have, x);
+            if (RT > 1) {
+                if ((threadIdx.x & 15) == 0) top[RT > 1 ? k : 0][slot] = m;
+            } else if ((threadIdx.x & 15) == 0 && have) {
+                a.scale[(v >> 4) * a.scale_stride + row] = m / kFp8Max;
+            }
+        } else if (have) {
+            store8(a.out, row * nv + v, out == SPEC_DTYPE_F32, x);
+        }
     }
+    if (RT > 1 && out == SPEC_DTYPE_E4M3) {
+        __syncthreads();
+        if (threadIdx.x < 16 * V) {
+            const int k = threadIdx.x >> 4, r = threadIdx.x & 15, b = chunk * V + k;
+            if (row0 + r < a.rows && b * 16 < nv) a.scale[b * a.scale_stride + row0 + r] = top[RT > 1 ? k : 0][r] / kFp8Max;
+        }
+    }
+}
+
+template <bool F32, bool GATED>
+static cudaError_t launch_act_t(const ActArgs& a, int out, int sms, cudaStream_t st) {
+    // 16 rows and four blocks of them a CTA where that gives every SM one, else a row's blocks side by side
+    const long long blocks = scale_blocks(a.dim), groups = ((long long)a.rows + 15) / 16;
+    if ((blocks + 3) / 4 * groups >= sms) {
+        const long long chunks = (blocks + 3) / 4;
+        return launch_pdl(act_kernel<F32, GATED, 16, 4>, dim3((unsigned)(chunks * groups)), kActThreads, 0, st, a, out, (int)chunks);
+    }
+    const long long chunks = (blocks + 15) / 16;
+    return launch_pdl(act_kernel<F32, GATED, 1, 1>, dim3((unsigned)(chunks * a.rows)), kActThreads, 0, st, a, out, (int)chunks);
 }
 
 cudaError_t launch_act(const ActArgs& a, spec_dtype_t in, spec_dtype_t out, cudaStream_t st) {
-    const unsigned per_row = (unsigned)(a.dim / 8 + 15) / 16 * 16;
-    const unsigned total = per_row * (unsigned)a.rows;         // (checked below 2^31)
-    const unsigned per = kActThreads * kActVectors;
-    return launch_pdl(act_kernel, dim3((total + per - 1) / per), kActThreads, 0, st, a, in == SPEC_DTYPE_F32, (int)out, per_row, total);
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return e;
+    const int sms = di.sm_count;
+    if (in == SPEC_DTYPE_F32) return a.up ? launch_act_t<true, true>(a, (int)out, sms, st) : launch_act_t<true, false>(a, (int)out, sms, st);
+    return a.up ? launch_act_t<false, true>(a, (int)out, sms, st) : launch_act_t<false, false>(a, (int)out, sms, st);
 }
 
 // ---- rounding of weights -------------------------------------------------------------
-// A CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const TileQuantArgs a, bool f32, int tiles_n) {
+// A CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.  (Two blocks side by side, so that rows
+// are read 512 bytes at a time: 64.3 us for 55.7 at 24576 x 4096; 512 threads a block: 57.9.)
+template <bool F32>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const TileQuantArgs a, int tiles_n) {
+    constexpr int VECTORS = 8, STEP = 16;
     __shared__ float part[8];
     pdl_trigger();
     const int ti = blockIdx.x / tiles_n, tb = blockIdx.x - ti * tiles_n, nv = a.dim / 8;
     const int v = tb * 16 + (threadIdx.x & 15), r0 = ti * kScaleBlock + (threadIdx.x >> 4);
-    float x[8][8], m = 0.f;
+    Raw8<F32> x[VECTORS];
+    float m = 0.f;
     pdl_wait();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < VECTORS; ++k)
+        x[k].load(a.x + (int64_t)(r0 + STEP * k) * a.xs * (F32 ? 4 : 2), v, v < nv && r0 + STEP * k < a.rows);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-        if (v < nv && r0 + 16 * k < a.rows) load8(a.x + (int64_t)(r0 + 16 * k) * a.xs * (f32 ? 4 : 2), v, f32, x[k]);
+    for (int k = 0; k < VECTORS; ++k) {
+        float y[8];
+        x[k].get(y);
+        m = fmaxf(m, top8(y));
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, top8(x[k]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -230,8 +288,11 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const TileQuantArgs
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (v < nv && r0 + 16 * k < a.rows) store8_e4m3(a.out, (int64_t)(r0 + 16 * k) * nv + v, m, x[k]);
+    for (int k = 0; k < VECTORS; ++k) {
+        float y[8];
+        x[k].get(y);
+        if (v < nv && r0 + STEP * k < a.rows) store8_e4m3(a.out, (int64_t)(r0 + STEP * k) * nv + v, m, y);
+    }
     if (threadIdx.x == 0) a.scale[(int64_t)ti * a.scale_stride + tb] = m / kFp8Max;
 }
 
@@ -239,7 +300,8 @@ cudaError_t launch_quantize_tiles(const TileQuantArgs& a, spec_dtype_t in, cudaS
     const int tiles_n = scale_blocks(a.dim);
     const long long tiles = (long long)scale_blocks(a.rows) * tiles_n;
     if (tiles >= (1LL << 31)) return cudaErrorInvalidValue;
-    return launch_pdl(quantize_tiles_kernel, dim3((unsigned)tiles), 256, 0, st, a, in == SPEC_DTYPE_F32, tiles_n);
+    return in == SPEC_DTYPE_F32 ? launch_pdl(quantize_tiles_kernel<true>, dim3((unsigned)tiles), 256, 0, st, a, tiles_n)
+                                : launch_pdl(quantize_tiles_kernel<false>, dim3((unsigned)tiles), 256, 0, st, a, tiles_n);
 }
 
 }  // namespace sv
