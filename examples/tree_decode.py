@@ -13,9 +13,17 @@ Every step runs the calls of this library in the order a serving loop would:
   token_logprobs       what the emitted tokens had as probability, the distribution's entropy and
                        its K best tokens, which are the branches when the position is drafted from
 
-The projections are plain matrix products; nothing is read back to the host between steps.
+The projections are plain matrix products, or, with the weights held in 8 bits, calls of this library
+too:
 
-  python examples/tree_decode.py [--batch 4] [--steps 24] [--fp8]
+  add_norm             the residual's addition, its norm, rows rounded to 8 bits
+  matmul_e4m3          the projections, and the logits
+  quantize_e4m3        the attention's output to 8 bits (and, once, the weights)
+  gated_act            the activation between the feed-forward products, to 8 bits
+
+Nothing is read back to the host between steps.
+
+  python examples/tree_decode.py [--batch 4] [--steps 24] [--fp8] [--fp8-weights]
 """
 from __future__ import annotations
 
@@ -33,7 +41,7 @@ class Decoder:
     """Layers of attention and a gated product, with root-mean-square norms."""
     vocab, dim, heads, kv_heads, head_dim, layers, rows = 512, 256, 8, 2, 64, 2, 4096
 
-    def __init__(self, seed: int = 0):
+    def __init__(self, seed: int = 0, fp8_weights: bool = False):
         g = torch.Generator().manual_seed(seed)
 
         def w(*shape):
@@ -47,6 +55,13 @@ class Decoder:
         self.down = [w(self.dim, 2 * self.dim) for _ in range(self.layers)]
         self.head = w(self.vocab, self.dim) * 2
         self.q_weight = [torch.ones(D, dtype=torch.bfloat16, device="cuda") for _ in range(self.layers)]
+        self.fp8_weights = fp8_weights
+        if fp8_weights:
+            def quantized(w):
+                return sv.quantize_e4m3(w, block_rows=128)
+            self.qkv8, self.proj8, self.up8, self.down8 = (
+                [quantized(w) for w in ws] for ws in (self.qkv, self.proj, self.up, self.down))
+            self.head8 = quantized(self.head)
         angle = torch.arange(self.rows)[:, None] * 10000.0 ** (-torch.arange(D // 2) / (D // 2))
         self.rope = torch.cat([angle.cos(), angle.sin()], 1).float().cuda()
 
@@ -65,6 +80,8 @@ class Decoder:
 
     def __call__(self, tokens, cache, ctx, parents=None, positions=None):
         """Logits [B, N, vocab] after each of tokens [B, N], which stand at ctx [B] on."""
+        if self.fp8_weights:
+            return self.forward8(tokens, cache, ctx, parents, positions)
         H, G, D = self.heads, self.kv_heads, self.head_dim
         B, N = tokens.shape
         x = self.embed[tokens.long()]
@@ -78,6 +95,24 @@ class Decoder:
             a, b = (self.norm(x) @ self.up[i].T).chunk(2, -1)
             x = x + (torch.nn.functional.silu(a) * b) @ self.down[i].T
         return (self.norm(x) @ self.head.T).float()
+
+    def forward8(self, tokens, cache, ctx, parents, positions):
+        """The same with 8-bit weights: a part's output is added to x by the next norm."""
+        H, G, D = self.heads, self.kv_heads, self.head_dim
+        B, N = tokens.shape
+        x = self.embed[tokens.long()]
+        h = sv.add_norm(x, e4m3=True)
+        for i in range(self.layers):
+            part = cache.layer(i)
+            q, k, v = sv.matmul_e4m3(*h, *self.qkv8[i]).view(B, N, H + 2 * G, D).split((H, G, G), 2)
+            q = sv.kv_append(part, q, k, v, ctx, self.rope, q_weight=self.q_weight[i],
+                             k_weight=self.q_weight[i], positions=positions)
+            y = sv.paged_attention(q, part, ctx, parents=parents)
+            y = sv.matmul_e4m3(*sv.quantize_e4m3(y.view(B, N, H * D)), *self.proj8[i])
+            *h, x = sv.add_norm(y, None, x, e4m3=True)
+            y = sv.matmul_e4m3(*sv.gated_act(sv.matmul_e4m3(*h, *self.up8[i]), e4m3=True), *self.down8[i])
+            *h, x = sv.add_norm(y, None, x, e4m3=True)
+        return sv.matmul_e4m3(*h, *self.head8, dtype=torch.float32)
 
 
 def generate(model: Decoder, prompt, steps: int, *, chain: int = 6, branches: int = 3, w: int = 2,
@@ -143,9 +178,10 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--steps", type=int, default=24)
-    ap.add_argument("--fp8", action="store_true")
+    ap.add_argument("--fp8", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--fp8-weights", action="store_true", help="8-bit weights")
     args = ap.parse_args()
-    model = Decoder()
+    model = Decoder(fp8_weights=args.fp8_weights)
     tokens, lengths, logprobs, accepted = generate(
         model, make_prompt(args.batch, 97, model.vocab), args.steps, fp8=args.fp8)
     for b in range(args.batch):
