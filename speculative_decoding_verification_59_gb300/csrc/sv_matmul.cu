@@ -147,46 +147,48 @@ __device__ __forceinline__ void tc_ld32_done(float* v) {
 // ---- few rows ----------------------------------------------------------------------
 // Up to 64 rows of x: the product is taken transposed, so that 128 weight rows are the
 // rows that the instruction wants and the few rows of x its free dimension T.  The weights are
-// read once, which bounds these calls.  A tile of 128 weight rows is shared by a cluster of S
-// CTAs, each with its part of the contraction; they add their sums over distributed shared
-// memory, in the order of their ranks, each a part of the columns.
-//   warp 0     loads: both operands and the rows' scales of a step into a ring, by TMA
+// read once, which bounds these calls.  A tile of 128 weight rows is shared by a cluster of S CTAs, each
+// with its part of the contraction; they add their sums over distributed shared memory, in the order of
+// their ranks, each a part of the columns.
+//   warp 0     loads: both operands and the rows' scales of BP blocks into a ring, by TMA
 //   warp 1     issues the products
 //   warps 2-5  running sums: a thread owns a weight row, the rows' scales are read from shared
 //              memory, the weights' scale is the tile's
+// Handing on a block takes a CTA's warps some 400 cycles of waits and arrivals, 16 KB in 0.2 us.  So two
+// CTAs an SM, 100 KB under way each, and for up to 16 rows two blocks at a time (one row, N = 6144 /
+// 8192, K = 4096: 6.26 / 7.23 us for 6.48 / 7.63; 64 rows, N = 24576: 24.8 for 23.2).  One CTA an SM
+// with all the ring: 7.0 / 8.1 and 27.5.  Equal shares of all tiles' blocks, their parts joined
+// through memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N =
+// 151936.
 template <int T>
 struct FewCfg {
-    static constexpr int SCALE = T * 4 < 128 ? 128 : T * 4;
-    static constexpr int STAGES = T <= 16 ? 6 : T <= 32 ? 5 : 4;         // and accumulators: one a stage
-    static constexpr int CTAS = 2;                        // on an SM
-    static constexpr int TMEM = T * STAGES <= 128 ? 128 : 256;
-    static constexpr int X_AT = kMmBytes, STAGE = kMmBytes + T * kMmTile;
+    static constexpr int BP = T <= 16 ? 2 : 1;            // blocks at a time
+    static constexpr int SCALE = BP * T * 4;
+    static constexpr int STAGES = T <= 16 ? 3 : T <= 32 ? 5 : 4;
+    static constexpr int COLS = BP * T, TMEM = COLS * STAGES <= 128 ? 128 : 256;   // accumulators: a stage's
+    static constexpr int X_AT = BP * kMmBytes, X_BYTES = T * kMmTile, BYTES = kMmBytes + X_BYTES, STAGE = BP * BYTES;
     static constexpr int SCALE_AT = STAGES * STAGE;
     static constexpr int SMEM = SCALE_AT + STAGES * SCALE + 1024;        // and room to align
-    static constexpr int THREADS = 192;
-    static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && CTAS * TMEM <= 512, "what an SM has");
+    static constexpr int THREADS = 192, CTAS = 2;
+    static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && CTAS * TMEM <= 512 && COLS * STAGES <= TMEM, "what an SM has");
     static_assert(3 * (SMEM + 1024) > 228 * 1024, "no more CTAs than tensor memory has room for");
-    static_assert(T * 512 <= SCALE_AT, "the sums of a CTA fit the ring");
+    static_assert(SCALE % 128 == 0 && T * kMmTile * 4 <= SCALE_AT, "alignment; the sums of a CTA fit the ring");
 };
 
 template <int T>
-__global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit,
+__global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit, int blocks, int S,
                                                                           const __grid_constant__ CUtensorMap xmap,
                                                                           const __grid_constant__ CUtensorMap wmap,
-                                                                          const __grid_constant__ CUtensorMap smap, int S) {
+                                                                          const __grid_constant__ CUtensorMap smap) {
     using C = FewCfg<T>;
     extern __shared__ unsigned char smem_raw[];
     // done: a step's products are complete; empty: its sums are taken, its stage and accumulator free
     __shared__ __align__(8) uint64_t full[C::STAGES], done[C::STAGES], empty[C::STAGES], drained;
     __shared__ uint32_t tmem_at;
-    __shared__ int failed;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int tile = blockIdx.x / S, rank = blockIdx.x - tile * S;     // (a cluster: S consecutive CTAs)
-    const int blocks = (a.K + kMmTile - 1) / kMmTile;
-    const int b0 = (int)((long long)blocks * rank / S), n = (int)((long long)blocks * (rank + 1) / S) - b0;
-    const int n0 = tile * kMmTile;
-
+    const int b0 = (int)((long long)blocks * rank / S), b1 = (int)((long long)blocks * (rank + 1) / S);
     if (warp == 0) {
         if (elect_one()) {
             for (int i = 0; i < C::STAGES; ++i) {
@@ -196,7 +198,6 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
             }
             mbar_init(&drained, 1);
             mbar_init_fence();
-            failed = 0;
             map_prefetch(&wmap);
             map_prefetch(&xmap);
             map_prefetch(&smap);
@@ -210,19 +211,27 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
     tc_after();
     const uint32_t tmem = tmem_at;
     pdl_wait();
+    int32_t* error = reinterpret_cast<int32_t*>(a.ws);
 
-    f32x2 acc[T / 2];
     if (warp == 0) {
-        int i = 0, s = 0, phase = 0;                       // step, its stage, how often the ring has come round (mod 2)
+        bool ok = true;
+        unsigned it = 0, s = 0, phase = 0;                 // step, its stage, how often the ring has come round (mod 2)
         const uint32_t base = smem_addr(smem);
-        for (; i < n; ++i) {
-            if (i >= C::STAGES && !wait_warp(&empty[s], phase ^ 1, limit)) break;
+        const bool lead = elect_one();
+        for (int b = b0; b < b1; b += C::BP, ++it) {
+            if (it >= C::STAGES) {
+                ok = wait_warp(&empty[s], phase ^ 1, limit);
+                if (!ok) break;
+            }
             const uint32_t at = base + s * C::STAGE;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&full[s], C::STAGE + T * 4);
-                tma_2d(at, &wmap, (b0 + i) * kMmTile, n0, &full[s]);
-                tma_2d(at + C::X_AT, &xmap, (b0 + i) * kMmTile, 0, &full[s]);
-                tma_2d(base + C::SCALE_AT + s * C::SCALE, &smap, 0, b0 + i, &full[s]);
+            const bool two = C::BP == 2 && b + 1 < b1;
+            if (lead) {
+                mbar_arrive_expect_tx(&full[s], (two ? 2 : 1) * C::BYTES + C::SCALE);
+                tma_2d(at, &wmap, b * kMmTile, tile * kMmTile, &full[s]);
+                if (two) tma_2d(at + kMmBytes, &wmap, (b + 1) * kMmTile, tile * kMmTile, &full[s]);
+                tma_2d(at + C::X_AT, &xmap, b * kMmTile, 0, &full[s]);
+                if (two) tma_2d(at + C::X_AT + C::X_BYTES, &xmap, (b + 1) * kMmTile, 0, &full[s]);
+                tma_2d(base + C::SCALE_AT + s * C::SCALE, &smap, 0, b, &full[s]);
             }
             __syncwarp();
             if (++s == C::STAGES) {
@@ -230,25 +239,31 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
                 phase ^= 1;
             }
         }
-        bool ok = i == n;
         // every copy has landed and every commit has arrived before the CTA ends
-        for (int j = max(0, i - C::STAGES); j < i; ++j) {
-            const int k = j % C::STAGES;
-            const uint32_t parity = (j / C::STAGES) & 1;
+        for (unsigned j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j) {
+            const unsigned k = j % C::STAGES, parity = (j / C::STAGES) & 1;
             if (!wait_warp(&full[k], parity, kTcWaitLimit) || !wait_warp(&done[k], parity, limit)) ok = false;
         }
-        if (!ok) failed = 1;
+        if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
     } else if (warp == 1) {
         const uint32_t id = tc_idesc(true, false, false, T);
         const uint64_t base = tc_desc(smem_addr(smem), 16, 1024);
-        int i = 0, s = 0, phase = 0;
-        for (; i < n; ++i) {
-            if (!wait_warp(&full[s], phase, limit)) break;
+        const bool lead = elect_one();
+        bool ok = true;
+        unsigned it = 0, s = 0, phase = 0;
+        for (int b = b0; b < b1; b += C::BP, ++it) {
+            ok = wait_warp(&full[s], phase, limit);
+            if (!ok) break;
             tc_after();
             const uint64_t wd = base + s * (C::STAGE >> 4), xd = wd + (C::X_AT >> 4);
-            if (elect_one()) {
+            const uint32_t to = tmem + s * C::COLS;
+            if (lead) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma<true>(tmem + s * T, wd + 2 * k, xd + 2 * k, id, k > 0);
+                for (int k = 0; k < 4; ++k) tc_mma<true>(to, wd + 2 * k, xd + 2 * k, id, k > 0);
+                if (C::BP == 2 && b + 1 < b1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma<true>(to + T, wd + (kMmBytes >> 4) + 2 * k, xd + (C::X_BYTES >> 4) + 2 * k, id, k > 0);
+                }
                 tc_commit(&done[s]);
             }
             __syncwarp();
@@ -257,48 +272,58 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
                 phase ^= 1;
             }
         }
-        if (i < n) {
-            failed = 1;
-            if (i > 0) {
-                if (elect_one()) tc_commit(&drained);
+        if (!ok) {
+            if (lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+            if (it > 0) {
+                if (lead) tc_commit(&drained);
                 __syncwarp();
                 wait_warp(&drained, 0, kTcWaitLimit);
             }
         }
-    } else {
-        const int quad = warp & 3;
+    }
+    const int quad = warp & 3, row = quad * 32 + lane;     // of a tile's weight rows (warps 2 to 5)
+    float acc[T];
+    // a row of x takes 32 neighbouring weight rows' results from a warp
+    auto put = [&](int m, float v) {
+        const int64_t at = (int64_t)m * a.old + (int64_t)tile * kMmTile + row;
+        if (a.f32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<unsigned short*>(a.out)[at] = (unsigned short)(pack_bf16(v, 0.f) & 0xffffu);
+    };
+    if (warp >= 2) {
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-        for (int c = 0; c < T / 2; ++c) acc[c] = 0;
-        // the tile's scales, 32 steps at a time, a lane each (one ahead of its use, a load a step
-        // held every step up for the memory's answer)
-        const float* wsc = a.wscale + (int64_t)tile * a.ws_stride + b0;
+        for (int c = 0; c < T; ++c) acc[c] = 0.f;
+        // the tile's scales, 32 blocks at a time, a lane each (one ahead of its use, a load a block
+        // held every block up for the memory's answer)
+        const float* wsc = a.wscale + (int64_t)tile * a.ws_stride;
         float wl = 0.f;
         bool ok = true;
-        int s = 0, phase = 0;
-        for (int i = 0; i < n; ++i) {
-            if ((i & 31) == 0 && i + lane < n) wl = ld_scale(wsc + i + lane);
-            const float wf = __shfl_sync(0xffffffffu, wl, i & 31);
-            const f32x2 w2 = f2_pack(wf, wf);
+        unsigned s = 0, phase = 0;
+        for (int b = b0; b < b1; b += C::BP) {
+            if (((b - b0) & 31) == 0 && b + lane < b1) wl = ld_scale(wsc + b + lane);
+            const bool two = C::BP == 2 && b + 1 < b1;
+            const float wf[2] = {__shfl_sync(0xffffffffu, wl, (b - b0) & 31), __shfl_sync(0xffffffffu, wl, (b - b0 + 1) & 31)};
             ok = wait_warp(&done[s], phase, limit);
             if (!ok) break;
             tc_after();
             const float4* xs = reinterpret_cast<const float4*>(smem + C::SCALE_AT + s * C::SCALE);
+            const uint32_t at = from + s * C::COLS;
             float v[2][16];
-            tc_ld16_start(from + s * T, v[0]);
+            tc_ld16_start(at, v[0]);
 #pragma unroll
-            for (int c = 0; c < T; c += 16) {
+            for (int c = 0; c < C::COLS; c += 16) {
+                if (c == T && !two) break;
                 float* now = v[(c >> 4) & 1];
                 tc_wait_ld();
                 tc_ld16_done(now);
-                if (c + 16 < T) tc_ld16_start(from + s * T + c + 16, v[((c >> 4) + 1) & 1]);
+                if (c + 16 < C::COLS && (c + 16 != T || two)) tc_ld16_start(at + c + 16, v[((c >> 4) + 1) & 1]);
+                const f32x2 w2 = f2_pack(wf[c >= T], wf[c >= T]);
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 f = xs[(c + e) >> 2];
-                    f32x2& p = acc[(c + e) >> 1];
-                    f32x2& q = acc[((c + e) >> 1) + 1];
-                    p = f2_fma(f2_pack(now[e], now[e + 1]), f2_mul(f2_pack(f.x, f.y), w2), p);
-                    q = f2_fma(f2_pack(now[e + 2], now[e + 3]), f2_mul(f2_pack(f.z, f.w), w2), q);
+                    float* to = acc + (c + e) % T;
+                    f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_mul(f2_pack(f.x, f.y), w2), f2_pack(to[0], to[1])), to[0], to[1]);
+                    f2_unpack(f2_fma(f2_pack(now[e + 2], now[e + 3]), f2_mul(f2_pack(f.z, f.w), w2), f2_pack(to[2], to[3])), to[2], to[3]);
                 }
             }
             tc_before();
@@ -309,46 +334,38 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
                 phase ^= 1;
             }
         }
-        if (!ok && lane == 0) failed = 1;
+        if (!ok) {                                         // a result that is not valid shows
+#pragma unroll
+            for (int c = 0; c < T; ++c) acc[c] = CUDART_NAN_F;
+            if (lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+        }
     }
     tc_before();
     __syncthreads();                                       // every product is done, the ring is free
     tc_after();
-    const int row = (warp & 3) * 32 + lane;                // of the tile (warps 2 to 5)
-    const float bad = failed ? CUDART_NAN_F : 0.f;         // a result that is not valid shows
-    if (failed && tid == 0) raise_error(reinterpret_cast<int32_t*>(a.ws), SPEC_DEVERR_TIMEOUT);
-    auto put = [&](int m, float v) {
-        const int64_t at = (int64_t)m * a.old + n0 + row;
-        if (a.f32) reinterpret_cast<float*>(a.out)[at] = v;
-        else reinterpret_cast<unsigned short*>(a.out)[at] = (unsigned short)(pack_bf16(v, 0.f) & 0xffffu);
-    };
+    const bool mine = warp >= 2 && tile * (long long)kMmTile + row < a.N;
     if (S == 1) {
-        if (warp >= 2 && n0 + row < a.N) {
+        if (mine) {
 #pragma unroll
-            for (int c = 0; c < T; c += 2) {
-                float lo, hi;
-                f2_unpack(acc[c >> 1], lo, hi);
-                if (c < a.M) put(c, lo + bad);
-                if (c + 1 < a.M) put(c + 1, hi + bad);
-            }
+            for (int c = 0; c < T; ++c)
+                if (c < a.M) put(c, acc[c]);
         }
     } else {
-        float* sums = reinterpret_cast<float*>(smem);      // [column][weight row]
+        float* sums = reinterpret_cast<float*>(smem) + row;            // [column][weight row]
         if (warp >= 2) {
 #pragma unroll
-            for (int c = 0; c < T; c += 2) {
-                float lo, hi;
-                f2_unpack(acc[c >> 1], lo, hi);
-                if (c < a.M) sums[c * kMmTile + row] = lo + bad;
-                if (c + 1 < a.M) sums[(c + 1) * kMmTile + row] = hi + bad;
-            }
+            for (int c = 0; c < T; ++c)
+                if (c < a.M) sums[c * kMmTile] = acc[c];
         }
         cluster_sync();
-        if (warp >= 2 && n0 + row < a.N) {
-            const uint32_t mine = smem_addr(sums) + row * 4;
+        if (mine) {
+            const uint32_t from = smem_addr(sums);
             for (int c = rank; c < a.M; c += S) {
-                float v = 0.f;
-                for (int r = 0; r < S; ++r) v += ld_cluster(cluster_addr(mine + c * kMmTile * 4, r));
+                float x[8], v = 0.f;                       // all under way at once
+#pragma unroll
+                for (int r = 0; r < 8; ++r) x[r] = r < S ? ld_cluster(cluster_addr(from + c * kMmTile * 4, r)) : 0.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v += x[r];
                 put(c, v);
             }
         }
@@ -696,7 +713,9 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                         }
                         const float fg = c < split ? f[j] : g[j];
 #pragma unroll
-                        for (int e = 0; e < L; ++e) acc[c + e] = fmaf(now[e], fg, acc[c + e]);
+                        for (int e = 0; e < L; e += 2)
+                            f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(acc[c + e], acc[c + e + 1])),
+                                      acc[c + e], acc[c + e + 1]);
                     }
                     if (++s == stages) {
                         s = 0;
@@ -865,28 +884,55 @@ static cudaError_t launch_clusters(void (*kfn)(KArgs...), int grid, int cluster,
 
 static uint32_t wait_limit() { return ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit; }
 
+// How many clusters of S = 1 to 8 CTAs run at once (they stay within groups of SMs).  The occupancy
+// query takes a kernel that allocates tensor memory for one that wants an SM to itself: it is
+// two, as shared memory and tensor memory are divided here.
 template <int T>
-static cudaError_t launch_few_t(const MatmulArgs& a, int sms, cudaStream_t st) {
+static cudaError_t few_clusters(int (&most)[9]) {
     using C = FewCfg<T>;
-    auto kfn = matmul_few_kernel<T>;
-    static DeviceSlots slots = {};
-    int unused = 0;
-    cudaError_t e = device_once(slots, &unused, [&](int, int* o) {
-        *o = 1;
-        return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    });
+    static DeviceSlots slots[9] = {};
+    for (int S = 1; S <= 8; ++S) {
+        const cudaError_t e = device_once(slots[S], &most[S], [&](int, int* o) {
+            cudaError_t x = cudaFuncSetAttribute(matmul_few_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (x != cudaSuccess) return x;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(8 * S));
+            cfg.blockDim = dim3(C::THREADS);
+            cfg.dynamicSmemBytes = C::SMEM;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)S;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            x = cudaOccupancyMaxActiveClusters(o, matmul_few_kernel<T>, &cfg);
+            *o *= C::CTAS;
+            return x;
+        });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int T>
+static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
+    using C = FewCfg<T>;
+    int most[9];
+    const cudaError_t e = few_clusters<T>(most);
     if (e != cudaSuccess) return e;
     const int tiles = (a.N - 1) / kMmTile + 1, blocks = scale_blocks(a.K);
-    // Clusters of a power of two: of six, which would use more of the SMs for 48 tiles, fewer fit at once
-    // (they stay within groups of SMs): 10.1 us for 7.5 at one row, N = 6144, K = 4096.
+    // The largest clusters of which all run at once, but that leave a CTA its two blocks.  (One row, N = 6144,
+    // K = 4096, 48 tiles: 6.3 us in clusters of five, of which 56 fit; 7.5 in four, 9.6 in six, of which 46
+    // do.)
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= C::CTAS * sms && S * 2 <= blocks) S *= 2;
+    for (int i = 2; i <= 8; ++i)
+        if (tiles <= most[i] && i * C::BP <= blocks) S = i;
     CUtensorMap xm, wm, sm;
     if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, T, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+        !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, C::BP, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    return launch_clusters(kfn, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), xm, wm, sm, S);
+    return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, xm, wm, sm);
 }
 
 // What a step of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows and
@@ -971,18 +1017,15 @@ static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
 
 constexpr int kMmFew = 64;             // rows that matmul_few_kernel takes
 
-// (Which calls share tiles depends on the device's SMs: every call of more rows has room for parts.)
+// (Which calls of more rows share tiles depends on the device's SMs: all have room for parts.)
 size_t matmul_workspace_size(int M, int, int) { return M <= kMmFew ? kMmTicketAt : kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
 
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    const int sms = di.sm_count;
-    if (a.M <= 16) return launch_few_t<16>(a, sms, st);
-    if (a.M <= 32) return launch_few_t<32>(a, sms, st);
-    if (a.M <= kMmFew) return launch_few_t<64>(a, sms, st);
-    return launch_many(a, sms, st);
+    if (a.M > kMmFew) return launch_many(a, di.sm_count, st);
+    return a.M <= 16 ? launch_few_t<16>(a, st) : a.M <= 32 ? launch_few_t<32>(a, st) : launch_few_t<64>(a, st);
 }
 
 }  // namespace sv
