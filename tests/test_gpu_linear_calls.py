@@ -201,3 +201,25 @@ def test_refusals(sv):
         with pytest.raises(error):
             call()
     assert sv.matmul_e4m3(q, s, w, ws).shape == (4, 4)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_captured_products(sv, M, N, K):
+    """A captured product replayed on contents that change: shared tiles' tickets are counted anew in every
+    replay."""
+    sets = [R.problem(M + 7 * i, M, N, K) for i in range(2)]
+    want = [sv.matmul_e4m3(*p, dtype=torch.float32) for p in sets]
+    x, xs, w, ws = R.problem(M, M, N, K)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        held = sv.matmul_e4m3(x, xs, w, ws, dtype=torch.float32)
+    for turn in range(4):
+        y, ys, v, vs = sets[turn % 2]
+        x.view(torch.uint8).copy_(y.view(torch.uint8))
+        w.view(torch.uint8).copy_(v.view(torch.uint8))
+        xs.copy_(ys)
+        ws.copy_(vs)
+        held.fill_(-1)
+        graph.replay()
+        assert torch.equal(held, want[turn % 2]), turn
