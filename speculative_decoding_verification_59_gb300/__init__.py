@@ -709,11 +709,12 @@ _ACTS = {"silu": SPEC_ACT_SILU, "gelu": SPEC_ACT_GELU_TANH}
 
 
 def _f32(dtype) -> bool:
-    if dtype is None:
-        return False
-    if dtype not in _logits_dtypes():
+    torch = _torch()
+    if dtype is torch.float32:
+        return True
+    if dtype is not torch.bfloat16:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    return dtype == _torch().float32
+    return False
 
 
 def add_norm(x, weight=None, residual=None, *, eps: float = 1e-6, e4m3: bool = False, dtype=None,

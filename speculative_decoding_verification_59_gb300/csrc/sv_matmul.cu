@@ -61,6 +61,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 // A scale.  (Not a read-only load, which could move ahead of the wait for the kernel before.)
 __device__ __forceinline__ float ld_scale(const float* p) {
     float v;
@@ -94,7 +99,7 @@ __device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 // A box from shared memory (written through proxy_fence before), as a group of its own; the wait until
-// all but N of the thread's groups have been read, and until all are written.
+// all but N of the thread's groups have been read.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -103,7 +108,6 @@ template <int N>
 __device__ __forceinline__ void tma_store_wait() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void map_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -122,10 +126,10 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 // Arrives on the barrier at this place in both CTAs when the products issued so far have completed.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+__device__ __forceinline__ void pair_commit(uint64_t* bar, unsigned short both) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                      smem_addr(bar)),
-                 "h"((unsigned short)3)
+                 "h"(both)
                  : "memory");
 }
 // 32 columns of the warp's 32 lanes; nothing may use v before tc_wait_ld and ld32_done.
@@ -167,16 +171,43 @@ struct FewCfg {
     static constexpr int STAGES = T <= 16 ? 3 : T <= 32 ? 5 : 4;
     static constexpr int COLS = BP * T, TMEM = COLS * STAGES <= 128 ? 128 : 256;   // accumulators: a stage's
     static constexpr int X_AT = BP * kMmBytes, X_BYTES = T * kMmTile, BYTES = kMmBytes + X_BYTES, STAGE = BP * BYTES;
-    static constexpr int SCALE_AT = STAGES * STAGE;
-    static constexpr int SMEM = SCALE_AT + STAGES * SCALE + 1024;        // and room to align
+    // Scales have a place more than the operands: an arrival does not wait for what the warp is still
+    // reading from shared memory, so a place is written again only when the warps have taken the step
+    // after (with as many places as stages, one row's scales in 10^5 came from the next round).
+    static constexpr int SCALE_AT = STAGES * STAGE, PLACES = STAGES + 1;
+    static constexpr int SMEM = SCALE_AT + PLACES * SCALE + 1024;        // and room to align
     static constexpr int THREADS = 192, CTAS = 2;
     static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && CTAS * TMEM <= 512 && COLS * STAGES <= TMEM, "what an SM has");
     static_assert(3 * (SMEM + 1024) > 228 * 1024, "no more CTAs than tensor memory has room for");
     static_assert(SCALE % 128 == 0 && T * kMmTile * 4 <= SCALE_AT, "alignment; the sums of a CTA fit the ring");
 };
 
+// n (up to 4) neighbouring results from element `at` of out on; wide: rows begin at 16 bytes.
+__device__ __forceinline__ void put4(const MatmulArgs& a, int64_t at, int n, bool wide, const float (&v)[4]) {
+    if (a.f32) {
+        float* to = reinterpret_cast<float*>(a.out) + at;
+        if (wide && n == 4) {
+            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) to[e] = v[e];
+        }
+    } else {
+        unsigned short* to = reinterpret_cast<unsigned short*>(a.out) + at;
+        const uint2 w = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        if (wide && n == 4) {
+            *reinterpret_cast<uint2*>(to) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) to[e] = (unsigned short)((e < 2 ? w.x : w.y) >> 16 * (e & 1));
+        }
+    }
+}
+
 template <int T>
-__global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit, int blocks, int S,
+__global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit, int blocks, int S, bool wide,
                                                                           const __grid_constant__ CUtensorMap xmap,
                                                                           const __grid_constant__ CUtensorMap wmap,
                                                                           const __grid_constant__ CUtensorMap smap) {
@@ -215,7 +246,7 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
 
     if (warp == 0) {
         bool ok = true;
-        unsigned it = 0, s = 0, phase = 0;                 // step, its stage, how often the ring has come round (mod 2)
+        unsigned it = 0, s = 0, phase = 0, place = 0;      // step, its stage, how often the ring has come round (mod 2)
         const uint32_t base = smem_addr(smem);
         const bool lead = elect_one();
         for (int b = b0; b < b1; b += C::BP, ++it) {
@@ -231,9 +262,10 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
                 if (two) tma_2d(at + kMmBytes, &wmap, (b + 1) * kMmTile, tile * kMmTile, &full[s]);
                 tma_2d(at + C::X_AT, &xmap, b * kMmTile, 0, &full[s]);
                 if (two) tma_2d(at + C::X_AT + C::X_BYTES, &xmap, (b + 1) * kMmTile, 0, &full[s]);
-                tma_2d(base + C::SCALE_AT + s * C::SCALE, &smap, 0, b, &full[s]);
+                tma_2d(base + C::SCALE_AT + place * C::SCALE, &smap, 0, b, &full[s]);
             }
             __syncwarp();
+            if (++place == C::PLACES) place = 0;
             if (++s == C::STAGES) {
                 s = 0;
                 phase ^= 1;
@@ -283,12 +315,6 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
     }
     const int quad = warp & 3, row = quad * 32 + lane;     // of a tile's weight rows (warps 2 to 5)
     float acc[T];
-    // a row of x takes 32 neighbouring weight rows' results from a warp
-    auto put = [&](int m, float v) {
-        const int64_t at = (int64_t)m * a.old + (int64_t)tile * kMmTile + row;
-        if (a.f32) reinterpret_cast<float*>(a.out)[at] = v;
-        else reinterpret_cast<unsigned short*>(a.out)[at] = (unsigned short)(pack_bf16(v, 0.f) & 0xffffu);
-    };
     if (warp >= 2) {
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
@@ -298,7 +324,7 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
         const float* wsc = a.wscale + (int64_t)tile * a.ws_stride;
         float wl = 0.f;
         bool ok = true;
-        unsigned s = 0, phase = 0;
+        unsigned s = 0, phase = 0, place = 0;
         for (int b = b0; b < b1; b += C::BP) {
             if (((b - b0) & 31) == 0 && b + lane < b1) wl = ld_scale(wsc + b + lane);
             const bool two = C::BP == 2 && b + 1 < b1;
@@ -306,7 +332,7 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
             ok = wait_warp(&done[s], phase, limit);
             if (!ok) break;
             tc_after();
-            const float4* xs = reinterpret_cast<const float4*>(smem + C::SCALE_AT + s * C::SCALE);
+            const float4* xs = reinterpret_cast<const float4*>(smem + C::SCALE_AT + place * C::SCALE);
             const uint32_t at = from + s * C::COLS;
             float v[2][16];
             tc_ld16_start(at, v[0]);
@@ -329,6 +355,7 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            if (++place == C::PLACES) place = 0;
             if (++s == C::STAGES) {
                 s = 0;
                 phase ^= 1;
@@ -343,34 +370,38 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
     tc_before();
     __syncthreads();                                       // every product is done, the ring is free
     tc_after();
-    const bool mine = warp >= 2 && tile * (long long)kMmTile + row < a.N;
-    if (S == 1) {
-        if (mine) {
+    // ---- the output: the CTAs' sums, [row of x][weight row], through shared memory; a thread takes
+    // four neighbouring weight rows of a row of x, a warp 128.  (A weight row a thread, with its sums in registers: 64
+    // stores of two bytes each for 64 rows, and as many dependent reads of other CTAs' sums.)
+    float* sums = reinterpret_cast<float*>(smem);
+    if (warp >= 2) {
 #pragma unroll
-            for (int c = 0; c < T; ++c)
-                if (c < a.M) put(c, acc[c]);
-        }
-    } else {
-        float* sums = reinterpret_cast<float*>(smem) + row;            // [column][weight row]
-        if (warp >= 2) {
-#pragma unroll
-            for (int c = 0; c < T; ++c)
-                if (c < a.M) sums[c * kMmTile] = acc[c];
-        }
-        cluster_sync();
-        if (mine) {
-            const uint32_t from = smem_addr(sums);
-            for (int c = rank; c < a.M; c += S) {
-                float x[8], v = 0.f;                       // all under way at once
-#pragma unroll
-                for (int r = 0; r < 8; ++r) x[r] = r < S ? ld_cluster(cluster_addr(from + c * kMmTile * 4, r)) : 0.f;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) v += x[r];
-                put(c, v);
-            }
-        }
-        cluster_sync();                                    // no CTA ends while another reads its sums
+        for (int c = 0; c < T; ++c)
+            if (c < a.M) sums[c * kMmTile + row] = acc[c];
     }
+    if (S == 1) __syncthreads();
+    else cluster_sync();
+    const int rows = (a.M - rank + S - 1) / S;             // of x: this CTA's are rank, rank + S, ...
+    const uint32_t from = smem_addr(sums);
+    for (int i = tid; i < rows * 32; i += C::THREADS) {
+        const int m = rank + (i >> 5) * S, o = (i & 31) * 4;
+        const int64_t n = (int64_t)tile * kMmTile + o;
+        if (n >= a.N) continue;
+        float4 x[8];                                       // all under way at once
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r >= S) break;
+            x[r] = ld_cluster4(cluster_addr(from + (m * kMmTile + o) * 4, S == 1 ? (uint32_t)rank : (uint32_t)r));
+        }
+        float v[4] = {};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r >= S) break;
+            v[0] += x[r].x, v[1] += x[r].y, v[2] += x[r].z, v[3] += x[r].w;
+        }
+        put4(a, (int64_t)m * a.old + n, (int)min((int64_t)4, a.N - n), wide, v);
+    }
+    if (S > 1) cluster_sync();                             // no CTA ends while another reads its sums
     if (warp == 1) tc_dealloc(tmem, C::TMEM);
 }
 
@@ -384,8 +415,14 @@ struct MmPlan {
     long long tiles, total;            // steps of all tiles
     int pairs, blocks, whole;          // blocks: steps of a tile
     int W, tiles_m;                    // a tile's weight rows; tiles of 256 rows of x
+    int split;                         // pairs of a cluster
     unsigned long long tag;
     __device__ __forceinline__ long long begin(int p) const { return whole ? tiles * p / pairs * blocks : total * p / pairs; }
+    // (a cluster's pairs share its tile)
+    __device__ __forceinline__ long long part_begin(int p) const {
+        const int tile = p / split, q = p - tile * split;
+        return (long long)tile * blocks + (long long)blocks * q / split;
+    }
     // the pair whose (equal) share has step u
     __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * pairs - 1) / total); }
 };
@@ -473,7 +510,8 @@ __host__ __device__ constexpr unsigned stages_of(int W) {
 __host__ __device__ constexpr unsigned buffers_of(int W) {
     return 512 / W < ManyCfg::NB ? 512 / W : ManyCfg::NB;
 }
-template <int W, bool SPLIT>
+enum MmMode { kMmWhole, kMmTickets, kMmCluster };
+template <int W, MmMode MODE>
 __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const MatmulArgs a, uint32_t limit, const MmPlan plan,
                                                                          const __grid_constant__ CUtensorMap xmap,
                                                                          const __grid_constant__ CUtensorMap wmap,
@@ -491,9 +529,11 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     __shared__ uint32_t tmem_at;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t rank = cluster_rank();
+    // (a cluster: pairs of a tile's, where they share it; the first CTA of a pair leads it)
+    const uint32_t place = cluster_rank(), rank = place & 1, leader = place & ~1u;
     const int pair = blockIdx.x >> 1, blocks = plan.blocks, tiles_m = plan.tiles_m;
-    const long long u0 = plan.begin(pair), u1 = plan.begin(pair + 1);
+    const long long u0 = MODE == kMmCluster ? plan.part_begin(pair) : plan.begin(pair);
+    const long long u1 = MODE == kMmCluster ? plan.part_begin(pair + 1) : plan.begin(pair + 1);
     const int first_tile = (int)(u0 / blocks), first_b = (int)(u0 - (long long)first_tile * blocks);
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -529,7 +569,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         if (warp == 0) {
             bool ok = true, free = false;
             unsigned it = 0, s = 0, phase = 0;             // step, its stage, how often the ring has come round (mod 2)
-            const uint32_t base = smem_addr(smem), bars = cluster_addr(smem_addr(full), 0);
+            const uint32_t base = smem_addr(smem), bars = cluster_addr(smem_addr(full), leader);
             uint64_t(&last)[C::STAGES] = done[TWO ? 1 : 0];
             const bool lead = elect_one();
             long long left = u1 - u0;
@@ -566,6 +606,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             }
             if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
         } else if (warp == 1 && rank == 0) {
+            const unsigned short both = (unsigned short)(3u << leader);
             const uint32_t id = tc_idesc(true, false, false, TWO ? H : W, 256);
             const uint64_t base = tc_desc(smem_addr(smem), 16, 1024);
             unsigned it = 0, s = 0, phase = 0, t = 0, t_phase = 0;
@@ -587,7 +628,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     if (lead) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) pair_mma(to, xd + 2 * k, wd + 2 * k, id, k > 0);
-                        pair_commit(&done[0][now]);
+                        pair_commit(&done[0][now], both);
                     }
                     if (!__all_sync(0xffffffffu, second)) {
                         ok = wait_warp(&t_empty[1][t], t_phase ^ 1, limit);
@@ -611,14 +652,14 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     const uint64_t wd2 = TWO ? wd + (H / 2 * kMmTile >> 4) : wd;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) pair_mma(to + (TWO ? 256 : 0), xd + 2 * k, wd2 + 2 * k, id, k > 0);
-                    pair_commit(&done[TWO ? 1 : 0][now]);
+                    pair_commit(&done[TWO ? 1 : 0][now], both);
                 }
                 ready = __all_sync(0xffffffffu, next);
             }
             if (!ok) {
                 if (lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
                 if (it > 0) {
-                    if (lead) pair_commit(&drained);
+                    if (lead) pair_commit(&drained, both);
                     __syncwarp();
                     wait_warp(&drained, 0, kTcWaitLimit);
                 }
@@ -660,126 +701,26 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             copies_done();
             if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
         }
+        __syncwarp();
+        if (MODE == kMmCluster) cluster_sync();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE));
         const int part = (warp - 4) >> 2, quad = warp & 3, half = TWO ? part : 0;
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (TWO ? part * 256 : part * H), step = TWO ? H : W;
-        unsigned char* const pieces = smem + C::OUT_AT + (warp - 4) * 4096;
-        const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), 0);
+        // (a cluster's sums lie in the output's place, its output in the ring's, which is free then)
+        unsigned char* const pieces = smem + (MODE == kMmCluster ? 0 : C::OUT_AT) + (warp - 4) * 4096;
+        static_assert(MODE != kMmCluster || W == 64, "a warp's sums fit its 4 KB");
+        const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), leader);
         unsigned gi = 0, s = 0, phase = 0, t = 0, stored = 0;
         bool ok = true;
         long long left = u1 - u0;
-        for (int tile = first_tile, at = first_b; left > 0; ++tile, at = 0) {
-            const int end = (int)min((long long)blocks, at + left);
-            left -= end - at;
+        float acc[C::COLS];
+        auto output = [&](int tile) {
             const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128 + quad * 32;
             const int n0 = tn * W + part * H;
-            const int split = (n0 / kScaleBlock + 1) * kScaleBlock - n0;     // columns of the first block
-            float acc[C::COLS];
-#pragma unroll
-            for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
-            for (int b4 = at; ok && b4 < end; b4 += 4, ++gi) {
-                const unsigned char* scales = smem + C::F_AT + gi % C::FS * C::F_BYTES;
-                ok = wait_warp(&f_full[gi % C::FS], (gi / C::FS) & 1, limit);
-                if (!ok) break;
-                const float4 fx = *reinterpret_cast<const float4*>(scales + (quad * 32 + lane) * 16);
-                const float4 fw = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32);
-                const float4 fv = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32 + 16);
-                const float f[4] = {fx.x * fw.x, fx.y * fw.y, fx.z * fw.z, fx.w * fw.w};
-                const float g[4] = {fx.x * fv.x, fx.y * fv.y, fx.z * fv.z, fx.w * fv.w};
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&f_empty[gi % C::FS]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (!ok || b4 + j >= end) continue;
-                    ok = wait_warp(&done[half][s], phase, limit);
-                    if (!ok) continue;
-                    tc_after();
-                    constexpr int L = 16;                  // columns a load
-                    float v[2][L];
-                    tc_ld16_start(from + t * step, v[0]);
-#pragma unroll
-                    for (int c = 0; c < C::COLS; c += L) {
-                        if (c >= H) break;
-                        float* now = v[(c / L) & 1];
-                        tc_wait_ld();
-                        tc_ld16_done(now);
-                        if (c + L < H) {
-                            tc_ld16_start(from + t * step + c + L, v[(c / L + 1) & 1]);
-                        } else {
-                            tc_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
-                        }
-                        const float fg = c < split ? f[j] : g[j];
-#pragma unroll
-                        for (int e = 0; e < L; e += 2)
-                            f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(acc[c + e], acc[c + e + 1])),
-                                      acc[c + e], acc[c + e + 1]);
-                    }
-                    if (++s == stages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                    if (++t == buffers) t = 0;
-                }
-            }
-            if (!ok) {                                     // a result that is not valid shows
-#pragma unroll
-                for (int c = 0; c < C::COLS; ++c) acc[c] = CUDART_NAN_F;
-            }
-            if (SPLIT && end - at < blocks) {
-                const MmParts parts(plan, tile);
-                const int n = parts.p1 - parts.p0 + 1, w = (int)rank * C::EW + warp - 4;
-                unsigned long long* ticket = reinterpret_cast<unsigned long long*>(a.ws + kMmTicketAt) + parts.p0 * 16 + w;
-                auto part_of = [&](int p) {
-                    return reinterpret_cast<float4*>(parts.part(plan, a.ws, p)) + (size_t)w * (C::PART / 4) + lane;
-                };
-                auto add = [&](int p) {
-                    const float4* q = part_of(p);
-                    constexpr int B = H < 32 ? H / 4 : 8, NBATCH = H / (4 * B);     // loads of a batch; one ahead
-                    float4 x[2][B];
-#pragma unroll
-                    for (int c = 0; c < B; ++c) x[0][c] = __ldcg(q + 4 * c * 8);
-#pragma unroll
-                    for (int k = 0; k < NBATCH; ++k) {
-                        if (k + 1 < NBATCH) {
-#pragma unroll
-                            for (int c = 0; c < B; ++c) x[(k + 1) & 1][c] = __ldcg(q + ((k + 1) * B + c) * 4 * 8);
-                        }
-#pragma unroll
-                        for (int c = 0; c < B; ++c) {
-                            float* to = acc + (k * B + c) * 4;
-                            const float4 y = x[k & 1][c];
-                            to[0] += y.x;
-                            to[1] += y.y;
-                            to[2] += y.z;
-                            to[3] += y.w;
-                        }
-                    }
-                };
-                // (of two parts, the second to be ready need not be written: their order does not matter)
-                bool second = false;
-                if (n == 2) {
-                    second = __any_sync(0xffffffffu, lane == 0 && tickets_taken(*reinterpret_cast<volatile unsigned long long*>(ticket), plan.tag) == 1);
-                }
-                if (!second) {
-                    float4* mine = part_of(pair);
-#pragma unroll
-                    for (int c = 0; c < H; c += 4) __stcg(mine + c * 8, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
-                }
-                if (!last_ticket(ticket, plan.tag, n, lane)) continue;
-                if (n > 2) {
-#pragma unroll
-                    for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
-                }
-#pragma unroll 1
-                for (int p = parts.p0; p <= parts.p1; ++p)
-                    if (n > 2 || p != pair) add(p);
-            }
             // ---- the tile's output, in pieces of 64 bytes of the warp's 32 rows: by TMA where the rows are
             // aligned, else (and for a last piece of half the columns) through the same place and registers
-            if (m0 >= a.M) continue;
+            if (m0 >= a.M) return;
             auto piece = [&](unsigned char* at_, int r, int c) { return reinterpret_cast<uint4*>(at_ + r * 64 + ((c ^ (r >> 1 & 3)) << 4)); };
             // cols columns from n on of the rows' 64 bytes, `vec` bytes a lane
             auto put = [&](unsigned char* from_, int n, int cols) {
@@ -842,8 +783,139 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     send(to, n0 + c0, min(32, H - c0), 32);
                 }
             }
+        };
+        for (int tile = first_tile, at = first_b; left > 0; ++tile, at = 0) {
+            const int end = (int)min((long long)blocks, at + left);
+            left -= end - at;
+            const int n0 = tile / tiles_m * W + part * H;
+            const int split = (n0 / kScaleBlock + 1) * kScaleBlock - n0;     // columns of the first block
+#pragma unroll
+            for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+            for (int b4 = at; ok && b4 < end; b4 += 4, ++gi) {
+                const unsigned char* scales = smem + C::F_AT + gi % C::FS * C::F_BYTES;
+                ok = wait_warp(&f_full[gi % C::FS], (gi / C::FS) & 1, limit);
+                if (!ok) break;
+                const float4 fx = *reinterpret_cast<const float4*>(scales + (quad * 32 + lane) * 16);
+                const float4 fw = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32);
+                const float4 fv = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32 + 16);
+                const float f[4] = {fx.x * fw.x, fx.y * fw.y, fx.z * fw.z, fx.w * fw.w};
+                const float g[4] = {fx.x * fv.x, fx.y * fv.y, fx.z * fv.z, fx.w * fv.w};
+                // the group before has been taken; this one may still be on its way from shared memory
+                if (lane == 0 && gi > 0) mbar_arrive(&f_empty[(gi - 1) % C::FS]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!ok || b4 + j >= end) continue;
+                    ok = wait_warp(&done[half][s], phase, limit);
+                    if (!ok) continue;
+                    tc_after();
+                    constexpr int L = 16;                  // columns a load
+                    float v[2][L];
+                    tc_ld16_start(from + t * step, v[0]);
+#pragma unroll
+                    for (int c = 0; c < C::COLS; c += L) {
+                        if (c >= H) break;
+                        float* now = v[(c / L) & 1];
+                        tc_wait_ld();
+                        tc_ld16_done(now);
+                        if (c + L < H) {
+                            tc_ld16_start(from + t * step + c + L, v[(c / L + 1) & 1]);
+                        } else {
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
+                        }
+                        const float fg = c < split ? f[j] : g[j];
+#pragma unroll
+                        for (int e = 0; e < L; e += 2)
+                            f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(acc[c + e], acc[c + e + 1])),
+                                      acc[c + e], acc[c + e + 1]);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    if (++t == buffers) t = 0;
+                }
+            }
+            if (!ok) {                                     // a result that is not valid shows
+#pragma unroll
+                for (int c = 0; c < C::COLS; ++c) acc[c] = CUDART_NAN_F;
+            }
+            if (MODE == kMmCluster) break;
+            if (MODE == kMmTickets && end - at < blocks) {
+                const MmParts parts(plan, tile);
+                const int n = parts.p1 - parts.p0 + 1, w = (int)rank * C::EW + warp - 4;
+                unsigned long long* ticket = reinterpret_cast<unsigned long long*>(a.ws + kMmTicketAt) + parts.p0 * 16 + w;
+                auto part_of = [&](int p) {
+                    return reinterpret_cast<float4*>(parts.part(plan, a.ws, p)) + (size_t)w * (C::PART / 4) + lane;
+                };
+                auto add = [&](int p) {
+                    const float4* q = part_of(p);
+                    constexpr int B = H < 32 ? H / 4 : 8, NBATCH = H / (4 * B);     // loads of a batch; one ahead
+                    float4 x[2][B];
+#pragma unroll
+                    for (int c = 0; c < B; ++c) x[0][c] = __ldcg(q + 4 * c * 8);
+#pragma unroll
+                    for (int k = 0; k < NBATCH; ++k) {
+                        if (k + 1 < NBATCH) {
+#pragma unroll
+                            for (int c = 0; c < B; ++c) x[(k + 1) & 1][c] = __ldcg(q + ((k + 1) * B + c) * 4 * 8);
+                        }
+#pragma unroll
+                        for (int c = 0; c < B; ++c) {
+                            float* to = acc + (k * B + c) * 4;
+                            const float4 y = x[k & 1][c];
+                            to[0] += y.x;
+                            to[1] += y.y;
+                            to[2] += y.z;
+                            to[3] += y.w;
+                        }
+                    }
+                };
+                // (of two parts, the second to be ready need not be written: their order does not matter)
+                bool second = false;
+                if (n == 2) {
+                    second = __any_sync(0xffffffffu, lane == 0 && tickets_taken(*reinterpret_cast<volatile unsigned long long*>(ticket), plan.tag) == 1);
+                }
+                if (!second) {
+                    float4* mine = part_of(pair);
+#pragma unroll
+                    for (int c = 0; c < H; c += 4) __stcg(mine + c * 8, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+                }
+                if (!last_ticket(ticket, plan.tag, n, lane)) continue;
+                if (n > 2) {
+#pragma unroll
+                    for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+                }
+#pragma unroll 1
+                for (int p = parts.p0; p <= parts.p1; ++p)
+                    if (n > 2 || p != pair) add(p);
+            }
+            output(tile);
         }
-        if (lane == 0) tma_store_wait_all();
+        if (MODE == kMmCluster) {
+            // The sums of the cluster's pairs over distributed shared memory, in their order: the first pair
+            // finishes the tile's first half of columns, the second the second.
+            float* sums = reinterpret_cast<float*>(smem + C::OUT_AT + (warp - 4) * 4096) + lane;       // [column][row]
+#pragma unroll
+            for (int c = 0; c < H; ++c) sums[c * 32] = acc[c];
+            cluster_sync();
+            if ((int)(place >> 1) == part) {
+#pragma unroll
+                for (int c = 0; c < H; ++c) acc[c] = 0.f;
+#pragma unroll 1
+                for (int p = 0; p < plan.split; ++p) {
+                    const uint32_t from_ = cluster_addr(smem_addr(sums), 2 * p + rank);
+                    float x[H];
+#pragma unroll
+                    for (int c = 0; c < H; ++c) x[c] = ld_cluster(from_ + c * 128);
+#pragma unroll
+                    for (int c = 0; c < H; ++c) acc[c] += x[c];
+                }
+                output(first_tile);
+            }
+        }
+        if (lane == 0) tma_store_wait<0>();
         __syncwarp();
         if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
     }
@@ -884,55 +956,94 @@ static cudaError_t launch_clusters(void (*kfn)(KArgs...), int grid, int cluster,
 
 static uint32_t wait_limit() { return ring_wait_limit() < kTcWaitLimit ? ring_wait_limit() : kTcWaitLimit; }
 
-// How many clusters of S = 1 to 8 CTAs run at once (they stay within groups of SMs).  The occupancy
-// query takes a kernel that allocates tensor memory for one that wants an SM to itself: it is
-// two, as shared memory and tensor memory are divided here.
-template <int T>
-static cudaError_t few_clusters(int (&most)[9]) {
-    using C = FewCfg<T>;
-    static DeviceSlots slots[9] = {};
-    for (int S = 1; S <= 8; ++S) {
-        const cudaError_t e = device_once(slots[S], &most[S], [&](int, int* o) {
-            cudaError_t x = cudaFuncSetAttribute(matmul_few_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-            if (x != cudaSuccess) return x;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(8 * S));
-            cfg.blockDim = dim3(C::THREADS);
-            cfg.dynamicSmemBytes = C::SMEM;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = (unsigned)S;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            x = cudaOccupancyMaxActiveClusters(o, matmul_few_kernel<T>, &cfg);
-            *o *= C::CTAS;
-            return x;
-        });
+// How many clusters of n CTAs run at once (they stay within groups of SMs).
+template <typename... KArgs>
+static cudaError_t clusters_at_once(int* count, void (*kfn)(KArgs...), int n, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(8 * n));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(count, kfn, &cfg);
+}
+
+static bool rows_aligned(const MatmulArgs& a) { return is_aligned(a.out, 16) && a.old * (a.f32 ? 4 : 2) % 16 == 0; }
+
+// What a device answers once: for each place of most, how many clusters run at once.  (Threads that ask
+// at the same time write the same answers; one look-up a call, as asking for the device takes the host
+// 30 ns.)
+template <int N>
+struct Clusters {
+    std::atomic<int> ready[kMaxDevices] = {}, most[kMaxDevices][N] = {};
+    template <typename F>
+    cudaError_t get(int (&out)[N], F ask) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const bool kept = dev >= 0 && dev < kMaxDevices;
+        if (kept && ready[dev].load(std::memory_order_acquire)) {
+            for (int i = 0; i < N; ++i) out[i] = most[dev][i].load(std::memory_order_relaxed);
+            return cudaSuccess;
+        }
+        for (int i = 0; i < N; ++i) {
+            e = ask(i, &out[i]);
+            if (e != cudaSuccess) return e;
+            if (kept) most[dev][i].store(out[i], std::memory_order_relaxed);
+        }
+        if (kept) ready[dev].store(1, std::memory_order_release);
+        return cudaSuccess;
     }
-    return cudaSuccess;
+};
+
+// Clusters of 1 to 8 CTAs.  The occupancy query takes a kernel that allocates tensor memory for one that
+// wants an SM to itself: it is two, as shared memory and tensor memory are divided here.
+template <int T>
+static cudaError_t few_clusters(int (&most)[8]) {
+    using C = FewCfg<T>;
+    static Clusters<8> table;
+    return table.get(most, [](int i, int* o) {
+        cudaError_t e = cudaFuncSetAttribute(matmul_few_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e == cudaSuccess) e = clusters_at_once(o, matmul_few_kernel<T>, i + 1, C::THREADS, C::SMEM);
+        *o *= C::CTAS;
+        return e;
+    });
 }
 
 template <int T>
 static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
     using C = FewCfg<T>;
-    int most[9];
+    int most[8];
     const cudaError_t e = few_clusters<T>(most);
     if (e != cudaSuccess) return e;
     const int tiles = (a.N - 1) / kMmTile + 1, blocks = scale_blocks(a.K);
-    // The largest clusters of which all run at once, but that leave a CTA its two blocks.  (One row, N = 6144,
-    // K = 4096, 48 tiles: 6.3 us in clusters of five, of which 56 fit; 7.5 in four, 9.6 in six, of which 46
-    // do.)
+    // Of the clusters of which all run at once, those that take the least: a CTA's blocks one after the other,
+    // and the join (measured at N = 1024, K = 512 to 4096; more tiles only wait for memory).  One row, N =
+    // 6144, K = 4096, 48 tiles: 6.3 us in clusters of five, of which 56 fit; 7.5 in four, 9.6 in six, of
+    // which 46 do.
+    constexpr double kStep = T <= 16 ? 0.17 : T <= 32 ? 0.22 : 0.28;
+    constexpr double kJoin[9] = {0, 0, 1.2, 0.9, 0.8, 1.0, 1.1, 1.3, 1.5};
     int S = 1;
-    for (int i = 2; i <= 8; ++i)
-        if (tiles <= most[i] && i * C::BP <= blocks) S = i;
+    double best = 1e300;
+    for (int i = 1; i <= 8 && i <= blocks; ++i) {
+        if (i > 1 && tiles > most[i - 1]) continue;
+        const int own = (blocks + i * C::BP - 1) / (i * C::BP) * C::BP;
+        const double us = own * kStep + (i == 1 ? 0.0 : T <= 16 ? 1.3 : kJoin[i]);
+        if (us <= best) {
+            best = us;
+            S = i;
+        }
+    }
     CUtensorMap xm, wm, sm;
     if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, T, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, C::BP, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
-    return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, xm, wm, sm);
+    return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, rows_aligned(a), xm, wm, sm);
 }
 
 // What a step of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows and
@@ -946,7 +1057,7 @@ constexpr MmWidth kMmWidths[4] = {{64, 0.213, 0.6}, {128, 0.266, 1.2}, {192, 0.3
 // Whole tiles in the width whose rounds of all pairs take the least, or equal shares, whose parts
 // cost their writing and reading, where that is less: few tiles with long contractions, or
 // little more than whole rounds.
-static MmPlan plan_many(const MatmulArgs& a, int sms) {
+static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) {
     MmPlan p = {};
     p.blocks = scale_blocks(a.K);
     p.tiles_m = (a.M - 1) / 256 + 1;
@@ -954,7 +1065,7 @@ static MmPlan plan_many(const MatmulArgs& a, int sms) {
     double best = 1e300;
     for (const MmWidth& w : kMmWidths) {
         const long long tiles = (long long)p.tiles_m * ((a.N - 1) / w.W + 1), total = tiles * p.blocks;
-        const auto take = [&](double us, long long pairs, int whole) {
+        const auto take = [&](double us, long long pairs, int whole, int split) {
             if (us >= best) return;
             best = us;
             p.W = w.W;
@@ -962,8 +1073,13 @@ static MmPlan plan_many(const MatmulArgs& a, int sms) {
             p.tiles = tiles;
             p.total = total;
             p.pairs = (int)pairs;
+            p.split = split;
         };
-        take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1);
+        take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1, 1);
+        for (int i = 0; i < 2 && w.W == 64; ++i) {
+            const int split = 2 << i;
+            if (tiles <= clusters[i] && split <= p.blocks) take((p.blocks + split - 1) / split * w.step + w.end + 1.0 + 0.25 * split, tiles * split, 1, split);
+        }
         if (w.W != 64 && w.W != 256) continue;
         for (int n = 2; n <= 8; ++n) {
             // (n: parts of a tile)
@@ -971,17 +1087,17 @@ static MmPlan plan_many(const MatmulArgs& a, int sms) {
             if (tiles * (n - 1) >= most && n > 2) break;
             if (total < 4 * pairs) break;
             const long long steps = (total + pairs - 1) / pairs;
-            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + 4.0 + (n - 1) * (w.W == 64 ? 1.0 : 3.0), pairs, 0);
+            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + 4.0 + (n - 1) * (w.W == 64 ? 1.0 : 3.0), pairs, 0, 1);
         }
     }
     p.tag = next_launch_tag();
     return p;
 }
 
-template <int W, bool SPLIT>
+template <int W, MmMode MODE>
 static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStream_t st) {
     using C = ManyCfg;
-    auto kfn = matmul_many_kernel<W, SPLIT>;
+    auto kfn = matmul_many_kernel<W, MODE>;
     static DeviceSlots slots = {};
     int unused = 0;
     cudaError_t e = device_once(slots, &unused, [&](int, int* o) {
@@ -990,7 +1106,7 @@ static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStrea
     });
     if (e != cudaSuccess) return e;
     const int elt = a.f32 ? 4 : 2;
-    const bool by_tma = is_aligned(a.out, 16) && a.old * elt % 16 == 0 && a.old * elt < (1LL << 40);
+    const bool by_tma = rows_aligned(a) && a.old * elt < (1LL << 40);
     // else the widest pieces that every row's begin allows
     const uint64_t align = reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.old * elt;
     const int vec = align % 8 == 0 ? 8 : align % 4 == 0 ? 4 : 2;
@@ -1000,18 +1116,33 @@ static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStrea
         (by_tma && !map_2d(&om, a.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.N, a.M, a.old * elt,
                            64 / elt, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
         return cudaErrorInvalidValue;
-    return launch_clusters(kfn, p.pairs * 2, 2, C::THREADS, C::SMEM, st, a, wait_limit(), p, xm, wm, om, by_tma, vec);
+    return launch_clusters(kfn, p.pairs * 2, MODE == kMmCluster ? 2 * p.split : 2, C::THREADS, C::SMEM, st, a, wait_limit(), p, xm, wm, om, by_tma, vec);
+}
+
+// Clusters of two and of four pairs.
+static cudaError_t many_clusters(int (&most)[2]) {
+    using C = ManyCfg;
+    static Clusters<2> table;
+    return table.get(most, [](int i, int* o) {
+        const auto kfn = matmul_many_kernel<64, kMmCluster>;
+        const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        return e != cudaSuccess ? e : clusters_at_once(o, kfn, 4 << i, C::THREADS, C::SMEM);
+    });
 }
 
 static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
     if ((long long)((a.M - 1) / 256 + 1) * ((a.N - 1) / 64 + 1) >= (1LL << 31)) return cudaErrorInvalidValue;
-    const MmPlan p = plan_many(a, sms);
-    if (!p.whole) return p.W == 64 ? launch_many_t<64, true>(a, p, st) : launch_many_t<256, true>(a, p, st);
+    int clusters[2];
+    const cudaError_t e = many_clusters(clusters);
+    if (e != cudaSuccess) return e;
+    const MmPlan p = plan_many(a, sms, clusters);
+    if (p.split > 1) return launch_many_t<64, kMmCluster>(a, p, st);
+    if (!p.whole) return p.W == 64 ? launch_many_t<64, kMmTickets>(a, p, st) : launch_many_t<256, kMmTickets>(a, p, st);
     switch (p.W) {
-        case 64: return launch_many_t<64, false>(a, p, st);
-        case 128: return launch_many_t<128, false>(a, p, st);
-        case 192: return launch_many_t<192, false>(a, p, st);
-        default: return launch_many_t<256, false>(a, p, st);
+        case 64: return launch_many_t<64, kMmWhole>(a, p, st);
+        case 128: return launch_many_t<128, kMmWhole>(a, p, st);
+        case 192: return launch_many_t<192, kMmWhole>(a, p, st);
+        default: return launch_many_t<256, kMmWhole>(a, p, st);
     }
 }
 

@@ -226,6 +226,21 @@ def test_matmul_repeats_itself(sv, M):
         assert torch.equal(first, sv.matmul_e4m3(x, xs, w, ws, dtype=torch.float32))
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 20000, 4096), (32, 20000, 4096), (16, 20000, 4096), (64, 1000, 4096), (100, 700, 4096),
+                                   (512, 6144, 4096), (700, 1000, 16384)])
+def test_matmul_agrees_with_itself_over_many_runs(sv, M, N, K):
+    """Enough runs, with the memory busy now and then, for a stage that is written again too early."""
+    p = R.problem(M, M, N, K)
+    first = sv.matmul_e4m3(*p, dtype=torch.float32)
+    other = torch.empty(32 << 20, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        if i % 3 == 0:
+            other.fill_(i)
+        differ += (sv.matmul_e4m3(*p, dtype=torch.float32) != first).sum()
+    assert int(differ) == 0
+
+
 def test_matmul_empty(sv):
     x, xs, w, ws = R.problem(0, 4, 32, 64)
     assert sv.matmul_e4m3(x[:0], xs[:0], w, ws).shape == (0, 32)

@@ -17,8 +17,10 @@ def sv():
     return m
 
 
-# few rows with one CTA and with clusters; whole tiles; tiles shared by pairs, of two widths
-SHAPES = [(3, 400, 128), (9, 300, 4096), (64, 1000, 2048), (100, 700, 1024), (700, 5000, 1040), (300, 128, 16384), (1100, 2600, 12288)]
+# few rows with one CTA and with clusters; clusters of pairs; whole tiles; tiles shared by pairs, of two
+# widths
+SHAPES = [(3, 400, 128), (9, 300, 4096), (64, 1000, 2048), (100, 700, 1024), (300, 128, 16384), (700, 5000, 1040), (600, 1000, 16384),
+          (1100, 2600, 12288)]
 
 
 def feed_forward(sv, seed, rows, dim, wide):
