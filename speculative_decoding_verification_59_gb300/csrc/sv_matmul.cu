@@ -6,6 +6,15 @@
 // are exact to fp32; the warps that read them add them, times the two scales, to
 // running sums in registers, while the next blocks' products run into the other
 // accumulators.
+//
+// Measured (one GB300, inputs new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
+// copy 6.8 TB/s):
+//   1 row, N = 6144, K = 4096: 6.4 us, 3.9 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 3.5 us
+//     of a call's begin and end.
+//   512 rows, N = 151936, K = 4096: 281 us, 2.27 PFLOP/s; N = 24576: 51 us, 2.0; 1152 rows, N = 4096, K =
+//     12288: 61 us, 1.9.  A step of 256 x 256 x 128 takes a pair 0.43 us, of which the products would
+//     take 0.27: the rest is the chain from an accumulator's last product to its next; and the clock
+//     falls to 1.75 GHz under it.  With constant inputs, which use less power: 255 us, 2.5 PFLOP/s.
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 #include "sv_linear.h"
@@ -471,8 +480,8 @@ __device__ __forceinline__ bool last_ticket(unsigned long long* w, unsigned long
 
 // ---- more rows ---------------------------------------------------------------------
 // A pair of CTAs takes 256 rows of x times W weight rows (cta_group::2: each loads its 128
-// rows of x and half of the weight rows, and holds its 128 rows' sums).  W, a multiple of 32 up to
-// 256, is chosen by the launch so that the tiles fill the pairs evenly.
+// rows of x and half of the weight rows, and holds its 128 rows' sums).  W, of 64, 128, 192 and 256, is
+// chosen by the launch so that the tiles fill the pairs evenly.
 //   warp 0      loads
 //   warp 1      issues the products (the pair's first CTA, for both)
 //   warp 2      brings the scales
@@ -482,7 +491,7 @@ __device__ __forceinline__ bool last_ticket(unsigned long long* w, unsigned long
 // accumulators, so that the second half's run while the first's are read.  Between an
 // accumulator's last product and its next lie a commit, a wake, its reading and an arrival in the other
 // CTA, some 1400 cycles in which two accumulators of 256 columns left the tensor cores idle half the
-// time.
+// time (512 x 38912 x 4096: 69 us so, 64 with halves).
 struct ManyCfg {
     static constexpr int EW = 8;                           // warps of the sums
     static constexpr int STAGES = 8, NB = 4;               // at most
@@ -519,6 +528,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     using C = ManyCfg;
     constexpr bool TWO = two_halves(W);
     constexpr int H = W / 2;
+    constexpr bool CROSS = kScaleBlock % H != 0;           // a half's columns may lie in two blocks of the weights
+    static_assert(H % 32 == 0 && H <= ManyCfg::COLS, "whole pieces of the output");
     constexpr unsigned stages = stages_of(W), buffers = buffers_of(W);
     constexpr uint32_t stage_bytes = C::X_BYTES + H * kMmTile;
     extern __shared__ unsigned char smem_raw[];
@@ -719,13 +730,20 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128 + quad * 32;
             const int n0 = tn * W + part * H;
             // ---- the tile's output, in pieces of 64 bytes of the warp's 32 rows: by TMA where the rows are
-            // aligned, else (and for a last piece of half the columns) through the same place and registers
+            // aligned, else through the same place and registers, `vec` bytes a lane
             if (m0 >= a.M) return;
             auto piece = [&](unsigned char* at_, int r, int c) { return reinterpret_cast<uint4*>(at_ + r * 64 + ((c ^ (r >> 1 & 3)) << 4)); };
-            // cols columns from n on of the rows' 64 bytes, `vec` bytes a lane
-            auto put = [&](unsigned char* from_, int n, int cols) {
-                const int elt = a.f32 ? 4 : 2, at_ = lane * vec & 63, e = at_ / elt, step_ = vec / 2;      // rows at a time
-                const bool have = e < cols && n + e < a.N;
+            auto send = [&](unsigned char* from_, int n) {
+                if (by_tma) {
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&omap, n, m0, smem_addr(from_));
+                    ++stored;
+                    return;
+                }
+                __syncwarp();
+                const int elt = a.f32 ? 4 : 2, at_ = lane * vec & 63, step_ = vec / 2;          // rows at a time
+                const bool have = n + at_ / elt < a.N;
                 char* to = a.out + ((int64_t)(m0 + lane * vec / 64) * a.old + n) * elt + at_;
 #pragma unroll 4
                 for (int r = lane * vec / 64; r < 32; r += step_, to += (int64_t)step_ * a.old * elt) {
@@ -735,18 +753,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     else if (vec == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(x);
                     else *reinterpret_cast<unsigned short*>(to) = *reinterpret_cast<const unsigned short*>(x);
                 }
-            };
-            auto send = [&](unsigned char* from_, int n, int cols, int full_cols) {
-                if (by_tma && cols == full_cols) {
-                    proxy_fence();
-                    __syncwarp();
-                    if (lane == 0) tma_store_2d(&omap, n, m0, smem_addr(from_));
-                    ++stored;
-                } else {
-                    __syncwarp();
-                    put(from_, n, cols);
-                    __syncwarp();
-                }
+                __syncwarp();
             };
             // (a piece's place is free again when the last store but one has been read)
             auto place = [&]() {
@@ -758,8 +765,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             };
             if (a.f32) {
 #pragma unroll
-                for (int c0 = 0; c0 < C::COLS; c0 += 16) {
-                    if (c0 >= H || n0 + c0 >= a.N) break;
+                for (int c0 = 0; c0 < H; c0 += 16) {
+                    if (n0 + c0 >= a.N) break;
                     unsigned char* to = place();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -767,12 +774,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                         *piece(to, lane, c) =
                             make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
                     }
-                    send(to, n0 + c0, 16, 16);
+                    send(to, n0 + c0);
                 }
             } else {
 #pragma unroll
-                for (int c0 = 0; c0 < C::COLS; c0 += 32) {
-                    if (c0 >= H || n0 + c0 >= a.N) break;
+                for (int c0 = 0; c0 < H; c0 += 32) {
+                    if (n0 + c0 >= a.N) break;
                     unsigned char* to = place();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -780,7 +787,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                         *piece(to, lane, c) =
                             make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                     }
-                    send(to, n0 + c0, min(32, H - c0), 32);
+                    send(to, n0 + c0);
                 }
             }
         };
@@ -797,7 +804,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 if (!ok) break;
                 const float4 fx = *reinterpret_cast<const float4*>(scales + (quad * 32 + lane) * 16);
                 const float4 fw = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32);
-                const float4 fv = *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32 + 16);
+                const float4 fv = CROSS ? *reinterpret_cast<const float4*>(scales + 128 * 16 + part * 32 + 16) : fw;
                 const float f[4] = {fx.x * fw.x, fx.y * fw.y, fx.z * fw.z, fx.w * fw.w};
                 const float g[4] = {fx.x * fv.x, fx.y * fv.y, fx.z * fv.z, fx.w * fv.w};
                 // the group before has been taken; this one may still be on its way from shared memory
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                             __syncwarp();
                             if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
                         }
-                        const float fg = c < split ? f[j] : g[j];
+                        const float fg = !CROSS || c < split ? f[j] : g[j];
 #pragma unroll
                         for (int e = 0; e < L; e += 2)
                             f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(acc[c + e], acc[c + e + 1])),
@@ -1106,9 +1113,10 @@ static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStrea
     });
     if (e != cudaSuccess) return e;
     const int elt = a.f32 ? 4 : 2;
-    const bool by_tma = rows_aligned(a) && a.old * elt < (1LL << 40);
-    // else the widest pieces that every row's begin allows
-    const uint64_t align = reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.old * elt;
+    // (a TMA store writes whole 16 bytes, also where its tensor ends inside them)
+    const bool by_tma = rows_aligned(a) && (int64_t)a.N * elt % 16 == 0 && a.old * elt < (1LL << 40);
+    // else the widest pieces that every row's begin and end allow
+    const uint64_t align = reinterpret_cast<uintptr_t>(a.out) | (uint64_t)a.old * elt | (uint64_t)a.N * elt;
     const int vec = align % 8 == 0 ? 8 : align % 4 == 0 ? 4 : 2;
     CUtensorMap xm, wm, om = {};
     if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||

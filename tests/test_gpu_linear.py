@@ -218,6 +218,20 @@ def test_matmul_strides_shapes_and_nan(sv, M):
     assert torch.equal(bad.isnan(), nan) and torch.equal(bad[~nan], got[~nan])
 
 
+@pytest.mark.parametrize("M", [5, 64, 100, 300])
+@pytest.mark.parametrize("N,stride,at", [(262, 264, 0), (263, 272, 0), (261, 268, 4), (130, 132, 2), (129, 131, 1), (70, 1000, 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matmul_into_wider_rows(sv, M, N, stride, at, dtype):
+    """Rows of an output that is a slice: whatever their stride's alignment, nothing beside them is written."""
+    p = R.problem(N, M, N, 400)
+    want = sv.matmul_e4m3(*p, dtype=dtype)
+    room = torch.full((M + 2, stride), -7.0, device="cuda", dtype=dtype)
+    got = sv.matmul_e4m3(*p, dtype=dtype, out=room[1:-1, at:at + N])
+    assert torch.equal(got, want)
+    room[1:-1, at:at + N] = -7
+    assert (room == -7).all()
+
+
 @pytest.mark.parametrize("M", [3, 100, 700])
 def test_matmul_repeats_itself(sv, M):
     x, xs, w, ws = R.problem(M, M, 1500, 2064)
