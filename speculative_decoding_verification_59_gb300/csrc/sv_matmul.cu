@@ -426,7 +426,8 @@ struct MmPlan {
     int W, tiles_m;                    // a tile's weight rows; tiles of 256 rows of x
     int split;                         // pairs of a cluster
     unsigned long long tag;
-    __device__ __forceinline__ long long begin(int p) const { return whole ? tiles * p / pairs * blocks : total * p / pairs; }
+    // equal shares: the first step of a pair's
+    __device__ __forceinline__ long long begin(int p) const { return total * p / pairs; }
     // (a cluster's pairs share its tile)
     __device__ __forceinline__ long long part_begin(int p) const {
         const int tile = p / split, q = p - tile * split;
@@ -543,9 +544,17 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     // (a cluster: pairs of a tile's, where they share it; the first CTA of a pair leads it)
     const uint32_t place = cluster_rank(), rank = place & 1, leader = place & ~1u;
     const int pair = blockIdx.x >> 1, blocks = plan.blocks, tiles_m = plan.tiles_m;
-    const long long u0 = MODE == kMmCluster ? plan.part_begin(pair) : plan.begin(pair);
-    const long long u1 = MODE == kMmCluster ? plan.part_begin(pair + 1) : plan.begin(pair + 1);
-    const int first_tile = (int)(u0 / blocks), first_b = (int)(u0 - (long long)first_tile * blocks);
+    // The first tile, its first step, and the steps to do.  Whole tiles go to the pairs in turn: those of the
+    // same weight rows are taken side by side, and the weights read once.
+    int first_tile = pair, first_b = 0;
+    long long steps = (plan.tiles - pair + plan.pairs - 1) / plan.pairs * blocks;
+    if (MODE != kMmWhole) {
+        const long long u0 = MODE == kMmCluster ? plan.part_begin(pair) : plan.begin(pair);
+        steps = (MODE == kMmCluster ? plan.part_begin(pair + 1) : plan.begin(pair + 1)) - u0;
+        first_tile = (int)(u0 / blocks);
+        first_b = (int)(u0 - (long long)first_tile * blocks);
+    }
+    const int turn = MODE == kMmWhole ? plan.pairs : 1;    // from one tile to the next
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
@@ -583,8 +592,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             const uint32_t base = smem_addr(smem), bars = cluster_addr(smem_addr(full), leader);
             uint64_t(&last)[C::STAGES] = done[TWO ? 1 : 0];
             const bool lead = elect_one();
-            long long left = u1 - u0;
-            for (int tile = first_tile, b = first_b; ok && left > 0; ++tile, b = 0) {
+            long long left = steps;
+            for (int tile = first_tile, b = first_b; ok && left > 0; tile += turn, b = 0) {
                 const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
                 // (a product's columns are half the first CTA's weight rows, half the second's)
                 const int n0 = tn * W + (int)rank * (TWO ? H / 2 : H);
@@ -625,7 +634,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             bool ok = true, ready = false;
             // (a barrier's phase before its first counts as complete: no step waits for an accumulator that
             // nothing has used)
-            for (long long left = u1 - u0; left > 0; --left, ++it) {
+            for (long long left = steps; left > 0; --left, ++it) {
                 if (!ready) {
                     ok = wait_warp(&full[s], phase, limit) && wait_warp(&t_empty[0][t], t_phase ^ 1, limit);
                     if (!ok) break;
@@ -681,8 +690,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             // step up by 600 to 700 cycles.)
             unsigned gi = 0;
             bool ok = true;
-            long long left = u1 - u0;
-            for (int tile = first_tile, at = first_b; ok && left > 0; ++tile, at = 0) {
+            long long left = steps;
+            for (int tile = first_tile, at = first_b; ok && left > 0; tile += turn, at = 0) {
                 const int end = (int)min((long long)blocks, at + left);
                 left -= end - at;
                 const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
@@ -724,7 +733,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), leader);
         unsigned gi = 0, s = 0, phase = 0, t = 0, stored = 0;
         bool ok = true;
-        long long left = u1 - u0;
+        long long left = steps;
         float acc[C::COLS];
         auto output = [&](int tile) {
             const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128 + quad * 32;
@@ -791,7 +800,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 }
             }
         };
-        for (int tile = first_tile, at = first_b; left > 0; ++tile, at = 0) {
+        for (int tile = first_tile, at = first_b; left > 0; tile += turn, at = 0) {
             const int end = (int)min((long long)blocks, at + left);
             left -= end - at;
             const int n0 = tile / tiles_m * W + part * H;

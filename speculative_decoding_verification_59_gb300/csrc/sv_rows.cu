@@ -57,8 +57,12 @@ __device__ __forceinline__ float top8(const float (&x)[8]) {
 }
 __device__ __forceinline__ void store8_e4m3(char* p, int64_t i, float top, const float (&x)[8]) {
     const float f = kFp8Max / top;
-    *reinterpret_cast<uint2*>(p + i * 8) = make_uint2(pack_e4m3(x[0] * f, x[1] * f) | pack_e4m3(x[2] * f, x[3] * f) << 16,
-                                                     pack_e4m3(x[4] * f, x[5] * f) | pack_e4m3(x[6] * f, x[7] * f) << 16);
+    const f32x2 f2 = f2_pack(f, f);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) f2_unpack(f2_mul(f2_pack(x[j], x[j + 1]), f2), y[j], y[j + 1]);
+    *reinterpret_cast<uint2*>(p + i * 8) =
+        make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16, pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
 }
 // Vector i of an output to 8 bits; all 16 lanes of a block take part, those without a vector
 // (have false) with x all zero.  The block's largest magnitude.
@@ -101,19 +105,25 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out
             q[j].get(r);
             if (a.res) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[j][e] += r[e];
+                for (int e = 0; e < 8; e += 2)
+                    f2_unpack(f2_add(f2_pack(h[j][e], h[j][e + 1]), f2_pack(r[e], r[e + 1])), h[j][e], h[j][e + 1]);
             }
         }
     };
-    float ss = 0.f;
+    f32x2 pair = 0;
     for (int v0 = in_row; v0 < (MORE ? nv : tpr); v0 += VPT * tpr) {
         fetch(v0);
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
+            for (int e = 0; e < 8; e += 2) {
+                const f32x2 x2 = f2_pack(h[j][e], h[j][e + 1]);
+                pair = f2_fma(x2, x2, pair);
+            }
     }
-    ss = warp_sum(ss);
+    float ss, odd;
+    f2_unpack(pair, ss, odd);
+    ss = warp_sum(ss + odd);
     if (tpr > 32) {
         if ((threadIdx.x & 31) == 0) part[warp] = ss;
         __syncthreads();
@@ -130,14 +140,13 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out
             const int v = v0 + j * tpr;
             const bool have = live && v < nv;
             if (have && a.sum) store8(sum, v, SF, h[j]);
-            float y[8];
+            float y[8], w[8];
+            if (a.w) unpack8(have ? *(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u), w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = h[j][e] * inv;
-            if (have && a.w) {
-                float w[8];
-                unpack8(*(reinterpret_cast<const uint4*>(a.w) + v), w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= w[e];
+            for (int e = 0; e < 8; e += 2) {
+                f32x2 y2 = f2_mul(f2_pack(h[j][e], h[j][e + 1]), f2_pack(inv, inv));
+                if (a.w) y2 = f2_mul(y2, f2_pack(w[e], w[e + 1]));
+                f2_unpack(y2, y[e], y[e + 1]);
             }
             if (out == SPEC_DTYPE_E4M3) {
                 const float m = put_e4m3(a.out, row * nv + v, have, y);
@@ -177,18 +186,39 @@ cudaError_t launch_add_norm(const NormArgs& a, spec_dtype_t x, spec_dtype_t sum,
 
 // ---- gated activation, rounding of rows ----------------------------------------------
 // x / (1 + e^-x); the tanh form of GELU is x over 1 + e^(-2u), u = sqrt(2 / pi) (x + 0.044715 x^3),
-// since (1 + tanh u) / 2 = 1 / (1 + e^(-2u)).
-__device__ __forceinline__ float activate(float x, int act) {
-    const float t = act == SPEC_ACT_SILU ? x : 1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.f);
-    return __fdividef(x, 1.f + __expf(-t));
+// since (1 + tanh u) / 2 = 1 / (1 + e^(-2u)).  Power and reciprocal are the special-function unit's
+// (2 and 1 units in the last place); past e^88 the reciprocal is zero, and so is the result.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// act(x) y, pairwise.
+template <int ACT>
+__device__ __forceinline__ void gate8(float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const f32x2 v = f2_pack(x[j], x[j + 1]);
+        f32x2 t = f2_mul(v, f2_pack(-1.4426950408889634f, -1.4426950408889634f));       // -log2 e
+        if constexpr (ACT == SPEC_ACT_GELU_TANH) {
+            // -2 sqrt(2 / pi) log2 e (x + 0.044715 x^3)
+            const f32x2 c = f2_fma(f2_mul(v, v), f2_pack(0.044715f, 0.044715f), f2_pack(1.f, 1.f));
+            t = f2_mul(f2_mul(v, c), f2_pack(-2.3022081986f, -2.3022081986f));
+        }
+        float a, b;
+        f2_unpack(t, a, b);
+        f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_pack(1.f, 1.f)), a, b);
+        f2_unpack(f2_mul(f2_mul(v, f2_pack(rcp_approx(a), rcp_approx(b))), f2_pack(y[j], y[j + 1])), x[j], x[j + 1]);
+    }
 }
 
 // A CTA takes RT rows and, 16 lanes a block, 16 / RT blocks of them at a time, V times.  Many rows: 16
 // rows of one block, whose scales then leave together in one line (a scale of 4 bytes by itself
 // costs a sector: 39.4 us for 33 at 16384 rows of 4096).
 constexpr int kActThreads = 256;
-template <bool F32, bool GATED, int RT, int V>
+template <bool F32, int ACT, int RT, int V>
 __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int out, int chunks) {
+    constexpr bool GATED = ACT != kActNone;
     constexpr int BT = 16 / RT;                           // blocks at a time
     __shared__ float top[RT > 1 ? V : 1][16];
     pdl_trigger();
@@ -214,8 +244,7 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int o
         if (GATED) {
             float y[8];
             u[k].get(y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], a.act) * y[e];
+            gate8<ACT>(x, y);
         }
         if (out == SPEC_DTYPE_E4M3) {
             const float m = put_e4m3(a.out, row * nv + v, have, x);
@@ -237,16 +266,16 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int o
     }
 }
 
-template <bool F32, bool GATED>
+template <bool F32, int ACT>
 static cudaError_t launch_act_t(const ActArgs& a, int out, int sms, cudaStream_t st) {
     // 16 rows and four blocks of them a CTA where that gives every SM one, else a row's blocks side by side
     const long long blocks = scale_blocks(a.dim), groups = ((long long)a.rows + 15) / 16;
     if ((blocks + 3) / 4 * groups >= sms) {
         const long long chunks = (blocks + 3) / 4;
-        return launch_pdl(act_kernel<F32, GATED, 16, 4>, dim3((unsigned)(chunks * groups)), kActThreads, 0, st, a, out, (int)chunks);
+        return launch_pdl(act_kernel<F32, ACT, 16, 4>, dim3((unsigned)(chunks * groups)), kActThreads, 0, st, a, out, (int)chunks);
     }
     const long long chunks = (blocks + 15) / 16;
-    return launch_pdl(act_kernel<F32, GATED, 1, 1>, dim3((unsigned)(chunks * a.rows)), kActThreads, 0, st, a, out, (int)chunks);
+    return launch_pdl(act_kernel<F32, ACT, 1, 1>, dim3((unsigned)(chunks * a.rows)), kActThreads, 0, st, a, out, (int)chunks);
 }
 
 cudaError_t launch_act(const ActArgs& a, spec_dtype_t in, spec_dtype_t out, cudaStream_t st) {
@@ -254,15 +283,22 @@ cudaError_t launch_act(const ActArgs& a, spec_dtype_t in, spec_dtype_t out, cuda
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
     const int sms = di.sm_count;
-    if (in == SPEC_DTYPE_F32) return a.up ? launch_act_t<true, true>(a, (int)out, sms, st) : launch_act_t<true, false>(a, (int)out, sms, st);
-    return a.up ? launch_act_t<false, true>(a, (int)out, sms, st) : launch_act_t<false, false>(a, (int)out, sms, st);
+    const int o = (int)out;
+    if (in == SPEC_DTYPE_F32)
+        return a.act == SPEC_ACT_SILU        ? launch_act_t<true, SPEC_ACT_SILU>(a, o, sms, st)
+               : a.act == SPEC_ACT_GELU_TANH ? launch_act_t<true, SPEC_ACT_GELU_TANH>(a, o, sms, st)
+                                             : launch_act_t<true, kActNone>(a, o, sms, st);
+    return a.act == SPEC_ACT_SILU        ? launch_act_t<false, SPEC_ACT_SILU>(a, o, sms, st)
+           : a.act == SPEC_ACT_GELU_TANH ? launch_act_t<false, SPEC_ACT_GELU_TANH>(a, o, sms, st)
+                                         : launch_act_t<false, kActNone>(a, o, sms, st);
 }
 
 // ---- rounding of weights -------------------------------------------------------------
-// A CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.  (Two blocks side by side, so that rows
-// are read 512 bytes at a time: 64.3 us for 55.7 at 24576 x 4096; 512 threads a block: 57.9.)
+// A CTA a block of 128 x 128: 16 lanes a row, 16 rows at a time.  24576 x 4096 bf16: 45.5 us, 6.6 TB/s,
+// with four CTAs an SM; 55 with the two that more registers leave; two blocks side by side, so that
+// rows are read 512 bytes at a time: 64.
 template <bool F32>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const TileQuantArgs a, int tiles_n) {
+__global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_tiles_kernel(const TileQuantArgs a, int tiles_n) {
     constexpr int VECTORS = 8, STEP = 16;
     __shared__ float part[8];
     pdl_trigger();
