@@ -541,8 +541,8 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
  *            i * scale_stride + b
  *
  * Rows of x, gate, up and the residual: row r at r * stride elements, 16-byte
- * aligned, strides multiples of 16 bytes (SPEC_ERR_MISALIGNED otherwise), bf16 or
- * fp32.  Outputs `out`: contiguous rows of dim elements, bf16, fp32 or e4m3 (then
+ * aligned, strides multiples of 16 bytes (SPEC_ERR_MISALIGNED otherwise; 0 for one row
+ * that all share), bf16 or fp32.  Outputs `out`: contiguous rows of dim elements, bf16, fp32 or e4m3 (then
  * out_scale is needed, with scale_stride >= rows, 0 for one row or one block).  dim is a multiple of 8, of 16
  * for an e4m3 output.  rows * (dim rounded up to 128) < 2^34.  Arithmetic is fp32,
  * each output rounded once.  An output may not overlap an input except as said.
@@ -552,8 +552,9 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
  * The residual's addition and the root-mean-square norm of its sum:
  *   h = x + residual (NULL: h = x),   sum_out = h in sum_dtype (nullable),
  *   out = h * rsqrt(mean(h^2) + eps) * weight      (h before its rounding; weight NULL: 1)
- *   residual, sum_out  of sum_dtype, strides of their own; sum_out may be the residual, or x of
- *                      that type, itself (same stride): the residual stream in place
+ *   residual, sum_out  of sum_dtype, strides of their own, sum_out's at least dim; sum_out may be
+ *                      the residual, or x of that type, itself (same stride): the residual
+ *                      stream in place
  *   weight             [dim] bf16, 16-byte aligned, nullable
  */
 spec_status_t spec_add_norm(const void* x, spec_dtype_t x_dtype, int64_t x_stride,

@@ -1,6 +1,7 @@
 // The C ABI of the target model's dense side: argument validation and
 // dispatch.  Declarations and contracts are in include/spec_verify.h.
 #include <math.h>
+#include <stdlib.h>
 
 #include "sv_linear.h"
 
@@ -45,6 +46,7 @@ spec_status_t spec_add_norm(const void* x, spec_dtype_t x_dtype, int64_t x_strid
     if (!row_aligned(x, x_dtype, x_stride) || (residual && !row_aligned(residual, sum_dtype, residual_stride)) ||
         (sum_out && !row_aligned(sum_out, sum_dtype, sum_stride)) || !is_aligned(weight, 16))
         return SPEC_ERR_MISALIGNED;
+    if (sum_out && rows > 1 && llabs(sum_stride) < dim) return SPEC_ERR_INVALID_ARG;       // rows of it that overlap
     NormArgs a = {};
     a.x = static_cast<const char*>(x);
     a.res = static_cast<const char*>(residual);

@@ -470,19 +470,21 @@ struct Flat {
     c10::IntArrayRef lead;
     at::ScalarType type = at::kByte;
 };
-// The one stride of t's dimensions but the last, taken as rows; that of packed rows where
-// there is one row only.
+// The one stride of t's dimensions but the last, taken as rows (0: all are one row, expanded); that of
+// packed rows where there is one row only.
 int64_t row_stride(const at::Tensor& t, const char* name, int64_t of_one) {
-    int64_t stride = 0, next = 0;
+    int64_t stride = of_one, next = 0;
+    bool found = false;
     for (int64_t d = t.dim() - 2; d >= 0; --d) {
         if (t.size(d) == 1) continue;
-        if (stride == 0) stride = t.stride(d);
+        if (!found) stride = t.stride(d);
         else if (t.stride(d) != next)
             throw PyFail{PyExc_ValueError, std::string(name) + ": rows must lie one stride apart, got strides " + shape_text(t.strides()) +
                                                " of shape " + shape_text(t.sizes())};
+        found = true;
         next = t.stride(d) * t.size(d);
     }
-    return stride == 0 ? of_one : stride;
+    return stride;
 }
 Flat flat_of(PyObject* o, const char* name, int device) {
     const at::Tensor& t = *tensor_of(o, name);

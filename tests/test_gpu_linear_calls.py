@@ -225,3 +225,32 @@ def test_captured_products(sv, M, N, K):
         held.fill_(-1)
         graph.replay()
         assert torch.equal(held, want[turn % 2]), turn
+
+
+@pytest.mark.parametrize("lead,strides", [((5,), (0,)), ((4, 3), (0, 0)), ((4, 3), (256, 0)), ((4, 3), (0, 256))])
+def test_expanded_rows(sv, lead, strides):
+    """One row in place of many: read as such, refused where rows lie otherwise than one stride apart, as an output and by
+    the product, which takes rows of their own."""
+    store = torch.randn((64, 256), device="cuda").to(torch.bfloat16)
+    x = store.as_strided(lead + (256,), strides + (1,))
+    shared = not any(strides)
+    for call in (lambda t: sv.add_norm(t, None, t), lambda t: sv.gated_act(t), lambda t: sv.quantize_e4m3(t)):
+        if shared:
+            assert all(torch.equal(a, b) for a, b in zip(call(x), call(x.contiguous())))
+        else:
+            with pytest.raises(ValueError, match="one stride apart"):
+                call(x)
+    with pytest.raises((ValueError, sv.SpecVerifyError)):
+        sv.add_norm(x.contiguous(), None, x.contiguous(), sum_out=x)
+    q, s = sv.quantize_e4m3(x.contiguous())
+    w, ws = sv.quantize_e4m3(store, block_rows=128)
+    q1, s1 = sv.quantize_e4m3(store)
+    q1 = q1.as_strided(lead + (256,), strides + (1,))
+    s1 = s1.as_strided(lead + (2,), tuple(d // 256 for d in strides) + (s1.stride(-1),))
+    for a, b in ((q1, s), (q, s1)):
+        with pytest.raises((ValueError, sv.SpecVerifyError)):
+            sv.matmul_e4m3(a, b, w, ws)
+    with pytest.raises((ValueError, sv.SpecVerifyError)):
+        sv.matmul_e4m3(q, s, w[:1], ws, out=store.as_strided(lead + (1,), strides + (1,)))
+    with pytest.raises((ValueError, sv.SpecVerifyError)):
+        sv.matmul_e4m3(q, s, q1[0, :1].expand(8, 256) if q1.dim() == 3 else q1[:1].expand(8, 256), ws)

@@ -53,6 +53,7 @@ def matmul(**kw):
     (dict(x=FAKE + 2), ALIGN), (dict(xs=260), ALIGN), (dict(xt=F32, xs=258), ALIGN), (dict(res=FAKE + 8), ALIGN),
     (dict(rs=257), ALIGN), (dict(sum=FAKE + 4), ALIGN), (dict(ss=4), ALIGN), (dict(w=FAKE + 2), ALIGN), (dict(dim=252), ALIGN),
     (dict(ot=E4M3, scale=FAKE, pitch=4, dim=248), ALIGN), (dict(out=FAKE + 8), ALIGN), (dict(ot=E4M3, scale=FAKE + 2, pitch=4), ALIGN),
+    (dict(ss=248), INVALID), (dict(ss=0), INVALID), (dict(ss=-128), INVALID),           # rows of the sum that overlap
     (dict(rows=0), sv.SPEC_OK), (dict(rows=0, x=None, out=None), sv.SPEC_OK)])
 def test_add_norm_refusals(kw, want):
     assert norm(**kw) == want
