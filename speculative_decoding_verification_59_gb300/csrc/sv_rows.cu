@@ -55,8 +55,8 @@ __device__ __forceinline__ float top8(const float (&x)[8]) {
     for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
     return m;
 }
-__device__ __forceinline__ void store8_e4m3(char* p, int64_t i, float top, const float (&x)[8]) {
-    const float f = kFp8Max / top;
+// x f, rounded.
+__device__ __forceinline__ void store8_e4m3(char* p, int64_t i, float f, const float (&x)[8]) {
     const f32x2 f2 = f2_pack(f, f);
     float y[8];
 #pragma unroll
@@ -65,21 +65,32 @@ __device__ __forceinline__ void store8_e4m3(char* p, int64_t i, float top, const
         make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16, pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
 }
 // Vector i of an output to 8 bits; all 16 lanes of a block take part, those without a vector
-// (have false) with x all zero.  The block's largest magnitude.
-__device__ __forceinline__ float put_e4m3(char* out, int64_t i, bool have, const float (&x)[8]) {
+// (have false) with x all zero.  The block's largest magnitude.  SCALED: of x `times`, a factor of the whole
+// row, which the scale takes up: q is rounded from x, not from a product rounded before.
+template <bool SCALED>
+__device__ __forceinline__ float put_e4m3(char* out, int64_t i, bool have, const float (&x)[8], float times) {
     float m = top8(x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = fmaxf(m, kFp8AmaxFloor);
-    if (have) store8_e4m3(out, i, m, x);
-    return m;
+    if (!SCALED) {
+        m = fmaxf(m, kFp8AmaxFloor);
+        if (have) store8_e4m3(out, i, kFp8Max / m, x);
+        return m;
+    }
+    const float top = m * times;
+    const bool above = top > kFp8AmaxFloor;
+    if (have) store8_e4m3(out, i, kFp8Max / (above ? m : kFp8AmaxFloor) * (above ? 1.f : times), x);
+    return above ? top : kFp8AmaxFloor;
 }
 
 // ---- residual and norm ---------------------------------------------------------------
 // A row is a group of TPR threads, VPT vectors each, held in registers between the
-// two uses.  MORE: longer rows, read once more for the second (from L2, mostly).
-template <bool XF, bool SF, int VPT, bool MORE>
-__global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out, int tpr) {
+// two uses.  MORE: longer rows, read once more for the second (from L2, mostly).  WIDE: rows of 512
+// threads, and registers for two of them on an SM, so that one's loads cover the other's sums (2000 rows
+// of 12000 to e4m3: 39 us for 54; rows of 4096, several a CTA, 42.0 for 43.2 to e4m3, but 65.4 for 62.4
+// with an fp32 residual).
+template <bool XF, bool SF, int VPT, bool WIDE, bool MORE>
+__global__ void __launch_bounds__(512, VPT == 4 && (WIDE || !(XF || SF)) ? 2 : 1) add_norm_kernel(const NormArgs a, int out, int tpr) {
     __shared__ float part[16];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, in_row = threadIdx.x & (tpr - 1), nv = a.dim / 8;
@@ -132,6 +143,7 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out
         for (int i = 0; i < tpr / 32; ++i) ss += part[first + i];
     }
     const float inv = rsqrtf(ss / (float)a.dim + a.eps);
+    const bool fp8 = out == SPEC_DTYPE_E4M3;
     // (all lanes stay: a block's 16 find its largest element together)
     for (int v0 = in_row; v0 - in_row < (MORE ? nv : 1); v0 += VPT * tpr) {
         if (MORE) fetch(v0);
@@ -144,12 +156,13 @@ __global__ void __launch_bounds__(512) add_norm_kernel(const NormArgs a, int out
             if (a.w) unpack8(have ? *(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u), w);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                f32x2 y2 = f2_mul(f2_pack(h[j][e], h[j][e + 1]), f2_pack(inv, inv));
+                f32x2 y2 = f2_pack(h[j][e], h[j][e + 1]);
+                if (!fp8) y2 = f2_mul(y2, f2_pack(inv, inv));
                 if (a.w) y2 = f2_mul(y2, f2_pack(w[e], w[e + 1]));
                 f2_unpack(y2, y[e], y[e + 1]);
             }
-            if (out == SPEC_DTYPE_E4M3) {
-                const float m = put_e4m3(a.out, row * nv + v, have, y);
+            if (fp8) {
+                const float m = put_e4m3<true>(a.out, row * nv + v, have, y, inv);
                 if (have && (v & 15) == 0) a.scale[(v >> 4) * a.scale_stride + row] = m / kFp8Max;
             } else if (have) store8(a.out, row * nv + v, out == SPEC_DTYPE_F32, y);
         }
@@ -169,10 +182,11 @@ static cudaError_t launch_add_norm_t(const NormArgs& a, int out, int sms, cudaSt
     while (tpr < 512 && tpr * vpt < nv) tpr *= 2;
     const int threads = tpr < 128 ? 128 : tpr;
     const dim3 grid((unsigned)(((long long)a.rows + threads / tpr - 1) / (threads / tpr)));
-    if (nv > 512 * 4) return launch_pdl(add_norm_kernel<XF, SF, 4, true>, grid, threads, 0, st, a, out, tpr);
-    if (vpt == 1) return launch_pdl(add_norm_kernel<XF, SF, 1, false>, grid, threads, 0, st, a, out, tpr);
-    if (vpt == 2) return launch_pdl(add_norm_kernel<XF, SF, 2, false>, grid, threads, 0, st, a, out, tpr);
-    return launch_pdl(add_norm_kernel<XF, SF, 4, false>, grid, threads, 0, st, a, out, tpr);
+    if (nv > 512 * 4) return launch_pdl(add_norm_kernel<XF, SF, 4, true, true>, grid, threads, 0, st, a, out, tpr);
+    if (vpt == 1) return launch_pdl(add_norm_kernel<XF, SF, 1, false, false>, grid, threads, 0, st, a, out, tpr);
+    if (vpt == 2) return launch_pdl(add_norm_kernel<XF, SF, 2, false, false>, grid, threads, 0, st, a, out, tpr);
+    if (tpr == 512) return launch_pdl(add_norm_kernel<XF, SF, 4, true, false>, grid, threads, 0, st, a, out, tpr);
+    return launch_pdl(add_norm_kernel<XF, SF, 4, false, false>, grid, threads, 0, st, a, out, tpr);
 }
 
 cudaError_t launch_add_norm(const NormArgs& a, spec_dtype_t x, spec_dtype_t sum, spec_dtype_t out, cudaStream_t st) {
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int o
             gate8<ACT>(x, y);
         }
         if (out == SPEC_DTYPE_E4M3) {
-            const float m = put_e4m3(a.out, row * nv + v, have, x);
+            const float m = put_e4m3<false>(a.out, row * nv + v, have, x, 1.f);
             if (RT > 1) {
                 if ((threadIdx.x & 15) == 0) top[RT > 1 ? k : 0][slot] = m;
             } else if ((threadIdx.x & 15) == 0 && have) {
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_tiles_kernel(const 
     for (int k = 0; k < VECTORS; ++k) {
         float y[8];
         x[k].get(y);
-        if (v < nv && r0 + STEP * k < a.rows) store8_e4m3(a.out, (int64_t)(r0 + STEP * k) * nv + v, m, y);
+        if (v < nv && r0 + STEP * k < a.rows) store8_e4m3(a.out, (int64_t)(r0 + STEP * k) * nv + v, kFp8Max / m, y);
     }
     if (threadIdx.x == 0) a.scale[(int64_t)ti * a.scale_stride + tb] = m / kFp8Max;
 }

@@ -95,6 +95,24 @@ def test_add_norm_zero_rows_and_odd_values(sv):
 
 
 # ---- gated activation, rounding ----------------------------------------------------------
+@pytest.mark.parametrize("weighted", [False, True])
+def test_add_norm_to_8_bits_small_blocks_and_odd_values(sv, weighted):
+    """Blocks under the least scale, and what is not finite, beside ordinary ones."""
+    g = gen(7)
+    x = torch.randn((5, 640), generator=g, device="cuda")
+    x[:, 128:256] *= 1e-21
+    x[:, 256:384] *= 3e-23
+    x[:, 384:512] = 0
+    w = (torch.rand(640, generator=g, device="cuda") + 0.5).to(torch.bfloat16) if weighted else None
+    R.check_e4m3(*sv.add_norm(x, w, e4m3=True), R.norm(x, w, None, 1e-6)[0], slack=2.0 ** -18)
+    want = sv.add_norm(x, w, e4m3=True)
+    x[1, 5], x[3, 630] = float("inf"), float("nan")
+    q, sc = sv.add_norm(x, w, e4m3=True)
+    ok = [0, 2, 4]
+    assert torch.equal(q[ok].float(), want[0][ok].float()) and torch.equal(sc[ok], want[1][ok])
+    assert q[3].float().isnan().all() and q[1, 5].float().isnan() and (q[1].float().nan_to_num() == 0).all()
+
+
 @pytest.mark.parametrize("rows,dim", [(1, 16), (7, 64), (3, 144), (33, 1008), (7, 12288), (129, 2048)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
 @pytest.mark.parametrize("xt", ["bfloat16", "float32"])
@@ -176,6 +194,13 @@ def test_matmul(sv, M, N, K):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_matmul_large(sv, M, N, K, dtype):
     check(sv, N, M, N, K, dtype)
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 64, 128), (70, 64, 400), (100, 130, 1168), (257, 500, 1680), (300, 200, 2000), (300, 1900, 5200),
+                                   (600, 1000, 16400), (520, 4700, 1296), (1152, 2000, 9008), (90, 4800, 1040)])
+def test_matmul_odd_numbers_of_blocks(sv, M, N, K):
+    """Steps of two blocks, parts of tiles and clusters whose blocks come out odd."""
+    check(sv, M + N, M, N, K, torch.float32)
 
 
 @pytest.mark.parametrize("M", [5, 120, 140])
