@@ -141,22 +141,6 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, unsigned short both) 
                  "h"(both)
                  : "memory");
 }
-// 32 columns of the warp's 32 lanes; nothing may use v before tc_wait_ld and ld32_done.
-__device__ __forceinline__ void tc_ld32_start(uint32_t at, float* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-          "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
-          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(at));
-}
-__device__ __forceinline__ void tc_ld32_done(float* v) {
-    tc_ld16_done(v);
-    tc_ld16_done(v + 16);
-}
-
 // ---- few rows ----------------------------------------------------------------------
 // Up to 64 rows of x: the product is taken transposed, so that 128 weight rows are the
 // rows that the instruction wants and the few rows of x its free dimension T.  The weights are
@@ -513,13 +497,15 @@ struct ManyCfg {
 // Whether the halves of a tile's columns are products of their own (a pair's product has a
 // multiple of 32 columns); stages of a ring; accumulators (of a half, where there are two).
 __host__ __device__ constexpr bool two_halves(int W) { return W > 128 && W % 64 == 0; }
+// Blocks of the contraction in a step, each with its accumulator: handing a step to the sums takes their warps
+// some 300 cycles besides its columns, which 64 columns are not worth (a block of theirs 0.15 us, 0.21 alone;
+// of 128 columns 0.245 alone, 0.255 by twos, whose stages are fewer).
+__host__ __device__ constexpr int blocks_of(int W) { return W == 64 ? 2 : 1; }
+__host__ __device__ constexpr unsigned least(unsigned a, unsigned b) { return a < b ? a : b; }
 __host__ __device__ constexpr unsigned stages_of(int W) {
-    return ManyCfg::OUT_AT / (ManyCfg::X_BYTES + W / 2 * kMmTile) < ManyCfg::STAGES ? ManyCfg::OUT_AT / (ManyCfg::X_BYTES + W / 2 * kMmTile)
-                                                                                     : ManyCfg::STAGES;
+    return least(ManyCfg::OUT_AT / (blocks_of(W) * (ManyCfg::X_BYTES + W / 2 * kMmTile)), ManyCfg::STAGES);
 }
-__host__ __device__ constexpr unsigned buffers_of(int W) {
-    return 512 / W < ManyCfg::NB ? 512 / W : ManyCfg::NB;
-}
+__host__ __device__ constexpr unsigned buffers_of(int W) { return least(512 / (blocks_of(W) * W), ManyCfg::NB); }
 enum MmMode { kMmWhole, kMmTickets, kMmCluster };
 template <int W, MmMode MODE>
 __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const MatmulArgs a, uint32_t limit, const MmPlan plan,
@@ -531,8 +517,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     constexpr int H = W / 2;
     constexpr bool CROSS = kScaleBlock % H != 0;           // a half's columns may lie in two blocks of the weights
     static_assert(H % 32 == 0 && H <= ManyCfg::COLS, "whole pieces of the output");
+    // Whether the sums ask for the next step's products ahead (1152 x 4096 x 12288, in shares: 58.5 us for 60.5;
+    // whole tiles with halves, bound by power: 239 for 236 at 512 x 151936 x 4096).
+    constexpr bool PEEK = !TWO || MODE == kMmTickets;
+    constexpr int BP = blocks_of(W);
     constexpr unsigned stages = stages_of(W), buffers = buffers_of(W);
-    constexpr uint32_t stage_bytes = C::X_BYTES + H * kMmTile;
+    constexpr uint32_t block_bytes = C::X_BYTES + H * kMmTile, stage_bytes = BP * block_bytes;
+    static_assert(BP == 1 || !TWO, "a step's accumulators");
     extern __shared__ unsigned char smem_raw[];
     // done: a step's products (of a half) are complete; after the second half's its stage is free.  (As
     // many as stages: an accumulator's next product waits for the sums, a stage's next load for done, so
@@ -597,7 +588,9 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
                 // (a product's columns are half the first CTA's weight rows, half the second's)
                 const int n0 = tn * W + (int)rank * (TWO ? H / 2 : H);
-                for (; b < blocks && left > 0; ++b, ++it, --left) {
+                const int end = (int)min((long long)blocks, b + left);
+                left -= end - b;
+                for (; b < end; b += BP, ++it) {
                     if (it >= stages && !free) {
                         ok = wait_warp(&last[s], phase ^ 1, limit);
                         if (!ok) break;
@@ -610,10 +603,16 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     }
                     free = phase_done(&last[s], phase ^ 1);
                     if (lead) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[now], 2 * stage_bytes);
-                        tma_2d_pair(at, &xmap, b * kMmTile, m0, bar);
-                        tma_2d_pair(at + C::X_BYTES, &wmap, b * kMmTile, n0, bar);
-                        if constexpr (TWO) tma_2d_pair(at + C::X_BYTES + H / 2 * kMmTile, &wmap, b * kMmTile, n0 + H, bar);
+                        const bool all = b + BP <= end;    // (else the step has one block of two)
+                        if (rank == 0) mbar_arrive_expect_tx(&full[now], all ? 2 * stage_bytes : 2 * block_bytes);
+#pragma unroll
+                        for (int k = 0; k < BP; ++k) {
+                            if (k > 0 && !all) break;
+                            const uint32_t to = at + k * block_bytes;
+                            tma_2d_pair(to, &xmap, (b + k) * kMmTile, m0, bar);
+                            tma_2d_pair(to + C::X_BYTES, &wmap, (b + k) * kMmTile, n0, bar);
+                            if constexpr (TWO) tma_2d_pair(to + C::X_BYTES + H / 2 * kMmTile, &wmap, (b + k) * kMmTile, n0 + H, bar);
+                        }
                     }
                     free = __all_sync(0xffffffffu, free);
                 }
@@ -634,14 +633,21 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             bool ok = true, ready = false;
             // (a barrier's phase before its first counts as complete: no step waits for an accumulator that
             // nothing has used)
-            for (long long left = steps; left > 0; --left, ++it) {
+            int b = first_b, end = (int)min((long long)blocks, b + steps);
+            for (long long left = steps; left > 0; ++it) {
+                const int n = BP == 1 ? 1 : min(BP, end - b);      // blocks of the step
+                left -= n;
+                if constexpr (BP > 1) {
+                    b += n;
+                    if (b == end) b = 0, end = (int)min((long long)blocks, left);
+                }
                 if (!ready) {
                     ok = wait_warp(&full[s], phase, limit) && wait_warp(&t_empty[0][t], t_phase ^ 1, limit);
                     if (!ok) break;
                 }
                 tc_after();
                 const uint64_t xd = base + s * (stage_bytes >> 4), wd = xd + (C::X_BYTES >> 4);
-                const uint32_t to = tmem + t * (TWO ? H : W);
+                const uint32_t to = tmem + t * (TWO ? H : BP * W);
                 const unsigned now = s;
                 if constexpr (TWO) {
                     const bool second = phase_done(&t_empty[1][t], t_phase ^ 1);
@@ -672,6 +678,11 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     const uint64_t wd2 = TWO ? wd + (H / 2 * kMmTile >> 4) : wd;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) pair_mma(to + (TWO ? 256 : 0), xd + 2 * k, wd2 + 2 * k, id, k > 0);
+                    if (BP > 1 && n > 1) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            pair_mma(to + W, xd + (block_bytes >> 4) + 2 * k, wd + (block_bytes >> 4) + 2 * k, id, k > 0);
+                    }
                     pair_commit(&done[TWO ? 1 : 0][now], both);
                 }
                 ready = __all_sync(0xffffffffu, next);
@@ -726,13 +737,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE));
         const int part = (warp - 4) >> 2, quad = warp & 3, half = TWO ? part : 0;
-        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (TWO ? part * 256 : part * H), step = TWO ? H : W;
+        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (TWO ? part * 256 : part * H), step = TWO ? H : BP * W;
         // (a cluster's sums lie in the output's place, its output in the ring's, which is free then)
         unsigned char* const pieces = smem + (MODE == kMmCluster ? 0 : C::OUT_AT) + (warp - 4) * 4096;
         static_assert(MODE != kMmCluster || W == 64, "a warp's sums fit its 4 KB");
         const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), leader);
         unsigned gi = 0, s = 0, phase = 0, t = 0, stored = 0;
-        bool ok = true;
+        bool ok = true, there = false;
         long long left = steps;
         float acc[C::COLS];
         auto output = [&](int tile) {
@@ -819,37 +830,44 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 // the group before has been taken; this one may still be on its way from shared memory
                 if (lane == 0 && gi > 0) mbar_arrive(&f_empty[(gi - 1) % C::FS]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; j += BP) {
                     if (!ok || b4 + j >= end) continue;
-                    ok = wait_warp(&done[half][s], phase, limit);
+                    if (!PEEK || !there) ok = wait_warp(&done[half][s], phase, limit);
                     if (!ok) continue;
                     tc_after();
                     constexpr int L = 16;                  // columns a load
+                    const uint32_t at_ = from + t * step;
+                    const bool all = b4 + j + BP <= end;
                     float v[2][L];
-                    tc_ld16_start(from + t * step, v[0]);
-#pragma unroll
-                    for (int c = 0; c < C::COLS; c += L) {
-                        if (c >= H) break;
-                        float* now = v[(c / L) & 1];
-                        tc_wait_ld();
-                        tc_ld16_done(now);
-                        if (c + L < H) {
-                            tc_ld16_start(from + t * step + c + L, v[(c / L + 1) & 1]);
-                        } else {
-                            tc_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
-                        }
-                        const float fg = !CROSS || c < split ? f[j] : g[j];
-#pragma unroll
-                        for (int e = 0; e < L; e += 2)
-                            f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(acc[c + e], acc[c + e + 1])),
-                                      acc[c + e], acc[c + e + 1]);
-                    }
+                    tc_ld16_start(at_, v[0]);
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1;
                     }
+#pragma unroll
+                    for (int c = 0; c < BP * H; c += L) {
+                        if (BP > 1 && c == H && !all) break;
+                        float* now = v[(c / L) & 1];
+                        tc_wait_ld();
+                        tc_ld16_done(now);
+                        const int next = c + L;
+                        if (next < BP * H && (next != H || all)) {
+                            tc_ld16_start(at_ + next / H * W + next % H, v[(next / L) & 1]);
+                        } else {
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(t_free + t * 8);
+                            // (the next step's products: the answer comes while the last sums are made)
+                            if (PEEK) there = phase_done(&done[half][s], phase);
+                        }
+                        const float fg = !CROSS || c < split ? f[j + c / H] : g[j];
+#pragma unroll
+                        for (int e = 0; e < L; e += 2) {
+                            float* to = acc + c % H + e;
+                            f2_unpack(f2_fma(f2_pack(now[e], now[e + 1]), f2_pack(fg, fg), f2_pack(to[0], to[1])), to[0], to[1]);
+                        }
+                    }
+                    if (PEEK) there = __all_sync(0xffffffffu, there);
                     if (++t == buffers) t = 0;
                 }
             }
@@ -1062,13 +1080,13 @@ static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
     return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, rows_aligned(a), xm, wm, sm);
 }
 
-// What a step of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows and
-// K = 1024 and 4096).
+// What a block of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows, 76 tiles and
+// K = 1024 to 8192).
 struct MmWidth {
     int W;
     double step, end;
 };
-constexpr MmWidth kMmWidths[4] = {{64, 0.213, 0.6}, {128, 0.266, 1.2}, {192, 0.36, 1.7}, {256, 0.426, 2.0}};
+constexpr MmWidth kMmWidths[4] = {{64, 0.16, 0.8}, {128, 0.245, 1.3}, {192, 0.345, 1.7}, {256, 0.405, 1.9}};
 
 // Whole tiles in the width whose rounds of all pairs take the least, or equal shares, whose parts
 // cost their writing and reading, where that is less: few tiles with long contractions, or
@@ -1094,7 +1112,7 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) 
         take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1, 1);
         for (int i = 0; i < 2 && w.W == 64; ++i) {
             const int split = 2 << i;
-            if (tiles <= clusters[i] && split <= p.blocks) take((p.blocks + split - 1) / split * w.step + w.end + 1.0 + 0.25 * split, tiles * split, 1, split);
+            if (tiles <= clusters[i] && split <= p.blocks) take((p.blocks + split - 1) / split * w.step + w.end + (split == 2 ? 0.9 : 2.2), tiles * split, 1, split);
         }
         if (w.W != 64 && w.W != 256) continue;
         for (int n = 2; n <= 8; ++n) {
@@ -1103,7 +1121,7 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) 
             if (tiles * (n - 1) >= most && n > 2) break;
             if (total < 4 * pairs) break;
             const long long steps = (total + pairs - 1) / pairs;
-            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + 4.0 + (n - 1) * (w.W == 64 ? 1.0 : 3.0), pairs, 0, 1);
+            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + (w.W == 64 ? 3.5 + 2.0 * (n - 1) : 4.0 + 3.0 * (n - 1)), pairs, 0, 1);
         }
     }
     p.tag = next_launch_tag();
