@@ -7,14 +7,16 @@
 // running sums in registers, while the next blocks' products run into the other
 // accumulators.
 //
-// Measured (one GB300, inputs new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
+// Measured (one GB300, random inputs, new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
 // copy 6.8 TB/s):
 //   1 row, N = 6144, K = 4096: 6.4 us, 3.9 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 3.5 us
 //     of a call's begin and end.
-//   512 rows, N = 151936, K = 4096: 281 us, 2.27 PFLOP/s; N = 24576: 51 us, 2.0; 1152 rows, N = 4096, K =
-//     12288: 61 us, 1.9.  A step of 256 x 256 x 128 takes a pair 0.43 us, of which the products would
-//     take 0.27: the rest is the chain from an accumulator's last product to its next; and the clock
-//     falls to 1.75 GHz under it.  With constant inputs, which use less power: 255 us, 2.5 PFLOP/s.
+//   512 rows, N = 151936, K = 4096: 268 us, 2.38 PFLOP/s; N = 24576: 48 us, 2.15; 1152 rows, N = 4096, K =
+//     12288: 60.9 us, 1.9.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
+//     take 0.27: the rest is the chain from an accumulator's last product to its next, and what L2 brings (64
+//     KB a step and pair, 11 TB/s in all: with half the bytes of both operands left out, the largest
+//     took 211 us for 240); and the clock falls to 1.75 GHz under it.  (Constant inputs, which use less power: 240
+//     us, 2.65 PFLOP/s.)
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 #include "sv_linear.h"
@@ -152,11 +154,12 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, unsigned short both) 
 //   warps 2-5  running sums: a thread owns a weight row, the rows' scales are read from shared
 //              memory, the weights' scale is the tile's
 // Handing on a block takes a CTA's warps some 400 cycles of waits and arrivals, 16 KB in 0.2 us.  So two
-// CTAs an SM, 100 KB under way each, and for up to 16 rows two blocks at a time (one row, N = 6144 /
-// 8192, K = 4096: 6.26 / 7.23 us for 6.48 / 7.63; 64 rows, N = 24576: 24.8 for 23.2).  One CTA an SM
-// with all the ring: 7.0 / 8.1 and 27.5.  Equal shares of all tiles' blocks, their parts joined
-// through memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N =
-// 151936.
+// CTAs an SM, 100 KB under way each (one with all the ring: 7.0 us for 6.3 at one row, N = 6144, K = 4096,
+// 27.5 for 22 at 64 rows, N = 24576), and for up to 16 rows two blocks at a time (one row: 6.26 for 6.48;
+// 64 rows so: 24.8 for 23.2).  Equal shares of all tiles' blocks, their parts joined through
+// memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N = 151936.  65
+// to 128 rows this way: 6.4 us for the 5.6 of pairs at 1000 x 1040, 28.9 for 27.3 at 24576 x 4096, and
+// 18.5 for 20.7 only at 4096 x 12288.
 template <int T>
 struct FewCfg {
     static constexpr int BP = T <= 16 ? 2 : 1;            // blocks at a time

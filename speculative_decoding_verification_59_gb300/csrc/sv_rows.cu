@@ -5,7 +5,8 @@
 //   scale = max(max |y|, 1e-20) / 448,   q = e4m3(y * (448 / max(max |y|, 1e-20))).
 // All in fp32, rounded once.  A thread works on vectors of 8 elements, so 16
 // neighbouring lanes hold a block and find its largest element in four shuffles.
-// Memory bounds all of them from some 256 rows of 4096 on, the launch below that.
+// Memory bounds all of them from some 1000 rows of 4096 on (a copy: 6.8 TB/s), a launch and one
+// dependent load below that.
 #include "sv_kv.cuh"
 #include "sv_linear.h"
 
@@ -175,7 +176,7 @@ static cudaError_t launch_add_norm_t(const NormArgs& a, int out, int sms, cudaSt
     // Few rows: as many threads a row as it has vectors (the time is one row's).  More: two or four
     // vectors a thread, so that an SM holds more rows' loads under way (rows of 4096, one / two / four
     // a thread: 512 rows 5.9 / 4.5 / 5.5 us, 8192 of an fp32 residual 87 / 61.5 / 62, 8192 to e4m3
-    // 71.6 / 47.5 / 45.8).
+    // 71.6 / 47.5 / 45.8, since down to 40.9: 6.5 TB/s with the fp32 residual, 5.8 to e4m3, 2.3 us for a row).
     int vpt = nv > 1024 ? 4 : a.rows <= 2 * sms ? (nv > 512 ? 2 : 1) : a.rows <= 32 * sms ? 2 : 4;
     while (vpt > 1 && nv <= 32 * (vpt / 2)) vpt /= 2;
     int tpr = 32;
@@ -228,7 +229,9 @@ __device__ __forceinline__ void gate8(float (&x)[8], const float (&y)[8]) {
 
 // A CTA takes RT rows and, 16 lanes a block, 16 / RT blocks of them at a time, V times.  Many rows: 16
 // rows of one block, whose scales then leave together in one line (a scale of 4 bytes by itself
-// costs a sector: 39.4 us for 33 at 16384 rows of 4096).
+// costs a sector: 39.4 us for 33 at 16384 rows of 4096).  Activation of 4000 x 12288 bf16 to e4m3: 38.7 us,
+// 6.4 TB/s; of 1152: 12.5, 5.7 (issue slots are 60 % busy; with divisions and single arithmetic, 82 %,
+// 15.1); to bf16 4000 take 43.4, 6.8.  7 rows: 1.6.  Rounding of 16384 x 4096: 33.4, 6.1.
 constexpr int kActThreads = 256;
 template <bool F32, int ACT, int RT, int V>
 __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int out, int chunks) {
