@@ -727,6 +727,8 @@ def add_norm(x, weight=None, residual=None, *, eps: float = 1e-6, e4m3: bool = F
     takes them); and with a residual, last, the sum in the residual's dtype, which sum_out
     may name a place for: the residual itself, say.  Small outputs (up to 2^20 elements) share
     one allocation."""
+    if e4m3 and dtype is not None:
+        raise ValueError("dtype is the output's without e4m3")
     return (_marshal_module or _load_marshal()).add_norm(
         x, weight, residual, eps, e4m3, dtype is not None and _f32(dtype), sum_out, stream)
 
@@ -738,6 +740,8 @@ def gated_act(gate, up=None, *, act: str = "silu", e4m3: bool = False, dtype=Non
     add_norm does."""
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    if e4m3 and dtype is not None:
+        raise ValueError("dtype is the output's without e4m3")
     return (_marshal_module or _load_marshal()).gated_act(
         gate, up, _ACTS[act], e4m3, dtype is not None and _f32(dtype), stream)
 

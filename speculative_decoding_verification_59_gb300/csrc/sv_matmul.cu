@@ -37,6 +37,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Without an order of memory: that all have come, no more.  (At a kernel's end the release waits for its
+// stores to be acknowledged, 0.4 to 0.5 us of every call.)  What other CTAs send or read has to have
+// come by then.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // One lane of a converged warp.  (Loads and products are issued by loops that the whole warp
 // runs, so that addresses and descriptors stay in uniform registers: in a branch of one lane
 // the four products of a step took 315 cycles to issue.)
@@ -397,7 +404,7 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
         }
         put4(a, (int64_t)m * a.old + n, (int)min((int64_t)4, a.N - n), wide, v);
     }
-    if (S > 1) cluster_sync();                             // no CTA ends while another reads its sums
+    if (S > 1) cluster_meet();                             // no CTA ends while another reads its sums
     if (warp == 1) tc_dealloc(tmem, C::TMEM);
 }
 
@@ -533,6 +540,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     // no phase is passed unseen.)
     __shared__ __align__(8) uint64_t full[C::STAGES], done[2][C::STAGES], t_empty[2][C::NB], f_full[C::FS], f_empty[C::FS], drained;
     __shared__ uint32_t tmem_at;
+    __shared__ int failed;
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // (a cluster: pairs of a tile's, where they share it; the first CTA of a pair leads it)
@@ -565,6 +573,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         }
         mbar_init(&drained, 1);
         mbar_init_fence();
+        failed = 0;
         map_prefetch(&xmap);
         map_prefetch(&wmap);
         if (by_tma) map_prefetch(&omap);
@@ -576,7 +585,10 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     tc_after();
     const uint32_t tmem = tmem_at;
     pdl_wait();
-    int32_t* error = reinterpret_cast<int32_t*>(a.ws);
+    auto fail = [&]() {
+        raise_error(reinterpret_cast<int32_t*>(a.ws), SPEC_DEVERR_TIMEOUT);
+        failed = 1;
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LESS));
@@ -626,7 +638,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 if (rank == 0 && !wait_warp(&full[k], parity, kTcWaitLimit)) ok = false;
                 if (!wait_warp(&last[k], parity, limit)) ok = false;
             }
-            if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+            if (!ok && lane == 0) fail();
         } else if (warp == 1 && rank == 0) {
             const unsigned short both = (unsigned short)(3u << leader);
             const uint32_t id = tc_idesc(true, false, false, TWO ? H : W, 256);
@@ -690,8 +702,14 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 }
                 ready = __all_sync(0xffffffffu, next);
             }
+            // the other CTA's last arrivals have come (t and t_phase: the next step's)
+            for (unsigned j = 0; ok && j < buffers && j < it; ++j) {
+                if (t == 0) t_phase ^= 1;
+                t = t == 0 ? buffers - 1 : t - 1;
+                ok = wait_warp(&t_empty[0][t], t_phase, kTcWaitLimit) && (!TWO || wait_warp(&t_empty[1][t], t_phase, kTcWaitLimit));
+            }
             if (!ok) {
-                if (lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+                if (lane == 0) fail();
                 if (it > 0) {
                     if (lead) pair_commit(&drained, both);
                     __syncwarp();
@@ -733,7 +751,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 }
             }
             copies_done();
-            if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+            if (!ok && lane == 0) fail();
         }
         __syncwarp();
         if (MODE == kMmCluster) cluster_sync();
@@ -954,11 +972,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         }
         if (lane == 0) tma_store_wait<0>();
         __syncwarp();
-        if (!ok && lane == 0) raise_error(error, SPEC_DEVERR_TIMEOUT);
+        if (!ok && lane == 0) fail();
     }
     tc_before();
     __syncthreads();
-    cluster_sync();
+    if (failed) cluster_sync();                            // (arrivals that nobody has waited for)
+    else cluster_meet();
     tc_after();
     if (warp == 1) pair_dealloc(tmem, 512);
 }
@@ -1127,7 +1146,8 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) 
             take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + (w.W == 64 ? 3.5 + 2.0 * (n - 1) : 4.0 + 3.0 * (n - 1)), pairs, 0, 1);
         }
     }
-    p.tag = next_launch_tag();
+    // (times an odd number: one tag a launch as before, but none that small numbers left in a workspace could be)
+    p.tag = next_launch_tag() * 0x9e3779b97bull & ((1ull << 40) - 1);
     return p;
 }
 

@@ -243,6 +243,20 @@ def test_matmul_strides_shapes_and_nan(sv, M):
     assert torch.equal(bad.isnan(), nan) and torch.equal(bad[~nan], got[~nan])
 
 
+@pytest.mark.parametrize("M", [2, 33, 70, 270])
+@pytest.mark.parametrize("K", [1, 3, 17, 129])
+def test_matmul_short_contractions(sv, M, K):
+    x, xs, w, ws = R.problem(M + K, M, 90, K)
+    rows = []
+    for t in (x, w):                                          # NaN from K on
+        wide = torch.full((t.shape[0], 144), 0x7f, dtype=torch.uint8, device="cuda")
+        wide[:, :K] = t.view(torch.uint8)
+        rows.append(wide.view(torch.float8_e4m3fn)[:, :K])
+    got = sv.matmul_e4m3(rows[0], xs, rows[1], ws, dtype=torch.float32)
+    ref, mags = R.matmul(x, xs, w, ws)
+    assert ((got.double() - ref).abs() <= R.matmul_bound(ref, mags, K, torch.float32)).all()
+
+
 @pytest.mark.parametrize("M", [5, 64, 100, 300])
 @pytest.mark.parametrize("N,stride,at", [(262, 264, 0), (263, 272, 0), (261, 268, 4), (130, 132, 2), (129, 131, 1), (70, 1000, 8)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

@@ -109,6 +109,9 @@ def test_helpers_refuse_tensors_that_are_not_on_a_gpu():
         sv.gated_act(x, act="relu")
     with pytest.raises(TypeError, match="float32 or bfloat16"):
         sv.add_norm(x, dtype=torch.float16)
+    for call in (sv.add_norm, sv.gated_act):
+        with pytest.raises(ValueError, match="without e4m3"):
+            call(x, e4m3=True, dtype=torch.float32)
 
 
 def test_plain_forms():
