@@ -9,9 +9,9 @@
 //
 // Measured (one GB300, random inputs, new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
 // copy 6.8 TB/s):
-//   1 row, N = 6144, K = 4096: 6.4 us, 3.9 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 3.5 us
-//     of a call's begin and end.
-//   512 rows, N = 151936, K = 4096: 268 us, 2.38 PFLOP/s; N = 24576: 48 us, 2.15; 1152 rows, N = 4096, K =
+//   1 row, N = 6144, K = 4096: 5.9 us, 4.3 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 2 us from
+//     one call's last store to the next one's first load and of the join.
+//   512 rows, N = 151936, K = 4096: 270 us, 2.36 PFLOP/s; N = 24576: 48 us, 2.15; 1152 rows, N = 4096, K =
 //     12288: 60.9 us, 1.9.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
 //     take 0.27: the rest is the chain from an accumulator's last product to its next, and what L2 brings (64
 //     KB a step and pair, 11 TB/s in all: with half the bytes of both operands left out, the largest
