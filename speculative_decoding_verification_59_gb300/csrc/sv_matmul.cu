@@ -11,8 +11,8 @@
 // copy 6.8 TB/s):
 //   1 row, N = 6144, K = 4096: 5.9 us, 4.3 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 2 us from
 //     one call's last store to the next one's first load and of the join.
-//   512 rows, N = 151936, K = 4096: 270 us, 2.36 PFLOP/s; N = 24576: 48 us, 2.15; 1152 rows, N = 4096, K =
-//     12288: 60.9 us, 1.9.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
+//   512 rows, N = 151936, K = 4096: 267 us, 2.39 PFLOP/s; N = 24576: 47 us, 2.2; 1152 rows, N = 4096, K =
+//     12288: 49.8 us, 2.3.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
 //     take 0.27: the rest is the chain from an accumulator's last product to its next, and what L2 brings (64
 //     KB a step and pair, 11 TB/s in all: with half the bytes of both operands left out, the largest
 //     took 211 us for 240); and the clock falls to 1.75 GHz under it.  (Constant inputs, which use less power: 240
@@ -166,7 +166,7 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, unsigned short both) 
 // 64 rows so: 24.8 for 23.2).  Equal shares of all tiles' blocks, their parts joined through
 // memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N = 151936.  65
 // to 128 rows this way: 6.4 us for the 5.6 of pairs at 1000 x 1040, 28.9 for 27.3 at 24576 x 4096, and
-// 18.5 for 20.7 only at 4096 x 12288.
+// 18.5 for 20.7 only at 4096 x 12288 (single CTAs: 16.8).
 template <int T>
 struct FewCfg {
     static constexpr int BP = T <= 16 ? 2 : 1;            // blocks at a time
@@ -409,16 +409,17 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
 }
 
 // ---- shares and parts ----------------------------------------------------------------
-// For more rows the steps (blocks of the contraction) of all tiles, end to end, are dealt to pairs of CTAs:
-// whole tiles, or equal shares that may begin and end inside a tile.  Of a tile in several
-// shares, each warp of each pair leaves its part of the sums in the workspace and takes a ticket; the
+// For more rows the steps (blocks of the contraction) of all tiles, end to end, are dealt to pairs of CTAs, or to
+// CTAs by themselves: whole tiles, or, to pairs, equal shares that may begin and end inside a tile.  Of a tile in
+// several shares, each warp of each pair leaves its part of the sums in the workspace and takes a ticket; the
 // one that takes the last adds the parts in their order, whichever that was, and writes the
 // output.  Nobody waits for anybody.
 struct MmPlan {
     long long tiles, total;            // steps of all tiles
-    int pairs, blocks, whole;          // blocks: steps of a tile
-    int W, tiles_m;                    // a tile's weight rows; tiles of 256 rows of x
-    int split;                         // pairs of a cluster
+    int pairs, blocks, whole;          // pairs, or single CTAs; blocks: steps of a tile
+    int W, tiles_m;                    // a tile's weight rows; tiles of 256 (128) rows of x
+    int split;                         // pairs (CTAs) of a cluster
+    int pair;                          // CTAs in pairs, or each by itself
     unsigned long long tag;
     // equal shares: the first step of a pair's
     __device__ __forceinline__ long long begin(int p) const { return total * p / pairs; }
@@ -475,8 +476,10 @@ __device__ __forceinline__ bool last_ticket(unsigned long long* w, unsigned long
 
 // ---- more rows ---------------------------------------------------------------------
 // A pair of CTAs takes 256 rows of x times W weight rows (cta_group::2: each loads its 128
-// rows of x and half of the weight rows, and holds its 128 rows' sums).  W, of 64, 128, 192 and 256, is
-// chosen by the launch so that the tiles fill the pairs evenly.
+// rows of x and half of the weight rows, and holds its 128 rows' sums), or a CTA by itself 128 times W.  A
+// pair brings 64 KB for 256 x 256 x 128, two CTAs 96: 235 us for 267 at 512 x 151936 x 4096.  Single
+// ones divide rows and tiles more finely: 1152 rows, 4096 x 12288: 47 us for 58; 128 rows, 24576 x 4096: 23 for
+// 28.  Which, and W, of 64, 128, 192 and 256, is chosen by the launch so that the tiles fill them evenly.
 //   warp 0      loads
 //   warp 1      issues the products (the pair's first CTA, for both)
 //   warp 2      brings the scales
@@ -512,12 +515,13 @@ __host__ __device__ constexpr bool two_halves(int W) { return W > 128 && W % 64 
 // of 128 columns 0.245 alone, 0.255 by twos, whose stages are fewer).
 __host__ __device__ constexpr int blocks_of(int W) { return W == 64 ? 2 : 1; }
 __host__ __device__ constexpr unsigned least(unsigned a, unsigned b) { return a < b ? a : b; }
-__host__ __device__ constexpr unsigned stages_of(int W) {
-    return least(ManyCfg::OUT_AT / (blocks_of(W) * (ManyCfg::X_BYTES + W / 2 * kMmTile)), ManyCfg::STAGES);
+__host__ __device__ constexpr unsigned stages_of(int W, bool pair) {
+    return least(ManyCfg::OUT_AT / (blocks_of(W) * (ManyCfg::X_BYTES + W / (pair ? 2 : 1) * kMmTile)), ManyCfg::STAGES);
 }
-__host__ __device__ constexpr unsigned buffers_of(int W) { return least(512 / (blocks_of(W) * W), ManyCfg::NB); }
+// (no more than stages: a barrier of products counts two rounds of its stage before the sums have seen one)
+__host__ __device__ constexpr unsigned buffers_of(int W, bool pair) { return least(least(512 / (blocks_of(W) * W), ManyCfg::NB), stages_of(W, pair)); }
 enum MmMode { kMmWhole, kMmTickets, kMmCluster };
-template <int W, MmMode MODE>
+template <int W, MmMode MODE, bool PAIR>
 __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const MatmulArgs a, uint32_t limit, const MmPlan plan,
                                                                          const __grid_constant__ CUtensorMap xmap,
                                                                          const __grid_constant__ CUtensorMap wmap,
@@ -527,12 +531,16 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     constexpr int H = W / 2;
     constexpr bool CROSS = kScaleBlock % H != 0;           // a half's columns may lie in two blocks of the weights
     static_assert(H % 32 == 0 && H <= ManyCfg::COLS, "whole pieces of the output");
-    // Whether the sums ask for the next step's products ahead (1152 x 4096 x 12288, in shares: 58.5 us for 60.5;
+    // Whether the sums ask for the next step's products ahead (1152 x 4096 x 12288, then in shares: 58.5 us for 60.5;
     // whole tiles with halves, bound by power: 239 for 236 at 512 x 151936 x 4096).
     constexpr bool PEEK = !TWO || MODE == kMmTickets;
     constexpr int BP = blocks_of(W);
-    constexpr unsigned stages = stages_of(W), buffers = buffers_of(W);
-    constexpr uint32_t block_bytes = C::X_BYTES + H * kMmTile, stage_bytes = BP * block_bytes;
+    constexpr int CTAS = PAIR ? 2 : 1, ROWS = CTAS * 128;  // a tile's CTAs and rows of x
+    constexpr int OWN = W / CTAS;                          // weight rows that a CTA loads
+    constexpr unsigned stages = stages_of(W, PAIR), buffers = buffers_of(W, PAIR);
+    constexpr uint32_t block_bytes = C::X_BYTES + OWN * kMmTile, stage_bytes = BP * block_bytes;
+    static_assert(stages >= 3, "loads under way");
+    static_assert(MODE != kMmTickets || PAIR, "the workspace has tickets and parts for pairs");
     static_assert(BP == 1 || !TWO, "a step's accumulators");
     extern __shared__ unsigned char smem_raw[];
     // done: a step's products (of a half) are complete; after the second half's its stage is free.  (As
@@ -544,8 +552,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // (a cluster: pairs of a tile's, where they share it; the first CTA of a pair leads it)
-    const uint32_t place = cluster_rank(), rank = place & 1, leader = place & ~1u;
-    const int pair = blockIdx.x >> 1, blocks = plan.blocks, tiles_m = plan.tiles_m;
+    const uint32_t place = cluster_rank(), rank = PAIR ? place & 1 : 0, leader = place - rank;
+    const int pair = blockIdx.x / CTAS, blocks = plan.blocks, tiles_m = plan.tiles_m;
     // The first tile, its first step, and the steps to do.  Whole tiles go to the pairs in turn: those of the
     // same weight rows are taken side by side, and the weights read once.
     int first_tile = pair, first_b = 0;
@@ -564,8 +572,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             mbar_init(&done[1][i], 1);
         }
         for (int i = 0; i < C::NB; ++i) {                  // both CTAs' warps
-            mbar_init(&t_empty[0][i], TWO ? C::EW : 2 * C::EW);
-            mbar_init(&t_empty[1][i], C::EW);
+            mbar_init(&t_empty[0][i], CTAS * C::EW / (TWO ? 2 : 1));
+            mbar_init(&t_empty[1][i], CTAS * C::EW / 2);
         }
         for (int i = 0; i < C::FS; ++i) {
             mbar_init(&f_full[i], 32);
@@ -578,7 +586,10 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         map_prefetch(&wmap);
         if (by_tma) map_prefetch(&omap);
     }
-    if (warp == 1) pair_alloc(&tmem_at, 512);
+    if (warp == 1) {
+        if (PAIR) pair_alloc(&tmem_at, 512);
+        else tc_alloc(&tmem_at, 512);
+    }
     pdl_trigger();
     tc_before();
     cluster_sync();
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             const bool lead = elect_one();
             long long left = steps;
             for (int tile = first_tile, b = first_b; ok && left > 0; tile += turn, b = 0) {
-                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
+                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * ROWS + (int)rank * 128;
                 // (a product's columns are half the first CTA's weight rows, half the second's)
                 const int n0 = tn * W + (int)rank * (TWO ? H / 2 : H);
                 const int end = (int)min((long long)blocks, b + left);
@@ -619,14 +630,19 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     free = phase_done(&last[s], phase ^ 1);
                     if (lead) {
                         const bool all = b + BP <= end;    // (else the step has one block of two)
-                        if (rank == 0) mbar_arrive_expect_tx(&full[now], all ? 2 * stage_bytes : 2 * block_bytes);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[now], CTAS * (all ? stage_bytes : block_bytes));
 #pragma unroll
                         for (int k = 0; k < BP; ++k) {
                             if (k > 0 && !all) break;
                             const uint32_t to = at + k * block_bytes;
-                            tma_2d_pair(to, &xmap, (b + k) * kMmTile, m0, bar);
-                            tma_2d_pair(to + C::X_BYTES, &wmap, (b + k) * kMmTile, n0, bar);
-                            if constexpr (TWO) tma_2d_pair(to + C::X_BYTES + H / 2 * kMmTile, &wmap, (b + k) * kMmTile, n0 + H, bar);
+                            if constexpr (PAIR) {
+                                tma_2d_pair(to, &xmap, (b + k) * kMmTile, m0, bar);
+                                tma_2d_pair(to + C::X_BYTES, &wmap, (b + k) * kMmTile, n0, bar);
+                                if constexpr (TWO) tma_2d_pair(to + C::X_BYTES + H / 2 * kMmTile, &wmap, (b + k) * kMmTile, n0 + H, bar);
+                            } else {
+                                tma_2d(to, &xmap, (b + k) * kMmTile, m0, &full[now]);
+                                tma_2d(to + C::X_BYTES, &wmap, (b + k) * kMmTile, n0, &full[now]);
+                            }
                         }
                     }
                     free = __all_sync(0xffffffffu, free);
@@ -641,7 +657,15 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             if (!ok && lane == 0) fail();
         } else if (warp == 1 && rank == 0) {
             const unsigned short both = (unsigned short)(3u << leader);
-            const uint32_t id = tc_idesc(true, false, false, TWO ? H : W, 256);
+            const uint32_t id = tc_idesc(true, false, false, TWO ? H : W, ROWS);
+            const auto mma = [&](uint32_t d, uint64_t x, uint64_t w, bool add) {
+                if constexpr (PAIR) pair_mma(d, x, w, id, add);
+                else tc_mma<true>(d, x, w, id, add);
+            };
+            const auto commit = [&](uint64_t* bar) {
+                if constexpr (PAIR) pair_commit(bar, both);
+                else tc_commit(bar);
+            };
             const uint64_t base = tc_desc(smem_addr(smem), 16, 1024);
             unsigned it = 0, s = 0, phase = 0, t = 0, t_phase = 0;
             const bool lead = elect_one();
@@ -668,8 +692,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                     const bool second = phase_done(&t_empty[1][t], t_phase ^ 1);
                     if (lead) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) pair_mma(to, xd + 2 * k, wd + 2 * k, id, k > 0);
-                        pair_commit(&done[0][now], both);
+                        for (int k = 0; k < 4; ++k) mma(to, xd + 2 * k, wd + 2 * k, k > 0);
+                        commit(&done[0][now]);
                     }
                     if (!__all_sync(0xffffffffu, second)) {
                         ok = wait_warp(&t_empty[1][t], t_phase ^ 1, limit);
@@ -690,15 +714,15 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 }
                 const bool next = phase_done(&full[s], phase) & phase_done(&t_empty[0][t], t_phase ^ 1);
                 if (lead) {
-                    const uint64_t wd2 = TWO ? wd + (H / 2 * kMmTile >> 4) : wd;
+                    const uint64_t wd2 = TWO ? wd + (OWN / 2 * kMmTile >> 4) : wd;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) pair_mma(to + (TWO ? 256 : 0), xd + 2 * k, wd2 + 2 * k, id, k > 0);
+                    for (int k = 0; k < 4; ++k) mma(to + (TWO ? 256 : 0), xd + 2 * k, wd2 + 2 * k, k > 0);
                     if (BP > 1 && n > 1) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            pair_mma(to + W, xd + (block_bytes >> 4) + 2 * k, wd + (block_bytes >> 4) + 2 * k, id, k > 0);
+                            mma(to + W, xd + (block_bytes >> 4) + 2 * k, wd + (block_bytes >> 4) + 2 * k, k > 0);
                     }
-                    pair_commit(&done[TWO ? 1 : 0][now], both);
+                    commit(&done[TWO ? 1 : 0][now]);
                 }
                 ready = __all_sync(0xffffffffu, next);
             }
@@ -711,7 +735,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             if (!ok) {
                 if (lane == 0) fail();
                 if (it > 0) {
-                    if (lead) pair_commit(&drained, both);
+                    if (lead) commit(&drained);
                     __syncwarp();
                     wait_warp(&drained, 0, kTcWaitLimit);
                 }
@@ -726,7 +750,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
             for (int tile = first_tile, at = first_b; ok && left > 0; tile += turn, at = 0) {
                 const int end = (int)min((long long)blocks, at + left);
                 left -= end - at;
-                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128;
+                const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * ROWS + (int)rank * 128;
                 // the first 16 lanes: a half's first or second 128-block of the weights, and a step of the four
                 const int wrow = min((tn * W + (lane >> 3 & 1) * H) / kScaleBlock + (lane >> 2 & 1), (a.N - 1) / kScaleBlock);
                 const float* wsc = a.wscale + (int64_t)wrow * a.ws_stride;
@@ -768,7 +792,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         long long left = steps;
         float acc[C::COLS];
         auto output = [&](int tile) {
-            const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * 256 + (int)rank * 128 + quad * 32;
+            const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * ROWS + (int)rank * 128 + quad * 32;
             const int n0 = tn * W + part * H;
             // ---- the tile's output, in pieces of 64 bytes of the warp's 32 rows: by TMA where the rows are
             // aligned, else through the same place and registers, `vec` bytes a lane
@@ -955,12 +979,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
 #pragma unroll
             for (int c = 0; c < H; ++c) sums[c * 32] = acc[c];
             cluster_sync();
-            if ((int)(place >> 1) == part) {
+            if ((int)place / CTAS == part) {
 #pragma unroll
                 for (int c = 0; c < H; ++c) acc[c] = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < plan.split; ++p) {
-                    const uint32_t from_ = cluster_addr(smem_addr(sums), 2 * p + rank);
+                    const uint32_t from_ = cluster_addr(smem_addr(sums), CTAS * p + rank);
                     float x[H];
 #pragma unroll
                     for (int c = 0; c < H; ++c) x[c] = ld_cluster(from_ + c * 128);
@@ -979,7 +1003,10 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
     if (failed) cluster_sync();                            // (arrivals that nobody has waited for)
     else cluster_meet();
     tc_after();
-    if (warp == 1) pair_dealloc(tmem, 512);
+    if (warp == 1) {
+        if (PAIR) pair_dealloc(tmem, 512);
+        else tc_dealloc(tmem, 512);
+    }
 }
 
 // ---- launches -----------------------------------------------------------------------
@@ -1102,48 +1129,58 @@ static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
     return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, rows_aligned(a), xm, wm, sm);
 }
 
-// What a block of a tile W columns wide takes a pair, and a tile's end (us, measured at 512 rows, 76 tiles and
-// K = 1024 to 8192).
+// What a block of a tile W columns wide takes, and a tile's end (us, measured at 512 rows, as many tiles
+// as pairs, or as single CTAs, fit at once, and K = 1024 to 8192).
 struct MmWidth {
     int W;
     double step, end;
 };
-constexpr MmWidth kMmWidths[4] = {{64, 0.16, 0.8}, {128, 0.245, 1.3}, {192, 0.345, 1.7}, {256, 0.405, 1.9}};
+constexpr MmWidth kMmPairs[4] = {{64, 0.16, 0.8}, {128, 0.245, 1.3}, {192, 0.345, 1.7}, {256, 0.405, 1.9}};
+constexpr MmWidth kMmSingles[4] = {{64, 0.19, 0.8}, {128, 0.28, 1.3}, {192, 0.4, 1.7}, {256, 0.44, 1.9}};
+// Joining a cluster's sums: of two, four and eight.
+constexpr double kMmJoin[3] = {0.9, 2.2, 3.6};
 
-// Whole tiles in the width whose rounds of all pairs take the least, or equal shares, whose parts
+// Whole tiles in the width whose rounds of all pairs or CTAs take the least, or equal shares, whose parts
 // cost their writing and reading, where that is less: few tiles with long contractions, or
 // little more than whole rounds.
-static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) {
+static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[3]) {
     MmPlan p = {};
     p.blocks = scale_blocks(a.K);
-    p.tiles_m = (a.M - 1) / 256 + 1;
-    const long long most = sms / 2 < kMmMaxPairs ? sms / 2 : kMmMaxPairs;
+    const long long pairs_most = sms / 2 < kMmMaxPairs ? sms / 2 : kMmMaxPairs;
     double best = 1e300;
-    for (const MmWidth& w : kMmWidths) {
-        const long long tiles = (long long)p.tiles_m * ((a.N - 1) / w.W + 1), total = tiles * p.blocks;
-        const auto take = [&](double us, long long pairs, int whole, int split) {
-            if (us >= best) return;
-            best = us;
-            p.W = w.W;
-            p.whole = whole;
-            p.tiles = tiles;
-            p.total = total;
-            p.pairs = (int)pairs;
-            p.split = split;
-        };
-        take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1, 1);
-        for (int i = 0; i < 2 && w.W == 64; ++i) {
-            const int split = 2 << i;
-            if (tiles <= clusters[i] && split <= p.blocks) take((p.blocks + split - 1) / split * w.step + w.end + (split == 2 ? 0.9 : 2.2), tiles * split, 1, split);
-        }
-        if (w.W != 64 && w.W != 256) continue;
-        for (int n = 2; n <= 8; ++n) {
-            // (n: parts of a tile)
-            const long long pairs = tiles * n < most ? tiles * n : most;
-            if (tiles * (n - 1) >= most && n > 2) break;
-            if (total < 4 * pairs) break;
-            const long long steps = (total + pairs - 1) / pairs;
-            take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + (w.W == 64 ? 3.5 + 2.0 * (n - 1) : 4.0 + 3.0 * (n - 1)), pairs, 0, 1);
+    for (int single = 0; single < 2; ++single) {
+        const int tiles_m = single ? (a.M - 1) / 128 + 1 : (a.M - 1) / 256 + 1;
+        const long long most = single ? sms : pairs_most;
+        for (const MmWidth& w : single ? kMmSingles : kMmPairs) {
+            const long long tiles = (long long)tiles_m * ((a.N - 1) / w.W + 1), total = tiles * p.blocks;
+            const auto take = [&](double us, long long pairs, int whole, int split) {
+                if (us >= best) return;
+                best = us;
+                p.W = w.W;
+                p.pair = !single;
+                p.tiles_m = tiles_m;
+                p.whole = whole;
+                p.tiles = tiles;
+                p.total = total;
+                p.pairs = (int)pairs;
+                p.split = split;
+            };
+            take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1, 1);
+            // (a cluster has up to eight CTAs)
+            for (int i = 0; i < (single ? 3 : 2) && w.W == 64; ++i) {
+                const int split = 2 << i;
+                if (tiles <= clusters[single ? i : i + 1] && split <= p.blocks)
+                    take((p.blocks + split - 1) / split * w.step + w.end + kMmJoin[i], tiles * split, 1, split);
+            }
+            if (single || (w.W != 64 && w.W != 256)) continue;
+            for (int n = 2; n <= 8; ++n) {
+                // (n: parts of a tile)
+                const long long pairs = tiles * n < most ? tiles * n : most;
+                if (tiles * (n - 1) >= most && n > 2) break;
+                if (total < 4 * pairs) break;
+                const long long steps = (total + pairs - 1) / pairs;
+                take(1.1 * steps * w.step + ((double)steps / p.blocks + 1) * w.end + (w.W == 64 ? 3.5 + 2.0 * (n - 1) : 4.0 + 3.0 * (n - 1)), pairs, 0, 1);
+            }
         }
     }
     // (times an odd number: one tag a launch as before, but none that small numbers left in a workspace could be)
@@ -1151,10 +1188,11 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[2]) 
     return p;
 }
 
-template <int W, MmMode MODE>
+template <int W, MmMode MODE, bool PAIR>
 static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStream_t st) {
     using C = ManyCfg;
-    auto kfn = matmul_many_kernel<W, MODE>;
+    auto kfn = matmul_many_kernel<W, MODE, PAIR>;
+    constexpr int CTAS = PAIR ? 2 : 1;
     static DeviceSlots slots = {};
     int unused = 0;
     cudaError_t e = device_once(slots, &unused, [&](int, int* o) {
@@ -1170,38 +1208,43 @@ static cudaError_t launch_many_t(const MatmulArgs& a, const MmPlan& p, cudaStrea
     const int vec = align % 8 == 0 ? 8 : align % 4 == 0 ? 4 : 2;
     CUtensorMap xm, wm, om = {};
     if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, two_halves(W) ? W / 4 : W / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, PAIR && two_halves(W) ? W / 4 : W / CTAS, CU_TENSOR_MAP_SWIZZLE_128B) ||
         (by_tma && !map_2d(&om, a.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.N, a.M, a.old * elt,
                            64 / elt, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
         return cudaErrorInvalidValue;
-    return launch_clusters(kfn, p.pairs * 2, MODE == kMmCluster ? 2 * p.split : 2, C::THREADS, C::SMEM, st, a, wait_limit(), p, xm, wm, om, by_tma, vec);
+    return launch_clusters(kfn, p.pairs * CTAS, MODE == kMmCluster ? CTAS * p.split : CTAS, C::THREADS, C::SMEM, st, a, wait_limit(), p, xm, wm, om, by_tma, vec);
 }
 
-// Clusters of two and of four pairs.
-static cudaError_t many_clusters(int (&most)[2]) {
+// Clusters of two, four and eight CTAs.
+static cudaError_t many_clusters(int (&most)[3]) {
     using C = ManyCfg;
-    static Clusters<2> table;
+    static Clusters<3> table;
     return table.get(most, [](int i, int* o) {
-        const auto kfn = matmul_many_kernel<64, kMmCluster>;
+        const auto kfn = matmul_many_kernel<64, kMmCluster, false>;
         const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        return e != cudaSuccess ? e : clusters_at_once(o, kfn, 4 << i, C::THREADS, C::SMEM);
+        return e != cudaSuccess ? e : clusters_at_once(o, kfn, 2 << i, C::THREADS, C::SMEM);
     });
 }
 
+template <bool PAIR>
+static cudaError_t launch_whole(const MatmulArgs& a, const MmPlan& p, cudaStream_t st) {
+    if (p.split > 1) return launch_many_t<64, kMmCluster, PAIR>(a, p, st);
+    switch (p.W) {
+        case 64: return launch_many_t<64, kMmWhole, PAIR>(a, p, st);
+        case 128: return launch_many_t<128, kMmWhole, PAIR>(a, p, st);
+        case 192: return launch_many_t<192, kMmWhole, PAIR>(a, p, st);
+        default: return launch_many_t<256, kMmWhole, PAIR>(a, p, st);
+    }
+}
+
 static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
-    if ((long long)((a.M - 1) / 256 + 1) * ((a.N - 1) / 64 + 1) >= (1LL << 31)) return cudaErrorInvalidValue;
-    int clusters[2];
+    if ((long long)((a.M - 1) / 128 + 1) * ((a.N - 1) / 64 + 1) >= (1LL << 31)) return cudaErrorInvalidValue;
+    int clusters[3];
     const cudaError_t e = many_clusters(clusters);
     if (e != cudaSuccess) return e;
     const MmPlan p = plan_many(a, sms, clusters);
-    if (p.split > 1) return launch_many_t<64, kMmCluster>(a, p, st);
-    if (!p.whole) return p.W == 64 ? launch_many_t<64, kMmTickets>(a, p, st) : launch_many_t<256, kMmTickets>(a, p, st);
-    switch (p.W) {
-        case 64: return launch_many_t<64, kMmWhole>(a, p, st);
-        case 128: return launch_many_t<128, kMmWhole>(a, p, st);
-        case 192: return launch_many_t<192, kMmWhole>(a, p, st);
-        default: return launch_many_t<256, kMmWhole>(a, p, st);
-    }
+    if (!p.whole) return p.W == 64 ? launch_many_t<64, kMmTickets, true>(a, p, st) : launch_many_t<256, kMmTickets, true>(a, p, st);
+    return p.pair ? launch_whole<true>(a, p, st) : launch_whole<false>(a, p, st);
 }
 
 constexpr int kMmFew = 64;             // rows that matmul_few_kernel takes
