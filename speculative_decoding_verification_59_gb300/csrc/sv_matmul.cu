@@ -783,15 +783,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE));
         const int part = (warp - 4) >> 2, quad = warp & 3, half = TWO ? part : 0;
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (TWO ? part * 256 : part * H), step = TWO ? H : BP * W;
-        // (a cluster's sums lie in the output's place, its output in the ring's, which is free then)
-        unsigned char* const pieces = smem + (MODE == kMmCluster ? 0 : C::OUT_AT) + (warp - 4) * 4096;
-        static_assert(MODE != kMmCluster || W == 64, "a warp's sums fit its 4 KB");
+        unsigned char* const pieces = smem + C::OUT_AT + (warp - 4) * 4096;
         const uint32_t t_free = cluster_addr(smem_addr(t_empty[half]), leader);
         unsigned gi = 0, s = 0, phase = 0, t = 0, stored = 0;
         bool ok = true, there = false;
         long long left = steps;
         float acc[C::COLS];
-        auto output = [&](int tile) {
+        auto output = [&](int tile, int lo, int hi) {      // of the warp's columns lo to hi
             const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * ROWS + (int)rank * 128 + quad * 32;
             const int n0 = tn * W + part * H;
             // ---- the tile's output, in pieces of 64 bytes of the warp's 32 rows: by TMA where the rows are
@@ -832,6 +830,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
 #pragma unroll
                 for (int c0 = 0; c0 < H; c0 += 16) {
                     if (n0 + c0 >= a.N) break;
+                    if (MODE == kMmCluster && (c0 < lo || c0 >= hi)) continue;
                     unsigned char* to = place();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -845,6 +844,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
 #pragma unroll
                 for (int c0 = 0; c0 < H; c0 += 32) {
                     if (n0 + c0 >= a.N) break;
+                    if (MODE == kMmCluster && (c0 < lo || c0 >= hi)) continue;
                     unsigned char* to = place();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -970,28 +970,41 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1) matmul_many_kernel(const 
                 for (int p = parts.p0; p <= parts.p1; ++p)
                     if (n > 2 || p != pair) add(p);
             }
-            output(tile);
+            output(tile, 0, H);
         }
         if (MODE == kMmCluster) {
-            // The sums of the cluster's pairs over distributed shared memory, in their order: the first pair
-            // finishes the tile's first half of columns, the second the second.
-            float* sums = reinterpret_cast<float*>(smem + C::OUT_AT + (warp - 4) * 4096) + lane;       // [column][row]
+            // The sums of the cluster's pairs (or CTAs) over distributed shared memory, in their order: each finishes
+            // its share of the tile's columns, of 32 at least.  (They lie in the ring, which is free once the last
+            // products are complete; where a wait ran out, copies may still arrive there.)
+            static_assert(MODE != kMmCluster || !TWO, "a warp has seen all products complete");
+            float* sums = reinterpret_cast<float*>(smem + (warp - 4) * H * 128) + lane;       // [column][row]
 #pragma unroll
             for (int c = 0; c < H; ++c) sums[c * 32] = acc[c];
+            if (!ok && lane == 0) fail();
             cluster_sync();
-            if ((int)place / CTAS == part) {
+            const int share = max(1, W / 32 / plan.split) * 32, at = (int)place / CTAS * share, lo = at - part * H;
+            if (at < W && lo >= 0 && lo < H) {
 #pragma unroll
                 for (int c = 0; c < H; ++c) acc[c] = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < plan.split; ++p) {
                     const uint32_t from_ = cluster_addr(smem_addr(sums), CTAS * p + rank);
-                    float x[H];
 #pragma unroll
-                    for (int c = 0; c < H; ++c) x[c] = ld_cluster(from_ + c * 128);
+                    for (int c0 = 0; c0 < H; c0 += 32) {
+                        if (c0 < lo || c0 >= lo + share) continue;
+                        float x[32];
 #pragma unroll
-                    for (int c = 0; c < H; ++c) acc[c] += x[c];
+                        for (int c = 0; c < 32; ++c) x[c] = ld_cluster(from_ + (c0 + c) * 128);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) acc[c0 + c] += x[c];
+                    }
+                    if (__float_as_int(ld_cluster(cluster_addr(smem_addr(&failed), CTAS * p + rank))) != 0) ok = false;
                 }
-                output(first_tile);
+                if (!ok) {
+#pragma unroll
+                    for (int c = 0; c < H; ++c) acc[c] = CUDART_NAN_F;
+                }
+                output(first_tile, lo, lo + share);
             }
         }
         if (lane == 0) tma_store_wait<0>();
@@ -1166,8 +1179,9 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[3]) 
                 p.split = split;
             };
             take((double)((tiles + most - 1) / most) * (p.blocks * w.step + w.end), tiles < most ? tiles : most, 1, 1);
-            // (a cluster has up to eight CTAs)
-            for (int i = 0; i < (single ? 3 : 2) && w.W == 64; ++i) {
+            // Clusters, of up to eight CTAs.  (Of the wider tiles, two pairs only were the fastest anywhere:
+            // 256 rows, 4096 x 12288: 19.1 us for 20.8 with whole tiles of 64.)
+            for (int i = 0; i < (w.W == 64 ? (single ? 3 : 2) : w.W == 128 && !single ? 1 : 0); ++i) {
                 const int split = 2 << i;
                 if (tiles <= clusters[single ? i : i + 1] && split <= p.blocks)
                     take((p.blocks + split - 1) / split * w.step + w.end + kMmJoin[i], tiles * split, 1, split);
@@ -1228,6 +1242,7 @@ static cudaError_t many_clusters(int (&most)[3]) {
 
 template <bool PAIR>
 static cudaError_t launch_whole(const MatmulArgs& a, const MmPlan& p, cudaStream_t st) {
+    if (PAIR && p.split > 1 && p.W == 128) return launch_many_t<128, kMmCluster, true>(a, p, st);
     if (p.split > 1) return launch_many_t<64, kMmCluster, PAIR>(a, p, st);
     switch (p.W) {
         case 64: return launch_many_t<64, kMmWhole, PAIR>(a, p, st);

@@ -11,8 +11,9 @@ import test_gpu_linear_calls as calls  # noqa: E402
 from test_gpu_linear_calls import sv  # noqa: E402,F401
 
 SHAPES = [
-    # pairs: tiles of 64, 128, 192, 256; clusters of two pairs and of four; shares of tiles of 64 and of 256
-    (100, 300, 400), (500, 3000, 400), (600, 4000, 528), (700, 5000, 528), (128, 128, 2064), (128, 70, 8208), (700, 1000, 16400),
+    # pairs: tiles of 64, 128, 192, 256; clusters of two pairs and of four, of two with tiles of 128; shares of
+    # tiles of 64 and of 256
+    (100, 300, 400), (500, 3000, 400), (600, 4000, 528), (700, 5000, 528), (128, 128, 2064), (128, 70, 8208), (250, 4000, 12304), (700, 1000, 16400),
     (600, 2000, 16400), (2000, 3000, 8192),
     # single CTAs: tiles of 64, 128, 192, 256; clusters of two, four and eight
     (300, 3000, 1040), (257, 5000, 1040), (600, 5000, 528), (300, 12000, 528), (65, 3000, 2064), (100, 2000, 8208), (128, 64, 12304)]
