@@ -230,7 +230,7 @@ __device__ __forceinline__ void gate8(float (&x)[8], const float (&y)[8]) {
 // A CTA takes RT rows and, 16 lanes a block, 16 / RT blocks of them at a time, V times.  Many rows: 16
 // rows of one block, whose scales then leave together in one line (a scale of 4 bytes by itself
 // costs a sector: 39.4 us for 33 at 16384 rows of 4096).  Activation of 4000 x 12288 bf16 to e4m3: 38.7 us,
-// 6.4 TB/s; of 1152: 12.5, 5.7 (issue slots are 60 % busy; with divisions and single arithmetic, 82 %,
+// 6.4 TB/s; of 1152: 12.4, 5.7 (issue slots are 60 % busy; with divisions and single arithmetic, 82 %,
 // 15.1); to bf16 4000 take 43.4, 6.8.  7 rows: 1.6.  Rounding of 16384 x 4096: 33.4, 6.1.
 constexpr int kActThreads = 256;
 template <bool F32, int ACT, int RT, int V>
@@ -285,11 +285,13 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int o
 
 template <bool F32, int ACT>
 static cudaError_t launch_act_t(const ActArgs& a, int out, int sms, cudaStream_t st) {
-    // 16 rows and four blocks of them a CTA where that gives every SM one, else a row's blocks side by side
+    // 16 rows and three blocks of them a CTA where that gives every SM one, else a row's blocks side by side.  (Two, three, four,
+    // six: activation of 1152 x 12288 12.7 / 12.5 / 12.8 / 13.8 us, rounding of 1152 x 4096 4.35 / 3.85 / 4.05 / 4.5,
+    // of 16384 37.7 / 33.5 / 33.2 / 34.6.)
     const long long blocks = scale_blocks(a.dim), groups = ((long long)a.rows + 15) / 16;
-    if ((blocks + 3) / 4 * groups >= sms) {
-        const long long chunks = (blocks + 3) / 4;
-        return launch_pdl(act_kernel<F32, ACT, 16, 4>, dim3((unsigned)(chunks * groups)), kActThreads, 0, st, a, out, (int)chunks);
+    if ((blocks + 2) / 3 * groups >= sms) {
+        const long long chunks = (blocks + 2) / 3;
+        return launch_pdl(act_kernel<F32, ACT, 16, 3>, dim3((unsigned)(chunks * groups)), kActThreads, 0, st, a, out, (int)chunks);
     }
     const long long chunks = (blocks + 15) / 16;
     return launch_pdl(act_kernel<F32, ACT, 1, 1>, dim3((unsigned)(chunks * a.rows)), kActThreads, 0, st, a, out, (int)chunks);
