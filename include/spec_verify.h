@@ -543,8 +543,8 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
  * Rows of x, gate, up and the residual: row r at r * stride elements, 16-byte
  * aligned, strides multiples of 16 bytes (SPEC_ERR_MISALIGNED otherwise; 0 for one row
  * that all share), bf16 or fp32.  Outputs `out`: contiguous rows of dim elements, bf16, fp32 or e4m3 (then
- * out_scale is needed, with scale_stride >= rows, 0 for one row or one block).  dim is a multiple of 8, of 16
- * for an e4m3 output.  rows * (dim rounded up to 128) < 2^34.  Arithmetic is fp32,
+ * out_scale is needed, with scale_stride >= rows; 0 may stand there for rows of one block).  dim is a
+ * multiple of 8, of 16 for an e4m3 output.  rows * (dim rounded up to 128) < 2^34.  Arithmetic is fp32,
  * each output rounded once.  An output may not overlap an input except as said.
  * ======================================================================== */
 
@@ -578,7 +578,8 @@ spec_status_t spec_gated_act(const void* gate, const void* up, spec_dtype_t dtyp
 
 /*
  * Rounds rows (block_rows 1) or a weight (block_rows 128) to 8 bits; scales as above
- * (a weight's scale_stride is at least the number of a row's blocks).
+ * (a weight's scale_stride is at least the number of a row's blocks; 0 may stand there for up to
+ * 128 rows).
  */
 spec_status_t spec_quantize_e4m3(const void* x, spec_dtype_t dtype, int64_t x_stride, int rows,
                                  int dim, int block_rows, void* out, float* out_scale,

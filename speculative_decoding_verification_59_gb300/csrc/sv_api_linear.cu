@@ -16,10 +16,11 @@ static int bytes_of(spec_dtype_t t) { return t == SPEC_DTYPE_F32 ? 4 : t == SPEC
 static bool row_aligned(const void* p, spec_dtype_t t, int64_t stride) {
     return is_aligned(p, 16) && stride * bytes_of(t) % 16 == 0;
 }
-// An output with contiguous rows of dim elements, and its scales.
-static spec_status_t check_out(const void* out, spec_dtype_t t, int dim, const float* scale, int64_t scale_stride, int64_t least) {
+// An output with contiguous rows of dim elements, and its scales: `steps` strides of at least `least`
+// apart (of one, none is used, and 0 may stand there).
+static spec_status_t check_out(const void* out, spec_dtype_t t, int dim, const float* scale, int64_t scale_stride, int64_t least, int steps) {
     if (!out) return SPEC_ERR_INVALID_ARG;
-    if (t == SPEC_DTYPE_E4M3 && (!scale || (scale_stride < least && scale_stride != 0))) return SPEC_ERR_INVALID_ARG;
+    if (t == SPEC_DTYPE_E4M3 && (!scale || (scale_stride < least && (scale_stride != 0 || steps > 1)))) return SPEC_ERR_INVALID_ARG;
     if (dim % (t == SPEC_DTYPE_E4M3 ? 16 : 8)) return SPEC_ERR_MISALIGNED;
     if (!is_aligned(out, 16) || (t == SPEC_DTYPE_E4M3 && !is_aligned(scale, 4))) return SPEC_ERR_MISALIGNED;
     return SPEC_OK;
@@ -41,7 +42,7 @@ spec_status_t spec_add_norm(const void* x, spec_dtype_t x_dtype, int64_t x_strid
     if (!sizes_fit(rows, dim) || !(eps >= 0.f) || !isfinite(eps) || (sum_out && !residual)) return SPEC_ERR_INVALID_ARG;
     if (rows == 0) return SPEC_OK;
     if (!x) return SPEC_ERR_INVALID_ARG;
-    const spec_status_t s = check_out(out, out_dtype, dim, out_scale, scale_stride, rows);
+    const spec_status_t s = check_out(out, out_dtype, dim, out_scale, scale_stride, rows, scale_blocks(dim));
     if (s != SPEC_OK) return s;
     if (!row_aligned(x, x_dtype, x_stride) || (residual && !row_aligned(residual, sum_dtype, residual_stride)) ||
         (sum_out && !row_aligned(sum_out, sum_dtype, sum_stride)) || !is_aligned(weight, 16))
@@ -71,7 +72,7 @@ spec_status_t spec_gated_act(const void* gate, const void* up, spec_dtype_t dtyp
     if (!sizes_fit(rows, dim) || (act != SPEC_ACT_SILU && act != SPEC_ACT_GELU_TANH)) return SPEC_ERR_INVALID_ARG;
     if (rows == 0) return SPEC_OK;
     if (!gate || !up) return SPEC_ERR_INVALID_ARG;
-    const spec_status_t s = check_out(out, out_dtype, dim, out_scale, scale_stride, rows);
+    const spec_status_t s = check_out(out, out_dtype, dim, out_scale, scale_stride, rows, scale_blocks(dim));
     if (s != SPEC_OK) return s;
     if (!row_aligned(gate, dtype, gate_stride) || !row_aligned(up, dtype, up_stride)) return SPEC_ERR_MISALIGNED;
     const ActArgs a{static_cast<const char*>(gate), static_cast<const char*>(up), gate_stride, up_stride, static_cast<char*>(out),
@@ -85,7 +86,9 @@ spec_status_t spec_quantize_e4m3(const void* x, spec_dtype_t dtype, int64_t x_st
     if (!sizes_fit(rows, dim) || (block_rows != 1 && block_rows != kScaleBlock)) return SPEC_ERR_INVALID_ARG;
     if (rows == 0) return SPEC_OK;
     if (!x) return SPEC_ERR_INVALID_ARG;
-    const spec_status_t s = check_out(out, SPEC_DTYPE_E4M3, dim, out_scale, scale_stride, block_rows == 1 ? rows : scale_blocks(dim));
+    const int blocks = scale_blocks(dim);
+    const spec_status_t s = block_rows == 1 ? check_out(out, SPEC_DTYPE_E4M3, dim, out_scale, scale_stride, rows, blocks)
+                                            : check_out(out, SPEC_DTYPE_E4M3, dim, out_scale, scale_stride, blocks, scale_blocks(rows));
     if (s != SPEC_OK) return s;
     if (!row_aligned(x, dtype, x_stride)) return SPEC_ERR_MISALIGNED;
     if (block_rows == 1) {
