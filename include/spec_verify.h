@@ -611,6 +611,25 @@ spec_status_t spec_matmul_e4m3(const void* x, int64_t x_stride, const float* x_s
                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * How spec_matmul_e4m3 divides a product of these sizes among the SMs: five numbers to plan[],
+ *   [0]  the way: one of spec_matmul_way_t
+ *   [1]  weight rows of a tile
+ *   [2]  CTAs that take a tile (of one contraction) together: 1, or 2 (a pair)
+ *   [3]  CTAs or pairs that are launched (few rows: 0)
+ *   [4]  parts of a tile's contraction: 1, those of a cluster, or the most that equal shares leave in
+ *        a tile (few rows: 0)
+ * sms 0: on the current device.  Else on one of `sms` SMs, of which clusters[0], [1] and [2] clusters of
+ * two, four and eight CTAs run at once; host only then, no CUDA call.
+ */
+typedef enum {
+    SPEC_MATMUL_FEW = 0,          /* up to 64 rows: the product transposed */
+    SPEC_MATMUL_WHOLE = 1,        /* whole tiles in turn */
+    SPEC_MATMUL_CLUSTERS = 2,     /* a cluster's CTAs or pairs share a tile's contraction */
+    SPEC_MATMUL_SHARES = 3        /* equal shares of all tiles, joined through the workspace */
+} spec_matmul_way_t;
+spec_status_t spec_matmul_plan(int M, int N, int K, int sms, const int32_t* clusters, int32_t* plan);
+
+/*
  * Test hook for the kernels' bounded waits (the source pages have no
  * counterpart).  Every wait of the streaming kernels on a shared-memory
  * barrier of their bulk-copy ring gives up after a number of polls (seconds of

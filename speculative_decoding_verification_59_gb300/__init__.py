@@ -38,6 +38,10 @@ SPEC_DTYPE_BF16 = 1
 SPEC_DTYPE_E4M3 = 2
 SPEC_ACT_SILU = 0
 SPEC_ACT_GELU_TANH = 1
+SPEC_MATMUL_FEW = 0
+SPEC_MATMUL_WHOLE = 1
+SPEC_MATMUL_CLUSTERS = 2
+SPEC_MATMUL_SHARES = 3
 SPEC_DEVERR_TOKEN_RANGE = 1
 SPEC_DEVERR_EMPTY_ROW = 2
 SPEC_DEVERR_TREE_PARENT = 4
@@ -96,6 +100,7 @@ SIGNATURES = {
     "spec_gated_act": ([_P, _P, _I, _L, _L, _I, _I, _I, _P, _I, _P, _L, _P], _I),
     "spec_quantize_e4m3": ([_P, _I, _L, _I, _I, _I, _P, _P, _L, _P], _I),
     "spec_matmul_workspace_size": ([_I, _I, _I], _S),
+    "spec_matmul_plan": ([_I, _I, _I, _I, _P, _P], _I),
     "spec_matmul_e4m3": ([_P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _P, _I, _L, _P, _S, _P], _I),
     "spec_verify_read_error": ([_P, _P, _P], _I),
     "spec_verify_status_string": ([_I], ctypes.c_char_p),
@@ -768,3 +773,12 @@ def matmul_e4m3(x, x_scale, w, w_scale, *, dtype=None, out=None, workspace=None,
             x.numel() // max(x.shape[-1], 1), w.shape[0], x.shape[-1]), stream)
     return (_marshal_module or _load_marshal()).matmul_e4m3(
         x, x_scale, w, w_scale, dtype is not None and _f32(dtype), out, workspace, stream)
+
+
+def matmul_plan(M: int, N: int, K: int, sms: int = 0, clusters=(0, 0, 0)):
+    """How matmul_e4m3 divides a product of these sizes (see spec_matmul_plan): (way, a tile's weight rows, CTAs
+    that take a tile together, CTAs or pairs in all, parts of a tile), on the current device or on
+    one of `sms` SMs, of which `clusters` clusters of two, four and eight CTAs run at once."""
+    given, plan = (ctypes.c_int32 * 3)(*clusters), (ctypes.c_int32 * 5)()
+    _check(load_library().spec_matmul_plan(M, N, K, sms, ctypes.addressof(given), ctypes.addressof(plan)), "spec_matmul_plan")
+    return tuple(plan)

@@ -105,6 +105,16 @@ size_t spec_matmul_workspace_size(int M, int N, int K) {
     return matmul_workspace_size(M, N, K);
 }
 
+spec_status_t spec_matmul_plan(int M, int N, int K, int sms, const int32_t* clusters, int32_t* plan) {
+    if (M < 1 || N < 1 || K < 1 || sms < 0 || (sms > 0 && !clusters) || !plan) return SPEC_ERR_INVALID_ARG;
+    if (K > INT32_MAX - 256 || M > INT32_MAX - 256 || N > INT32_MAX - 256) return SPEC_ERR_INVALID_ARG;
+    int out[5];
+    const cudaError_t e = matmul_plan(M, N, K, sms, clusters, out);
+    if (e != cudaSuccess) return e == cudaErrorInvalidValue ? SPEC_ERR_INVALID_ARG : SPEC_ERR_CUDA;
+    for (int i = 0; i < 5; ++i) plan[i] = out[i];
+    return SPEC_OK;
+}
+
 spec_status_t spec_matmul_e4m3(const void* x, int64_t x_stride, const float* x_scale, int64_t x_scale_stride, const void* w,
                                int64_t w_stride, const float* w_scale, int64_t w_scale_stride, int M, int N, int K, void* out,
                                spec_dtype_t out_dtype, int64_t out_stride, void* workspace, size_t workspace_bytes,

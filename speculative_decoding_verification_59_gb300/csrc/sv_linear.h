@@ -56,5 +56,7 @@ struct MatmulArgs {
 };
 size_t matmul_workspace_size(int M, int N, int K);
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st);
+// spec_matmul_plan's entries.
+cudaError_t matmul_plan(int M, int N, int K, int sms, const int* clusters, int (&out)[5]);
 
 }  // namespace sv

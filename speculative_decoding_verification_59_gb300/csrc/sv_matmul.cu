@@ -422,14 +422,14 @@ struct MmPlan {
     int pair;                          // CTAs in pairs, or each by itself
     unsigned long long tag;
     // equal shares: the first step of a pair's
-    __device__ __forceinline__ long long begin(int p) const { return total * p / pairs; }
+    __host__ __device__ __forceinline__ long long begin(int p) const { return total * p / pairs; }
     // (a cluster's pairs share its tile)
     __device__ __forceinline__ long long part_begin(int p) const {
         const int tile = p / split, q = p - tile * split;
         return (long long)tile * blocks + (long long)blocks * q / split;
     }
     // the pair whose (equal) share has step u
-    __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * pairs - 1) / total); }
+    __host__ __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * pairs - 1) / total); }
 };
 // The workspace: error word (256 bytes), a ticket for each pair's last tile, CTA and warp, two parts a pair.
 constexpr int kMmMaxPairs = 80;
@@ -1156,16 +1156,16 @@ constexpr double kMmJoin[3] = {0.9, 2.2, 3.6};
 // Whole tiles in the width whose rounds of all pairs or CTAs take the least, or equal shares, whose parts
 // cost their writing and reading, where that is less: few tiles with long contractions, or
 // little more than whole rounds.
-static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[3]) {
+static MmPlan plan_many(int M, int N, int K, int sms, const int (&clusters)[3]) {
     MmPlan p = {};
-    p.blocks = scale_blocks(a.K);
+    p.blocks = scale_blocks(K);
     const long long pairs_most = sms / 2 < kMmMaxPairs ? sms / 2 : kMmMaxPairs;
     double best = 1e300;
     for (int single = 0; single < 2; ++single) {
-        const int tiles_m = single ? (a.M - 1) / 128 + 1 : (a.M - 1) / 256 + 1;
+        const int tiles_m = single ? (M - 1) / 128 + 1 : (M - 1) / 256 + 1;
         const long long most = single ? sms : pairs_most;
         for (const MmWidth& w : single ? kMmSingles : kMmPairs) {
-            const long long tiles = (long long)tiles_m * ((a.N - 1) / w.W + 1), total = tiles * p.blocks;
+            const long long tiles = (long long)tiles_m * ((N - 1) / w.W + 1), total = tiles * p.blocks;
             const auto take = [&](double us, long long pairs, int whole, int split) {
                 if (us >= best) return;
                 best = us;
@@ -1197,8 +1197,6 @@ static MmPlan plan_many(const MatmulArgs& a, int sms, const int (&clusters)[3]) 
             }
         }
     }
-    // (times an odd number: one tag a launch as before, but none that small numbers left in a workspace could be)
-    p.tag = next_launch_tag() * 0x9e3779b97bull & ((1ull << 40) - 1);
     return p;
 }
 
@@ -1252,12 +1250,16 @@ static cudaError_t launch_whole(const MatmulArgs& a, const MmPlan& p, cudaStream
     }
 }
 
+static bool tiles_fit(int M, int N) { return (long long)((M - 1) / 128 + 1) * ((N - 1) / 64 + 1) < (1LL << 31); }
+
 static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
-    if ((long long)((a.M - 1) / 128 + 1) * ((a.N - 1) / 64 + 1) >= (1LL << 31)) return cudaErrorInvalidValue;
+    if (!tiles_fit(a.M, a.N)) return cudaErrorInvalidValue;
     int clusters[3];
     const cudaError_t e = many_clusters(clusters);
     if (e != cudaSuccess) return e;
-    const MmPlan p = plan_many(a, sms, clusters);
+    MmPlan p = plan_many(a.M, a.N, a.K, sms, clusters);
+    // (times an odd number: one tag a launch as before, but none that small numbers left in a workspace could be)
+    p.tag = next_launch_tag() * 0x9e3779b97bull & ((1ull << 40) - 1);
     if (!p.whole) return p.W == 64 ? launch_many_t<64, kMmTickets, true>(a, p, st) : launch_many_t<256, kMmTickets, true>(a, p, st);
     return p.pair ? launch_whole<true>(a, p, st) : launch_whole<false>(a, p, st);
 }
@@ -1266,6 +1268,37 @@ constexpr int kMmFew = 64;             // rows that matmul_few_kernel takes
 
 // (Which calls of more rows share tiles depends on the device's SMs: all have room for parts.)
 size_t matmul_workspace_size(int M, int, int) { return M <= kMmFew ? kMmTicketAt : kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
+
+cudaError_t matmul_plan(int M, int N, int K, int sms, const int* clusters, int (&out)[5]) {
+    if (M <= kMmFew) {
+        out[0] = SPEC_MATMUL_FEW, out[1] = kMmTile, out[2] = 1, out[3] = 0, out[4] = 0;
+        return cudaSuccess;
+    }
+    if (!tiles_fit(M, N)) return cudaErrorInvalidValue;
+    int most[3];
+    if (sms > 0) {
+        for (int i = 0; i < 3; ++i) most[i] = clusters[i];
+    } else {
+        DeviceInfo di;
+        cudaError_t e = device_info(&di);
+        if (e == cudaSuccess) e = many_clusters(most);
+        if (e != cudaSuccess) return e;
+        sms = di.sm_count;
+    }
+    const MmPlan p = plan_many(M, N, K, sms, most);
+    out[0] = !p.whole ? SPEC_MATMUL_SHARES : p.split > 1 ? SPEC_MATMUL_CLUSTERS : SPEC_MATMUL_WHOLE;
+    out[1] = p.W;
+    out[2] = p.pair ? 2 : 1;
+    out[3] = p.pairs;
+    out[4] = p.split;
+    if (!p.whole) {
+        for (long long t = 0; t < p.tiles; ++t) {
+            const int n = p.of((t + 1) * p.blocks - 1) - p.of(t * p.blocks) + 1;
+            if (n > out[4]) out[4] = n;
+        }
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     DeviceInfo di;
