@@ -591,9 +591,10 @@ spec_status_t spec_quantize_e4m3(const void* x, spec_dtype_t dtype, int64_t x_st
  *                                     sum over k in b of x[m, k] w[n, k]
  *   x        [M, K] e4m3, w [N, K] e4m3: 16-byte aligned, strides multiples of 16 and at least K
  *            (of a single row none is used)
- *   x_scale  fp32, block b of row m at b * x_scale_stride + m: 16-byte aligned, the stride a
- *            multiple of 4 and at least M (of a single block none is used).  What lies between
- *            M and the stride does not matter
+ *   x_scale  fp32, block b of row m at b * x_scale_stride + m, the stride at least M (of a single
+ *            block none is used).  What lies between M and the stride does not matter.  For 2 to 64
+ *            rows 16-byte aligned and the stride a multiple of 4; for one row (the last of a prompt,
+ *            say) and for more than 64 neither is needed
  *   w_scale  fp32, at (n / 128) * w_scale_stride + b
  *   out      [M, N] bf16 or fp32, row m at m * out_stride (elements, at least N)
  * Any M, N >= 0 and K >= 1, odd ones included; rows whose stride is a multiple of 16 bytes are

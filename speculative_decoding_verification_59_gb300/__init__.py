@@ -762,8 +762,9 @@ def quantize_e4m3(x, *, block_rows: int = 1, stream=None):
 def matmul_e4m3(x, x_scale, w, w_scale, *, dtype=None, out=None, workspace=None, stream=None):
     """The product of 8-bit rows with an 8-bit weight (see spec_matmul_e4m3): x [..., K] and w [N, K]
     float8_e4m3fn with the scales that quantize_e4m3, add_norm and gated_act give, [...,
-    ceil(K / 128)] with stride 1 from row to row, and [ceil(N / 128), ceil(K / 128)].  Returns [..., N] of
-    dtype (bfloat16 by default, or float32).  workspace: a Workspace, whose read_error() then
+    ceil(K / 128)] with stride 1 from row to row, and [ceil(N / 128), ceil(K / 128)].  Rows may be a part of
+    what those calls gave, q[a:b] with scale[a:b]: one row, or more than 64, any; 2 to 64 rows from a
+    multiple of 4 on.  Returns [..., N] of dtype (bfloat16 by default, or float32).  workspace: a Workspace, whose read_error() then
     tells of waits that ran out (NaN in the results either way), or a uint8 tensor of
     spec_matmul_workspace_size() bytes, its first 256 zero, that no call on another stream
     uses at the same time.  None: one kept for the device and stream to the program's end (a

@@ -129,9 +129,10 @@ spec_status_t spec_matmul_e4m3(const void* x, int64_t x_stride, const float* x_s
         return SPEC_ERR_INVALID_ARG;
     if (K > INT32_MAX - 256 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || x_stride >= (1LL << 40) || w_stride >= (1LL << 40) || x_scale_stride >= (1LL << 38))
         return SPEC_ERR_INVALID_ARG;
-    if (!is_aligned(x, 16) || !is_aligned(w, 16) || !is_aligned(x_scale, 16) || (M > 1 && x_stride % 16) || (N > 1 && w_stride % 16) ||
-        (blocks > 1 && x_scale_stride % 4) || !is_aligned(w_scale, 4) || !is_aligned(out, bytes_of(out_dtype)) ||
-        !is_aligned(workspace, 256))
+    const bool few = M > 1 && M <= kMmFew;     // rows whose scales a TMA load brings
+    if (!is_aligned(x, 16) || !is_aligned(w, 16) || !is_aligned(x_scale, few ? 16 : 4) || (M > 1 && x_stride % 16) ||
+        (N > 1 && w_stride % 16) || (few && blocks > 1 && x_scale_stride % 4) || !is_aligned(w_scale, 4) ||
+        !is_aligned(out, bytes_of(out_dtype)) || !is_aligned(workspace, 256))
         return SPEC_ERR_MISALIGNED;
     if (workspace_bytes < matmul_workspace_size(M, N, K)) return SPEC_ERR_WORKSPACE_TOO_SMALL;
     MatmulArgs a = {};

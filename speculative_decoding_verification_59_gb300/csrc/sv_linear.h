@@ -43,6 +43,7 @@ struct TileQuantArgs {
 };
 cudaError_t launch_quantize_tiles(const TileQuantArgs& a, spec_dtype_t in, cudaStream_t st);
 
+constexpr int kMmFew = 64;             // rows that the transposed product takes
 struct MatmulArgs {
     const char *x, *w;                 // e4m3
     int64_t xld, wld;                  // bytes between rows

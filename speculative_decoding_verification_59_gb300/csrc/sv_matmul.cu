@@ -209,7 +209,9 @@ __device__ __forceinline__ void put4(const MatmulArgs& a, int64_t at, int n, boo
     }
 }
 
-template <int T>
+// ANY: one row, whose scales lie anywhere: they are loaded with the tile's and multiplied there, and every place
+// holds ones.
+template <int T, bool ANY = false>
 __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_few_kernel(const MatmulArgs a, uint32_t limit, int blocks, int S, bool wide,
                                                                           const __grid_constant__ CUtensorMap xmap,
                                                                           const __grid_constant__ CUtensorMap wmap,
@@ -234,11 +236,14 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
             mbar_init_fence();
             map_prefetch(&wmap);
             map_prefetch(&xmap);
-            map_prefetch(&smap);
+            if (!ANY) map_prefetch(&smap);
         }
         __syncwarp();
     }
     if (warp == 1) tc_alloc(&tmem_at, C::TMEM);
+    if (ANY) {
+        for (int i = tid; i < C::PLACES * C::SCALE / 4; i += C::THREADS) reinterpret_cast<float*>(smem + C::SCALE_AT)[i] = 1.f;
+    }
     pdl_trigger();
     tc_before();
     __syncthreads();
@@ -260,12 +265,12 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
             const uint32_t at = base + s * C::STAGE;
             const bool two = C::BP == 2 && b + 1 < b1;
             if (lead) {
-                mbar_arrive_expect_tx(&full[s], (two ? 2 : 1) * C::BYTES + C::SCALE);
+                mbar_arrive_expect_tx(&full[s], (two ? 2 : 1) * C::BYTES + (ANY ? 0 : C::SCALE));
                 tma_2d(at, &wmap, b * kMmTile, tile * kMmTile, &full[s]);
                 if (two) tma_2d(at + kMmBytes, &wmap, (b + 1) * kMmTile, tile * kMmTile, &full[s]);
                 tma_2d(at + C::X_AT, &xmap, b * kMmTile, 0, &full[s]);
                 if (two) tma_2d(at + C::X_AT + C::X_BYTES, &xmap, (b + 1) * kMmTile, 0, &full[s]);
-                tma_2d(base + C::SCALE_AT + place * C::SCALE, &smap, 0, b, &full[s]);
+                if (!ANY) tma_2d(base + C::SCALE_AT + place * C::SCALE, &smap, 0, b, &full[s]);
             }
             __syncwarp();
             if (++place == C::PLACES) place = 0;
@@ -329,7 +334,10 @@ __global__ void __launch_bounds__(FewCfg<T>::THREADS, FewCfg<T>::CTAS) matmul_fe
         bool ok = true;
         unsigned s = 0, phase = 0, place = 0;
         for (int b = b0; b < b1; b += C::BP) {
-            if (((b - b0) & 31) == 0 && b + lane < b1) wl = ld_scale(wsc + b + lane);
+            if (((b - b0) & 31) == 0 && b + lane < b1) {
+                wl = ld_scale(wsc + b + lane);
+                if (ANY) wl *= ld_scale(a.xscale + (b + lane) * a.xs_stride);
+            }
             const bool two = C::BP == 2 && b + 1 < b1;
             const float wf[2] = {__shfl_sync(0xffffffffu, wl, (b - b0) & 31), __shfl_sync(0xffffffffu, wl, (b - b0 + 1) & 31)};
             ok = wait_warp(&done[s], phase, limit);
@@ -1110,11 +1118,20 @@ static cudaError_t few_clusters(int (&most)[8]) {
     });
 }
 
-template <int T>
+template <int T, bool ANY = false>
 static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
     using C = FewCfg<T>;
+    const auto kfn = matmul_few_kernel<T, ANY>;
     int most[8];
-    const cudaError_t e = few_clusters<T>(most);
+    cudaError_t e = few_clusters<T>(most);
+    if (ANY && e == cudaSuccess) {
+        static DeviceSlots slots = {};
+        int unused = 0;
+        e = device_once(slots, &unused, [&](int, int* o) {
+            *o = 1;
+            return cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        });
+    }
     if (e != cudaSuccess) return e;
     const int tiles = (a.N - 1) / kMmTile + 1, blocks = scale_blocks(a.K);
     // Of the clusters of which all run at once, those that take the least: a CTA's blocks one after the other,
@@ -1134,12 +1151,12 @@ static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
             S = i;
         }
     }
-    CUtensorMap xm, wm, sm;
+    CUtensorMap xm, wm, sm = {};
     if (!map_2d(&xm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.K, a.M, a.xld, kMmTile, T, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.wld, kMmTile, kMmTile, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, C::BP, CU_TENSOR_MAP_SWIZZLE_NONE))
+        (!ANY && !map_2d(&sm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.xscale, a.M, blocks, a.xs_stride * 4, T, C::BP, CU_TENSOR_MAP_SWIZZLE_NONE)))
         return cudaErrorInvalidValue;
-    return launch_clusters(matmul_few_kernel<T>, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, rows_aligned(a), xm, wm, sm);
+    return launch_clusters(kfn, tiles * S, S, C::THREADS, C::SMEM, st, a, wait_limit(), blocks, S, rows_aligned(a), xm, wm, sm);
 }
 
 // What a block of a tile W columns wide takes, and a tile's end (us, measured at 512 rows, as many tiles
@@ -1264,8 +1281,6 @@ static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
     return p.pair ? launch_whole<true>(a, p, st) : launch_whole<false>(a, p, st);
 }
 
-constexpr int kMmFew = 64;             // rows that matmul_few_kernel takes
-
 // (Which calls of more rows share tiles depends on the device's SMs: all have room for parts.)
 size_t matmul_workspace_size(int M, int, int) { return M <= kMmFew ? kMmTicketAt : kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
 
@@ -1305,6 +1320,7 @@ cudaError_t launch_matmul(const MatmulArgs& a, cudaStream_t st) {
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
     if (a.M > kMmFew) return launch_many(a, di.sm_count, st);
+    if (a.M == 1 && !(is_aligned(a.xscale, 16) && a.xs_stride % 4 == 0)) return launch_few_t<16, true>(a, st);
     return a.M <= 16 ? launch_few_t<16>(a, st) : a.M <= 32 ? launch_few_t<32>(a, st) : launch_few_t<64>(a, st);
 }
 
