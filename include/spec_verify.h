@@ -599,7 +599,8 @@ spec_status_t spec_quantize_e4m3(const void* x, spec_dtype_t dtype, int64_t x_st
  *   out      [M, N] bf16 or fp32, row m at m * out_stride (elements, at least N)
  * Any M, N >= 0 and K >= 1, odd ones included; rows whose stride is a multiple of 16 bytes are
  * written fastest.  Sums are fp32: of a block's products in tensor memory, then, scaled,
- * over the blocks, in an order that the sizes alone decide.
+ * over the blocks, in an order that the sizes and the device decide (its SMs, and the clusters that it
+ * holds at once): the same call on the same device gives the same bits.
  * Workspace: spec_matmul_workspace_size() bytes, 256-byte aligned, its first 256 bytes
  * zero-filled once (the error word; a wait that runs out sets SPEC_DEVERR_TIMEOUT there and
  * leaves NaN in the results it concerns).  Calls that share one must not overlap.

@@ -764,11 +764,11 @@ def matmul_e4m3(x, x_scale, w, w_scale, *, dtype=None, out=None, workspace=None,
     float8_e4m3fn with the scales that quantize_e4m3, add_norm and gated_act give, [...,
     ceil(K / 128)] with stride 1 from row to row, and [ceil(N / 128), ceil(K / 128)].  Rows may be a part of
     what those calls gave, q[a:b] with scale[a:b]: one row, or more than 64, any; 2 to 64 rows from a
-    multiple of 4 on.  Returns [..., N] of dtype (bfloat16 by default, or float32).  workspace: a Workspace, whose read_error() then
-    tells of waits that ran out (NaN in the results either way), or a uint8 tensor of
-    spec_matmul_workspace_size() bytes, its first 256 zero, that no call on another stream
-    uses at the same time.  None: one kept for the device and stream to the program's end (a
-    captured call gets one of its graph's)."""
+    multiple of 4 on.  Returns [..., N] of dtype (bfloat16 by default, or float32).  workspace: a
+    Workspace, whose read_error() then tells of waits that ran out (NaN in the results either way),
+    or a uint8 tensor of spec_matmul_workspace_size() bytes, its first 256 zero, that no call on
+    another stream uses at the same time.  None: one kept for the device and stream to the
+    program's end (a captured call gets one of its graph's)."""
     if isinstance(workspace, Workspace):
         workspace = _scratch(workspace, 0, load_library().spec_matmul_workspace_size(
             x.numel() // max(x.shape[-1], 1), w.shape[0], x.shape[-1]), stream)

@@ -3,9 +3,10 @@
 //   out[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{k in block b} x[m, k] w[n, k].
 // The scales change with every 128 elements of the contraction, so an
 // accumulator in tensor memory holds one block's products only.  The inner sums
-// are exact to fp32; the warps that read them add them, times the two scales, to
-// running sums in registers, while the next blocks' products run into the other
-// accumulators.
+// are fp32 (exact where 24 bits hold them; of products 2^28 apart, off by up to 3 steps of
+// 2^-23 of what their magnitudes add up to); the warps that read them add them, times the
+// two scales, to running sums in registers, while the next blocks' products run into
+// the other accumulators.
 //
 // Measured (one GB300, random inputs, new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
 // copy 6.8 TB/s):
