@@ -10,10 +10,10 @@
 //
 // Measured (one GB300, random inputs, new every time, bf16 out; bf16 products of cuBLAS reach 1924 TFLOP/s, a
 // copy 6.8 TB/s):
-//   1 row, N = 6144, K = 4096: 5.9 us, 4.3 TB/s; N = 151936: 90.5 us, 6.9 TB/s.  Memory, and some 2 us from
-//     one call's last store to the next one's first load and of the join.
-//   512 rows, N = 151936, K = 4096: 267 us, 2.39 PFLOP/s; N = 24576: 47 us, 2.2; 1152 rows, N = 4096, K =
-//     12288: 49.8 us, 2.3.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
+//   1 row, N = 6144, K = 4096: 5.9 us, 4.3 TB/s (7.4 with more weights in turn than L2 holds); N = 151936: 90
+//     us, 6.9 TB/s.  Memory, and some 2 us from one call's last store to the next one's first load and of the join.
+//   512 rows, N = 151936, K = 4096: 265 us, 2.4 PFLOP/s; N = 24576: 47 us, 2.2; 1152 rows, N = 4096, K =
+//     12288: 50 us, 2.3.  A step of 256 x 256 x 128 takes a pair 0.4 us, of which the products would
 //     take 0.27: the rest is the chain from an accumulator's last product to its next, and what L2 brings (64
 //     KB a step and pair, 11 TB/s in all: with half the bytes of both operands left out, the largest
 //     took 211 us for 240); and the clock falls to 1.75 GHz under it.  (Constant inputs, which use less power: 240
@@ -165,7 +165,9 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar, unsigned short both) 
 // CTAs an SM, 100 KB under way each (one with all the ring: 7.0 us for 6.3 at one row, N = 6144, K = 4096,
 // 27.5 for 22 at 64 rows, N = 24576), and for up to 16 rows two blocks at a time (one row: 6.26 for 6.48;
 // 64 rows so: 24.8 for 23.2).  Equal shares of all tiles' blocks, their parts joined through
-// memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N = 151936.  65
+// memory, gained nothing here over a cluster or a CTA a tile: 96.8 us for 94.5 at one row, N = 151936.  (These
+// pairs of times are from before a kernel's end lost its release, 0.4 to 0.5 us of each: now 5.9 us
+// at one row, N = 6144, and 21.7 at 64 rows, N = 24576, where 192 tiles leave 112 of 304 places empty.)  65
 // to 128 rows this way: 6.4 us for the 5.6 of pairs at 1000 x 1040, 28.9 for 27.3 at 24576 x 4096, and
 // 18.5 for 20.7 only at 4096 x 12288 (single CTAs: 16.8).
 template <int T>
@@ -177,7 +179,10 @@ struct FewCfg {
     static constexpr int X_AT = BP * kMmBytes, X_BYTES = T * kMmTile, BYTES = kMmBytes + X_BYTES, STAGE = BP * BYTES;
     // Scales have a place more than the operands: an arrival does not wait for what the warp is still
     // reading from shared memory, so a place is written again only when the warps have taken the step
-    // after (with as many places as stages, one row's scales in 10^5 came from the next round).
+    // after (with as many places as stages, one row's scales in 10^5 came from the next round).  No barrier
+    // says that its reads have come by then, the sums do: before the arrival of step i + 1 stand its
+    // multiply-adds, each of which adds to what step i's left, which needed step i's scale.  Sums in two sets, or
+    // steps whose multiply-adds move behind the next one's arrival, would take that away.
     static constexpr int SCALE_AT = STAGES * STAGE, PLACES = STAGES + 1;
     static constexpr int SMEM = SCALE_AT + PLACES * SCALE + 1024;        // and room to align
     static constexpr int THREADS = 192, CTAS = 2;
@@ -1138,7 +1143,7 @@ static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
     // Of the clusters of which all run at once, those that take the least: a CTA's blocks one after the other,
     // and the join (measured at N = 1024, K = 512 to 4096; more tiles only wait for memory).  One row, N =
     // 6144, K = 4096, 48 tiles: 6.3 us in clusters of five, of which 56 fit; 7.5 in four, 9.6 in six, of
-    // which 46 do.
+    // which 46 do.  (Before a kernel's end lost its release: five take 5.9 now.)
     constexpr double kStep = T <= 16 ? 0.17 : T <= 32 ? 0.22 : 0.28;
     constexpr double kJoin[9] = {0, 0, 1.2, 0.9, 0.8, 1.0, 1.1, 1.3, 1.5};
     int S = 1;
@@ -1161,7 +1166,9 @@ static cudaError_t launch_few_t(const MatmulArgs& a, cudaStream_t st) {
 }
 
 // What a block of a tile W columns wide takes, and a tile's end (us, measured at 512 rows, as many tiles
-// as pairs, or as single CTAs, fit at once, and K = 1024 to 8192).
+// as pairs, or as single CTAs, fit at once, and K = 1024 to 8192).  They know no memory: where the weights'
+// bytes bound a call, at 65 to 256 rows, it takes longer than they say (128 x 24576 x 4096: 22.3 us for 14.5, 128 x
+// 4096 x 12288: 16.6 for 10.8).
 struct MmWidth {
     int W;
     double step, end;
@@ -1204,6 +1211,9 @@ static MmPlan plan_many(int M, int N, int K, int sms, const int (&clusters)[3]) 
                 if (tiles <= clusters[single ? i : i + 1] && split <= p.blocks)
                     take((p.blocks + split - 1) / split * w.step + w.end + kMmJoin[i], tiles * split, 1, split);
             }
+            // Shares.  (Of tiles of 64 beside clusters with tiles of 128, which came later: 221 x 1175 x 32304 27.8 us for 35.0, 195 x
+            // 4992 x 15872 34.3 for 36.7, but eight other sizes of ten that take them 0 to 30 % slower, 501 x 2616 x 15952
+            // 41.6 for 31.6: their cost is set too low.)
             if (single || (w.W != 64 && w.W != 256)) continue;
             for (int n = 2; n <= 8; ++n) {
                 // (n: parts of a tile)
@@ -1282,7 +1292,7 @@ static cudaError_t launch_many(const MatmulArgs& a, int sms, cudaStream_t st) {
     return p.pair ? launch_whole<true>(a, p, st) : launch_whole<false>(a, p, st);
 }
 
-// (Which calls of more rows share tiles depends on the device's SMs: all have room for parts.)
+// (Which calls of more rows share tiles depends on the device too, which is not asked here: all have room for parts, 42 MB.)
 size_t matmul_workspace_size(int M, int, int) { return M <= kMmFew ? kMmTicketAt : kMmPartAt + 2 * kMmMaxPairs * kMmPartBytes; }
 
 cudaError_t matmul_plan(int M, int N, int K, int sms, const int* clusters, int (&out)[5]) {

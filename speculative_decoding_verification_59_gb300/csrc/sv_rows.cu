@@ -176,7 +176,8 @@ static cudaError_t launch_add_norm_t(const NormArgs& a, int out, int sms, cudaSt
     // Few rows: as many threads a row as it has vectors (the time is one row's).  More: two or four
     // vectors a thread, so that an SM holds more rows' loads under way (rows of 4096, one / two / four
     // a thread: 512 rows 5.9 / 4.5 / 5.5 us, 8192 of an fp32 residual 87 / 61.5 / 62, 8192 to e4m3
-    // 71.6 / 47.5 / 45.8, since down to 40.9: 6.5 TB/s with the fp32 residual, 5.8 to e4m3, 2.3 us for a row).
+    // 71.6 / 47.5 / 45.8, since down to 41.7: 6.4 TB/s with the fp32 residual, 5.7 to e4m3, 2.2 us for a row.  Between
+    // them less: 512 rows with a bf16 residual to e4m3 5.2 us, 2.8 TB/s, 1152 rows 9.4, 3.5, 2000 of 12000 38.7, 4.4.)
     int vpt = nv > 1024 ? 4 : a.rows <= 2 * sms ? (nv > 512 ? 2 : 1) : a.rows <= 32 * sms ? 2 : 4;
     while (vpt > 1 && nv <= 32 * (vpt / 2)) vpt /= 2;
     int tpr = 32;
@@ -229,9 +230,9 @@ __device__ __forceinline__ void gate8(float (&x)[8], const float (&y)[8]) {
 
 // A CTA takes RT rows and, 16 lanes a block, 16 / RT blocks of them at a time, V times.  Many rows: 16
 // rows of one block, whose scales then leave together in one line (a scale of 4 bytes by itself
-// costs a sector: 39.4 us for 33 at 16384 rows of 4096).  Activation of 4000 x 12288 bf16 to e4m3: 38.7 us,
-// 6.4 TB/s; of 1152: 12.4, 5.7 (issue slots are 60 % busy; with divisions and single arithmetic, 82 %,
-// 15.1); to bf16 4000 take 43.4, 6.8.  7 rows: 1.6.  Rounding of 16384 x 4096: 33.4, 6.1.
+// costs a sector: 39.4 us for 33 at 16384 rows of 4096).  Activation of 4000 x 12288 bf16 to e4m3: 38.5 us,
+// 6.4 TB/s; of 1152: 12.3, 5.8 (issue slots are 60 % busy; with divisions and single arithmetic, 82 %,
+// 15.1); to bf16 4000 take 43.4, 6.8.  7 rows: 1.5.  Rounding of 16384 x 4096: 33.1, 6.1; of 1152: 4.2.
 constexpr int kActThreads = 256;
 template <bool F32, int ACT, int RT, int V>
 __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int out, int chunks) {
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActArgs a, int o
 template <bool F32, int ACT>
 static cudaError_t launch_act_t(const ActArgs& a, int out, int sms, cudaStream_t st) {
     // 16 rows and three blocks of them a CTA where that gives every SM one, else a row's blocks side by side.  (Two, three, four,
-    // six: activation of 1152 x 12288 12.7 / 12.5 / 12.8 / 13.8 us, rounding of 1152 x 4096 4.35 / 3.85 / 4.05 / 4.5,
-    // of 16384 37.7 / 33.5 / 33.2 / 34.6.)
+    // six, in one run: activation of 1152 x 12288 12.7 / 12.5 / 12.8 / 13.8 us, rounding of 1152 x 4096 4.35 / 3.85 / 4.05 /
+    // 4.5, of 16384 37.7 / 33.5 / 33.2 / 34.6.)
     const long long blocks = scale_blocks(a.dim), groups = ((long long)a.rows + 15) / 16;
     if ((blocks + 2) / 3 * groups >= sms) {
         const long long chunks = (blocks + 2) / 3;
