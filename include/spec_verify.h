@@ -620,7 +620,7 @@ spec_status_t spec_matmul_e4m3(const void* x, int64_t x_stride, const float* x_s
  *   [3]  CTAs or pairs that are launched (few rows: 0)
  *   [4]  parts of a tile's contraction: 1, those of a cluster, or the most that equal shares leave in
  *        a tile (few rows: 0)
- * sms 0: on the current device.  Else on one of `sms` SMs, of which clusters[0], [1] and [2] clusters of
+ * sms 0: on the current device.  Else on one of `sms` SMs (two at least), of which clusters[0], [1] and [2] clusters of
  * two, four and eight CTAs run at once; host only then, no CUDA call.
  */
 typedef enum {

@@ -106,7 +106,7 @@ size_t spec_matmul_workspace_size(int M, int N, int K) {
 }
 
 spec_status_t spec_matmul_plan(int M, int N, int K, int sms, const int32_t* clusters, int32_t* plan) {
-    if (M < 1 || N < 1 || K < 1 || sms < 0 || (sms > 0 && !clusters) || !plan) return SPEC_ERR_INVALID_ARG;
+    if (M < 1 || N < 1 || K < 1 || sms < 0 || sms == 1 || (sms > 0 && !clusters) || !plan) return SPEC_ERR_INVALID_ARG;
     if (K > INT32_MAX - 256 || M > INT32_MAX - 256 || N > INT32_MAX - 256) return SPEC_ERR_INVALID_ARG;
     int out[5];
     const cudaError_t e = matmul_plan(M, N, K, sms, clusters, out);
